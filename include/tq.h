@@ -36,14 +36,16 @@
  *     ordering between them) must be ordered by the caller or use separate
  *     contexts.
  *   - CUDA graphs: after one eager call on a context (which sizes its
- *     workspace), tq_encode_append and tq_decode_attention can be captured
- *     and replayed; device-side counters and the status word reset
+ *     workspace), the calls can be captured and replayed (a workspace that a
+ *     later, larger call replaces stays allocated until tq_free, so graphs
+ *     captured with it stay good; two graphs of one context share it and must
+ *     not overlap on the GPU); device-side counters and the status word reset
  *     themselves, tensor maps are built at capture, and the decode grid is
  *     fixed by the max_len_hint given at capture (it must cover the lengths
  *     every replay sees).
  *   - Conditions only the GPU can see (a sequence whose append passes the
  *     capacity, a norm that overflows fp16, a sequence shorter than the query
- *     block, a pipeline wait that timed out) never trap: the kernels OR a bit
+ *     block, a list with a bad index, a pipeline wait that timed out) never trap: the kernels OR a bit
  *     into the context's device status word, read by tq_get_status.
  */
 #ifndef TQ_H
@@ -86,6 +88,8 @@ extern "C" {
 #define TQ_STATUS_NORM_OVERFLOW   2u  /* a vector norm overflowed fp16; stored as +inf */
 #define TQ_STATUS_SHORT_CONTEXT   4u  /* a query row saw no token (length < Tq); its output is 0 */
 #define TQ_STATUS_PIPELINE_STALL  8u  /* a bounded in-kernel wait gave up; results are invalid */
+#define TQ_STATUS_BAD_INDEX      16u  /* a device-side list (sequence bounds, places, sequences) was out of
+                                       * range or in conflict; what it named was left untouched */
 
 typedef struct tq_ctx tq_ctx;
 
@@ -156,6 +160,31 @@ int tq_encode_append(tq_ctx **ctx, const tq_cache *cache, const void *k_new,
                      const void *v_new, int32_t t_new, void *stream);
 
 /*
+ * Append packed tokens: the prompts (or prompt chunks, or drafted tokens) of
+ * all sequences back to back, each of its own length.
+ *   k_new, v_new: fp16 [total, num_kv_heads, 128] device pointers (token-major,
+ *                 the layout a projection of packed tokens has).
+ *   cu_seqlens:   int32 [batch + 1] device pointer, non-decreasing; the tokens
+ *                 of sequence b are rows cu_seqlens[b] .. cu_seqlens[b+1] - 1
+ *                 (none when equal).  Rows outside [cu_seqlens[0],
+ *                 cu_seqlens[batch]) are ignored.
+ *   total:        rows of k_new and v_new; 0 is a no-op.
+ * Row cu_seqlens[b] + j is written at position lengths[b] + j; afterwards
+ * lengths[b] += cu_seqlens[b+1] - cu_seqlens[b].  A sequence that would pass
+ * the capacity is left untouched and TQ_STATUS_CAPACITY is raised; bounds that
+ * decrease, are negative or pass total raise TQ_STATUS_BAD_INDEX, that
+ * sequence's length is not advanced, and records past the lengths are
+ * unspecified.
+ * The records are tq_encode_append's, except that every code is decided
+ * exactly: an element near a decision midpoint is decided from the exact
+ * transform, so the codes do not depend on the kernel (more than 4096 vectors
+ * per stream take the tensor-core encode) or on the rounding of fp32 sums.
+ */
+int tq_encode_append_packed(tq_ctx **ctx, const tq_cache *cache, const void *k_new,
+                            const void *v_new, const int32_t *cu_seqlens, int32_t total,
+                            void *stream);
+
+/*
  * Decode attention over the visible cache (scores, online softmax, rotated-
  * basis P.V, split-K combine, inverse rotation of the output).
  *   q:   fp16 [batch, num_q_heads, tq, 128] device pointer.
@@ -190,6 +219,104 @@ int tq_decode_attention(tq_ctx **ctx, const tq_cache *cache, const void *q,
 int tq_prefill_attention(tq_ctx **ctx, const tq_cache *cache, const void *q,
                          int32_t num_q_heads, int32_t tq, int32_t max_len_hint,
                          float scale, void *out, void *stream);
+
+/*
+ * Prefill attention of packed sequences: tq_prefill_attention for query blocks
+ * of different lengths, back to back.
+ *   q, out:      fp16 [total, num_q_heads, 128] device pointers (token-major).
+ *   cu_seqlens:  int32 [batch + 1] device pointer, as in
+ *                tq_encode_append_packed; sequence b has the query rows
+ *                cu_seqlens[b] .. cu_seqlens[b+1] - 1, n_b of them.
+ *   Row cu_seqlens[b] + j attends to tokens [0, lengths[b] - n_b + j] of
+ *   sequence b (the block's own tokens were appended before the call).  Output
+ *   rows that belong to no sequence are left as they were.  A row that sees no
+ *   token gives 0 and raises TQ_STATUS_SHORT_CONTEXT; bounds that decrease,
+ *   are negative or pass total raise TQ_STATUS_BAD_INDEX and the sequence's
+ *   rows are left as they were.
+ *   The other arguments, the supported modes and the group size as in
+ *   tq_prefill_attention.  A V norm that overflowed fp16 counts as 65504 (so
+ *   it cannot turn rows that do not see its token into NaN).
+ */
+int tq_prefill_attention_packed(tq_ctx **ctx, const tq_cache *cache, const void *q,
+                                int32_t num_q_heads, const int32_t *cu_seqlens, int32_t total,
+                                int32_t max_len_hint, float scale, void *out, void *stream);
+
+/*
+ * Attention of a tree of drafted tokens: the last tq tokens of every sequence
+ * (appended before the call) are drafted nodes, and node j attends to the
+ * whole context before them, [0, lengths[b] - tq), and to the drafted tokens
+ * that its mask names.
+ *   q, out:    fp16 [batch, num_q_heads, tq, 128] device pointers;
+ *              1 <= tq <= TQ_MAX_TREE_NODES, at most 128 query heads per KV head.
+ *   tree_mask: uint32 [mask_batch, tq, ceil(tq / 32)] device pointer, 4-byte
+ *              aligned: bit i % 32 of word i / 32 of row j is set where node j
+ *              attends to drafted token i (its ancestors and itself in a
+ *              tree; any mask is allowed, bits at tq and above are ignored).
+ *              Padding nodes have no bit set and see the context alone.
+ *   mask_batch: 1 (one mask for all sequences) or batch.
+ *   max_len_hint, scale: as in tq_decode_attention; tokens past the hint are
+ *              not read.
+ * A row that sees no token gives 0 and raises TQ_STATUS_SHORT_CONTEXT.  Where
+ * lengths[b] < tq the first tq - lengths[b] drafted tokens do not exist.
+ * A drafted token that a row does not see adds nothing to it, whatever its
+ * record holds (a V norm that overflowed fp16 counts as 65504 in the tokens of
+ * the drafted block).  Every mode and codebook is supported.  The call uses
+ * the context's workspace like tq_decode_attention.
+ */
+#define TQ_MAX_TREE_NODES 256
+int tq_tree_attention(tq_ctx **ctx, const tq_cache *cache, const void *q, int32_t num_q_heads,
+                      int32_t tq, int32_t max_len_hint, float scale, const uint32_t *tree_mask,
+                      int32_t mask_batch, void *out, void *stream);
+
+/* Host-only: the mask of one tree from its parents: parents[i] is the node
+ * that node i follows, -1 for a node that follows the context, always below i
+ * (parents come first).  words: num_nodes * ceil(num_nodes / 32) words, row j
+ * holding j's ancestors and j. */
+int tq_tree_mask(const int32_t *parents, int32_t num_nodes, uint32_t *words);
+
+/*
+ * Keep the accepted ones of a block of drafted tokens and drop the others.
+ *   start:      int32 [batch] device pointer: the first token of the block
+ *               (the length before the block was appended).
+ *   num_drafted: tokens of the block, 1 .. capacity.
+ *   keep:       int32 [batch, max_keep] device pointer: places in the block,
+ *               0 .. num_drafted - 1, strictly ascending; a tree's accepted
+ *               path is so when parents come before their children.
+ *   num_keep:   int32 [batch] device pointer: how many of the row count,
+ *               0 .. max_keep (0 takes the whole block back).
+ * Record start[b] + keep[b][i] moves to start[b] + i for every KV head, and
+ * lengths[b] = start[b] + num_keep[b].  Records move bit for bit; those past
+ * the new length stay as they are.  A sequence whose start, count or places
+ * are out of range or not ascending is left untouched and
+ * TQ_STATUS_BAD_INDEX is raised.
+ */
+int tq_cache_compact(tq_ctx **ctx, const tq_cache *cache, const int32_t *start, int32_t num_drafted,
+                     const int32_t *keep, const int32_t *num_keep, int32_t max_keep, void *stream);
+
+/*
+ * Copy sequences within a cache (forking a prompt for parallel samples or
+ * beams) or from one cache to another (a finished prefill that moves to the
+ * decode's cache, or a cache of a larger capacity): the first n tokens of
+ * sequence src_seq[m] become sequence dst_seq[m], and its length becomes n.
+ *   dst, src:   the same cache, or two whose buffers do not overlap; of one
+ *               mode, num_kv_heads, rot_seed, v_rescale and codebooks (else
+ *               TQ_ERR_INVALID_ARG); batch and capacity may differ.
+ *   dst_seq, src_seq: int32 [num_pairs] device pointers.
+ *   num_tokens: int32 [num_pairs] device pointer with each n, 0 .. the
+ *               source's length, or NULL for whole sources.  n = 0 frees the
+ *               destination; within one cache dst_seq[m] == src_seq[m] cuts a
+ *               sequence off at n.
+ *   max_len_hint: an upper bound of every n (sizes the grid), at most the
+ *               source's capacity.
+ * A pair with a sequence or n out of range is skipped and raises
+ * TQ_STATUS_BAD_INDEX; so is a pair whose destination is also another pair's
+ * destination or, within one cache, another pair's source.  An n past the
+ * destination's capacity or the hint skips the pair and raises
+ * TQ_STATUS_CAPACITY.  num_pairs == 0 is a no-op.
+ */
+int tq_cache_copy(tq_ctx **ctx, const tq_cache *dst, const tq_cache *src, const int32_t *dst_seq,
+                  const int32_t *src_seq, const int32_t *num_tokens, int32_t num_pairs,
+                  int32_t max_len_hint, void *stream);
 
 /*
  * Sparse-V decode: tq_decode_attention, except that a token whose softmax

@@ -41,6 +41,9 @@ TQ_STATUS_CAPACITY = 1
 TQ_STATUS_NORM_OVERFLOW = 2
 TQ_STATUS_SHORT_CONTEXT = 4
 TQ_STATUS_PIPELINE_STALL = 8
+TQ_STATUS_BAD_INDEX = 16
+
+TQ_MAX_TREE_NODES = 256
 
 # every entry point declared in include/tq.h: name -> (restype, argtypes)
 _c = ctypes
@@ -60,6 +63,19 @@ _SIGS = {
     "tq_decode_attention_noalloc": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_int32,
                                                _c.c_int32, _c.c_float, _c.c_void_p, _c.c_void_p,
                                                _c.c_void_p]),
+    "tq_encode_append_packed": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.c_void_p, _c.c_void_p,
+                                           _c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_void_p]),
+    "tq_prefill_attention_packed": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.c_void_p, _c.c_void_p,
+                                               _c.c_int32, _c.c_void_p, _c.c_int32, _c.c_int32,
+                                               _c.c_float, _c.c_void_p, _c.c_void_p]),
+    "tq_tree_attention": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.c_void_p, _c.c_void_p, _c.c_int32,
+                                     _c.c_int32, _c.c_int32, _c.c_float, _c.c_void_p, _c.c_int32,
+                                     _c.c_void_p, _c.c_void_p]),
+    "tq_tree_mask": (_c.c_int, [_c.POINTER(_c.c_int32), _c.c_int32, _c.POINTER(_c.c_uint32)]),
+    "tq_cache_compact": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.c_void_p, _c.c_void_p, _c.c_int32,
+                                    _c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_void_p]),
+    "tq_cache_copy": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                 _c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_int32, _c.c_void_p]),
     "tq_selftest_bounded_wait": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.c_int32, _c.c_void_p]),
     "tq_free": (None, [_c.c_void_p]),
     "tq_get_status": (_c.c_int, [_c.c_void_p, _c.POINTER(_c.c_uint32)]),
@@ -296,6 +312,110 @@ def tq_decode_attention_noalloc(cache: Cache, q, out, max_len_hint: int, scale: 
                                              int(q.shape[2]), int(max_len_hint), float(scale),
                                              _ptr(out), _ptr(status), _stream(stream)),
            "tq_decode_attention_noalloc")
+
+
+def _tensor(name: str, t, dtype, shape, cache) -> None:
+    """A contiguous tensor of this type and shape (None: any size) on the
+    cache's device; ValueError otherwise."""
+    if (t.dtype != dtype or not t.is_contiguous() or t.dim() != len(shape)
+            or any(w is not None and int(g) != w for g, w in zip(t.shape, shape))):
+        want = ", ".join("*" if w is None else str(w) for w in shape)
+        raise ValueError(f"{name} must be contiguous {dtype} [{want}], "
+                         f"got {t.dtype} {list(t.shape)}" + ("" if t.is_contiguous() else " (strided)"))
+    if t.device != cache.v_data.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.v_data.device}")
+    import torch
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current CUDA device")
+
+
+def tq_encode_append_packed(ctx: Context, cache: Cache, k_new, v_new, cu_seqlens, stream=None) -> None:
+    """Append packed k_new/v_new fp16 [total, Hkv, 128]: rows cu_seqlens[b] ..
+    cu_seqlens[b + 1] - 1 (int32 [B + 1] on the device) go to sequence b."""
+    import torch
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        _tensor(name, t, torch.float16, (int(k_new.shape[0]), cache.num_kv_heads, 128), cache)
+    _tensor("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), cache)
+    _check(lib().tq_encode_append_packed(ctypes.byref(ctx.ptr), ctypes.byref(cache.struct),
+                                         _ptr(k_new), _ptr(v_new), _ptr(cu_seqlens),
+                                         int(k_new.shape[0]), _stream(stream)),
+           "tq_encode_append_packed")
+
+
+def tq_prefill_attention_packed(ctx: Context, cache: Cache, q, out, cu_seqlens, max_len_hint: int,
+                                scale: float = 0.0, stream=None) -> None:
+    """Causal attention of packed query blocks q[total, Hq, 128] (already
+    appended to the cache): rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 belong
+    to sequence b.  Output rows of no sequence are left as they were."""
+    import torch
+    _tensor("q", q, torch.float16, (None, None, 128), cache)
+    _tensor("out", out, torch.float16, tuple(q.shape), cache)
+    _tensor("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), cache)
+    _check(lib().tq_prefill_attention_packed(ctypes.byref(ctx.ptr), ctypes.byref(cache.struct),
+                                             _ptr(q), int(q.shape[1]), _ptr(cu_seqlens),
+                                             int(q.shape[0]), int(max_len_hint), float(scale),
+                                             _ptr(out), _stream(stream)),
+           "tq_prefill_attention_packed")
+
+
+def tq_tree_attention(ctx: Context, cache: Cache, q, out, tree_mask, max_len_hint: int,
+                      scale: float = 0.0, stream=None) -> None:
+    """Attention of a tree of drafted tokens q[B, Hq, Tq, 128], the last Tq
+    tokens of every sequence.  tree_mask: int32 [1 or B, Tq, ceil(Tq / 32)]
+    words (``tq_tree_mask``), bit i of row j set where node j sees node i."""
+    import torch
+    _tensor("q", q, torch.float16, (cache.batch, None, None, 128), cache)
+    _tensor("out", out, torch.float16, tuple(q.shape), cache)
+    n = int(q.shape[2])
+    _tensor("tree_mask", tree_mask, torch.int32,
+            (1 if tree_mask.shape[0] == 1 else cache.batch, n, (n + 31) // 32), cache)
+    _check(lib().tq_tree_attention(ctypes.byref(ctx.ptr), ctypes.byref(cache.struct), _ptr(q),
+                                   int(q.shape[1]), n, int(max_len_hint), float(scale),
+                                   _ptr(tree_mask), int(tree_mask.shape[0]), _ptr(out),
+                                   _stream(stream)), "tq_tree_attention")
+
+
+def tq_tree_mask(parents):
+    """The int32 mask words [N, ceil(N / 32)] (a CPU tensor) of a tree whose
+    node i follows node parents[i], or the context where that is -1."""
+    import torch
+    n = len(parents)
+    words = (n + 31) // 32
+    buf = (ctypes.c_uint32 * max(n * words, 1))()
+    _check(lib().tq_tree_mask((ctypes.c_int32 * max(n, 1))(*[int(x) for x in parents]), n, buf),
+           "tq_tree_mask")
+    return torch.frombuffer(bytearray(buf), dtype=torch.int32).reshape(n, words)
+
+
+def tq_cache_compact(ctx: Context, cache: Cache, start, keep, num_keep, num_drafted: int,
+                     stream=None) -> None:
+    """Keep tokens start[b] + keep[b, :num_keep[b]] of the drafted block
+    [start[b], start[b] + num_drafted) as start[b], start[b] + 1, ... and cut
+    the sequence off behind them (all int32 on the device)."""
+    import torch
+    _tensor("start", start, torch.int32, (cache.batch,), cache)
+    _tensor("keep", keep, torch.int32, (cache.batch, None), cache)
+    _tensor("num_keep", num_keep, torch.int32, (cache.batch,), cache)
+    _check(lib().tq_cache_compact(ctypes.byref(ctx.ptr), ctypes.byref(cache.struct), _ptr(start),
+                                  int(num_drafted), _ptr(keep), _ptr(num_keep), int(keep.shape[1]),
+                                  _stream(stream)), "tq_cache_compact")
+
+
+def tq_cache_copy(ctx: Context, dst: Cache, src: Cache, dst_seq, src_seq, max_len_hint: int,
+                  num_tokens=None, stream=None) -> None:
+    """Sequence dst_seq[m] of `dst` becomes the first num_tokens[m] tokens (None:
+    all) of sequence src_seq[m] of `src`, which may be the same cache."""
+    import torch
+    m = int(dst_seq.shape[0])
+    for name, t in (("dst_seq", dst_seq), ("src_seq", src_seq), ("num_tokens", num_tokens)):
+        if t is not None:
+            _tensor(name, t, torch.int32, (m,), dst)
+    if src.v_data.device != dst.v_data.device:
+        raise ValueError("the two caches are on different devices")
+    _check(lib().tq_cache_copy(ctypes.byref(ctx.ptr), ctypes.byref(dst.struct),
+                               ctypes.byref(src.struct), _ptr(dst_seq), _ptr(src_seq),
+                               _ptr(num_tokens), m, int(max_len_hint), _stream(stream)),
+           "tq_cache_copy")
 
 
 def tq_selftest_bounded_wait(ctx: Context, limit_us: int, stream=None) -> None:

@@ -230,7 +230,7 @@ int plan_ctas(int kb, int vb, bool table, bool res, int group_rows, long long un
 }
 
 int plan_decode(const tq_cache* c, const void* q, const void* out, int num_q_heads, int tq_rows,
-                int max_len_hint, float scale, DecodePlan* pl) {
+                int max_len_hint, float scale, DecodePlan* pl, int max_rows) {
     int r = check_cache(c, &pl->kb, &pl->vb);
     if (r != TQ_OK) return r;
     if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out)) return TQ_ERR_INVALID_ARG;
@@ -241,7 +241,7 @@ int plan_decode(const tq_cache* c, const void* q, const void* out, int num_q_hea
     if (!std::isfinite(c->v_rescale)) return TQ_ERR_INVALID_ARG;
     pl->group = num_q_heads / c->num_kv_heads;
     pl->rows = pl->group * tq_rows;
-    if (pl->rows > 256) return TQ_ERR_UNSUPPORTED;
+    if (pl->rows > max_rows) return TQ_ERR_UNSUPPORTED;
     pl->group_rows = tq::group_rows_for(pl->rows, pl->kb);
     pl->row_groups = (pl->rows + pl->group_rows - 1) / pl->group_rows;
     pl->units = 1ll * c->batch * c->num_kv_heads * pl->row_groups;
@@ -255,7 +255,7 @@ int launch_decode_plan(const DecodePlan& pl, const tq_cache* c, const CodebookTa
                        const CodebookTables& vt, const uint32_t signs[4], const CUtensorMap* kmap,
                        const void* q, int num_q_heads, int tq_rows, int max_len_hint, float scale,
                        float tau, void* out, float* part, uint32_t* status, cudaStream_t stream,
-                       cudaEvent_t ev0, cudaEvent_t ev1, uint32_t* sparse_tiles) {
+                       cudaEvent_t ev0, cudaEvent_t ev1, uint32_t* sparse_tiles, const TreeMask* tree) {
     if (tau > 0.f && sparse_tiles == nullptr) return TQ_ERR_INVALID_ARG;
     const size_t slots = decode_slots(pl);
     const float sc = (scale == 0.f) ? 1.0f / std::sqrt(float(kD)) : scale;
@@ -284,6 +284,11 @@ int launch_decode_plan(const DecodePlan& pl, const tq_cache* c, const CodebookTa
     p.sparse_tau = tau;
     p.sparse_tiles = sparse_tiles;
     p.table = tq::mode_table(c->mode) ? 1 : 0;
+    if (tree != nullptr) {
+        p.tree = tree->words;
+        p.tree_words = (tq_rows + 31) / 32;
+        p.tree_per_seq = tree->shared ? 0 : tq_rows * p.tree_words;
+    }
     if (pl.kb != 16) {
         std::memcpy(p.ktab, kt.tab, sizeof(p.ktab));
         std::memcpy(p.ktab8, kt.tab8, sizeof(p.ktab8));
@@ -325,6 +330,9 @@ struct tq_ctx {
     uint32_t* d_words = nullptr;  // [0] status, [1] encode ticket counter, [2..3] sparse-V tiles, [4] encode tile counter
     float* d_work = nullptr;
     size_t work_bytes = 0;
+    // workspaces that a larger problem replaced: a CUDA graph captured with
+    // one of them still writes there, so they live until tq_free
+    std::vector<float*> old_work;
     CodebookTables ktab, vtab;
     bool signs_valid = false;
     uint64_t seed = 0;
@@ -400,6 +408,43 @@ int prepare_kmap(tq_ctx* ctx, const tq_cache* c) {
     return TQ_OK;
 }
 
+// Bytes of a K and a V record of a mode.
+void record_bytes_of(int mode, int kb, int vb, int32_t* rbk, int32_t* rbv) {
+    *rbk = tq::mode_table(mode) ? 64 : kb * 16;
+    *rbv = tq::mode_table(mode) ? 64 : vb * 16;
+}
+
+// An append's parameters but for the token counts.
+void fill_encode(tq_ctx* ctx, const tq_cache* c, const void* k_new, const void* v_new, int kb,
+                 tq::EncodeParams* p) {
+    p->k_new = static_cast<const __half*>(k_new);
+    p->v_new = static_cast<const __half*>(v_new);
+    p->k_codes = static_cast<uint8_t*>(c->k_data);
+    p->k_norm = static_cast<__half*>(c->k_norm);
+    p->v_codes = static_cast<uint8_t*>(c->v_data);
+    p->v_norm = static_cast<__half*>(c->v_norm);
+    p->lengths = c->lengths;
+    p->status = ctx->d_words;
+    p->counter = ctx->d_words + 1;
+    p->tiles_next = ctx->d_words + 4;
+    p->batch = c->batch;
+    p->hkv = c->num_kv_heads;
+    p->cap = c->capacity;
+    tq::div_magic(uint32_t(c->num_kv_heads), &p->div_h_m, &p->div_h_s);
+    std::memcpy(p->signs, ctx->signs, sizeof(p->signs));
+    if (kb != 16) {
+        std::memcpy(p->k_gt, ctx->ktab.gt, sizeof(p->k_gt));
+        std::memcpy(p->k_ge, ctx->ktab.ge, sizeof(p->k_ge));
+    }
+    std::memcpy(p->v_gt, ctx->vtab.gt, sizeof(p->v_gt));
+    std::memcpy(p->v_ge, ctx->vtab.ge, sizeof(p->v_ge));
+    if (tq::mode_table(c->mode)) {
+        p->table = 1;
+        std::memcpy(p->k_cb, c->codebook_k, sizeof(p->k_cb));
+        std::memcpy(p->v_cb, c->codebook_v, sizeof(p->v_cb));
+    }
+}
+
 // The event pair bracketing the next timed launch (none when timing is off).
 int timing_events(tq_ctx* ctx, cudaEvent_t* e0, cudaEvent_t* e1) {
     *e0 = *e1 = nullptr;
@@ -418,10 +463,18 @@ int timing_events(tq_ctx* ctx, cudaEvent_t* e0, cudaEvent_t* e1) {
 
 int ensure_work(tq_ctx* ctx, size_t bytes) {
     if (ctx->work_bytes >= bytes) return TQ_OK;
-    if (ctx->d_work) cudaFree(ctx->d_work);
-    ctx->d_work = nullptr;
-    ctx->work_bytes = 0;
-    if (cudaMalloc(&ctx->d_work, bytes) != cudaSuccess) return TQ_ERR_NOMEM;
+    // (doubled where there is room, so the replaced ones add up to less than
+    // the current one)
+    const size_t twice = std::max(bytes, 2 * ctx->work_bytes);
+    float* p = nullptr;
+    if (cudaMalloc(&p, twice) == cudaSuccess) {
+        bytes = twice;
+    } else {
+        (void)cudaGetLastError();
+        if (twice == bytes || cudaMalloc(&p, bytes) != cudaSuccess) return TQ_ERR_NOMEM;
+    }
+    if (ctx->d_work) ctx->old_work.push_back(ctx->d_work);
+    ctx->d_work = p;
     ctx->work_bytes = bytes;
     return TQ_OK;
 }
@@ -533,34 +586,9 @@ int tq_encode_append(tq_ctx** pctx, const tq_cache* c, const void* k_new, const 
     if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
     if ((r = prepare_tables(ctx, c, kb, vb)) != TQ_OK) return r;
     tq::EncodeParams p{};
-    p.k_new = static_cast<const __half*>(k_new);
-    p.v_new = static_cast<const __half*>(v_new);
-    p.k_codes = static_cast<uint8_t*>(c->k_data);
-    p.k_norm = static_cast<__half*>(c->k_norm);
-    p.v_codes = static_cast<uint8_t*>(c->v_data);
-    p.v_norm = static_cast<__half*>(c->v_norm);
-    p.lengths = c->lengths;
-    p.status = ctx->d_words;
-    p.counter = ctx->d_words + 1;
-    p.tiles_next = ctx->d_words + 4;
-    p.batch = c->batch;
-    p.hkv = c->num_kv_heads;
+    fill_encode(ctx, c, k_new, v_new, kb, &p);
     p.t_new = t_new;
-    p.cap = c->capacity;
     tq::div_magic(uint32_t(t_new), &p.div_t_m, &p.div_t_s);
-    tq::div_magic(uint32_t(c->num_kv_heads), &p.div_h_m, &p.div_h_s);
-    std::memcpy(p.signs, ctx->signs, sizeof(p.signs));
-    if (kb != 16) {
-        std::memcpy(p.k_gt, ctx->ktab.gt, sizeof(p.k_gt));
-        std::memcpy(p.k_ge, ctx->ktab.ge, sizeof(p.k_ge));
-    }
-    std::memcpy(p.v_gt, ctx->vtab.gt, sizeof(p.v_gt));
-    std::memcpy(p.v_ge, ctx->vtab.ge, sizeof(p.v_ge));
-    if (tq::mode_table(c->mode)) {
-        p.table = 1;
-        std::memcpy(p.k_cb, c->codebook_k, sizeof(p.k_cb));
-        std::memcpy(p.v_cb, c->codebook_v, sizeof(p.v_cb));
-    }
     CUtensorMap kmap, vmap;
     const uint64_t nvec = uint64_t(c->batch) * c->num_kv_heads * t_new;
     if (nvec > uint64_t(tq::kEncodeSmallMax)) {
@@ -573,18 +601,112 @@ int tq_encode_append(tq_ctx** pctx, const tq_cache* c, const void* k_new, const 
         tq::launch_encode(kb, vb, p, &kmap, &vmap, static_cast<cudaStream_t>(stream))));
 }
 
+int tq_encode_append_packed(tq_ctx** pctx, const tq_cache* c, const void* k_new, const void* v_new,
+                            const int32_t* cu_seqlens, int32_t total, void* stream) {
+    int kb, vb;
+    int r = check_cache(c, &kb, &vb);
+    if (r != TQ_OK) return r;
+    if (total < 0 || cu_seqlens == nullptr) return TQ_ERR_INVALID_ARG;
+    if (total == 0) return TQ_OK;
+    if (k_new == nullptr || v_new == nullptr || !aligned16(k_new) || !aligned16(v_new))
+        return TQ_ERR_INVALID_ARG;
+    const uint64_t nvec = uint64_t(total) * c->num_kv_heads;
+    if (nvec >= (1ull << 31)) return TQ_ERR_UNSUPPORTED;
+    tq_ctx* ctx;
+    if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
+    if ((r = prepare_tables(ctx, c, kb, vb)) != TQ_OK) return r;
+    tq::EncodeParams p{};
+    fill_encode(ctx, c, k_new, v_new, kb, &p);
+    p.cu = cu_seqlens;
+    p.total = total;
+    if (kb != 16) std::memcpy(p.k_mag, c->codebook_k + (1 << (kb - 1)), sizeof(float) << (kb - 1));
+    std::memcpy(p.v_mag, c->codebook_v + (1 << (vb - 1)), sizeof(float) << (vb - 1));
+    CUtensorMap kmap, vmap;
+    if (nvec > uint64_t(tq::kEncodeSmallMax)) {
+        if ((r = tq::host::encode_rows_map(&kmap, k_new, nvec)) != TQ_OK ||
+            (r = tq::host::encode_rows_map(&vmap, v_new, nvec)) != TQ_OK)
+            return r;
+    }
+    ctx->last_stream = static_cast<cudaStream_t>(stream);
+    return cuda_err(static_cast<cudaError_t>(
+        tq::launch_encode_packed(kb, vb, p, &kmap, &vmap, static_cast<cudaStream_t>(stream))));
+}
+
 }  // extern "C"
 
 namespace {
+
+// Arguments that both prefill calls take.
+int check_prefill(const tq_cache* c, const void* q, int32_t num_q_heads, int32_t max_len_hint, float scale,
+                  const void* out, int* kb, int* vb) {
+    int r = check_cache(c, kb, vb);
+    if (r != TQ_OK) return r;
+    if (tq::mode_table(c->mode)) return TQ_ERR_UNSUPPORTED;
+    // the prefill K tile holds fp16 centroids: exact only for fp16 levels
+    if (*kb != 16 && !tq::host::codebook_is_fp16(c->codebook_k, c->codebook_k_size)) return TQ_ERR_UNSUPPORTED;
+    if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out)) return TQ_ERR_INVALID_ARG;
+    if (num_q_heads <= 0 || num_q_heads % c->num_kv_heads != 0) return TQ_ERR_INVALID_ARG;
+    if (max_len_hint <= 0 || max_len_hint > c->capacity) return TQ_ERR_INVALID_ARG;
+    if (!(scale >= 0.f) || !std::isfinite(scale)) return TQ_ERR_INVALID_ARG;
+    if (!std::isfinite(c->v_rescale)) return TQ_ERR_INVALID_ARG;
+    if (num_q_heads / c->num_kv_heads > 128) return TQ_ERR_UNSUPPORTED;
+    return TQ_OK;
+}
+
+// The parameters that both have, tables and tensor map included.
+int fill_prefill(tq_ctx* ctx, const tq_cache* c, const void* q, int32_t num_q_heads, int32_t max_len_hint,
+                 float scale, void* out, int kb, int vb, tq::PrefillParams* p) {
+    int r = prepare_tables(ctx, c, kb, vb);
+    if (r != TQ_OK) return r;
+    if (kb == 16 && (r = prepare_kmap(ctx, c)) != TQ_OK) return r;
+    p->k_codes = static_cast<const uint8_t*>(c->k_data);
+    p->k_norm = static_cast<const __half*>(c->k_norm);
+    p->v_codes = static_cast<const uint8_t*>(c->v_data);
+    p->v_norm = static_cast<const __half*>(c->v_norm);
+    p->lengths = c->lengths;
+    p->q = static_cast<const __half*>(q);
+    p->out = static_cast<__half*>(out);
+    p->status = ctx->d_words;
+    p->batch = c->batch;
+    p->hkv = c->num_kv_heads;
+    p->hq = num_q_heads;
+    p->group = num_q_heads / c->num_kv_heads;
+    p->cap = c->capacity;
+    p->max_len = max_len_hint;
+    p->pos_per_tile = 128 / p->group;
+    const float sc = (scale == 0.f) ? 1.0f / std::sqrt(float(kD)) : scale;
+    p->scale_log2e = sc * 1.4426950408889634f;
+    p->v_rescale = c->v_rescale;
+    if (kb != 16) std::memcpy(p->ktab, ctx->ktab.tab, sizeof(p->ktab));
+    std::memcpy(p->vtab, ctx->vtab.tab, sizeof(p->vtab));
+    std::memcpy(p->signs, ctx->signs, sizeof(p->signs));
+    return TQ_OK;
+}
+
+int run_prefill(tq_ctx* ctx, int kb, int vb, const tq::PrefillParams& p, cudaStream_t s) {
+    CUtensorMap dummy;
+    std::memset(&dummy, 0, sizeof(dummy));
+    ctx->last_stream = s;
+    cudaEvent_t e0 = nullptr, e1 = nullptr;
+    int r = timing_events(ctx, &e0, &e1);
+    if (r != TQ_OK) return r;
+    if (e0) cudaEventRecord(e0, s);
+    r = tq::launch_prefill(kb, vb, p, kb == 16 ? &ctx->kmap : &dummy, s);
+    if (e1) cudaEventRecord(e1, s);
+    return r == 0 ? TQ_OK : TQ_ERR_CUDA;
+}
 
 // Both decode entry points: tau = 0 is the plain decode, tau > 0 skips the V
 // work of 16-token tiles whose softmax weights are all below tau.
 int decode_impl(tq_ctx** pctx, const tq_cache* c, const void* q, int32_t num_q_heads,
                 int32_t tq_rows, int32_t max_len_hint, float scale, float tau, void* out,
-                void* stream) {
+                void* stream, const tq::host::TreeMask* tree = nullptr) {
     tq::host::DecodePlan pl;
-    int r = tq::host::plan_decode(c, q, out, num_q_heads, tq_rows, max_len_hint, scale, &pl);
+    int r = tq::host::plan_decode(c, q, out, num_q_heads, tq_rows, max_len_hint, scale, &pl,
+                                  tree != nullptr ? tq::kMaxTreeGroup * TQ_MAX_TREE_NODES : 256);
     if (r != TQ_OK) return r;
+    // (chunk counts and their products with the grid are 32-bit in the kernels)
+    if (tree != nullptr && pl.units * ((max_len_hint + 31) / 32) >= (1ll << 30)) return TQ_ERR_UNSUPPORTED;
     tq_ctx* ctx;
     if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
     if ((r = prepare_tables(ctx, c, pl.kb, pl.vb)) != TQ_OK) return r;
@@ -597,7 +719,7 @@ int decode_impl(tq_ctx** pctx, const tq_cache* c, const void* q, int32_t num_q_h
     return tq::host::launch_decode_plan(pl, c, ctx->ktab, ctx->vtab, ctx->signs, &ctx->kmap, q,
                                         num_q_heads, tq_rows, max_len_hint, scale, tau, out,
                                         ctx->d_work, ctx->d_words, static_cast<cudaStream_t>(stream),
-                                        e0, e1, ctx->d_words + 2);
+                                        e0, e1, ctx->d_words + 2, tree);
 }
 
 }  // namespace
@@ -616,66 +738,178 @@ int tq_decode_attention_sparse_v(tq_ctx** pctx, const tq_cache* c, const void* q
     return decode_impl(pctx, c, q, num_q_heads, tq_rows, max_len_hint, scale, tau, out, stream);
 }
 
+int tq_tree_attention(tq_ctx** pctx, const tq_cache* c, const void* q, int32_t num_q_heads, int32_t tq_rows,
+                      int32_t max_len_hint, float scale, const uint32_t* tree_mask, int32_t mask_batch,
+                      void* out, void* stream) {
+    if (c == nullptr || tree_mask == nullptr || (reinterpret_cast<uintptr_t>(tree_mask) & 3u) != 0)
+        return TQ_ERR_INVALID_ARG;
+    if (mask_batch != 1 && mask_batch != c->batch) return TQ_ERR_INVALID_ARG;
+    if (tq_rows > TQ_MAX_TREE_NODES) return TQ_ERR_UNSUPPORTED;
+    if (c->num_kv_heads > 0 && num_q_heads / c->num_kv_heads > tq::kMaxTreeGroup) return TQ_ERR_UNSUPPORTED;
+    const tq::host::TreeMask tree{tree_mask, mask_batch == 1};
+    return decode_impl(pctx, c, q, num_q_heads, tq_rows, max_len_hint, scale, 0.f, out, stream, &tree);
+}
+
+int tq_tree_mask(const int32_t* parents, int32_t num_nodes, uint32_t* words) {
+    if (parents == nullptr || words == nullptr || num_nodes <= 0) return TQ_ERR_INVALID_ARG;
+    if (num_nodes > TQ_MAX_TREE_NODES) return TQ_ERR_UNSUPPORTED;
+    for (int i = 0; i < num_nodes; ++i)
+        if (parents[i] < -1 || parents[i] >= i) return TQ_ERR_INVALID_ARG;
+    const int w = (num_nodes + 31) / 32;
+    for (int i = 0; i < num_nodes; ++i) {
+        uint32_t* row = words + i * w;
+        for (int k = 0; k < w; ++k) row[k] = parents[i] >= 0 ? words[parents[i] * w + k] : 0u;
+        row[i >> 5] |= 1u << (i & 31);
+    }
+    return TQ_OK;
+}
+
 int tq_prefill_attention(tq_ctx** pctx, const tq_cache* c, const void* q, int32_t num_q_heads,
                          int32_t tq_rows, int32_t max_len_hint, float scale, void* out,
                          void* stream) {
     int kb, vb;
-    int r = check_cache(c, &kb, &vb);
+    int r = check_prefill(c, q, num_q_heads, max_len_hint, scale, out, &kb, &vb);
     if (r != TQ_OK) return r;
-    if (tq::mode_table(c->mode)) return TQ_ERR_UNSUPPORTED;
-    // the prefill K tile holds fp16 centroids: exact only for fp16 levels
-    if (kb != 16 && !tq::host::codebook_is_fp16(c->codebook_k, c->codebook_k_size)) return TQ_ERR_UNSUPPORTED;
-    if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out)) return TQ_ERR_INVALID_ARG;
-    if (num_q_heads <= 0 || num_q_heads % c->num_kv_heads != 0) return TQ_ERR_INVALID_ARG;
-    if (tq_rows <= 0 || max_len_hint <= 0 || max_len_hint > c->capacity) return TQ_ERR_INVALID_ARG;
-    if (tq_rows > max_len_hint) return TQ_ERR_INVALID_ARG;
-    if (!(scale >= 0.f) || !std::isfinite(scale)) return TQ_ERR_INVALID_ARG;
-    if (!std::isfinite(c->v_rescale)) return TQ_ERR_INVALID_ARG;
-    const int group = num_q_heads / c->num_kv_heads;
-    if (group > 128) return TQ_ERR_UNSUPPORTED;
+    if (tq_rows <= 0 || tq_rows > max_len_hint) return TQ_ERR_INVALID_ARG;
     const long long units = 1ll * c->batch * c->num_kv_heads;
     if (units > 65535) return TQ_ERR_UNSUPPORTED;
-    const int pos_per_tile = 128 / group;
-    const long long mtiles = (tq_rows + pos_per_tile - 1) / pos_per_tile;
     tq_ctx* ctx;
     if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
-    if ((r = prepare_tables(ctx, c, kb, vb)) != TQ_OK) return r;
-    if (kb == 16 && (r = prepare_kmap(ctx, c)) != TQ_OK) return r;
-
     tq::PrefillParams p{};
-    p.k_codes = static_cast<const uint8_t*>(c->k_data);
-    p.k_norm = static_cast<const __half*>(c->k_norm);
-    p.v_codes = static_cast<const uint8_t*>(c->v_data);
-    p.v_norm = static_cast<const __half*>(c->v_norm);
+    if ((r = fill_prefill(ctx, c, q, num_q_heads, max_len_hint, scale, out, kb, vb, &p)) != TQ_OK) return r;
+    p.tq = tq_rows;
+    p.mtiles = (tq_rows + p.pos_per_tile - 1) / p.pos_per_tile;
+    return run_prefill(ctx, kb, vb, p, static_cast<cudaStream_t>(stream));
+}
+
+int tq_prefill_attention_packed(tq_ctx** pctx, const tq_cache* c, const void* q, int32_t num_q_heads,
+                                const int32_t* cu_seqlens, int32_t total, int32_t max_len_hint, float scale,
+                                void* out, void* stream) {
+    int kb, vb;
+    int r = check_cache(c, &kb, &vb);
+    if (r != TQ_OK) return r;
+    if (cu_seqlens == nullptr || total < 0) return TQ_ERR_INVALID_ARG;
+    if (total == 0) return TQ_OK;
+    if ((r = check_prefill(c, q, num_q_heads, max_len_hint, scale, out, &kb, &vb)) != TQ_OK) return r;
+    tq_ctx* ctx;
+    if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
+    tq::PrefillParams p{};
+    if ((r = fill_prefill(ctx, c, q, num_q_heads, max_len_hint, scale, out, kb, vb, &p)) != TQ_OK) return r;
+    p.cu = cu_seqlens;
+    p.total = total;
+    // ceil(n / span) summed over the sequences with rows is at most this
+    const int span = 2 * p.pos_per_tile;
+    const long long slots = total / span + std::min(total, c->batch);
+    if (slots * c->num_kv_heads > 0x7fffffffll) return TQ_ERR_UNSUPPORTED;
+    p.slots = int(slots);
+    return run_prefill(ctx, kb, vb, p, static_cast<cudaStream_t>(stream));
+}
+
+int tq_cache_compact(tq_ctx** pctx, const tq_cache* c, const int32_t* start, int32_t num_drafted,
+                     const int32_t* keep, const int32_t* num_keep, int32_t max_keep, void* stream) {
+    int kb, vb;
+    int r = check_cache(c, &kb, &vb);
+    if (r != TQ_OK) return r;
+    if (start == nullptr || keep == nullptr || num_keep == nullptr) return TQ_ERR_INVALID_ARG;
+    if (num_drafted <= 0 || max_keep <= 0 || max_keep > num_drafted) return TQ_ERR_INVALID_ARG;
+    if (num_drafted > c->capacity) return TQ_ERR_CAPACITY;
+    tq_ctx* ctx;
+    if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
+    tq::CompactParams p{};
+    p.k_data = static_cast<uint8_t*>(c->k_data);
+    p.v_data = static_cast<uint8_t*>(c->v_data);
+    if (!tq::mode_table(c->mode)) {
+        if (kb != 16) p.k_norm = static_cast<__half*>(c->k_norm);
+        p.v_norm = static_cast<__half*>(c->v_norm);
+    }
     p.lengths = c->lengths;
-    p.q = static_cast<const __half*>(q);
-    p.out = static_cast<__half*>(out);
+    p.start = start;
+    p.keep = keep;
+    p.num_keep = num_keep;
     p.status = ctx->d_words;
     p.batch = c->batch;
     p.hkv = c->num_kv_heads;
-    p.hq = num_q_heads;
-    p.group = group;
-    p.tq = tq_rows;
     p.cap = c->capacity;
+    record_bytes_of(c->mode, kb, vb, &p.rbk, &p.rbv);
+    p.max_keep = max_keep;
+    p.num_drafted = num_drafted;
+    ctx->last_stream = static_cast<cudaStream_t>(stream);
+    return cuda_err(static_cast<cudaError_t>(tq::launch_compact(p, static_cast<cudaStream_t>(stream))));
+}
+
+int tq_cache_copy(tq_ctx** pctx, const tq_cache* dst, const tq_cache* src, const int32_t* dst_seq,
+                  const int32_t* src_seq, const int32_t* num_tokens, int32_t num_pairs, int32_t max_len_hint,
+                  void* stream) {
+    int kb, vb, kb2, vb2;
+    int r = check_cache(src, &kb, &vb);
+    if (r != TQ_OK) return r;
+    if ((r = check_cache(dst, &kb2, &vb2)) != TQ_OK) return r;
+    // one format: the records mean the same in both caches
+    if (dst->mode != src->mode || dst->num_kv_heads != src->num_kv_heads || dst->rot_seed != src->rot_seed ||
+        dst->v_rescale != src->v_rescale)
+        return TQ_ERR_INVALID_ARG;
+    if (kb != 16 && std::memcmp(dst->codebook_k, src->codebook_k, sizeof(float) << kb) != 0)
+        return TQ_ERR_INVALID_ARG;
+    if (std::memcmp(dst->codebook_v, src->codebook_v, sizeof(float) << vb) != 0) return TQ_ERR_INVALID_ARG;
+    if (num_pairs < 0 || max_len_hint <= 0 || max_len_hint > src->capacity) return TQ_ERR_INVALID_ARG;
+    if (num_pairs == 0) return TQ_OK;
+    if (dst_seq == nullptr || src_seq == nullptr) return TQ_ERR_INVALID_ARG;
+    tq::CopyParams p{};
+    record_bytes_of(src->mode, kb, vb, &p.rbk, &p.rbv);
+    // one cache (every buffer the same), or two that share no memory
+    p.same = src->k_data == dst->k_data;
+    const bool table = tq::mode_table(src->mode);
+    const size_t rows_s = size_t(src->batch) * src->num_kv_heads * src->capacity;
+    const size_t rows_d = size_t(dst->batch) * dst->num_kv_heads * dst->capacity;
+    struct Part {
+        const void *s, *d;
+        size_t bytes;
+    };
+    const Part parts[4] = {{src->k_data, dst->k_data, size_t(p.rbk)},
+                           {src->v_data, dst->v_data, size_t(p.rbv)},
+                           {table || kb == 16 ? nullptr : src->k_norm, table || kb == 16 ? nullptr : dst->k_norm, 2},
+                           {table ? nullptr : src->v_norm, table ? nullptr : dst->v_norm, 2}};
+    if (p.same) {
+        if (src->batch != dst->batch || src->capacity != dst->capacity || src->lengths != dst->lengths)
+            return TQ_ERR_INVALID_ARG;
+        for (const Part& a : parts)
+            if (a.s != a.d) return TQ_ERR_INVALID_ARG;
+    } else {
+        for (const Part& a : parts) {
+            if (a.s == nullptr) continue;
+            const uintptr_t s0 = reinterpret_cast<uintptr_t>(a.s), d0 = reinterpret_cast<uintptr_t>(a.d);
+            if (s0 < d0 + rows_d * a.bytes && d0 < s0 + rows_s * a.bytes) return TQ_ERR_INVALID_ARG;
+        }
+        const uintptr_t s0 = reinterpret_cast<uintptr_t>(src->lengths), d0 = reinterpret_cast<uintptr_t>(dst->lengths);
+        if (s0 < d0 + 4 * size_t(dst->batch) && d0 < s0 + 4 * size_t(src->batch)) return TQ_ERR_INVALID_ARG;
+    }
+    if (1ll * num_pairs * src->num_kv_heads * ((max_len_hint + tq::kCopyTokens - 1) / tq::kCopyTokens) > 0x7fffffffll)
+        return TQ_ERR_UNSUPPORTED;
+    tq_ctx* ctx;
+    if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
+    p.k_src = static_cast<const uint8_t*>(parts[0].s);
+    p.k_dst = static_cast<uint8_t*>(dst->k_data);
+    p.v_src = static_cast<const uint8_t*>(parts[1].s);
+    p.v_dst = static_cast<uint8_t*>(dst->v_data);
+    p.kn_src = static_cast<const __half*>(parts[2].s);
+    p.kn_dst = static_cast<__half*>(const_cast<void*>(parts[2].d));
+    p.vn_src = static_cast<const __half*>(parts[3].s);
+    p.vn_dst = static_cast<__half*>(const_cast<void*>(parts[3].d));
+    p.src_lengths = src->lengths;
+    p.dst_lengths = dst->lengths;
+    p.src = src_seq;
+    p.dst = dst_seq;
+    p.num_tokens = num_tokens;
+    p.status = ctx->d_words;
+    p.pairs = num_pairs;
+    p.hkv = src->num_kv_heads;
+    p.src_batch = src->batch;
+    p.dst_batch = dst->batch;
+    p.src_cap = src->capacity;
+    p.dst_cap = dst->capacity;
     p.max_len = max_len_hint;
-    p.pos_per_tile = pos_per_tile;
-    p.mtiles = int(mtiles);
-    const float sc = (scale == 0.f) ? 1.0f / std::sqrt(float(kD)) : scale;
-    p.scale_log2e = sc * 1.4426950408889634f;
-    p.v_rescale = c->v_rescale;
-    if (kb != 16) std::memcpy(p.ktab, ctx->ktab.tab, sizeof(p.ktab));
-    std::memcpy(p.vtab, ctx->vtab.tab, sizeof(p.vtab));
-    std::memcpy(p.signs, ctx->signs, sizeof(p.signs));
-    CUtensorMap dummy;
-    std::memset(&dummy, 0, sizeof(dummy));
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    ctx->last_stream = s;
-    cudaEvent_t e0 = nullptr, e1 = nullptr;
-    if ((r = timing_events(ctx, &e0, &e1)) != TQ_OK) return r;
-    if (e0) cudaEventRecord(e0, s);
-    r = tq::launch_prefill(kb, vb, p, kb == 16 ? &ctx->kmap : &dummy, s);
-    if (e1) cudaEventRecord(e1, s);
-    return r == 0 ? TQ_OK : TQ_ERR_CUDA;
+    ctx->last_stream = static_cast<cudaStream_t>(stream);
+    return cuda_err(static_cast<cudaError_t>(tq::launch_copy(p, static_cast<cudaStream_t>(stream))));
 }
 
 int tq_selftest_bounded_wait(tq_ctx** pctx, int32_t limit_us, void* stream) {
@@ -698,6 +932,7 @@ void tq_free(tq_ctx* ctx) {
         if (e.b) cudaEventDestroy(e.b);
     }
     if (ctx->d_work) cudaFree(ctx->d_work);
+    for (float* w : ctx->old_work) cudaFree(w);
     if (ctx->d_words) cudaFree(ctx->d_words);
     cudaSetDevice(prev);
     delete ctx;

@@ -162,6 +162,12 @@ __device__ __forceinline__ void dequant_group(const QuarterWords& q, const Table
     }
 }
 
+// Whether a row of a drafted tree sees token i of the block (i < 0: a token of
+// the context before it; the callers hold i below the block's size).
+__device__ __forceinline__ bool tree_sees(const uint32_t* row, int i) {
+    return i < 0 || ((row[i >> 5] >> (i & 31)) & 1u) != 0;
+}
+
 // Work split (token-balanced): the (batch, kv head, row group) units
 // are laid end to end as 32-token chunks, unit u holding ceil(min(len_b,
 // max_len) / 32) chunks of batch b; CTA c of P takes the global chunks
@@ -269,10 +275,24 @@ __device__ __forceinline__ Tables record_tables(const uint8_t* tab16) {
 // V tables of a table record.  Stage slots past the end of the context hold
 // stale bytes whose table could decode to inf or NaN, and a zero weight times
 // inf is NaN in the MMA, so those tokens get an all-zero table.
+// sat: values of a norm that overflowed count as +-65504 (a weight of 0 times
+// inf would be NaN in the rows that do not see the token).
 template <bool FULL>
-__device__ __forceinline__ Tables v_tables(const uint8_t* rec, bool valid) {
-    if (FULL || valid) return record_tables(rec + 48);
-    return Tables{0u, 0u, 0u, 0u};
+__device__ __forceinline__ Tables v_tables(const uint8_t* rec, bool valid, bool sat) {
+    if (FULL) return record_tables(rec + 48);
+    if (!valid) return Tables{0u, 0u, 0u, 0u};
+    if (!sat) return record_tables(rec + 48);
+    __align__(16) uint8_t tab[16];
+    const uint4 w = *reinterpret_cast<const uint4*>(rec + 48);
+    uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    const __half2 top = __half2half2(__ushort_as_half(0x7BFFu));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 v = __hmax2(__hmin2(*reinterpret_cast<const __half2*>(&ww[i]), top), __hneg2(top));
+        ww[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    *reinterpret_cast<uint4*>(tab) = make_uint4(ww[0], ww[1], ww[2], ww[3]);
+    return record_tables(tab);
 }
 
 // One CTA: 4 warps over this CTA's chunk range, one unit segment at a time.
@@ -498,7 +518,8 @@ __global__ void __launch_bounds__(128, DecCfg<KB, VB, ROWS, TAB, RES>::kMinCtas)
         // (tail / causal) and sparse paths ask
         auto row_lim = [&](int n, int e) { return L - p.tq + ((rbase + C::slot_row(n, e, t)) % p.tq); };
         auto row_ok = [&](int n, int e) { return rbase + C::slot_row(n, e, t) < p.rows; };
-        const int all_visible_below = L - p.tq + 1;  // tokens below this are seen by every row
+        // tokens below this are seen by every row (of a tree: the context before it)
+        const int all_visible_below = p.tree != nullptr ? L - p.tq : L - p.tq + 1;
 
         float O[NT][8][4];
 #pragma unroll
@@ -666,12 +687,29 @@ __global__ void __launch_bounds__(128, DecCfg<KB, VB, ROWS, TAB, RES>::kMinCtas)
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < NE; ++e) {
-                            const int lim = row_lim(n, e);
-                            x[tt][n][e] = (va && ga <= lim) ? x[tt][n][e] : -INFINITY;
-                            x[tt][n][e + 2] = (vb && gb <= lim) ? x[tt][n][e + 2] : -INFINITY;
+                            bool sa = va, sb = vb;
+                            if (p.tree != nullptr) {
+                                const uint32_t* row = p.tree + static_cast<size_t>(b) * p.tree_per_seq +
+                                                      ((rbase + C::slot_row(n, e, t)) % p.tq) * p.tree_words;
+                                sa = sa && tree_sees(row, ga - (L - p.tq));
+                                sb = sb && tree_sees(row, gb - (L - p.tq));
+                            } else {
+                                const int lim = row_lim(n, e);
+                                sa = sa && ga <= lim;
+                                sb = sb && gb <= lim;
+                            }
+                            x[tt][n][e] = sa ? x[tt][n][e] : -INFINITY;
+                            x[tt][n][e + 2] = sb ? x[tt][n][e + 2] : -INFINITY;
                         }
                     if (!va) nv[tt][0] = 0.f;
                     if (!vb) nv[tt][1] = 0.f;
+                    if (p.tree != nullptr) {
+                        // a V norm that overflowed (padding nodes of a tree may hold
+                        // anything) counts as 65504: 0 * inf would be NaN in the rows
+                        // that do not see the token
+                        nv[tt][0] = fminf(nv[tt][0], 65504.f);
+                        nv[tt][1] = fminf(nv[tt][1], 65504.f);
+                    }
                 }
             }
             // The exp2 base of a row stays at its running max until a score exceeds
@@ -781,6 +819,23 @@ __global__ void __launch_bounds__(128, DecCfg<KB, VB, ROWS, TAB, RES>::kMinCtas)
                 float nmax = fmaxf(nv[0][0], nv[0][1]);
 #pragma unroll
                 for (int tt = 1; tt < TPC; ++tt) nmax = fmaxf(nmax, fmaxf(nv[tt][0], nv[tt][1]));
+                if constexpr (!FULL) {
+                    // of a tree, only the norms of tokens that some row weighs count
+                    // (each thread looks at its own rows), so that a token nobody
+                    // sees does not move the roundings of the others
+                    if (p.tree != nullptr) {
+                        nmax = 0.f;
+#pragma unroll
+                        for (int tt = 0; tt < TPC; ++tt)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int e = 0; e < NE; ++e) {
+                                    if (x[tt][n][e] > 0.f) nmax = fmaxf(nmax, nv[tt][0]);
+                                    if (x[tt][n][e + 2] > 0.f) nmax = fmaxf(nmax, nv[tt][1]);
+                                }
+                    }
+                }
                 bigv = __any_sync(0xffffffffu, nmax > 2048.f);
             }
             (void)bigv;
@@ -817,8 +872,8 @@ __global__ void __launch_bounds__(128, DecCfg<KB, VB, ROWS, TAB, RES>::kMinCtas)
                     const QuarterWords va = load_quarter<VB>(rva + t * C::kQuarterV);
                     const QuarterWords vb = load_quarter<VB>(rvb + t * C::kQuarterV);
                     const Tables vt = v_tables_all();
-                    const Tables tva = TAB ? v_tables<FULL>(rva, tok0 + tile * 16 + g < t_end) : vt;
-                    const Tables tvb = TAB ? v_tables<FULL>(rvb, tok0 + tile * 16 + g + 8 < t_end) : vt;
+                    const Tables tva = TAB ? v_tables<FULL>(rva, tok0 + tile * 16 + g < t_end, p.tree != nullptr) : vt;
+                    const Tables tvb = TAB ? v_tables<FULL>(rvb, tok0 + tile * 16 + g + 8 < t_end, p.tree != nullptr) : vt;
                     auto vgroup = [&](auto jtag) {
                         constexpr int J = decltype(jtag)::value;
                         uint32_t ha[4], hb[4], unused[2];

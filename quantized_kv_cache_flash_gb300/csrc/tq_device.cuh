@@ -19,6 +19,7 @@ constexpr uint32_t kStatusCapacity = 1u;
 constexpr uint32_t kStatusNormOverflow = 2u;
 constexpr uint32_t kStatusShortContext = 4u;
 constexpr uint32_t kStatusPipelineStall = 8u;
+constexpr uint32_t kStatusBadIndex = 16u;
 
 // ---------------------------------------------------------------------------
 // PTX wrappers

@@ -195,11 +195,66 @@ __device__ __forceinline__ void store_norm(__half* dst_norm, uint8_t* dst, const
     *reinterpret_cast<uint4*>(dst + 48) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Packed appends: where row `tok` of the packed [total, Hkv, 128] inputs goes.
+// Sequence b owns rows cu[b] .. cu[b + 1] - 1; rows behind the last sequence,
+// rows of a sequence whose bounds are out of order or past the end, and rows
+// of a sequence that would pass its capacity go nowhere.
+struct PackedSlot {
+    int b, pos;       // sequence, token position in it
+    bool live;        // the row is written
+    bool first_over;  // the first row of a sequence that would pass the capacity
+};
+
+__device__ __forceinline__ bool packed_seq_ok(int first, int next, int total) {
+    return first >= 0 && next >= first && next <= total;
+}
+
+__device__ __forceinline__ PackedSlot packed_slot(const EncodeParams& p, int tok) {
+    // the last b with cu[b] <= tok (cu has a few KB and stays in L1)
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu[mid] <= tok) lo = mid;
+        else hi = mid;
+    }
+    PackedSlot s;
+    s.b = lo;
+    const int first = p.cu[lo], next = p.cu[lo + 1], L = p.lengths[lo];
+    const bool mine = packed_seq_ok(first, next, p.total) && tok >= first && tok < next;
+    const bool fits = L >= 0 && L <= p.cap - (next - first);
+    s.live = mine && fits;
+    s.first_over = mine && !fits && tok == first;
+    s.pos = s.live ? L + (tok - first) : 0;
+    return s;
+}
+
+// Tokens that a packed append adds to sequence b of length L (0 where it is
+// left untouched).
+__device__ __forceinline__ int packed_added(const EncodeParams& p, int b, int L) {
+    const int first = p.cu[b], next = p.cu[b + 1];
+    if (!packed_seq_ok(first, next, p.total)) {
+        atomicOr(p.status, kStatusBadIndex);
+        return 0;
+    }
+    return L >= 0 && L <= p.cap - (next - first) ? next - first : 0;
+}
+
+// Packed appends decide every code exactly.  The rotated values and the
+// thresholds carry fp32 rounding errors: about 1e-6 of the vector's norm n
+// (the sums of the transform, each of magnitude ~n, and sqrtf of a sum of
+// squares within 1.07e-6).  A vector with a value within kNearBand * n of a
+// threshold (3 in 1000 of Gaussian vectors) is encoded once more from its
+// exact transform: the sums of +-x are integers in units of 2^-24, below 2^47,
+// and the midpoints are compared in double.  So the codes do not depend on
+// which kernel or how many tokens took the vector.
+constexpr float kNearBand = 1.0f / 131072.0f;
+
 // Advance lengths[] after the last CTA of the launch has read it: one ticket
 // per CTA, taken once every thread of the CTA has read lengths[] for the last
 // time (so none sees an advanced length) and, for large appends, its
 // producer has stopped taking tiles; the counters are back at zero for the
 // next launch.
+template <bool PACKED>
 __device__ __forceinline__ void finish_append(const EncodeParams& p, int lane) {
     __shared__ unsigned int s_ticket;
     __syncthreads();
@@ -212,7 +267,11 @@ __device__ __forceinline__ void finish_append(const EncodeParams& p, int lane) {
         __threadfence();
         for (int bb = lane; bb < p.batch; bb += 32) {
             const int Lb = *((volatile int32_t*)p.lengths + bb);
-            if (Lb >= 0 && Lb + p.t_new <= p.cap) p.lengths[bb] = Lb + p.t_new;
+            if constexpr (PACKED) {
+                p.lengths[bb] = Lb + packed_added(p, bb, Lb);
+            } else {
+                if (Lb >= 0 && Lb + p.t_new <= p.cap) p.lengths[bb] = Lb + p.t_new;
+            }
         }
         if (lane == 0) {
             *((volatile uint32_t*)p.counter) = 0u;
@@ -227,6 +286,7 @@ __device__ __forceinline__ void finish_append(const EncodeParams& p, int lane) {
 // CTA writes lengths[], after every CTA has taken its ticket -- and the ticket
 // needs no fence before it: every read of lengths[] has been consumed (the
 // stores' addresses) when the CTA's threads meet at the barrier.
+template <bool PACKED>
 __device__ __forceinline__ void finish_append_small(const EncodeParams& p, int lane, int len_pre) {
     __shared__ unsigned int s_ticket;
     __syncthreads();
@@ -235,7 +295,11 @@ __device__ __forceinline__ void finish_append_small(const EncodeParams& p, int l
     if (s_ticket == gridDim.x - 1 && threadIdx.x < 32) {
         for (int bb = lane; bb < p.batch; bb += 32) {
             const int Lb = bb < 32 ? len_pre : *((volatile int32_t*)p.lengths + bb);
-            if (Lb >= 0 && Lb + p.t_new <= p.cap) p.lengths[bb] = Lb + p.t_new;
+            if constexpr (PACKED) {
+                p.lengths[bb] = Lb + packed_added(p, bb, Lb);
+            } else {
+                if (Lb >= 0 && Lb + p.t_new <= p.cap) p.lengths[bb] = Lb + p.t_new;
+            }
         }
         if (lane == 0) {
             *((volatile uint32_t*)p.counter) = 0u;
@@ -243,6 +307,103 @@ __device__ __forceinline__ void finish_append_small(const EncodeParams& p, int l
         }
         __threadfence();
     }
+}
+
+// The record of a vector whose codes the warp holds, lane l those of dims
+// 4l .. 4l + 3.
+template <int BITS>
+__device__ __forceinline__ void store_codes_warp(const uint32_t (&code)[4], uint8_t* dst, int lane) {
+    if constexpr (BITS == 4) {
+        // word k = dims 8k..8k+7 (lanes 2k, 2k+1): rank of dim 8k+j in bits
+        // 4j..4j+2; sign of dim 8k+j (j < 4) in bit 8j+7, of dim 8k+4+j in bit 8j+3
+        const bool upper = (lane & 1) != 0;
+        uint32_t part = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            part |= (code[i] & 7u) << (4 * i + (upper ? 16 : 0));
+            part |= (code[i] >> 3) << (8 * i + (upper ? 3 : 7));
+        }
+        const uint32_t other = __shfl_down_sync(0xffffffffu, part, 1);
+        if (!upper) reinterpret_cast<uint32_t*>(dst)[lane >> 1] = part | other;
+    } else {
+        // quarter q = lanes 8q..8q+7; lanes 8q+2k, 8q+2k+1 carry dims 32q+8k..+7
+        // (word k's nibbles); lanes 8q+6, 8q+7 carry dims 32q+24..31, whose
+        // code bit k goes to bit 4j+3 of word k.
+        const uint32_t nib = (code[0] & 7u) | ((code[1] & 7u) << 4) | ((code[2] & 7u) << 8) |
+                             ((code[3] & 7u) << 12);
+        uint32_t sp[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            sp[k] = (((code[0] >> k) & 1u) << 3) | (((code[1] >> k) & 1u) << 7) |
+                    (((code[2] >> k) & 1u) << 11) | (((code[3] >> k) & 1u) << 15);
+        const int qb = lane & ~7;
+        const uint32_t up = __shfl_down_sync(0xffffffffu, nib, 1);
+        uint32_t spw[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t s6 = __shfl_sync(0xffffffffu, sp[k], qb + 6);
+            const uint32_t s7 = __shfl_sync(0xffffffffu, sp[k], qb + 7);
+            spw[k] = s6 | (s7 << 16);
+        }
+        const int sub = lane & 7;
+        if (sub < 6 && (sub & 1) == 0) {
+            const int k = sub >> 1;
+            const uint32_t word = nib | (up << 16) | (k == 0 ? spw[0] : (k == 1 ? spw[1] : spw[2]));
+            reinterpret_cast<uint32_t*>(dst)[(lane >> 3) * 3 + k] = word;
+        }
+    }
+}
+
+// The codes of one vector from its exact transform (the warp's lane l holds
+// dims 4l .. 4l + 3 of x): Y = H (s * x) in integer units of 2^-24, compared
+// with the midpoints of the codebook (mag: its positive half) times sqrt(128) n
+// in double; ties to the lower index.
+template <int BITS>
+__device__ __noinline__ void encode_exact_warp(const uint2 raw, uint8_t* dst, const uint32_t (&signs)[4],
+                                               const float* mag, int lane) {
+    constexpr int H = 1 << (BITS - 1);
+    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&raw.x));
+    const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&raw.y));
+    const float x[4] = {f0.x, f0.y, f1.x, f1.y};
+    double ss = 0.0;   // (the square of an fp16 value is exact in double)
+    long long y[4];
+    const uint32_t sn = sign_nibble(signs, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        ss += static_cast<double>(x[i]) * static_cast<double>(x[i]);
+        const long long v = fp16_scaled_int(x[i]);
+        y[i] = ((sn >> i) & 1u) ? -v : v;
+    }
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+    const long long a0 = y[0] + y[1], a1 = y[0] - y[1], a2 = y[2] + y[3], a3 = y[2] - y[3];
+    y[0] = a0 + a2;
+    y[2] = a0 - a2;
+    y[1] = a1 + a3;
+    y[3] = a1 - a3;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long o = __shfl_xor_sync(0xffffffffu, y[i], m);
+            y[i] = (lane & m) ? (o - y[i]) : (y[i] + o);
+        }
+    }
+    const double unit = sqrt(128.0 * ss) * 16777216.0;   // sqrt(128) n in units of 2^-24
+    uint32_t code[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool neg = !(y[i] > 0);
+        const double a = fabs(static_cast<double>(y[i]));
+        uint32_t rank = 0;
+#pragma unroll
+        for (int k = 0; k < H - 1; ++k) {
+            const double t = 0.5 * (static_cast<double>(mag[k]) + static_cast<double>(mag[k + 1])) * unit;
+            rank += (neg ? (a >= t && a > 0.0) : a > t) ? 1u : 0u;
+        }
+        code[i] = (neg ? static_cast<uint32_t>(H) : 0u) | rank;
+    }
+    store_codes_warp<BITS>(code, dst, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -292,9 +453,11 @@ __device__ __forceinline__ float fma_sq_f16(unsigned short x, float acc) {
 //          dim 8k+j, bit 4j+3 = bit k of the code of dim 24+j.
 //   4-bit: word k = dims 8k..8k+7: rank of dim 8k+j in bits 4j..4j+2, the
 //          sign of dim 8k+j (j < 4) in bit 8j+7, of dim 8k+4+j in bit 8j+3.
-template <int BITS>
+//   NEAR: near becomes at most the smallest distance of a |y| from a T_k or 0.
+template <int BITS, bool NEAR>
 __device__ __forceinline__ void pack_quarter(const uint32_t (&r)[32],
-                                             const float (&T)[(1 << (BITS - 1)) - 1], uint32_t* w) {
+                                             const float (&T)[(1 << (BITS - 1)) - 1], uint32_t* w,
+                                             float& near) {
     auto shin = [](uint32_t acc, uint32_t v) { return __funnelshift_l(v, acc, 1); };  // acc << 1 | v >> 31
     if constexpr (BITS == 3) {
         struct Bits {
@@ -304,6 +467,8 @@ __device__ __forceinline__ void pack_quarter(const uint32_t (&r)[32],
             const float y = __uint_as_float(r[i]);
             const float a = fabsf(y);
             const float d0 = T[0] - a, d1 = T[1] - a, d2 = T[2] - a;
+            if constexpr (NEAR)
+                near = fminf(fminf(near, a), fminf(fminf(fabsf(d0), fabsf(d1)), fabsf(d2)));
             Bits o;
             o.b1 = fbits(d1);
             o.b0 = fbits(d0) ^ fbits(d1) ^ fbits(d2);
@@ -336,6 +501,11 @@ __device__ __forceinline__ void pack_quarter(const uint32_t (&r)[32],
                 uint32_t d[7];
 #pragma unroll
                 for (int t = 0; t < 7; ++t) d[t] = fbits(T[t] - a);
+                if constexpr (NEAR) {
+                    near = fminf(near, a);
+#pragma unroll
+                    for (int t = 0; t < 7; ++t) near = fminf(near, fabsf(__uint_as_float(d[t])));
+                }
                 const uint32_t x135 = d[1] ^ d[3] ^ d[5];
                 b2[j] = d[3];
                 b1[j] = x135;
@@ -412,7 +582,7 @@ __device__ __forceinline__ void build_rotation_b(uint8_t* sB, const uint32_t (&s
 constexpr int kTcEncWarps = 8;
 constexpr int kTcThreads = 32 * (kTcEncWarps + 1);
 
-template <int KB, int VB>
+template <int KB, int VB, bool PACKED>
 __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
     tq_encode_tc_kernel(const __grid_constant__ EncodeParams p, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
@@ -422,7 +592,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
     const int tid = threadIdx.x;
     const int lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int nvec = p.batch * p.hkv * p.t_new;   // below 2^31 (the host checks)
+    const int nvec = PACKED ? p.total * p.hkv : p.batch * p.hkv * p.t_new;   // below 2^31 (the host checks)
     const int tiles_s = (nvec + kTcVecs - 1) / kTcVecs;
     const int tiles_k = (KB == 0) ? 0 : tiles_s;
     const int tiles = tiles_k + tiles_s;
@@ -545,6 +715,14 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
             for (long long i = static_cast<long long>(blockIdx.x) * (32 * kTcEncWarps) + tid; i < n16;
                  i += static_cast<long long>(gridDim.x) * (32 * kTcEncWarps)) {
                 const int v = static_cast<int>(i >> 4);
+                if constexpr (PACKED) {
+                    const int tok = static_cast<int>((static_cast<uint64_t>(v) * p.div_h_m) >> p.div_h_s);
+                    const PackedSlot ps = packed_slot(p, tok);
+                    if (!ps.live) continue;   // (the V rows raise the status)
+                    const size_t pos = (static_cast<size_t>(ps.b) * p.hkv + (v - tok * p.hkv)) * p.cap + ps.pos;
+                    reinterpret_cast<uint4*>(p.k_codes + pos * 256)[i & 15] = reinterpret_cast<const uint4*>(p.k_new)[i];
+                    continue;
+                }
                 const int bh = static_cast<int>((static_cast<uint64_t>(v) * p.div_t_m) >> p.div_t_s);
                 const int t = v - bh * p.t_new;
                 const int b = static_cast<int>((static_cast<uint64_t>(bh) * p.div_h_m) >> p.div_h_s);
@@ -571,10 +749,19 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
             // where this thread's vector goes: lengths[] is read now and
             // looked at only after the norm
             const bool in_range = v < nvec;
-            const int bh = static_cast<int>((static_cast<uint64_t>(in_range ? v : 0) * p.div_t_m) >> p.div_t_s);
-            const int tt = (in_range ? v : 0) - bh * p.t_new;
-            const int b = static_cast<int>((static_cast<uint64_t>(bh) * p.div_h_m) >> p.div_h_s);
-            const int L = p.lengths[b];
+            int bh = 0, tt = 0, b = 0, L = 0;
+            PackedSlot ps{};
+            if constexpr (PACKED) {
+                const int vv = in_range ? v : 0;
+                const int tok = static_cast<int>((static_cast<uint64_t>(vv) * p.div_h_m) >> p.div_h_s);
+                ps = packed_slot(p, tok);
+                tt = vv - tok * p.hkv;   // the KV head
+            } else {
+                bh = static_cast<int>((static_cast<uint64_t>(in_range ? v : 0) * p.div_t_m) >> p.div_t_s);
+                tt = (in_range ? v : 0) - bh * p.t_new;
+                b = static_cast<int>((static_cast<uint64_t>(bh) * p.div_h_m) >> p.div_h_s);
+                L = p.lengths[b];
+            }
             // norm: the exact squares of the fp16 inputs summed in fp32 by 8
             // accumulators of 16 terms each, then pairwise: each square goes
             // through at most 15 + 3 = 18 roundings; certified or redone exactly
@@ -610,7 +797,11 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
 
             bool valid = in_range;
             size_t pos = 0;
-            if (valid) {
+            if constexpr (PACKED) {
+                if (in_range && is_v && tt == 0 && ps.first_over) atomicOr(p.status, kStatusCapacity);
+                valid = in_range && ps.live;
+                pos = (static_cast<size_t>(ps.b) * p.hkv + tt) * p.cap + ps.pos;
+            } else if (valid) {
                 if (L < 0 || L + p.t_new > p.cap) {
                     if (!is_v && tt == 0 && bh == b * p.hkv) atomicOr(p.status, kStatusCapacity);
                     valid = false;
@@ -634,6 +825,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
             if (lane == 0) mbar_arrive(bar_xfree + 8 * g);   // X read here and by the MMA
             tc_fence_after();
             const float scale = sqrtf(S32) * 11.313708498984761f;   // sqrt(128) n
+            float near = INFINITY;
             auto encode_vec = [&](auto bits_tag) {
                 constexpr int BITS = decltype(bits_tag)::value;
                 constexpr int NT = (1 << (BITS - 1)) - 1;
@@ -652,8 +844,8 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
                     tmem_ld32_issue(tacc + 64 * h, ra);
                     tmem_ld32_issue(tacc + 64 * h + 32, rb);
                     tmem_ld_wait(ra, rb);
-                    pack_quarter<BITS>(ra, T, w);
-                    pack_quarter<BITS>(rb, T, w + BITS);
+                    pack_quarter<BITS, PACKED>(ra, T, w, near);
+                    pack_quarter<BITS, PACKED>(rb, T, w + BITS, near);
                     if (valid) {
                         uint8_t* d = dst + h * 8 * BITS;
                         if constexpr (BITS == 4) {
@@ -678,10 +870,28 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_afree + 8 * g);
+            if constexpr (PACKED) {
+                // vectors too near a threshold, one at a time by the whole warp
+                // (a zero vector's codes are right: every y and T is 0)
+                unsigned redo = __ballot_sync(0xffffffffu, valid && S32 > 0.f && near <= kNearBand * sqrtf(S32));
+                while (redo) {
+                    const int src = __ffs(redo) - 1;
+                    redo &= redo - 1;
+                    const unsigned long long at =
+                        __shfl_sync(0xffffffffu, static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(dst)), src);
+                    const int vs = __shfl_sync(0xffffffffu, v, src);
+                    const __half* x = (is_v ? p.v_new : p.k_new) + static_cast<size_t>(vs) * kD;
+                    const uint2 raw = reinterpret_cast<const uint2*>(x)[lane];
+                    uint8_t* const out = reinterpret_cast<uint8_t*>(static_cast<uintptr_t>(at));
+                    __syncwarp();   // after that lane's own stores of the record
+                    if (is_v) encode_exact_warp<VB>(raw, out, p.signs, p.v_mag, lane);
+                    else encode_exact_warp<(KB == 0 ? VB : KB)>(raw, out, p.signs, p.k_mag, lane);
+                }
+            }
         }
         if (stalled && lane == 0) atomicOr(p.status, kStatusPipelineStall);
     }
-    finish_append(p, lane);   // every thread has read lengths[] for the last time, no more tiles taken
+    finish_append<PACKED>(p, lane);   // every thread has read lengths[] for the last time, no more tiles taken
     tc_fence_before();
     __syncthreads();
     if (warp == kTcEncWarps) tmem_dealloc(tmem, 256);
@@ -693,11 +903,12 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
 // fp32 midpoints (the large-append kernel compares the unnormalised value with
 // scaled thresholds: elements within ~1e-6 of a midpoint may round the other
 // way there).
-template <int BITS>
+template <int BITS, bool PACKED>
 __device__ __forceinline__ void encode_vector_warp(const uint2 raw, uint8_t* dst,
                                                    __half* dst_norm, const float* tcb,
                                                    const uint32_t (&signs)[4], const float* gt,
-                                                   const float* ge, uint32_t* status, int lane) {
+                                                   const float* ge, const float* mag, uint32_t* status,
+                                                   int lane) {
     const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&raw.x));
     const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&raw.y));
     float x[4] = {f0.x, f0.y, f1.x, f1.y};
@@ -741,123 +952,117 @@ __device__ __forceinline__ void encode_vector_warp(const uint2 raw, uint8_t* dst
     uint32_t code[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) code[i] = quantize_code<BITS>(x[i] * inv, gt, ge, any_tie);
-
-    if constexpr (BITS == 4) {
-        // word k = dims 8k..8k+7 (lanes 2k, 2k+1): rank of dim 8k+j in bits
-        // 4j..4j+2; sign of dim 8k+j (j < 4) in bit 8j+7, of dim 8k+4+j in bit 8j+3
-        const bool upper = (lane & 1) != 0;
-        uint32_t part = 0;
+    if constexpr (PACKED) {
+        // the same band around the thresholds as in the large-append kernel
+        float near = INFINITY;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            part |= (code[i] & 7u) << (4 * i + (upper ? 16 : 0));
-            part |= (code[i] >> 3) << (8 * i + (upper ? 3 : 7));
-        }
-        const uint32_t other = __shfl_down_sync(0xffffffffu, part, 1);
-        if (!upper) reinterpret_cast<uint32_t*>(dst)[lane >> 1] = part | other;
-    } else {
-        // quarter q = lanes 8q..8q+7; lanes 8q+2k, 8q+2k+1 carry dims 32q+8k..+7
-        // (word k's nibbles); lanes 8q+6, 8q+7 carry dims 32q+24..31, whose
-        // code bit k goes to bit 4j+3 of word k.
-        const uint32_t nib = (code[0] & 7u) | ((code[1] & 7u) << 4) | ((code[2] & 7u) << 8) |
-                             ((code[3] & 7u) << 12);
-        uint32_t sp[3];
+            const float a = fabsf(x[i] * inv);
+            near = fminf(near, a);
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
-            sp[k] = (((code[0] >> k) & 1u) << 3) | (((code[1] >> k) & 1u) << 7) |
-                    (((code[2] >> k) & 1u) << 11) | (((code[3] >> k) & 1u) << 15);
-        const int qb = lane & ~7;
-        const uint32_t up = __shfl_down_sync(0xffffffffu, nib, 1);
-        uint32_t spw[3];
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const uint32_t s6 = __shfl_sync(0xffffffffu, sp[k], qb + 6);
-            const uint32_t s7 = __shfl_sync(0xffffffffu, sp[k], qb + 7);
-            spw[k] = s6 | (s7 << 16);
+            for (int k = 0; k < H - 1; ++k) near = fminf(near, fabsf(gt[k] - a));
         }
-        const int sub = lane & 7;
-        if (sub < 6 && (sub & 1) == 0) {
-            const int k = sub >> 1;
-            const uint32_t word = nib | (up << 16) | (k == 0 ? spw[0] : (k == 1 ? spw[1] : spw[2]));
-            reinterpret_cast<uint32_t*>(dst)[(lane >> 3) * 3 + k] = word;
+        if (n > 0.f && __any_sync(0xffffffffu, near <= kNearBand * 0.08838834764831845f)) {
+            encode_exact_warp<BITS>(raw, dst, signs, mag, lane);
+            return;
         }
     }
+
+    store_codes_warp<BITS>(code, dst, lane);
 }
 
 // grid: 4 warps per CTA, warp = (K-or-V, vector).  KB = 0 copies fp16 K rows.
-template <int KB, int VB>
+template <int KB, int VB, bool PACKED>
 __global__ void __launch_bounds__(128) tq_encode_small_kernel(const __grid_constant__ EncodeParams p) {
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     const long long gw = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const long long nvec = static_cast<long long>(p.batch) * p.hkv * p.t_new;
+    const long long nvec = PACKED ? static_cast<long long>(p.total) * p.hkv
+                                  : static_cast<long long>(p.batch) * p.hkv * p.t_new;
     // lengths[lane] for the last CTA's update (warp 0), read now with the rest
     const int len_pre = (threadIdx.x < 32 && lane < p.batch) ? p.lengths[lane] : 0;
     if (gw < 2 * nvec) {
         const int which = static_cast<int>(gw & 1);  // 0 = K, 1 = V
         const long long v = gw >> 1;
-        const int t = static_cast<int>(v % p.t_new);
-        const long long bh = v / p.t_new;
-        const int b = static_cast<int>(bh / p.hkv);
         // the vector does not depend on the length: both loads go out together
         const __half* src = (which ? p.v_new : p.k_new) + v * kD;
         const uint2 raw = reinterpret_cast<const uint2*>(src)[lane];
-        const int L = p.lengths[b];
-        if (L < 0 || L + p.t_new > p.cap) {
-            if (lane == 0 && which == 0 && t == 0 && (bh % p.hkv) == 0)
-                atomicOr(p.status, kStatusCapacity);
+        bool live, first_over;   // first_over: one thread's per sequence that would pass the capacity
+        size_t pos;
+        if constexpr (PACKED) {
+            const int tok = static_cast<int>(v / p.hkv), h = static_cast<int>(v) - tok * p.hkv;
+            const PackedSlot ps = packed_slot(p, tok);
+            live = ps.live;
+            first_over = ps.first_over && h == 0;
+            pos = (static_cast<size_t>(ps.b) * p.hkv + h) * p.cap + ps.pos;
         } else {
-            const size_t pos = static_cast<size_t>(bh) * p.cap + L + t;
+            const int t = static_cast<int>(v % p.t_new);
+            const long long bh = v / p.t_new;
+            const int b = static_cast<int>(bh / p.hkv);
+            const int L = p.lengths[b];
+            live = !(L < 0 || L + p.t_new > p.cap);
+            first_over = !live && t == 0 && (bh % p.hkv) == 0;
+            pos = static_cast<size_t>(bh) * p.cap + L + t;
+        }
+        if (!live) {
+            if (lane == 0 && which == 0 && first_over) atomicOr(p.status, kStatusCapacity);
+        } else {
             if (which == 0) {
                 if constexpr (KB == 0) {
                     reinterpret_cast<uint2*>(p.k_codes + pos * 256)[lane] = raw;
                 } else {
-                    encode_vector_warp<KB>(raw, p.k_codes + pos * (p.table ? 64 : KB * 16),
-                                           p.k_norm + pos, p.table ? p.k_cb : nullptr, p.signs,
-                                           p.k_gt, p.k_ge, p.status, lane);
+                    encode_vector_warp<KB, PACKED>(raw, p.k_codes + pos * (p.table ? 64 : KB * 16),
+                                                   p.k_norm + pos, p.table ? p.k_cb : nullptr, p.signs,
+                                                   p.k_gt, p.k_ge, p.k_mag, p.status, lane);
                 }
             } else {
-                encode_vector_warp<VB>(raw, p.v_codes + pos * (p.table ? 64 : VB * 16),
-                                       p.v_norm + pos, p.table ? p.v_cb : nullptr, p.signs,
-                                       p.v_gt, p.v_ge, p.status, lane);
+                encode_vector_warp<VB, PACKED>(raw, p.v_codes + pos * (p.table ? 64 : VB * 16),
+                                               p.v_norm + pos, p.table ? p.v_cb : nullptr, p.signs,
+                                               p.v_gt, p.v_ge, p.v_mag, p.status, lane);
             }
         }
     }
-    finish_append_small(p, lane, len_pre);
+    finish_append_small<PACKED>(p, lane, len_pre);
 }
 
 
-template <int KB, int VB>
-static int launch_encode_tc(const EncodeParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
-                            dim3 grid, cudaStream_t stream) {
+template <int KB, int VB, bool PACKED>
+static int launch_encode_t(const EncodeParams& p, long long nvec, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                           cudaStream_t stream) {
+    if (nvec <= kEncodeSmallMax) {   // a warp per vector: short chains for small appends
+        const dim3 grid(static_cast<unsigned int>((2 * nvec + 3) / 4));
+        return launch_pdl(tq_encode_small_kernel<KB, VB, PACKED>, grid, dim3(128), 0, stream, p);
+    }
+    if (kmap == nullptr || vmap == nullptr) return cudaErrorInvalidValue;
+    const long long tiles = (KB == 0 ? 1 : 2) * ((nvec + kTcVecs - 1) / kTcVecs);
+    const dim3 grid(static_cast<unsigned int>(std::min<long long>(tiles, 152ll * kTcCtasPerSm)));
     static std::atomic<uint64_t> attr_done{0};   // two CTAs' shared memory: the largest carveout
-    const cudaError_t e = set_smem_attr_once(tq_encode_tc_kernel<KB, VB>, kTcSmemAlloc, attr_done, 100);
+    const cudaError_t e = set_smem_attr_once(tq_encode_tc_kernel<KB, VB, PACKED>, kTcSmemAlloc, attr_done, 100);
     if (e != cudaSuccess) return e;
-    return launch_pdl(tq_encode_tc_kernel<KB, VB>, grid, dim3(kTcThreads), kTcSmemAlloc, stream, p, *kmap,
+    return launch_pdl(tq_encode_tc_kernel<KB, VB, PACKED>, grid, dim3(kTcThreads), kTcSmemAlloc, stream, p, *kmap,
                       *vmap);
+}
+
+template <bool PACKED>
+static int launch_encode_bits(int kbits, int vbits, const EncodeParams& p, long long nvec, const CUtensorMap* kmap,
+                              const CUtensorMap* vmap, cudaStream_t stream) {
+    if (kbits == 16 && vbits == 4) return launch_encode_t<0, 4, PACKED>(p, nvec, kmap, vmap, stream);
+    if (kbits == 3 && vbits == 3) return launch_encode_t<3, 3, PACKED>(p, nvec, kmap, vmap, stream);
+    if (kbits == 4 && vbits == 4) return launch_encode_t<4, 4, PACKED>(p, nvec, kmap, vmap, stream);
+    if (kbits == 16 && vbits == 3) return launch_encode_t<0, 3, PACKED>(p, nvec, kmap, vmap, stream);
+    if (kbits == 4 && vbits == 3) return launch_encode_t<4, 3, PACKED>(p, nvec, kmap, vmap, stream);
+    return cudaErrorInvalidValue;
 }
 
 int launch_encode(int kbits, int vbits, const EncodeParams& p, const CUtensorMap* kmap,
                   const CUtensorMap* vmap, cudaStream_t stream) {
-    const long long nvec = 1ll * p.batch * p.hkv * p.t_new;
-    if (nvec <= kEncodeSmallMax) {   // a warp per vector: short chains for small appends
-        const dim3 grid(static_cast<unsigned int>((2 * nvec + 3) / 4)), block(128);
-        if (kbits == 16 && vbits == 4) return launch_pdl(tq_encode_small_kernel<0, 4>, grid, block, 0, stream, p);
-        if (kbits == 3 && vbits == 3) return launch_pdl(tq_encode_small_kernel<3, 3>, grid, block, 0, stream, p);
-        if (kbits == 4 && vbits == 4) return launch_pdl(tq_encode_small_kernel<4, 4>, grid, block, 0, stream, p);
-        if (kbits == 16 && vbits == 3) return launch_pdl(tq_encode_small_kernel<0, 3>, grid, block, 0, stream, p);
-        if (kbits == 4 && vbits == 3) return launch_pdl(tq_encode_small_kernel<4, 3>, grid, block, 0, stream, p);
-        return cudaErrorInvalidValue;
-    }
-    if (kmap == nullptr || vmap == nullptr) return cudaErrorInvalidValue;
-    const long long tiles = (kbits == 16 ? 1 : 2) * ((nvec + kTcVecs - 1) / kTcVecs);
-    const dim3 grid(static_cast<unsigned int>(std::min<long long>(tiles, 152ll * kTcCtasPerSm)));
-    if (kbits == 16 && vbits == 4) return launch_encode_tc<0, 4>(p, kmap, vmap, grid, stream);
-    if (kbits == 3 && vbits == 3) return launch_encode_tc<3, 3>(p, kmap, vmap, grid, stream);
-    if (kbits == 4 && vbits == 4) return launch_encode_tc<4, 4>(p, kmap, vmap, grid, stream);
-    if (kbits == 16 && vbits == 3) return launch_encode_tc<0, 3>(p, kmap, vmap, grid, stream);
-    if (kbits == 4 && vbits == 3) return launch_encode_tc<4, 3>(p, kmap, vmap, grid, stream);
-    return cudaErrorInvalidValue;
+    return launch_encode_bits<false>(kbits, vbits, p, 1ll * p.batch * p.hkv * p.t_new, kmap, vmap, stream);
+}
+
+int launch_encode_packed(int kbits, int vbits, const EncodeParams& p, const CUtensorMap* kmap,
+                         const CUtensorMap* vmap, cudaStream_t stream) {
+    return launch_encode_bits<true>(kbits, vbits, p, 1ll * p.total * p.hkv, kmap, vmap, stream);
 }
 
 }  // namespace tq

@@ -41,7 +41,14 @@ struct DecodeParams {
     uint32_t ktab8[2];
     int32_t res_shift;
     int32_t k_res;            // 1: the K codebook has entries that are not fp16 values
+    // Tree attention (tree != null): the last tq tokens are a drafted block,
+    // row j sees every token before it and token i of it where bit i of its
+    // words tree[b * tree_per_seq + j * tree_words ..] is set.
+    const uint32_t* tree;
+    int32_t tree_words, tree_per_seq;   // tree_per_seq 0: one mask for all sequences
 };
+
+constexpr int kMaxTreeGroup = 128;      // query heads per KV head of a tree
 
 struct CombineParams {
     const float* part_o;
@@ -76,6 +83,11 @@ struct EncodeParams {
     // table records: 48 bytes of 3-bit codes + fp16(c_j * n16), j = 0..7
     int32_t table;
     float k_cb[8], v_cb[8];
+    // packed appends (cu != null): k_new, v_new are [total, Hkv, 128] and
+    // sequence b's tokens are rows cu[b] .. cu[b + 1] - 1 (t_new is not used)
+    const int32_t* cu;        // [B + 1]
+    int32_t total;
+    float k_mag[8], v_mag[8]; // the positive half of the codebooks, ascending
 };
 
 // Chunked-prefill attention (tcgen05) parameters.  One CTA = one (query
@@ -94,6 +106,45 @@ struct PrefillParams {
     int32_t mtiles;           // tiles per kv head
     float scale_log2e, v_rescale;
     uint32_t ktab[4], vtab[4], signs[4];
+    // packed sequences (cu != null): q and out are [total, Hq, 128], sequence
+    // b's rows cu[b] .. cu[b + 1] - 1 (tq and mtiles are not used)
+    const int32_t* cu;        // [B + 1]
+    int32_t total;
+    int32_t slots;            // query tile pairs of all sequences, at most
+};
+
+// Keeping the accepted tokens of a drafted block (see tq_cache_compact).
+struct CompactParams {
+    uint8_t* k_data;          // packed codes, table records or fp16 K rows
+    uint8_t* v_data;
+    __half* k_norm;           // null where the mode has none
+    __half* v_norm;
+    int32_t* lengths;
+    const int32_t* start;     // [B] first token of the drafted block
+    const int32_t* keep;      // [B, max_keep] places in the block, ascending
+    const int32_t* num_keep;  // [B]
+    uint32_t* status;
+    int32_t batch, hkv, cap, rbk, rbv, max_keep, num_drafted;
+};
+
+// Copying sequences (see tq_cache_copy).
+struct CopyParams {
+    const uint8_t* k_src;
+    const uint8_t* v_src;
+    const __half* kn_src;     // null where the mode has none
+    const __half* vn_src;
+    uint8_t* k_dst;
+    uint8_t* v_dst;
+    __half* kn_dst;
+    __half* vn_dst;
+    const int32_t* src_lengths;
+    int32_t* dst_lengths;
+    const int32_t* src;       // [pairs] sequence of the source cache
+    const int32_t* dst;       // [pairs] sequence of the destination cache
+    const int32_t* num_tokens;  // [pairs], or null: the whole source
+    uint32_t* status;
+    int32_t pairs, hkv, src_batch, dst_batch, src_cap, dst_cap, rbk, rbv, max_len;
+    int32_t same;             // 1: source and destination are one cache
 };
 
 // Division of 0 <= n < 2^31 by a constant d >= 1 as a multiply-high: with
@@ -118,12 +169,19 @@ int launch_combine(const CombineParams& p, cudaStream_t stream);
 constexpr long long kEncodeSmallMax = 4096;
 int launch_encode(int kbits, int vbits, const EncodeParams& p, const CUtensorMap* kmap,
                   const CUtensorMap* vmap, cudaStream_t stream);
+// The same for packed appends (p.cu); nvec = p.total * p.hkv decides the kernel.
+int launch_encode_packed(int kbits, int vbits, const EncodeParams& p, const CUtensorMap* kmap,
+                         const CUtensorMap* vmap, cudaStream_t stream);
 
 // Resident CTAs per SM of a decode variant (for the host split planner);
 // res: the variant with the centroid residual product.
 int decode_ctas_per_sm(int kbits, int vbits, int group_rows, bool table, bool res);
 int launch_prefill(int kbits, int vbits, const PrefillParams& p, const CUtensorMap* kmap,
-                   cudaStream_t stream);
+                   cudaStream_t stream);   // packed sequences where p.cu is set
+int launch_compact(const CompactParams& p, cudaStream_t stream);
+// CTAs = pairs * hkv * ceil(max_len / kCopyTokens), below 2^31
+constexpr int kCopyTokens = 256;
+int launch_copy(const CopyParams& p, cudaStream_t stream);
 int launch_selftest_stall(uint32_t* status, uint64_t limit_ns, cudaStream_t stream);
 
 // Query rows per row group for `rows` query rows of one KV head: 4 when K is
@@ -228,8 +286,14 @@ struct DecodePlan {
     long long units;   // (batch, kv head, row group) units
     int ctas;          // decode grid
 };
+// (max_rows: query rows per KV head that the caller takes)
 int plan_decode(const tq_cache* c, const void* q, const void* out, int num_q_heads, int tq_rows,
-                int max_len_hint, float scale, DecodePlan* pl);
+                int max_len_hint, float scale, DecodePlan* pl, int max_rows = 256);
+// The mask of a drafted tree: words[(shared ? 0 : b)][tq][ceil(tq / 32)].
+struct TreeMask {
+    const uint32_t* words;
+    bool shared;
+};
 // Split-K scratch of a plan: (ctas + units) slots of 16 rows x (128 + 2) floats.
 inline size_t decode_slots(const DecodePlan& pl) { return size_t(pl.ctas + pl.units) * 16; }
 // Launch the decode and combine kernels of a plan on `stream`, the partials
@@ -239,7 +303,8 @@ int launch_decode_plan(const DecodePlan& pl, const tq_cache* c, const CodebookTa
                        const CodebookTables& vt, const uint32_t signs[4], const CUtensorMap* kmap,
                        const void* q, int num_q_heads, int tq_rows, int max_len_hint, float scale,
                        float tau, void* out, float* part, uint32_t* status, cudaStream_t stream,
-                       cudaEvent_t ev0, cudaEvent_t ev1, uint32_t* sparse_tiles = nullptr);
+                       cudaEvent_t ev0, cudaEvent_t ev1, uint32_t* sparse_tiles = nullptr,
+                       const TreeMask* tree = nullptr);
 
 }  // namespace host
 

@@ -58,9 +58,9 @@ struct PreCfg {
     static constexpr int kSlot = (kSlotRaw + kSlotAlign - 1) / kSlotAlign * kSlotAlign;
     static constexpr int kColOff = kStgOff + 2 * kSlot;         // fp32 n_k * scale * log2(e) [128]
     // mbarriers stg[2], S[2], O[2] (one per query tile), V^T stored, K stored,
-    // tile 1's softmax done; TMEM slot; last tile copied
+    // tile 1's softmax done; TMEM slot; last tile copied; the CTA's item (packed)
     static constexpr int kBarOff = kColOff + kTile * 4;
-    static constexpr int kSmem = kBarOff + 80;
+    static constexpr int kSmem = kBarOff + 88;
     static constexpr int kSmemAlloc = kSmem + 1024;             // base alignment slack
     static constexpr uint32_t kIdesc = umma_idesc_f16_f32(128, 128);
 };
@@ -111,7 +111,88 @@ __device__ __forceinline__ void wht128_thread(float (&x)[128]) {
     }
 }
 
-template <int KB, int VB>
+// Packed sequences: which query tile pair a CTA takes.  All pairs of all
+// sequences are ranked by the K/V tiles they read, most first (the grid then
+// ends on the shortest ones), and rank k of every KV head goes to the CTAs
+// k hkv .. k hkv + hkv - 1, so CTAs that start together read different KV
+// heads of the same tokens.  A pair's tile count grows with its place in the
+// sequence, so the pairs of a sequence that read more than c tiles are its last
+// ones, and their number is one division; the smallest c that leaves at most k
+// pairs above it is found by bisection, one warp adding the sequences up.
+struct PackedSeq {
+    int n, ctx, lim;   // query rows, tokens before them, tokens read at most
+};
+
+__device__ __forceinline__ PackedSeq packed_seq(const PrefillParams& p, int b) {
+    PackedSeq s{0, 0, 0};
+    if (b >= p.batch) return s;
+    const int first = p.cu[b], next = p.cu[b + 1], L = p.lengths[b];
+    if (first < 0 || next < first || next > p.total) return s;   // no rows (flagged by the first CTA)
+    s.n = next - first;
+    s.ctx = L - s.n;
+    s.lim = min(L, p.max_len);
+    return s;
+}
+
+// Pairs (of `span` positions each) of a sequence that read more than c tiles.
+__device__ __forceinline__ int pairs_above(const PackedSeq& s, int c, int span) {
+    const int all = (s.n + span - 1) / span;
+    if (c < 0) return all;
+    // pair q reads past tile c where its last row does: its last token, the
+    // smaller of ctx + min(n, (q + 1) span) - 1 and lim - 1, is at 128 c or after
+    const int need = 128 * c + 1 - s.ctx;   // positions up to that row
+    if (128 * c >= s.lim || need > s.n) return 0;
+    return all - (need <= span ? 0 : (need - 1) / span);
+}
+
+__device__ __forceinline__ int warp_sum(int v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// (sequence, pair) of rank k, by one warp; b = -1 past the last one.
+__device__ __forceinline__ void packed_find(const PrefillParams& p, int k, int lane, int& b, int& pair) {
+    const int span = 2 * p.pos_per_tile;
+    const PackedSeq mine = packed_seq(p, lane);
+    auto above = [&](int c) {
+        int v = pairs_above(mine, c, span);
+        for (int bb = 32 + lane; bb < p.batch; bb += 32) v += pairs_above(packed_seq(p, bb), c, span);
+        return warp_sum(v);
+    };
+    b = -1;
+    pair = 0;
+    if (k >= above(-1)) return;
+    int lo = -1, hi = (p.max_len + 127) / 128;   // above(lo) > k >= above(hi) = 0
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (above(mid) > k) lo = mid;
+        else hi = mid;
+    }
+    // the pairs of hi tiles, sequence after sequence
+    int left = k - above(hi);
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const PackedSeq s = b0 == 0 ? mine : packed_seq(p, b0 + lane);
+        const int skip = pairs_above(s, hi, span), here = pairs_above(s, hi - 1, span) - skip;
+        int inc = here;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, inc > left);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            const int all = (s.n + span - 1) / span;
+            b = b0 + l;
+            pair = __shfl_sync(0xffffffffu, all - skip - here + (left - (inc - here)), l);
+            return;
+        }
+        left -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+}
+
+template <int KB, int VB, bool PACKED>
 __global__ void __launch_bounds__(256, 1)
     tq_prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap kmap) {
     using C = PreCfg<KB, VB>;
@@ -123,24 +204,58 @@ __global__ void __launch_bounds__(256, 1)
     // hold the rows of the first tile, warps 4-7 those of the second
     const int tl = tid >> 7, r = tid & 127;
 
-    // heaviest (latest) query tiles first
-    const int npairs = (p.mtiles + 1) / 2;
-    const int pair = npairs - 1 - static_cast<int>(blockIdx.x);
+    // this CTA's (batch, kv head, query tile pair), the sequence's query rows
+    // and query tiles and its row 0 in packed q and out
+    int b, h, pair, tqn, mtiles, qrow0 = 0;
+    if constexpr (PACKED) {
+        griddep_wait();
+        int* s_item = reinterpret_cast<int*>(smem + C::kBarOff + 80);
+        if (warp == 0) {
+            int fb, fp;
+            packed_find(p, static_cast<int>(blockIdx.x) / p.hkv, tid, fb, fp);
+            if (tid == 0) {
+                s_item[0] = fb;
+                s_item[1] = fp;
+            }
+        } else if (warp == 1 && blockIdx.x == 0) {
+            bool bad = false;
+            for (int bb = tid - 32; bb < p.batch; bb += 32)
+                bad = bad || p.cu[bb] < 0 || p.cu[bb + 1] < p.cu[bb] || p.cu[bb + 1] > p.total;
+            if (bad) atomicOr(p.status, kStatusBadIndex);
+        }
+        __syncthreads();
+        b = s_item[0];
+        pair = s_item[1];
+        if (b < 0) return;   // past the last pair (uniform over the CTA)
+        h = static_cast<int>(blockIdx.x) % p.hkv;
+        qrow0 = p.cu[b];
+        tqn = p.cu[b + 1] - qrow0;
+        mtiles = (tqn + p.pos_per_tile - 1) / p.pos_per_tile;
+    } else {
+        // heaviest (latest) query tiles first
+        mtiles = p.mtiles;
+        pair = (mtiles + 1) / 2 - 1 - static_cast<int>(blockIdx.x);
+        b = blockIdx.y / p.hkv;
+        h = blockIdx.y - b * p.hkv;
+        tqn = p.tq;
+        griddep_wait();  // cache, lengths and q come from earlier work on the stream
+    }
     const int mt = 2 * pair + tl;
-    const int unit = blockIdx.y;  // b * hkv + h
-    const int b = unit / p.hkv, h = unit - b * p.hkv;
-    griddep_wait();  // cache, lengths and q come from earlier work on the stream
+    const int unit = b * p.hkv + h;
     const int L = p.lengths[b];
     const int t_lim = min(L, p.max_len);
     // row r of tile mt: query position j, head hl of the group
     const int jl = r / p.group, hl = r - jl * p.group;
     const int j = mt * p.pos_per_tile + jl;
-    const bool row_ok = mt < p.mtiles && jl < p.pos_per_tile && j < p.tq;
-    const int lim = row_ok ? min(L - p.tq + j, t_lim - 1) : -1;  // last visible token
+    const bool row_ok = mt < mtiles && jl < p.pos_per_tile && j < tqn;
+    const int lim = row_ok ? min(L - tqn + j, t_lim - 1) : -1;  // last visible token
     // this tile's rows see every token up to lim_lo; the CTA's tiles end at `last`
-    const int lim_lo = mt < p.mtiles ? min(L - p.tq + mt * p.pos_per_tile, t_lim - 1) : -1;
-    const int j_hi = min(p.tq - 1, (2 * pair + 2) * p.pos_per_tile - 1);
-    const int last = min(L - p.tq + j_hi, t_lim - 1);
+    const int lim_lo = mt < mtiles ? min(L - tqn + mt * p.pos_per_tile, t_lim - 1) : -1;
+    const int j_hi = min(tqn - 1, (2 * pair + 2) * p.pos_per_tile - 1);
+    const int last = min(L - tqn + j_hi, t_lim - 1);
+    // this row of q and out
+    const size_t io = (PACKED ? (static_cast<size_t>(qrow0) + j) * p.hq + h * p.group + hl
+                              : (static_cast<size_t>(b) * p.hq + h * p.group + hl) * tqn + j) * kD;
     const int ntiles = last >= 0 ? last / C::kTile + 1 : 0;
     const size_t row0 = static_cast<size_t>(unit) * p.cap;
 
@@ -198,7 +313,7 @@ __global__ void __launch_bounds__(256, 1)
     {
         float x[128];
         if (row_ok) {
-            const __half* qp = p.q + ((static_cast<size_t>(b) * p.hq + h * p.group + hl) * p.tq + j) * kD;
+            const __half* qp = p.q + io;
 #pragma unroll
             for (int k = 0; k < 128; k += 8) {
                 const uint4 w = *reinterpret_cast<const uint4*>(qp + k);
@@ -334,8 +449,13 @@ __global__ void __launch_bounds__(256, 1)
         dequant_q32<VB>(vrec + tb * C::kRbV + tq4 * (C::kRbV / 4), vt, hb);
         // n_v scales the stored values, so P itself goes to the MMA: 128 x
         // 128 multiplies a tile instead of the 256 x 128 of scaling P
-        const __half2 na = tok0 + ta < t_lim ? __half2half2(vnorm[ta]) : __float2half2_rn(0.f);
-        const __half2 nb = tok0 + tb < t_lim ? __half2half2(vnorm[tb]) : __float2half2_rn(0.f);
+        // (packed sequences: an overflowed norm counts as 65504, since 0 * inf
+        // would be NaN in the rows before its token)
+        auto norm2 = [&](int t) {
+            if (tok0 + t >= t_lim) return __float2half2_rn(0.f);
+            return __half2half2(PACKED ? __hmin(vnorm[t], __ushort_as_half(0x7BFFu)) : vnorm[t]);
+        };
+        const __half2 na = norm2(ta), nb = norm2(tb);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&ha[k]), na);
@@ -559,7 +679,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int d = 0; d < 128; ++d) o[d] = od[d];
             wht128_thread(o);
-            __half* op = p.out + ((static_cast<size_t>(b) * p.hq + h * p.group + hl) * p.tq + j) * kD;
+            __half* op = p.out + io;
 #pragma unroll
             for (int k = 0; k < 128; k += 8) {
                 float y[8];
@@ -588,10 +708,17 @@ __global__ void __launch_bounds__(256, 1)
 template <int KB, int VB>
 static int launch_prefill_t(const PrefillParams& p, const CUtensorMap* kmap, cudaStream_t stream) {
     using C = PreCfg<KB, VB>;
+    if (p.cu != nullptr) {
+        static std::atomic<uint64_t> attr_done{0};
+        const cudaError_t e = set_smem_attr_once(tq_prefill_kernel<KB, VB, true>, C::kSmemAlloc, attr_done);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(tq_prefill_kernel<KB, VB, true>, dim3(p.slots * p.hkv), dim3(256), C::kSmemAlloc, stream, p,
+                          *kmap);
+    }
     static std::atomic<uint64_t> attr_done{0};
-    const cudaError_t e = set_smem_attr_once(tq_prefill_kernel<KB, VB>, C::kSmemAlloc, attr_done);
+    const cudaError_t e = set_smem_attr_once(tq_prefill_kernel<KB, VB, false>, C::kSmemAlloc, attr_done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(tq_prefill_kernel<KB, VB>, dim3((p.mtiles + 1) / 2, p.batch * p.hkv), dim3(256),
+    return launch_pdl(tq_prefill_kernel<KB, VB, false>, dim3((p.mtiles + 1) / 2, p.batch * p.hkv), dim3(256),
                       C::kSmemAlloc, stream, p, *kmap);
 }
 
