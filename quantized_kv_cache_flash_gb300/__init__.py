@@ -157,11 +157,12 @@ class Context:
 
     def __init__(self):
         self.ptr = ctypes.c_void_p(None)
+        self.ref = ctypes.byref(self.ptr)
 
     def free(self) -> None:
         if self.ptr.value:
             tq_free(self)
-            self.ptr = ctypes.c_void_p(None)
+            self.ptr.value = None
 
     def __del__(self):
         try:
@@ -229,6 +230,7 @@ class Cache:
         self._cbv = (ctypes.c_float * len(cbv))(*cbv)
         self.codebook_k = list(cbk)
         self.codebook_v = list(cbv)
+        self.device = self.v_data.device
         self.struct = tq_cache(
             mode, batch, num_kv_heads, 128, capacity,
             _ptr(self.k_data), _ptr(self.k_norm), _ptr(self.v_data), _ptr(self.v_norm),
@@ -236,6 +238,7 @@ class Cache:
             ctypes.cast(self._cbk, ctypes.POINTER(ctypes.c_float)), len(cbk),
             ctypes.cast(self._cbv, ctypes.POINTER(ctypes.c_float)), len(cbv),
             rot_seed, v_rescale)
+        self.ref = ctypes.byref(self.struct)
 
     def set_v_rescale(self, v: float) -> None:
         self.struct.v_rescale = v
@@ -315,30 +318,39 @@ def tq_decode_attention_noalloc(cache: Cache, q, out, max_len_hint: int, scale: 
 
 
 def _tensor(name: str, t, dtype, shape, cache) -> None:
-    """A contiguous tensor of this type and shape (None: any size) on the
-    cache's device; ValueError otherwise."""
-    if (t.dtype != dtype or not t.is_contiguous() or t.dim() != len(shape)
-            or any(w is not None and int(g) != w for g, w in zip(t.shape, shape))):
-        want = ", ".join("*" if w is None else str(w) for w in shape)
-        raise ValueError(f"{name} must be contiguous {dtype} [{want}], "
-                         f"got {t.dtype} {list(t.shape)}" + ("" if t.is_contiguous() else " (strided)"))
-    if t.device != cache.v_data.device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {cache.v_data.device}")
+    """A contiguous tensor of this type and shape on the cache's device;
+    ValueError otherwise."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == cache.device:
+        return
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}"
+                         + ("" if t.is_contiguous() else " (strided)"))
+    raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+
+
+def _launch_stream(cache, stream) -> int:
+    """The stream handle of a call on this cache: the given one or the current
+    one of the cache's device, which has to be the current device."""
     import torch
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, which is not the current CUDA device")
+    dev = cache.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {dev}, which is not the current CUDA device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return int(getattr(stream, "cuda_stream", stream))
 
 
 def tq_encode_append_packed(ctx: Context, cache: Cache, k_new, v_new, cu_seqlens, stream=None) -> None:
     """Append packed k_new/v_new fp16 [total, Hkv, 128]: rows cu_seqlens[b] ..
     cu_seqlens[b + 1] - 1 (int32 [B + 1] on the device) go to sequence b."""
     import torch
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        _tensor(name, t, torch.float16, (int(k_new.shape[0]), cache.num_kv_heads, 128), cache)
+    shape = (k_new.shape[0], cache.num_kv_heads, 128)
+    _tensor("k_new", k_new, torch.float16, shape, cache)
+    _tensor("v_new", v_new, torch.float16, shape, cache)
     _tensor("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), cache)
-    _check(lib().tq_encode_append_packed(ctypes.byref(ctx.ptr), ctypes.byref(cache.struct),
-                                         _ptr(k_new), _ptr(v_new), _ptr(cu_seqlens),
-                                         int(k_new.shape[0]), _stream(stream)),
+    _check(lib().tq_encode_append_packed(ctx.ref, cache.ref,
+                                         k_new.data_ptr(), v_new.data_ptr(), cu_seqlens.data_ptr(),
+                                         shape[0], _launch_stream(cache, stream)),
            "tq_encode_append_packed")
 
 
@@ -348,13 +360,16 @@ def tq_prefill_attention_packed(ctx: Context, cache: Cache, q, out, cu_seqlens, 
     appended to the cache): rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 belong
     to sequence b.  Output rows of no sequence are left as they were."""
     import torch
-    _tensor("q", q, torch.float16, (None, None, 128), cache)
-    _tensor("out", out, torch.float16, tuple(q.shape), cache)
+    if q.dim() != 3:
+        raise ValueError("q must be [total, Hq, 128]")
+    total, hq, _ = q.shape
+    _tensor("q", q, torch.float16, (total, hq, 128), cache)
+    _tensor("out", out, torch.float16, q.shape, cache)
     _tensor("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), cache)
-    _check(lib().tq_prefill_attention_packed(ctypes.byref(ctx.ptr), ctypes.byref(cache.struct),
+    _check(lib().tq_prefill_attention_packed(ctx.ref, cache.ref,
                                              _ptr(q), int(q.shape[1]), _ptr(cu_seqlens),
                                              int(q.shape[0]), int(max_len_hint), float(scale),
-                                             _ptr(out), _stream(stream)),
+                                             _ptr(out), _launch_stream(cache, stream)),
            "tq_prefill_attention_packed")
 
 
@@ -364,15 +379,18 @@ def tq_tree_attention(ctx: Context, cache: Cache, q, out, tree_mask, max_len_hin
     tokens of every sequence.  tree_mask: int32 [1 or B, Tq, ceil(Tq / 32)]
     words (``tq_tree_mask``), bit i of row j set where node j sees node i."""
     import torch
-    _tensor("q", q, torch.float16, (cache.batch, None, None, 128), cache)
-    _tensor("out", out, torch.float16, tuple(q.shape), cache)
-    n = int(q.shape[2])
+    if q.dim() != 4 or tree_mask.dim() != 3:
+        raise ValueError("q must be [B, Hq, Tq, 128] and tree_mask [1 or B, Tq, ceil(Tq / 32)]")
+    _, hq, n, _ = q.shape
+    per_seq = tree_mask.shape[0]
+    _tensor("q", q, torch.float16, (cache.batch, hq, n, 128), cache)
+    _tensor("out", out, torch.float16, q.shape, cache)
     _tensor("tree_mask", tree_mask, torch.int32,
-            (1 if tree_mask.shape[0] == 1 else cache.batch, n, (n + 31) // 32), cache)
-    _check(lib().tq_tree_attention(ctypes.byref(ctx.ptr), ctypes.byref(cache.struct), _ptr(q),
-                                   int(q.shape[1]), n, int(max_len_hint), float(scale),
-                                   _ptr(tree_mask), int(tree_mask.shape[0]), _ptr(out),
-                                   _stream(stream)), "tq_tree_attention")
+            (1 if per_seq == 1 else cache.batch, n, (n + 31) // 32), cache)
+    _check(lib().tq_tree_attention(ctx.ref, cache.ref, q.data_ptr(),
+                                   hq, n, int(max_len_hint), float(scale),
+                                   tree_mask.data_ptr(), per_seq, out.data_ptr(),
+                                   _launch_stream(cache, stream)), "tq_tree_attention")
 
 
 def tq_tree_mask(parents):
@@ -394,11 +412,13 @@ def tq_cache_compact(ctx: Context, cache: Cache, start, keep, num_keep, num_draf
     the sequence off behind them (all int32 on the device)."""
     import torch
     _tensor("start", start, torch.int32, (cache.batch,), cache)
-    _tensor("keep", keep, torch.int32, (cache.batch, None), cache)
+    if keep.dim() != 2:
+        raise ValueError("keep must be [B, max_keep]")
+    _tensor("keep", keep, torch.int32, (cache.batch, keep.shape[1]), cache)
     _tensor("num_keep", num_keep, torch.int32, (cache.batch,), cache)
-    _check(lib().tq_cache_compact(ctypes.byref(ctx.ptr), ctypes.byref(cache.struct), _ptr(start),
-                                  int(num_drafted), _ptr(keep), _ptr(num_keep), int(keep.shape[1]),
-                                  _stream(stream)), "tq_cache_compact")
+    _check(lib().tq_cache_compact(ctx.ref, cache.ref, start.data_ptr(),
+                                  int(num_drafted), keep.data_ptr(), num_keep.data_ptr(), keep.shape[1],
+                                  _launch_stream(cache, stream)), "tq_cache_compact")
 
 
 def tq_cache_copy(ctx: Context, dst: Cache, src: Cache, dst_seq, src_seq, max_len_hint: int,
@@ -406,15 +426,16 @@ def tq_cache_copy(ctx: Context, dst: Cache, src: Cache, dst_seq, src_seq, max_le
     """Sequence dst_seq[m] of `dst` becomes the first num_tokens[m] tokens (None:
     all) of sequence src_seq[m] of `src`, which may be the same cache."""
     import torch
-    m = int(dst_seq.shape[0])
-    for name, t in (("dst_seq", dst_seq), ("src_seq", src_seq), ("num_tokens", num_tokens)):
-        if t is not None:
-            _tensor(name, t, torch.int32, (m,), dst)
-    if src.v_data.device != dst.v_data.device:
+    m = dst_seq.numel()
+    _tensor("dst_seq", dst_seq, torch.int32, (m,), dst)
+    _tensor("src_seq", src_seq, torch.int32, (m,), dst)
+    if num_tokens is not None:
+        _tensor("num_tokens", num_tokens, torch.int32, (m,), dst)
+    if src.device != dst.device:
         raise ValueError("the two caches are on different devices")
-    _check(lib().tq_cache_copy(ctypes.byref(ctx.ptr), ctypes.byref(dst.struct),
-                               ctypes.byref(src.struct), _ptr(dst_seq), _ptr(src_seq),
-                               _ptr(num_tokens), m, int(max_len_hint), _stream(stream)),
+    _check(lib().tq_cache_copy(ctx.ref, dst.ref,
+                               src.ref, dst_seq.data_ptr(), src_seq.data_ptr(),
+                               _ptr(num_tokens), m, int(max_len_hint), _launch_stream(dst, stream)),
            "tq_cache_copy")
 
 

@@ -208,8 +208,6 @@ int encode_rows_map(CUtensorMap* map, const void* base, uint64_t rows) {
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? TQ_OK : TQ_ERR_CUDA;
 }
-
-constexpr int kSMs = 152;  // GB300 (only used to size the split grid)
 constexpr long long kMinChunks3 = 96;  // chunks per CTA below which a third wave does not pay
 
 // Decode grid: waves of resident CTAs -- the later ones, placed wherever a
@@ -636,6 +634,65 @@ int tq_encode_append_packed(tq_ctx** pctx, const tq_cache* c, const void* k_new,
 
 namespace {
 
+constexpr int kTreeDecodeRows = 16;   // rows per KV head up to which a tree runs on the decode kernel
+
+// Tree attention on the tensor cores, for arguments that plan_decode has checked.
+int tree_impl(tq_ctx** pctx, const tq_cache* c, const tq::host::DecodePlan& pl, const void* q, int32_t num_q_heads,
+              int32_t tq_rows, int32_t max_len_hint, float scale, const tq::host::TreeMask& tree, void* out,
+              cudaStream_t stream) {
+    const int row_tiles = (pl.rows + 127) / 128;
+    const long long units = 1ll * c->batch * c->num_kv_heads * row_tiles;
+    const long long chunks = units * ((max_len_hint + 127) / 128);
+    if (chunks >= (1ll << 30) || 1ll * c->batch * c->num_kv_heads * pl.rows >= (1ll << 31) - 8) return TQ_ERR_UNSUPPORTED;
+    tq_ctx* ctx;
+    int r = get_ctx(pctx, &ctx);
+    if (r != TQ_OK) return r;
+    if ((r = prepare_tables(ctx, c, pl.kb, pl.vb)) != TQ_OK) return r;
+    if (pl.kb == 16 && (r = prepare_kmap(ctx, c)) != TQ_OK) return r;
+    // one CTA per SM, each with two chunks at least (one per group of warps)
+    const int ctas = int(std::max<long long>(1, std::min<long long>(tq::host::kSMs, (chunks + 1) / 2)));
+    const size_t rows = size_t(ctas + units) * 128;
+    if ((r = ensure_work(ctx, rows * (kD + 2) * sizeof(float))) != TQ_OK) return r;
+    cudaEvent_t e0 = nullptr, e1 = nullptr;
+    if ((r = timing_events(ctx, &e0, &e1)) != TQ_OK) return r;
+    ctx->last_stream = stream;
+    tq::TreeParams p{};
+    p.k_codes = static_cast<const uint8_t*>(c->k_data);
+    p.k_norm = static_cast<const __half*>(c->k_norm);
+    p.v_codes = static_cast<const uint8_t*>(c->v_data);
+    p.v_norm = static_cast<const __half*>(c->v_norm);
+    p.lengths = c->lengths;
+    p.q = static_cast<const __half*>(q);
+    p.out = static_cast<__half*>(out);
+    p.tree = tree.words;
+    p.tree_words = (tq_rows + 31) / 32;
+    p.tree_per_seq = tree.shared ? 0 : tq_rows * p.tree_words;
+    p.part_o = ctx->d_work;
+    p.part_ml = ctx->d_work + rows * kD;
+    p.status = ctx->d_words;
+    p.batch = c->batch;
+    p.hkv = c->num_kv_heads;
+    p.hq = num_q_heads;
+    p.group = pl.group;
+    p.tq = tq_rows;
+    p.cap = c->capacity;
+    p.max_len = max_len_hint;
+    p.rows = pl.rows;
+    p.row_tiles = row_tiles;
+    p.per_b = c->num_kv_heads * row_tiles;
+    p.num_ctas = ctas;
+    const float sc = (scale == 0.f) ? 1.0f / std::sqrt(float(kD)) : scale;
+    p.scale_log2e = sc * 1.4426950408889634f;
+    p.v_rescale = c->v_rescale;
+    if (pl.kb != 16) std::memcpy(p.ktab, ctx->ktab.tab, sizeof(p.ktab));
+    std::memcpy(p.vtab, ctx->vtab.tab, sizeof(p.vtab));
+    std::memcpy(p.signs, ctx->signs, sizeof(p.signs));
+    CUtensorMap dummy;
+    std::memset(&dummy, 0, sizeof(dummy));
+    return cuda_err(static_cast<cudaError_t>(
+        tq::launch_tree(pl.kb, pl.vb, p, pl.kb == 16 ? &ctx->kmap : &dummy, stream, e0, e1)));
+}
+
 // Arguments that both prefill calls take.
 int check_prefill(const tq_cache* c, const void* q, int32_t num_q_heads, int32_t max_len_hint, float scale,
                   const void* out, int* kb, int* vb) {
@@ -747,6 +804,15 @@ int tq_tree_attention(tq_ctx** pctx, const tq_cache* c, const void* q, int32_t n
     if (tq_rows > TQ_MAX_TREE_NODES) return TQ_ERR_UNSUPPORTED;
     if (c->num_kv_heads > 0 && num_q_heads / c->num_kv_heads > tq::kMaxTreeGroup) return TQ_ERR_UNSUPPORTED;
     const tq::host::TreeMask tree{tree_mask, mask_batch == 1};
+    tq::host::DecodePlan pl;
+    const int r = tq::host::plan_decode(c, q, out, num_q_heads, tq_rows, max_len_hint, scale, &pl,
+                                        tq::kMaxTreeGroup * TQ_MAX_TREE_NODES);
+    if (r != TQ_OK) return r;
+    // The decode kernel's row groups hold up to 16 rows, and each group
+    // dequantises the context anew; the tensor-core kernel shares it between 128.
+    if (pl.rows > kTreeDecodeRows && !tq::mode_table(c->mode) && !pl.res)
+        return tree_impl(pctx, c, pl, q, num_q_heads, tq_rows, max_len_hint, scale, tree, out,
+                         static_cast<cudaStream_t>(stream));
     return decode_impl(pctx, c, q, num_q_heads, tq_rows, max_len_hint, scale, 0.f, out, stream, &tree);
 }
 

@@ -489,4 +489,52 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
     asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
+// ---- tiles dequantised for the tcgen05 attention kernels ----
+// 32 dims (a quarter) of a record as fp16 pairs.
+template <int BITS>
+__device__ __forceinline__ void dequant_q32(const uint8_t* rec, const Tables& t, uint32_t (&h)[16]) {
+    if constexpr (BITS == 3) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(rec);
+        dequant3_quarter(w[0], w[1], w[2], t, h);
+    } else {
+        dequant4_quarter(*reinterpret_cast<const uint4*>(rec), t, h);
+    }
+}
+
+// Four 8x8 b16 matrices stored transposed: register i of lane 4r + c holds
+// elements (r, 2c) and (r, 2c+1) of matrix i; matrix i's row k lands at the
+// address given by lane 8i + k as elements (0..7, k).
+__device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2,
+                                              uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(addr),
+                 "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+                 : "memory");
+}
+
+// In-thread 128-point Walsh-Hadamard transform (unnormalised).  From stride
+// 2 on, a butterfly's elements i, i + 1 pair with i + h, i + h + 1, so those
+// stages run on packed fp32 pairs (a - b as fma(b, -1, a), exact).
+__device__ __forceinline__ void wht128_thread(float (&x)[128]) {
+#pragma unroll
+    for (int i = 0; i < 128; i += 2) {
+        const float a = x[i], b = x[i + 1];
+        x[i] = a + b;
+        x[i + 1] = a - b;
+    }
+    const float2 m1 = make_float2(-1.f, -1.f);
+#pragma unroll
+    for (int h = 2; h < 128; h <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 128; i += 2) {
+            if (i & h) continue;
+            const float2 a = make_float2(x[i], x[i + 1]), b = make_float2(x[i + h], x[i + h + 1]);
+            const float2 sum = __fadd2_rn(a, b), dif = __ffma2_rn(b, m1, a);
+            x[i] = sum.x;
+            x[i + 1] = sum.y;
+            x[i + h] = dif.x;
+            x[i + h + 1] = dif.y;
+        }
+    }
+}
+
 }  // namespace tq

@@ -113,6 +113,29 @@ struct PrefillParams {
     int32_t slots;            // query tile pairs of all sequences, at most
 };
 
+// Tree attention on the tensor cores (tq_tree.cu): units are (batch, kv head,
+// tile of 128 query rows), a row of a unit is node * group + head of the group.
+struct TreeParams {
+    const uint8_t* k_codes;   // packed K codes (fp16 K: read through the tensor map)
+    const __half* k_norm;
+    const uint8_t* v_codes;
+    const __half* v_norm;
+    const int32_t* lengths;   // [B]
+    const __half* q;          // [B, Hq, Tq, 128]
+    __half* out;
+    const uint32_t* tree;     // as in DecodeParams
+    int32_t tree_words, tree_per_seq;
+    float* part_o;            // [num_ctas + units, 128, 128]
+    float* part_ml;           // [num_ctas + units, 128, 2]
+    uint32_t* status;
+    int32_t batch, hkv, hq, group, tq, cap, max_len;
+    int32_t rows;             // group * tq
+    int32_t row_tiles, per_b; // tiles of rows per KV head, units per sequence
+    int32_t num_ctas;
+    float scale_log2e, v_rescale;
+    uint32_t ktab[4], vtab[4], signs[4];
+};
+
 // Keeping the accepted tokens of a drafted block (see tq_cache_compact).
 struct CompactParams {
     uint8_t* k_data;          // packed codes, table records or fp16 K rows
@@ -178,6 +201,8 @@ int launch_encode_packed(int kbits, int vbits, const EncodeParams& p, const CUte
 int decode_ctas_per_sm(int kbits, int vbits, int group_rows, bool table, bool res);
 int launch_prefill(int kbits, int vbits, const PrefillParams& p, const CUtensorMap* kmap,
                    cudaStream_t stream);   // packed sequences where p.cu is set
+int launch_tree(int kbits, int vbits, const TreeParams& p, const CUtensorMap* kmap, cudaStream_t stream,
+                cudaEvent_t ev0, cudaEvent_t ev1);
 int launch_compact(const CompactParams& p, cudaStream_t stream);
 // CTAs = pairs * hkv * ceil(max_len / kCopyTokens), below 2^31
 constexpr int kCopyTokens = 256;
@@ -260,6 +285,8 @@ struct CodebookTables {
     uint32_t tab8[2] = {};
     int res_shift = 0;
 };
+
+constexpr int kSMs = 152;  // GB300 (only used to size the split grids)
 
 int cuda_err_code(cudaError_t e);
 bool aligned16(const void* p);
