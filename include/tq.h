@@ -259,8 +259,8 @@ int tq_prefill_attention_packed(tq_ctx **ctx, const tq_cache *cache, const void 
  * A row that sees no token gives 0 and raises TQ_STATUS_SHORT_CONTEXT.  Where
  * lengths[b] < tq the first tq - lengths[b] drafted tokens do not exist.
  * A drafted token that a row does not see adds nothing to it, whatever its
- * record holds (a V norm that overflowed fp16 counts as 65504 in the tokens of
- * the drafted block).  Every mode and codebook is supported.  The call uses
+ * record holds (norms that overflowed fp16 or NaN in padding nodes; rows that
+ * do see such a token need not be finite).  Every mode and codebook is supported.  The call uses
  * the context's workspace like tq_decode_attention.
  */
 #define TQ_MAX_TREE_NODES 256

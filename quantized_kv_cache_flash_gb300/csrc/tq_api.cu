@@ -652,7 +652,8 @@ int tree_impl(tq_ctx** pctx, const tq_cache* c, const tq::host::DecodePlan& pl, 
     // one CTA per SM, each with two chunks at least (one per group of warps)
     const int ctas = int(std::max<long long>(1, std::min<long long>(tq::host::kSMs, (chunks + 1) / 2)));
     const size_t rows = size_t(ctas + units) * 128;
-    if ((r = ensure_work(ctx, rows * (kD + 2) * sizeof(float))) != TQ_OK) return r;
+    const size_t q_bytes = size_t(units) * (pl.kb == 16 ? 32768 : 65536);
+    if ((r = ensure_work(ctx, q_bytes + rows * (kD + 2) * sizeof(float))) != TQ_OK) return r;
     cudaEvent_t e0 = nullptr, e1 = nullptr;
     if ((r = timing_events(ctx, &e0, &e1)) != TQ_OK) return r;
     ctx->last_stream = stream;
@@ -667,8 +668,9 @@ int tree_impl(tq_ctx** pctx, const tq_cache* c, const tq::host::DecodePlan& pl, 
     p.tree = tree.words;
     p.tree_words = (tq_rows + 31) / 32;
     p.tree_per_seq = tree.shared ? 0 : tq_rows * p.tree_words;
-    p.part_o = ctx->d_work;
-    p.part_ml = ctx->d_work + rows * kD;
+    p.q_tiles = reinterpret_cast<uint8_t*>(ctx->d_work);
+    p.part_o = ctx->d_work + q_bytes / sizeof(float);
+    p.part_ml = p.part_o + rows * kD;
     p.status = ctx->d_words;
     p.batch = c->batch;
     p.hkv = c->num_kv_heads;
