@@ -437,25 +437,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             bad = end_segment(s.ntiles);
         }
     } else if (wg >= 2) {
-        // ---- dequantising warps: K(n) (quantized K) and V(n)^T, a token's norm per thread ----
+        // ---- dequantising warps: K(n) (quantized K) with both norms of the tile's
+        // tokens, one per thread, and V(n)^T ----
         regs_dec<kRegsDequant>();
         const int r = tid & 127;
-        const bool is_k = wg == 2;
-        const __half* norms = is_k ? p.k_norm : p.v_norm;
         bool bad = false;
         while (pos < hi && !bad) {
             const Segment s = segment();
-            auto norm = [&](int n) {   // (0 past the end)
-                const int t = (s.k0 + n) * kTok + r;
-                return n < s.ntiles && t < s.t_lim ? __half2float(norms[s.row0 + t]) : 0.f;
-            };
-            if (is_k) {
-                if constexpr (KB != 0) {
-                    float n0 = norm(0), n1 = norm(1);
+            if (wg == 2) {
+                auto norm_k = [&](int n) {   // (0 past the end)
+                    const int t = (s.k0 + n) * kTok + r;
+                    return KB != 0 && n < s.ntiles && t < s.t_lim ? __half2float(p.k_norm[s.row0 + t]) : 0.f;
+                };
+                auto norm_v = [&](int n) {
+                    const int t = (s.k0 + n) * kTok + r;
+                    return n < s.ntiles && t < s.t_lim ? __half2float(p.v_norm[s.row0 + t]) : 0.f;
+                };
+                float nk = norm_k(0), nv = norm_v(0);
 #pragma unroll 1
-                    for (int n = 0; n < s.ntiles; ++n) {
-                        const int t = tbase + n, u = t & 1;
-                        const float n2 = norm(n + 2);
+                for (int n = 0; n < s.ntiles; ++n) {
+                    const int t = tbase + n, u = t & 1;
+                    const float nk1 = norm_k(n + 1), nv1 = norm_v(n + 1);
+                    if constexpr (KB != 0) {
                         wait(bar_k + 8 * u, (t >> 1) & 1);
                         if (t >= 2) wait(bar_s + 8 * u, ((t >> 1) - 1) & 1);   // S(t - 2) has read its K tile
                         // a token per thread; the quarters are taken in an order that
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         const uint8_t* rec = smem + C::kSKOff + u * C::kSK + r * C::kRbK;
                         uint8_t* sK = smem + C::kKOff + u * 32768;
                         const int turn = KB == 4 ? r >> 1 : r >> 3;
-#pragma unroll 1
+#pragma unroll 2
                         for (int q = 0; q < 4; ++q) {
                             const int quarter = (q + turn) & 3;
                             uint32_t hh[16];
@@ -475,34 +478,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                     make_uint4(hh[4 * m], hh[4 * m + 1], hh[4 * m + 2], hh[4 * m + 3]);
                         }
                         fence_proxy_async();
-                        if (t >= 2) wait(bar_p + 8 * u, ((t >> 1) - 1) & 1);   // softmax(t - 2) has read the scales
-                        (reinterpret_cast<float*>(smem + C::kColOff) + u * kTok)[frag_place(r)] = n0 * p.scale_log2e;
-                        mbar_arrive(bar_kr + 8 * u);
-                        n0 = n1;
-                        n1 = n2;
                     }
-                }
-            } else {
-                const Tables vt{p.vtab[0], p.vtab[1], p.vtab[2], p.vtab[3]};
-                float n0 = norm(0), n1 = norm(1);
-#pragma unroll 1
-                for (int n = 0; n < s.ntiles; ++n) {
-                    const int t = tbase + n, u = t & 1;
-                    const float n2 = norm(n + 2);
-                    wait(bar_v + 8 * u, (t >> 1) & 1);
-                    if (t >= 2) wait(bar_o + 8 * u, ((t >> 1) - 1) & 1);   // P.V(t - 2) has read its V tile (and P its norms)
-                    store_vt<VB>(smem + C::kSVOff + u * C::kSV, smem + C::kVtOff + u * 32768, vt, warp & 3, lane);
-                    fence_proxy_async();
+                    if (t >= 2) wait(bar_p + 8 * u, ((t >> 1) - 1) & 1);   // softmax(t - 2) has read its scales and norms
+                    if constexpr (KB != 0)
+                        (reinterpret_cast<float*>(smem + C::kColOff) + u * kTok)[frag_place(r)] = nk * p.scale_log2e;
                     // (an overflowed norm counts as 65504: 0 * inf would be NaN in the
                     // rows that do not see the token; it does not count for the
                     // slack, so the rows that do may overflow)
-                    (reinterpret_cast<float*>(smem + C::kNvOff) + u * kTok)[frag_place(r)] = fminf(n0, 65504.f);
+                    (reinterpret_cast<float*>(smem + C::kNvOff) + u * kTok)[frag_place(r)] = fminf(nv, 65504.f);
                     // (non-negative floats order like their bits)
-                    const uint32_t nmax = __reduce_max_sync(0xffffffffu, n0 < 65536.f ? __float_as_uint(n0) : 0u);
+                    const uint32_t nmax = __reduce_max_sync(0xffffffffu, nv < 65536.f ? __float_as_uint(nv) : 0u);
                     if (lane == 0) (reinterpret_cast<uint32_t*>(smem + C::kNmOff) + 4 * u)[warp & 3] = nmax;
+                    mbar_arrive(bar_kr + 8 * u);
+                    nk = nk1;
+                    nv = nv1;
+                }
+            } else {
+                const Tables vt{p.vtab[0], p.vtab[1], p.vtab[2], p.vtab[3]};
+#pragma unroll 1
+                for (int n = 0; n < s.ntiles; ++n) {
+                    const int t = tbase + n, u = t & 1;
+                    wait(bar_v + 8 * u, (t >> 1) & 1);
+                    if (t >= 2) wait(bar_o + 8 * u, ((t >> 1) - 1) & 1);   // P.V(t - 2) has read its V tile
+                    store_vt<VB>(smem + C::kSVOff + u * C::kSV, smem + C::kVtOff + u * 32768, vt, warp & 3, lane);
+                    fence_proxy_async();
                     mbar_arrive(bar_vr + 8 * u);
-                    n0 = n1;
-                    n1 = n2;
                 }
             }
             bad = end_segment(s.ntiles);
@@ -527,15 +527,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const bool live = row32 < p.rows;              // some row of the warp's 32 exists
             const uint32_t* mask = p.tree + static_cast<size_t>(s.b) * p.tree_per_seq;
             float m_base[4], l_sum[4];   // base (log2) and this thread's part of the sum of rows v + 8q
+            int node[4];                 // and their drafted nodes
 #pragma unroll
-            for (int q = 0; q < 4; ++q) m_base[q] = -INFINITY, l_sum[q] = 0.f;
+            for (int q = 0; q < 4; ++q) {
+                m_base[q] = -INFINITY, l_sum[q] = 0.f;
+                node[q] = (row32 + (lane >> 2) + 8 * q) / p.group;
+            }
 #pragma unroll 1
             for (int n = 0; n < s.ntiles; ++n) {
                 const int t = tbase + n, u = t & 1;
                 const int tok0 = (s.k0 + n) * kTok + 64 * half;   // this warp's first token
-                wait(bar_vr + 8 * u, (t >> 1) & 1);                // norms (V(t) itself is the MMA's)
-                if constexpr (KB != 0) wait(bar_kr + 8 * u, (t >> 1) & 1);   // scales
-                if (t >= 2) wait(bar_o + 8 * u, ((t >> 1) - 1) & 1);         // P.V(t - 2) has read its P
+                wait(bar_kr + 8 * u, (t >> 1) & 1);                    // scales and norms
+                if (t >= 2) wait(bar_o + 8 * u, ((t >> 1) - 1) & 1);   // P.V(t - 2) has read its P
                 wait(bar_s + 8 * u, (t >> 1) & 1);
                 tc_fence_after();
                 if (live) {   // (uniform over the two warps of the rows)
@@ -561,65 +564,88 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             sum[q] = make_float2(0.f, 0.f);
                             mq[q] = -INFINITY;
                         }
-                        uint32_t v[2][2][8];   // [buffer][rows 0-15, 16-31]: 16 columns, the next ones in flight
-                        tmem_ld_frag_issue(t_s, v[0][0]);
-                        tmem_ld_frag_issue(s_hi, v[0][1]);
-#pragma unroll 1
-                        for (int c2 = 0; c2 < 2; ++c2) {
-                            uint32_t pk[2][8];   // P of 32 tokens
+                        // x of columns 16c .. 16c + 15 from S, and P from x (16 packed
+                        // columns per 32 tokens: e2 the half of them)
+                        auto scores = [&](int c, const uint32_t (&v0)[8], const uint32_t (&v1)[8], float2 (&x)[8]) {
+                            float4 s4 = make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e, p.scale_log2e);
+                            if constexpr (KB != 0) s4 = *reinterpret_cast<const float4*>(col + 16 * c);
 #pragma unroll
-                            for (int e2 = 0; e2 < 2; ++e2) {
-                                const int c = 2 * c2 + e2;
-                                tmem_ld_wait(v[e2][0], v[e2][1]);
-                                {   // (the last one fetches columns that nobody takes)
-                                    const int next = 16 * ((c + 1) & 3);
-                                    tmem_ld_frag_issue(t_s + next, v[1 - e2][0]);
-                                    tmem_ld_frag_issue(s_hi + next, v[1 - e2][1]);
+                            for (int e = 0; e < 8; ++e) {
+                                const int i = e >> 2, q = e & 3;
+                                const uint32_t* f = (q < 2 ? v0 : v1) + 4 * i + 2 * (q & 1);
+                                x[e] = __ffma2_rn(make_float2(__uint_as_float(f[0]), __uint_as_float(f[1])),
+                                                  i ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y), nb[q]);
+                            }
+                        };
+                        auto weigh = [&](int c, int e2, const float2 (&x)[8], uint32_t (&pk)[2][8]) {
+                            const float4 w4 = *reinterpret_cast<const float4*>(nvs + 16 * c);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int i = e >> 2, q = e & 3;
+                                mq[q] = fmaxf(mq[q], fmaxf(x[e].x, x[e].y));
+                                const float2 pe = make_float2(fast_exp2(x[e].x), fast_exp2(x[e].y));
+                                sum[q] = __fadd2_rn(sum[q], pe);
+                                const float2 w = __fmul2_rn(pe, i ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y));
+                                pk[q >> 1][2 * (2 * e2 + i) + (q & 1)] = pack_half2(w.x, w.y);
+                            }
+                        };
+                        if (tok0 + 64 <= full_below) {
+                            // every row sees these tokens: straight through, the next 16
+                            // columns in flight
+                            uint32_t v[2][2][8], pk[2][8];
+                            tmem_ld_frag_issue(t_s, v[0][0]);
+                            tmem_ld_frag_issue(s_hi, v[0][1]);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                tmem_ld_wait(v[c & 1][0], v[c & 1][1]);
+                                if (c < 3) {
+                                    tmem_ld_frag_issue(t_s + 16 * (c + 1), v[(c + 1) & 1][0]);
+                                    tmem_ld_frag_issue(s_hi + 16 * (c + 1), v[(c + 1) & 1][1]);
                                 }
-                                float4 s4 = make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e, p.scale_log2e);
-                                if constexpr (KB != 0) s4 = *reinterpret_cast<const float4*>(col + 16 * c);
-                                const float4 w4 = *reinterpret_cast<const float4*>(nvs + 16 * c);
                                 float2 x[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const int i = e >> 2, q = e & 3;
-                                    const uint32_t* f = v[e2][q >> 1] + 4 * i + 2 * (q & 1);
-                                    x[e] = __ffma2_rn(make_float2(__uint_as_float(f[0]), __uint_as_float(f[1])),
-                                                      i ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y), nb[q]);
+                                scores(c, v[c & 1][0], v[c & 1][1], x);
+                                weigh(c, c & 1, x, pk);
+                                if (c & 1) {
+                                    tmem_st_frag_issue(t_p + 8 * (c - 1), pk[0]);
+                                    tmem_st_frag_issue(p_hi + 8 * (c - 1), pk[1]);
                                 }
-                                const int t0 = tok0 + 16 * c;
-                                if (t0 + 16 > full_below) {   // (uniform) some row sees these tokens in part
+                            }
+                        } else {
+                            // the end of the context and the drafted block: with the mask
 #pragma unroll 1
+                            for (int c2 = 0; c2 < 2; ++c2) {
+                                uint32_t pk[2][8];
+#pragma unroll
+                                for (int e2 = 0; e2 < 2; ++e2) {
+                                    const int c = 2 * c2 + e2, t0 = tok0 + 16 * c;
+                                    uint32_t v0[8], v1[8];
+                                    tmem_ld_frag_issue(t_s + 16 * c, v0);
+                                    tmem_ld_frag_issue(s_hi + 16 * c, v1);
+                                    uint32_t seen[4];   // this thread's columns: bits 0, 1, 8, 9
+#pragma unroll
                                     for (int q = 0; q < 4; ++q) {
                                         const int rr = row32 + (lane >> 2) + 8 * q;
                                         uint32_t w = 0u;
                                         if (rr < p.rows && t0 < s.t_lim) {
-                                            w = tree_window(mask + (rr / p.group) * p.tree_words, p.tree_words, t0 - base);
+                                            w = tree_window(mask + node[q] * p.tree_words, p.tree_words, t0 - base);
                                             if (t0 + 16 > s.t_lim) w &= (1u << (s.t_lim - t0)) - 1u;
                                         }
-                                        w >>= 2 * (lane & 3);   // this thread's columns: bits 0, 1, 8, 9
-#pragma unroll
-                                        for (int e = 0; e < 8; ++e)
-                                            if ((e & 3) == q) {
-                                                if (!((w >> (8 * (e >> 2))) & 1u)) x[e].x = -INFINITY;
-                                                if (!((w >> (8 * (e >> 2))) & 2u)) x[e].y = -INFINITY;
-                                            }
+                                        seen[q] = w >> (2 * (lane & 3));
                                     }
-                                }
+                                    tmem_ld_wait(v0, v1);
+                                    float2 x[8];
+                                    scores(c, v0, v1, x);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const int i = e >> 2, q = e & 3;
-                                    mq[q] = fmaxf(mq[q], fmaxf(x[e].x, x[e].y));
-                                    const float2 pe = make_float2(fast_exp2(x[e].x), fast_exp2(x[e].y));
-                                    sum[q] = __fadd2_rn(sum[q], pe);
-                                    const float2 w = __fmul2_rn(pe, i ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y));
-                                    pk[q >> 1][2 * (2 * e2 + i) + (q & 1)] = pack_half2(w.x, w.y);
+                                    for (int e = 0; e < 8; ++e) {
+                                        if (!((seen[e & 3] >> (8 * (e >> 2))) & 1u)) x[e].x = -INFINITY;
+                                        if (!((seen[e & 3] >> (8 * (e >> 2))) & 2u)) x[e].y = -INFINITY;
+                                    }
+                                    weigh(c, e2, x, pk);
                                 }
+                                tmem_st_frag_issue(t_p + 16 * c2, pk[0]);
+                                tmem_st_frag_issue(p_hi + 16 * c2, pk[1]);
                             }
-                            tmem_st_frag_issue(t_p + 16 * c2, pk[0]);
-                            tmem_st_frag_issue(p_hi + 16 * c2, pk[1]);
                         }
-                        tmem_ld_wait(v[0][0], v[0][1]);
                         bool grow = false;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) grow |= mq[q] > (m_base[q] == -INFINITY ? -INFINITY : slack);
