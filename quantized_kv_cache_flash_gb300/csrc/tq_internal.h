@@ -127,7 +127,7 @@ struct TreeParams {
     int32_t tree_words, tree_per_seq;
     float* part_o;            // [num_ctas + units, 128, 128]
     float* part_ml;           // [num_ctas + units, 128, 2]
-    uint8_t* q_tiles;         // per unit Q' as MMA tiles: 64 KB (fp16 K: 32 KB)
+    uint8_t* q_tiles;         // per unit Q' (q_hi, q_lo): 64 KB (fp16 K: 32 KB)
     uint32_t* status;
     int32_t batch, hkv, hq, group, tq, cap, max_len;
     int32_t rows;             // group * tq

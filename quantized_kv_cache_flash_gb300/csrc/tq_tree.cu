@@ -19,17 +19,17 @@
 // thread issues the MMAs, two the copies.  So S(n + 1) and P.V(n - 1) run under
 // softmax(n).
 //
-// What bounds it: the tensor core and the operands that it reads from shared
-// memory (128 bytes a cycle: S reads 8 KB per MMA of 64 cycles, so 24 MMAs take
-// some 1500 cycles a tile); the exponentials take 1024 cycles of MUFU, the
-// dequantisation and the softmax some 1000 issue slots per scheduler.
+// What bounds it: a tile's 24 MMAs take 1536 cycles of the tensor core, its
+// shared-memory traffic (K, V and P tiles written and read by the MMAs, records,
+// scales) about as many at 128 bytes -- so Q' lies in tensor memory --, the exponentials 1024 cycles of MUFU,
+// dequantisation and softmax some 1000 issue slots per scheduler.
 //
 // Split: the (batch, kv head, row tile) units lie end to end as 128-token
 // chunks, and CTA c of P takes [c C / P, (c + 1) C / P) of the C chunks, from
 // the actual lengths; it writes one partial (m, l, O) per unit that it touches,
 // which tq_tree_combine_kernel merges, normalises and rotates back.  Q' is
-// rotated, split and laid out as MMA tiles by a small kernel before, while this
-// one sets up and dequantises its first tiles.
+// rotated and split by a small kernel before, while this one sets up and
+// dequantises its first tiles.
 #include <float.h>
 
 #include <algorithm>
@@ -49,14 +49,10 @@ template <int KB, int VB>
 struct TreeCfg {
     static constexpr int kRbK = (KB == 0) ? 256 : KB * 16;
     static constexpr int kRbV = VB * 16;
-    static constexpr int kQBytes = (KB == 0) ? 32768 : 65536;         // fp16 Q' (q_hi), and q_lo (quantized K)
-    static constexpr int kQloOff = kQBytes - 32768;
-    static constexpr int kVtOff = kQBytes;                            // two V^T tiles [dim][token] (32 KB each)
-    // quantized K: two K tiles [token][dim], and records; fp16 K: the MMA
-    // tiles as they are copied, three in turn
-    static constexpr int kKOff = kVtOff + 65536;
-    static constexpr int kKTiles = (KB == 0) ? 3 : 2;
-    static constexpr int kSKOff = kKOff + kKTiles * 32768;
+    static constexpr int kVtOff = 0;                                  // two V^T tiles [dim][token] (32 KB each)
+    static constexpr int kPOff = kVtOff + 65536;                      // two P tiles [row][token]
+    static constexpr int kKOff = kPOff + 65536;                       // two K tiles [token][dim] (fp16 K: as copied)
+    static constexpr int kSKOff = kKOff + 65536;                      // two tiles of K records (quantized K)
     static constexpr int kSK = (KB == 0) ? 0 : kTok * kRbK;
     static constexpr int kSVOff = kSKOff + 2 * kSK;                   // two tiles of V records
     static constexpr int kSV = kTok * kRbV;
@@ -64,11 +60,11 @@ struct TreeCfg {
     static constexpr int kNvOff = kColOff + 2 * kTok * 4;             // two tiles of n_v [128]
     static constexpr int kXmOff = kNvOff + 2 * kTok * 4;              // row maxima (or sums) between two warps [128]
     static constexpr int kNmOff = kXmOff + kTok * 4;                  // two tiles of the largest n_v of 32 tokens [4]
-    // mbarriers: K copied [3], V copied [2], K stored [2], V stored [2], P
-    // stored [2], S done [2], P.V done [2], K tile read [3] (fp16 K), Q' copied,
-    // all MMAs done (after a time-out)
+    // mbarriers, of even and odd tiles: K copied, V copied, K (and norms) stored,
+    // V stored, P stored, S done, P.V done; Q' stored, all MMAs done (after a
+    // time-out)
     static constexpr int kBarOff = kNmOff + 32;
-    static constexpr int kBars = 20;
+    static constexpr int kBars = 16;
     static constexpr int kSmem = kBarOff + 8 * kBars + 8;             // and the TMEM slot
     static constexpr int kSmemAlloc = kSmem + 256;   // to a 1024-byte boundary: the base is one, but for 256 bytes at most
     static_assert(kSmemAlloc <= 232448, "227 KB per CTA");
@@ -79,7 +75,7 @@ struct TreeCfg {
 // issuing threads.  Registers per thread after the split (their sum times 128
 // is at most the launch's 640 x 96).
 constexpr int kTreeThreads = 640;
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 152, kRegsDequant = 72, kRegsIssue = 32;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsDequant = 72, kRegsIssue = 48;
 static_assert(2 * kRegsSoftmax + 2 * kRegsDequant + kRegsIssue <= 5 * kRegsLaunch, "within the launch's registers");
 
 template <int N>
@@ -200,8 +196,9 @@ __device__ __forceinline__ uint32_t tree_window(const uint32_t* row, int W, int 
 
 }  // namespace
 
-// Q' of every unit as MMA tiles: a warp per row (the rows past the last one are
-// zero), lane l dims 4l .. 4l + 3.
+// Q' of every unit, fp16 (q_hi, then q_lo): a warp per row (the rows past the
+// last one are zero), lane l dims 4l .. 4l + 3, stored as [16 pieces of 8 dims]
+// [128 rows], so that the rows' threads read 16 bytes each, together.
 template <bool ROTATE>
 __global__ void __launch_bounds__(256) tq_tree_q_kernel(const __grid_constant__ TreeParams p) {
     const int lane = threadIdx.x & 31;
@@ -233,7 +230,8 @@ __global__ void __launch_bounds__(256) tq_tree_q_kernel(const __grid_constant__ 
             lv = make_uint2(pack_half2(x[0] - h0.x, x[1] - h0.y), pack_half2(x[2] - h1.x, x[3] - h1.y));
         }
     }
-    uint8_t* tile = p.q_tiles + static_cast<size_t>(unit) * (ROTATE ? 65536 : 32768) + sw128_offset(r, 4 * lane);
+    uint8_t* tile = p.q_tiles + static_cast<size_t>(unit) * (ROTATE ? 65536 : 32768) +
+                    ((lane >> 1) * kTreeRows + r) * 16 + (lane & 1) * 8;
     *reinterpret_cast<uint2*>(tile) = hv;
     if constexpr (ROTATE) *reinterpret_cast<uint2*>(tile + 32768) = lv;
 }
@@ -268,29 +266,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
 
     const uint32_t bars = smem_u32(smem + C::kBarOff);
-    const uint32_t bar_k = bars, bar_v = bars + 24, bar_kr = bars + 40, bar_vr = bars + 56, bar_p = bars + 72,
-                   bar_s = bars + 88, bar_o = bars + 104, bar_kf = bars + 120, bar_q = bars + 144, bar_x = bars + 152;
+    const uint32_t bar_k = bars, bar_v = bars + 16, bar_kr = bars + 32, bar_vr = bars + 48, bar_p = bars + 64,
+                   bar_s = bars + 80, bar_o = bars + 96, bar_q = bars + 112, bar_x = bars + 120;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * C::kBars);
     if (tid == 0) {
-        for (int i = 0; i < 5; ++i) mbar_init(bar_k + 8 * i, 1);      // K copied, V copied
+        for (int i = 0; i < 4; ++i) mbar_init(bar_k + 8 * i, 1);      // K copied, V copied
         for (int i = 0; i < 4; ++i) mbar_init(bar_kr + 8 * i, 128);   // K stored, V stored
         for (int i = 0; i < 2; ++i) mbar_init(bar_p + 8 * i, 256);    // P stored
-        for (int i = 0; i < 9; ++i) mbar_init(bar_s + 8 * i, 1);      // S done, P.V done, K tile read, Q' copied, all done
+        for (int i = 0; i < 4; ++i) mbar_init(bar_s + 8 * i, 1);      // S done, P.V done
+        mbar_init(bar_q, 256);                                        // Q' stored
+        mbar_init(bar_x, 1);
         fence_barrier_init();
     }
     if (warp == 0) tmem_alloc(smem_u32(tslot), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // tensor memory: S of even and odd tiles (128 columns each), P of both (64 each), O (128)
-    const uint32_t tmem = *tslot, tm_p = tmem + 256, tm_o = tmem + 384;
+    // tensor memory: S of even and odd tiles (128 columns each), O (128), q_hi and
+    // q_lo (64 each)
+    const uint32_t tmem = *tslot, tm_o = tmem + 256, tm_q = tmem + 384;
 
     bool stalled = false;   // once set, waits return at once and nothing more is issued
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (!stalled && !mbar_wait_bounded(bar, parity)) stalled = true;
     };
     // Tile n of a segment is tile t = tbase + n of the CTA: it takes the buffers
-    // t & 1 (of the K ring t % 3), whose barriers' phase is t >> 1 (t / 3).
+    // t & 1, whose barriers' phase is t >> 1.
     int tbase = 0, pos = lo;
     uint32_t segs = 0;
 
@@ -326,74 +327,82 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     };
 
     if (wg == 4) {
-        // ---- issuing threads: the MMAs, the Q' and K copies, the V copies ----
+        // ---- issuing threads: the MMAs, the K copies, the V copies ----
         regs_dec<kRegsIssue>();
         const int role = warp & 3;
         bool bad = false;
         while (pos < hi && !bad) {
             const Segment s = segment();
-            if (role == 0 && lane == 0) {
+            if (role == 0) {
+                // The whole warp runs the loop, so that addresses and descriptors stay
+                // in uniform registers, and one lane issues.
+                const uint32_t one = lane == 0 ? 1u : 0u;
+                const uint32_t tmu = __shfl_sync(0xffffffffu, tmem, 0);
+                const uint64_t vdesc = umma_desc_sw128(__shfl_sync(0xffffffffu, smem_u32(smem + C::kVtOff), 0));
+                const uint64_t pdesc = umma_desc_sw128(__shfl_sync(0xffffffffu, smem_u32(smem + C::kPOff), 0));
+                const uint64_t kdesc = umma_desc_sw128(__shfl_sync(0xffffffffu, smem_u32(smem + C::kKOff), 0));
+                auto commit = [&](uint32_t bar) {
+                    if (lane == 0) umma_commit(bar);
+                    __syncwarp();
+                };
                 wait(bar_q, segs & 1);
+                bool quit = __any_sync(0xffffffffu, stalled);
                 // S(0), S(1), P.V(0), S(2), P.V(1), ...
 #pragma unroll 1
-                for (int i = 0; i < s.ntiles + 2; ++i) {
+                for (int i = 0; i < s.ntiles + 2 && !quit; ++i) {
                     const int n = i - 2;   // P.V(n), then S(n + 2)
                     if (n >= 0) {
                         const int t = tbase + n, u = t & 1;
                         wait(bar_vr + 8 * u, (t >> 1) & 1);
                         wait(bar_p + 8 * u, (t >> 1) & 1);
-                        if (stalled) break;
+                        quit = __any_sync(0xffffffffu, stalled);
+                        if (quit) break;
                         tc_fence_after();
-                        const uint32_t vt = smem_u32(smem + C::kVtOff + u * 32768);
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            umma_f16_ts(tm_o, tm_p + 64 * u + 8 * kk,
-                                        umma_desc_sw128(vt + (kk >> 2) * 16384 + (kk & 3) * 32), C::kIdesc,
-                                        (n > 0 || kk > 0) ? 1u : 0u);
-                        umma_commit(bar_o + 8 * u);
-                    }
-                    if (i < s.ntiles) {
-                        // (the S tile is free: P(i - 2) was stored)
-                        const int t = tbase + i, u = t & 1;
-                        if constexpr (KB == 0) wait(bar_k + 8 * (t % 3), (t / 3) & 1);
-                        else wait(bar_kr + 8 * u, (t >> 1) & 1);
-                        if (stalled) break;
-                        tc_fence_after();
-                        const uint32_t kbase = smem_u32(smem + C::kKOff + (KB == 0 ? t % 3 : u) * 32768);
+                        const uint32_t off = static_cast<uint32_t>(u) * (32768 >> 4), more = n > 0 ? 1u : 0u;
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {
-                            const uint32_t koff = (kk >> 2) * 16384 + (kk & 3) * 32;
-                            umma_f16(tmem + 128 * u, umma_desc_sw128(smem_u32(smem) + koff),
-                                     umma_desc_sw128(kbase + koff), C::kIdesc, kk > 0 ? 1u : 0u);
-                            if constexpr (KB != 0)
-                                umma_f16(tmem + 128 * u, umma_desc_sw128(smem_u32(smem) + C::kQloOff + koff),
-                                         umma_desc_sw128(kbase + koff), C::kIdesc, 1u);
+                            const uint32_t k = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                            umma_f16_if(one, tmu + 256, pdesc + off + k, vdesc + off + k, C::kIdesc, kk > 0 ? 1u : more);
                         }
-                        umma_commit(bar_s + 8 * u);
-                        if constexpr (KB == 0) umma_commit(bar_kf + 8 * (t % 3));
+                        commit(bar_o + 8 * u);
+                    }
+                    if (i < s.ntiles) {   // (P(n), and with it the softmax's reads of this S tile, is done)
+                        const int t = tbase + i, u = t & 1;
+                        if constexpr (KB == 0) wait(bar_k + 8 * u, (t >> 1) & 1);
+                        else wait(bar_kr + 8 * u, (t >> 1) & 1);
+                        quit = __any_sync(0xffffffffu, stalled);
+                        if (quit) break;
+                        tc_fence_after();
+                        const uint64_t kd = kdesc + static_cast<uint32_t>(u) * (32768 >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint64_t d = kd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+                            umma_f16_ts_if(one, tmu + 128 * u, tmu + 384 + 8 * kk, d, C::kIdesc, kk > 0 ? 1u : 0u);
+                            if constexpr (KB != 0) umma_f16_ts_if(one, tmu + 128 * u, tmu + 448 + 8 * kk, d, C::kIdesc, 1u);
+                        }
+                        commit(bar_s + 8 * u);
                     }
                 }
                 // on a time-out, what is in flight ends before the memory goes
                 // away: a last commit completes behind all of it
-                if (stalled) {
-                    atomicOr(p.status, kStatusPipelineStall);
-                    umma_commit(bar_x);
-                    (void)mbar_wait_bounded(bar_x, 0);
+                if (quit) {
+                    stalled = true;
+                    if (lane == 0) {
+                        atomicOr(p.status, kStatusPipelineStall);
+                        umma_commit(bar_x);
+                        (void)mbar_wait_bounded(bar_x, 0);
+                    }
                 }
             } else if (role == 1 && lane == 0) {
-                if (segs == 0) griddep_wait();   // the Q' tiles
-                const uint8_t* qt = p.q_tiles + static_cast<size_t>(s.b * p.per_b + s.ui) * C::kQBytes;
-                fence_proxy_async();
-                mbar_arrive_expect_tx(bar_q, C::kQBytes);
-                bulk_g2s(smem_u32(smem), qt, C::kQBytes, bar_q);
                 int sent = 0;
 #pragma unroll 1
                 for (int n = 0; n < s.ntiles; ++n, ++sent) {   // K records (fp16 K: MMA tiles)
                     const int t = tbase + n, tok0 = (s.k0 + n) * kTok;
+                    const uint32_t bar = bar_k + 8 * (t & 1);
                     if constexpr (KB == 0) {
-                        if (t >= 3) wait(bar_kf + 8 * (t % 3), (t / 3 - 1) & 1);   // S has read the ring's tile t - 3
+                        if (t >= 2) wait(bar_s + 8 * (t & 1), ((t >> 1) - 1) & 1);   // S(t - 2) has read its K tile
                         if (stalled) break;
-                        const uint32_t bar = bar_k + 8 * (t % 3), dst = smem_u32(smem + C::kKOff + (t % 3) * 32768);
+                        const uint32_t dst = smem_u32(smem + C::kKOff + (t & 1) * 32768);
                         mbar_arrive_expect_tx(bar, 32768);
 #pragma unroll 1
                         for (int q = 0; q < 8; ++q)
@@ -402,7 +411,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     } else {
                         if (t >= 2) wait(bar_kr + 8 * (t & 1), ((t >> 1) - 1) & 1);   // the records of tile t - 2 are read
                         if (stalled) break;
-                        const uint32_t bytes = min(kTok, s.t_lim - tok0) * C::kRbK, bar = bar_k + 8 * (t & 1);
+                        const uint32_t bytes = min(kTok, s.t_lim - tok0) * C::kRbK;
                         fence_proxy_async();
                         mbar_arrive_expect_tx(bar, bytes);
                         bulk_g2s(smem_u32(smem + C::kSKOff + (t & 1) * C::kSK), p.k_codes + (s.row0 + tok0) * C::kRbK, bytes,
@@ -410,11 +419,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     }
                 }
                 if (stalled) {   // the copies in flight land first
-                    (void)mbar_wait_bounded(bar_q, segs & 1);
-                    for (int n = max(0, sent - 3); n < sent; ++n) {
-                        const int t = tbase + n;
-                        (void)mbar_wait_bounded(bar_k + 8 * (KB == 0 ? t % 3 : t & 1), (KB == 0 ? t / 3 : t >> 1) & 1);
-                    }
+                    for (int n = max(0, sent - 2); n < sent; ++n)
+                        (void)mbar_wait_bounded(bar_k + 8 * ((tbase + n) & 1), ((tbase + n) >> 1) & 1);
                 }
             } else if (role == 2 && lane == 0) {
                 int sent = 0;
@@ -526,6 +532,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const int row32 = (s.ui % p.row_tiles) * kTreeRows + 32 * quad;
             const bool live = row32 < p.rows;              // some row of the warp's 32 exists
             const uint32_t* mask = p.tree + static_cast<size_t>(s.b) * p.tree_per_seq;
+            // Q' of the unit into tensor memory: lane = row, q_hi by the first four
+            // warps, q_lo by the others
+            if (segs == 0) griddep_wait();
+            if (KB != 0 || half == 0) {
+                const uint4* q16 = reinterpret_cast<const uint4*>(
+                                       p.q_tiles + static_cast<size_t>(s.b * p.per_b + s.ui) * (KB == 0 ? 32768 : 65536) +
+                                       half * 32768) + 32 * quad + lane;
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint4 x = __ldcg(q16 + (8 * c + e) * kTreeRows);
+                        w[4 * e] = x.x, w[4 * e + 1] = x.y, w[4 * e + 2] = x.z, w[4 * e + 3] = x.w;
+                    }
+                    tmem_st32(tm_q + lanes + 64 * half + 32 * c, w);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(bar_q);
             float m_base[4], l_sum[4];   // base (log2) and this thread's part of the sum of rows v + 8q
             int node[4];                 // and their drafted nodes
 #pragma unroll
@@ -543,16 +569,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 tc_fence_after();
                 if (live) {   // (uniform over the two warps of the rows)
                     const uint32_t t_s = tmem + 128 * u + 64 * half + lanes, s_hi = t_s + (16u << 16);
-                    const uint32_t t_p = tm_p + 64 * u + 32 * half + lanes, p_hi = t_p + (16u << 16);
                     const float* col = reinterpret_cast<const float*>(smem + C::kColOff) + u * kTok + c4;
                     const float* nvs = reinterpret_cast<const float*>(smem + C::kNvOff) + u * kTok + c4;
                     // how far a score may pass its row's base: p n_v stays below 2^15.99
                     const float4 nm = *reinterpret_cast<const float4*>(smem + C::kNmOff + 16 * u);
                     const float slack = fmaxf(
                         0.f, fminf(kSlack, 15.99f - __log2f(fmaxf(fmaxf(nm.x, nm.y), fmaxf(nm.z, nm.w)))));
+                    // stmatrix: lane 8m + k gives row k of matrix m, rows 8m .. 8m + 7 of
+                    // the warp's 32 and eight tokens
+                    const uint32_t prow = smem_u32(smem + C::kPOff + u * 32768) + half * 16384 + (32 * quad + lane) * 128;
                     // One pass over S; a second one when some score has passed its
                     // row's base by more than the slack (a row's first tile, hardly
                     // any other), against bases moved to the tile's maxima.
+                    const bool masked = tok0 + 64 > full_below;   // some row sees these tokens in part
 #pragma unroll 1
                     for (int pass = 0;; ++pass) {
                         float2 sum[4], nb[4];
@@ -564,9 +593,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             sum[q] = make_float2(0.f, 0.f);
                             mq[q] = -INFINITY;
                         }
-                        // x of columns 16c .. 16c + 15 from S, and P from x (16 packed
-                        // columns per 32 tokens: e2 the half of them)
-                        auto scores = [&](int c, const uint32_t (&v0)[8], const uint32_t (&v1)[8], float2 (&x)[8]) {
+                        // x of columns 16c .. 16c + 15 from S, and P from x
+                        auto scores = [&](int c, const uint32_t* v0, const uint32_t* v1, float2 (&x)[8]) {
                             float4 s4 = make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e, p.scale_log2e);
                             if constexpr (KB != 0) s4 = *reinterpret_cast<const float4*>(col + 16 * c);
 #pragma unroll
@@ -577,73 +605,59 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                                   i ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y), nb[q]);
                             }
                         };
-                        auto weigh = [&](int c, int e2, const float2 (&x)[8], uint32_t (&pk)[2][8]) {
+                        auto weigh = [&](int c, const float2 (&x)[8]) {
                             const float4 w4 = *reinterpret_cast<const float4*>(nvs + 16 * c);
+                            uint32_t pk[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                const int i = e >> 2, q = e & 3;
+                                const int q = e & 3;
                                 mq[q] = fmaxf(mq[q], fmaxf(x[e].x, x[e].y));
                                 const float2 pe = make_float2(fast_exp2(x[e].x), fast_exp2(x[e].y));
                                 sum[q] = __fadd2_rn(sum[q], pe);
-                                const float2 w = __fmul2_rn(pe, i ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y));
-                                pk[q >> 1][2 * (2 * e2 + i) + (q & 1)] = pack_half2(w.x, w.y);
+                                const float2 w = __fmul2_rn(pe, e >> 2 ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y));
+                                pk[e] = pack_half2(w.x, w.y);
                             }
+                            stsm_x4(prow + (((2 * c) ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+                            stsm_x4(prow + (((2 * c + 1) ^ (lane & 7)) << 4), pk[4], pk[5], pk[6], pk[7]);
                         };
-                        if (tok0 + 64 <= full_below) {
-                            // every row sees these tokens: straight through, the next 16
-                            // columns in flight
-                            uint32_t v[2][2][8], pk[2][8];
-                            tmem_ld_frag_issue(t_s, v[0][0]);
-                            tmem_ld_frag_issue(s_hi, v[0][1]);
+                        if (!masked) {
+                            uint32_t v[2][32];
+                            tmem_ld_frag_issue(t_s, v[0]);
+                            tmem_ld_frag_issue(s_hi, v[1]);
+                            tmem_ld_wait(v[0], v[1]);
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
-                                tmem_ld_wait(v[c & 1][0], v[c & 1][1]);
-                                if (c < 3) {
-                                    tmem_ld_frag_issue(t_s + 16 * (c + 1), v[(c + 1) & 1][0]);
-                                    tmem_ld_frag_issue(s_hi + 16 * (c + 1), v[(c + 1) & 1][1]);
-                                }
                                 float2 x[8];
-                                scores(c, v[c & 1][0], v[c & 1][1], x);
-                                weigh(c, c & 1, x, pk);
-                                if (c & 1) {
-                                    tmem_st_frag_issue(t_p + 8 * (c - 1), pk[0]);
-                                    tmem_st_frag_issue(p_hi + 8 * (c - 1), pk[1]);
-                                }
+                                scores(c, v[0] + 8 * c, v[1] + 8 * c, x);
+                                weigh(c, x);
                             }
                         } else {
-                            // the end of the context and the drafted block: with the mask
 #pragma unroll 1
-                            for (int c2 = 0; c2 < 2; ++c2) {
-                                uint32_t pk[2][8];
+                            for (int c = 0; c < 4; ++c) {
+                                const int t0 = tok0 + 16 * c;
+                                uint32_t v0[8], v1[8];
+                                tmem_ld_frag_issue(t_s + 16 * c, v0);
+                                tmem_ld_frag_issue(s_hi + 16 * c, v1);
+                                uint32_t seen[4];   // this thread's columns: bits 0, 1, 8, 9
 #pragma unroll
-                                for (int e2 = 0; e2 < 2; ++e2) {
-                                    const int c = 2 * c2 + e2, t0 = tok0 + 16 * c;
-                                    uint32_t v0[8], v1[8];
-                                    tmem_ld_frag_issue(t_s + 16 * c, v0);
-                                    tmem_ld_frag_issue(s_hi + 16 * c, v1);
-                                    uint32_t seen[4];   // this thread's columns: bits 0, 1, 8, 9
-#pragma unroll
-                                    for (int q = 0; q < 4; ++q) {
-                                        const int rr = row32 + (lane >> 2) + 8 * q;
-                                        uint32_t w = 0u;
-                                        if (rr < p.rows && t0 < s.t_lim) {
-                                            w = tree_window(mask + node[q] * p.tree_words, p.tree_words, t0 - base);
-                                            if (t0 + 16 > s.t_lim) w &= (1u << (s.t_lim - t0)) - 1u;
-                                        }
-                                        seen[q] = w >> (2 * (lane & 3));
+                                for (int q = 0; q < 4; ++q) {
+                                    const int rr = row32 + (lane >> 2) + 8 * q;
+                                    uint32_t w = 0u;
+                                    if (rr < p.rows && t0 < s.t_lim) {
+                                        w = tree_window(mask + node[q] * p.tree_words, p.tree_words, t0 - base);
+                                        if (t0 + 16 > s.t_lim) w &= (1u << (s.t_lim - t0)) - 1u;
                                     }
-                                    tmem_ld_wait(v0, v1);
-                                    float2 x[8];
-                                    scores(c, v0, v1, x);
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) {
-                                        if (!((seen[e & 3] >> (8 * (e >> 2))) & 1u)) x[e].x = -INFINITY;
-                                        if (!((seen[e & 3] >> (8 * (e >> 2))) & 2u)) x[e].y = -INFINITY;
-                                    }
-                                    weigh(c, e2, x, pk);
+                                    seen[q] = w >> (2 * (lane & 3));
                                 }
-                                tmem_st_frag_issue(t_p + 16 * c2, pk[0]);
-                                tmem_st_frag_issue(p_hi + 16 * c2, pk[1]);
+                                tmem_ld_wait(v0, v1);
+                                float2 x[8];
+                                scores(c, v0, v1, x);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    if (!((seen[e & 3] >> (8 * (e >> 2))) & 1u)) x[e].x = -INFINITY;
+                                    if (!((seen[e & 3] >> (8 * (e >> 2))) & 2u)) x[e].y = -INFINITY;
+                                }
+                                weigh(c, x);
                             }
                         }
                         bool grow = false;
@@ -654,7 +668,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             for (int q = 0; q < 4; ++q) l_sum[q] += sum[q].x + sum[q].y;
                             break;
                         }
-                        tmem_st_wait();   // (P is stored again)
                         // the rows' maxima over both warps' tokens
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -704,7 +717,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             }
                         }
                     }
-                    tmem_st_wait();
+                    fence_proxy_async();   // the MMA reads P through the async proxy
                 }
                 tc_fence_before();
                 mbar_arrive(bar_p + 8 * u);   // P(t) is stored, S(t), the scales and norms are read
