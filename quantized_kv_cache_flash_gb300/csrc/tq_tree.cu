@@ -58,13 +58,12 @@ struct TreeCfg {
     static constexpr int kSV = kTok * kRbV;
     static constexpr int kColOff = kSVOff + 2 * kSV;                  // two tiles of n_k scale log2 e [128]
     static constexpr int kNvOff = kColOff + 2 * kTok * 4;             // two tiles of n_v [128]
-    static constexpr int kXmOff = kNvOff + 2 * kTok * 4;              // row maxima (or sums) between two warps [128]
-    static constexpr int kNmOff = kXmOff + kTok * 4;                  // two tiles of the largest n_v of 32 tokens [4]
+    static constexpr int kNmOff = kNvOff + 2 * kTok * 4;              // two tiles of the largest n_v of 32 tokens [4]
     // mbarriers, of even and odd tiles: K copied, V copied, K (and norms) stored,
-    // V stored, P stored, S done, P.V done; Q' stored, all MMAs done (after a
-    // time-out)
+    // V stored, P stored, S done, P.V done; Q' stored, all MMAs done [2] (after
+    // a time-out)
     static constexpr int kBarOff = kNmOff + 32;
-    static constexpr int kBars = 16;
+    static constexpr int kBars = 18;
     static constexpr int kSmem = kBarOff + 8 * kBars + 8;             // and the TMEM slot
     static constexpr int kSmemAlloc = kSmem + 256;   // to a 1024-byte boundary: the base is one, but for 256 bytes at most
     static_assert(kSmemAlloc <= 232448, "227 KB per CTA");
@@ -75,7 +74,7 @@ struct TreeCfg {
 // issuing threads.  Registers per thread after the split (their sum times 128
 // is at most the launch's 640 x 96).
 constexpr int kTreeThreads = 640;
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsDequant = 72, kRegsIssue = 48;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsDequant = 72, kRegsIssue = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsDequant + kRegsIssue <= 5 * kRegsLaunch, "within the launch's registers");
 
 template <int N>
@@ -276,6 +275,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int i = 0; i < 4; ++i) mbar_init(bar_s + 8 * i, 1);      // S done, P.V done
         mbar_init(bar_q, 256);                                        // Q' stored
         mbar_init(bar_x, 1);
+        mbar_init(bar_x + 8, 1);
         fence_barrier_init();
     }
     if (warp == 0) tmem_alloc(smem_u32(tslot), 512);
@@ -327,70 +327,62 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     };
 
     if (wg == 4) {
-        // ---- issuing threads: the MMAs, the K copies, the V copies ----
+        // ---- issuing warps: S, the K copies, the V copies, P.V ----
         regs_dec<kRegsIssue>();
         const int role = warp & 3;
         bool bad = false;
         while (pos < hi && !bad) {
             const Segment s = segment();
-            if (role == 0) {
-                // The whole warp runs the loop, so that addresses and descriptors stay
-                // in uniform registers, and one lane issues.
+            if (role == 0 || role == 3) {
+                // S(n) and P.V(n) by a warp each, so that the tensor core has the
+                // other's products while one waits.  The whole warp runs the loop, so
+                // that addresses and descriptors stay in uniform registers, and one
+                // lane issues.
                 const uint32_t one = lane == 0 ? 1u : 0u;
                 const uint32_t tmu = __shfl_sync(0xffffffffu, tmem, 0);
-                const uint64_t vdesc = umma_desc_sw128(__shfl_sync(0xffffffffu, smem_u32(smem + C::kVtOff), 0));
-                const uint64_t pdesc = umma_desc_sw128(__shfl_sync(0xffffffffu, smem_u32(smem + C::kPOff), 0));
-                const uint64_t kdesc = umma_desc_sw128(__shfl_sync(0xffffffffu, smem_u32(smem + C::kKOff), 0));
-                auto commit = [&](uint32_t bar) {
-                    if (lane == 0) umma_commit(bar);
-                    __syncwarp();
-                };
-                wait(bar_q, segs & 1);
-                bool quit = __any_sync(0xffffffffu, stalled);
-                // S(0), S(1), P.V(0), S(2), P.V(1), ...
+                const uint64_t adesc = umma_desc_sw128(__shfl_sync(0xffffffffu, smem_u32(smem + C::kPOff), 0));
+                const uint64_t bdesc =
+                    umma_desc_sw128(__shfl_sync(0xffffffffu, smem_u32(smem + (role == 0 ? C::kKOff : C::kVtOff)), 0));
+                if (role == 0) wait(bar_q, segs & 1);
 #pragma unroll 1
-                for (int i = 0; i < s.ntiles + 2 && !quit; ++i) {
-                    const int n = i - 2;   // P.V(n), then S(n + 2)
-                    if (n >= 0) {
-                        const int t = tbase + n, u = t & 1;
+                for (int n = 0; n < s.ntiles; ++n) {
+                    const int t = tbase + n, u = t & 1;
+                    const uint32_t off = static_cast<uint32_t>(u) * (32768 >> 4);
+                    if (role == 0) {
+                        wait((KB == 0 ? bar_k : bar_kr) + 8 * u, (t >> 1) & 1);
+                        if (t >= 2) wait(bar_p + 8 * u, ((t >> 1) - 1) & 1);   // softmax(t - 2) has read this S tile
+                    } else {
                         wait(bar_vr + 8 * u, (t >> 1) & 1);
                         wait(bar_p + 8 * u, (t >> 1) & 1);
-                        quit = __any_sync(0xffffffffu, stalled);
-                        if (quit) break;
-                        tc_fence_after();
-                        const uint32_t off = static_cast<uint32_t>(u) * (32768 >> 4), more = n > 0 ? 1u : 0u;
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const uint32_t k = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                            umma_f16_if(one, tmu + 256, pdesc + off + k, vdesc + off + k, C::kIdesc, kk > 0 ? 1u : more);
-                        }
-                        commit(bar_o + 8 * u);
                     }
-                    if (i < s.ntiles) {   // (P(n), and with it the softmax's reads of this S tile, is done)
-                        const int t = tbase + i, u = t & 1;
-                        if constexpr (KB == 0) wait(bar_k + 8 * u, (t >> 1) & 1);
-                        else wait(bar_kr + 8 * u, (t >> 1) & 1);
-                        quit = __any_sync(0xffffffffu, stalled);
-                        if (quit) break;
-                        tc_fence_after();
-                        const uint64_t kd = kdesc + static_cast<uint32_t>(u) * (32768 >> 4);
+                    if (__any_sync(0xffffffffu, stalled)) break;
+                    tc_fence_after();
+                    if (role == 0) {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {
-                            const uint64_t d = kd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+                            const uint64_t d = bdesc + off + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
                             umma_f16_ts_if(one, tmu + 128 * u, tmu + 384 + 8 * kk, d, C::kIdesc, kk > 0 ? 1u : 0u);
                             if constexpr (KB != 0) umma_f16_ts_if(one, tmu + 128 * u, tmu + 448 + 8 * kk, d, C::kIdesc, 1u);
                         }
-                        commit(bar_s + 8 * u);
+                    } else {
+                        const uint32_t more = n > 0 ? 1u : 0u;
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint32_t k = off + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+                            umma_f16_if(one, tmu + 256, adesc + k, bdesc + k, C::kIdesc, kk > 0 ? 1u : more);
+                        }
                     }
+                    if (lane == 0) umma_commit((role == 0 ? bar_s : bar_o) + 8 * u);
+                    __syncwarp();
                 }
                 // on a time-out, what is in flight ends before the memory goes
-                // away: a last commit completes behind all of it
-                if (quit) {
+                // away: a last commit completes behind all of this warp's products
+                if (__any_sync(0xffffffffu, stalled)) {
                     stalled = true;
                     if (lane == 0) {
                         atomicOr(p.status, kStatusPipelineStall);
-                        umma_commit(bar_x);
-                        (void)mbar_wait_bounded(bar_x, 0);
+                        umma_commit(bar_x + 8 * (role >> 1));
+                        (void)mbar_wait_bounded(bar_x + 8 * (role >> 1), 0);
                     }
                 }
             } else if (role == 1 && lane == 0) {
@@ -514,23 +506,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             bad = end_segment(s.ntiles);
         }
     } else {
-        // ---- softmax warps: warp w has rows 32 (w & 3) .. + 31 and tokens 64 (w >> 2) .. + 63
-        // of a tile, as MMA fragments: lane 4v + c has rows v + 8q (q = 0..3) and
-        // columns 2c, 2c + 1 of every eight, so a thread reads a quarter of its
-        // tokens' scales and norms (with a row per thread, their broadcast reads
+        // ---- softmax warps: warp w has rows 32 (w & 3) + 16 (w >> 2) .. + 15 as MMA
+        // fragments: lane 4v + c has rows v and v + 8 and columns 2c, 2c + 1 of
+        // every eight, so a thread reads a quarter of the tile's scales and norms (with a row per thread, their broadcast reads
         // took a third of the shared-memory bandwidth that the MMAs need) ----
         regs_inc<kRegsSoftmax>();
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-        const int c4 = 64 * half + 4 * (lane & 3);   // this thread's place in a tile's scales and norms
-        float* xm = reinterpret_cast<float*>(smem + C::kXmOff) + 32 * quad;
+        const int c4 = 4 * (lane & 3);   // this thread's place in a tile's scales and norms
         bool bad = false;
         while (pos < hi && !bad) {
             const Segment s = segment();
             const int base = s.L - p.tq;                   // first drafted token
             const int full_below = min(base, s.t_lim);     // tokens below this are seen by every row
             const int row32 = (s.ui % p.row_tiles) * kTreeRows + 32 * quad;
-            const bool live = row32 < p.rows;              // some row of the warp's 32 exists
+            const int row16 = row32 + 16 * half;           // this warp's first row
+            const bool live = row16 < p.rows;
             const uint32_t* mask = p.tree + static_cast<size_t>(s.b) * p.tree_per_seq;
             // Q' of the unit into tensor memory: lane = row, q_hi by the first four
             // warps, q_lo by the others
@@ -552,169 +543,148 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             tc_fence_before();
             mbar_arrive(bar_q);
-            float m_base[4], l_sum[4];   // base (log2) and this thread's part of the sum of rows v + 8q
-            int node[4];                 // and their drafted nodes
+            float m_base[2], l_sum[2];   // base (log2) and this thread's part of the sum of rows v + 8q
+            const uint32_t* mrow[2];     // and their masks
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 m_base[q] = -INFINITY, l_sum[q] = 0.f;
-                node[q] = (row32 + (lane >> 2) + 8 * q) / p.group;
+                const int rr = row16 + (lane >> 2) + 8 * q;
+                mrow[q] = rr < p.rows ? mask + (rr / p.group) * p.tree_words : nullptr;
             }
 #pragma unroll 1
             for (int n = 0; n < s.ntiles; ++n) {
                 const int t = tbase + n, u = t & 1;
-                const int tok0 = (s.k0 + n) * kTok + 64 * half;   // this warp's first token
+                const int tok0 = (s.k0 + n) * kTok;
                 wait(bar_kr + 8 * u, (t >> 1) & 1);                    // scales and norms
                 if (t >= 2) wait(bar_o + 8 * u, ((t >> 1) - 1) & 1);   // P.V(t - 2) has read its P
                 wait(bar_s + 8 * u, (t >> 1) & 1);
                 tc_fence_after();
-                if (live) {   // (uniform over the two warps of the rows)
-                    const uint32_t t_s = tmem + 128 * u + 64 * half + lanes, s_hi = t_s + (16u << 16);
+                if (live) {   // (warp-uniform)
+                    const uint32_t t_s = tmem + 128 * u + lanes + (static_cast<uint32_t>(16 * half) << 16);
                     const float* col = reinterpret_cast<const float*>(smem + C::kColOff) + u * kTok + c4;
                     const float* nvs = reinterpret_cast<const float*>(smem + C::kNvOff) + u * kTok + c4;
                     // how far a score may pass its row's base: p n_v stays below 2^15.99
                     const float4 nm = *reinterpret_cast<const float4*>(smem + C::kNmOff + 16 * u);
                     const float slack = fmaxf(
                         0.f, fminf(kSlack, 15.99f - __log2f(fmaxf(fmaxf(nm.x, nm.y), fmaxf(nm.z, nm.w)))));
-                    // stmatrix: lane 8m + k gives row k of matrix m, rows 8m .. 8m + 7 of
-                    // the warp's 32 and eight tokens
-                    const uint32_t prow = smem_u32(smem + C::kPOff + u * 32768) + half * 16384 + (32 * quad + lane) * 128;
+                    // stmatrix: lane 8m + k gives row k of matrix m: rows 0-7 and 8-15 of
+                    // eight tokens, then of the next eight
+                    const uint32_t prow =
+                        smem_u32(smem + C::kPOff + u * 32768) + (32 * quad + 16 * half + (lane & 15)) * 128;
                     // One pass over S; a second one when some score has passed its
                     // row's base by more than the slack (a row's first tile, hardly
                     // any other), against bases moved to the tile's maxima.
-                    const bool masked = tok0 + 64 > full_below;   // some row sees these tokens in part
+                    const bool masked = tok0 + kTok > full_below;   // some row sees the tile in part
 #pragma unroll 1
                     for (int pass = 0;; ++pass) {
-                        float2 sum[4], nb[4];
-                        float mq[4];
+                        float2 sum[2], nb[2];
+                        float mq[2];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
+                        for (int q = 0; q < 2; ++q) {
                             const float b0 = m_base[q] == -INFINITY ? 0.f : -m_base[q];
                             nb[q] = make_float2(b0, b0);
                             sum[q] = make_float2(0.f, 0.f);
                             mq[q] = -INFINITY;
                         }
-                        // x of columns 16c .. 16c + 15 from S, and P from x
-                        auto scores = [&](int c, const uint32_t* v0, const uint32_t* v1, float2 (&x)[8]) {
+                        // x of columns 16c .. 16c + 15 from S, x[2i + q], and P from x
+                        auto scores = [&](int c, const uint32_t* v, float2 (&x)[4]) {
                             float4 s4 = make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e, p.scale_log2e);
                             if constexpr (KB != 0) s4 = *reinterpret_cast<const float4*>(col + 16 * c);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int i = e >> 2, q = e & 3;
-                                const uint32_t* f = (q < 2 ? v0 : v1) + 4 * i + 2 * (q & 1);
-                                x[e] = __ffma2_rn(make_float2(__uint_as_float(f[0]), __uint_as_float(f[1])),
+                            for (int e = 0; e < 4; ++e) {
+                                const int i = e >> 1, q = e & 1;
+                                x[e] = __ffma2_rn(make_float2(__uint_as_float(v[4 * i + 2 * q]), __uint_as_float(v[4 * i + 2 * q + 1])),
                                                   i ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y), nb[q]);
                             }
                         };
-                        auto weigh = [&](int c, const float2 (&x)[8]) {
+                        auto weigh = [&](int c, const float2 (&x)[4]) {
                             const float4 w4 = *reinterpret_cast<const float4*>(nvs + 16 * c);
-                            uint32_t pk[8];
+                            uint32_t pk[4];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int q = e & 3;
+                            for (int e = 0; e < 4; ++e) {
+                                const int q = e & 1;
                                 mq[q] = fmaxf(mq[q], fmaxf(x[e].x, x[e].y));
                                 const float2 pe = make_float2(fast_exp2(x[e].x), fast_exp2(x[e].y));
                                 sum[q] = __fadd2_rn(sum[q], pe);
-                                const float2 w = __fmul2_rn(pe, e >> 2 ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y));
+                                const float2 w = __fmul2_rn(pe, e >> 1 ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y));
                                 pk[e] = pack_half2(w.x, w.y);
                             }
-                            stsm_x4(prow + (((2 * c) ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
-                            stsm_x4(prow + (((2 * c + 1) ^ (lane & 7)) << 4), pk[4], pk[5], pk[6], pk[7]);
+                            stsm_x4(prow + (c >> 2) * 16384 + (((2 * (c & 3) + (lane >> 4)) ^ (lane & 7)) << 4), pk[0], pk[1],
+                                    pk[2], pk[3]);
                         };
                         if (!masked) {
-                            uint32_t v[2][32];
+                            uint32_t v[2][32];   // 64 columns each
                             tmem_ld_frag_issue(t_s, v[0]);
-                            tmem_ld_frag_issue(s_hi, v[1]);
-                            tmem_ld_wait(v[0], v[1]);
+                            tmem_ld_wait(v[0]);
+                            tmem_ld_frag_issue(t_s + 64, v[1]);
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                float2 x[8];
-                                scores(c, v[0] + 8 * c, v[1] + 8 * c, x);
+                            for (int c = 0; c < 8; ++c) {
+                                if (c == 4) tmem_ld_wait(v[1]);
+                                float2 x[4];
+                                scores(c, v[c >> 2] + 8 * (c & 3), x);
                                 weigh(c, x);
                             }
                         } else {
 #pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
+                            for (int c = 0; c < 8; ++c) {
                                 const int t0 = tok0 + 16 * c;
-                                uint32_t v0[8], v1[8];
-                                tmem_ld_frag_issue(t_s + 16 * c, v0);
-                                tmem_ld_frag_issue(s_hi + 16 * c, v1);
-                                uint32_t seen[4];   // this thread's columns: bits 0, 1, 8, 9
+                                uint32_t v[8];
+                                tmem_ld_frag_issue(t_s + 16 * c, v);
+                                uint32_t seen[2];   // this thread's columns: bits 0, 1, 8, 9
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int rr = row32 + (lane >> 2) + 8 * q;
+                                for (int q = 0; q < 2; ++q) {
                                     uint32_t w = 0u;
-                                    if (rr < p.rows && t0 < s.t_lim) {
-                                        w = tree_window(mask + node[q] * p.tree_words, p.tree_words, t0 - base);
+                                    if (mrow[q] != nullptr && t0 < s.t_lim) {
+                                        w = tree_window(mrow[q], p.tree_words, t0 - base);
                                         if (t0 + 16 > s.t_lim) w &= (1u << (s.t_lim - t0)) - 1u;
                                     }
                                     seen[q] = w >> (2 * (lane & 3));
                                 }
-                                tmem_ld_wait(v0, v1);
-                                float2 x[8];
-                                scores(c, v0, v1, x);
+                                tmem_ld_wait(v);
+                                float2 x[4];
+                                scores(c, v, x);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    if (!((seen[e & 3] >> (8 * (e >> 2))) & 1u)) x[e].x = -INFINITY;
-                                    if (!((seen[e & 3] >> (8 * (e >> 2))) & 2u)) x[e].y = -INFINITY;
+                                for (int e = 0; e < 4; ++e) {
+                                    if (!((seen[e & 1] >> (8 * (e >> 1))) & 1u)) x[e].x = -INFINITY;
+                                    if (!((seen[e & 1] >> (8 * (e >> 1))) & 2u)) x[e].y = -INFINITY;
                                 }
                                 weigh(c, x);
                             }
                         }
                         bool grow = false;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) grow |= mq[q] > (m_base[q] == -INFINITY ? -INFINITY : slack);
-                        if (pass > 0 || !named_bar_or(1 + quad, 64, grow)) {
+                        for (int q = 0; q < 2; ++q) grow |= mq[q] > (m_base[q] == -INFINITY ? -INFINITY : slack);
+                        if (pass > 0 || !__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) l_sum[q] += sum[q].x + sum[q].y;
+                            for (int q = 0; q < 2; ++q) l_sum[q] += sum[q].x + sum[q].y;
                             break;
                         }
-                        // the rows' maxima over both warps' tokens
+                        float alpha[2];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            mq[q] = fmaxf(mq[q], __shfl_xor_sync(0xffffffffu, mq[q], 1));
-                            mq[q] = fmaxf(mq[q], __shfl_xor_sync(0xffffffffu, mq[q], 2));
-                        }
-                        float* mine = xm + (lane >> 2);
-                        if (half == 1 && (lane & 3) == 0)
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) mine[8 * q] = mq[q];
-                        named_bar_sync(1 + quad, 64);
-                        if (half == 0) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) mq[q] = fmaxf(mq[q], mine[8 * q]);
-                            __syncwarp();
-                            if ((lane & 3) == 0)
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) mine[8 * q] = mq[q];
-                        }
-                        named_bar_sync(1 + quad, 64);
-                        float alpha[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (half == 1) mq[q] = mine[8 * q];
+                        for (int q = 0; q < 2; ++q) {   // the row's maximum is spread over its four lanes
+                            float mx = fmaxf(mq[q], __shfl_xor_sync(0xffffffffu, mq[q], 1));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                             const bool fresh = m_base[q] == -INFINITY;
-                            const bool up = mq[q] > (fresh ? -INFINITY : slack);
-                            alpha[q] = up ? (fresh ? 0.f : fast_exp2(-mq[q])) : 1.f;
+                            const bool up = mx > (fresh ? -INFINITY : slack);
+                            alpha[q] = up ? (fresh ? 0.f : fast_exp2(-mx)) : 1.f;
                             l_sum[q] *= alpha[q];
-                            if (up) m_base[q] = (fresh ? 0.f : m_base[q]) + mq[q];
+                            if (up) m_base[q] = (fresh ? 0.f : m_base[q]) + mx;
                         }
-                        if (n > 0) {   // rescale the rows of O, this warp its 64 columns; there lane = row
+                        if (n > 0) {   // rescale the rows of O
                             wait(bar_o + 8 * (1 - u), ((t - 1) >> 1) & 1);   // P.V(t - 1) is done
                             tc_fence_after();
-                            float al = 1.f;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const float o = __shfl_sync(0xffffffffu, alpha[q], 4 * (lane & 7));
-                                if ((lane >> 3) == q) al = o;
-                            }
+                            const uint32_t t_or = tm_o + lanes + (static_cast<uint32_t>(16 * half) << 16);
 #pragma unroll 1
-                            for (int c = 0; c < 2; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32(tm_o + lanes + 64 * half + 32 * c, o);
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t o[8];
+                                tmem_ld_frag_issue(t_or + 16 * c, o);
+                                tmem_ld_wait(o);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                                tmem_st32(tm_o + lanes + 64 * half + 32 * c, o);
+                                for (int e = 0; e < 8; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[(e >> 1) & 1]);
+                                tmem_st_frag256(t_or + 16 * c, o);
                             }
+                            tmem_st_wait();
                         }
                     }
                     fence_proxy_async();   // the MMA reads P through the async proxy
@@ -731,17 +701,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             tc_fence_after();
             if (pos + s.ntiles >= hi || stalled) griddep_launch_dependents();   // last segment: let the merge launch
             const int late = named_bar_or(5, 256, stalled);                  // (both V^T tiles are free)
-            if (live && !late) {
-                float* sl = reinterpret_cast<float*>(smem + C::kNvOff) + 32 * quad;    // (the norms and scales are read)
-                float* sm = reinterpret_cast<float*>(smem + C::kColOff) + 32 * quad;
+            if (row32 < p.rows && !late) {
+                float2* sml = reinterpret_cast<float2*>(smem + C::kColOff) + 32 * quad;   // (the scales and norms are read)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 2; ++q) {
                     float l = l_sum[q] + __shfl_xor_sync(0xffffffffu, l_sum[q], 1);
                     l += __shfl_xor_sync(0xffffffffu, l, 2);
-                    if ((lane & 3) == 0) {
-                        if (half == 1) xm[(lane >> 2) + 8 * q] = l;
-                        else sl[(lane >> 2) + 8 * q] = l, sm[(lane >> 2) + 8 * q] = m_base[q];
-                    }
+                    if ((lane & 3) == 0) sml[16 * half + (lane >> 2) + 8 * q] = make_float2(m_base[q], l);
                 }
                 const int r = 32 * quad + lane;
                 uint8_t* xo = smem + C::kVtOff + r * 512;
@@ -768,7 +734,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     reinterpret_cast<float4*>(p.part_o + (slot_row + row) * kD)[lane] = make_float4(a.x, a.y, b.x, b.y);
                 }
                 if (half == 0 && lane < nrows)
-                    reinterpret_cast<float2*>(p.part_ml)[slot_row + lane] = make_float2(sm[lane], sl[lane] + xm[lane]);
+                    reinterpret_cast<float2*>(p.part_ml)[slot_row + lane] = sml[lane];
             }
             bad = end_segment(s.ntiles);   // everything is free for the next segment
         }
