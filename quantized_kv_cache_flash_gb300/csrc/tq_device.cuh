@@ -579,10 +579,11 @@ __device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t r0, uint32
 }
 
 // The same untransposed: lane 8i + k gives the address of row k of matrix i.
+// (No memory clobber: loads of other shared memory may move across it; what
+// reads the matrices is ordered behind it by a volatile fence.)
 __device__ __forceinline__ void stsm_x4(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(r0), "r"(r1),
-                 "r"(r2), "r"(r3)
-                 : "memory");
+                 "r"(r2), "r"(r3));
 }
 
 // In-thread 128-point Walsh-Hadamard transform (unnormalised).  From stride

@@ -443,19 +443,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         while (pos < hi && !bad) {
             const Segment s = segment();
             if (wg == 2) {
-                auto norm_k = [&](int n) {   // (0 past the end)
+                // (raw halves, converted where they are used: a tile later)
+                auto norm = [&](const __half* norms, int n) {   // (0 past the end)
                     const int t = (s.k0 + n) * kTok + r;
-                    return KB != 0 && n < s.ntiles && t < s.t_lim ? __half2float(p.k_norm[s.row0 + t]) : 0.f;
+                    return n < s.ntiles && t < s.t_lim ? norms[s.row0 + t] : __ushort_as_half(0);
                 };
-                auto norm_v = [&](int n) {
-                    const int t = (s.k0 + n) * kTok + r;
-                    return n < s.ntiles && t < s.t_lim ? __half2float(p.v_norm[s.row0 + t]) : 0.f;
-                };
-                float nk = norm_k(0), nv = norm_v(0);
+                __half nk = __ushort_as_half(0), nk1 = nk;
+                if constexpr (KB != 0) nk = norm(p.k_norm, 0);
+                __half nvh = norm(p.v_norm, 0);
 #pragma unroll 1
                 for (int n = 0; n < s.ntiles; ++n) {
                     const int t = tbase + n, u = t & 1;
-                    const float nk1 = norm_k(n + 1), nv1 = norm_v(n + 1);
+                    if constexpr (KB != 0) nk1 = norm(p.k_norm, n + 1);
+                    const __half nv1 = norm(p.v_norm, n + 1);
                     if constexpr (KB != 0) {
                         wait(bar_k + 8 * u, (t >> 1) & 1);
                         if (t >= 2) wait(bar_s + 8 * u, ((t >> 1) - 1) & 1);   // S(t - 2) has read its K tile
@@ -479,7 +479,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     }
                     if (t >= 2) wait(bar_p + 8 * u, ((t >> 1) - 1) & 1);   // softmax(t - 2) has read its scales and norms
                     if constexpr (KB != 0)
-                        (reinterpret_cast<float*>(smem + C::kColOff) + u * kTok)[frag_place(r)] = nk * p.scale_log2e;
+                        (reinterpret_cast<float*>(smem + C::kColOff) + u * kTok)[frag_place(r)] =
+                            __half2float(nk) * p.scale_log2e;
+                    const float nv = __half2float(nvh);
                     // (an overflowed norm counts as 65504: 0 * inf would be NaN in the
                     // rows that do not see the token; it does not count for the
                     // slack, so the rows that do may overflow)
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     if (lane == 0) (reinterpret_cast<uint32_t*>(smem + C::kNmOff) + 4 * u)[warp & 3] = nmax;
                     mbar_arrive(bar_kr + 8 * u);
                     nk = nk1;
-                    nv = nv1;
+                    nvh = nv1;
                 }
             } else {
                 const Tables vt{p.vtab[0], p.vtab[1], p.vtab[2], p.vtab[3]};
@@ -567,125 +569,152 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     const float4 nm = *reinterpret_cast<const float4*>(smem + C::kNmOff + 16 * u);
                     const float slack = fmaxf(
                         0.f, fminf(kSlack, 15.99f - __log2f(fmaxf(fmaxf(nm.x, nm.y), fmaxf(nm.z, nm.w)))));
+                    const float most = fast_exp2(slack);
                     // stmatrix: lane 8m + k gives row k of matrix m: rows 0-7 and 8-15 of
                     // eight tokens, then of the next eight
                     const uint32_t prow =
                         smem_u32(smem + C::kPOff + u * 32768) + (32 * quad + 16 * half + (lane & 15)) * 128;
-                    // One pass over S; a second one when some score has passed its
-                    // row's base by more than the slack (a row's first tile, hardly
-                    // any other), against bases moved to the tile's maxima.
                     const bool masked = tok0 + kTok > full_below;   // some row sees the tile in part
-#pragma unroll 1
-                    for (int pass = 0;; ++pass) {
-                        float2 sum[2], nb[2];
-                        float mq[2];
+                    float2 nb[2], sum[2];
+                    auto scale4 = [&](int c) {
+                        if constexpr (KB != 0) return *reinterpret_cast<const float4*>(col + 16 * c);
+                        return make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e, p.scale_log2e);
+                    };
+                    auto norm4 = [&](int c) { return *reinterpret_cast<const float4*>(nvs + 16 * c); };
+                    // x of columns 16c .. 16c + 15 from S, x[2i + q], and P from x
+                    auto scores = [&](const float4& s4, const uint32_t* v, float2 (&x)[4]) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = e >> 1, q = e & 1;
+                            x[e] = __ffma2_rn(make_float2(__uint_as_float(v[4 * i + 2 * q]), __uint_as_float(v[4 * i + 2 * q + 1])),
+                                              i ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y), nb[q]);
+                        }
+                    };
+                    auto hide = [&](int c, float2 (&x)[4]) {   // tokens that a row does not see
+                        const int t0 = tok0 + 16 * c;
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t w = 0u;
+                            if (mrow[q] != nullptr && t0 < s.t_lim) {
+                                w = tree_window(mrow[q], p.tree_words, t0 - base);
+                                if (t0 + 16 > s.t_lim) w &= (1u << (s.t_lim - t0)) - 1u;
+                            }
+                            w >>= 2 * (lane & 3);   // this thread's columns: bits 0, 1, 8, 9
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                if (!((w >> (8 * i)) & 1u)) x[2 * i + q].x = -INFINITY;
+                                if (!((w >> (8 * i)) & 2u)) x[2 * i + q].y = -INFINITY;
+                            }
+                        }
+                    };
+                    auto weigh = [&](int c, const float4& w4, const float2 (&x)[4]) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int q = e & 1;
+                            const float2 pe = make_float2(fast_exp2(x[e].x), fast_exp2(x[e].y));
+                            sum[q] = __fadd2_rn(sum[q], pe);
+                            const float2 w = __fmul2_rn(pe, e >> 1 ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y));
+                            pk[e] = pack_half2(w.x, w.y);
+                        }
+                        stsm_x4(prow + (c >> 2) * 16384 + (((2 * (c & 3) + (lane >> 4)) ^ (lane & 7)) << 4), pk[0], pk[1],
+                                pk[2], pk[3]);
+                    };
+                    auto set_base = [&]() {
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const float b0 = m_base[q] == -INFINITY ? 0.f : -m_base[q];
                             nb[q] = make_float2(b0, b0);
                             sum[q] = make_float2(0.f, 0.f);
-                            mq[q] = -INFINITY;
                         }
-                        // x of columns 16c .. 16c + 15 from S, x[2i + q], and P from x
-                        auto scores = [&](int c, const uint32_t* v, float2 (&x)[4]) {
-                            float4 s4 = make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e, p.scale_log2e);
-                            if constexpr (KB != 0) s4 = *reinterpret_cast<const float4*>(col + 16 * c);
+                    };
+                    // P against the rows' bases.  A score that passes its base by more
+                    // than the slack shows in the thread's sum (which may also pass
+                    // 2^slack without one); then, and on a row's first tile, the bases
+                    // move to the tile's maxima before (another) pass.
+                    bool move = __any_sync(0xffffffffu, m_base[0] == -INFINITY || m_base[1] == -INFINITY);
+#pragma unroll 1
+                    for (;;) {
+                        set_base();
+                        if (move) {
+                            float mq[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t v[8];
+                                tmem_ld_frag_issue(t_s + 16 * c, v);
+                                tmem_ld_wait(v);
+                                float2 x[4];
+                                scores(scale4(c), v, x);
+                                if (masked) hide(c, x);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int i = e >> 1, q = e & 1;
-                                x[e] = __ffma2_rn(make_float2(__uint_as_float(v[4 * i + 2 * q]), __uint_as_float(v[4 * i + 2 * q + 1])),
-                                                  i ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y), nb[q]);
+                                for (int e = 0; e < 4; ++e) mq[e & 1] = fmaxf(mq[e & 1], fmaxf(x[e].x, x[e].y));
                             }
-                        };
-                        auto weigh = [&](int c, const float2 (&x)[4]) {
-                            const float4 w4 = *reinterpret_cast<const float4*>(nvs + 16 * c);
-                            uint32_t pk[4];
+                            float alpha[2];
+                            bool grow = false;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int q = e & 1;
-                                mq[q] = fmaxf(mq[q], fmaxf(x[e].x, x[e].y));
-                                const float2 pe = make_float2(fast_exp2(x[e].x), fast_exp2(x[e].y));
-                                sum[q] = __fadd2_rn(sum[q], pe);
-                                const float2 w = __fmul2_rn(pe, e >> 1 ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y));
-                                pk[e] = pack_half2(w.x, w.y);
+                            for (int q = 0; q < 2; ++q) {   // the row's maximum is spread over its four lanes
+                                float mx = fmaxf(mq[q], __shfl_xor_sync(0xffffffffu, mq[q], 1));
+                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                                const bool fresh = m_base[q] == -INFINITY;
+                                const bool up = mx > (fresh ? -INFINITY : slack);
+                                alpha[q] = up ? (fresh ? 0.f : fast_exp2(-mx)) : 1.f;
+                                l_sum[q] *= alpha[q];
+                                if (up) m_base[q] = (fresh ? 0.f : m_base[q]) + mx;
+                                grow |= up;
                             }
-                            stsm_x4(prow + (c >> 2) * 16384 + (((2 * (c & 3) + (lane >> 4)) ^ (lane & 7)) << 4), pk[0], pk[1],
-                                    pk[2], pk[3]);
-                        };
+                            if (n > 0 && __any_sync(0xffffffffu, grow)) {   // rescale the rows of O
+                                wait(bar_o + 8 * (1 - u), ((t - 1) >> 1) & 1);   // P.V(t - 1) is done
+                                tc_fence_after();
+                                const uint32_t t_or = tm_o + lanes + (static_cast<uint32_t>(16 * half) << 16);
+#pragma unroll 1
+                                for (int c = 0; c < 8; ++c) {
+                                    uint32_t o[8];
+                                    tmem_ld_frag_issue(t_or + 16 * c, o);
+                                    tmem_ld_wait(o);
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e)
+                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[(e >> 1) & 1]);
+                                    tmem_st_frag256(t_or + 16 * c, o);
+                                }
+                                tmem_st_wait();
+                            }
+                            set_base();
+                        }
                         if (!masked) {
                             uint32_t v[2][32];   // 64 columns each
                             tmem_ld_frag_issue(t_s, v[0]);
+                            float4 s4 = scale4(0), w4 = norm4(0);
                             tmem_ld_wait(v[0]);
                             tmem_ld_frag_issue(t_s + 64, v[1]);
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
+                                const float4 sn = scale4((c + 1) & 7), wn = norm4((c + 1) & 7);   // of the next columns
                                 if (c == 4) tmem_ld_wait(v[1]);
                                 float2 x[4];
-                                scores(c, v[c >> 2] + 8 * (c & 3), x);
-                                weigh(c, x);
+                                scores(s4, v[c >> 2] + 8 * (c & 3), x);
+                                weigh(c, w4, x);
+                                s4 = sn;
+                                w4 = wn;
                             }
                         } else {
 #pragma unroll 1
                             for (int c = 0; c < 8; ++c) {
-                                const int t0 = tok0 + 16 * c;
                                 uint32_t v[8];
                                 tmem_ld_frag_issue(t_s + 16 * c, v);
-                                uint32_t seen[2];   // this thread's columns: bits 0, 1, 8, 9
-#pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    uint32_t w = 0u;
-                                    if (mrow[q] != nullptr && t0 < s.t_lim) {
-                                        w = tree_window(mrow[q], p.tree_words, t0 - base);
-                                        if (t0 + 16 > s.t_lim) w &= (1u << (s.t_lim - t0)) - 1u;
-                                    }
-                                    seen[q] = w >> (2 * (lane & 3));
-                                }
                                 tmem_ld_wait(v);
                                 float2 x[4];
-                                scores(c, v, x);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if (!((seen[e & 1] >> (8 * (e >> 1))) & 1u)) x[e].x = -INFINITY;
-                                    if (!((seen[e & 1] >> (8 * (e >> 1))) & 2u)) x[e].y = -INFINITY;
-                                }
-                                weigh(c, x);
+                                scores(scale4(c), v, x);
+                                hide(c, x);
+                                weigh(c, norm4(c), x);
                             }
                         }
-                        bool grow = false;
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) grow |= mq[q] > (m_base[q] == -INFINITY ? -INFINITY : slack);
-                        if (pass > 0 || !__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) l_sum[q] += sum[q].x + sum[q].y;
+                        const float s0 = sum[0].x + sum[0].y, s1 = sum[1].x + sum[1].y;
+                        if (move || !__any_sync(0xffffffffu, fmaxf(s0, s1) > most)) {
+                            l_sum[0] += s0;
+                            l_sum[1] += s1;
                             break;
                         }
-                        float alpha[2];
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {   // the row's maximum is spread over its four lanes
-                            float mx = fmaxf(mq[q], __shfl_xor_sync(0xffffffffu, mq[q], 1));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                            const bool fresh = m_base[q] == -INFINITY;
-                            const bool up = mx > (fresh ? -INFINITY : slack);
-                            alpha[q] = up ? (fresh ? 0.f : fast_exp2(-mx)) : 1.f;
-                            l_sum[q] *= alpha[q];
-                            if (up) m_base[q] = (fresh ? 0.f : m_base[q]) + mx;
-                        }
-                        if (n > 0) {   // rescale the rows of O
-                            wait(bar_o + 8 * (1 - u), ((t - 1) >> 1) & 1);   // P.V(t - 1) is done
-                            tc_fence_after();
-                            const uint32_t t_or = tm_o + lanes + (static_cast<uint32_t>(16 * half) << 16);
-#pragma unroll 1
-                            for (int c = 0; c < 8; ++c) {
-                                uint32_t o[8];
-                                tmem_ld_frag_issue(t_or + 16 * c, o);
-                                tmem_ld_wait(o);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[(e >> 1) & 1]);
-                                tmem_st_frag256(t_or + 16 * c, o);
-                            }
-                            tmem_st_wait();
-                        }
+                        move = true;
                     }
                     fence_proxy_async();   // the MMA reads P through the async proxy
                 }
