@@ -208,6 +208,19 @@ int encode_rows_map(CUtensorMap* map, const void* base, uint64_t rows) {
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? TQ_OK : TQ_ERR_CUDA;
 }
+int encode_tokens_map(CUtensorMap* map, const void* base, uint64_t heads, uint64_t tokens) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode_tiled();
+    if (enc == nullptr) return TQ_ERR_CUDA;
+    cuuint64_t dims[3] = {kD, heads, tokens};
+    cuuint64_t strides[2] = {kD * 2, kD * 2 * heads};
+    cuuint32_t box[3] = {64, 1, 128};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? TQ_OK : TQ_ERR_CUDA;
+}
+
 constexpr long long kMinChunks3 = 96;  // chunks per CTA below which a third wave does not pay
 
 // Decode grid: waves of resident CTAs -- the later ones, placed wherever a
@@ -621,8 +634,8 @@ int tq_encode_append_packed(tq_ctx** pctx, const tq_cache* c, const void* k_new,
     std::memcpy(p.v_mag, c->codebook_v + (1 << (vb - 1)), sizeof(float) << (vb - 1));
     CUtensorMap kmap, vmap;
     if (nvec > uint64_t(tq::kEncodeSmallMax)) {
-        if ((r = tq::host::encode_rows_map(&kmap, k_new, nvec)) != TQ_OK ||
-            (r = tq::host::encode_rows_map(&vmap, v_new, nvec)) != TQ_OK)
+        if ((r = tq::host::encode_tokens_map(&kmap, k_new, c->num_kv_heads, total)) != TQ_OK ||
+            (r = tq::host::encode_tokens_map(&vmap, v_new, c->num_kv_heads, total)) != TQ_OK)
             return r;
     }
     ctx->last_stream = static_cast<cudaStream_t>(stream);

@@ -356,8 +356,10 @@ __device__ __forceinline__ void store_codes_warp(const uint32_t (&code)[4], uint
 
 // The codes of one vector from its exact transform (the warp's lane l holds
 // dims 4l .. 4l + 3 of x): Y = H (s * x) in integer units of 2^-24, compared
-// with the midpoints of the codebook (mag: its positive half) times sqrt(128) n
-// in double; ties to the lower index.
+// with the midpoints of the codebook (mag: its positive half) times sqrt(128) n.
+// Those are formed in double, a midpoint per lane -- double arithmetic is slow
+// here -- and compared as integers: Y > t is Y > floor(t), Y >= t is Y >= ceil(t).
+// Ties go to the lower index.
 template <int BITS>
 __device__ __noinline__ void encode_exact_warp(const uint2 raw, uint8_t* dst, const uint32_t (&signs)[4],
                                                const float* mag, int lane) {
@@ -389,20 +391,27 @@ __device__ __noinline__ void encode_exact_warp(const uint2 raw, uint8_t* dst, co
             y[i] = (lane & m) ? (o - y[i]) : (y[i] + o);
         }
     }
-    const double unit = sqrt(128.0 * ss) * 16777216.0;   // sqrt(128) n in units of 2^-24
-    uint32_t code[4];
+    const int k = lane < H - 1 ? lane : 0;   // this lane's midpoint, in units of 2^-24
+    const double t = 0.5 * (static_cast<double>(mag[k]) + static_cast<double>(mag[k + 1])) *
+                     (sqrt(128.0 * ss) * 16777216.0);
+    const long long below = __double2ll_rd(t), above = __double2ll_ru(t);
+    long long a[4];
+    bool neg[4];
+    uint32_t rank[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const bool neg = !(y[i] > 0);
-        const double a = fabs(static_cast<double>(y[i]));
-        uint32_t rank = 0;
-#pragma unroll
-        for (int k = 0; k < H - 1; ++k) {
-            const double t = 0.5 * (static_cast<double>(mag[k]) + static_cast<double>(mag[k + 1])) * unit;
-            rank += (neg ? (a >= t && a > 0.0) : a > t) ? 1u : 0u;
-        }
-        code[i] = (neg ? static_cast<uint32_t>(H) : 0u) | rank;
+        neg[i] = !(y[i] > 0);
+        a[i] = neg[i] ? -y[i] : y[i];
     }
+#pragma unroll
+    for (int j = 0; j < H - 1; ++j) {
+        const long long lo = __shfl_sync(0xffffffffu, below, j), hi = __shfl_sync(0xffffffffu, above, j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rank[i] += (neg[i] ? (a[i] >= hi && a[i] > 0) : a[i] > lo) ? 1u : 0u;
+    }
+    uint32_t code[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) code[i] = (neg[i] ? static_cast<uint32_t>(H) : 0u) | rank[i];
     store_codes_warp<BITS>(code, dst, lane);
 }
 
@@ -453,11 +462,51 @@ __device__ __forceinline__ float fma_sq_f16(unsigned short x, float acc) {
 //          dim 8k+j, bit 4j+3 = bit k of the code of dim 24+j.
 //   4-bit: word k = dims 8k..8k+7: rank of dim 8k+j in bits 4j..4j+2, the
 //          sign of dim 8k+j (j < 4) in bit 8j+7, of dim 8k+4+j in bit 8j+3.
-//   NEAR: near becomes at most the smallest distance of a |y| from a T_k or 0.
+//   NEAR: the smallest of near becomes at most that of all |y|'s distances from a
+//   T_k or 0.
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Word of 8 dims of a 4-bit record (see pack_quarter).
+template <bool NEAR>
+__device__ __forceinline__ uint32_t pack_word4(const uint32_t* r, const float (&T)[7], float (&near)[4]) {
+    auto shin = [](uint32_t acc, uint32_t v) { return __funnelshift_l(v, acc, 1); };
+    uint32_t b0[8], b1[8], b2[8], p[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float y = __uint_as_float(r[j]);
+        const float a = fabsf(y);
+        uint32_t d[7];
+#pragma unroll
+        for (int t = 0; t < 7; ++t) d[t] = fbits(T[t] - a);
+        if constexpr (NEAR) {
+            // (four chains over the elements, 3-input minima)
+            auto ab = [&](int t) { return fabsf(__uint_as_float(d[t])); };
+            near[j & 3] = min3(near[j & 3], min3(a, ab(0), ab(1)),
+                               min3(min3(ab(2), ab(3), ab(4)), ab(5), ab(6)));
+        }
+        const uint32_t x135 = d[1] ^ d[3] ^ d[5];
+        b2[j] = d[3];
+        b1[j] = x135;
+        b0[j] = x135 ^ d[0] ^ d[2] ^ d[4] ^ d[6];
+        p[j] = fbits(__fsub_rn(0.f, y));
+    }
+    uint32_t acc = 0;
+#pragma unroll
+    for (int j = 7; j >= 0; --j) {
+        const int s = (j & 1) ? (j - 1) / 2 : 4 + j / 2;   // whose sign sits in bit 4j+3
+        acc = shin(shin(shin(shin(acc, p[s]), b2[j]), b1[j]), b0[j]);
+    }
+    return acc ^ 0x88888888u;
+}
+
 template <int BITS, bool NEAR>
 __device__ __forceinline__ void pack_quarter(const uint32_t (&r)[32],
                                              const float (&T)[(1 << (BITS - 1)) - 1], uint32_t* w,
-                                             float& near) {
+                                             float (&near)[4]) {
     auto shin = [](uint32_t acc, uint32_t v) { return __funnelshift_l(v, acc, 1); };  // acc << 1 | v >> 31
     if constexpr (BITS == 3) {
         struct Bits {
@@ -468,7 +517,7 @@ __device__ __forceinline__ void pack_quarter(const uint32_t (&r)[32],
             const float a = fabsf(y);
             const float d0 = T[0] - a, d1 = T[1] - a, d2 = T[2] - a;
             if constexpr (NEAR)
-                near = fminf(fminf(near, a), fminf(fminf(fabsf(d0), fabsf(d1)), fabsf(d2)));
+                near[i & 3] = min3(near[i & 3], a, min3(fabsf(d0), fabsf(d1), fabsf(d2)));
             Bits o;
             o.b1 = fbits(d1);
             o.b0 = fbits(d0) ^ fbits(d1) ^ fbits(d2);
@@ -492,34 +541,7 @@ __device__ __forceinline__ void pack_quarter(const uint32_t (&r)[32],
         w[2] = a2 ^ 0xCCCCCCCCu;
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t b0[8], b1[8], b2[8], p[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float y = __uint_as_float(r[8 * k + j]);
-                const float a = fabsf(y);
-                uint32_t d[7];
-#pragma unroll
-                for (int t = 0; t < 7; ++t) d[t] = fbits(T[t] - a);
-                if constexpr (NEAR) {
-                    near = fminf(near, a);
-#pragma unroll
-                    for (int t = 0; t < 7; ++t) near = fminf(near, fabsf(__uint_as_float(d[t])));
-                }
-                const uint32_t x135 = d[1] ^ d[3] ^ d[5];
-                b2[j] = d[3];
-                b1[j] = x135;
-                b0[j] = x135 ^ d[0] ^ d[2] ^ d[4] ^ d[6];
-                p[j] = fbits(__fsub_rn(0.f, y));
-            }
-            uint32_t acc = 0;
-#pragma unroll
-            for (int j = 7; j >= 0; --j) {
-                const int s = (j & 1) ? (j - 1) / 2 : 4 + j / 2;   // whose sign sits in bit 4j+3
-                acc = shin(shin(shin(shin(acc, p[s]), b2[j]), b1[j]), b0[j]);
-            }
-            w[k] = acc ^ 0x88888888u;
-        }
+        for (int k = 0; k < 4; ++k) w[k] = pack_word4<NEAR>(r + 8 * k, T, near);
     }
 }
 
@@ -593,7 +615,11 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
     const int lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int nvec = PACKED ? p.total * p.hkv : p.batch * p.hkv * p.t_new;   // below 2^31 (the host checks)
-    const int tiles_s = (nvec + kTcVecs - 1) / kTcVecs;
+    // a packed append's tile is 128 tokens of one KV head (rows then write
+    // neighbouring records; with the vectors taken in the order of the input, a
+    // token's heads next to each other, the scattered stores took twice as long),
+    // the heads of a token block one after the other
+    const int tiles_s = PACKED ? (p.total + kTcVecs - 1) / kTcVecs * p.hkv : (nvec + kTcVecs - 1) / kTcVecs;
     const int tiles_k = (KB == 0) ? 0 : tiles_s;
     const int tiles = tiles_k + tiles_s;
     const uint32_t bar_full = smem_u32(smem + kTcBarOff);   // + 8 s
@@ -617,11 +643,17 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
         }
         s_tile[s] = t;
         const bool is_v = t >= tiles_k;
-        const int row0 = (is_v ? t - tiles_k : t) * kTcVecs;
+        const int ts = is_v ? t - tiles_k : t;
         const uint32_t dst = smem_u32(smem + kTcXOff + s * 32768);
         mbar_arrive_expect_tx(bar, 32768);
-        tma_g2s_2d(dst, is_v ? &vmap : &kmap, 0, row0, bar);
-        tma_g2s_2d(dst + 16384, is_v ? &vmap : &kmap, 64, row0, bar);
+        if constexpr (PACKED) {
+            const int blk = static_cast<int>((static_cast<uint64_t>(ts) * p.div_h_m) >> p.div_h_s);
+            tma_g2s_3d(dst, is_v ? &vmap : &kmap, 0, ts - blk * p.hkv, blk * kTcVecs, bar);
+            tma_g2s_3d(dst + 16384, is_v ? &vmap : &kmap, 64, ts - blk * p.hkv, blk * kTcVecs, bar);
+        } else {
+            tma_g2s_2d(dst, is_v ? &vmap : &kmap, 0, ts * kTcVecs, bar);
+            tma_g2s_2d(dst + 16384, is_v ? &vmap : &kmap, 64, ts * kTcVecs, bar);
+        }
         return true;
     };
     const bool producer = tid == 32 * kTcEncWarps;
@@ -745,17 +777,20 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
             const int t = s_tile[g];
             if (t < 0) break;
             const bool is_v = t >= tiles_k;
-            const int v = (is_v ? t - tiles_k : t) * kTcVecs + r;
+            int v = (is_v ? t - tiles_k : t) * kTcVecs + r;
             // where this thread's vector goes: lengths[] is read now and
             // looked at only after the norm
-            const bool in_range = v < nvec;
+            bool in_range = v < nvec;
             int bh = 0, tt = 0, b = 0, L = 0;
             PackedSlot ps{};
             if constexpr (PACKED) {
-                const int vv = in_range ? v : 0;
-                const int tok = static_cast<int>((static_cast<uint64_t>(vv) * p.div_h_m) >> p.div_h_s);
-                ps = packed_slot(p, tok);
-                tt = vv - tok * p.hkv;   // the KV head
+                const int ts = is_v ? t - tiles_k : t;
+                const int blk = static_cast<int>((static_cast<uint64_t>(ts) * p.div_h_m) >> p.div_h_s);
+                const int tok = blk * kTcVecs + r;
+                tt = ts - blk * p.hkv;   // the KV head
+                in_range = tok < p.total;
+                ps = packed_slot(p, in_range ? tok : 0);
+                v = tok * p.hkv + tt;
             } else {
                 bh = static_cast<int>((static_cast<uint64_t>(in_range ? v : 0) * p.div_t_m) >> p.div_t_s);
                 tt = (in_range ? v : 0) - bh * p.t_new;
@@ -825,7 +860,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
             if (lane == 0) mbar_arrive(bar_xfree + 8 * g);   // X read here and by the MMA
             tc_fence_after();
             const float scale = sqrtf(S32) * 11.313708498984761f;   // sqrt(128) n
-            float near = INFINITY;
+            float near4[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
             auto encode_vec = [&](auto bits_tag) {
                 constexpr int BITS = decltype(bits_tag)::value;
                 constexpr int NT = (1 << (BITS - 1)) - 1;
@@ -837,6 +872,28 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
 #pragma unroll
                     for (int i = 0; i < NT; ++i) T[i] = p.k_gt[i] * scale;
                 }
+                if constexpr (PACKED) {
+                    // few dims a turn: with the distances kept, two quarters unrolled
+                    // outgrow the instruction cache
+#pragma unroll 1
+                    for (int q = 0; q < (BITS == 4 ? 8 : 4); ++q) {
+                        if constexpr (BITS == 4) {   // 16 dims: two words
+                            uint32_t ra[16];
+                            tmem_ld16(tacc + 16 * q, ra);
+                            const uint32_t w0 = pack_word4<true>(ra, T, near4), w1 = pack_word4<true>(ra + 8, T, near4);
+                            if (valid) *reinterpret_cast<uint2*>(dst + 8 * q) = make_uint2(w0, w1);
+                        } else {
+                            uint32_t w[BITS], ra[32];
+                            tmem_ld32(tacc + 32 * q, ra);
+                            pack_quarter<BITS, true>(ra, T, w, near4);
+                            if (valid) {
+#pragma unroll
+                                for (int i = 0; i < 3; ++i) reinterpret_cast<uint32_t*>(dst + 12 * q)[i] = w[i];
+                            }
+                        }
+                    }
+                    return;
+                }
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {   // quarters 2h, 2h+1 (bytes 8 h BITS ..)
                     uint32_t w[2 * BITS];
@@ -844,8 +901,8 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
                     tmem_ld32_issue(tacc + 64 * h, ra);
                     tmem_ld32_issue(tacc + 64 * h + 32, rb);
                     tmem_ld_wait(ra, rb);
-                    pack_quarter<BITS, PACKED>(ra, T, w, near);
-                    pack_quarter<BITS, PACKED>(rb, T, w + BITS, near);
+                    pack_quarter<BITS, false>(ra, T, w, near4);
+                    pack_quarter<BITS, false>(rb, T, w + BITS, near4);
                     if (valid) {
                         uint8_t* d = dst + h * 8 * BITS;
                         if constexpr (BITS == 4) {
@@ -873,6 +930,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
             if constexpr (PACKED) {
                 // vectors too near a threshold, one at a time by the whole warp
                 // (a zero vector's codes are right: every y and T is 0)
+                const float near = fminf(fminf(near4[0], near4[1]), fminf(near4[2], near4[3]));
                 unsigned redo = __ballot_sync(0xffffffffu, valid && S32 > 0.f && near <= kNearBand * sqrtf(S32));
                 while (redo) {
                     const int src = __ffs(redo) - 1;
@@ -1035,7 +1093,8 @@ static int launch_encode_t(const EncodeParams& p, long long nvec, const CUtensor
         return launch_pdl(tq_encode_small_kernel<KB, VB, PACKED>, grid, dim3(128), 0, stream, p);
     }
     if (kmap == nullptr || vmap == nullptr) return cudaErrorInvalidValue;
-    const long long tiles = (KB == 0 ? 1 : 2) * ((nvec + kTcVecs - 1) / kTcVecs);
+    const long long tiles = (KB == 0 ? 1 : 2) * (PACKED ? (p.total + kTcVecs - 1) / kTcVecs * 1ll * p.hkv
+                                                        : (nvec + kTcVecs - 1) / kTcVecs);
     const dim3 grid(static_cast<unsigned int>(std::min<long long>(tiles, 152ll * kTcCtasPerSm)));
     static std::atomic<uint64_t> attr_done{0};   // two CTAs' shared memory: the largest carveout
     const cudaError_t e = set_smem_attr_once(tq_encode_tc_kernel<KB, VB, PACKED>, kTcSmemAlloc, attr_done, 100);

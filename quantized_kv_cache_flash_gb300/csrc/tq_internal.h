@@ -302,6 +302,9 @@ int encode_kmap(CUtensorMap* map, const tq_cache* c);
 // Tensor map of `rows` fp16 vectors of 128 dims at `base` (16-byte aligned),
 // boxes of 128 rows x 64 halves (128-byte swizzle): the encode's input tiles.
 int encode_rows_map(CUtensorMap* map, const void* base, uint64_t rows);
+// Tensor map of fp16 vectors [tokens, heads, 128] at `base`, boxes of 128 tokens
+// of one head x 64 halves: a packed append's input tiles.
+int encode_tokens_map(CUtensorMap* map, const void* base, uint64_t heads, uint64_t tokens);
 // Whether every entry of a codebook is an fp16 value (no rounding residual).
 bool codebook_is_fp16(const float* cb, int n);
 
