@@ -574,7 +574,28 @@ __device__ __forceinline__ void tmem_st_frag256(uint32_t taddr, const uint32_t (
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
+// 16 lanes x 16 columns: lane 4g + t stores column 4j + t of row g from v[2j]
+// and of row g + 8 from v[2j + 1] (j = 0..3).  Complete after tmem_st_wait.
+__device__ __forceinline__ void tmem_st_frag_issue(uint32_t taddr, const uint32_t (&v)[8]) {
+    __syncwarp();
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&a)[8], uint32_t (&b)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                   "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// Where token t's scale and norm lie for a softmax on fragments: the four of lane
+// t's columns (2t, 2t + 1, 8 + 2t, 9 + 2t of 16) together.
+__device__ __forceinline__ int frag_place(int t) {
+    return (t & ~15) | ((t & 6) << 1) | ((t & 8) >> 2) | (t & 1);
+}
 
 // ---- tiles dequantised for the tcgen05 attention kernels ----
 // 32 dims (a quarter) of a record as fp16 pairs.

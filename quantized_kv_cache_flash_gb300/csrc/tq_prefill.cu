@@ -57,11 +57,13 @@ struct PreCfg {
     static constexpr int kSlotAlign = (KB == 0) ? 1024 : 128;
     static constexpr int kSlot = (kSlotRaw + kSlotAlign - 1) / kSlotAlign * kSlotAlign;
     static constexpr int kColOff = kStgOff + 2 * kSlot;         // fp32 n_k * scale * log2(e) [128]
+    static constexpr int kNvOff = kColOff + kTile * 4;          // packed: fp32 n_v [128], the largest of 32 [4]
     // mbarriers stg[2], S[2], O[2] (one per query tile), V^T stored, K stored,
     // tile 1's softmax done; TMEM slot; last tile copied; the CTA's item (packed)
-    static constexpr int kBarOff = kColOff + kTile * 4;
+    static constexpr int kBarOff = kNvOff + kTile * 4 + 16;
     static constexpr int kSmem = kBarOff + 88;
-    static constexpr int kSmemAlloc = kSmem + 1024;             // base alignment slack
+    static constexpr int kSmemAlloc = kSmem + 896;              // to a 1024-byte boundary from a 128-byte one
+    static_assert(kSmemAlloc <= 232448, "227 KB per CTA");
     static constexpr uint32_t kIdesc = umma_idesc_f16_f32(128, 128);
 };
 
@@ -337,8 +339,12 @@ __global__ void __launch_bounds__(256, 1)
             const Tables kt{p.ktab[0], p.ktab[1], p.ktab[2], p.ktab[3]};
             const uint8_t* rec = smem + C::kStgOff + (n & 1) * C::kSlot + r * C::kRbK;
             uint8_t* sK = smem + C::kKOff;
+            // (packed: the quarters in an order that differs between lanes whose
+            // records start in the same banks)
+            const int turn = PACKED ? (KB == 4 ? r >> 1 : r >> 3) : 0;
 #pragma unroll 1
-            for (int quarter = 0; quarter < 4; ++quarter) {
+            for (int q = 0; q < 4; ++q) {
+                const int quarter = (q + turn) & 3;
                 uint32_t hh[16];
                 dequant_q32<KB>(rec + quarter * (C::kRbK / 4), kt, hh);
 #pragma unroll
@@ -350,11 +356,23 @@ __global__ void __launch_bounds__(256, 1)
         }
     };
     // colK of tile n (n_k * scale * log2 e per token, 0 past the end)
+    // (packed: in the order of the softmax's fragments, with the V norms, 0 past
+    // the end; one that overflowed counts as 65504, since 0 * inf would be NaN in the
+    // rows before its token, and not for the slack)
     auto k_scales = [&](int n) {
+        const uint8_t* slot = smem + C::kStgOff + (n & 1) * C::kSlot;
+        const bool in = n * C::kTile + r < t_lim;
         if constexpr (KB != 0) {
-            const uint8_t* slot = smem + C::kStgOff + (n & 1) * C::kSlot;
             const float nk = __half2float(reinterpret_cast<const __half*>(slot + C::kSK)[r]);
-            colK[r] = n * C::kTile + r < t_lim ? nk * p.scale_log2e : 0.f;
+            colK[PACKED ? frag_place(r) : r] = in ? nk * p.scale_log2e : 0.f;
+        }
+        if constexpr (PACKED) {
+            const float nv = in ? __half2float(reinterpret_cast<const __half*>(slot + C::kSK + C::kSKn + C::kSV)[r]) : 0.f;
+            float* nvs = reinterpret_cast<float*>(smem + C::kNvOff);
+            nvs[frag_place(r)] = fminf(nv, 65504.f);
+            // (non-negative floats order like their bits)
+            const uint32_t top = __reduce_max_sync(0xffffffffu, nv < 65536.f ? __float_as_uint(nv) : 0u);
+            if ((r & 31) == 0) reinterpret_cast<uint32_t*>(nvs + C::kTile)[r >> 5] = top;
         }
     };
     // S_t(n) = Q'_t . K(n)^T into tile t's S columns
@@ -391,31 +409,29 @@ __global__ void __launch_bounds__(256, 1)
     auto v_dequant = [&](int n, int vw) {
         const Tables vt{p.vtab[0], p.vtab[1], p.vtab[2], p.vtab[3]};
         const uint8_t* slot = smem + C::kStgOff + (n & 1) * C::kSlot;
-        const int tok0 = n * C::kTile;
+        [[maybe_unused]] const int tok0 = n * C::kTile;
         const int lane = tid & 31, g = lane >> 2, tq4 = lane & 3;
         const int ta = 16 * vw + g, tb = ta + 8;
         const uint8_t* vrec = slot + C::kSK + C::kSKn;
-        const __half* vnorm = reinterpret_cast<const __half*>(slot + C::kSK + C::kSKn + C::kSV);
+        [[maybe_unused]] const __half* vnorm = reinterpret_cast<const __half*>(slot + C::kSK + C::kSKn + C::kSV);
         // tokens past the end: stale records still decode to finite
         // centroids, and their norm (and weight) is 0
         uint32_t ha[16], hb[16];
         dequant_q32<VB>(vrec + ta * C::kRbV + tq4 * (C::kRbV / 4), vt, ha);
         dequant_q32<VB>(vrec + tb * C::kRbV + tq4 * (C::kRbV / 4), vt, hb);
         // n_v scales the stored values, so P itself goes to the MMA: 128 x
-        // 128 multiplies a tile instead of the 256 x 128 of scaling P
-        // (packed sequences: an overflowed norm counts as 65504, since 0 * inf
-        // would be NaN in the rows before its token)
-        auto norm2 = [&](int t) {
-            if (tok0 + t >= t_lim) return __float2half2_rn(0.f);
-            return __half2half2(PACKED ? __hmin(vnorm[t], __ushort_as_half(0x7BFFu)) : vnorm[t]);
-        };
-        const __half2 na = norm2(ta), nb = norm2(tb);
+        // 128 multiplies a tile instead of the 256 x 128 of scaling P.  (Packed: P
+        // takes the norm and V stays the centroids, exact, so a term is rounded once.)
+        if constexpr (!PACKED) {
+            const __half2 na = tok0 + ta < t_lim ? __half2half2(vnorm[ta]) : __float2half2_rn(0.f);
+            const __half2 nb = tok0 + tb < t_lim ? __half2half2(vnorm[tb]) : __float2half2_rn(0.f);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&ha[k]), na);
-            const __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&hb[k]), nb);
-            ha[k] = *reinterpret_cast<const uint32_t*>(&a);
-            hb[k] = *reinterpret_cast<const uint32_t*>(&b);
+            for (int k = 0; k < 16; ++k) {
+                const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&ha[k]), na);
+                const __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&hb[k]), nb);
+                ha[k] = *reinterpret_cast<const uint32_t*>(&a);
+                hb[k] = *reinterpret_cast<const uint32_t*>(&b);
+            }
         }
         // stmatrix k2 stores dim pairs 2k2 (matrices 0, 1: tokens A, B) and
         // 2k2+1 (matrices 2, 3); lane 8j + c gives row c of matrix j: dim
@@ -515,6 +531,194 @@ __global__ void __launch_bounds__(256, 1)
         l_sum += st.x + st.y;
     };
 
+    // Packed: the same as MMA fragments.  Lane 4v + c of a warp has rows v + 8q (q =
+    // 0..3) of its 32 and columns 2c, 2c + 1 of every eight, so a thread reads a
+    // quarter of the tile's scales and norms.  A tile that every row sees takes one
+    // pass, P in registers until it is known that no score passes its row's base by
+    // more than the slack (which shows in the thread's sums); then, with the mask,
+    // and on a row's first tile, the rows' maxima are taken first.
+    float fm[4], fl[4];   // base (log2) and this thread's part of the sum
+    int flim[4];          // last visible token
+    if constexpr (PACKED) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int rq = 32 * (warp & 3) + ((tid & 31) >> 2) + 8 * q, jq = rq / p.group;
+            fm[q] = -INFINITY;
+            fl[q] = 0.f;
+            flim[q] = mt < mtiles && jq < p.pos_per_tile && mt * p.pos_per_tile + jq < tqn
+                          ? min(L - tqn + mt * p.pos_per_tile + jq, t_lim - 1)
+                          : -1;
+        }
+    }
+    auto softmax_frag = [&](int n) {
+        const int lane = tid & 31, tok0 = n * C::kTile;
+        const float* col = colK + 4 * (lane & 3);
+        const float* nvs = reinterpret_cast<const float*>(smem + C::kNvOff) + 4 * (lane & 3);
+        const float4 nm = *reinterpret_cast<const float4*>(smem + C::kNvOff + C::kTile * 4);
+        // p n_v stays below 2^15.99
+        const float slack =
+            fmaxf(0.f, fminf(10.f, 15.99f - __log2f(fmaxf(fmaxf(nm.x, nm.y), fmaxf(nm.z, nm.w)))));
+        const float most = fast_exp2(slack);
+        const bool masked = tok0 + C::kTile - 1 > lim_lo;
+        const uint32_t t_hi = t_s + (16u << 16);   // rows 16-31
+        float2 nb[4], sum[4];
+        auto scale4 = [&](int c) {
+            if constexpr (KB != 0) return *reinterpret_cast<const float4*>(col + 16 * c);
+            return make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e, p.scale_log2e);
+        };
+        // x of columns 16c .. 16c + 15 (x[4i + q]) from the S values of rows 0-15 and 16-31
+        auto scores = [&](int c, const uint32_t* v0, const uint32_t* v1, float2 (&x)[8]) {
+            const float4 s4 = scale4(c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = e >> 2, q = e & 3;
+                const uint32_t* f = (q < 2 ? v0 : v1) + 4 * i + 2 * (q & 1);
+                x[e] = __ffma2_rn(make_float2(__uint_as_float(f[0]), __uint_as_float(f[1])),
+                                  i ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y), nb[q]);
+            }
+        };
+        auto hide = [&](int c, float2 (&x)[8]) {   // tokens past a row's last visible one
+            const int t0 = tok0 + 16 * c + 2 * (lane & 3);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int left = flim[e & 3] - t0 - 8 * (e >> 2);
+                if (left < 0) x[e].x = -INFINITY;
+                if (left < 1) x[e].y = -INFINITY;
+            }
+        };
+        // P of the columns, as the fragments of a store of 16 packed columns (j = 0..3:
+        // eight tokens each; the pair j0, j0 + 1 here)
+        auto weigh = [&](int c, int j0, const float2 (&x)[8], uint32_t (&pk)[2][8]) {
+            const float4 w4 = *reinterpret_cast<const float4*>(nvs + 16 * c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = e >> 2, q = e & 3;
+                const float2 pe = make_float2(fast_exp2(x[e].x), fast_exp2(x[e].y));
+                sum[q] = __fadd2_rn(sum[q], pe);
+                const float2 w = __fmul2_rn(pe, i ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y));
+                pk[q >> 1][2 * (j0 + i) + (q & 1)] = pack_half2(w.x, w.y);
+            }
+        };
+        auto set_base = [&]() {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float b0 = fm[q] == -INFINITY ? 0.f : -fm[q];
+                nb[q] = make_float2(b0, b0);
+                sum[q] = make_float2(0.f, 0.f);
+            }
+        };
+        bool fresh_row = false;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) fresh_row = fresh_row || fm[q] == -INFINITY;
+        bool move = masked || __any_sync(0xffffffffu, fresh_row);
+#pragma unroll 1
+        for (;;) {
+            set_base();
+            if (move) {   // the rows' maxima, which may move their bases
+                float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t v0[8], v1[8];
+                    tmem_ld_frag_issue(t_s + 16 * c, v0);
+                    tmem_ld_frag_issue(t_hi + 16 * c, v1);
+                    tmem_ld_wait(v0, v1);
+                    float2 x[8];
+                    scores(c, v0, v1, x);
+                    if (masked) hide(c, x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mq[e & 3] = fmaxf(mq[e & 3], fmaxf(x[e].x, x[e].y));
+                }
+                float alpha[4];
+                bool grow = false;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {   // a row's maximum is spread over its four lanes
+                    float mx = fmaxf(mq[q], __shfl_xor_sync(0xffffffffu, mq[q], 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const bool fresh = fm[q] == -INFINITY;
+                    const bool up = mx > (fresh ? -INFINITY : slack);
+                    alpha[q] = up ? (fresh ? 0.f : fast_exp2(-mx)) : 1.f;
+                    fl[q] *= alpha[q];
+                    if (up) fm[q] = (fresh ? 0.f : fm[q]) + mx;
+                    grow = grow || up;
+                }
+                if (issued_o > 0 && __any_sync(0xffffffffu, grow)) {   // rescale O (P.V(n-1) is done)
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t o0[8], o1[8];
+                        tmem_ld_frag_issue(t_o + 16 * c, o0);
+                        tmem_ld_frag_issue(t_o + (16u << 16) + 16 * c, o1);
+                        tmem_ld_wait(o0, o1);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            o0[e] = __float_as_uint(__uint_as_float(o0[e]) * alpha[(e >> 1) & 1]);
+                            o1[e] = __float_as_uint(__uint_as_float(o1[e]) * alpha[2 + ((e >> 1) & 1)]);
+                        }
+                        tmem_st_frag256(t_o + 16 * c, o0);
+                        tmem_st_frag256(t_o + (16u << 16) + 16 * c, o1);
+                    }
+                    tmem_st_wait();
+                }
+                set_base();
+            }
+            if (masked) {
+                // 32 tokens a turn, P over columns of S that have been read
+#pragma unroll 1
+                for (int c = 0; c < 8; c += 2) {
+                    uint32_t pk[2][8];
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; ++h2) {
+                        uint32_t v0[8], v1[8];
+                        tmem_ld_frag_issue(t_s + 16 * (c + h2), v0);
+                        tmem_ld_frag_issue(t_hi + 16 * (c + h2), v1);
+                        tmem_ld_wait(v0, v1);
+                        float2 x[8];
+                        scores(c + h2, v0, v1, x);
+                        hide(c + h2, x);
+                        weigh(c + h2, 2 * h2, x, pk);
+                    }
+                    tmem_st_frag_issue(t_s + 8 * c, pk[0]);
+                    tmem_st_frag_issue(t_hi + 8 * c, pk[1]);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) fl[q] += sum[q].x + sum[q].y;
+                break;
+            }
+            uint32_t pk[4][2][8];
+            uint32_t v[2][2][8];   // 16 columns at a time, the next ones in flight
+            tmem_ld_frag_issue(t_s, v[0][0]);
+            tmem_ld_frag_issue(t_hi, v[0][1]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                tmem_ld_wait(v[c & 1][0], v[c & 1][1]);
+                if (c < 7) {
+                    tmem_ld_frag_issue(t_s + 16 * (c + 1), v[(c + 1) & 1][0]);
+                    tmem_ld_frag_issue(t_hi + 16 * (c + 1), v[(c + 1) & 1][1]);
+                }
+                float2 x[8];
+                scores(c, v[c & 1][0], v[c & 1][1], x);
+                weigh(c, 2 * (c & 1), x, pk[c >> 1]);
+            }
+            float s4[4], top = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                s4[q] = sum[q].x + sum[q].y;
+                top = fmaxf(top, s4[q]);
+            }
+            if (move || !__any_sync(0xffffffffu, top > most)) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) fl[q] += s4[q];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_st_frag_issue(t_s + 16 * c, pk[c][0]);
+                    tmem_st_frag_issue(t_hi + 16 * c, pk[c][1]);
+                }
+                break;
+            }
+            move = true;
+        }
+        tmem_st_wait();
+    };
+
     // Query tile 0's warps (0-3) dequantise K and its scales and issue S_0 and
     // P.V_0 (thread 0); query tile 1's warps (4-7) dequantise V and issue S_1,
     // P.V_1 and the copies (thread 128).  Per K/V tile n the tensor core takes
@@ -567,7 +771,8 @@ __global__ void __launch_bounds__(256, 1)
         }
         wait(bar_st, n & 1);
         tc_fence_after();
-        softmax(n);
+        if constexpr (PACKED) softmax_frag(n);
+        else softmax(n);
         tc_fence_before();
         if (named_bar_or(1 + tl, 128, stalled)) stalled = true;  // P_tl(n) is stored
         tc_fence_after();
@@ -603,6 +808,17 @@ __global__ void __launch_bounds__(256, 1)
     if (issued_o > 0 && !mbar_wait_bounded(bar_ot, (issued_o - 1) & 1)) ok = false;
     ok = __syncthreads_and(ok) != 0;  // one decision for the whole CTA
     tc_fence_after();
+    if constexpr (PACKED) {   // the sums, a row per thread from here on
+        float* rows = reinterpret_cast<float*>(smem + C::kColOff);   // (scales and norms are read; 256 floats)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float l = fl[q] + __shfl_xor_sync(0xffffffffu, fl[q], 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            if ((tid & 3) == 0) rows[128 * tl + 32 * (warp & 3) + ((tid & 31) >> 2) + 8 * q] = l;
+        }
+        __syncwarp();
+        l_sum = rows[tid];
+    }
     if (!ok) {
         if (tid == 0) atomicOr(p.status, kStatusPipelineStall);
     } else {

@@ -113,12 +113,6 @@ __device__ __forceinline__ void store_vt(const uint8_t* rec, uint8_t* sVt, const
     }
 }
 
-// Where token t's scale and norm lie: the four of lane t's columns (2t, 2t + 1,
-// 8 + 2t, 9 + 2t of 16) together.
-__device__ __forceinline__ int frag_place(int t) {
-    return (t & ~15) | ((t & 6) << 1) | ((t & 8) >> 2) | (t & 1);
-}
-
 __device__ __forceinline__ int tree_chunks(int L, int max_len) {
     const int n = min(L, max_len);
     return n > 0 ? (n + kTok - 1) / kTok : 0;

@@ -186,8 +186,10 @@ def test_prefill_rows_within_their_bounds(dev, case):
             S.assert_rows(got[cu[b]:cu[b + 1], h * G:(h + 1) * G], want, bound, f"b{b} h{h}")
 
 
-def test_prefill_equals_the_padded_call(dev):
-    # equal blocks: the same tiles, so the same bits
+def test_prefill_agrees_with_the_padded_call(dev):
+    """Equal blocks through both calls: each is within its row bounds of the exact
+    row (the padded call rounds a term of P.V twice, the packed one once), so their
+    distance is within the sum."""
     mode, B, Hq, Hkv, n, L, cap = "turbo3", 3, 28, 4, 150, 400, 400
     rec = H.random_cache(mode, B, Hkv, cap, 33)
     q = wl.random_fp16(34, (B, Hq, n, 128))
@@ -199,7 +201,13 @@ def test_prefill_equals_the_padded_call(dev):
     qp = qd.transpose(1, 2).reshape(B * n, Hq, 128).contiguous()
     b = torch.empty_like(qp)
     tqf.tq_prefill_attention_packed(ctx, cache, qp, b, i32(cum([n] * B), dev), L)
-    assert torch.equal(a.transpose(1, 2).reshape(B * n, Hq, 128), b)
+    got = b.view(B, n, Hq, 128).transpose(1, 2).float().cpu().numpy()
+    for s in range(B):
+        K, V = S.kv_of(mode, rec, s, 1, L)
+        rows = q[s, 7:14].reshape(-1, 128)
+        seen = np.arange(L)[None, :] <= np.tile(L - n + np.arange(n), 7)[:, None]
+        _, bound = S.attention_rows(rows, K, V, seen, 1 / math.sqrt(128))
+        S.assert_rows(got[s, 7:14], a[s, 7:14].float().cpu().numpy().astype(np.float64), 2 * bound, f"b{s}")
 
 
 def test_prefill_bad_bounds_short_contexts_and_overflowed_norms(dev):
@@ -238,7 +246,8 @@ def test_prefill_bad_bounds_short_contexts_and_overflowed_norms(dev):
 
 def test_packed_serving_round_in_a_graph(dev):
     """Append then prefill of packed prompts, eager and replayed from a graph,
-    against the same tokens through the padded calls of one sequence each."""
+    against the same tokens one sequence at a time (the same tiles, so the same
+    bits)."""
     mode, Hq, Hkv, cap, new = "turbo3", 28, 4, 800, [257, 31, 700, 1]
     B, cu = len(new), cum(new)
     k, v = wl.random_fp16(80, (cu[-1], Hkv, 128)), wl.random_fp16(81, (cu[-1], Hkv, 128))
@@ -266,10 +275,9 @@ def test_packed_serving_round_in_a_graph(dev):
     assert tqf.tq_get_status(ctx) == 0
     for b in range(B):
         one, c1 = tqf.Cache(tqf.MODES[mode], 1, Hkv, cap, dev), tqf.Context()
-        rows = slice(cu[b], cu[b + 1])
-        at = lambda x: x[rows].transpose(0, 1).unsqueeze(0).contiguous()  # noqa: E731
-        tqf.tq_encode_append_packed(c1, one, kd[rows].contiguous(), vd[rows].contiguous(), i32([0, new[b]], dev))
-        o1 = torch.empty_like(at(qd))
-        tqf.tq_prefill_attention(c1, one, at(qd), o1, new[b])
-        assert torch.equal(at(eager), o1), b
+        k1, v1, q1, e1 = (x[cu[b]:cu[b + 1]].contiguous() for x in (kd, vd, qd, eager))
+        tqf.tq_encode_append_packed(c1, one, k1, v1, i32([0, new[b]], dev))
+        o1 = torch.empty_like(q1)
+        tqf.tq_prefill_attention_packed(c1, one, q1, o1, i32([0, new[b]], dev), new[b])
+        assert torch.equal(e1, o1), b
         assert torch.equal(one.k_data[0, :, :new[b]], cache.k_data[b, :, :new[b]])
