@@ -56,16 +56,12 @@ struct PreCfg {
     // (fp16 K is read by the MMA straight from the slot: 1024-byte aligned)
     static constexpr int kSlotAlign = (KB == 0) ? 1024 : 128;
     static constexpr int kSlot = (kSlotRaw + kSlotAlign - 1) / kSlotAlign * kSlotAlign;
-    static constexpr int kVt2Off = kStgOff + 2 * kSlot;         // packed, fp16 K: a second V^T tile
-    static constexpr int kColOff = kVt2Off + (KB == 0 ? 32768 : 0);   // fp32 n_k * scale * log2(e) [128]
-    // packed: fp32 n_v [128] and the largest of each 32 [4]; fp16 K: per query tile
-    static constexpr int kNvOff = kColOff + kTile * 4;
-    static constexpr int kNvBytes = kTile * 4 + 16;
+    static constexpr int kColOff = kStgOff + 2 * kSlot;         // fp32 n_k * scale * log2(e) [128]
+    static constexpr int kNvOff = kColOff + kTile * 4;          // packed: fp32 n_v [128], the largest of 32 [4]
     // mbarriers stg[2], S[2], O[2] (one per query tile), V^T stored, K stored,
     // tile 1's softmax done; TMEM slot; last tile copied; the CTA's item (packed)
-    // (packed, fp16 K, of even and odd tiles: V^T stored, V^T read, slot read)
-    static constexpr int kBarOff = kNvOff + (KB == 0 ? 2 : 1) * kNvBytes;
-    static constexpr int kSmem = kBarOff + 88 + (KB == 0 ? 48 : 0);
+    static constexpr int kBarOff = kNvOff + kTile * 4 + 16;
+    static constexpr int kSmem = kBarOff + 88;
     static constexpr int kSmemAlloc = kSmem + 896;              // to a 1024-byte boundary from a 128-byte one
     static_assert(kSmemAlloc <= 232448, "227 KB per CTA");
     static constexpr uint32_t kIdesc = umma_idesc_f16_f32(128, 128);
@@ -254,16 +250,7 @@ __global__ void __launch_bounds__(256, 1)
         bulk_g2s(smem_u32(slot + C::kSK + C::kSKn + C::kSV), p.v_norm + row0 + tok0, nb, bar);
     };
 
-    // packed sequences with fp16 K: both query tiles dequantise half of V each
-    constexpr bool kHalves = PACKED && KB == 0;
-    const uint32_t bar_v2 = bar_stg + 88, bar_vf = bar_stg + 104, bar_sf = bar_stg + 120;
     if (tid == 0) {
-        if constexpr (kHalves)
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(bar_v2 + 8 * i, 256);   // every thread
-                mbar_init(bar_vf + 8 * i, 2);     // both P.V
-                mbar_init(bar_sf + 8 * i, 2);     // both S
-            }
         for (int i = 0; i < 6; ++i) mbar_init(bar_stg + 8 * i, 1);  // stg[2], S[2], O[2]
         mbar_init(bar_v, 128);  // the V dequant's threads
         mbar_init(bar_kr, 1);
@@ -381,7 +368,7 @@ __global__ void __launch_bounds__(256, 1)
         }
         if constexpr (PACKED) {
             const float nv = in ? __half2float(reinterpret_cast<const __half*>(slot + C::kSK + C::kSKn + C::kSV)[r]) : 0.f;
-            float* nvs = reinterpret_cast<float*>(smem + C::kNvOff + (kHalves ? tl * C::kNvBytes : 0));
+            float* nvs = reinterpret_cast<float*>(smem + C::kNvOff);
             nvs[frag_place(r)] = fminf(nv, 65504.f);
             // (non-negative floats order like their bits)
             const uint32_t top = __reduce_max_sync(0xffffffffu, nv < 65536.f ? __float_as_uint(nv) : 0u);
@@ -403,12 +390,12 @@ __global__ void __launch_bounds__(256, 1)
         umma_commit(bar_s + 8 * t2);
     };
     // O_t += P_t(n) . V(n), P from tensor memory over S_t
-    auto issue_pv = [&](int n, int t2, const uint8_t* vt) {
+    auto issue_pv = [&](int n, int t2) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
             const uint32_t koff = (kk >> 2) * 16384 + (kk & 3) * 32;
             umma_f16_ts(tmem + 256 * t2 + 128, tmem + 256 * t2 + 8 * kk,
-                        umma_desc_sw128(smem_u32(vt) + koff), C::kIdesc, (n > 0 || kk > 0) ? 1u : 0u);
+                        umma_desc_sw128(smem_u32(sVt) + koff), C::kIdesc, (n > 0 || kk > 0) ? 1u : 0u);
         }
         umma_commit(bar_o + 8 * t2);
     };
@@ -419,7 +406,7 @@ __global__ void __launch_bounds__(256, 1)
     // pi(d) = d ^ 2(d >> 5), which puts the 8 rows of each stored 8x8 matrix in
     // 8 different 16-byte bank groups (the epilogue reads O's columns back
     // through the same pi)
-    auto v_dequant = [&](int n, int vw, uint8_t* vt_dst) {
+    auto v_dequant = [&](int n, int vw) {
         const Tables vt{p.vtab[0], p.vtab[1], p.vtab[2], p.vtab[3]};
         const uint8_t* slot = smem + C::kStgOff + (n & 1) * C::kSlot;
         [[maybe_unused]] const int tok0 = n * C::kTile;
@@ -455,7 +442,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int par = 0; par < 2; ++par) {
             const int row = 32 * (sc >> 1) + 2 * ((((par << 1) | (sj >> 1)) ^ (sc >> 1)) & 3) + (sc & 1);
-            vaddr[par] = smem_u32(vt_dst) + (vw >> 2) * 16384 + row * 128 + ((tokc ^ (row & 7)) << 4);
+            vaddr[par] = smem_u32(sVt) + (vw >> 2) * 16384 + row * 128 + ((tokc ^ (row & 7)) << 4);
         }
 #pragma unroll
         for (int k2 = 0; k2 < 8; ++k2)
@@ -566,9 +553,8 @@ __global__ void __launch_bounds__(256, 1)
     auto softmax_frag = [&](int n) {
         const int lane = tid & 31, tok0 = n * C::kTile;
         const float* col = colK + 4 * (lane & 3);
-        const uint8_t* nv_base = smem + C::kNvOff + (kHalves ? tl * C::kNvBytes : 0);
-        const float* nvs = reinterpret_cast<const float*>(nv_base) + 4 * (lane & 3);
-        const float4 nm = *reinterpret_cast<const float4*>(nv_base + C::kTile * 4);
+        const float* nvs = reinterpret_cast<const float*>(smem + C::kNvOff) + 4 * (lane & 3);
+        const float4 nm = *reinterpret_cast<const float4*>(smem + C::kNvOff + C::kTile * 4);
         // p n_v stays below 2^15.99
         const float slack =
             fmaxf(0.f, fminf(10.f, 15.99f - __log2f(fmaxf(fmaxf(nm.x, nm.y), fmaxf(nm.z, nm.w)))));
@@ -743,57 +729,6 @@ __global__ void __launch_bounds__(256, 1)
     // is past its reads of the scales).  No thread leaves the loop early, so
     // every named barrier is met; after a wait times out the thread's later
     // waits return at once and it issues nothing more.
-    if constexpr (kHalves) {
-        // Packed, fp16 K (nothing to dequantise for S): each query tile's warps issue
-        // their S(n) as soon as the tile is there, dequantise half of V(n)^T under it
-        // into one of two tiles, take their softmax and issue their P.V.  A group
-        // waits for the other one only where V^T is whole, and where a tile or slot
-        // that both read is filled again (barriers that both groups' products
-        // commit to).
-        for (int n = 0; n < ntiles; ++n) {
-            const int u = n & 1;
-            uint8_t* vt = u ? smem + C::kVt2Off : sVt;
-            wait(bar_stg + 8 * u, (n >> 1) & 1);
-            if (n > 0) wait(bar_ot, (n - 1) & 1);   // P and O of this tile's last product are free
-            if (r == 0) {
-                tc_fence_after();
-                if (!stalled) {
-                    issue_s(n, tl);
-                    umma_commit(bar_sf + 8 * u);
-                }
-            }
-            __syncwarp();
-            k_scales(n);   // (the V norms, for this group)
-            if (n >= 2) wait(bar_vf + 8 * u, ((n >> 1) - 1) & 1);
-            v_dequant(n, 4 * tl + (warp & 3), vt);
-            fence_proxy_async();
-            mbar_arrive(bar_v2 + 8 * u);
-            named_bar_sync(1 + tl, 128);   // the norms are stored
-            wait(bar_st, u);
-            tc_fence_after();
-            softmax_frag(n);
-            tc_fence_before();
-            if (named_bar_or(1 + tl, 128, stalled)) stalled = true;   // P_tl(n) is stored, the norms are read
-            tc_fence_after();
-            if (r == 0) {
-                wait(bar_v2 + 8 * u, (n >> 1) & 1);
-                tc_fence_after();
-                if (!stalled) {
-                    issue_pv(n, tl, vt);
-                    umma_commit(bar_vf + 8 * u);
-                }
-                if (tl == 1 && n + 2 < ntiles) {
-                    wait(bar_sf + 8 * u, (n >> 1) & 1);   // both S(n) have read K (and V(n)^T is whole)
-                    if (!stalled) {
-                        fence_proxy_async();
-                        issue(n + 2);
-                        *last_issued = n + 2;
-                    }
-                }
-            }
-            ++issued_o;
-        }
-    } else {
     if (tl == 0 && ntiles > 0) {
         wait(bar_stg, 0);
         k_dequant(0);
@@ -820,8 +755,8 @@ __global__ void __launch_bounds__(256, 1)
                 wait(bar_o, (n - 1) & 1);
                 wait(bar_o + 8, (n - 1) & 1);
             }
-            v_dequant(n, warp - 4, sVt);
-            v_dequant(n, warp, sVt);
+            v_dequant(n, warp - 4);
+            v_dequant(n, warp);
             fence_proxy_async();
             mbar_arrive(bar_v);
             if (warp == 4) {
@@ -845,7 +780,7 @@ __global__ void __launch_bounds__(256, 1)
             if (r == 0) {
                 wait(bar_v, n & 1);  // V(n)^T is stored
                 tc_fence_after();
-                if (!stalled) issue_pv(n, 0, sVt);
+                if (!stalled) issue_pv(n, 0);
             }
             if (n + 1 < ntiles) {  // K(n+1), under tile 1's softmax(n)
                 wait(bar_stg + 8 * ((n + 1) & 1), ((n + 1) >> 1) & 1);
@@ -858,7 +793,7 @@ __global__ void __launch_bounds__(256, 1)
             // P.V_1(n) first: S_0(n+1) queues behind it on the tensor core
             mbar_arrive(bar_sm1);   // tile 1's softmax(n) is past its reads of the scales
             tc_fence_after();
-            if (!stalled) issue_pv(n, 1, sVt);
+            if (!stalled) issue_pv(n, 1);
             wait(bar_s, n & 1);     // S_0(n) is done (fp16 K reads it from the slot)
             if (!stalled && n + 2 < ntiles) {  // tile n's staging slot is consumed
                 issue(n + 2);
@@ -866,7 +801,6 @@ __global__ void __launch_bounds__(256, 1)
             }
         }
         ++issued_o;
-    }
     }
 
     // ---- epilogue: O / l, v_rescale, inverse rotation, fp16 ----
