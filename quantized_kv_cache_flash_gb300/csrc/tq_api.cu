@@ -763,7 +763,8 @@ int run_prefill(tq_ctx* ctx, int kb, int vb, const tq::PrefillParams& p, cudaStr
     int r = timing_events(ctx, &e0, &e1);
     if (r != TQ_OK) return r;
     if (e0) cudaEventRecord(e0, s);
-    r = tq::launch_prefill(kb, vb, p, kb == 16 ? &ctx->kmap : &dummy, s);
+    const auto launch = p.cu != nullptr ? tq::launch_packed_prefill : tq::launch_prefill;
+    r = launch(kb, vb, p, kb == 16 ? &ctx->kmap : &dummy, s);
     if (e1) cudaEventRecord(e1, s);
     return r == 0 ? TQ_OK : TQ_ERR_CUDA;
 }
@@ -883,6 +884,8 @@ int tq_prefill_attention_packed(tq_ctx** pctx, const tq_cache* c, const void* q,
     const long long slots = total / span + std::min(total, c->batch);
     if (slots * c->num_kv_heads > 0x7fffffffll) return TQ_ERR_UNSUPPORTED;
     p.slots = int(slots);
+    p.span = int32_t(span);
+    p.span_inv = uint32_t(((1ull << 32) + span - 1) / span);
     return run_prefill(ctx, kb, vb, p, static_cast<cudaStream_t>(stream));
 }
 

@@ -106,11 +106,13 @@ struct PrefillParams {
     int32_t mtiles;           // tiles per kv head
     float scale_log2e, v_rescale;
     uint32_t ktab[4], vtab[4], signs[4];
-    // packed sequences (cu != null): q and out are [total, Hq, 128], sequence
+    // packed sequences (tq_packed_prefill.cu; cu != null): q and out are [total, Hq, 128], sequence
     // b's rows cu[b] .. cu[b + 1] - 1 (tq and mtiles are not used)
     const int32_t* cu;        // [B + 1]
     int32_t total;
     int32_t slots;            // query tile pairs of all sequences, at most
+    int32_t span;             // positions per pair
+    uint32_t span_inv;        // 2^32 / span, rounded up
 };
 
 // Tree attention on the tensor cores (tq_tree.cu): units are (batch, kv head,
@@ -201,7 +203,8 @@ int launch_encode_packed(int kbits, int vbits, const EncodeParams& p, const CUte
 // res: the variant with the centroid residual product.
 int decode_ctas_per_sm(int kbits, int vbits, int group_rows, bool table, bool res);
 int launch_prefill(int kbits, int vbits, const PrefillParams& p, const CUtensorMap* kmap,
-                   cudaStream_t stream);   // packed sequences where p.cu is set
+                   cudaStream_t stream);
+int launch_packed_prefill(int kbits, int vbits, const PrefillParams& p, const CUtensorMap* kmap, cudaStream_t stream);
 int launch_tree(int kbits, int vbits, const TreeParams& p, const CUtensorMap* kmap, cudaStream_t stream,
                 cudaEvent_t ev0, cudaEvent_t ev1);
 int launch_compact(const CompactParams& p, cudaStream_t stream);

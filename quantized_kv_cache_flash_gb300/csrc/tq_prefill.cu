@@ -57,98 +57,15 @@ struct PreCfg {
     static constexpr int kSlotAlign = (KB == 0) ? 1024 : 128;
     static constexpr int kSlot = (kSlotRaw + kSlotAlign - 1) / kSlotAlign * kSlotAlign;
     static constexpr int kColOff = kStgOff + 2 * kSlot;         // fp32 n_k * scale * log2(e) [128]
-    static constexpr int kNvOff = kColOff + kTile * 4;          // packed: fp32 n_v [128], the largest of 32 [4]
     // mbarriers stg[2], S[2], O[2] (one per query tile), V^T stored, K stored,
-    // tile 1's softmax done; TMEM slot; last tile copied; the CTA's item (packed)
-    static constexpr int kBarOff = kNvOff + kTile * 4 + 16;
-    static constexpr int kSmem = kBarOff + 88;
-    static constexpr int kSmemAlloc = kSmem + 896;              // to a 1024-byte boundary from a 128-byte one
-    static_assert(kSmemAlloc <= 232448, "227 KB per CTA");
+    // tile 1's softmax done; TMEM slot; last tile copied
+    static constexpr int kBarOff = kColOff + kTile * 4;
+    static constexpr int kSmem = kBarOff + 80;
+    static constexpr int kSmemAlloc = kSmem + 1024;             // base alignment slack
     static constexpr uint32_t kIdesc = umma_idesc_f16_f32(128, 128);
 };
 
-// Packed sequences: which query tile pair a CTA takes.  All pairs of all
-// sequences are ranked by the K/V tiles they read, most first (the grid then
-// ends on the shortest ones), and rank k of every KV head goes to the CTAs
-// k hkv .. k hkv + hkv - 1, so CTAs that start together read different KV
-// heads of the same tokens.  A pair's tile count grows with its place in the
-// sequence, so the pairs of a sequence that read more than c tiles are its last
-// ones, and their number is one division; the smallest c that leaves at most k
-// pairs above it is found by bisection, one warp adding the sequences up.
-struct PackedSeq {
-    int n, ctx, lim;   // query rows, tokens before them, tokens read at most
-};
-
-__device__ __forceinline__ PackedSeq packed_seq(const PrefillParams& p, int b) {
-    PackedSeq s{0, 0, 0};
-    if (b >= p.batch) return s;
-    const int first = p.cu[b], next = p.cu[b + 1], L = p.lengths[b];
-    if (first < 0 || next < first || next > p.total) return s;   // no rows (flagged by the first CTA)
-    s.n = next - first;
-    s.ctx = L - s.n;
-    s.lim = min(L, p.max_len);
-    return s;
-}
-
-// Pairs (of `span` positions each) of a sequence that read more than c tiles.
-__device__ __forceinline__ int pairs_above(const PackedSeq& s, int c, int span) {
-    const int all = (s.n + span - 1) / span;
-    if (c < 0) return all;
-    // pair q reads past tile c where its last row does: its last token, the
-    // smaller of ctx + min(n, (q + 1) span) - 1 and lim - 1, is at 128 c or after
-    const int need = 128 * c + 1 - s.ctx;   // positions up to that row
-    if (128 * c >= s.lim || need > s.n) return 0;
-    return all - (need <= span ? 0 : (need - 1) / span);
-}
-
-__device__ __forceinline__ int warp_sum(int v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-// (sequence, pair) of rank k, by one warp; b = -1 past the last one.
-__device__ __forceinline__ void packed_find(const PrefillParams& p, int k, int lane, int& b, int& pair) {
-    const int span = 2 * p.pos_per_tile;
-    const PackedSeq mine = packed_seq(p, lane);
-    auto above = [&](int c) {
-        int v = pairs_above(mine, c, span);
-        for (int bb = 32 + lane; bb < p.batch; bb += 32) v += pairs_above(packed_seq(p, bb), c, span);
-        return warp_sum(v);
-    };
-    b = -1;
-    pair = 0;
-    if (k >= above(-1)) return;
-    int lo = -1, hi = (p.max_len + 127) / 128;   // above(lo) > k >= above(hi) = 0
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (above(mid) > k) lo = mid;
-        else hi = mid;
-    }
-    // the pairs of hi tiles, sequence after sequence
-    int left = k - above(hi);
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const PackedSeq s = b0 == 0 ? mine : packed_seq(p, b0 + lane);
-        const int skip = pairs_above(s, hi, span), here = pairs_above(s, hi - 1, span) - skip;
-        int inc = here;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, inc > left);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            const int all = (s.n + span - 1) / span;
-            b = b0 + l;
-            pair = __shfl_sync(0xffffffffu, all - skip - here + (left - (inc - here)), l);
-            return;
-        }
-        left -= __shfl_sync(0xffffffffu, inc, 31);
-    }
-}
-
-template <int KB, int VB, bool PACKED>
+template <int KB, int VB>
 __global__ void __launch_bounds__(256, 1)
     tq_prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap kmap) {
     using C = PreCfg<KB, VB>;
@@ -160,58 +77,24 @@ __global__ void __launch_bounds__(256, 1)
     // hold the rows of the first tile, warps 4-7 those of the second
     const int tl = tid >> 7, r = tid & 127;
 
-    // this CTA's (batch, kv head, query tile pair), the sequence's query rows
-    // and query tiles and its row 0 in packed q and out
-    int b, h, pair, tqn, mtiles, qrow0 = 0;
-    if constexpr (PACKED) {
-        griddep_wait();
-        int* s_item = reinterpret_cast<int*>(smem + C::kBarOff + 80);
-        if (warp == 0) {
-            int fb, fp;
-            packed_find(p, static_cast<int>(blockIdx.x) / p.hkv, tid, fb, fp);
-            if (tid == 0) {
-                s_item[0] = fb;
-                s_item[1] = fp;
-            }
-        } else if (warp == 1 && blockIdx.x == 0) {
-            bool bad = false;
-            for (int bb = tid - 32; bb < p.batch; bb += 32)
-                bad = bad || p.cu[bb] < 0 || p.cu[bb + 1] < p.cu[bb] || p.cu[bb + 1] > p.total;
-            if (bad) atomicOr(p.status, kStatusBadIndex);
-        }
-        __syncthreads();
-        b = s_item[0];
-        pair = s_item[1];
-        if (b < 0) return;   // past the last pair (uniform over the CTA)
-        h = static_cast<int>(blockIdx.x) % p.hkv;
-        qrow0 = p.cu[b];
-        tqn = p.cu[b + 1] - qrow0;
-        mtiles = (tqn + p.pos_per_tile - 1) / p.pos_per_tile;
-    } else {
-        // heaviest (latest) query tiles first
-        mtiles = p.mtiles;
-        pair = (mtiles + 1) / 2 - 1 - static_cast<int>(blockIdx.x);
-        b = blockIdx.y / p.hkv;
-        h = blockIdx.y - b * p.hkv;
-        tqn = p.tq;
-        griddep_wait();  // cache, lengths and q come from earlier work on the stream
-    }
+    // heaviest (latest) query tiles first
+    const int npairs = (p.mtiles + 1) / 2;
+    const int pair = npairs - 1 - static_cast<int>(blockIdx.x);
     const int mt = 2 * pair + tl;
-    const int unit = b * p.hkv + h;
+    const int unit = blockIdx.y;  // b * hkv + h
+    const int b = unit / p.hkv, h = unit - b * p.hkv;
+    griddep_wait();  // cache, lengths and q come from earlier work on the stream
     const int L = p.lengths[b];
     const int t_lim = min(L, p.max_len);
     // row r of tile mt: query position j, head hl of the group
     const int jl = r / p.group, hl = r - jl * p.group;
     const int j = mt * p.pos_per_tile + jl;
-    const bool row_ok = mt < mtiles && jl < p.pos_per_tile && j < tqn;
-    const int lim = row_ok ? min(L - tqn + j, t_lim - 1) : -1;  // last visible token
+    const bool row_ok = mt < p.mtiles && jl < p.pos_per_tile && j < p.tq;
+    const int lim = row_ok ? min(L - p.tq + j, t_lim - 1) : -1;  // last visible token
     // this tile's rows see every token up to lim_lo; the CTA's tiles end at `last`
-    const int lim_lo = mt < mtiles ? min(L - tqn + mt * p.pos_per_tile, t_lim - 1) : -1;
-    const int j_hi = min(tqn - 1, (2 * pair + 2) * p.pos_per_tile - 1);
-    const int last = min(L - tqn + j_hi, t_lim - 1);
-    // this row of q and out
-    const size_t io = (PACKED ? (static_cast<size_t>(qrow0) + j) * p.hq + h * p.group + hl
-                              : (static_cast<size_t>(b) * p.hq + h * p.group + hl) * tqn + j) * kD;
+    const int lim_lo = mt < p.mtiles ? min(L - p.tq + mt * p.pos_per_tile, t_lim - 1) : -1;
+    const int j_hi = min(p.tq - 1, (2 * pair + 2) * p.pos_per_tile - 1);
+    const int last = min(L - p.tq + j_hi, t_lim - 1);
     const int ntiles = last >= 0 ? last / C::kTile + 1 : 0;
     const size_t row0 = static_cast<size_t>(unit) * p.cap;
 
@@ -269,7 +152,7 @@ __global__ void __launch_bounds__(256, 1)
     {
         float x[128];
         if (row_ok) {
-            const __half* qp = p.q + io;
+            const __half* qp = p.q + ((static_cast<size_t>(b) * p.hq + h * p.group + hl) * p.tq + j) * kD;
 #pragma unroll
             for (int k = 0; k < 128; k += 8) {
                 const uint4 w = *reinterpret_cast<const uint4*>(qp + k);
@@ -339,12 +222,8 @@ __global__ void __launch_bounds__(256, 1)
             const Tables kt{p.ktab[0], p.ktab[1], p.ktab[2], p.ktab[3]};
             const uint8_t* rec = smem + C::kStgOff + (n & 1) * C::kSlot + r * C::kRbK;
             uint8_t* sK = smem + C::kKOff;
-            // (packed: the quarters in an order that differs between lanes whose
-            // records start in the same banks)
-            const int turn = PACKED ? (KB == 4 ? r >> 1 : r >> 3) : 0;
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                const int quarter = (q + turn) & 3;
+            for (int quarter = 0; quarter < 4; ++quarter) {
                 uint32_t hh[16];
                 dequant_q32<KB>(rec + quarter * (C::kRbK / 4), kt, hh);
 #pragma unroll
@@ -356,23 +235,11 @@ __global__ void __launch_bounds__(256, 1)
         }
     };
     // colK of tile n (n_k * scale * log2 e per token, 0 past the end)
-    // (packed: in the order of the softmax's fragments, with the V norms, 0 past
-    // the end; one that overflowed counts as 65504, since 0 * inf would be NaN in the
-    // rows before its token, and not for the slack)
     auto k_scales = [&](int n) {
-        const uint8_t* slot = smem + C::kStgOff + (n & 1) * C::kSlot;
-        const bool in = n * C::kTile + r < t_lim;
         if constexpr (KB != 0) {
+            const uint8_t* slot = smem + C::kStgOff + (n & 1) * C::kSlot;
             const float nk = __half2float(reinterpret_cast<const __half*>(slot + C::kSK)[r]);
-            colK[PACKED ? frag_place(r) : r] = in ? nk * p.scale_log2e : 0.f;
-        }
-        if constexpr (PACKED) {
-            const float nv = in ? __half2float(reinterpret_cast<const __half*>(slot + C::kSK + C::kSKn + C::kSV)[r]) : 0.f;
-            float* nvs = reinterpret_cast<float*>(smem + C::kNvOff);
-            nvs[frag_place(r)] = fminf(nv, 65504.f);
-            // (non-negative floats order like their bits)
-            const uint32_t top = __reduce_max_sync(0xffffffffu, nv < 65536.f ? __float_as_uint(nv) : 0u);
-            if ((r & 31) == 0) reinterpret_cast<uint32_t*>(nvs + C::kTile)[r >> 5] = top;
+            colK[r] = n * C::kTile + r < t_lim ? nk * p.scale_log2e : 0.f;
         }
     };
     // S_t(n) = Q'_t . K(n)^T into tile t's S columns
@@ -409,29 +276,26 @@ __global__ void __launch_bounds__(256, 1)
     auto v_dequant = [&](int n, int vw) {
         const Tables vt{p.vtab[0], p.vtab[1], p.vtab[2], p.vtab[3]};
         const uint8_t* slot = smem + C::kStgOff + (n & 1) * C::kSlot;
-        [[maybe_unused]] const int tok0 = n * C::kTile;
+        const int tok0 = n * C::kTile;
         const int lane = tid & 31, g = lane >> 2, tq4 = lane & 3;
         const int ta = 16 * vw + g, tb = ta + 8;
         const uint8_t* vrec = slot + C::kSK + C::kSKn;
-        [[maybe_unused]] const __half* vnorm = reinterpret_cast<const __half*>(slot + C::kSK + C::kSKn + C::kSV);
+        const __half* vnorm = reinterpret_cast<const __half*>(slot + C::kSK + C::kSKn + C::kSV);
         // tokens past the end: stale records still decode to finite
         // centroids, and their norm (and weight) is 0
         uint32_t ha[16], hb[16];
         dequant_q32<VB>(vrec + ta * C::kRbV + tq4 * (C::kRbV / 4), vt, ha);
         dequant_q32<VB>(vrec + tb * C::kRbV + tq4 * (C::kRbV / 4), vt, hb);
         // n_v scales the stored values, so P itself goes to the MMA: 128 x
-        // 128 multiplies a tile instead of the 256 x 128 of scaling P.  (Packed: P
-        // takes the norm and V stays the centroids, exact, so a term is rounded once.)
-        if constexpr (!PACKED) {
-            const __half2 na = tok0 + ta < t_lim ? __half2half2(vnorm[ta]) : __float2half2_rn(0.f);
-            const __half2 nb = tok0 + tb < t_lim ? __half2half2(vnorm[tb]) : __float2half2_rn(0.f);
+        // 128 multiplies a tile instead of the 256 x 128 of scaling P
+        const __half2 na = tok0 + ta < t_lim ? __half2half2(vnorm[ta]) : __float2half2_rn(0.f);
+        const __half2 nb = tok0 + tb < t_lim ? __half2half2(vnorm[tb]) : __float2half2_rn(0.f);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&ha[k]), na);
-                const __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&hb[k]), nb);
-                ha[k] = *reinterpret_cast<const uint32_t*>(&a);
-                hb[k] = *reinterpret_cast<const uint32_t*>(&b);
-            }
+        for (int k = 0; k < 16; ++k) {
+            const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&ha[k]), na);
+            const __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&hb[k]), nb);
+            ha[k] = *reinterpret_cast<const uint32_t*>(&a);
+            hb[k] = *reinterpret_cast<const uint32_t*>(&b);
         }
         // stmatrix k2 stores dim pairs 2k2 (matrices 0, 1: tokens A, B) and
         // 2k2+1 (matrices 2, 3); lane 8j + c gives row c of matrix j: dim
@@ -531,194 +395,6 @@ __global__ void __launch_bounds__(256, 1)
         l_sum += st.x + st.y;
     };
 
-    // Packed: the same as MMA fragments.  Lane 4v + c of a warp has rows v + 8q (q =
-    // 0..3) of its 32 and columns 2c, 2c + 1 of every eight, so a thread reads a
-    // quarter of the tile's scales and norms.  A tile that every row sees takes one
-    // pass, P in registers until it is known that no score passes its row's base by
-    // more than the slack (which shows in the thread's sums); then, with the mask,
-    // and on a row's first tile, the rows' maxima are taken first.
-    float fm[4], fl[4];   // base (log2) and this thread's part of the sum
-    int flim[4];          // last visible token
-    if constexpr (PACKED) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int rq = 32 * (warp & 3) + ((tid & 31) >> 2) + 8 * q, jq = rq / p.group;
-            fm[q] = -INFINITY;
-            fl[q] = 0.f;
-            flim[q] = mt < mtiles && jq < p.pos_per_tile && mt * p.pos_per_tile + jq < tqn
-                          ? min(L - tqn + mt * p.pos_per_tile + jq, t_lim - 1)
-                          : -1;
-        }
-    }
-    auto softmax_frag = [&](int n) {
-        const int lane = tid & 31, tok0 = n * C::kTile;
-        const float* col = colK + 4 * (lane & 3);
-        const float* nvs = reinterpret_cast<const float*>(smem + C::kNvOff) + 4 * (lane & 3);
-        const float4 nm = *reinterpret_cast<const float4*>(smem + C::kNvOff + C::kTile * 4);
-        // p n_v stays below 2^15.99
-        const float slack =
-            fmaxf(0.f, fminf(10.f, 15.99f - __log2f(fmaxf(fmaxf(nm.x, nm.y), fmaxf(nm.z, nm.w)))));
-        const float most = fast_exp2(slack);
-        const bool masked = tok0 + C::kTile - 1 > lim_lo;
-        const uint32_t t_hi = t_s + (16u << 16);   // rows 16-31
-        float2 nb[4], sum[4];
-        auto scale4 = [&](int c) {
-            if constexpr (KB != 0) return *reinterpret_cast<const float4*>(col + 16 * c);
-            return make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e, p.scale_log2e);
-        };
-        // x of columns 16c .. 16c + 15 (x[4i + q]) from the S values of rows 0-15 and 16-31
-        auto scores = [&](int c, const uint32_t* v0, const uint32_t* v1, float2 (&x)[8]) {
-            const float4 s4 = scale4(c);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = e >> 2, q = e & 3;
-                const uint32_t* f = (q < 2 ? v0 : v1) + 4 * i + 2 * (q & 1);
-                x[e] = __ffma2_rn(make_float2(__uint_as_float(f[0]), __uint_as_float(f[1])),
-                                  i ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y), nb[q]);
-            }
-        };
-        auto hide = [&](int c, float2 (&x)[8]) {   // tokens past a row's last visible one
-            const int t0 = tok0 + 16 * c + 2 * (lane & 3);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int left = flim[e & 3] - t0 - 8 * (e >> 2);
-                if (left < 0) x[e].x = -INFINITY;
-                if (left < 1) x[e].y = -INFINITY;
-            }
-        };
-        // P of the columns, as the fragments of a store of 16 packed columns (j = 0..3:
-        // eight tokens each; the pair j0, j0 + 1 here)
-        auto weigh = [&](int c, int j0, const float2 (&x)[8], uint32_t (&pk)[2][8]) {
-            const float4 w4 = *reinterpret_cast<const float4*>(nvs + 16 * c);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = e >> 2, q = e & 3;
-                const float2 pe = make_float2(fast_exp2(x[e].x), fast_exp2(x[e].y));
-                sum[q] = __fadd2_rn(sum[q], pe);
-                const float2 w = __fmul2_rn(pe, i ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y));
-                pk[q >> 1][2 * (j0 + i) + (q & 1)] = pack_half2(w.x, w.y);
-            }
-        };
-        auto set_base = [&]() {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float b0 = fm[q] == -INFINITY ? 0.f : -fm[q];
-                nb[q] = make_float2(b0, b0);
-                sum[q] = make_float2(0.f, 0.f);
-            }
-        };
-        bool fresh_row = false;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) fresh_row = fresh_row || fm[q] == -INFINITY;
-        bool move = masked || __any_sync(0xffffffffu, fresh_row);
-#pragma unroll 1
-        for (;;) {
-            set_base();
-            if (move) {   // the rows' maxima, which may move their bases
-                float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t v0[8], v1[8];
-                    tmem_ld_frag_issue(t_s + 16 * c, v0);
-                    tmem_ld_frag_issue(t_hi + 16 * c, v1);
-                    tmem_ld_wait(v0, v1);
-                    float2 x[8];
-                    scores(c, v0, v1, x);
-                    if (masked) hide(c, x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) mq[e & 3] = fmaxf(mq[e & 3], fmaxf(x[e].x, x[e].y));
-                }
-                float alpha[4];
-                bool grow = false;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {   // a row's maximum is spread over its four lanes
-                    float mx = fmaxf(mq[q], __shfl_xor_sync(0xffffffffu, mq[q], 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const bool fresh = fm[q] == -INFINITY;
-                    const bool up = mx > (fresh ? -INFINITY : slack);
-                    alpha[q] = up ? (fresh ? 0.f : fast_exp2(-mx)) : 1.f;
-                    fl[q] *= alpha[q];
-                    if (up) fm[q] = (fresh ? 0.f : fm[q]) + mx;
-                    grow = grow || up;
-                }
-                if (issued_o > 0 && __any_sync(0xffffffffu, grow)) {   // rescale O (P.V(n-1) is done)
-#pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        uint32_t o0[8], o1[8];
-                        tmem_ld_frag_issue(t_o + 16 * c, o0);
-                        tmem_ld_frag_issue(t_o + (16u << 16) + 16 * c, o1);
-                        tmem_ld_wait(o0, o1);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            o0[e] = __float_as_uint(__uint_as_float(o0[e]) * alpha[(e >> 1) & 1]);
-                            o1[e] = __float_as_uint(__uint_as_float(o1[e]) * alpha[2 + ((e >> 1) & 1)]);
-                        }
-                        tmem_st_frag256(t_o + 16 * c, o0);
-                        tmem_st_frag256(t_o + (16u << 16) + 16 * c, o1);
-                    }
-                    tmem_st_wait();
-                }
-                set_base();
-            }
-            if (masked) {
-                // 32 tokens a turn, P over columns of S that have been read
-#pragma unroll 1
-                for (int c = 0; c < 8; c += 2) {
-                    uint32_t pk[2][8];
-#pragma unroll
-                    for (int h2 = 0; h2 < 2; ++h2) {
-                        uint32_t v0[8], v1[8];
-                        tmem_ld_frag_issue(t_s + 16 * (c + h2), v0);
-                        tmem_ld_frag_issue(t_hi + 16 * (c + h2), v1);
-                        tmem_ld_wait(v0, v1);
-                        float2 x[8];
-                        scores(c + h2, v0, v1, x);
-                        hide(c + h2, x);
-                        weigh(c + h2, 2 * h2, x, pk);
-                    }
-                    tmem_st_frag_issue(t_s + 8 * c, pk[0]);
-                    tmem_st_frag_issue(t_hi + 8 * c, pk[1]);
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) fl[q] += sum[q].x + sum[q].y;
-                break;
-            }
-            uint32_t pk[4][2][8];
-            uint32_t v[2][2][8];   // 16 columns at a time, the next ones in flight
-            tmem_ld_frag_issue(t_s, v[0][0]);
-            tmem_ld_frag_issue(t_hi, v[0][1]);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                tmem_ld_wait(v[c & 1][0], v[c & 1][1]);
-                if (c < 7) {
-                    tmem_ld_frag_issue(t_s + 16 * (c + 1), v[(c + 1) & 1][0]);
-                    tmem_ld_frag_issue(t_hi + 16 * (c + 1), v[(c + 1) & 1][1]);
-                }
-                float2 x[8];
-                scores(c, v[c & 1][0], v[c & 1][1], x);
-                weigh(c, 2 * (c & 1), x, pk[c >> 1]);
-            }
-            float s4[4], top = 0.f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                s4[q] = sum[q].x + sum[q].y;
-                top = fmaxf(top, s4[q]);
-            }
-            if (move || !__any_sync(0xffffffffu, top > most)) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) fl[q] += s4[q];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_st_frag_issue(t_s + 16 * c, pk[c][0]);
-                    tmem_st_frag_issue(t_hi + 16 * c, pk[c][1]);
-                }
-                break;
-            }
-            move = true;
-        }
-        tmem_st_wait();
-    };
-
     // Query tile 0's warps (0-3) dequantise K and its scales and issue S_0 and
     // P.V_0 (thread 0); query tile 1's warps (4-7) dequantise V and issue S_1,
     // P.V_1 and the copies (thread 128).  Per K/V tile n the tensor core takes
@@ -771,8 +447,7 @@ __global__ void __launch_bounds__(256, 1)
         }
         wait(bar_st, n & 1);
         tc_fence_after();
-        if constexpr (PACKED) softmax_frag(n);
-        else softmax(n);
+        softmax(n);
         tc_fence_before();
         if (named_bar_or(1 + tl, 128, stalled)) stalled = true;  // P_tl(n) is stored
         tc_fence_after();
@@ -808,17 +483,6 @@ __global__ void __launch_bounds__(256, 1)
     if (issued_o > 0 && !mbar_wait_bounded(bar_ot, (issued_o - 1) & 1)) ok = false;
     ok = __syncthreads_and(ok) != 0;  // one decision for the whole CTA
     tc_fence_after();
-    if constexpr (PACKED) {   // the sums, a row per thread from here on
-        float* rows = reinterpret_cast<float*>(smem + C::kColOff);   // (scales and norms are read; 256 floats)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float l = fl[q] + __shfl_xor_sync(0xffffffffu, fl[q], 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            if ((tid & 3) == 0) rows[128 * tl + 32 * (warp & 3) + ((tid & 31) >> 2) + 8 * q] = l;
-        }
-        __syncwarp();
-        l_sum = rows[tid];
-    }
     if (!ok) {
         if (tid == 0) atomicOr(p.status, kStatusPipelineStall);
     } else {
@@ -849,7 +513,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int d = 0; d < 128; ++d) o[d] = od[d];
             wht128_thread(o);
-            __half* op = p.out + io;
+            __half* op = p.out + ((static_cast<size_t>(b) * p.hq + h * p.group + hl) * p.tq + j) * kD;
 #pragma unroll
             for (int k = 0; k < 128; k += 8) {
                 float y[8];
@@ -878,17 +542,10 @@ __global__ void __launch_bounds__(256, 1)
 template <int KB, int VB>
 static int launch_prefill_t(const PrefillParams& p, const CUtensorMap* kmap, cudaStream_t stream) {
     using C = PreCfg<KB, VB>;
-    if (p.cu != nullptr) {
-        static std::atomic<uint64_t> attr_done{0};
-        const cudaError_t e = set_smem_attr_once(tq_prefill_kernel<KB, VB, true>, C::kSmemAlloc, attr_done);
-        if (e != cudaSuccess) return e;
-        return launch_pdl(tq_prefill_kernel<KB, VB, true>, dim3(p.slots * p.hkv), dim3(256), C::kSmemAlloc, stream, p,
-                          *kmap);
-    }
     static std::atomic<uint64_t> attr_done{0};
-    const cudaError_t e = set_smem_attr_once(tq_prefill_kernel<KB, VB, false>, C::kSmemAlloc, attr_done);
+    const cudaError_t e = set_smem_attr_once(tq_prefill_kernel<KB, VB>, C::kSmemAlloc, attr_done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(tq_prefill_kernel<KB, VB, false>, dim3((p.mtiles + 1) / 2, p.batch * p.hkv), dim3(256),
+    return launch_pdl(tq_prefill_kernel<KB, VB>, dim3((p.mtiles + 1) / 2, p.batch * p.hkv), dim3(256),
                       C::kSmemAlloc, stream, p, *kmap);
 }
 

@@ -77,42 +77,6 @@ constexpr int kTreeThreads = 640;
 constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsDequant = 72, kRegsIssue = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsDequant + kRegsIssue <= 5 * kRegsLaunch, "within the launch's registers");
 
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-
-// V^T of 128 tokens from their records, by four warps (w = 0..3): lane 4v + t
-// dequantises quarter t of tokens 16 vw + v and + 8, stored transposed in rows
-// pi(d) = d ^ 2(d >> 5), whose 8 rows per stored matrix lie in different banks.
-template <int VB>
-__device__ __forceinline__ void store_vt(const uint8_t* rec, uint8_t* sVt, const Tables& vt, int w, int lane) {
-    constexpr int rb = VB * 16;
-    const int sj = lane >> 3, sc = lane & 7;
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-        const int vw = w + 4 * i;
-        const int ta = 16 * vw + (lane >> 2);
-        uint32_t ha[16], hb[16];
-        dequant_q32<VB>(rec + ta * rb + (lane & 3) * (rb / 4), vt, ha);
-        dequant_q32<VB>(rec + (ta + 8) * rb + (lane & 3) * (rb / 4), vt, hb);
-        const int tokc = 2 * (vw & 3) + (sj & 1);
-        uint32_t va[2];
-#pragma unroll
-        for (int par = 0; par < 2; ++par) {
-            const int row = 32 * (sc >> 1) + 2 * ((((par << 1) | (sj >> 1)) ^ (sc >> 1)) & 3) + (sc & 1);
-            va[par] = smem_u32(sVt) + (vw >> 2) * 16384 + row * 128 + ((tokc ^ (row & 7)) << 4);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            stsm_x4_trans(va[k & 1] + 1024 * (k >> 1), ha[2 * k], hb[2 * k], ha[2 * k + 1], hb[2 * k + 1]);
-    }
-}
-
 __device__ __forceinline__ int tree_chunks(int L, int max_len) {
     const int n = min(L, max_len);
     return n > 0 ? (n + kTok - 1) / kTok : 0;
