@@ -52,10 +52,11 @@ struct PackCfg {
     static constexpr int kColOff = kStgOff + 2 * kSlot;         // fp32 n_k * scale * log2(e) [128]
     static constexpr int kNvOff = kColOff + kTile * 4;          // fp32 n_v [128], fp16 largest n_v of 32 [4]
     // mbarriers: records copied [2], slot free [2], S done [2], P.V done [2], P stored
-    // [2], K stored, scales stored, V stored, Q' stored; the TMEM slot
+    // [2], K stored (dims 0-63, 64-127), scales stored, V stored, Q' stored, K's dims
+    // 0-63 read; the TMEM slot
     static constexpr int kBarOff = kNvOff + kTile * 4 + 8;
-    static constexpr int kSmem = kBarOff + 14 * 8 + 4;
-    static constexpr int kSmemAlloc = kSmem + 900;              // to a 1024-byte boundary from a 128-byte one
+    static constexpr int kSmem = kBarOff + 16 * 8 + 4;
+    static constexpr int kSmemAlloc = kSmem + 768;              // to a 1024-byte boundary from a 256-byte one
     static_assert(kSmemAlloc <= 232448, "227 KB per CTA");
     static constexpr uint32_t kIdesc = umma_idesc_f16_f32(128, 128);
 };
@@ -74,7 +75,7 @@ static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "within the 
 // sequences up.
 struct PackedSeq {
     int n, ctx, lim;   // query rows, tokens before them, tokens read at most
-    int all;           // pairs
+    int first, all;    // first row, pairs
 };
 
 // x / p.span for 0 <= x: the product with 2^32 / span rounded up is at most one off
@@ -84,10 +85,11 @@ __device__ __forceinline__ int over_span(const PrefillParams& p, int x) {
 }
 
 __device__ __forceinline__ PackedSeq packed_seq(const PrefillParams& p, int b) {
-    PackedSeq s{0, 0, 0, 0};
+    PackedSeq s{0, 0, 0, 0, 0};
     if (b >= p.batch) return s;
     const int first = p.cu[b], next = p.cu[b + 1], L = p.lengths[b];
     if (first < 0 || next < first || next > p.total) return s;   // no rows (flagged by the first CTA)
+    s.first = first;
     s.n = next - first;
     s.ctx = L - s.n;
     s.lim = min(L, p.max_len);
@@ -104,16 +106,17 @@ __device__ __forceinline__ int pairs_above(const PrefillParams& p, const PackedS
     return s.all - (need <= p.span ? 0 : over_span(p, need - 1));
 }
 
-// (sequence, pair) of rank k, by one warp; b = -1 past the last one.
-__device__ __forceinline__ void packed_find(const PrefillParams& p, int k, int lane, int& b, int& pair) {
+// The item of rank k, by one warp: sequence (-1 past the last rank), pair, and the
+// sequence's first row, rows and length.
+__device__ __forceinline__ void packed_find(const PrefillParams& p, int k, int lane, int* item) {
     const PackedSeq mine = packed_seq(p, lane);
     auto total = [&](auto&& f) {
         int v = f(mine);
         for (int bb = 32 + lane; bb < p.batch; bb += 32) v += f(packed_seq(p, bb));
         return __reduce_add_sync(0xffffffffu, v);
     };
-    b = -1;
-    pair = 0;
+    if (lane == 0) item[0] = -1;
+    __syncwarp();
     if (k >= total([](const PackedSeq& s) { return s.all; })) return;
     int longest = max(mine.lim, 0);
     for (int bb = 32 + lane; bb < p.batch; bb += 32) longest = max(longest, packed_seq(p, bb).lim);
@@ -138,9 +141,13 @@ __device__ __forceinline__ void packed_find(const PrefillParams& p, int k, int l
         }
         const unsigned hit = __ballot_sync(0xffffffffu, inc > left);
         if (hit) {
-            const int l = __ffs(hit) - 1;
-            b = b0 + l;
-            pair = __shfl_sync(0xffffffffu, s.all - skip - here + (left - (inc - here)), l);
+            if (lane == __ffs(hit) - 1) {
+                item[0] = b0 + lane;
+                item[1] = s.all - skip - here + (left - (inc - here));
+                item[2] = s.first;
+                item[3] = s.n;
+                item[4] = s.ctx + s.n;
+            }
             return;
         }
         left -= __shfl_sync(0xffffffffu, inc, 31);
@@ -161,9 +168,9 @@ __global__ void __launch_bounds__(kPackThreads, 1)
     // n_k * scale * log2(e) per token (quantized K), in frag_place order
     float* colK = reinterpret_cast<float*>(smem + C::kColOff);
     const uint32_t bar_stg = smem_u32(smem + C::kBarOff), bar_free = bar_stg + 16, bar_s = bar_stg + 32,
-                   bar_o = bar_stg + 48, bar_p = bar_stg + 64, bar_k = bar_stg + 80, bar_sc = bar_stg + 88,
-                   bar_v = bar_stg + 96, bar_q = bar_stg + 104;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 112);
+                   bar_o = bar_stg + 48, bar_p = bar_stg + 64, bar_k = bar_stg + 80, bar_sc = bar_stg + 96,
+                   bar_v = bar_stg + 104, bar_q = bar_stg + 112, bar_kr = bar_stg + 120;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 128);
     int* s_item = reinterpret_cast<int*>(smem + C::kColOff);   // until the first scales
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -172,8 +179,9 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             mbar_init(bar_s + 8 * i, 1);
             mbar_init(bar_o + 8 * i, 1);
             mbar_init(bar_p + 8 * i, 128);
+            mbar_init(bar_k + 8 * i, 128);
         }
-        mbar_init(bar_k, 128);
+        mbar_init(bar_kr, 1);
         mbar_init(bar_sc, 128);
         mbar_init(bar_v, 128);
         mbar_init(bar_q, 256);
@@ -183,12 +191,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
     if (warp == 1) tmem_alloc(smem_u32(tslot), 512);
     griddep_wait();  // cache, lengths, bounds and q come from earlier work on the stream
     if (warp == 0) {
-        int fb, fp;
-        packed_find(p, static_cast<int>(blockIdx.x) / p.hkv, tid, fb, fp);
-        if (tid == 0) {
-            s_item[0] = fb;
-            s_item[1] = fp;
-        }
+        packed_find(p, static_cast<int>(blockIdx.x) / p.hkv, tid, s_item);
     } else if (warp == 2 && blockIdx.x == 0) {
         bool bad = false;
         for (int bb = tid - 64; bb < p.batch; bb += 32)
@@ -199,16 +202,15 @@ __global__ void __launch_bounds__(kPackThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    const int b = s_item[0], pair = s_item[1];
+    // sequence, query tile pair, the sequence's first row in q and out, rows, length
+    const int b = s_item[0], pair = s_item[1], qrow0 = s_item[2], tqn = s_item[3], L = s_item[4];
     __syncthreads();   // (read: the scales may be written)
     if (b < 0) {   // past the last pair (uniform over the CTA)
         if (warp == 1) tmem_dealloc(tmem, 512);
         return;
     }
     const int h = static_cast<int>(blockIdx.x) % p.hkv;
-    const int qrow0 = p.cu[b], tqn = p.cu[b + 1] - qrow0;   // the sequence's rows in q and out
     const int mtiles = (tqn + p.pos_per_tile - 1) / p.pos_per_tile;
-    const int L = p.lengths[b];
     const int t_lim = min(L, p.max_len);
     const int j_hi = min(tqn - 1, (2 * pair + 2) * p.pos_per_tile - 1);
     const int last = min(L - tqn + j_hi, t_lim - 1);   // the last token that a row of the CTA sees
@@ -547,42 +549,38 @@ __global__ void __launch_bounds__(kPackThreads, 1)
         regs_dec<kRegsOther>();
         // ---- dequantise: thread r of 128 ----
         const int r = tid - 256;
-        auto k_dequant = [&](int n) {
+        // K's dims 64 half .. 64 half + 63, one token a thread
+        [[maybe_unused]] auto k_dequant = [&](int n, int half) {
             if constexpr (KB != 0) {
-                // (tables from the parameters at each use: none held across the loop)
                 const Tables kt{p.ktab[0], p.ktab[1], p.ktab[2], p.ktab[3]};
                 const uint8_t* rec = smem + C::kStgOff + (n & 1) * C::kSlot + r * C::kRbK;
-                uint8_t* sK = smem + C::kKOff;
+                uint8_t* sK = smem + C::kKOff + half * 16384;
                 // the quarters in an order that differs between lanes whose records
                 // start in the same banks
                 const int turn = KB == 4 ? r >> 1 : r >> 3;
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    const int quarter = (q + turn) & 3;
+                for (int q = 0; q < 2; ++q) {
+                    const int side = (q + turn) & 1;
                     uint32_t hh[16];
-                    dequant_q32<KB>(rec + quarter * (C::kRbK / 4), kt, hh);
+                    dequant_q32<KB>(rec + (2 * half + side) * (C::kRbK / 4), kt, hh);
 #pragma unroll
                     for (int m = 0; m < 4; ++m)
-                        *reinterpret_cast<uint4*>(sK + sw128_offset(r, 32 * quarter + 8 * m)) =
+                        *reinterpret_cast<uint4*>(sK + sw128_offset(r, 32 * side + 8 * m)) =
                             make_uint4(hh[4 * m], hh[4 * m + 1], hh[4 * m + 2], hh[4 * m + 3]);
                 }
                 fence_proxy_async();
+                mbar_arrive(bar_k + 8 * half);
             }
         };
-        // colK of tile n (n_k * scale * log2 e per token, 0 past the end)
-        // (packed: in the order of the softmax's fragments, with the V norms, 0 past
-        // the end; one that overflowed counts as 65504, since 0 * inf would be NaN in the
-        // rows before its token, and not for the slack)
         for (int n = 0; n < ntiles; ++n) {
             const uint8_t* slot = smem + C::kStgOff + (n & 1) * C::kSlot;
             wait(bar_stg + 8 * (n & 1), (n >> 1) & 1);
             if constexpr (KB != 0) {
-                if (n > 0) {   // K(n - 1) is read
-                    wait(bar_s, (n - 1) & 1);
-                    wait(bar_s + 8, (n - 1) & 1);
-                }
-                k_dequant(n);
-                mbar_arrive(bar_k);
+                // each half of K once S_0(n - 1) and S_1(n - 1) have read the one before
+                if (n > 0) wait(bar_kr, (n - 1) & 1);
+                k_dequant(n, 0);
+                if (n > 0) wait(bar_s + 8, (n - 1) & 1);
+                k_dequant(n, 1);
             }
             if (n > 0) {   // the scales and norms of n - 1 are read
                 wait(bar_p, (n - 1) & 1);
@@ -622,34 +620,41 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             wait(bar_q, 0);
             for (int n = 0; n < ntiles && !stalled; ++n) {
                 if constexpr (KB == 0) wait(bar_stg + 8 * (n & 1), (n >> 1) & 1);
-                else wait(bar_k, n & 1);
                 const uint32_t kbase =
                     (KB == 0) ? smem_u32(smem + C::kStgOff + (n & 1) * C::kSlot) : smem_u32(smem + C::kKOff);
 #pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
                     if (n > 0) wait(bar_o + 8 * t, (n - 1) & 1);   // P.V_t(n - 1) has read the P there
-                    if (stalled) break;
-                    tc_fence_after();
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t koff = (kk >> 2) * 16384 + (kk & 3) * 32;
-                        umma_f16(tmem + 256 * t, umma_desc_sw128(smem_u32(sQ) + t * 32768 + koff),
-                                 umma_desc_sw128(kbase + koff), C::kIdesc, kk > 0 ? 1u : 0u);
-                        if constexpr (KB != 0)  // + q_lo . K^T
-                            umma_f16(tmem + 256 * t, umma_desc_sw128(smem_u32(smem + C::kQloOff) + t * 32768 + koff),
-                                     umma_desc_sw128(kbase + koff), C::kIdesc, 1u);
+                    for (int half = 0; half < 2; ++half) {
+                        if (KB != 0 && t == 0) wait(bar_k + 8 * half, n & 1);
+                        if (!stalled) {
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const uint32_t koff = half * 16384 + kk * 32;
+                                umma_f16(tmem + 256 * t, umma_desc_sw128(smem_u32(sQ) + t * 32768 + koff),
+                                         umma_desc_sw128(kbase + koff), C::kIdesc, half + kk > 0 ? 1u : 0u);
+                                if constexpr (KB != 0)  // + q_lo . K^T
+                                    umma_f16(tmem + 256 * t,
+                                             umma_desc_sw128(smem_u32(smem + C::kQloOff) + t * 32768 + koff),
+                                             umma_desc_sw128(kbase + koff), C::kIdesc, 1u);
+                            }
+                            if (KB != 0 && t == 1 && half == 0) umma_commit(bar_kr);
+                        }
                     }
+                    if (stalled) break;   // (the MMAs in flight are waited for below)
                     umma_commit(bar_s + 8 * t);
                     if constexpr (KB == 0) umma_commit(bar_free + 8 * (n & 1));
                     ++done;
                 }
             }
-            // (after a time-out: the MMAs in flight end before tensor memory is freed)
-            if (stalled)
-                for (int t = 0; t < 2; ++t) {
-                    const int k = (done + 1 - t) / 2;
-                    if (k > 0) (void)mbar_wait_bounded(bar_s + 8 * t, (k - 1) & 1);
-                }
+            // after a time-out: the MMAs in flight, half a tile's among them, end before
+            // tensor memory is freed (the commit of the S that comes next)
+            if (stalled) {
+                umma_commit(bar_s + 8 * (done & 1));
+                (void)mbar_wait_bounded(bar_s + 8 * (done & 1), (done >> 1) & 1);
+            }
         } else if (warp == 13 && one) {   // O_t += P_t(n) . V(n), P from tensor memory over S_t
             int done = 0;
             for (int n = 0; n < ntiles && !stalled; ++n) {
@@ -669,11 +674,10 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                     ++done;
                 }
             }
-            if (stalled)
-                for (int t = 0; t < 2; ++t) {
-                    const int k = (done + 1 - t) / 2;
-                    if (k > 0) (void)mbar_wait_bounded(bar_o + 8 * t, (k - 1) & 1);
-                }
+            if (stalled) {
+                umma_commit(bar_o + 8 * (done & 1));
+                (void)mbar_wait_bounded(bar_o + 8 * (done & 1), (done >> 1) & 1);
+            }
         } else if (warp == 14 && one) {   // tile n into staging slot n & 1
             auto issue = [&](int n) {
                 const int tok0 = n * C::kTile;
