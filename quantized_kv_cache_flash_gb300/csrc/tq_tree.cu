@@ -63,7 +63,7 @@ struct TreeCfg {
     // V stored, P stored, S done, P.V done; Q' stored, all MMAs done [2] (after
     // a time-out)
     static constexpr int kBarOff = kNmOff + 32;
-    static constexpr int kBars = 18;
+    static constexpr int kBars = 20;
     static constexpr int kSmem = kBarOff + 8 * kBars + 8;             // and the TMEM slot
     static constexpr int kSmemAlloc = kSmem + 256;   // to a 1024-byte boundary: the base is one, but for 256 bytes at most
     static_assert(kSmemAlloc <= 232448, "227 KB per CTA");
@@ -224,7 +224,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
     const uint32_t bars = smem_u32(smem + C::kBarOff);
     const uint32_t bar_k = bars, bar_v = bars + 16, bar_kr = bars + 32, bar_vr = bars + 48, bar_p = bars + 64,
-                   bar_s = bars + 80, bar_o = bars + 96, bar_q = bars + 112, bar_x = bars + 120;
+                   bar_s = bars + 80, bar_o = bars + 96, bar_q = bars + 112, bar_x = bars + 120,
+                   bar_n = bars + 136;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * C::kBars);
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) mbar_init(bar_k + 8 * i, 1);      // K copied, V copied
@@ -232,8 +233,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int i = 0; i < 2; ++i) mbar_init(bar_p + 8 * i, 256);    // P stored
         for (int i = 0; i < 4; ++i) mbar_init(bar_s + 8 * i, 1);      // S done, P.V done
         mbar_init(bar_q, 256);                                        // Q' stored
-        mbar_init(bar_x, 1);
-        mbar_init(bar_x + 8, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_x + 8 * i, 1);
+            mbar_init(bar_n + 8 * i, 128);                            // scales and norms stored
+        }
         fence_barrier_init();
     }
     if (warp == 0) tmem_alloc(smem_u32(tslot), 512);
@@ -400,62 +403,71 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         bool bad = false;
         while (pos < hi && !bad) {
             const Segment s = segment();
+            // the tile's scales and norms, a token per thread: by the warps that have less
+            // to do (raw halves, a tile ahead, converted where they are used)
+            __half nk = __ushort_as_half(0), nv = nk;
+            auto load_norms = [&](int n) {   // (0 past the end)
+                const int t = (s.k0 + n) * kTok + r;
+                const bool in = n < s.ntiles && t < s.t_lim;
+                if constexpr (KB != 0) nk = in ? p.k_norm[s.row0 + t] : __ushort_as_half(0);
+                nv = in ? p.v_norm[s.row0 + t] : __ushort_as_half(0);
+            };
+            auto store_norms = [&](int n) {
+                const int t = tbase + n, u = t & 1;
+                if (t >= 2) wait(bar_p + 8 * u, ((t >> 1) - 1) & 1);   // softmax(t - 2) has read its own
+                if constexpr (KB != 0)
+                    (reinterpret_cast<float*>(smem + C::kColOff) + u * kTok)[frag_place(r)] =
+                        __half2float(nk) * p.scale_log2e;
+                const float x = __half2float(nv);
+                // (an overflowed norm counts as 65504: 0 * inf would be NaN in the
+                // rows that do not see the token; it does not count for the
+                // slack, so the rows that do may overflow)
+                (reinterpret_cast<float*>(smem + C::kNvOff) + u * kTok)[frag_place(r)] = fminf(x, 65504.f);
+                // (non-negative floats order like their bits)
+                const uint32_t nmax = __reduce_max_sync(0xffffffffu, x < 65536.f ? __float_as_uint(x) : 0u);
+                if (lane == 0) (reinterpret_cast<uint32_t*>(smem + C::kNmOff) + 4 * u)[warp & 3] = nmax;
+                mbar_arrive(bar_n + 8 * u);
+                load_norms(n + 1);
+            };
             if (wg == 2) {
-                // (raw halves, converted where they are used: a tile later)
-                auto norm = [&](const __half* norms, int n) {   // (0 past the end)
-                    const int t = (s.k0 + n) * kTok + r;
-                    return n < s.ntiles && t < s.t_lim ? norms[s.row0 + t] : __ushort_as_half(0);
-                };
-                __half nk = __ushort_as_half(0), nk1 = nk;
-                if constexpr (KB != 0) nk = norm(p.k_norm, 0);
-                __half nvh = norm(p.v_norm, 0);
+                if constexpr (KB == 0) load_norms(0);
 #pragma unroll 1
                 for (int n = 0; n < s.ntiles; ++n) {
-                    const int t = tbase + n, u = t & 1;
-                    if constexpr (KB != 0) nk1 = norm(p.k_norm, n + 1);
-                    const __half nv1 = norm(p.v_norm, n + 1);
-                    if constexpr (KB != 0) {
-                        wait(bar_k + 8 * u, (t >> 1) & 1);
-                        if (t >= 2) wait(bar_s + 8 * u, ((t >> 1) - 1) & 1);   // S(t - 2) has read its K tile
-                        // a token per thread; the quarters are taken in an order that
-                        // differs between lanes whose records start in the same banks
-                        const Tables kt{p.ktab[0], p.ktab[1], p.ktab[2], p.ktab[3]};
-                        const uint8_t* rec = smem + C::kSKOff + u * C::kSK + r * C::kRbK;
-                        uint8_t* sK = smem + C::kKOff + u * 32768;
-                        const int turn = KB == 4 ? r >> 1 : r >> 3;
-#pragma unroll 2
-                        for (int q = 0; q < 4; ++q) {
-                            const int quarter = (q + turn) & 3;
-                            uint32_t hh[16];
-                            dequant_q32<(KB == 0 ? 4 : KB)>(rec + quarter * (C::kRbK / 4), kt, hh);
-#pragma unroll
-                            for (int m = 0; m < 4; ++m)
-                                *reinterpret_cast<uint4*>(sK + sw128_offset(r, 32 * quarter + 8 * m)) =
-                                    make_uint4(hh[4 * m], hh[4 * m + 1], hh[4 * m + 2], hh[4 * m + 3]);
-                        }
-                        fence_proxy_async();
+                    if constexpr (KB == 0) {
+                        store_norms(n);
+                        continue;
                     }
-                    if (t >= 2) wait(bar_p + 8 * u, ((t >> 1) - 1) & 1);   // softmax(t - 2) has read its scales and norms
-                    if constexpr (KB != 0)
-                        (reinterpret_cast<float*>(smem + C::kColOff) + u * kTok)[frag_place(r)] =
-                            __half2float(nk) * p.scale_log2e;
-                    const float nv = __half2float(nvh);
-                    // (an overflowed norm counts as 65504: 0 * inf would be NaN in the
-                    // rows that do not see the token; it does not count for the
-                    // slack, so the rows that do may overflow)
-                    (reinterpret_cast<float*>(smem + C::kNvOff) + u * kTok)[frag_place(r)] = fminf(nv, 65504.f);
-                    // (non-negative floats order like their bits)
-                    const uint32_t nmax = __reduce_max_sync(0xffffffffu, nv < 65536.f ? __float_as_uint(nv) : 0u);
-                    if (lane == 0) (reinterpret_cast<uint32_t*>(smem + C::kNmOff) + 4 * u)[warp & 3] = nmax;
+                    const int t = tbase + n, u = t & 1;
+                    wait(bar_k + 8 * u, (t >> 1) & 1);
+                    if (t >= 2) wait(bar_s + 8 * u, ((t >> 1) - 1) & 1);   // S(t - 2) has read its K tile
+                    // a token per thread; the quarters are taken in an order that
+                    // differs between lanes whose records start in the same banks
+                    const Tables kt{p.ktab[0], p.ktab[1], p.ktab[2], p.ktab[3]};
+                    const uint8_t* rec = smem + C::kSKOff + u * C::kSK + r * C::kRbK;
+                    uint8_t* sK = smem + C::kKOff + u * 32768;
+                    const int turn = KB == 4 ? r >> 1 : r >> 3;
+                    // (rolled: unrolled by two the CTA's warps took 150 us at 64 nodes, 8
+                    // sequences of 24,000 tokens, so 142: what the instruction caches hold)
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        const int quarter = (q + turn) & 3;
+                        uint32_t hh[16];
+                        dequant_q32<(KB == 0 ? 4 : KB)>(rec + quarter * (C::kRbK / 4), kt, hh);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m)
+                            *reinterpret_cast<uint4*>(sK + sw128_offset(r, 32 * quarter + 8 * m)) =
+                                make_uint4(hh[4 * m], hh[4 * m + 1], hh[4 * m + 2], hh[4 * m + 3]);
+                    }
+                    fence_proxy_async();
                     mbar_arrive(bar_kr + 8 * u);
-                    nk = nk1;
-                    nvh = nv1;
                 }
             } else {
                 const Tables vt{p.vtab[0], p.vtab[1], p.vtab[2], p.vtab[3]};
+                if constexpr (KB != 0) load_norms(0);
 #pragma unroll 1
                 for (int n = 0; n < s.ntiles; ++n) {
                     const int t = tbase + n, u = t & 1;
+                    if constexpr (KB != 0) store_norms(n);
                     wait(bar_v + 8 * u, (t >> 1) & 1);
                     if (t >= 2) wait(bar_o + 8 * u, ((t >> 1) - 1) & 1);   // P.V(t - 2) has read its V tile
                     store_vt<VB>(smem + C::kSVOff + u * C::kSV, smem + C::kVtOff + u * 32768, vt, warp & 3, lane);
@@ -515,7 +527,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             for (int n = 0; n < s.ntiles; ++n) {
                 const int t = tbase + n, u = t & 1;
                 const int tok0 = (s.k0 + n) * kTok;
-                wait(bar_kr + 8 * u, (t >> 1) & 1);                    // scales and norms
+                wait(bar_n + 8 * u, (t >> 1) & 1);                     // scales and norms
                 if (t >= 2) wait(bar_o + 8 * u, ((t >> 1) - 1) & 1);   // P.V(t - 2) has read its P
                 wait(bar_s + 8 * u, (t >> 1) & 1);
                 tc_fence_after();
