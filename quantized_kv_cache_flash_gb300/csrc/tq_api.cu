@@ -647,7 +647,32 @@ int tq_encode_append_packed(tq_ctx** pctx, const tq_cache* c, const void* k_new,
 
 namespace {
 
-constexpr int kTreeDecodeRows = 16;   // rows per KV head up to which a tree runs on the decode kernel
+// Rows per KV head up to which a tree runs on the decode kernel, whose row groups hold
+// 16 and dequantise the context anew for each; the tensor-core kernel shares it between
+// 128 but takes three launches.  (turbo4, 8 sequences of 10,000 tokens, 32 / 8 heads: 16
+// rows 53 us there and 61 here, 20 rows 87 and 67, 128 rows 313 and 78; one of 2,000: 32
+// rows 17.9 and 13.2.)
+constexpr int kTreeDecodeRows = 16;
+
+// CTAs of a tree's split kernel, one per SM at most, for `units` of `per_unit` chunks
+// (at the length hint).  A CTA whose share crosses into another unit loads and
+// writes twice, and a unit's partials are merged one after another: so where as
+// many CTAs per unit as fit take no more chunks each than an even split over all
+// SMs would, or two, they do, with two chunks or more in contexts of more than
+// eight.  (Against an even split of two chunks or more over all SMs: 16 nodes, 8
+// sequences of 500 tokens and 8 KV heads 24.0 -> 19.0 us, one of 500 16.4 -> 12.5, one
+// of 8,000 and 4 KV heads 18.6 -> 14.9; one chunk a CTA there 15.6, and 14.3 for 13.0
+// in one of 2,000.)
+int plan_tree_ctas(long long units, int per_unit) {
+    constexpr int sms = tq::host::kSMs;
+    const long long chunks = units * per_unit;
+    if (units <= sms) {
+        const int fit = int(sms / units);
+        const int per = std::max((per_unit + fit - 1) / fit, per_unit > 8 ? 2 : 1);
+        if (per <= std::max<long long>(2, (chunks + sms - 1) / sms)) return int(units) * ((per_unit + per - 1) / per);
+    }
+    return int(std::min<long long>(sms, chunks));
+}
 
 // Tree attention on the tensor cores, for arguments that plan_decode has checked.
 int tree_impl(tq_ctx** pctx, const tq_cache* c, const tq::host::DecodePlan& pl, const void* q, int32_t num_q_heads,
@@ -662,8 +687,7 @@ int tree_impl(tq_ctx** pctx, const tq_cache* c, const tq::host::DecodePlan& pl, 
     if (r != TQ_OK) return r;
     if ((r = prepare_tables(ctx, c, pl.kb, pl.vb)) != TQ_OK) return r;
     if (pl.kb == 16 && (r = prepare_kmap(ctx, c)) != TQ_OK) return r;
-    // one CTA per SM, each with two chunks at least (one per group of warps)
-    const int ctas = int(std::max<long long>(1, std::min<long long>(tq::host::kSMs, (chunks + 1) / 2)));
+    const int ctas = plan_tree_ctas(units, (max_len_hint + 127) / 128);
     const size_t rows = size_t(ctas + units) * 128;
     const size_t q_bytes = size_t(units) * (pl.kb == 16 ? 32768 : 65536);
     if ((r = ensure_work(ctx, q_bytes + rows * (kD + 2) * sizeof(float))) != TQ_OK) return r;
@@ -824,8 +848,6 @@ int tq_tree_attention(tq_ctx** pctx, const tq_cache* c, const void* q, int32_t n
     const int r = tq::host::plan_decode(c, q, out, num_q_heads, tq_rows, max_len_hint, scale, &pl,
                                         tq::kMaxTreeGroup * TQ_MAX_TREE_NODES);
     if (r != TQ_OK) return r;
-    // The decode kernel's row groups hold up to 16 rows, and each group
-    // dequantises the context anew; the tensor-core kernel shares it between 128.
     if (pl.rows > kTreeDecodeRows && !tq::mode_table(c->mode) && !pl.res)
         return tree_impl(pctx, c, pl, q, num_q_heads, tq_rows, max_len_hint, scale, tree, out,
                          static_cast<cudaStream_t>(stream));
