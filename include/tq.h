@@ -234,8 +234,8 @@ int tq_prefill_attention(tq_ctx **ctx, const tq_cache *cache, const void *q,
  *   are negative or pass total raise TQ_STATUS_BAD_INDEX and the sequence's
  *   rows are left as they were.
  *   The other arguments, the supported modes and the group size as in
- *   tq_prefill_attention.  A V norm that overflowed fp16 counts as 65504 (so
- *   it cannot turn rows that do not see its token into NaN).
+ *   tq_prefill_attention.  A V norm that overflowed fp16 does not reach rows
+ *   that do not see its token; rows that do need not be finite.
  */
 int tq_prefill_attention_packed(tq_ctx **ctx, const tq_cache *cache, const void *q,
                                 int32_t num_q_heads, const int32_t *cu_seqlens, int32_t total,

@@ -246,7 +246,10 @@ __device__ __forceinline__ int packed_added(const EncodeParams& p, int b, int L)
 // threshold (3 in 1000 of Gaussian vectors) is encoded once more from its
 // exact transform: the sums of +-x are integers in units of 2^-24, below 2^47,
 // and the midpoints are compared in double.  So the codes do not depend on
-// which kernel or how many tokens took the vector.
+// which kernel or how many tokens took the vector.  What it costs: 20,480 tokens of
+// 8 KV heads take 39.4 us with 3 bits and 58.7 with 4 (distances from every threshold:
+// the kernel is bound by its arithmetic), tq_encode_append without it 28.7 and 39.3;
+// 32 prompts of 64 to 4096 tokens, 4 bits, 86 us (2 TB/s).
 constexpr float kNearBand = 1.0f / 131072.0f;
 
 // Advance lengths[] after the last CTA of the launch has read it: one ticket

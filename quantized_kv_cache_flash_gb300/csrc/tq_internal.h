@@ -191,7 +191,8 @@ int launch_decode(int kbits, int vbits, const DecodeParams& p, const CUtensorMap
 int launch_combine(const CombineParams& p, cudaStream_t stream);
 // Appends of more than kEncodeSmallMax vectors per stream run on the tensor
 // cores and read their inputs through kmap / vmap (encode_rows_map of k_new /
-// v_new); smaller ones ignore the maps.
+// v_new); smaller ones ignore the maps.  (Packed, 4 bits: 1024 vectors 7.0 us a warp
+// each and 13.1 on the tensor cores, 4096 10.3 and 13.1, 3 bits 9.7 and 10.4.)
 constexpr long long kEncodeSmallMax = 4096;
 int launch_encode(int kbits, int vbits, const EncodeParams& p, const CUtensorMap* kmap,
                   const CUtensorMap* vmap, cudaStream_t stream);

@@ -24,7 +24,17 @@
 // Tensor memory: per query tile S (128 columns, whose first 64 take P back as fp16
 // pairs) and O (128 columns), all 512.
 //
-// What bounds it: TODO.
+// What bounds it: per tile, the chain of a query tile's S, softmax and P.V (they take
+// turns on one S / P buffer; tensor memory is full) and the tensor core.  Quantized K:
+// 48 MMAs and the chain 1750 + 1700 + 900 cycles, with 250 of hand-overs between, in a
+// period of 4850; fp16 K: 32 MMAs, 1150 + 1700 + 900 in 3900.  Around the loop a CTA
+// takes some 18000 cycles for its item, Q' and the output.  Measured: 12 prompts of 64 to
+// 4096 tokens, turbo4, 32 / 8 heads, 436 us (613 TFLOP/s, q_lo's products not counted);
+// three chunks of 2047 to 8192 tokens behind up to 8191, fp16 K, 28 / 4 heads, 1630 us
+// (1.13 PFLOP/s); three prompts of 17 to 300 tokens 21 us.  With two groups of warps that
+// dequantise and issue for themselves the same calls took 541, 2255 and 25 us: the
+// thread that issues stands still while the tensor core works (600 to 1500 cycles a
+// product), as does the one that starts the copies (1000 a tile).
 #include "tq_device.cuh"
 #include "tq_internal.h"
 
@@ -550,6 +560,8 @@ __global__ void __launch_bounds__(kPackThreads, 1)
         // ---- dequantise: thread r of 128 ----
         const int r = tid - 256;
         // K's dims 64 half .. 64 half + 63, one token a thread
+        // (in halves, so that one is stored while S reads the other: 12 prompts of 64 to
+        // 4096 tokens 436 us, whole tiles 442)
         [[maybe_unused]] auto k_dequant = [&](int n, int half) {
             if constexpr (KB != 0) {
                 const Tables kt{p.ktab[0], p.ktab[1], p.ktab[2], p.ktab[3]};

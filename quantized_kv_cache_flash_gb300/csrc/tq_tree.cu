@@ -15,14 +15,19 @@
 //
 // A CTA is a pipeline over the 128-token tiles of its share, a stage per kind of
 // warp, with two K, V, S and P tiles between them: four warps dequantise K and
-// four V, eight run the softmax (fragments of 32 rows x 64 tokens per warp), one
-// thread issues the MMAs, two the copies.  So S(n + 1) and P.V(n - 1) run under
-// softmax(n).
+// four V, eight run the softmax (fragments of 16 rows x 128 tokens per warp), a warp
+// each issues S, P.V, the K copies and the V copies.  So S(n + 1) and P.V(n - 1) run
+// under softmax(n).
 //
-// What bounds it: a tile's 24 MMAs take 1536 cycles of the tensor core, its
-// shared-memory traffic (K, V and P tiles written and read by the MMAs, records,
-// scales) about as many at 128 bytes -- so Q' lies in tensor memory --, the exponentials 1024 cycles of MUFU,
-// dequantisation and softmax some 1000 issue slots per scheduler.
+// What bounds it: a tile takes 3000 cycles.  Its 24 MMAs are 1536 of the tensor core
+// (52% active measured); shared memory moves 2000 wavefronts of loads and stores and
+// 1024 of MMA operands (K, V and P, so Q' lies in tensor memory), together nine tenths of
+// the time; the schedulers issue 65% of it, half on the ALU's byte permutes.  All kinds of
+// warp share the instruction caches, so loops are rolled where they can be.  Measured:
+// 64 nodes, 8 sequences of 4000 to 16384 tokens, turbo4, 32 / 8 heads, 143 us (661 TFLOP/s,
+// q_lo's products not counted); 33 nodes, three of 777 to 16351, fp16 K, 28 / 4 heads,
+// 35.7 us; 16 nodes, one of 8192, turbo3, 16.6 us.  P over S in tensor memory took 147 us
+// for the first, Q' in shared memory besides 149.
 //
 // Split: the (batch, kv head, row tile) units lie end to end as 128-token
 // chunks, and CTA c of P takes [c C / P, (c + 1) C / P) of the C chunks, from
@@ -480,9 +485,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
     } else {
         // ---- softmax warps: warp w has rows 32 (w & 3) + 16 (w >> 2) .. + 15 as MMA
-        // fragments: lane 4v + c has rows v and v + 8 and columns 2c, 2c + 1 of
-        // every eight, so a thread reads a quarter of the tile's scales and norms (with a row per thread, their broadcast reads
-        // took a third of the shared-memory bandwidth that the MMAs need) ----
+        // fragments: lane 4v + c has rows v and v + 8 and columns 2c, 2c + 1 of every
+        // eight, so a thread reads a quarter of the tile's scales and norms (with a row
+        // per thread, their broadcast reads took a third of the shared-memory bandwidth
+        // that the MMAs need) ----
         regs_inc<kRegsSoftmax>();
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
