@@ -197,9 +197,11 @@ __global__ void __launch_bounds__(kPackThreads, 1)
         mbar_init(bar_q, 256);
         fence_barrier_init();
     }
-    // query tile t at columns 256 t: S, its first 64 reused for P as fp16 pairs, then O
-    if (warp == 1) tmem_alloc(smem_u32(tslot), 512);
     griddep_wait();  // cache, lengths, bounds and q come from earlier work on the stream
+    // query tile t at columns 256 t: S, its first 64 reused for P as fp16 pairs, then O
+    // (behind the wait: an append before may have let this grid start ahead of its own
+    // allocations)
+    if (warp == 1) tmem_alloc(smem_u32(tslot), 512);
     if (warp == 0) {
         packed_find(p, static_cast<int>(blockIdx.x) / p.hkv, tid, s_item);
     } else if (warp == 2 && blockIdx.x == 0) {
