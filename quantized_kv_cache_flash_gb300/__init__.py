@@ -231,6 +231,7 @@ class Cache:
         self.codebook_k = list(cbk)
         self.codebook_v = list(cbv)
         self.device = self.v_data.device
+        self.device_index = self.v_data.get_device()   # (-1: not on a CUDA device)
         self.struct = tq_cache(
             mode, batch, num_kv_heads, 128, capacity,
             _ptr(self.k_data), _ptr(self.k_norm), _ptr(self.v_data), _ptr(self.v_norm),
@@ -320,23 +321,24 @@ def tq_decode_attention_noalloc(cache: Cache, q, out, max_len_hint: int, scale: 
 def _tensor(name: str, t, dtype, shape, cache) -> None:
     """A contiguous tensor of this type and shape on the cache's device;
     ValueError otherwise."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == cache.device:
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == cache.device_index:
         return
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}"
                          + ("" if t.is_contiguous() else " (strided)"))
-    raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
 
 
 def _launch_stream(cache, stream) -> int:
     """The stream handle of a call on this cache: the given one or the current
     one of the cache's device, which has to be the current device."""
     import torch
-    dev = cache.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {dev}, which is not the current CUDA device")
+    dev = cache.device_index
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {cache.device}, which is not the current CUDA device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
+        return torch._C._cuda_getCurrentRawStream(dev)
     return int(getattr(stream, "cuda_stream", stream))
 
 
@@ -400,7 +402,7 @@ def tq_tree_mask(parents):
     n = len(parents)
     words = (n + 31) // 32
     buf = (ctypes.c_uint32 * max(n * words, 1))()
-    _check(lib().tq_tree_mask((ctypes.c_int32 * max(n, 1))(*[int(x) for x in parents]), n, buf),
+    _check(lib().tq_tree_mask((ctypes.c_int32 * max(n, 1))(*[max(-2, min(int(x), n)) for x in parents]), n, buf),
            "tq_tree_mask")
     return torch.frombuffer(bytearray(buf), dtype=torch.int32).reshape(n, words)
 

@@ -484,7 +484,14 @@ int ensure_work(tq_ctx* ctx, size_t bytes) {
         (void)cudaGetLastError();
         if (twice == bytes || cudaMalloc(&p, bytes) != cudaSuccess) return TQ_ERR_NOMEM;
     }
-    if (ctx->d_work) ctx->old_work.push_back(ctx->d_work);
+    if (ctx->d_work) {
+        try {
+            ctx->old_work.push_back(ctx->d_work);
+        } catch (...) {   // (no exception leaves a C entry)
+            cudaFree(p);
+            return TQ_ERR_NOMEM;
+        }
+    }
     ctx->d_work = p;
     ctx->work_bytes = bytes;
     return TQ_OK;
