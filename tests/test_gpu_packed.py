@@ -149,6 +149,8 @@ PREFILLS = [
     ("turbo4", 8, 2, [0] * 70, [(13 * i) % 41 for i in range(70)], None, 1.0),   # over 32 sequences
     ("turbo3", 8, 2, [200, 30], [300, 100], 450, 1.0),                # hint below a length
     ("turbo4_asym", 28, 4, [700, 0], [20, 500], None, 32.0),
+    ("turbo4", 8, 2, [1500, 0], [700, 40], None, 32.0),               # many tiles, bases that move late
+    ("turbo3_asym", 12, 2, [2000, 5], [300, 1], None, 4.0),           # G 6, fp16 K
 ]
 
 

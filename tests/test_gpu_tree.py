@@ -69,6 +69,9 @@ CASES = [
     ("turbo4_asym", 32, 8, [2000, 300], 40, True, 16.0),
     ("turbo4", 32, 8, [5000, 3], 48, False, 1.0),          # long: many splits of one unit
     ("turbo3_table", 32, 8, [700], 40, True, 1.0),
+    ("turbo4", 16, 8, [30 + 7 * i for i in range(40)], 9, False, 1.0),   # more units than SMs
+    ("turbo3_asym", 20, 4, [4200], 21, False, 1.0),        # CTAs of one unit each, many to merge
+    ("turbo4k_3v", 12, 2, [100, 3000, 0, 17], 30, False, 4.0),   # CTAs that cross into other units
 ]
 
 
