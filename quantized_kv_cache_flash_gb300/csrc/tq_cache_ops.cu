@@ -26,7 +26,7 @@ namespace tq {
 // head, sequence); every CTA checks its sequence's list before it writes.
 // The bytes are few (some KB per sequence): the call's time is a launch and
 // two dependent trips to memory (the list, then the records): 2.2 us a call in a
-// graph for 5 kept tokens of one sequence (4 KV heads, turbo3), 7 to 8 us issued one
+// graph for 5 kept tokens of one sequence (4 KV heads, turbo3), 6 us issued one
 // by one, which is the host's.
 // ---------------------------------------------------------------------------
 constexpr int kCompactGroup = 32;    // tokens loaded before any is stored

@@ -243,8 +243,11 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t 
 // Opt a kernel into `bytes` of dynamic shared memory (and, carveout >= 0, a
 // preferred shared-memory carveout) on the current device, once per device:
 // `done` keeps one bit per device ordinal (devices past 63 set it every call).
+// min_regs: the registers per thread that a kernel's split between its warp groups
+// counts on; built with fewer it would wait for them for ever, so it is refused.
 template <typename Kernel>
-cudaError_t set_smem_attr_once(Kernel kernel, int bytes, std::atomic<uint64_t>& done, int carveout = -1) {
+cudaError_t set_smem_attr_once(Kernel kernel, int bytes, std::atomic<uint64_t>& done, int carveout = -1,
+                               int min_regs = 0) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -253,6 +256,11 @@ cudaError_t set_smem_attr_once(Kernel kernel, int bytes, std::atomic<uint64_t>& 
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && carveout >= 0)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, carveout);
+    if (e == cudaSuccess && min_regs > 0) {
+        cudaFuncAttributes a;
+        e = cudaFuncGetAttributes(&a, kernel);
+        if (e == cudaSuccess && a.numRegs < min_regs) e = cudaErrorInvalidKernelImage;
+    }
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
     return e;
 }

@@ -740,7 +740,7 @@ template <int KB, int VB>
 static int launch_t(const PrefillParams& p, const CUtensorMap* kmap, cudaStream_t stream) {
     using C = PackCfg<KB, VB>;
     static std::atomic<uint64_t> attr_done{0};
-    const cudaError_t e = set_smem_attr_once(tq_packed_prefill_kernel<KB, VB>, C::kSmemAlloc, attr_done);
+    const cudaError_t e = set_smem_attr_once(tq_packed_prefill_kernel<KB, VB>, C::kSmemAlloc, attr_done, -1, kRegsLaunch);
     if (e != cudaSuccess) return e;
     return launch_pdl(tq_packed_prefill_kernel<KB, VB>, dim3(p.slots * p.hkv), dim3(kPackThreads), C::kSmemAlloc,
                       stream, p, *kmap);

@@ -845,7 +845,7 @@ static int launch_tree_t(const TreeParams& p, const CUtensorMap* kmap, cudaStrea
                          cudaEvent_t ev1) {
     using C = TreeCfg<KB, VB>;
     static std::atomic<uint64_t> attr_done{0};
-    cudaError_t e = set_smem_attr_once(tq_tree_kernel<KB, VB>, C::kSmemAlloc, attr_done);
+    cudaError_t e = set_smem_attr_once(tq_tree_kernel<KB, VB>, C::kSmemAlloc, attr_done, -1, kRegsLaunch);
     if (e != cudaSuccess) return e;
     if (ev0) cudaEventRecord(ev0, stream);
     e = launch_pdl(tq_tree_q_kernel<KB != 0>, dim3(p.batch * p.per_b * (kTreeRows / 8)), dim3(256), 0, stream, p);
