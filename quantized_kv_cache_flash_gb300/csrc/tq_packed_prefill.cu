@@ -328,12 +328,12 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             const float* col = colK + 4 * (lane & 3);
             const uint8_t* nv_base = smem + C::kNvOff;
             const float* nvs = reinterpret_cast<const float*>(nv_base) + 4 * (lane & 3);
+            // how far a score may pass its row's base: p n_v stays below 2^15 (from the
+            // largest norm's exponent)
             const uint2 top = *reinterpret_cast<const uint2*>(nv_base + C::kTile * 4);
-            const __half2 nm = __hmax2(*reinterpret_cast<const __half2*>(&top.x), *reinterpret_cast<const __half2*>(&top.y));
-            // p n_v stays below 2^15.99
-            const float slack =
-                fmaxf(0.f, fminf(10.f, 15.99f - __log2f(fmaxf(__low2float(nm), __high2float(nm)))));
-            const float most = fast_exp2(slack);
+            const uint32_t top2 = __vmaxu2(top.x, top.y), top1 = max(top2 & 0xffffu, top2 >> 16);
+            const int slack_i = max(0, min(10, 14 + 15 - static_cast<int>(top1 >> 10)));
+            const float slack = static_cast<float>(slack_i), most = __int_as_float((slack_i + 127) << 23);
             const bool masked = tok0 + C::kTile - 1 > lim_lo;
             const uint32_t t_hi = t_s + (16u << 16);   // rows 16-31
             float2 nb[4], sum[4];

@@ -49,7 +49,7 @@ namespace {
 
 constexpr int kTok = 128;            // tokens per tile (chunk)
 constexpr int kTreeRows = 128;       // query rows per unit
-constexpr float kSlack = 10.f;         // log2 by which a score may pass its row's base
+constexpr int kSlack = 10;             // log2 by which a score may pass its row's base
 
 template <int KB, int VB>
 struct TreeCfg {
@@ -542,11 +542,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     const uint32_t t_s = tmem + 128 * u + lanes + (static_cast<uint32_t>(16 * half) << 16);
                     const float* col = reinterpret_cast<const float*>(smem + C::kColOff) + u * kTok + c4;
                     const float* nvs = reinterpret_cast<const float*>(smem + C::kNvOff) + u * kTok + c4;
-                    // how far a score may pass its row's base: p n_v stays below 2^15.99
-                    const float4 nm = *reinterpret_cast<const float4*>(smem + C::kNmOff + 16 * u);
-                    const float slack = fmaxf(
-                        0.f, fminf(kSlack, 15.99f - __log2f(fmaxf(fmaxf(nm.x, nm.y), fmaxf(nm.z, nm.w)))));
-                    const float most = fast_exp2(slack);
+                    // how far a score may pass its row's base: p n_v stays below 2^15 (from the
+                    // largest norm's exponent)
+                    const uint4 nm = *reinterpret_cast<const uint4*>(smem + C::kNmOff + 16 * u);
+                    const int spare = 14 + 127 - static_cast<int>(max(max(nm.x, nm.y), max(nm.z, nm.w)) >> 23);
+                    const int slack_i = max(0, min(kSlack, spare));
+                    const float slack = static_cast<float>(slack_i), most = __int_as_float((slack_i + 127) << 23);
                     // stmatrix: lane 8m + k gives row k of matrix m: rows 0-7 and 8-15 of
                     // eight tokens, then of the next eight
                     const uint32_t prow =
