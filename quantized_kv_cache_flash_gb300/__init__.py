@@ -145,6 +145,19 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else int(t.data_ptr())
 
 
+# What the calls on packed sequences, trees and moves need of torch, bound by the first
+# cache (an import statement and torch.cuda's wrappers take 0.5 us of a call's 5.7).
+_F16 = _I32 = _current_device = _current_stream = None
+
+
+def _bind_torch() -> None:
+    global _F16, _I32, _current_device, _current_stream
+    import torch
+    _F16, _I32 = torch.float16, torch.int32
+    _current_device = getattr(torch._C, "_cuda_getDevice", None)
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
@@ -201,6 +214,8 @@ class Cache:
     def __init__(self, mode: int, batch: int, num_kv_heads: int, capacity: int, device,
                  codebook_k=None, codebook_v=None, rot_seed: int = 42, v_rescale: float = 1.0):
         import torch
+        if _F16 is None:
+            _bind_torch()
         kb, vb = MODE_BITS[mode]
         self.mode, self.batch, self.num_kv_heads, self.capacity = mode, batch, num_kv_heads, capacity
         table = mode in TABLE_MODES
@@ -333,23 +348,21 @@ def _tensor(name: str, t, dtype, shape, cache) -> None:
 def _launch_stream(cache, stream) -> int:
     """The stream handle of a call on this cache: the given one or the current
     one of the cache's device, which has to be the current device."""
-    import torch
     dev = cache.device_index
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _current_device():
         raise ValueError(f"the cache is on {cache.device}, which is not the current CUDA device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _current_stream(dev)
     return int(getattr(stream, "cuda_stream", stream))
 
 
 def tq_encode_append_packed(ctx: Context, cache: Cache, k_new, v_new, cu_seqlens, stream=None) -> None:
     """Append packed k_new/v_new fp16 [total, Hkv, 128]: rows cu_seqlens[b] ..
     cu_seqlens[b + 1] - 1 (int32 [B + 1] on the device) go to sequence b."""
-    import torch
     shape = (k_new.shape[0], cache.num_kv_heads, 128)
-    _tensor("k_new", k_new, torch.float16, shape, cache)
-    _tensor("v_new", v_new, torch.float16, shape, cache)
-    _tensor("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), cache)
+    _tensor("k_new", k_new, _F16, shape, cache)
+    _tensor("v_new", v_new, _F16, shape, cache)
+    _tensor("cu_seqlens", cu_seqlens, _I32, (cache.batch + 1,), cache)
     _check(lib().tq_encode_append_packed(ctx.ref, cache.ref,
                                          k_new.data_ptr(), v_new.data_ptr(), cu_seqlens.data_ptr(),
                                          shape[0], _launch_stream(cache, stream)),
@@ -361,13 +374,12 @@ def tq_prefill_attention_packed(ctx: Context, cache: Cache, q, out, cu_seqlens, 
     """Causal attention of packed query blocks q[total, Hq, 128] (already
     appended to the cache): rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 belong
     to sequence b.  Output rows of no sequence are left as they were."""
-    import torch
     if q.dim() != 3:
         raise ValueError("q must be [total, Hq, 128]")
     total, hq, _ = q.shape
-    _tensor("q", q, torch.float16, (total, hq, 128), cache)
-    _tensor("out", out, torch.float16, q.shape, cache)
-    _tensor("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), cache)
+    _tensor("q", q, _F16, (total, hq, 128), cache)
+    _tensor("out", out, _F16, q.shape, cache)
+    _tensor("cu_seqlens", cu_seqlens, _I32, (cache.batch + 1,), cache)
     _check(lib().tq_prefill_attention_packed(ctx.ref, cache.ref,
                                              _ptr(q), int(q.shape[1]), _ptr(cu_seqlens),
                                              int(q.shape[0]), int(max_len_hint), float(scale),
@@ -380,14 +392,13 @@ def tq_tree_attention(ctx: Context, cache: Cache, q, out, tree_mask, max_len_hin
     """Attention of a tree of drafted tokens q[B, Hq, Tq, 128], the last Tq
     tokens of every sequence.  tree_mask: int32 [1 or B, Tq, ceil(Tq / 32)]
     words (``tq_tree_mask``), bit i of row j set where node j sees node i."""
-    import torch
     if q.dim() != 4 or tree_mask.dim() != 3:
         raise ValueError("q must be [B, Hq, Tq, 128] and tree_mask [1 or B, Tq, ceil(Tq / 32)]")
     _, hq, n, _ = q.shape
     per_seq = tree_mask.shape[0]
-    _tensor("q", q, torch.float16, (cache.batch, hq, n, 128), cache)
-    _tensor("out", out, torch.float16, q.shape, cache)
-    _tensor("tree_mask", tree_mask, torch.int32,
+    _tensor("q", q, _F16, (cache.batch, hq, n, 128), cache)
+    _tensor("out", out, _F16, q.shape, cache)
+    _tensor("tree_mask", tree_mask, _I32,
             (1 if per_seq == 1 else cache.batch, n, (n + 31) // 32), cache)
     _check(lib().tq_tree_attention(ctx.ref, cache.ref, q.data_ptr(),
                                    hq, n, int(max_len_hint), float(scale),
@@ -412,12 +423,11 @@ def tq_cache_compact(ctx: Context, cache: Cache, start, keep, num_keep, num_draf
     """Keep tokens start[b] + keep[b, :num_keep[b]] of the drafted block
     [start[b], start[b] + num_drafted) as start[b], start[b] + 1, ... and cut
     the sequence off behind them (all int32 on the device)."""
-    import torch
-    _tensor("start", start, torch.int32, (cache.batch,), cache)
+    _tensor("start", start, _I32, (cache.batch,), cache)
     if keep.dim() != 2:
         raise ValueError("keep must be [B, max_keep]")
-    _tensor("keep", keep, torch.int32, (cache.batch, keep.shape[1]), cache)
-    _tensor("num_keep", num_keep, torch.int32, (cache.batch,), cache)
+    _tensor("keep", keep, _I32, (cache.batch, keep.shape[1]), cache)
+    _tensor("num_keep", num_keep, _I32, (cache.batch,), cache)
     _check(lib().tq_cache_compact(ctx.ref, cache.ref, start.data_ptr(),
                                   int(num_drafted), keep.data_ptr(), num_keep.data_ptr(), keep.shape[1],
                                   _launch_stream(cache, stream)), "tq_cache_compact")
@@ -427,12 +437,11 @@ def tq_cache_copy(ctx: Context, dst: Cache, src: Cache, dst_seq, src_seq, max_le
                   num_tokens=None, stream=None) -> None:
     """Sequence dst_seq[m] of `dst` becomes the first num_tokens[m] tokens (None:
     all) of sequence src_seq[m] of `src`, which may be the same cache."""
-    import torch
     m = dst_seq.numel()
-    _tensor("dst_seq", dst_seq, torch.int32, (m,), dst)
-    _tensor("src_seq", src_seq, torch.int32, (m,), dst)
+    _tensor("dst_seq", dst_seq, _I32, (m,), dst)
+    _tensor("src_seq", src_seq, _I32, (m,), dst)
     if num_tokens is not None:
-        _tensor("num_tokens", num_tokens, torch.int32, (m,), dst)
+        _tensor("num_tokens", num_tokens, _I32, (m,), dst)
     if src.device != dst.device:
         raise ValueError("the two caches are on different devices")
     _check(lib().tq_cache_copy(ctx.ref, dst.ref,
