@@ -368,6 +368,20 @@ using tq::host::build_tables;
 using tq::host::check_cache;
 using tq::host::make_signs;
 
+// Zeroes a new context's words, done when this returns: on a stream of its own, since
+// a memset on the default stream is asynchronous and nothing orders it before work on
+// a non-blocking stream, which would then take its tickets from uninitialised counters
+// or lose its status bits to the late memset.
+cudaError_t zero_words(uint32_t* words, size_t bytes) {
+    cudaStream_t s = nullptr;
+    cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (e != cudaSuccess) return e;
+    e = cudaMemsetAsync(words, 0, bytes, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    const cudaError_t d = cudaStreamDestroy(s);
+    return e != cudaSuccess ? e : d;
+}
+
 int get_ctx(tq_ctx** pctx, tq_ctx** out) {
     if (pctx == nullptr) return TQ_ERR_INVALID_ARG;
     int dev = 0;
@@ -380,7 +394,7 @@ int get_ctx(tq_ctx** pctx, tq_ctx** out) {
             delete c;
             return TQ_ERR_NOMEM;
         }
-        if (cudaMemset(c->d_words, 0, 64) != cudaSuccess) {
+        if (zero_words(c->d_words, 64) != cudaSuccess) {
             cudaFree(c->d_words);
             delete c;
             return TQ_ERR_CUDA;

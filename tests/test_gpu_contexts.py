@@ -1,0 +1,52 @@
+"""Contexts on the GPU: what a new one owes to work on other streams."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import quantized_kv_cache_flash_gb300 as tqf
+from quantized_kv_cache_flash_gb300 import workloads as wl
+from tests import helpers as H
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from quantized_kv_cache_flash_gb300 import build
+    build.build()
+    return torch.device("cuda", 0)
+
+
+def i32(x, dev):
+    return torch.tensor(x, dtype=torch.int32, device=dev)
+
+
+@pytest.mark.parametrize("n", [40, 5000])   # a warp per vector; the tensor-core kernel with its tile counter
+def test_first_call_on_a_side_stream_while_the_default_stream_is_busy(dev, n):
+    """The first call of a context creates it.  Its counters and status word are
+    zero for that call and nothing clears them behind it, whatever the default
+    stream still has to do."""
+    cap = (2 * n + 15) // 16 * 16
+    k, v = (H.upload(wl.random_fp16(50 + i, (n, 1, 128)), dev) for i in range(2))
+    cu = i32([0, n - 3, n], dev)
+    cache = tqf.Cache(tqf.MODES["turbo3"], 2, 1, cap, dev)
+    side = torch.cuda.Stream()
+    tqf.tq_encode_append_packed(tqf.Context(), cache, k, v, cu, stream=side)   # (loads the kernels)
+    torch.cuda.synchronize()
+    cache.lengths.copy_(i32([0, cap], dev))      # the second sequence is full
+    torch.cuda.synchronize()
+    torch.cuda.synchronize()
+    ctx = tqf.Context()
+    torch.cuda._sleep(200_000_000)               # some 0.1 s of the default stream
+    for _ in range(2):
+        tqf.tq_encode_append_packed(ctx, cache, k, v, cu, stream=side)
+    side.synchronize()
+    assert not torch.cuda.default_stream().query()   # (the appends did not wait for it)
+    torch.cuda.synchronize()
+    assert cache.lengths.cpu().tolist() == [2 * (n - 3), cap]
+    assert torch.equal(cache.v_data[0, 0, :n - 3], cache.v_data[0, 0, n - 3:2 * (n - 3)])
+    assert tqf.tq_get_status(ctx) == tqf.TQ_STATUS_CAPACITY
+    assert tqf.tq_get_status(ctx) == 0
