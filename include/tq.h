@@ -256,7 +256,8 @@ int tq_prefill_attention_packed(tq_ctx **ctx, const tq_cache *cache, const void 
  *   mask_batch: 1 (one mask for all sequences) or batch.
  *   max_len_hint, scale: as in tq_decode_attention; tokens past the hint are
  *              not read.
- * A row that sees no token gives 0 and raises TQ_STATUS_SHORT_CONTEXT.  Where
+ * A row that sees no token gives 0 and raises TQ_STATUS_SHORT_CONTEXT; one with a
+ * NaN score (q or the record of a token that it sees) is NaN.  Where
  * lengths[b] < tq the first tq - lengths[b] drafted tokens do not exist.
  * A drafted token that a row does not see adds nothing to it, whatever its
  * record holds (norms that overflowed fp16 or NaN in padding nodes; rows that

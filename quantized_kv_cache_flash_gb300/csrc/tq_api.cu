@@ -328,6 +328,7 @@ int launch_decode_plan(const DecodePlan& pl, const tq_cache* c, const CodebookTa
     cp.group_rows = pl.group_rows;
     cp.max_len = max_len_hint;
     cp.num_ctas = pl.ctas;
+    cp.nan_rows = tree != nullptr ? 1 : 0;
     cp.v_rescale = c->v_rescale;
     std::memcpy(cp.signs, signs, sizeof(cp.signs));
     return cuda_err_code(static_cast<cudaError_t>(tq::launch_combine(cp, stream)));

@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(32 * W) tq_combine_kernel(const __grid_constan
 
     float M = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool nan = false;   // of a tree: a partial's sum is NaN (its base is -inf where all its scores were)
     for (int i0 = warp; i0 < n; i0 += 8 * W) {
         // this pass: partials i0 + W k, k < 8; lane k < 8 holds partial k's (m, l)
         const bool mine = lane < 8 && used(i0 + W * lane);
@@ -94,6 +95,7 @@ __global__ void __launch_bounds__(32 * W) tq_combine_kernel(const __grid_constan
         const float2 ml = mine ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + row0 +
                                         16 * static_cast<size_t>(i0 + W * lane))
                                : make_float2(-INFINITY, 0.f);
+        nan = nan || ml.y != ml.y;
         float4 o[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -126,6 +128,7 @@ __global__ void __launch_bounds__(32 * W) tq_combine_kernel(const __grid_constan
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    if (p.nan_rows && __any_sync(0xffffffffu, nan)) den = __int_as_float(0x7fffffff);
     s_acc[warp][lane] = acc;
     if (lane == 0) {
         s_m[warp] = M;
@@ -148,6 +151,7 @@ __global__ void __launch_bounds__(32 * W) tq_combine_kernel(const __grid_constan
     }
     float inv = 0.f;
     if (dsum > 0.f) inv = p.v_rescale / dsum;
+    else if (p.nan_rows && dsum != dsum) inv = dsum;
     else if (lane == 0) atomicOr(p.status, kStatusShortContext);
     float v[4] = {a.x * inv, a.y * inv, a.z * inv, a.w * inv};
     wht128_lane4(v, lane);

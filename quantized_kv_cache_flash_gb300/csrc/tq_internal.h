@@ -57,6 +57,7 @@ struct CombineParams {
     __half* out;              // [B, Hq, Tq, 128]
     uint32_t* status;
     int32_t batch, hkv, hq, group, tq, row_groups, group_rows, max_len, num_ctas;
+    int32_t nan_rows;         // 1 (a tree's call): a row with a NaN sum is NaN, not a row that sees no token
     float v_rescale;
     uint32_t signs[4];
 };

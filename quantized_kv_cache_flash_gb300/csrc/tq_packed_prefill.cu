@@ -531,10 +531,11 @@ __global__ void __launch_bounds__(kPackThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 128; ++e) o[e] = 0.f;
             }
-            if (row_ok && !(l_sum > 0.f)) atomicOr(p.status, kStatusShortContext);
+            // (a NaN sum is a row of NaN scores, not one that sees no token)
+            if (row_ok && l_sum == 0.f) atomicOr(p.status, kStatusShortContext);
             // 1/l, v_rescale and the rotation's 1/sqrt(128), applied after the
             // (linear) transform in one packed multiply
-            const float g = l_sum > 0.f ? p.v_rescale / l_sum * 0.08838834764831845f : 0.f;
+            const float g = l_sum == 0.f ? 0.f : p.v_rescale / l_sum * 0.08838834764831845f;
             wht128_thread(o);
             // over this row of Q', which the MMAs have read
 #pragma unroll

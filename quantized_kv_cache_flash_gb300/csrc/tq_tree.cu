@@ -792,6 +792,7 @@ __global__ void __launch_bounds__(256) tq_tree_combine_kernel(const __grid_const
     griddep_wait();
     float M = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool nan = false;   // a partial's sum is NaN (its base is -inf where all its scores were): so is the row
     auto merge = [&](auto ahead) {   // with so many partials in flight
         constexpr int kAhead = decltype(ahead)::value;
         for (int i0 = 0; i0 < n; i0 += kAhead) {
@@ -807,7 +808,10 @@ __global__ void __launch_bounds__(256) tq_tree_combine_kernel(const __grid_const
             }
             float Mn = M;
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) Mn = fmaxf(Mn, ml[k].x);
+            for (int k = 0; k < kAhead; ++k) {
+                Mn = fmaxf(Mn, ml[k].x);
+                nan = nan || ml[k].y != ml[k].y;
+            }
             if (Mn == -INFINITY) continue;
             const float sc = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
             acc.x *= sc; acc.y *= sc; acc.z *= sc; acc.w *= sc;
@@ -828,7 +832,8 @@ __global__ void __launch_bounds__(256) tq_tree_combine_kernel(const __grid_const
     if (n > 4) merge(std::integral_constant<int, 8>{});
     else merge(std::integral_constant<int, 4>{});
     float inv = 0.f;
-    if (den > 0.f) inv = p.v_rescale / den;
+    if (nan) inv = __int_as_float(0x7fffffff);
+    else if (den > 0.f) inv = p.v_rescale / den;
     else if (lane == 0) atomicOr(p.status, kStatusShortContext);
     float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
     wht128_lane4(v, lane);
