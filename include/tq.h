@@ -172,9 +172,9 @@ int tq_encode_append(tq_ctx **ctx, const tq_cache *cache, const void *k_new,
  * Row cu_seqlens[b] + j is written at position lengths[b] + j; afterwards
  * lengths[b] += cu_seqlens[b+1] - cu_seqlens[b].  A sequence that would pass
  * the capacity is left untouched and TQ_STATUS_CAPACITY is raised; bounds that
- * decrease, are negative or pass total raise TQ_STATUS_BAD_INDEX, that
- * sequence's length is not advanced, and records past the lengths are
- * unspecified.
+ * decrease, are negative or pass total raise TQ_STATUS_BAD_INDEX and that
+ * sequence is left untouched (each sequence goes by its own two bounds: a row
+ * that several name is appended to each).
  * The records are tq_encode_append's, except that every code is decided
  * exactly: an element near a decision midpoint is decided from the exact
  * transform, so the codes do not depend on the kernel (more than 4096 vectors
@@ -232,7 +232,8 @@ int tq_prefill_attention(tq_ctx **ctx, const tq_cache *cache, const void *q,
  *   rows that belong to no sequence are left as they were.  A row that sees no
  *   token gives 0 and raises TQ_STATUS_SHORT_CONTEXT; bounds that decrease,
  *   are negative or pass total raise TQ_STATUS_BAD_INDEX and the sequence's
- *   rows are left as they were.
+ *   rows are left as they were.  (Where bounds decrease, sequences may share
+ *   rows: the output of a call that does so is unspecified.)
  *   The other arguments, the supported modes and the group size as in
  *   tq_prefill_attention.  A V norm that overflowed fp16 does not reach rows
  *   that do not see its token; rows that do need not be finite.

@@ -107,6 +107,23 @@ __device__ __forceinline__ unsigned short norm_to_half(U128 S) {
 }
 
 
+// The same of a vector that a warp holds, lane l dims 4l .. 4l + 3 (the 128-bit
+// integer sums of their exact squares are added across the warp).
+__device__ __forceinline__ unsigned short norm_exact_warp(float2 f0, float2 f1) {
+    U128 S = sq_u128(fp16_scaled_int(f0.x));
+    S = add128(S, sq_u128(fp16_scaled_int(f0.y)));
+    S = add128(S, sq_u128(fp16_scaled_int(f1.x)));
+    S = add128(S, sq_u128(fp16_scaled_int(f1.y)));
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) {
+        U128 o;
+        o.lo = __shfl_xor_sync(0xffffffffu, S.lo, m);
+        o.hi = __shfl_xor_sync(0xffffffffu, S.hi, m);
+        S = add128(S, o);
+    }
+    return norm_to_half(S);
+}
+
 __device__ __forceinline__ float half_bits_to_float(unsigned short b) {
     return (b >= 0x7C00u) ? 65536.f : __half2float(__ushort_as_half(b));
 }
@@ -292,7 +309,7 @@ __device__ __forceinline__ void finish_append(const EncodeParams& p, int lane) {
 template <bool PACKED>
 __device__ __forceinline__ void finish_append_small(const EncodeParams& p, int lane, int len_pre) {
     __shared__ unsigned int s_ticket;
-    __syncthreads();
+    if constexpr (!PACKED) __syncthreads();   // (packed: the caller's barrier)
     if (threadIdx.x == 0) s_ticket = atomicAdd(p.counter, 1u);
     __syncthreads();
     if (s_ticket == gridDim.x - 1 && threadIdx.x < 32) {
@@ -416,6 +433,45 @@ __device__ __noinline__ void encode_exact_warp(const uint2 raw, uint8_t* dst, co
 #pragma unroll
     for (int i = 0; i < 4; ++i) code[i] = (neg[i] ? static_cast<uint32_t>(H) : 0u) | rank[i];
     store_codes_warp<BITS>(code, dst, lane);
+}
+
+// Packed appends whose bounds decrease somewhere: sequences may then share rows, and
+// packed_slot names one of them a row.  The rows that belong to another sequence as well
+// are encoded for it here (a warp a vector, warp w of nw), so that every sequence whose
+// own bounds are in order holds all its records.
+template <int KB, int VB>
+__device__ __noinline__ void append_shared_rows(const EncodeParams& p, long long w, long long nw, int lane) {
+    for (int b = 0; b < p.batch; ++b) {
+        const int first = p.cu[b], n = p.cu[b + 1] - first, L = p.lengths[b];
+        if (!packed_seq_ok(first, p.cu[b + 1], p.total) || n == 0) continue;
+        if (L < 0 || L > p.cap - n) {
+            if (w == 0 && lane == 0) atomicOr(p.status, kStatusCapacity);
+            continue;
+        }
+        for (long long i = w; i < 2ll * n * p.hkv; i += nw) {
+            const int j = static_cast<int>((i >> 1) / p.hkv), h = static_cast<int>((i >> 1) - 1ll * j * p.hkv);
+            if (packed_slot(p, first + j).b == b) continue;   // has it
+            const bool is_v = (i & 1) != 0;
+            const __half* x = (is_v ? p.v_new : p.k_new) + (static_cast<size_t>(first + j) * p.hkv + h) * kD;
+            const uint2 raw = reinterpret_cast<const uint2*>(x)[lane];
+            const size_t pos = (static_cast<size_t>(b) * p.hkv + h) * p.cap + L + j;
+            if (!is_v && KB == 0) {
+                reinterpret_cast<uint2*>(p.k_codes + pos * 256)[lane] = raw;
+                continue;
+            }
+            const int bits = is_v ? VB : KB;
+            uint8_t* const dst = (is_v ? p.v_codes : p.k_codes) + pos * (p.table ? 64 : bits * 16);
+            const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&raw.x));
+            const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&raw.y));
+            const unsigned short nb = norm_exact_warp(f0, f1);
+            if (lane == 0) {
+                store_norm((is_v ? p.v_norm : p.k_norm) + pos, dst, p.table ? (is_v ? p.v_cb : p.k_cb) : nullptr, nb);
+                if (nb >= 0x7C00u) atomicOr(p.status, kStatusNormOverflow);
+            }
+            if (is_v) encode_exact_warp<VB>(raw, dst, p.signs, p.v_mag, lane);
+            else encode_exact_warp<(KB == 0 ? VB : KB)>(raw, dst, p.signs, p.k_mag, lane);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -557,18 +613,7 @@ __device__ __noinline__ unsigned short norm_exact_row(const uint8_t* xs, int row
     const uint2 raw = *reinterpret_cast<const uint2*>(src);
     const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&raw.x));
     const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&raw.y));
-    U128 S = sq_u128(fp16_scaled_int(f0.x));
-    S = add128(S, sq_u128(fp16_scaled_int(f0.y)));
-    S = add128(S, sq_u128(fp16_scaled_int(f1.x)));
-    S = add128(S, sq_u128(fp16_scaled_int(f1.y)));
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
-        U128 o;
-        o.lo = __shfl_xor_sync(0xffffffffu, S.lo, m);
-        o.hi = __shfl_xor_sync(0xffffffffu, S.hi, m);
-        S = add128(S, o);
-    }
-    return norm_to_half(S);
+    return norm_exact_warp(f0, f1);
 }
 
 // B[n][k] = H[n][k] s_k as fp16 +-1 in the K-major swizzled layout; thread
@@ -680,8 +725,12 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
     if (tid < 256) build_rotation_b(sB, p.signs, tid);
     fence_proxy_async();   // B's generic stores, seen by the tensor core
     griddep_wait();
+    [[maybe_unused]] bool down = false;   // packed: whether the bounds decrease somewhere
+    if constexpr (PACKED)
+        for (int bb = tid; bb < p.batch; bb += kTcThreads) down = down || p.cu[bb] > p.cu[bb + 1];
     tc_fence_before();
-    __syncthreads();
+    if constexpr (PACKED) down = __syncthreads_or(down) != 0;
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
 
@@ -952,6 +1001,10 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
         }
         if (stalled && lane == 0) atomicOr(p.status, kStatusPipelineStall);
     }
+    if constexpr (PACKED)
+        if (down)
+            append_shared_rows<KB, VB>(p, static_cast<long long>(blockIdx.x) * (kTcEncWarps + 1) + warp,
+                                       static_cast<long long>(gridDim.x) * (kTcEncWarps + 1), lane);
     finish_append<PACKED>(p, lane);   // every thread has read lengths[] for the last time, no more tiles taken
     tc_fence_before();
     __syncthreads();
@@ -1043,6 +1096,12 @@ __global__ void __launch_bounds__(128) tq_encode_small_kernel(const __grid_const
                                   : static_cast<long long>(p.batch) * p.hkv * p.t_new;
     // lengths[lane] for the last CTA's update (warp 0), read now with the rest
     const int len_pre = (threadIdx.x < 32 && lane < p.batch) ? p.lengths[lane] : 0;
+    // and the bounds that this thread checks at the end
+    int cu0 = 0, cu1 = 0;
+    if (PACKED && threadIdx.x < static_cast<unsigned int>(p.batch)) {
+        cu0 = p.cu[threadIdx.x];
+        cu1 = p.cu[threadIdx.x + 1];
+    }
     if (gw < 2 * nvec) {
         const int which = static_cast<int>(gw & 1);  // 0 = K, 1 = V
         const long long v = gw >> 1;
@@ -1082,6 +1141,14 @@ __global__ void __launch_bounds__(128) tq_encode_small_kernel(const __grid_const
                                                p.v_norm + pos, p.table ? p.v_cb : nullptr, p.signs,
                                                p.v_gt, p.v_ge, p.v_mag, p.status, lane);
             }
+        }
+    }
+    if constexpr (PACKED) {
+        bool down = threadIdx.x < static_cast<unsigned int>(p.batch) && cu0 > cu1;
+        for (int bb = threadIdx.x + 128; bb < p.batch; bb += 128) down = down || p.cu[bb] > p.cu[bb + 1];
+        if (__syncthreads_or(down)) {
+            append_shared_rows<KB, VB>(p, gw, 4ll * gridDim.x, lane);
+            __syncthreads();
         }
     }
     finish_append_small<PACKED>(p, lane, len_pre);
