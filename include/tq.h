@@ -175,10 +175,10 @@ int tq_encode_append(tq_ctx **ctx, const tq_cache *cache, const void *k_new,
  * decrease, are negative or pass total raise TQ_STATUS_BAD_INDEX and that
  * sequence is left untouched (each sequence goes by its own two bounds: a row
  * that several name is appended to each).
- * The records are tq_encode_append's, except that every code is decided
- * exactly: an element near a decision midpoint is decided from the exact
- * transform, so the codes do not depend on the kernel (more than 4096 vectors
- * per stream take the tensor-core encode) or on the rounding of fp32 sums.
+ * The records are tq_encode_append's, except that a code whose element is within
+ * the rounding errors of a decision midpoint is decided from exact sums (and the
+ * midpoint in 64 bits), whatever the codebook: so the codes do not depend on the
+ * kernel (more than 4096 vectors per stream take the tensor-core encode).
  */
 int tq_encode_append_packed(tq_ctx **ctx, const tq_cache *cache, const void *k_new,
                             const void *v_new, const int32_t *cu_seqlens, int32_t total,

@@ -132,6 +132,36 @@ int build_tables(const float* cb, int n, int bits, CodebookTables* t) {
         else if (double(f) == tau) { t->ge[k] = f; t->gt[k] = up; }
         else { t->ge[k] = up; t->gt[k] = up; }
     }
+    // The errors of an encode, in units of the vector's norm.  Thresholds (and what they
+    // are compared with): 15 roundings, 11 in the warp-per-vector kernel, of a threshold T,
+    // of which those above sqrt(128) are never near.  Values: that kernel's 7 levels of fp32
+    // sums round by 2^-24 of values of which any level's add up to at most sqrt(128) n.
+    // The tensor core takes the 128 products 16 at a time with the sum so far: every addend
+    // cut to 25 bits below the leading bit of the largest, the sum cut to 24 bits (measured:
+    // 262,144 sums of +-x equal this bit for bit).  Let P be the largest addend or sum.  A
+    // product loses under 2^-25 P, and only if it is below 2^-15 P; the sum so far only
+    // beside a larger product, under 2^-25 n; the result of step s under 2^-23 of itself.
+    // With L products that keep their bits |x| adds up to sqrt(L) n, so a sum on the way to
+    // a y near T stays below (sqrt(L) + T / n) n / 2, and after step s below sqrt(16 s) n and
+    // sqrt(128 - 16 s) n + T.  A vector without entries below fine_min n loses in the last
+    // two ways alone.  (1 % on top covers the small products' part of the sums and the
+    // rounding of the norm.)
+    const double root = std::sqrt(double(kD));
+    const double top = h > 1 ? 0.5 * (double(cb[n - 1]) + double(cb[n - 2])) * root : 0.0;
+    const double T = std::min(top, 1.01 * root);
+    auto lost = [&](int L) {   // in units of 2^-25 n
+        const double l1 = std::sqrt(double(L)), P = std::max(1.0, std::min(l1, 0.5 * (l1 + T)));
+        double sums = 0.0;
+        for (int s = 1; s <= 8; ++s)
+            sums += std::min(P, std::min(std::sqrt(16.0 * s), std::sqrt(128.0 - 16.0 * s) + T));
+        return (kD - L) * P + 7.0 + 4.0 * sums;
+    };
+    double way = 0.0;
+    for (int L = 1; L <= kD; ++L) way = std::max(way, lost(L));
+    t->near_tc = float(1.01 * (std::ldexp(way, -25) + 15.0 * std::ldexp(T, -24)));
+    t->near_fine = float(1.01 * (std::ldexp(lost(kD), -25) + 15.0 * std::ldexp(T, -24)));
+    t->fine_min = float(1.01 * std::ldexp(std::min(root, 0.5 * (root + T)), -15));
+    t->near_small = float(1.01 * (7.0 * std::ldexp(root, -24) + 11.0 * std::ldexp(T, -24)));
     std::memcpy(t->cb, cb, n * sizeof(float));
     t->bits = bits;
     t->valid = true;
@@ -654,8 +684,16 @@ int tq_encode_append_packed(tq_ctx** pctx, const tq_cache* c, const void* k_new,
     p.total = total;
     if (kb != 16) std::memcpy(p.k_mag, c->codebook_k + (1 << (kb - 1)), sizeof(float) << (kb - 1));
     std::memcpy(p.v_mag, c->codebook_v + (1 << (vb - 1)), sizeof(float) << (vb - 1));
+    const bool tc = nvec > uint64_t(tq::kEncodeSmallMax);
+    const CodebookTables &kt = ctx->ktab, &vt = ctx->vtab;
+    p.k_near = tc ? kt.near_tc : kt.near_small;   // (fp16 K: not looked at)
+    p.v_near = tc ? vt.near_tc : vt.near_small;
+    p.k_near_fine = kt.near_fine;
+    p.v_near_fine = vt.near_fine;
+    p.k_fine_min = kt.fine_min;
+    p.v_fine_min = vt.fine_min;
     CUtensorMap kmap, vmap;
-    if (nvec > uint64_t(tq::kEncodeSmallMax)) {
+    if (tc) {
         if ((r = tq::host::encode_tokens_map(&kmap, k_new, c->num_kv_heads, total)) != TQ_OK ||
             (r = tq::host::encode_tokens_map(&vmap, v_new, c->num_kv_heads, total)) != TQ_OK)
             return r;

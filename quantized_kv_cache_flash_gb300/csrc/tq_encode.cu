@@ -256,18 +256,16 @@ __device__ __forceinline__ int packed_added(const EncodeParams& p, int b, int L)
     return L >= 0 && L <= p.cap - (next - first) ? next - first : 0;
 }
 
-// Packed appends decide every code exactly.  The rotated values and the
-// thresholds carry fp32 rounding errors: about 1e-6 of the vector's norm n
-// (the sums of the transform, each of magnitude ~n, and sqrtf of a sum of
-// squares within 1.07e-6).  A vector with a value within kNearBand * n of a
-// threshold (3 in 1000 of Gaussian vectors) is encoded once more from its
-// exact transform: the sums of +-x are integers in units of 2^-24, below 2^47,
-// and the midpoints are compared in double.  So the codes do not depend on
-// which kernel or how many tokens took the vector.  What it costs: 20,480 tokens of
-// 8 KV heads take 39.4 us with 3 bits and 58.7 with 4 (distances from every threshold:
-// the kernel is bound by its arithmetic), tq_encode_append without it 28.7 and 39.3;
-// 32 prompts of 64 to 4096 tokens, 4 bits, 86 us (2 TB/s).
-constexpr float kNearBand = 1.0f / 131072.0f;
+// Packed appends decide every code from exact sums.  The rotated values and the
+// thresholds carry rounding errors; a vector with a value within their bound, k_near or
+// v_near times its norm n, of a threshold or 0 (a percent of Gaussian vectors) is encoded
+// once more from its exact transform: the sums of +-x are integers in units of 2^-24,
+// below 2^47, and the midpoints are taken in double.  So the codes do not depend on
+// which kernel or how many tokens took the vector (build_tables derives the bounds: a
+// vector without very small entries gets along with 1/2 to 1/3 of the general one, and
+// 29,800 tokens of 8 KV heads, 4 bits, take 87 us instead of 95).  What it costs: 20,480
+// tokens of 8 KV heads take 41.6 us with 3 bits and 60.0 with 4 (distances from every
+// threshold), tq_encode_append without it 30.3 and 41.6.
 
 // Advance lengths[] after the last CTA of the launch has read it: one ticket
 // per CTA, taken once every thread of the CTA has read lengths[] for the last
@@ -853,8 +851,10 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
             // accumulators of 16 terms each, then pairwise: each square goes
             // through at most 15 + 3 = 18 roundings; certified or redone exactly
             float S32;
+            [[maybe_unused]] float least = 0.f;   // (packed) the smallest |x|
             {
                 float acc[8];
+                [[maybe_unused]] __half2 lo2[2] = {__float2half2_rn(65504.f), __float2half2_rn(65504.f)};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll
@@ -867,7 +867,13 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
                         float& a = acc[4 * (c & 1) + e];
                         a = fma_sq_f16(static_cast<unsigned short>(ww[e]), a);
                         a = fma_sq_f16(static_cast<unsigned short>(ww[e] >> 16), a);
+                        if constexpr (PACKED)
+                            lo2[e & 1] = __hmin2(lo2[e & 1], __habs2(*reinterpret_cast<const __half2*>(&ww[e])));
                     }
+                }
+                if constexpr (PACKED) {
+                    lo2[0] = __hmin2(lo2[0], lo2[1]);
+                    least = fminf(__low2float(lo2[0]), __high2float(lo2[0]));
                 }
                 S32 = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
             }
@@ -983,7 +989,10 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
                 // vectors too near a threshold, one at a time by the whole warp
                 // (a zero vector's codes are right: every y and T is 0)
                 const float near = fminf(fminf(near4[0], near4[1]), fminf(near4[2], near4[3]));
-                unsigned redo = __ballot_sync(0xffffffffu, valid && S32 > 0.f && near <= kNearBand * sqrtf(S32));
+                const float nrm = sqrtf(S32);
+                const bool fine = least >= (is_v ? p.v_fine_min : p.k_fine_min) * nrm;
+                const float band = is_v ? (fine ? p.v_near_fine : p.v_near) : (fine ? p.k_near_fine : p.k_near);
+                unsigned redo = __ballot_sync(0xffffffffu, valid && S32 > 0.f && near <= band * nrm);
                 while (redo) {
                     const int src = __ffs(redo) - 1;
                     redo &= redo - 1;
@@ -1021,8 +1030,8 @@ template <int BITS, bool PACKED>
 __device__ __forceinline__ void encode_vector_warp(const uint2 raw, uint8_t* dst,
                                                    __half* dst_norm, const float* tcb,
                                                    const uint32_t (&signs)[4], const float* gt,
-                                                   const float* ge, const float* mag, uint32_t* status,
-                                                   int lane) {
+                                                   const float* ge, const float* mag, float near_band,
+                                                   uint32_t* status, int lane) {
     const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&raw.x));
     const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&raw.y));
     float x[4] = {f0.x, f0.y, f1.x, f1.y};
@@ -1067,7 +1076,7 @@ __device__ __forceinline__ void encode_vector_warp(const uint2 raw, uint8_t* dst
 #pragma unroll
     for (int i = 0; i < 4; ++i) code[i] = quantize_code<BITS>(x[i] * inv, gt, ge, any_tie);
     if constexpr (PACKED) {
-        // the same band around the thresholds as in the large-append kernel
+        // (the values here are y / (sqrt(128) n))
         float near = INFINITY;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1076,7 +1085,7 @@ __device__ __forceinline__ void encode_vector_warp(const uint2 raw, uint8_t* dst
 #pragma unroll
             for (int k = 0; k < H - 1; ++k) near = fminf(near, fabsf(gt[k] - a));
         }
-        if (n > 0.f && __any_sync(0xffffffffu, near <= kNearBand * 0.08838834764831845f)) {
+        if (n > 0.f && __any_sync(0xffffffffu, near <= near_band * 0.08838834764831845f)) {
             encode_exact_warp<BITS>(raw, dst, signs, mag, lane);
             return;
         }
@@ -1134,12 +1143,12 @@ __global__ void __launch_bounds__(128) tq_encode_small_kernel(const __grid_const
                 } else {
                     encode_vector_warp<KB, PACKED>(raw, p.k_codes + pos * (p.table ? 64 : KB * 16),
                                                    p.k_norm + pos, p.table ? p.k_cb : nullptr, p.signs,
-                                                   p.k_gt, p.k_ge, p.k_mag, p.status, lane);
+                                                   p.k_gt, p.k_ge, p.k_mag, p.k_near, p.status, lane);
                 }
             } else {
                 encode_vector_warp<VB, PACKED>(raw, p.v_codes + pos * (p.table ? 64 : VB * 16),
                                                p.v_norm + pos, p.table ? p.v_cb : nullptr, p.signs,
-                                               p.v_gt, p.v_ge, p.v_mag, p.status, lane);
+                                               p.v_gt, p.v_ge, p.v_mag, p.v_near, p.status, lane);
             }
         }
     }

@@ -89,6 +89,9 @@ struct EncodeParams {
     const int32_t* cu;        // [B + 1]
     int32_t total;
     float k_mag[8], v_mag[8]; // the positive half of the codebooks, ascending
+    // a value this close to a threshold (times the norm) is decided exactly; large appends:
+    // the second one for vectors without entries below fine_min (times the norm)
+    float k_near, v_near, k_near_fine, v_near_fine, k_fine_min, v_fine_min;
 };
 
 // Chunked-prefill attention (tcgen05) parameters.  One CTA = one (query
@@ -298,6 +301,10 @@ struct CodebookTables {
     // by magnitude rank), for the score's fp8 residual product
     uint32_t tab8[2] = {};
     int res_shift = 0;
+    // how far an encode's value and a threshold may be off together, as a multiple of
+    // the vector's norm: the warp-per-vector kernel and the tensor-core one (and that one
+    // where no entry is below fine_min times the norm)
+    float near_small = 0.f, near_tc = 0.f, near_fine = 0.f, fine_min = 0.f;
 };
 
 constexpr int kSMs = 152;  // GB300 (only used to size the split grids)
