@@ -264,6 +264,11 @@ int tq_prefill_attention_packed(tq_ctx **ctx, const tq_cache *cache, const void 
  * record holds (norms that overflowed fp16 or NaN in padding nodes; rows that
  * do see such a token need not be finite).  Every mode and codebook is supported.  The call uses
  * the context's workspace like tq_decode_attention.
+ * Precision: a weight times its V norm is rounded to fp16 once.  More than 16 rows per KV
+ * head (and tq_prefill_attention_packed) scale the weights so that this is 2^-11 of a term
+ * whatever the norms' size, down to terms of 2^-18 of a row's largest; fewer rows, table
+ * records and codebooks of other than fp16 values take the decode kernel, where a term
+ * below 2^-14 is rounded by up to 2^-25, as in tq_decode_attention.
  */
 #define TQ_MAX_TREE_NODES 256
 int tq_tree_attention(tq_ctx **ctx, const tq_cache *cache, const void *q, int32_t num_q_heads,

@@ -329,10 +329,12 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             const uint8_t* nv_base = smem + C::kNvOff;
             const float* nvs = reinterpret_cast<const float*>(nv_base) + 4 * (lane & 3);
             // how far a score may pass its row's base: p n_v stays below 2^15 (from the
-            // largest norm's exponent)
+            // largest norm's exponent; subnormal norms count as 2^-15), and how far the
+            // largest one does where the base moves (a term then starts at 2^4 or above
+            // whatever the norms' size, and loses bits below 2^-18)
             const uint2 top = *reinterpret_cast<const uint2*>(nv_base + C::kTile * 4);
             const uint32_t top2 = __vmaxu2(top.x, top.y), top1 = max(top2 & 0xffffu, top2 >> 16);
-            const int slack_i = max(0, min(10, 14 + 15 - static_cast<int>(top1 >> 10)));
+            const int slack_i = max(0, 14 + 15 - static_cast<int>(top1 >> 10));
             const float slack = static_cast<float>(slack_i), most = __int_as_float((slack_i + 127) << 23);
             const bool masked = tok0 + C::kTile - 1 > lim_lo;
             const uint32_t t_hi = t_s + (16u << 16);   // rows 16-31
@@ -411,6 +413,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                         const bool fresh = fm[q] == -INFINITY;
                         const bool up = mx > (fresh ? -INFINITY : slack);
+                        mx -= fmaxf(0.f, slack - 10.f);   // (what the base moves by)
                         alpha[q] = up ? (fresh ? 0.f : fast_exp2(-mx)) : 1.f;
                         fl[q] *= alpha[q];
                         if (up) fm[q] = (fresh ? 0.f : fm[q]) + mx;

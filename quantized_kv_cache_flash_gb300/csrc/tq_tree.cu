@@ -9,9 +9,12 @@
 // with Q' = Rot(q) as two fp16 halves (quantized K: K's tile holds the fp16
 // centroids, the norm goes to the fp32 scores) or q (fp16 K).  V's tile holds
 // the centroids themselves, exact in fp16, and the V norm goes into P, so a
-// term is rounded once.  The base of a row may trail its scores by 10 (log2), or
-// by as much less as keeps p n_v of the tile's largest norm in fp16: with a slack
-// of 4 every third tile had a row that moved its base, with 10 hardly any has.
+// term is rounded once.  With e the exponent of a tile's largest V norm, the base of a
+// row may trail its scores by 14 - e (log2; p n_v stays below 2^15), and where it moves
+// it stops 10 short of that, so the largest weights' terms start at 2^4 or above whatever
+// the norms' size (a term loses bits below 2^-18, and less than 2^-29 of the largest norm
+// where it vanishes).  With a margin of 4 every third tile had a row that moved its base,
+// with 10 hardly any has.
 //
 // A CTA is a pipeline over the 128-token tiles of its share, a stage per kind of
 // warp, with two K, V, S and P tiles between them: four warps dequantise K and
@@ -49,7 +52,7 @@ namespace {
 
 constexpr int kTok = 128;            // tokens per tile (chunk)
 constexpr int kTreeRows = 128;       // query rows per unit
-constexpr int kSlack = 10;             // log2 by which a score may pass its row's base
+constexpr int kMargin = 10;            // log2 by which scores may grow before their row's base moves again
 
 template <int KB, int VB>
 struct TreeCfg {
@@ -543,10 +546,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     const float* col = reinterpret_cast<const float*>(smem + C::kColOff) + u * kTok + c4;
                     const float* nvs = reinterpret_cast<const float*>(smem + C::kNvOff) + u * kTok + c4;
                     // how far a score may pass its row's base: p n_v stays below 2^15 (from the
-                    // largest norm's exponent)
+                    // largest norm's exponent, -24 at least), and how far the largest one does
+                    // where the base moves
                     const uint4 nm = *reinterpret_cast<const uint4*>(smem + C::kNmOff + 16 * u);
                     const int spare = 14 + 127 - static_cast<int>(max(max(nm.x, nm.y), max(nm.z, nm.w)) >> 23);
-                    const int slack_i = max(0, min(kSlack, spare));
+                    const int slack_i = max(0, min(14 + 24, spare));
                     const float slack = static_cast<float>(slack_i), most = __int_as_float((slack_i + 127) << 23);
                     // stmatrix: lane 8m + k gives row k of matrix m: rows 0-7 and 8-15 of
                     // eight tokens, then of the next eight
@@ -635,6 +639,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                                 const bool fresh = m_base[q] == -INFINITY;
                                 const bool up = mx > (fresh ? -INFINITY : slack);
+                                mx -= fmaxf(0.f, slack - kMargin);   // (what the base moves by)
                                 alpha[q] = up ? (fresh ? 0.f : fast_exp2(-mx)) : 1.f;
                                 l_sum[q] *= alpha[q];
                                 if (up) m_base[q] = (fresh ? 0.f : m_base[q]) + mx;

@@ -103,3 +103,74 @@ def test_prefill_row_of_nan_scores_is_nan(dev, mode, Hq, Hkv):
     assert bool(torch.isnan(got[lost]).all())
     assert torch.equal(got[~lost], want[~lost])
     assert tqf.tq_get_status(ctx) == 0
+
+
+# A term of P.V is rounded to fp16: at most 2^-11 of itself, or, below 2^-14, 2^-25.  The
+# largest weight of a row over a tile whose largest V norm is nmax stands at 2^4 / nmax at
+# least (a subnormal nmax counts as 2^-15 in the packed prefill), so what the second adds
+# over n tokens is at most n 2^-25 nmax / 2^4, with V's vectors up to 1.2 times their norm.
+# And an output element below 2^-14 is rounded by up to 2^-25, so a row of them by up to
+# sqrt(128) 2^-25 in the 2-norm (row_bound's own absolute term, 2^-24, is for one).
+def tiny_terms(n, nmax, v_rescale):
+    return n * 2.0 ** -29 * max(nmax, 2.0 ** -15) * 1.2 * v_rescale + math.sqrt(128.0) * 2.0 ** -25
+
+
+SIZES = {
+    # the V norms of a cache: all small, down to the smallest; mixed from tile to tile; and
+    # from token to token (the largest of each tile decide)
+    "2^-11": lambda n, t: n * np.float16(2.0 ** -11),
+    "2^-17": lambda n, t: n * np.float16(2.0 ** -17),
+    "2^-21": lambda n, t: n * np.float16(2.0 ** -21),
+    "tiles": lambda n, t: n * (2.0 ** -(7.0 * ((t // 128) % 4))).astype(np.float16),
+    "rising": lambda n, t: n * (2.0 ** -(20.0 - 5 * (t // 128) % 25)).astype(np.float16),
+    "large": lambda n, t: n * np.where((t // 128) % 2 == 1, 1500.0, 2.0 ** -12).astype(np.float16),
+}
+
+
+@pytest.mark.parametrize("size", sorted(SIZES))
+@pytest.mark.parametrize("qs", [1.0, 8.0])
+@pytest.mark.parametrize("mode,Hq,Hkv,N", [("turbo4", 8, 2, 30), ("turbo3_asym", 28, 4, 33), ("turbo3", 32, 8, 40)])
+def test_tree_rows_over_norms_of_every_size(dev, mode, Hq, Hkv, N, qs, size):
+    L, cap, G = 700 + N, 752, Hq // Hkv
+    rec = [None if r is None else np.array(r) for r in H.random_cache(mode, 1, Hkv, cap, 17)]
+    rec[3] = SIZES[size](rec[3], np.arange(cap)).astype(np.float16)
+    nmax = float(rec[3][:, :, :L].max())
+    vr = float(2.0 ** round(-math.log2(nmax)))
+    cache = H.gpu_cache_from_records(mode, 1, Hkv, cap, [L], *rec, dev, v_rescale=vr)
+    q = wl.random_fp16(18, (1, Hq, N, 128), scale=qs)
+    qd, ctx = H.upload(q, dev), tqf.Context()
+    out = torch.empty_like(qd)
+    tqf.tq_tree_attention(ctx, cache, qd, out, chains(1, N, dev), L)
+    assert tqf.tq_get_status(ctx) == 0
+    got = out.float().cpu().numpy()
+    seen = np.tile(np.arange(L)[None, :] <= (L - N + np.arange(N))[:, None], (G, 1))
+    for h in range(Hkv):
+        K, V = S.kv_of(mode, rec, 0, h, L, v_rescale=vr)
+        want, bound = S.attention_rows(q[0, h * G:(h + 1) * G].reshape(-1, 128), K, V, seen, 1 / math.sqrt(128))
+        S.assert_rows(got[0, h * G:(h + 1) * G], want, bound + tiny_terms(L, nmax, vr), f"h{h}")
+
+
+@pytest.mark.parametrize("size", sorted(SIZES))
+@pytest.mark.parametrize("qs", [1.0, 8.0])
+@pytest.mark.parametrize("mode,Hq,Hkv", [("turbo4", 8, 2), ("turbo3_asym", 28, 4)])
+def test_prefill_rows_over_norms_of_every_size(dev, mode, Hq, Hkv, qs, size):
+    new, ctx_len, cap, G = [200, 61], [500, 0], 704, Hq // Hkv
+    L = [a + b for a, b in zip(new, ctx_len)]
+    rec = [None if r is None else np.array(r) for r in H.random_cache(mode, 2, Hkv, cap, 19)]
+    rec[3] = SIZES[size](rec[3], np.arange(cap)).astype(np.float16)
+    nmax = float(rec[3].max())
+    vr = float(2.0 ** round(-math.log2(nmax)))
+    cache = H.gpu_cache_from_records(mode, 2, Hkv, cap, L, *rec, dev, v_rescale=vr)
+    q = wl.random_fp16(20, (261, Hq, 128), scale=qs)
+    qd, ctx = H.upload(q, dev), tqf.Context()
+    out = torch.empty_like(qd)
+    tqf.tq_prefill_attention_packed(ctx, cache, qd, out, i32([0, 200, 261], dev), max(L))
+    assert tqf.tq_get_status(ctx) == 0
+    got, cu = out.float().cpu().numpy(), [0, 200, 261]
+    for b in range(2):
+        last = np.repeat(ctx_len[b] + np.arange(new[b]), G)
+        for h in range(Hkv):
+            K, V = S.kv_of(mode, rec, b, h, L[b], v_rescale=vr)
+            want, bound = S.attention_rows(q[cu[b]:cu[b + 1], h * G:(h + 1) * G].reshape(-1, 128), K, V,
+                                           np.arange(L[b])[None, :] <= last[:, None], 1 / math.sqrt(128))
+            S.assert_rows(got[cu[b]:cu[b + 1], h * G:(h + 1) * G], want, bound + tiny_terms(L[b], nmax, vr), f"b{b} h{h}")
