@@ -704,11 +704,11 @@ __global__ void __launch_bounds__(128, DecCfg<KB, VB, ROWS, TAB, RES>::kMinCtas)
                     if (!va) nv[tt][0] = 0.f;
                     if (!vb) nv[tt][1] = 0.f;
                     if (p.tree != nullptr) {
-                        // a V norm that overflowed (padding nodes of a tree may hold
-                        // anything) counts as 65504: 0 * inf would be NaN in the rows
+                        // an infinite or NaN V norm (padding nodes of a tree may hold
+                        // anything) counts as +-65504: 0 * inf would be NaN in the rows
                         // that do not see the token
-                        nv[tt][0] = fminf(nv[tt][0], 65504.f);
-                        nv[tt][1] = fminf(nv[tt][1], 65504.f);
+                        nv[tt][0] = fmaxf(fminf(nv[tt][0], 65504.f), -65504.f);
+                        nv[tt][1] = fmaxf(fminf(nv[tt][1], 65504.f), -65504.f);
                     }
                 }
             }

@@ -612,9 +612,9 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             const float nv =
                 in ? __half2float(reinterpret_cast<const __half*>(slot + C::kSK + C::kSKn + C::kSV)[r]) : 0.f;
             float* nvs = reinterpret_cast<float*>(smem + C::kNvOff);
-            nvs[frag_place(r)] = fminf(nv, 65504.f);
+            nvs[frag_place(r)] = fmaxf(fminf(nv, 65504.f), -65504.f);
             // the largest finite one (non-negative floats order like their bits)
-            const uint32_t top = __reduce_max_sync(0xffffffffu, nv < 65536.f ? __float_as_uint(nv) : 0u);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, fabsf(nv) < 65536.f ? __float_as_uint(fabsf(nv)) : 0u);
             if ((r & 31) == 0)
                 reinterpret_cast<__half*>(nvs + C::kTile)[r >> 5] = __float2half_rn(__uint_as_float(top));
             mbar_arrive(bar_sc);

@@ -428,12 +428,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     (reinterpret_cast<float*>(smem + C::kColOff) + u * kTok)[frag_place(r)] =
                         __half2float(nk) * p.scale_log2e;
                 const float x = __half2float(nv);
-                // (an overflowed norm counts as 65504: 0 * inf would be NaN in the
-                // rows that do not see the token; it does not count for the
+                // (an infinite or NaN norm counts as +-65504: 0 * inf would be NaN in
+                // the rows that do not see the token; it does not count for the
                 // slack, so the rows that do may overflow)
-                (reinterpret_cast<float*>(smem + C::kNvOff) + u * kTok)[frag_place(r)] = fminf(x, 65504.f);
+                (reinterpret_cast<float*>(smem + C::kNvOff) + u * kTok)[frag_place(r)] =
+                    fmaxf(fminf(x, 65504.f), -65504.f);
                 // (non-negative floats order like their bits)
-                const uint32_t nmax = __reduce_max_sync(0xffffffffu, x < 65536.f ? __float_as_uint(x) : 0u);
+                const uint32_t nmax = __reduce_max_sync(0xffffffffu, fabsf(x) < 65536.f ? __float_as_uint(fabsf(x)) : 0u);
                 if (lane == 0) (reinterpret_cast<uint32_t*>(smem + C::kNmOff) + 4 * u)[warp & 3] = nmax;
                 mbar_arrive(bar_n + 8 * u);
                 load_norms(n + 1);

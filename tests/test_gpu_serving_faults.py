@@ -174,3 +174,36 @@ def test_prefill_rows_over_norms_of_every_size(dev, mode, Hq, Hkv, qs, size):
             want, bound = S.attention_rows(q[cu[b]:cu[b + 1], h * G:(h + 1) * G].reshape(-1, 128), K, V,
                                            np.arange(L[b])[None, :] <= last[:, None], 1 / math.sqrt(128))
             S.assert_rows(got[cu[b]:cu[b + 1], h * G:(h + 1) * G], want, bound + tiny_terms(L[b], nmax, vr), f"b{b} h{h}")
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan"), -65504.0])
+@pytest.mark.parametrize("mode,Hq,Hkv,N", [("turbo4", 32, 8, 40), ("turbo4_asym", 28, 4, 33), ("turbo3", 8, 2, 6),
+                                           ("turbo3_asym", 4, 2, 7)])
+def test_tree_norms_of_unseen_tokens_may_be_anything(dev, mode, Hq, Hkv, N, value):
+    """The last three nodes are padding that nobody sees, whatever their norms hold:
+    every row is within its bound."""
+    L, cap, G = 140 + N, 208, Hq // Hkv
+    rec = [None if r is None else np.array(r) for r in H.random_cache(mode, 1, Hkv, cap, 27)]
+    cache = H.gpu_cache_from_records(mode, 1, Hkv, cap, [L], *rec, dev)
+    for t in (cache.k_norm, cache.v_norm):
+        if t is not None:
+            t[:, :, L - 3:L] = value
+    seen = np.zeros((N, L), bool)
+    seen[:, :L - N] = True
+    for j in range(N):
+        seen[j, L - N:min(L - N + j + 1, L - 3)] = True
+    words = np.zeros((1, N, (N + 31) // 32), np.uint32)
+    for j in range(N):
+        for i in np.flatnonzero(seen[j, L - N:]):
+            words[0, j, i >> 5] |= np.uint32(1 << (i & 31))
+    q = wl.random_fp16(28, (1, Hq, N, 128))
+    qd, ctx = H.upload(q, dev), tqf.Context()
+    out = torch.empty_like(qd)
+    tqf.tq_tree_attention(ctx, cache, qd, out, torch.from_numpy(words.view(np.int32)).to(dev), L)
+    assert tqf.tq_get_status(ctx) == 0
+    got = out.float().cpu().numpy()
+    for h in range(Hkv):
+        K, V = S.kv_of(mode, rec, 0, h, L)
+        want, bound = S.attention_rows(q[0, h * G:(h + 1) * G].reshape(-1, 128), K, V, np.tile(seen, (G, 1)),
+                                       1 / math.sqrt(128))
+        S.assert_rows(got[0, h * G:(h + 1) * G], want, bound, f"h{h}")
