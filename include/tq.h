@@ -28,7 +28,8 @@
  *     void*, NULL = legacy default stream) and never synchronize, except
  *     tq_get_status (its context's latest stream) and tq_get_kernel_time.
  *   - All tensor pointers are DEVICE pointers owned by the caller; the library
- *     never frees them.  The library owns only the context (workspace, status
+ *     never frees them.  Lists of 32-bit numbers (lengths, bounds, masks, places)
+ *     are 4-byte aligned, or the call is an invalid argument.  The library owns only the context (workspace, status
  *     word, cached tables), created lazily when *ctx == NULL and released by
  *     tq_free.  A context is bound to the device that was current when it was
  *     created.  Its workspace and counters serve one call at a time: calls on
@@ -249,10 +250,10 @@ int tq_prefill_attention_packed(tq_ctx **ctx, const tq_cache *cache, const void 
  * that its mask names.
  *   q, out:    fp16 [batch, num_q_heads, tq, 128] device pointers;
  *              1 <= tq <= TQ_MAX_TREE_NODES, at most 128 query heads per KV head.
- *   tree_mask: uint32 [mask_batch, tq, ceil(tq / 32)] device pointer, 4-byte
- *              aligned: bit i % 32 of word i / 32 of row j is set where node j
- *              attends to drafted token i (its ancestors and itself in a
- *              tree; any mask is allowed, bits at tq and above are ignored).
+ *   tree_mask: uint32 [mask_batch, tq, ceil(tq / 32)] device pointer: bit
+ *              i % 32 of word i / 32 of row j is set where node j attends to
+ *              drafted token i (its ancestors and itself in a tree; any mask is
+ *              allowed, bits at tq and above are ignored).
  *              Padding nodes have no bit set and see the context alone.
  *   mask_batch: 1 (one mask for all sequences) or batch.
  *   max_len_hint, scale: as in tq_decode_attention; tokens past the hint are

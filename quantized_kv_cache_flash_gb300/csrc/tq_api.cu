@@ -32,6 +32,9 @@ int cuda_err_code(cudaError_t e) { return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// A list of 32-bit numbers that a kernel may read (null is not one).
+bool list_ok(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // splitmix64 (Steele, Lea, Flood 2014; the finaliser of Vigna's splitmix64.c)
 uint64_t splitmix64_next(uint64_t& state) {
     state += 0x9E3779B97F4A7C15ull;
@@ -176,8 +179,7 @@ int check_cache(const tq_cache* c, int* kb, int* vb) {
     if (c->batch <= 0 || c->num_kv_heads <= 0 || c->capacity <= 0 || (c->capacity % 16) != 0)
         return TQ_ERR_INVALID_ARG;
     const bool table = tq::mode_table(c->mode);  // table records: no norm arrays
-    if (c->k_data == nullptr || c->v_data == nullptr || c->lengths == nullptr)
-        return TQ_ERR_INVALID_ARG;
+    if (c->k_data == nullptr || c->v_data == nullptr || !list_ok(c->lengths)) return TQ_ERR_INVALID_ARG;
     if (!table && (c->v_norm == nullptr || (*kb != 16 && c->k_norm == nullptr)))
         return TQ_ERR_INVALID_ARG;
     if (!aligned16(c->k_data) || !aligned16(c->v_data) || (c->v_norm && !aligned16(c->v_norm)) ||
@@ -397,6 +399,7 @@ int cuda_err(cudaError_t e) { return tq::host::cuda_err_code(e); }
 using tq::host::aligned16;
 using tq::host::build_tables;
 using tq::host::check_cache;
+using tq::host::list_ok;
 using tq::host::make_signs;
 
 // Zeroes a new context's words, done when this returns: on a stream of its own, since
@@ -669,7 +672,7 @@ int tq_encode_append_packed(tq_ctx** pctx, const tq_cache* c, const void* k_new,
     int kb, vb;
     int r = check_cache(c, &kb, &vb);
     if (r != TQ_OK) return r;
-    if (total < 0 || cu_seqlens == nullptr) return TQ_ERR_INVALID_ARG;
+    if (total < 0 || !list_ok(cu_seqlens)) return TQ_ERR_INVALID_ARG;
     if (total == 0) return TQ_OK;
     if (k_new == nullptr || v_new == nullptr || !aligned16(k_new) || !aligned16(v_new))
         return TQ_ERR_INVALID_ARG;
@@ -898,8 +901,7 @@ int tq_decode_attention_sparse_v(tq_ctx** pctx, const tq_cache* c, const void* q
 int tq_tree_attention(tq_ctx** pctx, const tq_cache* c, const void* q, int32_t num_q_heads, int32_t tq_rows,
                       int32_t max_len_hint, float scale, const uint32_t* tree_mask, int32_t mask_batch,
                       void* out, void* stream) {
-    if (c == nullptr || tree_mask == nullptr || (reinterpret_cast<uintptr_t>(tree_mask) & 3u) != 0)
-        return TQ_ERR_INVALID_ARG;
+    if (c == nullptr || !list_ok(tree_mask)) return TQ_ERR_INVALID_ARG;
     if (mask_batch != 1 && mask_batch != c->batch) return TQ_ERR_INVALID_ARG;
     if (tq_rows > TQ_MAX_TREE_NODES) return TQ_ERR_UNSUPPORTED;
     if (c->num_kv_heads > 0 && num_q_heads / c->num_kv_heads > tq::kMaxTreeGroup) return TQ_ERR_UNSUPPORTED;
@@ -952,7 +954,7 @@ int tq_prefill_attention_packed(tq_ctx** pctx, const tq_cache* c, const void* q,
     int kb, vb;
     int r = check_cache(c, &kb, &vb);
     if (r != TQ_OK) return r;
-    if (cu_seqlens == nullptr || total < 0) return TQ_ERR_INVALID_ARG;
+    if (!list_ok(cu_seqlens) || total < 0) return TQ_ERR_INVALID_ARG;
     if (total == 0) return TQ_OK;
     if ((r = check_prefill(c, q, num_q_heads, max_len_hint, scale, out, &kb, &vb)) != TQ_OK) return r;
     tq_ctx* ctx;
@@ -976,7 +978,7 @@ int tq_cache_compact(tq_ctx** pctx, const tq_cache* c, const int32_t* start, int
     int kb, vb;
     int r = check_cache(c, &kb, &vb);
     if (r != TQ_OK) return r;
-    if (start == nullptr || keep == nullptr || num_keep == nullptr) return TQ_ERR_INVALID_ARG;
+    if (!list_ok(start) || !list_ok(keep) || !list_ok(num_keep)) return TQ_ERR_INVALID_ARG;
     if (num_drafted <= 0 || max_keep <= 0 || max_keep > num_drafted) return TQ_ERR_INVALID_ARG;
     if (num_drafted > c->capacity) return TQ_ERR_CAPACITY;
     tq_ctx* ctx;
@@ -1019,7 +1021,8 @@ int tq_cache_copy(tq_ctx** pctx, const tq_cache* dst, const tq_cache* src, const
     if (std::memcmp(dst->codebook_v, src->codebook_v, sizeof(float) << vb) != 0) return TQ_ERR_INVALID_ARG;
     if (num_pairs < 0 || max_len_hint <= 0 || max_len_hint > src->capacity) return TQ_ERR_INVALID_ARG;
     if (num_pairs == 0) return TQ_OK;
-    if (dst_seq == nullptr || src_seq == nullptr) return TQ_ERR_INVALID_ARG;
+    if (!list_ok(dst_seq) || !list_ok(src_seq) || (num_tokens != nullptr && !list_ok(num_tokens)))
+        return TQ_ERR_INVALID_ARG;
     tq::CopyParams p{};
     record_bytes_of(src->mode, kb, vb, &p.rbk, &p.rbv);
     // one cache (every buffer the same), or two that share no memory

@@ -311,6 +311,8 @@ constexpr int kSMs = 152;  // GB300 (only used to size the split grids)
 
 int cuda_err_code(cudaError_t e);
 bool aligned16(const void* p);
+// Non-null and 4-byte aligned: a list of 32-bit numbers that a kernel reads.
+bool list_ok(const void* p);
 // Mode, shape, pointers and codebooks of a cache; *kb, *vb = its bits (16 = fp16 K).
 int check_cache(const tq_cache* c, int* kb, int* vb);
 // (Re)builds *t unless it already holds this codebook.
