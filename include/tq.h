@@ -294,9 +294,8 @@ int tq_tree_mask(const int32_t *parents, int32_t num_nodes, uint32_t *words);
  *               0 .. max_keep (0 takes the whole block back).
  * Record start[b] + keep[b][i] moves to start[b] + i for every KV head, and
  * lengths[b] = start[b] + num_keep[b].  Records move bit for bit; those past
- * the new length stay as they are.  A sequence whose start, count or places
- * are out of range or not ascending is left untouched and
- * TQ_STATUS_BAD_INDEX is raised.
+ * The lists must not lie in lengths, which the call writes (a start taken from
+ * there is copied first); they are an invalid argument then.
  */
 int tq_cache_compact(tq_ctx **ctx, const tq_cache *cache, const int32_t *start, int32_t num_drafted,
                      const int32_t *keep, const int32_t *num_keep, int32_t max_keep, void *stream);
@@ -320,7 +319,8 @@ int tq_cache_compact(tq_ctx **ctx, const tq_cache *cache, const int32_t *start, 
  * TQ_STATUS_BAD_INDEX; so is a pair whose destination is also another pair's
  * destination or, within one cache, another pair's source.  An n past the
  * destination's capacity or the hint skips the pair and raises
- * TQ_STATUS_CAPACITY.  num_pairs == 0 is a no-op.
+ * TQ_STATUS_CAPACITY.  num_pairs == 0 is a no-op.  The lists must not lie in the
+ * destination's lengths, which the call writes: they are an invalid argument then.
  */
 int tq_cache_copy(tq_ctx **ctx, const tq_cache *dst, const tq_cache *src, const int32_t *dst_seq,
                   const int32_t *src_seq, const int32_t *num_tokens, int32_t num_pairs,

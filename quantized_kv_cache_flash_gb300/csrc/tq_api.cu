@@ -467,6 +467,12 @@ int prepare_kmap(tq_ctx* ctx, const tq_cache* c) {
     return TQ_OK;
 }
 
+// Whether a list of n 32-bit numbers shares memory with a cache's lengths.
+bool in_lengths(const int32_t* list, long long n, const tq_cache* c) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(list), l = reinterpret_cast<uintptr_t>(c->lengths);
+    return list != nullptr && a < l + 4 * uintptr_t(c->batch) && l < a + 4 * uintptr_t(n);
+}
+
 // Bytes of a K and a V record of a mode.
 void record_bytes_of(int mode, int kb, int vb, int32_t* rbk, int32_t* rbv) {
     *rbk = tq::mode_table(mode) ? 64 : kb * 16;
@@ -980,6 +986,10 @@ int tq_cache_compact(tq_ctx** pctx, const tq_cache* c, const int32_t* start, int
     if (r != TQ_OK) return r;
     if (!list_ok(start) || !list_ok(keep) || !list_ok(num_keep)) return TQ_ERR_INVALID_ARG;
     if (num_drafted <= 0 || max_keep <= 0 || max_keep > num_drafted) return TQ_ERR_INVALID_ARG;
+    // (one CTA of a sequence writes its length while others still read the lists)
+    if (in_lengths(start, c->batch, c) || in_lengths(keep, 1ll * c->batch * max_keep, c) ||
+        in_lengths(num_keep, c->batch, c))
+        return TQ_ERR_INVALID_ARG;
     if (num_drafted > c->capacity) return TQ_ERR_CAPACITY;
     tq_ctx* ctx;
     if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
@@ -1022,6 +1032,9 @@ int tq_cache_copy(tq_ctx** pctx, const tq_cache* dst, const tq_cache* src, const
     if (num_pairs < 0 || max_len_hint <= 0 || max_len_hint > src->capacity) return TQ_ERR_INVALID_ARG;
     if (num_pairs == 0) return TQ_OK;
     if (!list_ok(dst_seq) || !list_ok(src_seq) || (num_tokens != nullptr && !list_ok(num_tokens)))
+        return TQ_ERR_INVALID_ARG;
+    if (in_lengths(dst_seq, num_pairs, dst) || in_lengths(src_seq, num_pairs, dst) ||
+        in_lengths(num_tokens, num_pairs, dst))   // (written while other CTAs read the lists)
         return TQ_ERR_INVALID_ARG;
     tq::CopyParams p{};
     record_bytes_of(src->mode, kb, vb, &p.rbk, &p.rbv);

@@ -40,3 +40,18 @@ def test_misaligned_lists(lib, off):
                     (lib.tq_cache_compact, (LIST, 8, LIST2, LIST3, 4))):
         assert call(f, _cache(lengths=lengths), *args) == bad
     assert call(lib.tq_cache_copy, far(lengths=far().lengths + off), _cache(), LIST, LIST2, None, 2, 64) == bad
+
+
+def test_lists_that_lie_in_the_lengths(lib):
+    """The lengths are written while other CTAs of the call still read the lists."""
+    bad = tqf.TQ_ERR_INVALID_ARG
+    c = _cache(batch=3)
+    at = c.lengths
+    for i in range(3):
+        for shared in (at, at + 8, at - 4):
+            a = [LIST, LIST2, LIST3]
+            a[i] = shared
+            assert call(lib.tq_cache_compact, _cache(batch=3), a[0], 8, a[1], a[2], 4) == bad
+            # within a cache, and from another one
+            assert call(lib.tq_cache_copy, _cache(batch=3), _cache(batch=3), a[0], a[1], a[2], 2, 64) == bad
+            assert call(lib.tq_cache_copy, _cache(batch=3), far(batch=3), a[0], a[1], a[2], 2, 64) == bad
