@@ -38,8 +38,9 @@
  *     contexts.
  *   - CUDA graphs: after one eager call on a context (which sizes its
  *     workspace), the calls can be captured and replayed (a workspace that a
- *     later, larger call replaces stays allocated until tq_free, so graphs
- *     captured with it stay good; two graphs of one context share it and must
+ *     later, larger call replaces then stays allocated until tq_free, so graphs
+ *     captured with it stay good: growing such a context takes up to four times
+ *     the largest call's workspace; two graphs of one context share it and must
  *     not overlap on the GPU); device-side counters and the status word reset
  *     themselves, tensor maps are built at capture, and the decode grid is
  *     fixed by the max_len_hint given at capture (it must cover the lengths

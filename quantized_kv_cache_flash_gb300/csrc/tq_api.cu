@@ -374,9 +374,10 @@ struct tq_ctx {
     uint32_t* d_words = nullptr;  // [0] status, [1] encode ticket counter, [2..3] sparse-V tiles, [4] encode tile counter
     float* d_work = nullptr;
     size_t work_bytes = 0;
-    // workspaces that a larger problem replaced: a CUDA graph captured with
-    // one of them still writes there, so they live until tq_free
+    // workspaces that a larger problem replaced after a call was captured: a
+    // CUDA graph may still write there, so they live until tq_free
     std::vector<float*> old_work;
+    bool captured = false;   // some call that uses the workspace was captured
     CodebookTables ktab, vtab;
     bool signs_valid = false;
     uint64_t seed = 0;
@@ -526,17 +527,40 @@ int timing_events(tq_ctx* ctx, cudaEvent_t* e0, cudaEvent_t* e1) {
     return TQ_OK;
 }
 
-int ensure_work(tq_ctx* ctx, size_t bytes) {
+// The workspace of a call of `bytes` on `stream`.  A context that no graph capture has used
+// frees the one it outgrows first (cudaFree waits for the calls in flight), so that it
+// holds what its largest call needs.  After a capture the graphs still write to theirs:
+// those live until tq_free, and growth is by doubling where there is room, so that the
+// replaced ones add up to less than the current one.
+int ensure_work(tq_ctx* ctx, size_t bytes, cudaStream_t stream) {
+    if (!ctx->captured) {
+        cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(stream, &st) != cudaSuccess) (void)cudaGetLastError();
+        else ctx->captured = st != cudaStreamCaptureStatusNone;
+    }
     if (ctx->work_bytes >= bytes) return TQ_OK;
-    // (doubled where there is room, so the replaced ones add up to less than
-    // the current one)
+    if (!ctx->captured) {
+        if (ctx->d_work) cudaFree(ctx->d_work);
+        ctx->d_work = nullptr;
+        ctx->work_bytes = 0;
+        if (cudaMalloc(&ctx->d_work, bytes) != cudaSuccess) {
+            (void)cudaGetLastError();
+            ctx->d_work = nullptr;
+            return TQ_ERR_NOMEM;
+        }
+        ctx->work_bytes = bytes;
+        return TQ_OK;
+    }
     const size_t twice = std::max(bytes, 2 * ctx->work_bytes);
     float* p = nullptr;
     if (cudaMalloc(&p, twice) == cudaSuccess) {
         bytes = twice;
     } else {
         (void)cudaGetLastError();
-        if (twice == bytes || cudaMalloc(&p, bytes) != cudaSuccess) return TQ_ERR_NOMEM;
+        if (twice == bytes || cudaMalloc(&p, bytes) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return TQ_ERR_NOMEM;
+        }
     }
     if (ctx->d_work) {
         try {
@@ -759,7 +783,7 @@ int tree_impl(tq_ctx** pctx, const tq_cache* c, const tq::host::DecodePlan& pl, 
     const int ctas = plan_tree_ctas(units, (max_len_hint + 127) / 128);
     const size_t rows = size_t(ctas + units) * 128;
     const size_t q_bytes = size_t(units) * (pl.kb == 16 ? 32768 : 65536);
-    if ((r = ensure_work(ctx, q_bytes + rows * (kD + 2) * sizeof(float))) != TQ_OK) return r;
+    if ((r = ensure_work(ctx, q_bytes + rows * (kD + 2) * sizeof(float), stream)) != TQ_OK) return r;
     cudaEvent_t e0 = nullptr, e1 = nullptr;
     if ((r = timing_events(ctx, &e0, &e1)) != TQ_OK) return r;
     ctx->last_stream = stream;
@@ -878,7 +902,7 @@ int decode_impl(tq_ctx** pctx, const tq_cache* c, const void* q, int32_t num_q_h
     if ((r = prepare_tables(ctx, c, pl.kb, pl.vb)) != TQ_OK) return r;
     if (pl.kb == 16 && (r = prepare_kmap(ctx, c)) != TQ_OK) return r;
     const size_t slots = tq::host::decode_slots(pl);
-    if ((r = ensure_work(ctx, slots * (kD + 2) * sizeof(float))) != TQ_OK) return r;
+    if ((r = ensure_work(ctx, slots * (kD + 2) * sizeof(float), static_cast<cudaStream_t>(stream))) != TQ_OK) return r;
     cudaEvent_t e0 = nullptr, e1 = nullptr;
     if ((r = timing_events(ctx, &e0, &e1)) != TQ_OK) return r;
     ctx->last_stream = static_cast<cudaStream_t>(stream);

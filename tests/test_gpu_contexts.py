@@ -50,3 +50,49 @@ def test_first_call_on_a_side_stream_while_the_default_stream_is_busy(dev, n):
     assert torch.equal(cache.v_data[0, 0, :n - 3], cache.v_data[0, 0, n - 3:2 * (n - 3)])
     assert tqf.tq_get_status(ctx) == tqf.TQ_STATUS_CAPACITY
     assert tqf.tq_get_status(ctx) == 0
+
+
+def tree_args(B, Hq, N, dev):
+    q = H.upload(wl.random_fp16(60 + N, (B, Hq, N, 128)), dev)
+    return q, torch.empty_like(q), tqf.tq_tree_mask([i - 1 for i in range(N)]).to(dev).unsqueeze(0)
+
+
+def taken(calls, cache, ctx):
+    """Device memory that a context's calls allocate."""
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    for q, out, mask in calls:
+        tqf.tq_tree_attention(ctx, cache, q, out, mask, 512)
+    torch.cuda.synchronize()
+    return before - torch.cuda.mem_get_info()[0]
+
+
+def test_a_growing_context_holds_its_largest_workspace_alone(dev):
+    """Calls of growing size, none captured: what the context holds in the end is what
+    its largest call takes on a context of its own."""
+    B, Hq, Hkv, cap = 8, 32, 8, 512
+    rec = H.random_cache("turbo4", B, Hkv, cap, 64)
+    cache = H.gpu_cache_from_records("turbo4", B, Hkv, cap, [cap] * B, *rec, dev)
+    calls = [tree_args(B, Hq, N, dev) for N in (40, 96, 160, 256)]
+    torch.cuda.empty_cache()
+    taken(calls[-1:], cache, tqf.Context())      # (loads the kernels)
+    grown, alone = tqf.Context(), tqf.Context()
+    held = taken(calls, cache, grown)
+    assert held > 50 << 20
+    want = [c[1].clone() for c in calls]
+    need = taken(calls[-1:], cache, alone)
+    assert held <= need + (4 << 20)              # (the allocator's 2 MB steps)
+    # the same with every call captured before the next grows: the graphs stay good
+    graphs, ctx = [], tqf.Context()
+    for q, out, mask in calls:
+        tqf.tq_tree_attention(ctx, cache, q, out, mask, cap)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tqf.tq_tree_attention(ctx, cache, q, out, mask, cap)
+        graphs.append(g)
+    for (_, out, _), g, w in zip(calls, graphs, want):
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, w)
+    assert tqf.tq_get_status(ctx) == 0
