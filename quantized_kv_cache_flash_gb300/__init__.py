@@ -345,6 +345,14 @@ def _tensor(name: str, t, dtype, shape, cache) -> None:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
 
 
+def _int32(name: str, x) -> int:
+    """x as the C call's 32-bit integer (ctypes would cut a larger one off)."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7FFFFFFF:
+        raise ValueError(f"{name} is past 32 bits: {x}")
+    return x
+
+
 def _launch_stream(cache, stream) -> int:
     """The stream handle of a call on this cache: the given one or the current
     one of the cache's device, which has to be the current device."""
@@ -382,7 +390,7 @@ def tq_prefill_attention_packed(ctx: Context, cache: Cache, q, out, cu_seqlens, 
     _tensor("cu_seqlens", cu_seqlens, _I32, (cache.batch + 1,), cache)
     _check(lib().tq_prefill_attention_packed(ctx.ref, cache.ref,
                                              _ptr(q), int(q.shape[1]), _ptr(cu_seqlens),
-                                             int(q.shape[0]), int(max_len_hint), float(scale),
+                                             int(q.shape[0]), _int32("max_len_hint", max_len_hint), float(scale),
                                              _ptr(out), _launch_stream(cache, stream)),
            "tq_prefill_attention_packed")
 
@@ -401,7 +409,7 @@ def tq_tree_attention(ctx: Context, cache: Cache, q, out, tree_mask, max_len_hin
     _tensor("tree_mask", tree_mask, _I32,
             (1 if per_seq == 1 else cache.batch, n, (n + 31) // 32), cache)
     _check(lib().tq_tree_attention(ctx.ref, cache.ref, q.data_ptr(),
-                                   hq, n, int(max_len_hint), float(scale),
+                                   hq, n, _int32("max_len_hint", max_len_hint), float(scale),
                                    tree_mask.data_ptr(), per_seq, out.data_ptr(),
                                    _launch_stream(cache, stream)), "tq_tree_attention")
 
@@ -429,7 +437,7 @@ def tq_cache_compact(ctx: Context, cache: Cache, start, keep, num_keep, num_draf
     _tensor("keep", keep, _I32, (cache.batch, keep.shape[1]), cache)
     _tensor("num_keep", num_keep, _I32, (cache.batch,), cache)
     _check(lib().tq_cache_compact(ctx.ref, cache.ref, start.data_ptr(),
-                                  int(num_drafted), keep.data_ptr(), num_keep.data_ptr(), keep.shape[1],
+                                  _int32("num_drafted", num_drafted), keep.data_ptr(), num_keep.data_ptr(), keep.shape[1],
                                   _launch_stream(cache, stream)), "tq_cache_compact")
 
 
@@ -446,7 +454,7 @@ def tq_cache_copy(ctx: Context, dst: Cache, src: Cache, dst_seq, src_seq, max_le
         raise ValueError("the two caches are on different devices")
     _check(lib().tq_cache_copy(ctx.ref, dst.ref,
                                src.ref, dst_seq.data_ptr(), src_seq.data_ptr(),
-                               _ptr(num_tokens), m, int(max_len_hint), _launch_stream(dst, stream)),
+                               _ptr(num_tokens), m, _int32("max_len_hint", max_len_hint), _launch_stream(dst, stream)),
            "tq_cache_copy")
 
 

@@ -55,3 +55,18 @@ def test_lists_that_lie_in_the_lengths(lib):
             # within a cache, and from another one
             assert call(lib.tq_cache_copy, _cache(batch=3), _cache(batch=3), a[0], a[1], a[2], 2, 64) == bad
             assert call(lib.tq_cache_copy, _cache(batch=3), far(batch=3), a[0], a[1], a[2], 2, 64) == bad
+
+
+@pytest.mark.parametrize("n", [1 << 31, (1 << 32) + 32, -(1 << 31) - 1])
+def test_numbers_past_32_bits(lib, n):
+    """The binding refuses what the C call's integers would cut off to another number."""
+    torch = pytest.importorskip("torch")
+    cache, ctx = tqf.Cache(tqf.MODES["turbo3"], 2, 2, 32, "cpu"), tqf.Context()
+    h = lambda *s: torch.zeros(*s, dtype=torch.float16)  # noqa: E731
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    for name, f in (("max_len_hint", lambda: tqf.tq_prefill_attention_packed(ctx, cache, h(5, 4, 128), h(5, 4, 128), i(3), n)),
+                    ("max_len_hint", lambda: tqf.tq_tree_attention(ctx, cache, h(2, 4, 3, 128), h(2, 4, 3, 128), i(1, 3, 1), n)),
+                    ("max_len_hint", lambda: tqf.tq_cache_copy(ctx, cache, cache, i(2), i(2), n)),
+                    ("num_drafted", lambda: tqf.tq_cache_compact(ctx, cache, i(2), i(2, 4), i(2), n))):
+        with pytest.raises(ValueError, match=name):
+            f()
