@@ -1057,9 +1057,6 @@ int tq_cache_copy(tq_ctx** pctx, const tq_cache* dst, const tq_cache* src, const
     if (num_pairs == 0) return TQ_OK;
     if (!list_ok(dst_seq) || !list_ok(src_seq) || (num_tokens != nullptr && !list_ok(num_tokens)))
         return TQ_ERR_INVALID_ARG;
-    if (in_lengths(dst_seq, num_pairs, dst) || in_lengths(src_seq, num_pairs, dst) ||
-        in_lengths(num_tokens, num_pairs, dst))   // (written while other CTAs read the lists)
-        return TQ_ERR_INVALID_ARG;
     tq::CopyParams p{};
     record_bytes_of(src->mode, kb, vb, &p.rbk, &p.rbv);
     // one cache (every buffer the same), or two that share no memory
@@ -1091,6 +1088,9 @@ int tq_cache_copy(tq_ctx** pctx, const tq_cache* dst, const tq_cache* src, const
     }
     if (1ll * num_pairs * src->num_kv_heads * ((max_len_hint + tq::kCopyTokens - 1) / tq::kCopyTokens) > 0x7fffffffll)
         return TQ_ERR_UNSUPPORTED;
+    if (in_lengths(dst_seq, num_pairs, dst) || in_lengths(src_seq, num_pairs, dst) ||
+        in_lengths(num_tokens, num_pairs, dst))   // (written while other CTAs read the lists)
+        return TQ_ERR_INVALID_ARG;
     tq_ctx* ctx;
     if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
     p.k_src = static_cast<const uint8_t*>(parts[0].s);
