@@ -96,3 +96,59 @@ def test_a_growing_context_holds_its_largest_workspace_alone(dev):
         torch.cuda.synchronize()
         assert torch.equal(out, w)
     assert tqf.tq_get_status(ctx) == 0
+
+
+def test_two_contexts_in_flight_on_two_streams(dev):
+    """Calls of two contexts, each on a stream and a cache of its own, issued in turn
+    without a wait between them: what each gives is what it gives alone."""
+    B, Hq, Hkv, cap, N = 3, 32, 8, 2560, 40
+    steps = 6
+
+    def state(seed):
+        rec = H.random_cache("turbo4", B, Hkv, cap, seed)
+        cache = H.gpu_cache_from_records("turbo4", B, Hkv, cap, [2000, 700, 64], *rec, dev)
+        k, v = (H.upload(wl.random_fp16(seed + i, (3 * N, Hkv, 128)), dev) for i in (1, 2))
+        q = H.upload(wl.random_fp16(seed + 3, (B, Hq, N, 128)), dev)
+        qp = H.upload(wl.random_fp16(seed + 4, (3 * N, Hq, 128)), dev)
+        return dict(cache=cache, ctx=tqf.Context(), k=k, v=v, q=q, qp=qp,
+                    cu=i32([0, N, 2 * N, 3 * N], dev), start=i32([2000, 700, 64], dev),
+                    keep=i32([[0, 5, 7, 20]] * 3, dev), count=i32([4, 2, 0], dev),
+                    mask=tqf.tq_tree_mask([i - 1 for i in range(N)]).to(dev).unsqueeze(0))
+
+    def step(s, stream, outs):
+        """One round of a speculative step: append, tree, prefill, keep, cut back."""
+        with torch.cuda.stream(stream):
+            s["cache"].lengths.copy_(s["start"])
+            tqf.tq_encode_append_packed(s["ctx"], s["cache"], s["k"], s["v"], s["cu"])
+            a, b = torch.empty_like(s["q"]), torch.empty_like(s["qp"])
+            tqf.tq_tree_attention(s["ctx"], s["cache"], s["q"], a, s["mask"], cap)
+            tqf.tq_prefill_attention_packed(s["ctx"], s["cache"], s["qp"], b, s["cu"], cap)
+            tqf.tq_cache_compact(s["ctx"], s["cache"], s["start"], s["keep"], s["count"], N)
+            d = torch.empty_like(s["q"][:, :, :1].contiguous())
+            tqf.tq_decode_attention(s["ctx"], s["cache"], s["q"][:, :, :1].contiguous(), d, cap)
+            outs.append((a, b, d, s["cache"].lengths.clone()))
+
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    want = []
+    for seed in (70, 80):
+        outs = []
+        s = state(seed)
+        torch.cuda.synchronize()
+        step(s, one, outs)
+        torch.cuda.synchronize()
+        want.append(outs[0])
+        assert tqf.tq_get_status(s["ctx"]) == 0
+    x, y = state(70), state(80)
+    torch.cuda.synchronize()
+    got = [], []
+    torch.cuda._sleep(20_000_000)   # (the first calls of both are queued when the GPU gets to them)
+    one.wait_stream(torch.cuda.current_stream())
+    two.wait_stream(torch.cuda.current_stream())
+    for _ in range(steps):
+        step(x, one, got[0])
+        step(y, two, got[1])
+    torch.cuda.synchronize()
+    for outs, w in zip(got, want):
+        for o in outs:
+            assert all(torch.equal(a, b) for a, b in zip(o, w))
+    assert tqf.tq_get_status(x["ctx"]) == 0 and tqf.tq_get_status(y["ctx"]) == 0
