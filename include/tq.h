@@ -29,13 +29,13 @@
  *     tq_get_status (its context's latest stream) and tq_get_kernel_time.
  *   - All tensor pointers are DEVICE pointers owned by the caller; the library
  *     never frees them.  Lists of 32-bit numbers (lengths, bounds, masks, places)
- *     are 4-byte aligned, or the call is an invalid argument.  The library owns only the context (workspace, status
- *     word, cached tables), created lazily when *ctx == NULL and released by
- *     tq_free.  A context is bound to the device that was current when it was
- *     created.  Its workspace and counters serve one call at a time: calls on
- *     one context that could overlap on the GPU (different streams without an
- *     ordering between them) must be ordered by the caller or use separate
- *     contexts.
+ *     are 4-byte aligned, or the call is an invalid argument.  The library owns
+ *     only the context (workspace, status word, cached tables), created lazily
+ *     when *ctx == NULL and released by tq_free.  A context is bound to the device
+ *     that was current when it was created.  Its workspace and counters serve one
+ *     call at a time: calls on one context that could overlap on the GPU
+ *     (different streams without an ordering between them) must be ordered by the
+ *     caller or use separate contexts.
  *   - CUDA graphs: after one eager call on a context (which sizes its
  *     workspace), the calls can be captured and replayed (a workspace that a
  *     later, larger call replaces then stays allocated until tq_free, so graphs

@@ -258,14 +258,16 @@ __device__ __forceinline__ int packed_added(const EncodeParams& p, int b, int L)
 
 // Packed appends decide every code from exact sums.  The rotated values and the
 // thresholds carry rounding errors; a vector with a value within their bound, k_near or
-// v_near times its norm n, of a threshold or 0 (a percent of Gaussian vectors) is encoded
-// once more from its exact transform: the sums of +-x are integers in units of 2^-24,
-// below 2^47, and the midpoints are taken in double.  So the codes do not depend on
-// which kernel or how many tokens took the vector (build_tables derives the bounds: a
-// vector without very small entries gets along with 1/2 to 1/3 of the general one, and
-// 29,800 tokens of 8 KV heads, 4 bits, take 87 us instead of 95).  What it costs: 20,480
-// tokens of 8 KV heads take 41.6 us with 3 bits and 60.0 with 4 (distances from every
-// threshold), tq_encode_append without it 30.3 and 41.6.
+// v_near times its norm n, of a threshold or 0 is encoded once more from its exact
+// transform: the sums of +-x are integers in units of 2^-24, below 2^47, and the midpoints
+// are taken in double.  So the codes do not depend on which kernel or how many tokens took
+// the vector.  build_tables derives the bounds; a vector without very small entries (four
+// Gaussian ones of five) gets along with less than half of the general one, and 4 in 1000
+// Gaussian vectors are encoded twice with 3 bits, 9 with 4 (29,800 tokens of 8 KV heads, 4
+// bits: 87 us, 95 with the general bound for all).  The distances from every threshold
+// make the rest of the cost: of 20,480 tokens of 8 KV heads 41.6 us with 3 bits and 60.0
+// with 4, where tq_encode_append without them takes 30.3 and 41.6.  The kernel is then
+// bound by the ALU pipe (0.69 of its cycles: minima, logic, shifts; issue 0.67).
 
 // Advance lengths[] after the last CTA of the launch has read it: one ticket
 // per CTA, taken once every thread of the CTA has read lengths[] for the last
