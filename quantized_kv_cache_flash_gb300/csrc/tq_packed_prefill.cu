@@ -29,9 +29,9 @@
 // 48 MMAs and the chain 1750 + 1700 + 900 cycles, with 250 of hand-overs between, in a
 // period of 4850; fp16 K: 32 MMAs, 1150 + 1700 + 900 in 3900.  Around the loop a CTA
 // takes some 18000 cycles for its item, Q' and the output.  Measured: 12 prompts of 64 to
-// 4096 tokens, turbo4, 32 / 8 heads, 436 us (613 TFLOP/s, q_lo's products not counted);
-// three chunks of 2047 to 8192 tokens behind up to 8191, fp16 K, 28 / 4 heads, 1622 us
-// (1.14 PFLOP/s); three prompts of 17 to 300 tokens 21 us.  With two groups of warps that
+// 4096 tokens, turbo4, 32 / 8 heads, 439 us (608 TFLOP/s, q_lo's products not counted);
+// three chunks of 2047 to 8192 tokens behind up to 8191, fp16 K, 28 / 4 heads, 1604 us
+// (1.15 PFLOP/s); three prompts of 17 to 300 tokens 21 us.  With two groups of warps that
 // dequantise and issue for themselves the same calls took 541, 2255 and 25 us: the
 // thread that issues stands still while the tensor core works (600 to 1500 cycles a
 // product), as does the one that starts the copies (1000 a tile).

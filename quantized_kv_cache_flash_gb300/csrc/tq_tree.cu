@@ -27,9 +27,9 @@
 // 1024 of MMA operands (K, V and P, so Q' lies in tensor memory), together nine tenths of
 // the time; the schedulers issue 65% of it, half on the ALU's byte permutes.  All kinds of
 // warp share the instruction caches, so loops are rolled where they can be.  Measured:
-// 64 nodes, 8 sequences of 4000 to 16384 tokens, turbo4, 32 / 8 heads, 142 us (666 TFLOP/s,
+// 64 nodes, 8 sequences of 4000 to 16384 tokens, turbo4, 32 / 8 heads, 143 us (661 TFLOP/s,
 // q_lo's products not counted); 33 nodes, three of 777 to 16351, fp16 K, 28 / 4 heads,
-// 35.5 us; 16 nodes, one of 8192, turbo3, 16.6 us.  P over S in tensor memory took 147 us
+// 36 us; 16 nodes, one of 8192, turbo3, 16.7 us.  P over S in tensor memory took 147 us
 // for the first, Q' in shared memory besides 149.
 //
 // Split: the (batch, kv head, row tile) units lie end to end as 128-token
