@@ -92,6 +92,7 @@ extern "C" {
 #define TQ_STATUS_PIPELINE_STALL  8u  /* a bounded in-kernel wait gave up; results are invalid */
 #define TQ_STATUS_BAD_INDEX      16u  /* a device-side list (sequence bounds, places, sequences) was out of
                                        * range or in conflict; what it named was left untouched */
+#define TQ_STATUS_BAD_VALUE      32u  /* a row of probabilities had no positive entry */
 
 typedef struct tq_ctx tq_ctx;
 
@@ -326,6 +327,106 @@ int tq_cache_compact(tq_ctx **ctx, const tq_cache *cache, const int32_t *start, 
 int tq_cache_copy(tq_ctx **ctx, const tq_cache *dst, const tq_cache *src, const int32_t *dst_seq,
                   const int32_t *src_seq, const int32_t *num_tokens, int32_t num_pairs,
                   int32_t max_len_hint, void *stream);
+
+/*
+ * The softmax weight that every cached token gets from a block of queries, added
+ * up over time: what an eviction goes by (tq_cache_evict).  For token t of sequence
+ * b and KV head h
+ *   A[b, h, t] = sum over the query heads of h and the tq queries of their softmax
+ *                weight on t (query j attends to tokens [0, lengths[b] - tq + j]),
+ *   weights[b, h, t] = (t < seen[b] ? decay * weights[b, h, t] : 0) + A[b, h, t].
+ *   q:       fp16 [batch, num_q_heads, tq, 128] device pointer; any tq >= 1: a decode
+ *            step's query, the last tokens of a prompt, or all of them.
+ *   weights: fp32 [batch, num_kv_heads, capacity] device pointer, 16-byte aligned.
+ *            Tokens at lengths[b] and above, or at max_len_hint and above, are left
+ *            as they were.
+ *   decay:   finite, >= 0: what remains of the weights so far (1: a plain sum).  With
+ *            0 they are not read.
+ *   seen:    int32 [batch] device pointer: the first tokens of each sequence that have
+ *            a weight already; the others start from 0 whatever their place holds.
+ *            NULL: all but the last tq (the block was appended for this call).
+ *   num_q_heads, max_len_hint, scale: as in tq_prefill_attention, and so are the
+ *            supported modes and codebooks and the group size.
+ * Scores are those of the attention calls.  A row that sees no token adds nothing and
+ * raises TQ_STATUS_SHORT_CONTEXT.  V is not read.  The sums run in fp32 in an order
+ * that depends on the call's shape alone: the same call gives the same bits.  The
+ * call uses the context's workspace like tq_decode_attention.
+ */
+int tq_attention_weights(tq_ctx **ctx, const tq_cache *cache, const void *q, int32_t num_q_heads,
+                         int32_t tq, int32_t max_len_hint, float scale, float decay,
+                         const int32_t *seen, float *weights, void *stream);
+
+/*
+ * Evict by weight: of sequence b's L = lengths[b] tokens, n = num_keep[b] stay for
+ * each KV head: the first `sinks`, the last `recent`, and of the others those of the
+ * largest weights (of equal ones the first; NaN counts as -infinity).  They keep their
+ * order and become tokens 0 .. n - 1; every KV head has tokens of its own.  L <= n
+ * keeps all.
+ *   dst, src:    the same cache (in place), or two as in tq_cache_copy, of one batch
+ *                (a prompt's cache pressed into a smaller one for the decode; src is
+ *                left as it was).  dst's lengths become min(L, n).
+ *   weights:     fp32 [batch, num_kv_heads, src capacity] device pointer.
+ *   new_weights: fp32 [batch, num_kv_heads, dst capacity] device pointer that takes
+ *                the kept tokens' weights, or NULL.  In place it may be `weights`
+ *                itself; it must not overlap it in another way.
+ *   num_keep:    int32 [batch] device pointer, sinks + recent .. max_keep where the
+ *                sequence is longer.
+ *   kept:        int32 [batch, num_kv_heads, max_keep] device pointer that takes the
+ *                places the kept tokens had, ascending; entries past min(L, n) are
+ *                left as they were.
+ *   sinks, recent: >= 0.
+ *   max_len_hint: an upper bound of every length, at most src's capacity.
+ * Records move bit for bit, in every mode.  A sequence with a count out of range (below 0,
+ * above max_keep, or below sinks + recent where tokens are to go) is left untouched and
+ * raises TQ_STATUS_BAD_INDEX; one longer than the hint, or whose kept tokens pass
+ * dst's capacity, is left untouched and raises TQ_STATUS_CAPACITY.  num_keep must not
+ * lie in dst's lengths, which the call writes, nor kept or new_weights in a cache's
+ * lengths: they are an invalid argument then.
+ */
+int tq_cache_evict(tq_ctx **ctx, const tq_cache *dst, const tq_cache *src, const float *weights,
+                   float *new_weights, const int32_t *num_keep, int32_t *kept, int32_t max_keep,
+                   int32_t sinks, int32_t recent, int32_t max_len_hint, void *stream);
+
+/*
+ * Verify drafted tokens: the path of a drafted tree that speculative sampling accepts
+ * under the target's probabilities, and the token that follows it.  Node 0 is the last
+ * settled token (always kept); the others were drafted after their parents.
+ *   tokens:   int32 [batch, num_nodes] device pointer; node 0's is not looked at.
+ *   parents:  int32 [parents_batch, num_nodes] device pointer, parents_batch 1 or batch:
+ *             the node that node i > 0 follows, 0 .. i - 1, or -1 for a padding node,
+ *             which is never tried.
+ *   target:   fp32 [batch, num_nodes, ld_target] device pointer: row i holds the
+ *             target's vocab probabilities of the token after node i, then padding.
+ *   draft:    fp32 [batch, num_nodes, ld_draft] device pointer: row i holds the
+ *             probabilities from which the children of node i were drawn,
+ *             independently; NULL where they were not drawn (looked up, or the most
+ *             probable ones): a child then counts as drawn with certainty.
+ *   uniforms: fp32 [batch, num_nodes] device pointer, numbers of [0, 1): entry i > 0
+ *             decides on node i, entry 0 draws the token that follows.
+ * From node 0 on, with p and q the rows at the path's end, r = p and Z = 1: its children
+ * in order, child c of token x is accepted (and is the path's end from there on) where
+ * u_c q(x) Z < r(x); otherwise r becomes max(r - Z q, 0) and Z its sum.  When no child
+ * is left the next token is the first whose running sum of r passes u_0 times the
+ * whole of it (r = p after all where nothing is left).  The accepted tokens and the
+ * next one are then distributed as the target's own samples.
+ *   keep:     int32 [batch, num_nodes] device pointer: the path's nodes, ascending,
+ *             then -1.  With the places of a drafted block as nodes, keep and num_keep
+ *             are tq_cache_compact's arguments (max_keep = num_nodes).
+ *   num_keep: int32 [batch] device pointer: 1 .. num_nodes.
+ *   next_token: int32 [batch] device pointer.
+ * Probabilities are taken to 2^-56 and added exactly, so no decision depends on the
+ * order of a sum.  What is not above 0 (NaN) counts as 0, what is above 1 as 1; a row
+ * whose sum passes 2^8 gives an unspecified next token (of the vocabulary).  A tried
+ * node with a parent or a token out of range counts as a padding node and raises
+ * TQ_STATUS_BAD_INDEX; a target's row without positive entries at the path's end gives
+ * token 0 and raises TQ_STATUS_BAD_VALUE.  num_nodes <= TQ_MAX_TREE_NODES, vocab <=
+ * 2^30, ld_target and ld_draft >= vocab; target and draft are 4-byte aligned (rows on
+ * 16-byte boundaries are read fastest).  The outputs must not overlap the inputs.
+ */
+int tq_verify_tree(tq_ctx **ctx, const int32_t *tokens, const int32_t *parents, int32_t parents_batch,
+                   const float *target, int64_t ld_target, const float *draft, int64_t ld_draft,
+                   const float *uniforms, int32_t batch, int32_t num_nodes, int32_t vocab, int32_t *keep,
+                   int32_t *num_keep, int32_t *next_token, void *stream);
 
 /*
  * Sparse-V decode: tq_decode_attention, except that a token whose softmax

@@ -42,6 +42,7 @@ TQ_STATUS_NORM_OVERFLOW = 2
 TQ_STATUS_SHORT_CONTEXT = 4
 TQ_STATUS_PIPELINE_STALL = 8
 TQ_STATUS_BAD_INDEX = 16
+TQ_STATUS_BAD_VALUE = 32
 
 TQ_MAX_TREE_NODES = 256
 
@@ -76,6 +77,16 @@ _SIGS = {
                                     _c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_void_p]),
     "tq_cache_copy": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.c_void_p, _c.c_void_p, _c.c_void_p,
                                  _c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_int32, _c.c_void_p]),
+    "tq_attention_weights": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.c_void_p, _c.c_void_p, _c.c_int32,
+                                        _c.c_int32, _c.c_int32, _c.c_float, _c.c_float, _c.c_void_p,
+                                        _c.c_void_p, _c.c_void_p]),
+    "tq_cache_evict": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                  _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_int32,
+                                  _c.c_int32, _c.c_int32, _c.c_void_p]),
+    "tq_verify_tree": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.c_void_p, _c.c_void_p, _c.c_int32,
+                                  _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_void_p,
+                                  _c.c_int32, _c.c_int32, _c.c_int32, _c.c_void_p, _c.c_void_p,
+                                  _c.c_void_p, _c.c_void_p]),
     "tq_selftest_bounded_wait": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.c_int32, _c.c_void_p]),
     "tq_free": (None, [_c.c_void_p]),
     "tq_get_status": (_c.c_int, [_c.c_void_p, _c.POINTER(_c.c_uint32)]),
@@ -147,13 +158,13 @@ def _ptr(t) -> Optional[int]:
 
 # What the calls on packed sequences, trees and moves need of torch, bound by the first
 # cache (an import statement and torch.cuda's wrappers take 0.5 us of a call's 5.7).
-_F16 = _I32 = _current_device = _current_stream = None
+_F16 = _F32 = _I32 = _current_device = _current_stream = None
 
 
 def _bind_torch() -> None:
-    global _F16, _I32, _current_device, _current_stream
+    global _F16, _F32, _I32, _current_device, _current_stream
     import torch
-    _F16, _I32 = torch.float16, torch.int32
+    _F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
     _current_device = getattr(torch._C, "_cuda_getDevice", None)
     _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -456,6 +467,95 @@ def tq_cache_copy(ctx: Context, dst: Cache, src: Cache, dst_seq, src_seq, max_le
                                src.ref, dst_seq.data_ptr(), src_seq.data_ptr(),
                                _ptr(num_tokens), m, _int32("max_len_hint", max_len_hint), _launch_stream(dst, stream)),
            "tq_cache_copy")
+
+
+def tq_attention_weights(ctx: Context, cache: Cache, q, weights, max_len_hint: int, decay: float = 1.0,
+                         seen=None, scale: float = 0.0, stream=None) -> None:
+    """weights fp32 [B, Hkv, capacity]: what the tokens below seen[b] (int32 [B] on the
+    device; None: all but the last Tq) have, times `decay`, plus the softmax weight
+    that every token gets from the queries q[B, Hq, Tq, 128] of its KV head."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, Tq, 128]")
+    _, hq, n, _ = q.shape
+    _tensor("q", q, _F16, (cache.batch, hq, n, 128), cache)
+    _tensor("weights", weights, _F32, (cache.batch, cache.num_kv_heads, cache.capacity), cache)
+    if seen is not None:
+        _tensor("seen", seen, _I32, (cache.batch,), cache)
+    _check(lib().tq_attention_weights(ctx.ref, cache.ref, q.data_ptr(), hq, n,
+                                      _int32("max_len_hint", max_len_hint), float(scale), float(decay),
+                                      _ptr(seen), weights.data_ptr(), _launch_stream(cache, stream)),
+           "tq_attention_weights")
+
+
+def tq_cache_evict(ctx: Context, dst: Cache, src: Cache, weights, num_keep, kept, max_len_hint: int,
+                   new_weights=None, sinks: int = 0, recent: int = 0, stream=None) -> None:
+    """Keep num_keep[b] tokens of every sequence of `src` for each KV head: the first
+    `sinks`, the last `recent` and the others of the largest weights (fp32 [B, Hkv,
+    src.capacity]).  They become the sequence in `dst`, which may be `src`; kept int32
+    [B, Hkv, max_keep] takes their places, new_weights (fp32 [B, Hkv, dst.capacity];
+    in place it may be `weights`) their weights."""
+    if kept.dim() != 3:
+        raise ValueError("kept must be [B, Hkv, max_keep]")
+    _tensor("weights", weights, _F32, (src.batch, src.num_kv_heads, src.capacity), src)
+    _tensor("num_keep", num_keep, _I32, (src.batch,), src)
+    _tensor("kept", kept, _I32, (src.batch, src.num_kv_heads, kept.shape[2]), src)
+    if new_weights is not None:
+        _tensor("new_weights", new_weights, _F32, (dst.batch, dst.num_kv_heads, dst.capacity), src)
+    if src.device != dst.device:
+        raise ValueError("the two caches are on different devices")
+    _check(lib().tq_cache_evict(ctx.ref, dst.ref, src.ref, weights.data_ptr(), _ptr(new_weights),
+                                num_keep.data_ptr(), kept.data_ptr(), kept.shape[2], _int32("sinks", sinks),
+                                _int32("recent", recent), _int32("max_len_hint", max_len_hint),
+                                _launch_stream(src, stream)), "tq_cache_evict")
+
+
+class _On:
+    """The device of a call that has no cache, as the checks ask a cache for it."""
+
+    def __init__(self, t):
+        if _F16 is None:
+            _bind_torch()
+        self.device, self.device_index = t.device, t.get_device()
+
+
+def _rows(name: str, t, shape, on) -> int:
+    """Elements from one row to the next of probabilities fp32 [B, N, V] on this
+    device, whose rows may have padding behind them."""
+    if t.dtype != _F32 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {_F32} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != on.device_index:
+        raise ValueError(f"{name} is on {t.device}, the target on {on.device}")
+    b, n, v = shape
+    step = t.stride(1) if n > 1 else t.stride(0) if b > 1 else v
+    if (v > 1 and t.stride(2) != 1) or step < v or (b > 1 and t.stride(0) != n * step):
+        raise ValueError(f"{name} must have rows of one distance, got strides {list(t.stride())}")
+    return step
+
+
+def tq_verify_tree(ctx: Context, tokens, parents, target, draft, uniforms, keep, num_keep, next_token,
+                   stream=None) -> None:
+    """The path of drafted trees that speculative sampling accepts, and the token that
+    follows it: tokens int32 [B, N] (node 0 is settled), parents int32 [1 or B, N],
+    target and draft (or None) fp32 [B, N, V] probabilities after each node, uniforms
+    fp32 [B, N]; into keep int32 [B, N] (nodes, then -1), num_keep and next_token
+    int32 [B]."""
+    if target.dim() != 3 or parents.dim() != 2:
+        raise ValueError("target must be [B, N, V] and parents [1 or B, N]")
+    on = _On(target)
+    shape = b, n, v = tuple(target.shape)
+    ld_t = _rows("target", target, shape, on)
+    ld_d = _rows("draft", draft, shape, on) if draft is not None else 0
+    per_seq = parents.shape[0]
+    _tensor("tokens", tokens, _I32, (b, n), on)
+    _tensor("parents", parents, _I32, (1 if per_seq == 1 else b, n), on)
+    _tensor("uniforms", uniforms, _F32, (b, n), on)
+    _tensor("keep", keep, _I32, (b, n), on)
+    _tensor("num_keep", num_keep, _I32, (b,), on)
+    _tensor("next_token", next_token, _I32, (b,), on)
+    _check(lib().tq_verify_tree(ctx.ref, tokens.data_ptr(), parents.data_ptr(), per_seq, target.data_ptr(),
+                                ld_t, _ptr(draft), ld_d, uniforms.data_ptr(), b, n, _int32("vocab", v),
+                                keep.data_ptr(), num_keep.data_ptr(), next_token.data_ptr(),
+                                _launch_stream(on, stream)), "tq_verify_tree")
 
 
 def tq_selftest_bounded_wait(ctx: Context, limit_us: int, stream=None) -> None:

@@ -480,6 +480,60 @@ void record_bytes_of(int mode, int kb, int vb, int32_t* rbk, int32_t* rbv) {
     *rbv = tq::mode_table(mode) ? 64 : vb * 16;
 }
 
+// The buffers of two caches of one format (or of one cache): K, V and their norms.
+struct CachePair {
+    struct Part {
+        const void *s, *d;    // null where the mode has none
+        size_t bytes;         // of a token
+    } parts[4];
+    int32_t rbk, rbv;
+    int32_t same;             // 1: one cache
+};
+
+// Two caches whose records mean the same.
+int check_formats(const tq_cache* dst, const tq_cache* src, int* kb, int* vb) {
+    int kb2, vb2;
+    int r = check_cache(src, kb, vb);
+    if (r != TQ_OK) return r;
+    if ((r = check_cache(dst, &kb2, &vb2)) != TQ_OK) return r;
+    if (dst->mode != src->mode || dst->num_kv_heads != src->num_kv_heads || dst->rot_seed != src->rot_seed ||
+        dst->v_rescale != src->v_rescale)
+        return TQ_ERR_INVALID_ARG;
+    if (*kb != 16 && std::memcmp(dst->codebook_k, src->codebook_k, sizeof(float) << *kb) != 0)
+        return TQ_ERR_INVALID_ARG;
+    if (std::memcmp(dst->codebook_v, src->codebook_v, sizeof(float) << *vb) != 0) return TQ_ERR_INVALID_ARG;
+    return TQ_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+// One cache (every buffer the same), or two that share no memory.
+int check_buffers(const tq_cache* dst, const tq_cache* src, int kb, int vb, CachePair* pair) {
+    record_bytes_of(src->mode, kb, vb, &pair->rbk, &pair->rbv);
+    pair->same = src->k_data == dst->k_data;
+    const bool table = tq::mode_table(src->mode), kn = !table && kb != 16;
+    const size_t rows_s = size_t(src->batch) * src->num_kv_heads * src->capacity;
+    const size_t rows_d = size_t(dst->batch) * dst->num_kv_heads * dst->capacity;
+    pair->parts[0] = {src->k_data, dst->k_data, size_t(pair->rbk)};
+    pair->parts[1] = {src->v_data, dst->v_data, size_t(pair->rbv)};
+    pair->parts[2] = {kn ? src->k_norm : nullptr, kn ? dst->k_norm : nullptr, 2};
+    pair->parts[3] = {table ? nullptr : src->v_norm, table ? nullptr : dst->v_norm, 2};
+    if (pair->same) {
+        if (src->batch != dst->batch || src->capacity != dst->capacity || src->lengths != dst->lengths)
+            return TQ_ERR_INVALID_ARG;
+        for (const auto& a : pair->parts)
+            if (a.s != a.d) return TQ_ERR_INVALID_ARG;
+        return TQ_OK;
+    }
+    for (const auto& a : pair->parts)
+        if (a.s != nullptr && overlap(a.s, rows_s * a.bytes, a.d, rows_d * a.bytes)) return TQ_ERR_INVALID_ARG;
+    return overlap(src->lengths, 4 * size_t(src->batch), dst->lengths, 4 * size_t(dst->batch)) ? TQ_ERR_INVALID_ARG
+                                                                                               : TQ_OK;
+}
+
 // An append's parameters but for the token counts.
 void fill_encode(tq_ctx* ctx, const tq_cache* c, const void* k_new, const void* v_new, int kb,
                  tq::EncodeParams* p) {
@@ -1042,50 +1096,20 @@ int tq_cache_compact(tq_ctx** pctx, const tq_cache* c, const int32_t* start, int
 int tq_cache_copy(tq_ctx** pctx, const tq_cache* dst, const tq_cache* src, const int32_t* dst_seq,
                   const int32_t* src_seq, const int32_t* num_tokens, int32_t num_pairs, int32_t max_len_hint,
                   void* stream) {
-    int kb, vb, kb2, vb2;
-    int r = check_cache(src, &kb, &vb);
+    int kb, vb;
+    int r = check_formats(dst, src, &kb, &vb);
     if (r != TQ_OK) return r;
-    if ((r = check_cache(dst, &kb2, &vb2)) != TQ_OK) return r;
-    // one format: the records mean the same in both caches
-    if (dst->mode != src->mode || dst->num_kv_heads != src->num_kv_heads || dst->rot_seed != src->rot_seed ||
-        dst->v_rescale != src->v_rescale)
-        return TQ_ERR_INVALID_ARG;
-    if (kb != 16 && std::memcmp(dst->codebook_k, src->codebook_k, sizeof(float) << kb) != 0)
-        return TQ_ERR_INVALID_ARG;
-    if (std::memcmp(dst->codebook_v, src->codebook_v, sizeof(float) << vb) != 0) return TQ_ERR_INVALID_ARG;
     if (num_pairs < 0 || max_len_hint <= 0 || max_len_hint > src->capacity) return TQ_ERR_INVALID_ARG;
     if (num_pairs == 0) return TQ_OK;
     if (!list_ok(dst_seq) || !list_ok(src_seq) || (num_tokens != nullptr && !list_ok(num_tokens)))
         return TQ_ERR_INVALID_ARG;
     tq::CopyParams p{};
-    record_bytes_of(src->mode, kb, vb, &p.rbk, &p.rbv);
-    // one cache (every buffer the same), or two that share no memory
-    p.same = src->k_data == dst->k_data;
-    const bool table = tq::mode_table(src->mode);
-    const size_t rows_s = size_t(src->batch) * src->num_kv_heads * src->capacity;
-    const size_t rows_d = size_t(dst->batch) * dst->num_kv_heads * dst->capacity;
-    struct Part {
-        const void *s, *d;
-        size_t bytes;
-    };
-    const Part parts[4] = {{src->k_data, dst->k_data, size_t(p.rbk)},
-                           {src->v_data, dst->v_data, size_t(p.rbv)},
-                           {table || kb == 16 ? nullptr : src->k_norm, table || kb == 16 ? nullptr : dst->k_norm, 2},
-                           {table ? nullptr : src->v_norm, table ? nullptr : dst->v_norm, 2}};
-    if (p.same) {
-        if (src->batch != dst->batch || src->capacity != dst->capacity || src->lengths != dst->lengths)
-            return TQ_ERR_INVALID_ARG;
-        for (const Part& a : parts)
-            if (a.s != a.d) return TQ_ERR_INVALID_ARG;
-    } else {
-        for (const Part& a : parts) {
-            if (a.s == nullptr) continue;
-            const uintptr_t s0 = reinterpret_cast<uintptr_t>(a.s), d0 = reinterpret_cast<uintptr_t>(a.d);
-            if (s0 < d0 + rows_d * a.bytes && d0 < s0 + rows_s * a.bytes) return TQ_ERR_INVALID_ARG;
-        }
-        const uintptr_t s0 = reinterpret_cast<uintptr_t>(src->lengths), d0 = reinterpret_cast<uintptr_t>(dst->lengths);
-        if (s0 < d0 + 4 * size_t(dst->batch) && d0 < s0 + 4 * size_t(src->batch)) return TQ_ERR_INVALID_ARG;
-    }
+    CachePair pair;
+    if ((r = check_buffers(dst, src, kb, vb, &pair)) != TQ_OK) return r;
+    p.rbk = pair.rbk;
+    p.rbv = pair.rbv;
+    p.same = pair.same;
+    const auto& parts = pair.parts;
     if (1ll * num_pairs * src->num_kv_heads * ((max_len_hint + tq::kCopyTokens - 1) / tq::kCopyTokens) > 0x7fffffffll)
         return TQ_ERR_UNSUPPORTED;
     if (in_lengths(dst_seq, num_pairs, dst) || in_lengths(src_seq, num_pairs, dst) ||
@@ -1116,6 +1140,168 @@ int tq_cache_copy(tq_ctx** pctx, const tq_cache* dst, const tq_cache* src, const
     p.max_len = max_len_hint;
     ctx->last_stream = static_cast<cudaStream_t>(stream);
     return cuda_err(static_cast<cudaError_t>(tq::launch_copy(p, static_cast<cudaStream_t>(stream))));
+}
+
+int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_t num_q_heads, int32_t tq_rows,
+                         int32_t max_len_hint, float scale, float decay, const int32_t* seen, float* weights,
+                         void* stream) {
+    int kb, vb;
+    int r = check_prefill(c, q, num_q_heads, max_len_hint, scale, weights, &kb, &vb);
+    if (r != TQ_OK) return r;
+    if (tq_rows <= 0 || tq_rows > max_len_hint) return TQ_ERR_INVALID_ARG;
+    if (seen != nullptr && !list_ok(seen)) return TQ_ERR_INVALID_ARG;
+    if (!(decay >= 0.f) || !std::isfinite(decay)) return TQ_ERR_INVALID_ARG;
+    tq::WeightsParams p{};
+    p.group = num_q_heads / c->num_kv_heads;
+    const long long rows = 1ll * p.group * tq_rows, units = 1ll * c->batch * c->num_kv_heads;
+    if (units * rows >= (1ll << 31) - 256) return TQ_ERR_UNSUPPORTED;
+    tq_ctx* ctx;
+    if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
+    if ((r = prepare_tables(ctx, c, kb, vb)) != TQ_OK) return r;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((r = ensure_work(ctx, size_t(units * rows) * (kD + 1) * sizeof(float), s)) != TQ_OK) return r;
+    p.k_codes = static_cast<const uint8_t*>(c->k_data);
+    p.k_norm = static_cast<const __half*>(c->k_norm);
+    p.lengths = c->lengths;
+    p.q = static_cast<const __half*>(q);
+    p.seen = seen;
+    p.weights = weights;
+    p.q_rot = ctx->d_work;
+    p.lse = ctx->d_work + size_t(units * rows) * kD;
+    p.status = ctx->d_words;
+    p.batch = c->batch;
+    p.hkv = c->num_kv_heads;
+    p.hq = num_q_heads;
+    p.tq = tq_rows;
+    p.rows = int32_t(rows);
+    p.cap = c->capacity;
+    p.max_len = max_len_hint;
+    const float sc = (scale == 0.f) ? 1.0f / std::sqrt(float(kD)) : scale;
+    p.scale_log2e = sc * 1.4426950408889634f;
+    p.decay = decay;
+    if (kb != 16) std::memcpy(p.ktab, ctx->ktab.tab, sizeof(p.ktab));
+    std::memcpy(p.signs, ctx->signs, sizeof(p.signs));
+    ctx->last_stream = s;
+    return cuda_err(static_cast<cudaError_t>(tq::launch_weights(kb, p, s)));
+}
+
+int tq_cache_evict(tq_ctx** pctx, const tq_cache* dst, const tq_cache* src, const float* weights,
+                   float* new_weights, const int32_t* num_keep, int32_t* kept, int32_t max_keep, int32_t sinks,
+                   int32_t recent, int32_t max_len_hint, void* stream) {
+    int kb, vb;
+    CachePair pair;
+    int r = check_formats(dst, src, &kb, &vb);
+    if (r != TQ_OK) return r;
+    if ((r = check_buffers(dst, src, kb, vb, &pair)) != TQ_OK) return r;
+    if (dst->batch != src->batch) return TQ_ERR_INVALID_ARG;
+    if (max_keep <= 0 || sinks < 0 || recent < 0 || sinks > max_keep || recent > max_keep - sinks)
+        return TQ_ERR_INVALID_ARG;
+    if (max_len_hint <= 0 || max_len_hint > src->capacity) return TQ_ERR_INVALID_ARG;
+    if (!list_ok(num_keep) || !list_ok(kept) || weights == nullptr || !aligned16(weights) ||
+        (new_weights != nullptr && !aligned16(new_weights)))
+        return TQ_ERR_INVALID_ARG;
+    const long long units = 1ll * src->batch * src->num_kv_heads;
+    if (units * tq::kEvictMoveCtas > 0x7fffffffll || units * max_keep >= (1ll << 31)) return TQ_ERR_UNSUPPORTED;
+    const size_t rows_s = size_t(units) * src->capacity, rows_d = size_t(units) * dst->capacity;
+    // what the call writes shares no memory with what it reads, but for the weights in place
+    if (in_lengths(num_keep, src->batch, dst) || in_lengths(kept, units * max_keep, dst) ||
+        in_lengths(kept, units * max_keep, src))
+        return TQ_ERR_INVALID_ARG;
+    if (overlap(kept, 4 * size_t(units) * max_keep, num_keep, 4 * size_t(src->batch)) ||
+        overlap(kept, 4 * size_t(units) * max_keep, weights, 4 * rows_s))
+        return TQ_ERR_INVALID_ARG;
+    if (new_weights != nullptr) {
+        if (in_lengths(reinterpret_cast<int32_t*>(new_weights), rows_d, dst) ||
+            in_lengths(reinterpret_cast<int32_t*>(new_weights), rows_d, src) ||
+            overlap(new_weights, 4 * rows_d, num_keep, 4 * size_t(src->batch)) ||
+            overlap(new_weights, 4 * rows_d, kept, 4 * size_t(units) * max_keep))
+            return TQ_ERR_INVALID_ARG;
+        if (!(pair.same && new_weights == weights) && overlap(new_weights, 4 * rows_d, weights, 4 * rows_s))
+            return TQ_ERR_INVALID_ARG;
+    }
+    tq_ctx* ctx;
+    if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((r = ensure_work(ctx, sizeof(int32_t) * size_t(src->batch), s)) != TQ_OK) return r;
+    tq::EvictParams p{};
+    p.k_src = static_cast<const uint8_t*>(pair.parts[0].s);
+    p.k_dst = static_cast<uint8_t*>(const_cast<void*>(pair.parts[0].d));
+    p.v_src = static_cast<const uint8_t*>(pair.parts[1].s);
+    p.v_dst = static_cast<uint8_t*>(const_cast<void*>(pair.parts[1].d));
+    p.kn_src = static_cast<const __half*>(pair.parts[2].s);
+    p.kn_dst = static_cast<__half*>(const_cast<void*>(pair.parts[2].d));
+    p.vn_src = static_cast<const __half*>(pair.parts[3].s);
+    p.vn_dst = static_cast<__half*>(const_cast<void*>(pair.parts[3].d));
+    p.src_lengths = src->lengths;
+    p.dst_lengths = dst->lengths;
+    p.weights = weights;
+    p.new_weights = new_weights;
+    p.num_keep = num_keep;
+    p.kept = kept;
+    p.counts = reinterpret_cast<int32_t*>(ctx->d_work);
+    p.status = ctx->d_words;
+    p.batch = src->batch;
+    p.hkv = src->num_kv_heads;
+    p.src_cap = src->capacity;
+    p.dst_cap = dst->capacity;
+    p.rbk = pair.rbk;
+    p.rbv = pair.rbv;
+    p.max_keep = max_keep;
+    p.max_len = max_len_hint;
+    p.sinks = sinks;
+    p.recent = recent;
+    p.same = pair.same;
+    ctx->last_stream = s;
+    return cuda_err(static_cast<cudaError_t>(tq::launch_evict(p, s)));
+}
+
+int tq_verify_tree(tq_ctx** pctx, const int32_t* tokens, const int32_t* parents, int32_t parents_batch,
+                   const float* target, int64_t ld_target, const float* draft, int64_t ld_draft,
+                   const float* uniforms, int32_t batch, int32_t num_nodes, int32_t vocab, int32_t* keep,
+                   int32_t* num_keep, int32_t* next_token, void* stream) {
+    if (batch <= 0 || num_nodes <= 0 || vocab <= 0) return TQ_ERR_INVALID_ARG;
+    if (parents_batch != 1 && parents_batch != batch) return TQ_ERR_INVALID_ARG;
+    if (num_nodes > TQ_MAX_TREE_NODES || vocab > (1 << 30) || batch > (1 << 24)) return TQ_ERR_UNSUPPORTED;
+    if (ld_target < vocab || (draft != nullptr && ld_draft < vocab)) return TQ_ERR_INVALID_ARG;
+    const long long rows = 1ll * batch * num_nodes;
+    // (byte offsets in 64 bits)
+    if (ld_target > (1ll << 60) / rows || (draft != nullptr && ld_draft > (1ll << 60) / rows)) return TQ_ERR_UNSUPPORTED;
+    if (!list_ok(tokens) || !list_ok(parents) || !list_ok(target) || !list_ok(uniforms) || !list_ok(keep) ||
+        !list_ok(num_keep) || !list_ok(next_token) || (draft != nullptr && !list_ok(draft)))
+        return TQ_ERR_INVALID_ARG;
+    const size_t n = size_t(batch), list = 4 * size_t(rows);
+    const struct { const void* at; size_t bytes; } in[] = {
+        {tokens, list}, {parents, 4 * size_t(parents_batch) * num_nodes}, {uniforms, list},
+        {target, 4 * (size_t(rows - 1) * size_t(ld_target) + vocab)},
+        {draft, draft != nullptr ? 4 * (size_t(rows - 1) * size_t(ld_draft) + vocab) : 0}},
+        out[] = {{keep, list}, {num_keep, 4 * n}, {next_token, 4 * n}};
+    for (int i = 0; i < 3; ++i) {
+        for (const auto& x : in)
+            if (x.bytes != 0 && overlap(out[i].at, out[i].bytes, x.at, x.bytes)) return TQ_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i].at, out[i].bytes, out[j].at, out[j].bytes)) return TQ_ERR_INVALID_ARG;
+    }
+    tq_ctx* ctx;
+    const int r = get_ctx(pctx, &ctx);
+    if (r != TQ_OK) return r;
+    tq::VerifyParams p{};
+    p.tokens = tokens;
+    p.parents = parents;
+    p.target = target;
+    p.draft = draft;
+    p.uniforms = uniforms;
+    p.keep = keep;
+    p.num_keep = num_keep;
+    p.next = next_token;
+    p.status = ctx->d_words;
+    p.ld_target = ld_target;
+    p.ld_draft = ld_draft;
+    p.batch = batch;
+    p.nodes = num_nodes;
+    p.vocab = vocab;
+    p.parents_per_seq = parents_batch == 1 ? 0 : num_nodes;
+    ctx->last_stream = static_cast<cudaStream_t>(stream);
+    return cuda_err(static_cast<cudaError_t>(tq::launch_verify(p, static_cast<cudaStream_t>(stream))));
 }
 
 int tq_selftest_bounded_wait(tq_ctx** pctx, int32_t limit_us, void* stream) {

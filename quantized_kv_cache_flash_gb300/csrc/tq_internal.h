@@ -177,6 +177,62 @@ struct CopyParams {
     int32_t same;             // 1: source and destination are one cache
 };
 
+// The softmax weights that tokens get (see tq_attention_weights).  A row of a (batch, KV
+// head) unit is query position * group + head of the group.
+struct WeightsParams {
+    const uint8_t* k_codes;   // packed K codes, or fp16 K rows
+    const __half* k_norm;
+    const int32_t* lengths;   // [B]
+    const __half* q;          // [B, Hq, Tq, 128]
+    const int32_t* seen;      // [B] tokens that have a weight already, or null: all but the last tq
+    float* weights;           // [B, Hkv, cap]
+    float* q_rot;             // workspace: rotated queries [units, rows, 128]
+    float* lse;               // workspace: log2 of each row's sum [units, rows]
+    uint32_t* status;
+    int32_t batch, hkv, hq, group, tq, rows, cap, max_len;
+    float scale_log2e, decay;
+    uint32_t ktab[4], signs[4];
+};
+
+// Eviction by weight (see tq_cache_evict).
+struct EvictParams {
+    const uint8_t* k_src;
+    const uint8_t* v_src;
+    const __half* kn_src;     // null where the mode has none
+    const __half* vn_src;
+    uint8_t* k_dst;
+    uint8_t* v_dst;
+    __half* kn_dst;
+    __half* vn_dst;
+    const int32_t* src_lengths;
+    int32_t* dst_lengths;
+    const float* weights;     // [B, Hkv, src_cap]
+    float* new_weights;       // [B, Hkv, dst_cap], or null
+    const int32_t* num_keep;  // [B]
+    int32_t* kept;            // [B, Hkv, max_keep]
+    int32_t* counts;          // workspace: tokens kept per sequence, -1 where it is left as it was
+    uint32_t* status;
+    int32_t batch, hkv, src_cap, dst_cap, rbk, rbv, max_keep, max_len, sinks, recent;
+    int32_t same;             // 1: in place
+    int32_t keys_held;        // keys per CTA in shared memory
+    int32_t move_ctas;        // CTAs per unit of the move to another cache
+};
+
+// Verification of drafted tokens (see tq_verify_tree).
+struct VerifyParams {
+    const int32_t* tokens;    // [B, N]
+    const int32_t* parents;   // [1 or B, N]
+    const float* target;      // [B, N] rows of ld_target floats
+    const float* draft;       // [B, N] rows of ld_draft floats, or null
+    const float* uniforms;    // [B, N]
+    int32_t* keep;            // [B, N]
+    int32_t* num_keep;        // [B]
+    int32_t* next;            // [B]
+    uint32_t* status;
+    int64_t ld_target, ld_draft;
+    int32_t batch, nodes, vocab, parents_per_seq;
+};
+
 // Division of 0 <= n < 2^31 by a constant d >= 1 as a multiply-high: with
 // l = ceil(log2 d), s = 31 + l and m = ceil(2^s / d) (below 2^32),
 // floor(n m / 2^s) = floor(n / d), because m d - 2^s < d <= 2^l and
@@ -216,6 +272,10 @@ int launch_compact(const CompactParams& p, cudaStream_t stream);
 // CTAs = pairs * hkv * ceil(max_len / kCopyTokens), below 2^31
 constexpr int kCopyTokens = 256;
 int launch_copy(const CopyParams& p, cudaStream_t stream);
+int launch_weights(int kbits, const WeightsParams& p, cudaStream_t stream);
+constexpr int kEvictMoveCtas = 8;   // of the cluster that moves a unit's records in place
+int launch_evict(EvictParams p, cudaStream_t stream);
+int launch_verify(const VerifyParams& p, cudaStream_t stream);
 int launch_selftest_stall(uint32_t* status, uint64_t limit_ns, cudaStream_t stream);
 
 // Query rows per row group for `rows` query rows of one KV head: 4 when K is
