@@ -879,6 +879,9 @@ int tree_impl(tq_ctx** pctx, const tq_cache* c, const tq::host::DecodePlan& pl, 
         tq::launch_tree(pl.kb, pl.vb, p, pl.kb == 16 ? &ctx->kmap : &dummy, stream, e0, e1)));
 }
 
+// Workspace that a tq_attention_weights call keeps to: more queries are taken in blocks.
+constexpr size_t kWeightsWork = size_t(512) << 20;
+
 // Arguments that both prefill calls take.
 int check_prefill(const tq_cache* c, const void* q, int32_t num_q_heads, int32_t max_len_hint, float scale,
                   const void* out, int* kb, int* vb) {
@@ -1154,20 +1157,36 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
     tq::WeightsParams p{};
     p.group = num_q_heads / c->num_kv_heads;
     const long long rows = 1ll * p.group * tq_rows, units = 1ll * c->batch * c->num_kv_heads;
-    if (units * rows >= (1ll << 31) - 256) return TQ_ERR_UNSUPPORTED;
+    if (rows >= (1ll << 31) - 256 || units > 65535) return TQ_ERR_UNSUPPORTED;
     tq_ctx* ctx;
     if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
     if ((r = prepare_tables(ctx, c, kb, vb)) != TQ_OK) return r;
+    if (kb == 16 && (r = prepare_kmap(ctx, c)) != TQ_OK) return r;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((r = ensure_work(ctx, size_t(units * rows) * (kD + 1) * sizeof(float), s)) != TQ_OK) return r;
+    // Pairs of query tiles in blocks whose workspace stays below kWeightsWork (64-bit
+    // rows * tokens otherwise); one pair needs no sums per pair.
+    const long long pairs = (rows + 255) / 256, tiles = (max_len_hint + 127) / 128;
+    const size_t q_pair = kb == 16 ? 65536 : 131072;
+    const size_t per_pair = size_t(units) * (q_pair + 256 * 12 + (pairs > 1 ? size_t(tiles) * 512 : 0));
+    const long long block = std::max<long long>(
+        1, std::min<long long>(pairs, std::min<long long>(kWeightsWork / per_pair, (1ll << 30) / (units * tiles))));
+    const int ctas = int(std::min<long long>(tq::host::kSMs, units * block * tiles));
+    if ((r = ensure_work(ctx, per_pair * block + size_t(ctas) * 2048, s)) != TQ_OK) return r;
     p.k_codes = static_cast<const uint8_t*>(c->k_data);
     p.k_norm = static_cast<const __half*>(c->k_norm);
     p.lengths = c->lengths;
     p.q = static_cast<const __half*>(q);
     p.seen = seen;
     p.weights = weights;
-    p.q_rot = ctx->d_work;
-    p.lse = ctx->d_work + size_t(units * rows) * kD;
+    uint8_t* work = reinterpret_cast<uint8_t*>(ctx->d_work);
+    p.q_tiles = work;
+    work += size_t(units) * block * q_pair;
+    p.part_ml = reinterpret_cast<float2*>(work);
+    work += (size_t(units) * block + ctas) * 2048;
+    p.lse = reinterpret_cast<float*>(work);
+    work += size_t(units) * block * 1024;
+    p.part_w = pairs > 1 ? reinterpret_cast<float*>(work) : nullptr;
+    p.part_len = int32_t(tiles * 128);
     p.status = ctx->d_words;
     p.batch = c->batch;
     p.hkv = c->num_kv_heads;
@@ -1176,13 +1195,22 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
     p.rows = int32_t(rows);
     p.cap = c->capacity;
     p.max_len = max_len_hint;
+    p.ctas = ctas;
     const float sc = (scale == 0.f) ? 1.0f / std::sqrt(float(kD)) : scale;
     p.scale_log2e = sc * 1.4426950408889634f;
     p.decay = decay;
     if (kb != 16) std::memcpy(p.ktab, ctx->ktab.tab, sizeof(p.ktab));
     std::memcpy(p.signs, ctx->signs, sizeof(p.signs));
+    CUtensorMap dummy;
+    std::memset(&dummy, 0, sizeof(dummy));
     ctx->last_stream = s;
-    return cuda_err(static_cast<cudaError_t>(tq::launch_weights(kb, p, s)));
+    for (long long q0 = 0; q0 < pairs; q0 += block) {
+        p.pair0 = int32_t(q0);
+        p.pairs = int32_t(std::min(block, pairs - q0));
+        const int e = tq::launch_weights(kb, p, kb == 16 ? &ctx->kmap : &dummy, s);
+        if (e != 0) return TQ_ERR_CUDA;
+    }
+    return TQ_OK;
 }
 
 int tq_cache_evict(tq_ctx** pctx, const tq_cache* dst, const tq_cache* src, const float* weights,

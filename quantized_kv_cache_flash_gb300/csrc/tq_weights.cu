@@ -1,7 +1,26 @@
 // The softmax weights that cached tokens get from a block of queries
-// (tq_attention_weights), the plain way: K tiles dequantised to fp32 in shared
-// memory, scores as fp32 sums, two passes over them (the rows' log-sum-exp, then the
-// tokens' sums).
+// (tq_attention_weights), on the 5th-generation tensor cores.
+//
+// Per (batch, KV head) unit the rows are query position * group + head of the group, a
+// pair of 128-row query tiles at a time.  A token's sum needs every row's normaliser, so
+// the scores are taken twice:
+//   stats  S[128 rows x 128 tok] = Q' . K^T     a thread a row: its maximum and sum of exp2
+//   lse    the partial sums of a row's tokens joined
+//   sum    S[128 tok x 128 rows] = K . Q'^T     a thread a token: sum of exp2(s - lse[row])
+// Both orientations read the same tiles (Q' and K are K-major either way), and neither
+// needs a value of another lane.  Q' = Rot(q) as q_hi + q_lo (quantized K, whose tile
+// holds the fp16 centroids, exact) or q (fp16 K); it is laid out once by a kernel before.
+//
+// The tiles of all (sequence, pair, KV head) units, laid end to end, are split evenly
+// over one CTA per SM; a CTA's run may end one unit and begin the next.  With several
+// pairs a token's sums are written per pair and added up by a last kernel, in the
+// pairs' order.
+//
+// Roles of a CTA's warps (hand-overs through mbarriers, every wait bounded):
+//   0-3, 4-7  stats: a query tile's rows each; sum: every second K tile's tokens each
+//   8-11      dequantise K (n) (quantized K)
+//   12        issues the MMAs     13  copies Q' and the records (fp16 K: the tiles)
+// Tensor memory: two buffers of 256 columns, S(n) of both query tiles.
 #include <algorithm>
 
 #include "tq_device.cuh"
@@ -9,161 +28,543 @@
 
 namespace tq {
 
-constexpr int kWtTok = 64, kWtRows = 16, kWtThreads = 128, kWtStride = kD + 1;
+constexpr int kWtTile = 128;
+constexpr int kWtThreads = 512;
 
-// Rot(q) (quantized K) or q as fp32 rows of the workspace; a warp a row.
-__global__ void __launch_bounds__(128) tq_weights_rows_kernel(const __grid_constant__ WeightsParams p, int quantized) {
+template <int KB>
+struct WtCfg {
+    static constexpr int kRbK = (KB == 0) ? 256 : KB * 16;
+    static constexpr int kSlots = (KB == 0) ? 4 : 2;            // K tiles
+    static constexpr int kQBytes = (KB == 0) ? 32768 : 65536;   // of a query tile: q_hi, q_lo
+    static constexpr int kQOff = 0;
+    static constexpr int kKOff = 2 * kQBytes;
+    static constexpr int kStgOff = kKOff + kSlots * 32768;      // records and norms [2]
+    static constexpr int kStg = (KB == 0) ? 0 : kWtTile * kRbK + 256;
+    static constexpr int kColOff = kStgOff + 2 * kStg;          // fp32 n_k * scale * log2(e) [2][128]
+    static constexpr int kLseOff = kColOff + 1024;              // fp32 [256]
+    // records copied [2], records read [2], K stored [kSlots], K read [kSlots], S done
+    // [2], S read [2], Q' copied; the TMEM slot
+    static constexpr int kBarOff = kLseOff + 1024;
+    static constexpr int kSmem = kBarOff + (9 + 2 * kSlots) * 8 + 8;
+    static constexpr int kSmemAlloc = kSmem + 768;              // to a 1024-byte boundary from a 256-byte one
+    static_assert(kSmemAlloc <= 232448, "227 KB per CTA");
+    static constexpr uint32_t kIdesc = umma_idesc_f16_f32(128, 128);
+};
+
+// A unit's part of a CTA's run: K tiles [k0, k1) of (sequence b, KV head h, pair).
+struct WtSeg {
+    int b, h, pair, k0, k1, L;
+};
+
+// K tiles that the rows of a pair see.
+__device__ __forceinline__ int wt_tiles(const WeightsParams& p, int L, int pair) {
+    const int r_hi = min(p.rows, 256 * (pair + 1)) - 1;
+    const int last = min(min(L, p.max_len) - 1, L - p.tq + r_hi / p.group);
+    return last < 0 ? 0 : last / kWtTile + 1;
+}
+
+// Sums over the (sequence, pair) groups, by a warp: the tiles of all of them over the
+// KV heads, and (want >= 0) of those before group `want`.
+__device__ __forceinline__ void wt_total(const WeightsParams& p, int lane, int want, int& all, int& before) {
+    const int groups = p.batch * p.pairs;
+    all = before = 0;
+    for (int g = lane; g < groups; g += 32) {
+        const int b = g / p.pairs;
+        const int n = p.hkv * wt_tiles(p, p.lengths[b], p.pair0 + g - b * p.pairs);
+        all += n;
+        if (g < want) before += n;
+    }
+    all = __reduce_add_sync(0xffffffffu, all);
+    before = __reduce_add_sync(0xffffffffu, before);
+}
+
+// A CTA's run [pos, hi) of the tiles, unit after unit; each warp keeps its own.
+struct WtRun {
+    int pos, hi;
+    int b, pair, h, tile, L, nt;
+
+    __device__ __forceinline__ void enter(const WeightsParams& p) {   // L and nt of (b, pair), past empty ones
+        for (; b < p.batch; pair = 0, ++b) {
+            L = p.lengths[b];
+            for (; pair < p.pairs; ++pair)
+                if ((nt = wt_tiles(p, L, p.pair0 + pair)) > 0) return;
+        }
+    }
+    __device__ __forceinline__ void start(const WeightsParams& p, int lane) {
+        int all, none;
+        wt_total(p, lane, -1, all, none);
+        const long long c = blockIdx.x;
+        pos = static_cast<int>(c * all / gridDim.x);
+        hi = static_cast<int>((c + 1) * all / gridDim.x);
+        b = pair = h = tile = L = nt = 0;
+        if (pos >= hi) return;
+        // the group that holds pos
+        const int groups = p.batch * p.pairs;
+        int cum = 0;
+        for (int g0 = 0; g0 < groups; g0 += 32) {
+            const int g = g0 + lane, bb = min(g / p.pairs, p.batch - 1);
+            const int n = g < groups ? p.hkv * wt_tiles(p, p.lengths[bb], p.pair0 + g - bb * p.pairs) : 0;
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, cum + inc > pos);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                const int local = pos - cum - __shfl_sync(0xffffffffu, inc - n, l);
+                b = (g0 + l) / p.pairs;
+                pair = g0 + l - b * p.pairs;
+                enter(p);
+                h = local / nt;
+                tile = local - h * nt;
+                return;
+            }
+            cum += __shfl_sync(0xffffffffu, inc, 31);
+        }
+    }
+    __device__ __forceinline__ bool next(const WeightsParams& p, WtSeg& s) {
+        if (pos >= hi) return false;
+        s = WtSeg{b, h, pair, tile, min(nt, tile + hi - pos), L};
+        pos += s.k1 - s.k0;
+        tile = 0;
+        if (++h == p.hkv) {
+            h = 0;
+            ++pair;
+            enter(p);
+        }
+        return true;
+    }
+};
+
+// Rot(q) as q_hi and q_lo (quantized K), or q, in the MMA layout; a warp a row.
+template <bool QUANT>
+__global__ void __launch_bounds__(256) tq_weights_rows_kernel(const __grid_constant__ WeightsParams p) {
     const int lane = threadIdx.x & 31;
-    const size_t row = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    const int per = p.pairs * 256;
+    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     griddep_wait();
-    if (row >= static_cast<size_t>(p.batch) * p.hkv * p.rows) return;
-    const int unit = static_cast<int>(row / p.rows), r = static_cast<int>(row % p.rows);
-    const int b = unit / p.hkv, h = unit % p.hkv, j = r / p.group, g = r % p.group;
-    const __half* q = p.q + ((static_cast<size_t>(b) * p.hq + h * p.group + g) * p.tq + j) * kD + 4 * lane;
-    float v[4];
-    for (int i = 0; i < 4; ++i) v[i] = __half2float(q[i]);
-    if (quantized) {
-        const uint32_t sn = sign_nibble(p.signs, lane);
-        for (int i = 0; i < 4; ++i) v[i] = ((sn >> i) & 1u) ? -v[i] : v[i];
-        wht128_lane4(v, lane);
-        for (int i = 0; i < 4; ++i) v[i] *= 0.08838834764831845f;
+    griddep_launch_dependents();
+    const int unit = static_cast<int>(row / per), rl = static_cast<int>(row - static_cast<long long>(unit) * per);
+    const int b = unit / p.hkv, h = unit - b * p.hkv, r = p.pair0 * 256 + rl;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r < p.rows) {
+        const int j = r / p.group, g = r - j * p.group;
+        const uint2 w = *reinterpret_cast<const uint2*>(
+            p.q + ((static_cast<size_t>(b) * p.hq + h * p.group + g) * p.tq + j) * kD + 4 * lane);
+        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+        v[0] = f0.x, v[1] = f0.y, v[2] = f1.x, v[3] = f1.y;
+        if constexpr (QUANT) {
+            const uint32_t sn = sign_nibble(p.signs, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = ((sn >> i) & 1u) ? -v[i] : v[i];
+            wht128_lane4(v, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] *= 0.08838834764831845f;   // 1/sqrt(128)
+        }
     }
-    *reinterpret_cast<float4*>(p.q_rot + row * kD + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
-    if (lane == 0 && min(p.lengths[b], p.max_len) - 1 < 0) atomicOr(p.status, kStatusShortContext);
-    else if (lane == 0 && p.lengths[b] - p.tq + j < 0) atomicOr(p.status, kStatusShortContext);
-}
-
-// A tile of 64 tokens from tok0 as fp32 levels (times the norm, and the softmax scale).
-template <int KB>
-__device__ void load_k(const WeightsParams& p, size_t row0, int tok0, int lim, float* sK) {
-    const Tables kt{p.ktab[0], p.ktab[1], p.ktab[2], p.ktab[3]};
-    for (int x = threadIdx.x; x < kWtTok * 4; x += kWtThreads) {
-        const int t = x >> 2, q = x & 3;
-        uint32_t hh[16];
-        float s = p.scale_log2e;
-        const bool in = tok0 + t < lim;
-        const size_t at = row0 + (in ? tok0 + t : 0);
-        if constexpr (KB == 0) {
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(p.k_codes + at * 256) + 16 * q;
-            for (int i = 0; i < 16; ++i) hh[i] = src[i];
-        } else {
-            dequant_q32<KB>(p.k_codes + at * (16 * KB) + q * 4 * KB, kt, hh);
-            s *= __half2float(p.k_norm[at]);
-        }
-        for (int i = 0; i < 16; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh[i]));
-            sK[t * kWtStride + 32 * q + 2 * i] = in ? f.x * s : 0.f;
-            sK[t * kWtStride + 32 * q + 2 * i + 1] = in ? f.y * s : 0.f;
-        }
+    uint8_t* tile = p.q_tiles + (static_cast<size_t>(unit) * (per / 128) + rl / 128) * (QUANT ? 65536 : 32768);
+    const uint2 hi = make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
+    *reinterpret_cast<uint2*>(tile + sw128_offset(rl & 127, 4 * lane)) = hi;
+    if constexpr (QUANT) {   // q_lo = Rot(q) - q_hi (exact in fp32), rounded once more
+        const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&hi.x));
+        const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&hi.y));
+        *reinterpret_cast<uint2*>(tile + 32768 + sw128_offset(rl & 127, 4 * lane)) =
+            make_uint2(pack_half2(v[0] - h0.x, v[1] - h0.y), pack_half2(v[2] - h1.x, v[3] - h1.y));
     }
 }
 
-template <int KB>
-__global__ void __launch_bounds__(kWtThreads) tq_weights_lse_kernel(const __grid_constant__ WeightsParams p) {
-    __shared__ float sK[kWtTok * kWtStride];
-    __shared__ float sQ[kWtRows * kD];
-    __shared__ float sM[kWtThreads], sL[kWtThreads];
+template <int KB, bool SUM>
+__global__ void __launch_bounds__(kWtThreads, 1)
+    tq_weights_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap kmap) {
+    using C = WtCfg<KB>;
+    constexpr int NS = C::kSlots;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    float* s_col = reinterpret_cast<float*>(smem + C::kColOff);
+    float* s_lse = reinterpret_cast<float*>(smem + C::kLseOff);
+    const uint32_t bar_stg = smem_u32(smem + C::kBarOff), bar_stgf = bar_stg + 16, bar_s = bar_stg + 32,
+                   bar_sf = bar_stg + 48, bar_q = bar_stg + 64, bar_k = bar_stg + 72, bar_kf = bar_k + 8 * NS;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (9 + 2 * NS) * 8);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_stg + 8 * i, 1);
+            mbar_init(bar_stgf + 8 * i, 128);
+            mbar_init(bar_s + 8 * i, 1);
+            mbar_init(bar_sf + 8 * i, SUM ? 128 : 256);
+        }
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(bar_k + 8 * i, KB == 0 ? 1 : 128);
+            mbar_init(bar_kf + 8 * i, 1);
+        }
+        mbar_init(bar_q, 1);
+        fence_barrier_init();
+    }
+    if (KB == 0 && tid == 0) prefetch_tensormap(&kmap);
     griddep_wait();
-    const int groups = (p.rows + kWtRows - 1) / kWtRows;
-    const int unit = static_cast<int>(blockIdx.x) / groups, r0 = (static_cast<int>(blockIdx.x) % groups) * kWtRows;
-    const int b = unit / p.hkv, tid = threadIdx.x;
-    const int L = p.lengths[b], lim = min(L, p.max_len);
-    const size_t qrow = static_cast<size_t>(unit) * p.rows;
-    for (int x = tid; x < kWtRows * kD; x += kWtThreads)
-        sQ[x] = r0 + x / kD < p.rows ? p.q_rot[(qrow + r0) * kD + x] : 0.f;
-    float m[8], l[8];
-    for (int i = 0; i < 8; ++i) m[i] = -INFINITY, l[i] = 0.f;
-    const int t = tid & 63, half = tid >> 6;
-    const int r_last = min(p.rows - 1, r0 + kWtRows - 1);
-    const int last = min(lim - 1, L - p.tq + r_last / p.group);
-    for (int tok0 = 0; tok0 <= last; tok0 += kWtTok) {
-        __syncthreads();
-        load_k<KB>(p, static_cast<size_t>(unit) * p.cap, tok0, lim, sK);
-        __syncthreads();
-        float s[8] = {};
-        for (int d = 0; d < kD; ++d)
-            for (int i = 0; i < 8; ++i) s[i] = fmaf(sK[t * kWtStride + d], sQ[(8 * half + i) * kD + d], s[i]);
-        for (int i = 0; i < 8; ++i) {
-            const int r = r0 + 8 * half + i;
-            if (tok0 + t < lim && tok0 + t <= L - p.tq + r / p.group) {
-                const float mn = s[i] > m[i] || s[i] != s[i] ? s[i] : m[i];
-                l[i] = (m[i] == -INFINITY ? 0.f : l[i] * fast_exp2(m[i] - mn)) + fast_exp2(s[i] - mn);
-                m[i] = mn;
+    griddep_launch_dependents();
+    WtRun run;
+    run.start(p, lane);
+    if (run.pos >= run.hi) return;   // (uniform over the CTA; nothing allocated yet)
+    if (warp == 0) tmem_alloc(smem_u32(tslot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+
+    bool stalled = false;  // once set, waits return at once and no MMA or copy is issued
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!stalled && !mbar_wait_bounded(bar, parity)) stalled = true;
+    };
+    int n = 0;             // K tiles so far, over the units
+    WtSeg s;
+    if (warp < 8) {
+        const int wg = warp >> 2, r = tid & 127;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        while (run.next(p, s)) {
+            const int lim = min(s.L, p.max_len);
+            const int row0 = (p.pair0 + s.pair) * 256;            // the pair's first row
+            const int unit = (s.b * p.pairs + s.pair) * p.hkv + s.h;
+            if constexpr (SUM) {
+                named_bar_sync(1, 256);   // (the unit before is done with its values)
+                s_lse[tid] = p.lse[static_cast<size_t>(unit) * 256 + tid];
+                named_bar_sync(1, 256);
+                const int nrows = min(256, p.rows - row0);
+                // tokens that every row of the pair sees
+                const int all_see = s.L - p.tq + row0 / p.group;
+                const int seen = p.seen != nullptr ? p.seen[s.b] : s.L - p.tq;
+                for (int k = s.k0; k < s.k1; ++k, ++n) {
+                    if ((n & 1) != wg) continue;
+                    wait(bar_s + 8 * wg, (n >> 1) & 1);
+                    tc_fence_after();
+                    const int t = k * kWtTile + r;
+                    const float c = KB == 0 ? p.scale_log2e : s_col[128 * wg + r];
+                    // rows [lo, nrows) see this token
+                    const long long lo = static_cast<long long>(t - (s.L - p.tq)) * p.group - row0;
+                    const bool masked = k * kWtTile + kWtTile - 1 > all_see;
+                    float w = 0.f;
+                    for (int x = 0; x < nrows; x += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(tmem + 256 * wg + x + lane_off, v);
+                        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+                        const float4* ls = reinterpret_cast<const float4*>(s_lse + x);
+                        if (masked || x + 32 > nrows) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 l = ls[e];
+                                const float y0 = fast_exp2(fmaf(__uint_as_float(v[4 * e]), c, -l.x));
+                                const float y1 = fast_exp2(fmaf(__uint_as_float(v[4 * e + 1]), c, -l.y));
+                                const float y2 = fast_exp2(fmaf(__uint_as_float(v[4 * e + 2]), c, -l.z));
+                                const float y3 = fast_exp2(fmaf(__uint_as_float(v[4 * e + 3]), c, -l.w));
+                                const int q = x + 4 * e;
+                                if (q >= lo && q < nrows) a0 += y0;
+                                if (q + 1 >= lo && q + 1 < nrows) a1 += y1;
+                                if (q + 2 >= lo && q + 2 < nrows) a2 += y2;
+                                if (q + 3 >= lo && q + 3 < nrows) a3 += y3;
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 l = ls[e];
+                                a0 += fast_exp2(fmaf(__uint_as_float(v[4 * e]), c, -l.x));
+                                a1 += fast_exp2(fmaf(__uint_as_float(v[4 * e + 1]), c, -l.y));
+                                a2 += fast_exp2(fmaf(__uint_as_float(v[4 * e + 2]), c, -l.z));
+                                a3 += fast_exp2(fmaf(__uint_as_float(v[4 * e + 3]), c, -l.w));
+                            }
+                        }
+                        w += (a0 + a1) + (a2 + a3);
+                    }
+                    tc_fence_before();
+                    mbar_arrive(bar_sf + 8 * wg);
+                    if (t < lim && !stalled) {
+                        if (p.part_w != nullptr) {
+                            p.part_w[(static_cast<size_t>(s.b * p.hkv + s.h) * p.pairs + s.pair) * p.part_len + t] = w;
+                        } else {
+                            float* out = p.weights + static_cast<size_t>(s.b * p.hkv + s.h) * p.cap + t;
+                            *out = (t < seen && p.decay != 0.f ? p.decay * *out : 0.f) + w;
+                        }
+                    }
+                }
+            } else {
+                // rows of query tile wg: last visible token of this row, and of all of them
+                const int first = row0 + 128 * wg, row = first + r;
+                const int mine = row < p.rows ? min(s.L - p.tq + row / p.group, lim - 1) : -1;
+                const int all_see = first + 127 < p.rows ? min(s.L - p.tq + first / p.group, lim - 1) : -1;
+                const bool any = first < p.rows;
+                float m = -INFINITY, l = 0.f;
+                for (int k = s.k0; k < s.k1; ++k, ++n) {
+                    const int buf = n & 1;
+                    wait(bar_s + 8 * buf, (n >> 1) & 1);
+                    tc_fence_after();
+                    if (any) {
+                        const bool masked = k * kWtTile + kWtTile - 1 > all_see;
+#pragma unroll 1
+                        for (int x = 0; x < 128; x += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(tmem + 256 * buf + 128 * wg + x + lane_off, v);
+                            const float4* col = reinterpret_cast<const float4*>(s_col + 128 * buf + x);
+                            float mx = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 c = KB == 0 ? make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e,
+                                                                       p.scale_log2e)
+                                                         : col[e];
+                                float y[4] = {__uint_as_float(v[4 * e]) * c.x, __uint_as_float(v[4 * e + 1]) * c.y,
+                                              __uint_as_float(v[4 * e + 2]) * c.z, __uint_as_float(v[4 * e + 3]) * c.w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    if (masked && k * kWtTile + x + 4 * e + i > mine) y[i] = -INFINITY;
+                                    mx = fmaxf(mx, y[i]);
+                                    v[4 * e + i] = __float_as_uint(y[i]);
+                                }
+                            }
+                            if (mx > m) {   // (m = -inf: l is 0)
+                                l *= m == -INFINITY ? 0.f : fast_exp2(m - mx);
+                                m = mx;
+                            }
+                            const float base = m == -INFINITY ? 0.f : m;
+                            float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) a[e & 3] += fast_exp2(__uint_as_float(v[e]) - base);
+                            l += (a[0] + a[1]) + (a[2] + a[3]);
+                        }
+                    }
+                    tc_fence_before();
+                    mbar_arrive(bar_sf + 8 * buf);
+                }
+                p.part_ml[(static_cast<size_t>(blockIdx.x) + unit) * 256 + 128 * wg + r] = make_float2(m, l);
+            }
+        }
+    } else if (warp < 12) {
+        if constexpr (KB != 0) {   // a token a thread
+            const int r = tid - 256;
+            const Tables kt{p.ktab[0], p.ktab[1], p.ktab[2], p.ktab[3]};
+            while (run.next(p, s)) {
+                const int lim = min(s.L, p.max_len);
+                for (int k = s.k0; k < s.k1; ++k, ++n) {
+                    const int buf = n & 1;
+                    const uint8_t* stg = smem + C::kStgOff + buf * C::kStg;
+                    uint8_t* sK = smem + C::kKOff + buf * 32768;
+                    wait(bar_stg + 8 * buf, (n >> 1) & 1);
+                    if (n >= 2) wait(bar_kf + 8 * buf, ((n >> 1) - 1) & 1);
+                    // the quarters in an order that differs between lanes whose records
+                    // start in the same banks
+                    const int turn = KB == 4 ? r >> 1 : r >> 3;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        const int side = (q + turn) & 3;
+                        uint32_t hh[16];
+                        dequant_q32<KB>(stg + r * C::kRbK + side * (C::kRbK / 4), kt, hh);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m)
+                            *reinterpret_cast<uint4*>(sK + sw128_offset(r, 32 * side + 8 * m)) =
+                                make_uint4(hh[4 * m], hh[4 * m + 1], hh[4 * m + 2], hh[4 * m + 3]);
+                    }
+                    const float nk = __half2float(reinterpret_cast<const __half*>(stg + kWtTile * C::kRbK)[r]);
+                    mbar_arrive(bar_stgf + 8 * buf);
+                    if (n >= 2) wait(bar_sf + 8 * buf, ((n >> 1) - 1) & 1);   // the scales of n - 2 are read
+                    s_col[128 * buf + r] = k * kWtTile + r < lim ? nk * p.scale_log2e : 0.f;
+                    fence_proxy_async();
+                    mbar_arrive(bar_k + 8 * buf);
+                }
+            }
+        }
+    } else if (warp == 12) {
+        const bool one = lane == 0;
+        int seg = 0, done = 0;
+        while (run.next(p, s)) {
+            if (!one) continue;
+            const int tiles = (p.pair0 + s.pair) * 256 + 128 < p.rows ? 2 : 1;   // query tiles with rows
+            wait(bar_q, seg++ & 1);
+            for (int k = s.k0; k < s.k1; ++k, ++n) {
+                const int buf = n & 1, slot = n & (NS - 1);
+                wait(bar_k + 8 * slot, (n / NS) & 1);
+                if (n >= 2) wait(bar_sf + 8 * buf, ((n >> 1) - 1) & 1);
+                if (stalled) break;
+                tc_fence_after();
+                const uint32_t kbase = smem_u32(smem + C::kKOff) + slot * 32768;
+#pragma unroll 1
+                for (int t = 0; t < tiles; ++t) {
+                    const uint32_t qbase = smem_u32(smem + C::kQOff) + t * C::kQBytes;
+                    const uint32_t d = tmem + 256 * buf + 128 * t;
+                    // q_lo first: the sums are cut at every step, the less the smaller they are
+#pragma unroll
+                    for (int part = KB == 0 ? 1 : 0; part < 2; ++part)
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint32_t koff = (kk >> 2) * 16384 + (kk & 3) * 32;
+                            const uint64_t qd = umma_desc_sw128(qbase + (part == 0 ? 32768 : 0) + koff);
+                            const uint64_t kd = umma_desc_sw128(kbase + koff);
+                            const uint32_t acc = kk > 0 || (KB != 0 && part == 1) ? 1u : 0u;
+                            if constexpr (SUM) umma_f16(d, kd, qd, C::kIdesc, acc);
+                            else umma_f16(d, qd, kd, C::kIdesc, acc);
+                        }
+                }
+                umma_commit(bar_s + 8 * buf);
+                umma_commit(bar_kf + 8 * slot);
+                ++done;
+            }
+            if (stalled) break;
+        }
+        // after a time-out: the MMAs in flight end before tensor memory is freed
+        if (one && stalled && done > 0)
+            (void)mbar_wait_bounded(bar_kf + 8 * ((done - 1) & (NS - 1)), ((done - 1) / NS) & 1);
+        __syncwarp();
+    } else if (warp == 13) {
+        const bool one = lane == 0;
+        int seg = 0, begun = 0;   // tiles whose copies were issued
+        bool q_open = false;
+        while (run.next(p, s)) {
+            if (!one) continue;
+            const int lim = min(s.L, p.max_len);
+            const size_t row0 = static_cast<size_t>(s.b * p.hkv + s.h) * p.cap;
+            const int unit_q = s.b * p.hkv + s.h;
+            const int tiles = (p.pair0 + s.pair) * 256 + 128 < p.rows ? 2 : 1;
+            // Q' once the last MMAs of the unit before have read theirs (phase after phase:
+            // with quantized K the copies may be two tiles of a slot ahead)
+            if (KB != 0 && n > 2) wait(bar_kf + 8 * ((n - 3) & (NS - 1)), ((n - 3) / NS) & 1);
+            if (n > 0) wait(bar_kf + 8 * ((n - 1) & (NS - 1)), ((n - 1) / NS) & 1);
+            if (stalled) break;
+            mbar_arrive_expect_tx(bar_q, tiles * C::kQBytes);
+            for (int t = 0; t < tiles; ++t)
+                bulk_g2s(smem_u32(smem + C::kQOff) + t * C::kQBytes,
+                         p.q_tiles + ((static_cast<size_t>(unit_q) * p.pairs + s.pair) * 2 + t) * C::kQBytes, C::kQBytes,
+                         bar_q);
+            ++seg;
+            q_open = true;
+            for (int k = s.k0; k < s.k1; ++k, ++n) {
+                const int tok0 = k * kWtTile;
+                if constexpr (KB == 0) {
+                    const int slot = n & (NS - 1);
+                    if (n >= NS) wait(bar_kf + 8 * slot, (n / NS - 1) & 1);
+                    if (stalled) break;
+                    mbar_arrive_expect_tx(bar_k + 8 * slot, 32768);
+                    // (rows past the tensor's end are zero-filled; masked later)
+                    for (int half = 0; half < 2; ++half)
+                        for (int rb = 0; rb < 4; ++rb)
+                            tma_g2s_2d(smem_u32(smem + C::kKOff) + slot * 32768 + half * 16384 + rb * 4096, &kmap,
+                                       half * 64, static_cast<int32_t>(row0 + tok0 + rb * 32), bar_k + 8 * slot);
+                } else {
+                    const int buf = n & 1;
+                    if (n >= 2) wait(bar_stgf + 8 * buf, ((n >> 1) - 1) & 1);
+                    if (stalled) break;
+                    const int nval = min(kWtTile, lim - tok0);
+                    const uint32_t nb = static_cast<uint32_t>((nval + 7) & ~7) * 2;
+                    const uint32_t dst = smem_u32(smem + C::kStgOff) + buf * C::kStg;
+                    mbar_arrive_expect_tx(bar_stg + 8 * buf, nval * C::kRbK + nb);
+                    bulk_g2s(dst, p.k_codes + (row0 + tok0) * C::kRbK, nval * C::kRbK, bar_stg + 8 * buf);
+                    bulk_g2s(dst + kWtTile * C::kRbK, p.k_norm + row0 + tok0, nb, bar_stg + 8 * buf);
+                }
+                ++begun;
+            }
+            if (stalled) break;
+        }
+        // (after a time-out: the copies in flight land before shared memory goes away)
+        if (one && stalled) {
+            if (q_open) (void)mbar_wait_bounded(bar_q, (seg - 1) & 1);
+            constexpr int ring = KB == 0 ? NS : 2;
+            for (int x = max(begun - ring, 0); x < begun; ++x)
+                (void)mbar_wait_bounded((KB == 0 ? bar_k : bar_stg) + 8 * (x % ring), (x / ring) & 1);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    if (__syncthreads_or(stalled) && tid == 0) atomicOr(p.status, kStatusPipelineStall);
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// A row's partial sums joined: lse = log2 of its sum of exp2(score); a CTA per (sequence,
+// pair, KV head), a thread a row.  Rows that see no token: +inf.
+__global__ void __launch_bounds__(256) tq_weights_lse_kernel(const __grid_constant__ WeightsParams p) {
+    __shared__ int s_all, s_before;
+    const int tid = threadIdx.x;
+    const int unit = static_cast<int>(blockIdx.x);
+    const int group = unit / p.hkv, h = unit - group * p.hkv;
+    const int b = group / p.pairs, pair = group - b * p.pairs;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (tid < 32) {
+        int all, before;
+        wt_total(p, tid, group, all, before);
+        if (tid == 0) {
+            s_all = all;
+            s_before = before;
+        }
+    }
+    __syncthreads();
+    const int nt = wt_tiles(p, p.lengths[b], p.pair0 + pair);
+    float M = -INFINITY, sum = 0.f;
+    if (nt > 0) {
+        const long long all = s_all, P = p.ctas, k0 = s_before + static_cast<long long>(h) * nt;
+        // the CTAs whose runs meet tiles [k0, k0 + nt)
+        const int c0 = static_cast<int>(((k0 + 1) * P - 1) / all), c1 = static_cast<int>(((k0 + nt) * P - 1) / all);
+        const float2* ml = p.part_ml + static_cast<size_t>(unit) * 256 + tid;
+        for (int c = c0; c <= c1; ++c) {
+            if (c * all / P >= (c + 1) * all / P) continue;   // (an empty run wrote nothing)
+            const float2 x = __ldcg(ml + static_cast<size_t>(c) * 256);
+            const float mn = fmaxf(M, x.x);
+            if (x.x != -INFINITY || x.y != 0.f) {
+                sum = (M == -INFINITY ? sum : sum * fast_exp2(M - mn)) +
+                      (x.x == -INFINITY ? x.y : x.y * fast_exp2(x.x - mn));
+                M = mn;
             }
         }
     }
-    for (int i = 0; i < 8; ++i) {
-        __syncthreads();
-        sM[tid] = m[i];
-        sL[tid] = l[i];
-        __syncthreads();
-        if (t == 0 && r0 + 8 * half + i < p.rows) {
-            float M = -INFINITY, S = 0.f;
-            for (int k = 0; k < 64; ++k) M = fmaxf(M, sM[tid + k]);
-            for (int k = 0; k < 64; ++k)
-                if (sM[tid + k] != -INFINITY) S += sL[tid + k] * fast_exp2(sM[tid + k] - M);
-            p.lse[qrow + r0 + 8 * half + i] = M == -INFINITY && S == 0.f ? INFINITY : M + log2f(S);
-        }
-    }
+    const bool none = M == -INFINITY && sum == 0.f;   // (a NaN sum is a row of NaN scores)
+    p.lse[static_cast<size_t>(unit) * 256 + tid] = none ? INFINITY : M + log2f(sum);
+    if (none && (p.pair0 + pair) * 256 + tid < p.rows) atomicOr(p.status, kStatusShortContext);
 }
 
-template <int KB>
-__global__ void __launch_bounds__(kWtThreads) tq_weights_sum_kernel(const __grid_constant__ WeightsParams p) {
-    __shared__ float sK[kWtTok * kWtStride];
-    __shared__ float sQ[kWtRows * kD];
-    __shared__ float sW[kWtThreads], sLse[kWtRows];
+// A token's sums over the pairs that see it, added to its weight.
+__global__ void __launch_bounds__(256) tq_weights_add_kernel(const __grid_constant__ WeightsParams p) {
+    const int per = (p.max_len + 255) / 256;
+    const int unit = static_cast<int>(blockIdx.x) / per, t = (static_cast<int>(blockIdx.x) - unit * per) * 256 + threadIdx.x;
     griddep_wait();
-    const int tiles = (p.max_len + kWtTok - 1) / kWtTok;
-    const int unit = static_cast<int>(blockIdx.x) / tiles, tok0 = (static_cast<int>(blockIdx.x) % tiles) * kWtTok;
-    const int b = unit / p.hkv, tid = threadIdx.x;
-    const int L = p.lengths[b], lim = min(L, p.max_len);
-    if (tok0 >= lim) return;
-    const size_t qrow = static_cast<size_t>(unit) * p.rows;
-    load_k<KB>(p, static_cast<size_t>(unit) * p.cap, tok0, lim, sK);
-    const int t = tid & 63, half = tid >> 6;
-    float a = 0.f;
-    for (int r0 = 0; r0 < p.rows; r0 += kWtRows) {
-        __syncthreads();
-        for (int x = tid; x < kWtRows * kD; x += kWtThreads)
-            sQ[x] = r0 + x / kD < p.rows ? p.q_rot[(qrow + r0) * kD + x] : 0.f;
-        if (tid < kWtRows) sLse[tid] = r0 + tid < p.rows ? p.lse[qrow + r0 + tid] : INFINITY;
-        __syncthreads();
-        float s[8] = {};
-        for (int d = 0; d < kD; ++d)
-            for (int i = 0; i < 8; ++i) s[i] = fmaf(sK[t * kWtStride + d], sQ[(8 * half + i) * kD + d], s[i]);
-        for (int i = 0; i < 8; ++i) {
-            const int r = r0 + 8 * half + i;
-            if (r < p.rows && tok0 + t <= L - p.tq + r / p.group) a += fast_exp2(s[i] - sLse[8 * half + i]);
-        }
-    }
-    sW[tid] = a;
-    __syncthreads();
-    if (tid < kWtTok && tok0 + tid < lim) {
-        const int seen = p.seen != nullptr ? p.seen[b] : L - p.tq;
-        float* w = p.weights + static_cast<size_t>(unit) * p.cap + tok0 + tid;
-        const float old = tok0 + tid < seen && p.decay != 0.f ? p.decay * *w : 0.f;
-        *w = old + (sW[tid] + sW[tid + 64]);
-    }
+    griddep_launch_dependents();
+    const int b = unit / p.hkv, L = p.lengths[b];
+    if (t >= min(L, p.max_len)) return;
+    const int seen = p.seen != nullptr ? p.seen[b] : L - p.tq;
+    float* out = p.weights + static_cast<size_t>(unit) * p.cap + t;
+    const float* part = p.part_w + static_cast<size_t>(unit) * p.pairs * p.part_len + t;
+    // the first row that sees the token, and its pair
+    const long long row = max(0ll, static_cast<long long>(t - (L - p.tq)) * p.group);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int q = max(0, static_cast<int>(row / 256) - p.pair0); q < p.pairs; ++q)
+        sum += __ldcg(part + static_cast<size_t>(q) * p.part_len);
+    float old = 0.f;
+    if (p.pair0 > 0) old = *out;   // (a call in several blocks of pairs)
+    else if (t < seen && p.decay != 0.f) old = p.decay * *out;
+    *out = old + sum;
 }
 
 template <int KB>
-static int launch_t(const WeightsParams& p, cudaStream_t stream) {
-    const long long units = 1ll * p.batch * p.hkv;
-    const long long g0 = (units * p.rows + 3) / 4, g1 = units * ((p.rows + kWtRows - 1) / kWtRows),
-                    g2 = units * ((p.max_len + kWtTok - 1) / kWtTok);
-    if (g1 > 0x7fffffffll || g2 > 0x7fffffffll) return cudaErrorInvalidValue;
-    cudaError_t e = launch_pdl(tq_weights_rows_kernel, dim3(static_cast<unsigned>(g0)), dim3(128), 0, stream, p, KB);
+static int launch_t(const WeightsParams& p, const CUtensorMap* kmap, cudaStream_t stream) {
+    using C = WtCfg<KB>;
+    static std::atomic<uint64_t> done0{0}, done1{0};
+    cudaError_t e = set_smem_attr_once(tq_weights_kernel<KB, false>, C::kSmemAlloc, done0);
+    if (e == cudaSuccess) e = set_smem_attr_once(tq_weights_kernel<KB, true>, C::kSmemAlloc, done1);
+    if (e != cudaSuccess) return e;
+    const unsigned units = static_cast<unsigned>(p.batch) * p.hkv;
+    e = launch_pdl(tq_weights_rows_kernel<KB != 0>, dim3(units * p.pairs * 32), dim3(256), 0, stream, p);
     if (e == cudaSuccess)
-        e = launch_pdl(tq_weights_lse_kernel<KB>, dim3(static_cast<unsigned>(g1)), dim3(kWtThreads), 0, stream, p);
+        e = launch_pdl(tq_weights_kernel<KB, false>, dim3(p.ctas), dim3(kWtThreads), C::kSmemAlloc, stream, p, *kmap);
+    if (e == cudaSuccess) e = launch_pdl(tq_weights_lse_kernel, dim3(units * p.pairs), dim3(256), 0, stream, p);
     if (e == cudaSuccess)
-        e = launch_pdl(tq_weights_sum_kernel<KB>, dim3(static_cast<unsigned>(g2)), dim3(kWtThreads), 0, stream, p);
+        e = launch_pdl(tq_weights_kernel<KB, true>, dim3(p.ctas), dim3(kWtThreads), C::kSmemAlloc, stream, p, *kmap);
+    if (e == cudaSuccess && p.part_w != nullptr)
+        e = launch_pdl(tq_weights_add_kernel, dim3(units * ((p.max_len + 255) / 256)), dim3(256), 0, stream, p);
     return e;
 }
 
-int launch_weights(int kbits, const WeightsParams& p, cudaStream_t stream) {
-    if (kbits == 16) return launch_t<0>(p, stream);
-    if (kbits == 3) return launch_t<3>(p, stream);
-    if (kbits == 4) return launch_t<4>(p, stream);
+int launch_weights(int kbits, const WeightsParams& p, const CUtensorMap* kmap, cudaStream_t stream) {
+    if (kbits == 16) return launch_t<0>(p, kmap, stream);
+    if (kbits == 3) return launch_t<3>(p, kmap, stream);
+    if (kbits == 4) return launch_t<4>(p, kmap, stream);
     return cudaErrorInvalidValue;
 }
 
