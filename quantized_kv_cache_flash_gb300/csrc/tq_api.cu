@@ -881,6 +881,8 @@ int tree_impl(tq_ctx** pctx, const tq_cache* c, const tq::host::DecodePlan& pl, 
 
 // Workspace that a tq_attention_weights call keeps to: more queries are taken in blocks.
 constexpr size_t kWeightsWork = size_t(512) << 20;
+// Rows per KV head up to which its scores go through the workspace.
+constexpr int kWeightsStepRows = 16;
 
 // Arguments that both prefill calls take.
 int check_prefill(const tq_cache* c, const void* q, int32_t num_q_heads, int32_t max_len_hint, float scale,
@@ -1154,15 +1156,56 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
     if (tq_rows <= 0 || tq_rows > max_len_hint) return TQ_ERR_INVALID_ARG;
     if (seen != nullptr && !list_ok(seen)) return TQ_ERR_INVALID_ARG;
     if (!(decay >= 0.f) || !std::isfinite(decay)) return TQ_ERR_INVALID_ARG;
-    tq::WeightsParams p{};
-    p.group = num_q_heads / c->num_kv_heads;
-    const long long rows = 1ll * p.group * tq_rows, units = 1ll * c->batch * c->num_kv_heads;
+    const int group = num_q_heads / c->num_kv_heads;
+    const long long rows = 1ll * group * tq_rows, units = 1ll * c->batch * c->num_kv_heads;
     if (rows >= (1ll << 31) - 256 || units > 65535) return TQ_ERR_UNSUPPORTED;
     tq_ctx* ctx;
     if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
     if ((r = prepare_tables(ctx, c, kb, vb)) != TQ_OK) return r;
     if (kb == 16 && (r = prepare_kmap(ctx, c)) != TQ_OK) return r;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const float sc = (scale == 0.f) ? 1.0f / std::sqrt(float(kD)) : scale;
+    CUtensorMap dummy;
+    std::memset(&dummy, 0, sizeof(dummy));
+    const CUtensorMap* kmap = kb == 16 ? &ctx->kmap : &dummy;
+    ctx->last_stream = s;
+    if (rows <= kWeightsStepRows) {
+        const int gr = std::max(tq::group_rows_for(int(rows), kb), kb == 16 ? 8 : 4);
+        const long long chunks = units * ((max_len_hint + 31) / 32);
+        const size_t scores = size_t(chunks) * 32 * gr * sizeof(float);
+        if (scores <= kWeightsWork) {
+            tq::StepParams p{};
+            p.ctas = int(std::min<long long>(2ll * tq::host::kSMs * tq::weights_step_ctas_per_sm(kb, gr),
+                                             std::max<long long>(1, (chunks + 7) / 8)));
+            const size_t part = size_t(p.ctas + units) * gr * sizeof(float2);
+            if ((r = ensure_work(ctx, scores + part, s)) != TQ_OK) return r;
+            p.k_codes = static_cast<const uint8_t*>(c->k_data);
+            p.k_norm = static_cast<const __half*>(c->k_norm);
+            p.lengths = c->lengths;
+            p.q = static_cast<const __half*>(q);
+            p.seen = seen;
+            p.weights = weights;
+            p.scores = ctx->d_work;
+            p.part_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ctx->d_work) + scores);
+            p.status = ctx->d_words;
+            p.batch = c->batch;
+            p.hkv = c->num_kv_heads;
+            p.hq = num_q_heads;
+            p.group = group;
+            p.tq = tq_rows;
+            p.rows = int32_t(rows);
+            p.cap = c->capacity;
+            p.max_len = max_len_hint;
+            p.score_len = (max_len_hint + 31) / 32 * 32;
+            p.scale_log2e = sc * 1.4426950408889634f;
+            p.decay = decay;
+            if (kb != 16) std::memcpy(p.ktab, ctx->ktab.tab, sizeof(p.ktab));
+            std::memcpy(p.signs, ctx->signs, sizeof(p.signs));
+            return cuda_err(static_cast<cudaError_t>(tq::launch_weights_step(kb, gr, p, kmap, s)));
+        }
+    }
+    tq::WeightsParams p{};
+    p.group = group;
     // Pairs of query tiles in blocks whose workspace stays below kWeightsWork (64-bit
     // rows * tokens otherwise); one pair needs no sums per pair.
     const long long pairs = (rows + 255) / 256, tiles = (max_len_hint + 127) / 128;
@@ -1196,18 +1239,14 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
     p.cap = c->capacity;
     p.max_len = max_len_hint;
     p.ctas = ctas;
-    const float sc = (scale == 0.f) ? 1.0f / std::sqrt(float(kD)) : scale;
     p.scale_log2e = sc * 1.4426950408889634f;
     p.decay = decay;
     if (kb != 16) std::memcpy(p.ktab, ctx->ktab.tab, sizeof(p.ktab));
     std::memcpy(p.signs, ctx->signs, sizeof(p.signs));
-    CUtensorMap dummy;
-    std::memset(&dummy, 0, sizeof(dummy));
-    ctx->last_stream = s;
     for (long long q0 = 0; q0 < pairs; q0 += block) {
         p.pair0 = int32_t(q0);
         p.pairs = int32_t(std::min(block, pairs - q0));
-        const int e = tq::launch_weights(kb, p, kb == 16 ? &ctx->kmap : &dummy, s);
+        const int e = tq::launch_weights(kb, p, kmap, s);
         if (e != 0) return TQ_ERR_CUDA;
     }
     return TQ_OK;

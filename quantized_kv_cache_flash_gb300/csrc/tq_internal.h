@@ -199,6 +199,23 @@ struct WeightsParams {
     uint32_t ktab[4], signs[4];
 };
 
+// The same for up to 16 rows per KV head (tq_weights_step.cu), in groups as the decode's
+// (group_rows_for).
+struct StepParams {
+    const uint8_t* k_codes;
+    const __half* k_norm;
+    const int32_t* lengths;
+    const __half* q;
+    const int32_t* seen;
+    float* weights;
+    float* scores;            // workspace: [units][score_len][group rows], log2 units
+    float2* part_ml;          // workspace: [ctas + units][group rows]
+    uint32_t* status;
+    int32_t batch, hkv, hq, group, tq, rows, cap, max_len, score_len, ctas;
+    float scale_log2e, decay;
+    uint32_t ktab[4], signs[4];
+};
+
 // Eviction by weight (see tq_cache_evict).
 struct EvictParams {
     const uint8_t* k_src;
@@ -278,6 +295,8 @@ int launch_compact(const CompactParams& p, cudaStream_t stream);
 constexpr int kCopyTokens = 256;
 int launch_copy(const CopyParams& p, cudaStream_t stream);
 int launch_weights(int kbits, const WeightsParams& p, const CUtensorMap* kmap, cudaStream_t stream);
+int launch_weights_step(int kbits, int group_rows, const StepParams& p, const CUtensorMap* kmap, cudaStream_t stream);
+int weights_step_ctas_per_sm(int kbits, int group_rows);
 constexpr int kEvictMoveCtas = 8;   // of the cluster that moves a unit's records in place
 int launch_evict(EvictParams p, cudaStream_t stream);
 int launch_verify(const VerifyParams& p, cudaStream_t stream);

@@ -1,0 +1,469 @@
+// tq_attention_weights for few rows per KV head (a decode step): up to 16.
+//
+// Two kernels.  The first is the decode kernel's K half: CTAs with equal shares of all
+// units' 32-token chunks, their warps streaming chunks through private rings of bulk
+// copies, dequantising in registers, scores by warp MMAs with 16 tokens as M.  It writes
+// the scores (fp32, log2 units) to the workspace and a (maximum, sum of exp2) per row and
+// share.  A thread keeps its own tokens' maximum and sum of each of its rows, so no lane
+// waits for another until the share ends.  The second joins a unit's shares to the rows'
+// log-sum-exp and turns the scores into the tokens' weights, a token a thread.  (Scores
+// of 4 to 8 rows are 16 to 32 bytes a token, mostly served by L2; reading K once more
+// would be 48 to 256 and another dequantisation.)
+#include <algorithm>
+
+#include "tq_decode_kernel.cuh"
+
+namespace tq {
+
+template <int KB, int ROWS>
+struct StepCfg {
+    static constexpr int kWarps = 4;
+    static constexpr int NT = ROWS == 16 ? 2 : 1;           // 8-column MMA n-tiles
+    static constexpr bool kPair = KB != 0 && ROWS == 4;     // column 2i: q_hi of row i, 2i + 1: q_lo
+    static constexpr bool kQlo = KB != 0 && ROWS != 4;      // q_lo as a second B operand
+    static constexpr int NE = kPair ? 1 : 2;                // query rows per thread per n-tile
+    static constexpr int kStages = KB == 0 ? 2 : 4;
+    static constexpr int kMinCtas = KB == 0 ? 3 : 4;        // resident CTAs per SM
+    static constexpr int kRbK = KB == 0 ? 256 : KB * 16;
+    static constexpr int kKnOff = kChunkTokens * kRbK;
+    static constexpr int kStageRaw = kKnOff + (KB == 0 ? 0 : kChunkTokens * 2);
+    static constexpr int kStageAlign = KB == 0 ? 1024 : 128;
+    static constexpr int kStage = (kStageRaw + kStageAlign - 1) / kStageAlign * kStageAlign;
+    static constexpr int kPipe = kWarps * kStages * kStage;
+    static constexpr int kQStride = kD + 8;                 // (16-byte pads: columns on different banks)
+    static constexpr int kQOff = kPipe;
+    static constexpr int kQloOff = kQOff + 8 * NT * kQStride * 2;
+    static constexpr int kBarOff = kQloOff + (kQlo ? 8 * NT * kQStride * 2 : 0);
+    static constexpr int kScanOff = (kBarOff + kWarps * kStages * 8 + 15) / 16 * 16;
+    static constexpr int kMlOff = kScanOff + kWarps * 512;  // (m, l) of the warps' rows
+    static constexpr int kSmem = kMlOff + kWarps * ROWS * 8;
+    static constexpr int kSmemAlloc = kSmem + 1024;
+
+    __device__ static __forceinline__ int slot_row(int n, int e, int t) { return kPair ? t : 8 * n + 2 * t + e; }
+};
+
+// (m, l) += a part whose maximum is mb and sum lb.
+__device__ __forceinline__ void join(float& m, float& l, float mb, float lb) {
+    const float mn = fmaxf(m, mb);
+    l = (m == -INFINITY ? l : l * fast_exp2(m - mn)) + (mb == -INFINITY ? lb : lb * fast_exp2(mb - mn));
+    m = mn;
+}
+
+template <int KB, int ROWS>
+__global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
+    tq_step_scores_kernel(const __grid_constant__ StepParams p, const __grid_constant__ CUtensorMap kmap) {
+    using C = StepCfg<KB, ROWS>;
+    constexpr int NT = C::NT, NE = C::NE;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+    const int lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    uint8_t* wpipe = smem + warp * C::kStages * C::kStage;
+    const uint32_t bar0 = smem_u32(smem + C::kBarOff) + warp * C::kStages * 8;
+    if (lane == 0) {
+        for (int s = 0; s < C::kStages; ++s) mbar_init(bar0 + 8 * s, 1);
+        fence_barrier_init();
+    }
+    if (KB == 0 && threadIdx.x == 0) prefetch_tensormap(&kmap);
+    __syncwarp();
+
+    griddep_wait();
+    BatchScan scan;
+    scan.init(reinterpret_cast<int*>(smem + C::kScanOff) + warp * 128, p.lengths, p.batch, p.hkv, p.max_len, lane);
+    const int all = __shfl_sync(0xffffffffu, scan.total(p.lengths, p.batch, p.hkv, p.max_len, lane), 0);
+    const int P = static_cast<int>(gridDim.x), c_me = static_cast<int>(blockIdx.x);
+    const int cq = all / P, cr = all - cq * P;
+    const int lo = c_me * cq + (c_me * cr) / P;
+    const int hi = (c_me + 1) * cq + ((c_me + 1) * cr) / P;
+    if (lo >= hi) return;   // (uniform over the CTA)
+    __half* sQ = reinterpret_cast<__half*>(smem + C::kQOff);
+    __half* sQlo = reinterpret_cast<__half*>(smem + C::kQloOff);
+    const uint32_t q_lds = smem_u32(sQ) + ((lane & 7) * C::kQStride + 8 * (lane >> 3)) * 2;
+    const uint32_t qlo_lds = smem_u32(sQlo) + ((lane & 7) * C::kQStride + 8 * (lane >> 3)) * 2;
+    const Tables kt{p.ktab[0], p.ktab[1], p.ktab[2], p.ktab[3]};
+    float2* sML = reinterpret_cast<float2*>(smem + C::kMlOff);
+
+    int stage = 0;
+    uint32_t phase = 0;
+    int pos = lo;
+    while (pos < hi) {
+        int b, before, L, nch;
+        scan.locate(p.lengths, p.batch, p.hkv, p.max_len, pos, lane, b, before, L, nch);
+        b = __shfl_sync(0xffffffffu, b, 0);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        L = __shfl_sync(0xffffffffu, L, 0);
+        nch = __shfl_sync(0xffffffffu, nch, 0);
+        const int h = (pos - before) / nch, k0 = pos - before - h * nch;
+        const int k1 = min(nch, k0 + (hi - pos));
+        const int unit = b * p.hkv + h;
+        const int t_begin = k0 * kChunkTokens, t_end = min(k1 * kChunkTokens, min(L, p.max_len));
+        const int nchunks = k1 - k0;
+        const size_t row0 = static_cast<size_t>(unit) * p.cap;
+
+        auto issue = [&](int c, int st) {   // lane 0 only
+            const int tok0 = t_begin + c * kChunkTokens;
+            const int nval = min(kChunkTokens, t_end - tok0);
+            const uint32_t dst = smem_u32(wpipe + st * C::kStage), bar = bar0 + st * 8;
+            if constexpr (KB == 0) {
+                mbar_arrive_expect_tx(bar, 2 * 4096);
+                tma_g2s_2d(dst, &kmap, 0, static_cast<int32_t>(row0 + tok0), bar);
+                tma_g2s_2d(dst + 4096, &kmap, 64, static_cast<int32_t>(row0 + tok0), bar);
+            } else {
+                const uint32_t nb = static_cast<uint32_t>((nval + 7) & ~7) * 2;   // norms, 16-byte multiple
+                mbar_arrive_expect_tx(bar, nval * C::kRbK + nb);
+                bulk_g2s(dst, p.k_codes + (row0 + tok0) * C::kRbK, nval * C::kRbK, bar);
+                bulk_g2s(dst + C::kKnOff, p.k_norm + row0 + tok0, nb, bar);
+            }
+        };
+        if (lane == 0) {
+            for (int s = 0; s < C::kStages; ++s) {
+                const int c = warp + C::kWarps * s;
+                int si = stage + s;
+                if (si >= C::kStages) si -= C::kStages;
+                if (c < nchunks) issue(c, si);
+            }
+        }
+        __syncwarp();
+
+        // ---- the query rows -> shared, as the decode kernel lays them out ----
+        for (int r = warp; r < ROWS; r += C::kWarps) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            if (r < p.rows) {
+                const int j = r / p.group, gl = r - j * p.group;
+                const uint2 raw = *reinterpret_cast<const uint2*>(
+                    p.q + ((static_cast<size_t>(b) * p.hq + h * p.group + gl) * p.tq + j) * kD + lane * 4);
+                const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&raw.x));
+                const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&raw.y));
+                v[0] = f0.x; v[1] = f0.y; v[2] = f1.x; v[3] = f1.y;
+                if constexpr (KB != 0) {
+                    const uint32_t sn = sign_nibble(p.signs, lane);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = ((sn >> i) & 1u) ? -v[i] : v[i];
+                    wht128_lane4(v, lane);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] *= 0.08838834764831845f;   // 1/sqrt(128)
+                }
+            }
+            const uint32_t qh0 = pack_half2(v[0], v[1]), qh1 = pack_half2(v[2], v[3]);
+            if constexpr (KB != 0) {
+                // k-index 16 kc + 8 hi + 2 t + e holds dim 32 t + 4 kc + 2 hi + e
+                const int kk = 16 * (lane & 7) + 2 * (lane >> 3);
+                __half* qrow = sQ + (C::kPair ? 2 * r : r) * C::kQStride;
+                *reinterpret_cast<uint32_t*>(qrow + kk) = qh0;
+                *reinterpret_cast<uint32_t*>(qrow + kk + 8) = qh1;
+                const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&qh0));
+                const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&qh1));
+                __half* lrow = C::kPair ? sQ + (2 * r + 1) * C::kQStride : sQlo + r * C::kQStride;
+                *reinterpret_cast<uint32_t*>(lrow + kk) = pack_half2(v[0] - h0.x, v[1] - h0.y);
+                *reinterpret_cast<uint32_t*>(lrow + kk + 8) = pack_half2(v[2] - h1.x, v[3] - h1.y);
+            } else {
+                *reinterpret_cast<uint2*>(sQ + r * C::kQStride + 4 * lane) = make_uint2(qh0, qh1);
+            }
+        }
+        __syncthreads();
+
+        auto load_qb = [&](uint32_t base, int n, int kc2, uint32_t (&bq)[4]) {
+            ldsm_x4(base + (8 * n * C::kQStride + 32 * kc2) * 2, bq[0], bq[1], bq[2], bq[3]);
+        };
+        float m[NT][NE], l[NT][NE];
+        int lim[NT][NE];   // last visible token of the thread's rows
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                m[n][e] = -INFINITY;
+                l[n][e] = 0.f;
+                lim[n][e] = min(L - p.tq + C::slot_row(n, e, t) / p.group, t_end - 1);
+            }
+        float* out = p.scores + static_cast<size_t>(unit) * p.score_len * ROWS;
+        const int all_see = min(L - p.tq, t_end - 1);   // (padding rows see more; nobody reads them)
+
+        // a chunk: scores to the workspace, maxima and sums in registers
+        auto process = [&](const uint8_t* st, int tok0, auto full_tag) {
+            constexpr bool FULL = decltype(full_tag)::value;
+            float x[2][NT][4];
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) x[tt][n][0] = x[tt][n][1] = x[tt][n][2] = x[tt][n][3] = 0.f;
+                if constexpr (KB == 0) {
+                    const int mi = lane >> 3;
+                    const int row = tt * 16 + (mi & 1) * 8 + (lane & 7);
+#pragma unroll
+                    for (int kc2 = 0; kc2 < 4; ++kc2) {
+                        uint32_t qb[NT][4];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) load_qb(q_lds, n, kc2, qb[n]);
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) {
+                            const int db = 4 * kc2 + 2 * kk + (mi >> 1);
+                            uint32_t a0, a1, a2, a3;
+                            ldsm_x4(smem_u32(st) + (db >> 3) * 4096 + row * 128 + (((db & 7) ^ (row & 7)) << 4), a0, a1,
+                                    a2, a3);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16(x[tt][n], a0, a1, a2, a3, qb[n][2 * kk], qb[n][2 * kk + 1]);
+                        }
+                    }
+                } else {
+                    const QuarterWords wa = load_quarter<KB>(st + (tt * 16 + g) * C::kRbK + t * (C::kRbK / 4));
+                    const QuarterWords wb = load_quarter<KB>(st + (tt * 16 + g + 8) * C::kRbK + t * (C::kRbK / 4));
+                    auto kgroup = [&](auto jtag) {
+                        constexpr int J = decltype(jtag)::value;
+                        uint32_t ha[4], hb[4], unused[2];
+                        dequant_group<KB, J, false>(wa, kt, 0u, 0u, ha, unused);
+                        dequant_group<KB, J, false>(wb, kt, 0u, 0u, hb, unused);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            uint32_t qb[4];
+                            if constexpr (C::kQlo) {
+                                load_qb(qlo_lds, n, J, qb);
+                                mma_f16(x[tt][n], ha[0], hb[0], ha[1], hb[1], qb[0], qb[1]);
+                                mma_f16(x[tt][n], ha[2], hb[2], ha[3], hb[3], qb[2], qb[3]);
+                            }
+                            load_qb(q_lds, n, J, qb);
+                            mma_f16(x[tt][n], ha[0], hb[0], ha[1], hb[1], qb[0], qb[1]);
+                            mma_f16(x[tt][n], ha[2], hb[2], ha[3], hb[3], qb[2], qb[3]);
+                        }
+                    };
+                    kgroup(std::integral_constant<int, 0>{});
+                    kgroup(std::integral_constant<int, 1>{});
+                    kgroup(std::integral_constant<int, 2>{});
+                    kgroup(std::integral_constant<int, 3>{});
+                    if constexpr (C::kPair) {   // q_lo's column into q_hi's
+                        x[tt][0][0] += x[tt][0][1];
+                        x[tt][0][2] += x[tt][0][3];
+                    }
+                }
+            }
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                const int ta = tt * 16 + g, tb = ta + 8;
+                float ka = p.scale_log2e, kb2 = p.scale_log2e;
+                if constexpr (KB != 0) {
+                    ka *= __half2float(*reinterpret_cast<const __half*>(st + C::kKnOff + 2 * ta));
+                    kb2 *= __half2float(*reinterpret_cast<const __half*>(st + C::kKnOff + 2 * tb));
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int e = 0; e < NE; ++e) {
+                        x[tt][n][e] *= ka;
+                        x[tt][n][e + 2] *= kb2;
+                        if (!FULL) {
+                            if (tok0 + ta > lim[n][e]) x[tt][n][e] = -INFINITY;
+                            if (tok0 + tb > lim[n][e]) x[tt][n][e + 2] = -INFINITY;
+                        }
+                    }
+                    const int col = C::slot_row(n, 0, t);
+                    float* oa = out + static_cast<size_t>(tok0 + ta) * ROWS + col;
+                    float* ob = out + static_cast<size_t>(tok0 + tb) * ROWS + col;
+                    if constexpr (NE == 2) {
+                        if (FULL || tok0 + ta < t_end) *reinterpret_cast<float2*>(oa) = make_float2(x[tt][n][0], x[tt][n][1]);
+                        if (FULL || tok0 + tb < t_end) *reinterpret_cast<float2*>(ob) = make_float2(x[tt][n][2], x[tt][n][3]);
+                    } else {
+                        if (FULL || tok0 + ta < t_end) *oa = x[tt][n][0];
+                        if (FULL || tok0 + tb < t_end) *ob = x[tt][n][2];
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    const float mx = fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2]));
+                    if (mx > m[n][e]) {
+                        l[n][e] *= m[n][e] == -INFINITY ? 1.f : fast_exp2(m[n][e] - mx);   // (l is 0 there, or NaN)
+                        m[n][e] = mx;
+                    }
+                    const float base = m[n][e] == -INFINITY ? 0.f : m[n][e];
+                    l[n][e] += (fast_exp2(x[0][n][e] - base) + fast_exp2(x[0][n][e + 2] - base)) +
+                               (fast_exp2(x[1][n][e] - base) + fast_exp2(x[1][n][e + 2] - base));
+                }
+        };
+
+        bool stalled = false;
+        int c = warp;
+        for (; c < nchunks; c += C::kWarps) {
+            const bool ok = mbar_wait_bounded(bar0 + 8 * stage, phase);
+            if (__any_sync(0xffffffffu, !ok)) { stalled = true; break; }
+            const uint8_t* st = wpipe + stage * C::kStage;
+            const int tok0 = t_begin + c * kChunkTokens;
+            if (tok0 + kChunkTokens - 1 <= all_see) process(st, tok0, std::true_type{});
+            else process(st, tok0, std::false_type{});
+            __syncwarp();
+            const int cn = c + C::kWarps * C::kStages;
+            if (cn < nchunks && lane == 0) {
+                fence_proxy_async();
+                issue(cn, stage);
+            }
+            if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+        }
+        if (pos + nchunks >= hi) griddep_launch_dependents();
+        if (stalled) {   // this warp's copies still in flight land (bounded)
+            for (int k = 0; k < C::kStages; ++k) {
+                if (c + C::kWarps * k >= nchunks) break;
+                (void)mbar_wait_bounded(bar0 + 8 * stage, phase);
+                if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+            }
+            if (lane == 0) atomicOr(p.status, kStatusPipelineStall);
+        }
+
+        // ---- the share's (m, l) of each row ----
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1)
+                    join(m[n][e], l[n][e], __shfl_xor_sync(0xffffffffu, m[n][e], o),
+                         __shfl_xor_sync(0xffffffffu, l[n][e], o));
+                if (g == 0) sML[warp * ROWS + C::slot_row(n, e, t)] = make_float2(m[n][e], l[n][e]);
+            }
+        __syncthreads();
+        if (threadIdx.x < ROWS) {
+            float2 a = sML[threadIdx.x];
+#pragma unroll
+            for (int w = 1; w < C::kWarps; ++w) {
+                const float2 o = sML[w * ROWS + threadIdx.x];
+                join(a.x, a.y, o.x, o.y);
+            }
+            p.part_ml[(static_cast<size_t>(blockIdx.x) + unit) * ROWS + threadIdx.x] = a;
+        }
+        if (__syncthreads_or(stalled)) break;
+        pos += nchunks;
+    }
+}
+
+// The tokens' weights from the scores; a CTA 256 * TOK tokens of a unit.
+template <int ROWS, int TOK>
+__global__ void __launch_bounds__(256) tq_step_sums_kernel(const __grid_constant__ StepParams p) {
+    __shared__ float2 s_part[16][ROWS];
+    __shared__ float s_lse[ROWS];
+    const int tid = threadIdx.x;
+    const int per = (p.max_len + 256 * TOK - 1) / (256 * TOK);
+    const int unit = static_cast<int>(blockIdx.x) / per;
+    const int t0 = (static_cast<int>(blockIdx.x) - unit * per) * 256 * TOK + tid;
+    const int b = unit / p.hkv, h = unit - b * p.hkv;
+    // (lengths may be read before the wait: the scores kernel's CTAs waited for what wrote
+    // them before any of them let this grid launch)
+    const int L = p.lengths[b], lim = min(L, p.max_len);
+    // chunks of all units, and of those before this sequence
+    int before = 0, all = 0;
+    for (int bb = tid & 31; bb < p.batch; bb += 32) {
+        const int v = unit_chunks(p.lengths, bb, p.max_len) * p.hkv;
+        all += v;
+        if (bb < b) before += v;
+    }
+    all = __reduce_add_sync(0xffffffffu, all);
+    before = __reduce_add_sync(0xffffffffu, before);
+    const int nch = unit_chunks(p.lengths, b, p.max_len);
+    griddep_wait();
+    griddep_launch_dependents();
+    const bool first = t0 - tid == 0;
+    if (t0 - tid >= lim && !first) return;   // (uniform over the CTA)
+
+    // the scores, in flight while the shares are joined
+    float x[TOK][ROWS];
+    float old[TOK];
+    float* out = p.weights + static_cast<size_t>(unit) * p.cap;
+    const int seen = p.seen != nullptr ? p.seen[b] : L - p.tq;
+    const float4* sc = reinterpret_cast<const float4*>(p.scores + static_cast<size_t>(unit) * p.score_len * ROWS);
+#pragma unroll
+    for (int k = 0; k < TOK; ++k) {
+        const int t = t0 + 256 * k;
+        old[k] = 0.f;
+        if (t < lim) {
+#pragma unroll
+            for (int i = 0; i < ROWS / 4; ++i) {
+                const float4 v = __ldcg(sc + static_cast<size_t>(t) * (ROWS / 4) + i);
+                x[k][4 * i] = v.x, x[k][4 * i + 1] = v.y, x[k][4 * i + 2] = v.z, x[k][4 * i + 3] = v.w;
+            }
+            if (t < seen && p.decay != 0.f) old[k] = p.decay * out[t];
+        }
+    }
+    {   // thread (i, r): every 16th share of row r
+        const int i = tid / 16, r = tid % 16;
+        float m = -INFINITY, l = 0.f;
+        if (nch > 0 && r < ROWS) {
+            const int P = p.ctas, cq = all / P, cr = all - cq * P;
+            const int k_first = before + h * nch;
+            const int c0 = static_cast<int>((static_cast<long long>(k_first + 1) * P - 1) / all);
+            const int c1 = static_cast<int>((static_cast<long long>(k_first + nch) * P - 1) / all);
+            for (int c = c0 + i; c <= c1; c += 16) {
+                if (c * cq + (c * cr) / P >= (c + 1) * cq + ((c + 1) * cr) / P) continue;   // (an empty share)
+                const float2 v = __ldcg(p.part_ml + (static_cast<size_t>(c) + unit) * ROWS + r);
+                join(m, l, v.x, v.y);
+            }
+        }
+        if (r < ROWS) s_part[i][r] = make_float2(m, l);
+    }
+    __syncthreads();
+    if (tid < ROWS) {
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) join(m, l, s_part[i][tid].x, s_part[i][tid].y);
+        const bool none = m == -INFINITY && l == 0.f;
+        s_lse[tid] = none || tid >= p.rows ? INFINITY : m + log2f(l);
+        if (none && tid < p.rows && first) atomicOr(p.status, kStatusShortContext);
+    }
+    __syncthreads();
+    float lse[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) lse[r] = s_lse[r];
+#pragma unroll
+    for (int k = 0; k < TOK; ++k) {
+        const int t = t0 + 256 * k;
+        if (t >= lim) continue;
+        float w = 0.f;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)   // (-inf: hidden, also from a row of NaN)
+            w += r < p.rows && x[k][r] != -INFINITY ? fast_exp2(x[k][r] - lse[r]) : 0.f;
+        out[t] = old[k] + w;
+    }
+}
+
+template <int KB, int ROWS>
+static int launch_t(const StepParams& p, const CUtensorMap* kmap, cudaStream_t stream) {
+    using C = StepCfg<KB, ROWS>;
+    static std::atomic<uint64_t> attr_done{0};
+    cudaError_t e = set_smem_attr_once(tq_step_scores_kernel<KB, ROWS>, C::kSmemAlloc, attr_done);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(tq_step_scores_kernel<KB, ROWS>, dim3(p.ctas), dim3(128), C::kSmemAlloc, stream, p, *kmap);
+    if (e != cudaSuccess) return e;
+    const unsigned units = static_cast<unsigned>(p.batch) * p.hkv;
+    const unsigned small = (p.max_len + 255) / 256;
+    // few tokens: a token a thread (one trip of loads more SMs share); else four
+    if (ROWS == 16 || units * small <= 4 * 152)
+        return launch_pdl(tq_step_sums_kernel<ROWS, 1>, dim3(units * small), dim3(256), 0, stream, p);
+    return launch_pdl(tq_step_sums_kernel<ROWS, ROWS == 16 ? 1 : 4>, dim3(units * ((p.max_len + 1023) / 1024)),
+                      dim3(256), 0, stream, p);
+}
+
+int launch_weights_step(int kbits, int rows, const StepParams& p, const CUtensorMap* kmap, cudaStream_t stream) {
+    if (kbits == 16) return rows <= 8 ? launch_t<0, 8>(p, kmap, stream) : launch_t<0, 16>(p, kmap, stream);
+    if (kbits == 3)
+        return rows == 4   ? launch_t<3, 4>(p, kmap, stream)
+               : rows == 8 ? launch_t<3, 8>(p, kmap, stream)
+                           : launch_t<3, 16>(p, kmap, stream);
+    if (kbits == 4)
+        return rows == 4   ? launch_t<4, 4>(p, kmap, stream)
+               : rows == 8 ? launch_t<4, 8>(p, kmap, stream)
+                           : launch_t<4, 16>(p, kmap, stream);
+    return cudaErrorInvalidValue;
+}
+
+// Resident CTAs per SM of the scores kernel.
+template <int KB, int ROWS>
+static int ctas_t() {
+    using C = StepCfg<KB, ROWS>;
+    return std::min(C::kMinCtas, (228 * 1024) / (C::kSmemAlloc + 1024));
+}
+int weights_step_ctas_per_sm(int kbits, int rows) {
+    if (kbits == 16) return rows <= 8 ? ctas_t<0, 8>() : ctas_t<0, 16>();
+    if (kbits == 3) return rows == 4 ? ctas_t<3, 4>() : rows == 8 ? ctas_t<3, 8>() : ctas_t<3, 16>();
+    return rows == 4 ? ctas_t<4, 4>() : rows == 8 ? ctas_t<4, 8>() : ctas_t<4, 16>();
+}
+
+}  // namespace tq
