@@ -24,22 +24,37 @@ namespace tq {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
-constexpr int kSelKeysMax = 48 * 1024;   // keys that shared memory holds (192 KB); more are read anew a pass
 
-// Integers in the weights' order; NaN counts as -inf, -0 as 0.
+// Integers in the weights' order; NaN counts as -inf, -0 as 0.  They are 0x007fffff ..
+// 0xff800000, so that 0 is left for tokens that do not exist and kKeyHeld for those that
+// stay whatever their weight.
+constexpr uint32_t kKeyHeld = 0xffffffffu;
 __device__ __forceinline__ uint32_t weight_key(float w) {
     if (w != w) w = -INFINITY;
     const uint32_t u = __float_as_uint(w + 0.f);   // (-0 + 0 = 0)
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kSelThreads) tq_evict_select_kernel(const __grid_constant__ EvictParams p) {
-    extern __shared__ uint32_t s_keys[];
+// The lowest r bits that are set.
+__device__ __forceinline__ uint32_t lowest_bits(uint32_t mask, int r) {
+    if (r >= __popc(mask)) return mask;
+    uint32_t got = 0;
+    for (; r > 0; --r) {
+        got |= mask & (0u - mask);
+        mask &= mask - 1u;
+    }
+    return got;
+}
+
+// T threads; a warp has a run of 32 KPT tokens, lane l every 32nd from its l-th, the
+// keys in registers.  KPT = 0: runs of any length, the weights read anew a pass.
+template <int T, int KPT>
+__global__ void __launch_bounds__(T, T == 512 ? 2 : 1) tq_evict_select_kernel(const __grid_constant__ EvictParams p) {
+    constexpr int W = T / 32;
+    static_assert(KPT <= 32, "a lane keeps a group's masks");
     __shared__ uint32_t s_hist[kSelBins];
-    __shared__ uint32_t s_warp[kSelWarps], s_warp2[kSelWarps];
+    __shared__ uint32_t s_warp[W], s_warp2[W];
     __shared__ uint32_t s_digit, s_above;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = static_cast<int>(blockIdx.x) / p.hkv, h = static_cast<int>(blockIdx.x) - b * p.hkv;
@@ -55,111 +70,135 @@ __global__ void __launch_bounds__(kSelThreads) tq_evict_select_kernel(const __gr
         p.counts[b] = flag ? -1 : count;
         if (flag) atomicOr(p.status, flag);
     }
-    if (flag) return;
+    if (flag || n == 0) return;
     int32_t* kept = p.kept + static_cast<size_t>(blockIdx.x) * p.max_keep;
     if (L <= n) {
-        for (int i = tid; i < L; i += kSelThreads) kept[i] = i;
+        for (int i = tid; i < L; i += T) kept[i] = i;
         return;
     }
-    // tokens [lo, hi) are weighed, m of them kept (0 <= m < hi - lo)
-    const int lo = p.sinks, hi = L - p.recent, m = n - p.sinks - p.recent;
+    const int lo = p.sinks, hi = L - p.recent;   // tokens [lo, hi) go by their weights
     const float* w = p.weights + static_cast<size_t>(blockIdx.x) * p.src_cap;
-    const bool held = L <= p.keys_held;
-    uint32_t prefix = 0, need = static_cast<uint32_t>(m);   // digits so far; how many of the keys with them are kept
-    auto key_at = [&](int t) { return held ? s_keys[t] : weight_key(__ldg(w + t)); };
-    if (m > 0) {
-#pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const int bins = pass == 2 ? 1024 : 2048;
-            for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
-            __syncthreads();
-            if (pass == 0) {
-                for (int t = lo + tid; t < hi; t += kSelThreads) {
-                    const uint32_t key = weight_key(__ldg(w + t));
-                    if (held) s_keys[t] = key;
-                    atomicAdd(&s_hist[key >> 21], 1u);
-                }
-            } else {
-                const int above = shift + (pass == 1 ? 11 : 10);
-                for (int t = lo + tid; t < hi; t += kSelThreads) {
-                    const uint32_t key = key_at(t);
-                    if ((key >> above) == (prefix >> above)) atomicAdd(&s_hist[(key >> shift) & (bins - 1)], 1u);
-                }
-            }
-            __syncthreads();
-            // the bin whose keys, with those of the bins above it, first make `need`:
-            // thread i has bins from the top, per of them
-            const int per = bins / kSelThreads;
-            uint32_t mine = 0;
-            for (int e = 0; e < per; ++e) mine += s_hist[bins - 1 - (tid * per + e)];
-            uint32_t inc = mine;
+    auto key_of = [&](int t, float v) { return t >= L ? 0u : t < lo || t >= hi ? kKeyHeld : weight_key(v); };
+    const int groups = (L + 31) / 32, per = KPT > 0 ? KPT : (groups + W - 1) / W;
+    const int g0 = warp * per, g1 = min(groups, g0 + per);
+    uint32_t key[KPT > 0 ? KPT : 1];
+    if constexpr (KPT > 0) {
+        float v[KPT];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            if (lane == 31) s_warp[warp] = inc;
-            __syncthreads();
-            for (int i = 0; i < warp; ++i) inc += s_warp[i];
-            if (inc >= need && inc - mine < need) {   // (one thread)
-                uint32_t run = inc - mine;
-                int e = 0;
-                for (; e < per; ++e) {
-                    const uint32_t c = s_hist[bins - 1 - (tid * per + e)];
-                    if (run + c >= need) break;
-                    run += c;
-                }
-                s_digit = static_cast<uint32_t>(bins - 1 - (tid * per + e));
-                s_above = run;
-            }
-            __syncthreads();
-            prefix |= s_digit << shift;
-            need -= s_above;
+        for (int i = 0; i < KPT; ++i) {
+            const int t = 32 * (g0 + i) + lane;
+            v[i] = t >= lo && t < hi ? __ldg(w + t) : 0.f;
         }
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) key[i] = key_of(32 * (g0 + i) + lane, v[i]);
     }
-    // a warp's run of tokens (whole groups of 32): how many it keeps for sure, and
-    // how many are equal to the smallest
-    const int groups = (L + 31) / 32, per = (groups + kSelWarps - 1) / kSelWarps;
-    const int g0 = min(groups, warp * per), g1 = min(groups, g0 + per);
-    auto look = [&](int t, bool& sure, bool& same) {
-        sure = t < L && (t < lo || t >= hi);
-        same = false;
-        if (m > 0 && t >= lo && t < hi) {
-            const uint32_t key = key_at(t);
-            sure = key > prefix;
-            same = key == prefix;
-        }
+    auto key_at = [&](int g) {
+        const int t = 32 * g + lane;
+        return key_of(t, t >= lo && t < hi ? __ldg(w + t) : 0.f);
     };
-    uint32_t sures = 0, sames = 0;
-    for (int g = g0; g < g1; ++g) {
-        bool sure, same;
-        look(32 * g + lane, sure, same);
-        sures += __popc(__ballot_sync(0xffffffffu, sure));
-        sames += __popc(__ballot_sync(0xffffffffu, same));
+    // digits so far; how many of the keys with them are kept
+    uint32_t prefix = 0, need = static_cast<uint32_t>(n);
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const int bins = pass == 2 ? 1024 : 2048;
+        for (int i = tid; i < bins; i += T) s_hist[i] = 0;
+        __syncthreads();
+        auto add = [&](uint32_t k) {
+            if (pass == 0 || ((k ^ prefix) >> (pass == 1 ? 21 : 10)) == 0) atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1u);
+        };
+        if constexpr (KPT > 0) {
+#pragma unroll
+            for (int i = 0; i < KPT; ++i)
+                if (pass > 0 || g0 + i < g1) add(key[i]);
+        } else {
+            for (int g = g0; g < g1; ++g) add(key_at(g));
+        }
+        __syncthreads();
+        // the bin whose keys, with those of the bins above it, first make `need`:
+        // thread i has bins from the top, `own` of them
+        const int own = bins / T;
+        uint32_t mine = 0;
+#pragma unroll
+        for (int e = 0; e < own; ++e) mine += s_hist[bins - 1 - (tid * own + e)];
+        uint32_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) s_warp[warp] = inc;
+        __syncthreads();
+        inc += __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
+        if (inc >= need && inc - mine < need) {   // (one thread)
+            uint32_t run = inc - mine;
+            int e = 0;
+            for (; e < own; ++e) {
+                const uint32_t c = s_hist[bins - 1 - (tid * own + e)];
+                if (run + c >= need) break;
+                run += c;
+            }
+            s_digit = static_cast<uint32_t>(bins - 1 - (tid * own + e));
+            s_above = run;
+        }
+        __syncthreads();
+        prefix |= s_digit << shift;
+        need -= s_above;
     }
-    __syncthreads();   // (s_warp of the last pass is read)
+    // Tokens above the smallest kept weight stay, of those equal to it the first `need`:
+    // counted over the warp's run, then over the warps, then written.
+    uint32_t above = 0, same = 0;   // KPT > 0: masks of group `lane` of the run
+    uint32_t n_above = 0, n_same = 0;
+    if constexpr (KPT > 0) {
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const uint32_t x = __ballot_sync(0xffffffffu, key[i] > prefix), y = __ballot_sync(0xffffffffu, key[i] == prefix);
+            if (lane == i) above = x, same = y;
+        }
+        n_above = __popc(above);
+        n_same = __popc(same);
+    } else {
+        for (int g = g0; g < g1; ++g) {
+            const uint32_t k = key_at(g);
+            n_above += k > prefix;
+            n_same += k == prefix;
+        }
+    }
+    const uint32_t all_above = __reduce_add_sync(0xffffffffu, n_above), all_same = __reduce_add_sync(0xffffffffu, n_same);
     if (lane == 0) {
-        s_warp[warp] = sures;
-        s_warp2[warp] = sames;
+        s_warp[warp] = all_above;   // (read in the last pass before its last barrier)
+        s_warp2[warp] = all_same;
     }
     __syncthreads();
-    uint32_t at = 0, equal = 0;   // kept tokens and equal ones before the run
-    for (int i = 0; i < warp; ++i) {
-        at += s_warp[i];
-        equal += s_warp2[i];
-    }
-    at += min(equal, need);
+    uint32_t equal = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp2[lane] : 0u);
+    uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u) + min(equal, need);
     const uint32_t below = (1u << lane) - 1u;
-    for (int g = g0; g < g1; ++g) {
-        bool sure, same;
-        look(32 * g + lane, sure, same);
-        const unsigned same_mask = __ballot_sync(0xffffffffu, same);
-        const bool keep = sure || (same && equal + __popc(same_mask & below) < need);
-        const unsigned mask = __ballot_sync(0xffffffffu, keep);
-        if (keep) kept[at + __popc(mask & below)] = 32 * g + lane;
-        at += __popc(mask);
-        equal += __popc(same_mask);
+    if constexpr (KPT > 0) {
+        uint32_t ia = n_above, is = n_same;   // inclusive sums over the run's groups
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, ia, o), y = __shfl_up_sync(0xffffffffu, is, o);
+            if (lane >= o) ia += x, is += y;
+        }
+        const uint32_t e0 = equal + is - n_same;   // equal ones before this group
+        const uint32_t keep = above | (e0 < need ? lowest_bits(same, static_cast<int>(need - e0)) : 0u);
+        // (kept before it: those above, and of the equal ones what `need` allows)
+        const uint32_t first = at + (ia - n_above) + (min(e0, need) - min(equal, need));
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const uint32_t mask = __shfl_sync(0xffffffffu, keep, i), base = __shfl_sync(0xffffffffu, first, i);
+            if ((mask >> lane) & 1u) kept[base + __popc(mask & below)] = 32 * (g0 + i) + lane;
+        }
+    } else {
+        for (int g = g0; g < g1; ++g) {
+            const uint32_t k = key_at(g);
+            const uint32_t same_mask = __ballot_sync(0xffffffffu, k == prefix);
+            const bool keep = k > prefix || (k == prefix && equal + __popc(same_mask & below) < need);
+            const uint32_t mask = __ballot_sync(0xffffffffu, keep);
+            if (keep) kept[at + __popc(mask & below)] = 32 * g + lane;
+            at += __popc(mask);
+            equal += __popc(same_mask);
+        }
     }
 }
 
@@ -261,11 +300,17 @@ static int launch_move(EvictParams& p, cudaStream_t stream) {
 }
 
 int launch_evict(EvictParams p, cudaStream_t stream) {
-    static std::atomic<uint64_t> attr_done{0};
-    cudaError_t e = set_smem_attr_once(tq_evict_select_kernel, kSelKeysMax * 4, attr_done);
-    if (e != cudaSuccess) return e;
-    p.keys_held = p.max_len <= kSelKeysMax ? p.max_len : 0;
-    e = launch_pdl(tq_evict_select_kernel, dim3(p.batch * p.hkv), dim3(kSelThreads), size_t(p.keys_held) * 4, stream, p);
+    // The smallest variant that holds the keys of the longest sequence in registers; 1024
+    // threads where every unit has an SM of its own.
+    const unsigned units = static_cast<unsigned>(p.batch) * p.hkv;
+    const bool wide = units <= host::kSMs;
+    auto select = [&](auto kernel, int threads) { return launch_pdl(kernel, dim3(units), dim3(threads), 0, stream, p); };
+    cudaError_t e;
+    if (p.max_len > 32768) e = select(tq_evict_select_kernel<1024, 0>, 1024);
+    else if (p.max_len > 16384) e = select(tq_evict_select_kernel<1024, 32>, 1024);
+    else if (p.max_len > 8192) e = wide ? select(tq_evict_select_kernel<1024, 16>, 1024) : select(tq_evict_select_kernel<512, 32>, 512);
+    else if (p.max_len > 4096) e = wide ? select(tq_evict_select_kernel<1024, 8>, 1024) : select(tq_evict_select_kernel<512, 16>, 512);
+    else e = select(tq_evict_select_kernel<512, 8>, 512);
     if (e != cudaSuccess) return e;
     if (p.rbk == 256 && p.rbv == 64) return launch_move<16, 4>(p, stream);
     if (p.rbk == 256 && p.rbv == 48) return launch_move<16, 3>(p, stream);

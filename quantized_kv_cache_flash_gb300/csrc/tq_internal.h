@@ -236,7 +236,6 @@ struct EvictParams {
     uint32_t* status;
     int32_t batch, hkv, src_cap, dst_cap, rbk, rbv, max_keep, max_len, sinks, recent;
     int32_t same;             // 1: in place
-    int32_t keys_held;        // keys per CTA in shared memory
     int32_t move_ctas;        // CTAs per unit of the move to another cache
 };
 

@@ -11,13 +11,15 @@
 // then distributed as the target's own samples.  Without draft rows a child is a
 // point mass at its token.
 //
-// Decisions at a border must not depend on the order of a sum, so every value is an
-// integer: a probability is taken to 2^-56 (less than what a sum in 64-bit floating
-// point loses), sums are exact and the same however the row is split.
+// Decisions at a border need more than fp32: what is left of a token is a pair of fp32
+// numbers (differences and products with their rounding errors, 2^-48 or less off), a
+// thread's sum is such a pair, and from there on sums are integers in units of 2^-56, the
+// same however the row is split.  (Everything as 64-bit integers took 63 us for 8 trees
+// of 64 nodes over 131,072 tokens.)
 //
-// A cluster of 8 CTAs takes a sequence.  All of them walk the tree alike, on the
+// A cluster of 4 to 16 CTAs takes a sequence.  All of them walk the tree alike, on the
 // first tests' numbers, which are fetched together at the start; where a sum over
-// the vocabulary is needed each reads an eighth of the rows and the sums meet in
+// the vocabulary is needed each reads its part of the rows and the sums meet in
 // distributed shared memory.
 #include <cooperative_groups.h>
 
@@ -28,30 +30,58 @@ namespace tq {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVerCtas = 8;              // of a cluster
-constexpr int kVerThreads = 512;
+constexpr int kVerCtas = 16;             // of a cluster, at most
+constexpr int kVerThreads = 1024;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerNodes = TQ_MAX_TREE_NODES;
+constexpr int kVerGroups = 2;            // groups of 4 elements that a thread holds
+constexpr float kUnits = 72057594037927936.f;   // 2^56
 
 // What is not above 0 (a NaN) counts as 0, what is above 1 as 1.
 __device__ __forceinline__ float unit(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
-// x of [0, 1] in units of 2^-56.
-__device__ __forceinline__ uint64_t to_q56(float x) { return __float2ull_rz(unit(x) * 72057594037927936.f); }
 // A uniform number in units of 2^-64.
 __device__ __forceinline__ uint64_t to_q64(float u) {
     u = unit(u);
     return u < 1.f ? __float2ull_rz(u * 18446744073709551616.f) : ~0ull;
 }
-__device__ __forceinline__ uint64_t mul_q56(uint64_t a, uint64_t b) {
-    return (__umul64hi(a, b) << 8) | ((a * b) >> 56);
+
+// A number as a sum of two fp32 ones, |l| at most half a step of h.
+struct Two {
+    float h, l;
+};
+// In units of 2^-56 (of a number that is not below 0).
+__device__ __forceinline__ uint64_t to_q56(Two x) {
+    const long long n = __float2ll_rz(x.h * kUnits) + __float2ll_rz(x.l * kUnits);
+    return n > 0 ? static_cast<uint64_t>(n) : 0ull;
 }
-__device__ __forceinline__ uint64_t sub_to_0(uint64_t a, uint64_t b) { return a > b ? a - b : 0ull; }
+__device__ __forceinline__ Two from_q56(uint64_t n) {
+    const float h = __ull2float_rn(n) * (1.f / kUnits);
+    return Two{h, __ll2float_rn(static_cast<long long>(n) - __float2ll_rz(h * kUnits)) * (1.f / kUnits)};
+}
+__device__ __forceinline__ void add_to(Two& sum, Two x) {   // Knuth's two-sum, then the low parts
+    const float s = __fadd_rn(sum.h, x.h), v = __fsub_rn(s, sum.h);
+    const float e = __fadd_rn(__fsub_rn(sum.h, __fsub_rn(s, v)), __fsub_rn(x.h, v));
+    sum.h = s;
+    sum.l = __fadd_rn(sum.l, __fadd_rn(e, x.l));
+}
+// max(w - z q, 0)
+__device__ __forceinline__ Two less(Two w, Two z, float q) {
+    const float ph = __fmul_rn(z.h, q);
+    const float pl = __fmaf_rn(z.l, q, __fmaf_rn(z.h, q, -ph));   // (Dekker's product, with an fma)
+    const float s = __fsub_rn(w.h, ph), v = __fsub_rn(s, w.h);
+    const float e = __fsub_rn(__fsub_rn(w.h, __fsub_rn(s, v)), __fadd_rn(ph, v));
+    const float t = __fadd_rn(e, __fsub_rn(w.l, pl));
+    const float h = __fadd_rn(s, t);
+    return h > 0.f ? Two{h, __fsub_rn(t, __fsub_rn(h, s))} : Two{0.f, 0.f};
+}
 
 struct VerifyShared {
     int parent[kVerNodes];     // -1: never tried
     int token[kVerNodes];
     float u[kVerNodes], p[kVerNodes], q[kVerNodes];   // p, q: of the node's token after its parent
-    uint64_t z[kVerNodes];     // Z_k at the path's end
+    double z[kVerNodes];       // Z_k at the path's end, k > 0
+    Two z2[kVerNodes];         // the same
+    uint32_t first[kVerNodes / 32];   // bit i: accepted if it is its parent's first child to be tried
     int gone[kVerNodes];       // without draft rows: the tokens rejected there
     int path[kVerNodes];
     uint64_t warp_sum[kVerWarps];
@@ -60,16 +90,21 @@ struct VerifyShared {
     int tested;                // the child rejected last
 };
 
-// What is left of a token after k rejections.
+// What is left of a token after rejection j, from what was before.
 template <bool DRAFT>
-__device__ __forceinline__ uint64_t left_of(const VerifyShared& s, int k, float p, float q, int token) {
-    uint64_t w = to_q56(p);
-    if constexpr (DRAFT) {
-        const uint64_t d = to_q56(q);
-        for (int j = 0; j < k; ++j) w = sub_to_0(w, mul_q56(s.z[j], d));
-    } else {
-        for (int j = 0; j < k; ++j)
-            if (s.gone[j] == token) w = 0ull;
+__device__ __forceinline__ Two reject(const VerifyShared& s, int j, Two w, float q, int token) {
+    if constexpr (!DRAFT) return s.gone[j] == token ? Two{0.f, 0.f} : w;
+    if (j > 0) return less(w, s.z2[j], q);
+    const float h = __fsub_rn(w.h, q);   // (Z_0 = 1; exact with its error where p > q)
+    return h > 0.f ? Two{h, __fsub_rn(__fsub_rn(w.h, h), q)} : Two{0.f, 0.f};
+}
+// What is left of one token after k rejections, for a test.
+template <bool DRAFT>
+__device__ __forceinline__ double left_of_64(const VerifyShared& s, int k, float p, float q, int token) {
+    double w = unit(p);
+    for (int j = 0; j < k; ++j) {
+        if constexpr (DRAFT) w = fmax(w - (j == 0 ? 1.0 : s.z[j]) * double(unit(q)), 0.0);
+        else if (s.gone[j] == token) w = 0.0;
     }
     return w;
 }
@@ -88,12 +123,13 @@ __device__ __forceinline__ float4 row4(const float* base, int x, int off, int en
 }
 
 template <bool DRAFT>
-__global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads)
+__global__ void __launch_bounds__(kVerThreads, 1)
     tq_verify_kernel(const __grid_constant__ VerifyParams p) {
     __shared__ VerifyShared s;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
-    const int b = static_cast<int>(blockIdx.x) / kVerCtas;
+    const int ctas = static_cast<int>(cluster.num_blocks());
+    const int b = static_cast<int>(blockIdx.x) / ctas;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_wait();
     griddep_launch_dependents();
@@ -101,7 +137,10 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads)
 
     // ---- the nodes, and the numbers of each one's first test ----
     bool bad = false;
-    for (int i = tid; i < p.nodes; i += kVerThreads) {
+    static_assert(kVerNodes <= kVerThreads, "a node a thread");
+    bool first = false;
+    if (tid < p.nodes) {
+        const int i = tid;
         const int up = p.parents[static_cast<size_t>(b) * p.parents_per_seq + i];
         const int x = p.tokens[row0 + i];
         s.u[i] = p.uniforms[row0 + i];
@@ -112,16 +151,19 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads)
         s.parent[i] = tried ? up : -1;
         s.p[i] = tried ? __ldg(p.target + (row0 + up) * p.ld_target + x) : 0.f;
         s.q[i] = !tried ? 0.f : DRAFT ? __ldg(p.draft + (row0 + up) * p.ld_draft + x) : 1.f;
+        // (a product of 48 bits: exact)
+        first = double(unit(s.u[i])) * double(unit(s.q[i])) < double(unit(s.p[i]));
     }
+    const unsigned first_mask = __ballot_sync(0xffffffffu, first);
+    if (lane == 0 && warp < kVerNodes / 32) s.first[warp] = first_mask;
     if (bad && rank == 0) atomicOr(p.status, kStatusBadIndex);
     if (tid == 0) {
         s.cur = 0;
         s.k = 0;
         s.len = 1;
         s.path[0] = 0;
-        s.z[0] = 1ull << 56;
         // (stands where no element is found: a row without positive entries, or whose sum
-        // passes 2^8; the warp that finds one writes after a cluster barrier)
+        // passes 2^7; the warp that finds one writes after a cluster barrier)
         if (rank == 0) p.next[b] = 0;
     }
     __syncthreads();
@@ -130,28 +172,52 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads)
     // (a contiguous run of elements a warp); then over the cluster.
     int sweeps = 0;
     int run0 = 0, run1 = 0, off = 0;   // this warp's groups of 4 elements; the row's offset
-    auto left4 = [&](const float* pr, const float* qr, int x, int k, bool aligned, uint64_t (&w)[4]) {
+    const float *pr = nullptr, *qr = nullptr;
+    bool aligned = true;
+    // a batch of groups x0 + lane + 32 i: what is left of the target's numbers, the draft's
+    Two w[kVerGroups][4];
+    float q[kVerGroups][4];
+    auto load = [&](int x0) {
         const int end = off + p.vocab;
-        const float4 a = row4(pr, x, off, end);
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (DRAFT) {
-            if (k > 0) {
-                if (aligned) {
-                    const float4 v = row4(qr, x, off, end);
-                    d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
-                } else {
+        float4 a[kVerGroups], d[kVerGroups];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (4 * x + e >= off && 4 * x + e < end) d[e] = __ldg(qr + 4 * x + e);
+        for (int i = 0; i < kVerGroups; ++i) {
+            const int x = x0 + lane + 32 * i;
+            a[i] = d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < run1) {
+                a[i] = row4(pr, x, off, end);
+                if constexpr (DRAFT) {
+                    if (aligned) {
+                        d[i] = row4(qr, x, off, end);
+                    } else {
+                        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (4 * x + e >= off && 4 * x + e < end) v[e] = __ldg(qr + 4 * x + e);
+                        d[i] = make_float4(v[0], v[1], v[2], v[3]);
+                    }
                 }
             }
         }
-        const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = left_of<DRAFT>(s, k, av[e], d[e], 4 * x + e - off);
+        for (int i = 0; i < kVerGroups; ++i) {
+            const float av[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, dv[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[i][e] = Two{unit(av[e]), 0.f};
+                q[i][e] = unit(dv[e]);
+            }
+        }
     };
-    const float *pr = nullptr, *qr = nullptr;
-    bool aligned = true;
+    auto apply = [&](int x0, int j0, int j1) {   // rejections j0 .. j1 - 1
+#pragma unroll 1
+        for (int j = j0; j < j1; ++j)
+#pragma unroll
+            for (int i = 0; i < kVerGroups; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[i][e] = reject<DRAFT>(s, j, w[i][e], q[i][e], 4 * (x0 + lane + 32 * i) + e - off);
+    };
     auto rows_of = [&](int cur) {
         const float* a = p.target + (row0 + cur) * p.ld_target;
         off = static_cast<int>((reinterpret_cast<uintptr_t>(a) >> 2) & 3);
@@ -161,49 +227,66 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads)
             aligned = (reinterpret_cast<uintptr_t>(qr) & 15u) == 0;
         }
         const int groups = (off + p.vocab + 3) / 4;
-        const int per = (groups + kVerCtas * kVerWarps - 1) / (kVerCtas * kVerWarps);
+        const int per = (groups + ctas * kVerWarps - 1) / (ctas * kVerWarps);
         run0 = min(groups, (rank * kVerWarps + warp) * per);
         run1 = min(groups, run0 + per);
+        return per <= 32 * kVerGroups;
     };
+    bool held = false;            // the batch is the warp's whole run of the row,
+    int held_cur = -1, held_k = 0;  // of this node after that many rejections
     auto sweep = [&](int cur, int k) {
-        rows_of(cur);
-        uint64_t sum = 0;
-        for (int x = run0 + lane; x < run1; x += 32) {
-            uint64_t w[4];
-            left4(pr, qr, x, k, aligned, w);
-            sum += (w[0] + w[1]) + (w[2] + w[3]);
+        held = rows_of(cur);
+        Two part{0.f, 0.f};
+        for (int x0 = run0; x0 < run1; x0 += 32 * kVerGroups) {
+            if (!held || held_cur != cur || held_k > k) {
+                load(x0);
+                held_k = 0;
+            }
+            apply(x0, held_k, k);
+#pragma unroll
+            for (int i = 0; i < kVerGroups; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) add_to(part, w[i][e]);
         }
+        held_cur = cur;
+        held_k = k;
+        uint64_t sum = to_q56(part);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) s.warp_sum[warp] = sum;
         __syncthreads();
         const int par = sweeps++ & 1;
-        if (tid < kVerCtas) {
-            uint64_t all = 0;
-            for (int i = 0; i < kVerWarps; ++i) all += s.warp_sum[i];
+        if (warp == 0) {
+            uint64_t all = lane < kVerWarps ? s.warp_sum[lane] : 0ull;
+#pragma unroll
+            for (int o = kVerWarps / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
             // (two slots: a CTA may be at its next sweep before another has read this one)
-            *cluster.map_shared_rank(&s.cta_sum[par][rank], tid) = all;
+            if (lane < ctas) *cluster.map_shared_rank(&s.cta_sum[par][rank], lane) = all;
         }
         cluster.sync();
-        uint64_t all = 0;
-        for (int i = 0; i < kVerCtas; ++i) all += s.cta_sum[par][i];
-        return all;
+    };
+    // The whole of the last sweep, for every lane of a warp.
+    auto whole = [&]() {
+        uint64_t all = lane < ctas ? s.cta_sum[(sweeps - 1) & 1][lane] : 0ull;
+#pragma unroll
+        for (int o = kVerCtas / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        return __shfl_sync(0xffffffffu, all, 0);
     };
 
     // ---- the walk ----
+    const int up0 = lane < p.nodes ? s.parent[lane] : -1;   // (the first 32 nodes' at hand)
     for (;;) {
         if (warp == 0) {
             int cur = s.cur, k = s.k, len = s.len;
-            int tested = len > 1 ? s.path[len - 1] : 0;
-            if (k > 0) tested = s.tested;
+            int tested = k > 0 ? s.tested : cur;   // (children come after their parent)
             int done = 0;
             for (;;) {
                 int child = -1;
-                for (int w = (tested + 1) & ~31; w < p.nodes && child < 0; w += 32) {
-                    const int i = w + lane;
-                    const unsigned hit =
-                        __ballot_sync(0xffffffffu, i > tested && i < p.nodes && s.parent[i] == cur);
-                    if (hit) child = w + __ffs(hit) - 1;
+                for (int x = (tested + 1) & ~31; x < p.nodes && child < 0; x += 32) {
+                    const int i = x + lane;
+                    const int up = x == 0 ? up0 : i < p.nodes ? s.parent[i] : -1;
+                    const unsigned hit = __ballot_sync(0xffffffffu, i > tested && up == cur);
+                    if (hit) child = x + __ffs(hit) - 1;
                 }
                 if (child < 0) {
                     done = 1;
@@ -211,11 +294,11 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads)
                 }
                 tested = child;
                 bool yes;
-                if (k == 0) {   // (a product of 48 bits: exact)
-                    yes = double(unit(s.u[child])) * double(unit(s.q[child])) < double(unit(s.p[child]));
+                if (k == 0) {
+                    yes = (s.first[child >> 5] >> (child & 31)) & 1u;
                 } else {
-                    const uint64_t w = left_of<DRAFT>(s, k, s.p[child], s.q[child], s.token[child]);
-                    yes = __umul64hi(to_q64(s.u[child]), mul_q56(s.z[k], to_q56(s.q[child]))) < w;
+                    const double left = left_of_64<DRAFT>(s, k, s.p[child], s.q[child], s.token[child]);
+                    yes = double(unit(s.u[child])) * double(unit(s.q[child])) * s.z[k] < left;
                 }
                 if (!yes) break;   // (the sum of what is left comes next)
                 cur = child;
@@ -239,61 +322,79 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads)
         }
         __syncthreads();
         if (s.done) break;
-        const int k = s.k;
-        const uint64_t z = sweep(s.cur, k);
-        __syncthreads();
-        if (tid == 0) s.z[k] = z;
-        __syncthreads();
+        sweep(s.cur, s.k);
+        if (warp == 0) {
+            const uint64_t z = whole();
+            if (lane == 0) {
+                s.z[s.k] = double(z) / kUnits;
+                s.z2[s.k] = from_q56(z);
+            }
+            __syncwarp();
+        }
     }
 
     // ---- the token that follows ----
     int k = s.k;
     const int cur = s.cur;
     // (after a rejection the last sweep left its sums)
-    uint64_t all = 0;
-    if (k > 0) {
-        for (int i = 0; i < kVerCtas; ++i) all += s.cta_sum[(sweeps - 1) & 1][i];
-    }
+    uint64_t all = k > 0 ? whole() : 0ull;
     if (all == 0) {   // a leaf, or nothing left: the target's row itself
         k = 0;
-        all = sweep(cur, 0);
-        __syncthreads();
+        sweep(cur, 0);
+        all = whole();
     }
     if (all == 0) {
         if (rank == 0 && tid == 0) atomicOr(p.status, kStatusBadValue);
     } else {
         uint64_t t = __umul64hi(to_q64(s.u[0]), all);
         // the CTA, the warp and the element whose running sum passes t < all
-        uint64_t before = 0;
-        for (int i = 0; i < rank; ++i) before += s.cta_sum[(sweeps - 1) & 1][i];
-        for (int i = 0; i < warp; ++i) before += s.warp_sum[i];
+        uint64_t before = (lane < rank ? s.cta_sum[(sweeps - 1) & 1][lane] : 0ull) + (lane < warp ? s.warp_sum[lane] : 0ull);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
         if (t >= before && t - before < s.warp_sum[warp]) {   // (one warp of the cluster)
             t -= before;
-            for (int x0 = run0; x0 < run1; x0 += 32) {
-                uint64_t w[4] = {0, 0, 0, 0};
-                if (x0 + lane < run1) left4(pr, qr, x0 + lane, k, aligned, w);
-                const uint64_t own = (w[0] + w[1]) + (w[2] + w[3]);
-                uint64_t inc = own;
+            bool found = false;
+            int last = -1;   // the last token with anything left, so far
+            for (int x0 = run0; x0 < run1 && !found; x0 += 32 * kVerGroups) {
+                if (!held) {
+                    load(x0);
+                    apply(x0, 0, k);
+                }
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += y;
-                }
-                const unsigned hit = __ballot_sync(0xffffffffu, inc > t);
-                if (hit) {
-                    if (lane == __ffs(hit) - 1) {
-                        uint64_t run = inc - own;
-                        int e = 0;
-                        for (; e < 3; ++e) {
-                            run += w[e];
-                            if (run > t) break;
-                        }
-                        p.next[b] = min(4 * (x0 + lane) + e - off, p.vocab - 1);
+                for (int i = 0; i < kVerGroups; ++i) {
+                    const int at = 4 * (x0 + lane + 32 * i) - off;   // the first of the lane's four tokens
+                    uint64_t n[4], own = 0;
+                    int mine = -1;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        own += n[e] = to_q56(w[i][e]);
+                        if (w[i][e].h > 0.f) mine = at + e;
                     }
-                    break;
+                    uint64_t inc = own;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                        if (lane >= o) inc += y;
+                    }
+                    const unsigned hit = __ballot_sync(0xffffffffu, inc > t);
+                    if (hit && !found) {
+                        if (lane == __ffs(hit) - 1) {
+                            uint64_t run = inc - own;
+                            int e = 0;
+                            for (; e < 3; ++e) {
+                                run += n[e];
+                                if (run > t) break;
+                            }
+                            p.next[b] = min(at + e, p.vocab - 1);
+                        }
+                        found = true;
+                    }
+                    last = max(last, __reduce_max_sync(0xffffffffu, mine));
+                    t -= __shfl_sync(0xffffffffu, inc, 31);
                 }
-                t -= __shfl_sync(0xffffffffu, inc, 31);
             }
+            // (the threads' sums and these differ in the last places: t may lie between)
+            if (!found && last >= 0 && lane == 0) p.next[b] = last;
         }
     }
     if (rank == 0) {
@@ -303,10 +404,38 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads)
     cluster.sync();   // (no CTA leaves while another may still write to its shared memory)
 }
 
+template <bool DRAFT>
+static int launch_t(const VerifyParams& p, cudaStream_t stream) {
+    static std::atomic<uint64_t> attr_done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (bit == 0 || (attr_done.load(std::memory_order_acquire) & bit) == 0) {
+        e = cudaFuncSetAttribute(tq_verify_kernel<DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        attr_done.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    // as many CTAs as fit at once, one per SM
+    int ctas = kVerCtas;
+    while (ctas > 1 && 1ll * p.batch * ctas > host::kSMs) ctas /= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * ctas);
+    cfg.blockDim = dim3(kVerThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, tq_verify_kernel<DRAFT>, p);
+}
+
 int launch_verify(const VerifyParams& p, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(p.batch) * kVerCtas);
-    if (p.draft != nullptr) return launch_pdl(tq_verify_kernel<true>, grid, dim3(kVerThreads), 0, stream, p);
-    return launch_pdl(tq_verify_kernel<false>, grid, dim3(kVerThreads), 0, stream, p);
+    return p.draft != nullptr ? launch_t<true>(p, stream) : launch_t<false>(p, stream);
 }
 
 }  // namespace tq
