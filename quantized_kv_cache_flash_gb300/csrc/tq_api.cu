@@ -1158,7 +1158,7 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
     if (!(decay >= 0.f) || !std::isfinite(decay)) return TQ_ERR_INVALID_ARG;
     const int group = num_q_heads / c->num_kv_heads;
     const long long rows = 1ll * group * tq_rows, units = 1ll * c->batch * c->num_kv_heads;
-    if (rows >= (1ll << 31) - 256 || units > 65535) return TQ_ERR_UNSUPPORTED;
+    if (rows * units >= (1ll << 31) - 256 || units > 65535) return TQ_ERR_UNSUPPORTED;
     tq_ctx* ctx;
     if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
     if ((r = prepare_tables(ctx, c, kb, vb)) != TQ_OK) return r;
@@ -1209,8 +1209,8 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
     // Pairs of query tiles in blocks whose workspace stays below kWeightsWork (64-bit
     // rows * tokens otherwise); one pair needs no sums per pair.
     const long long pairs = (rows + 255) / 256, tiles = (max_len_hint + 127) / 128;
-    const size_t q_pair = kb == 16 ? 65536 : 131072;
-    const size_t per_pair = size_t(units) * (q_pair + 256 * 12 + (pairs > 1 ? size_t(tiles) * 512 : 0));
+    const size_t q_pair = kb == 16 ? 0 : 131072;   // (fp16 K: read from q)
+    const size_t per_pair = size_t(units) * (q_pair + 256 * 8 + (pairs > 1 ? size_t(tiles) * 512 : 0));
     const long long block = std::max<long long>(
         1, std::min<long long>(pairs, std::min<long long>(kWeightsWork / per_pair, (1ll << 30) / (units * tiles))));
     const int ctas = int(std::min<long long>(tq::host::kSMs, units * block * tiles));
@@ -1226,8 +1226,6 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
     work += size_t(units) * block * q_pair;
     p.part_ml = reinterpret_cast<float2*>(work);
     work += (size_t(units) * block + ctas) * 2048;
-    p.lse = reinterpret_cast<float*>(work);
-    work += size_t(units) * block * 1024;
     p.part_w = pairs > 1 ? reinterpret_cast<float*>(work) : nullptr;
     p.part_len = int32_t(tiles * 128);
     p.status = ctx->d_words;
@@ -1243,10 +1241,15 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
     p.decay = decay;
     if (kb != 16) std::memcpy(p.ktab, ctx->ktab.tab, sizeof(p.ktab));
     std::memcpy(p.signs, ctx->signs, sizeof(p.signs));
+    CUtensorMap qmap;
+    if (kb == 16) {
+        r = tq::host::encode_rows_map(&qmap, q, uint64_t(c->batch) * num_q_heads * tq_rows);
+        if (r != TQ_OK) return r;
+    }
     for (long long q0 = 0; q0 < pairs; q0 += block) {
         p.pair0 = int32_t(q0);
         p.pairs = int32_t(std::min(block, pairs - q0));
-        const int e = tq::launch_weights(kb, p, kmap, s);
+        const int e = tq::launch_weights(kb, p, kmap, kb == 16 ? &qmap : &dummy, s);
         if (e != 0) return TQ_ERR_CUDA;
     }
     return TQ_OK;

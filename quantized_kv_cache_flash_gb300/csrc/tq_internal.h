@@ -178,8 +178,8 @@ struct CopyParams {
 };
 
 // The softmax weights that tokens get (see tq_attention_weights).  A row of a (batch, KV
-// head) unit is query position * group + head of the group; 256 rows are a pair of query
-// tiles.  A call takes the pairs pair0 .. pair0 + pairs - 1.
+// head) unit is head of the group * tq + query position; 256 rows are a pair of query tiles.
+//  A call takes the pairs pair0 .. pair0 + pairs - 1.
 struct WeightsParams {
     const uint8_t* k_codes;   // packed K codes (fp16 K: read through the tensor map)
     const __half* k_norm;
@@ -188,9 +188,8 @@ struct WeightsParams {
     const int32_t* seen;      // [B] tokens that have a weight already, or null: all but the last tq
     float* weights;           // [B, Hkv, cap]
     // workspace
-    uint8_t* q_tiles;         // [units][pairs][2] Q' tiles: q_hi, q_lo (fp16 K: q), 32 KB each
+    uint8_t* q_tiles;         // [units][pairs][2] Q' tiles: q_hi, q_lo, 32 KB each (quantized K)
     float2* part_ml;          // [ctas + units * pairs][256] a run's (maximum, sum) of each row
-    float* lse;               // [batch][pairs][hkv][256]
     float* part_w;            // [units][pairs][part_len] sums per pair; null: one pair, added at once
     uint32_t* status;
     int32_t batch, hkv, hq, group, tq, rows, cap, max_len;
@@ -293,7 +292,8 @@ int launch_compact(const CompactParams& p, cudaStream_t stream);
 // CTAs = pairs * hkv * ceil(max_len / kCopyTokens), below 2^31
 constexpr int kCopyTokens = 256;
 int launch_copy(const CopyParams& p, cudaStream_t stream);
-int launch_weights(int kbits, const WeightsParams& p, const CUtensorMap* kmap, cudaStream_t stream);
+int launch_weights(int kbits, const WeightsParams& p, const CUtensorMap* kmap, const CUtensorMap* qmap,
+                   cudaStream_t stream);
 int launch_weights_step(int kbits, int group_rows, const StepParams& p, const CUtensorMap* kmap, cudaStream_t stream);
 int weights_step_ctas_per_sm(int kbits, int group_rows);
 constexpr int kEvictMoveCtas = 8;   // of the cluster that moves a unit's records in place

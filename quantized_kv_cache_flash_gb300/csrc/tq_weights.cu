@@ -1,11 +1,10 @@
 // The softmax weights that cached tokens get from a block of queries
 // (tq_attention_weights), on the 5th-generation tensor cores.
 //
-// Per (batch, KV head) unit the rows are query position * group + head of the group, a
-// pair of 128-row query tiles at a time.  A token's sum needs every row's normaliser, so
+// Per (batch, KV head) unit the rows are head of the group * tq + query position (as q lies
+// in memory), a pair of 128-row query tiles at a time.  A token's sum needs every row's normaliser, so
 // the scores are taken twice:
-//   stats  S[128 rows x 128 tok] = Q' . K^T     a thread a row: its maximum and sum of exp2
-//   lse    the partial sums of a row's tokens joined
+//   stats  S[128 rows x 128 tok] = Q' . K^T     a thread a row: its sum of exp2 (of a base)
 //   sum    S[128 tok x 128 rows] = K . Q'^T     a thread a token: sum of exp2(s - lse[row])
 // Both orientations read the same tiles (Q' and K are K-major either way), and neither
 // needs a value of another lane.  Q' = Rot(q) as q_hi + q_lo (quantized K, whose tile
@@ -41,10 +40,11 @@ struct WtCfg {
     static constexpr int kStgOff = kKOff + kSlots * 32768;      // records and norms [2]
     static constexpr int kStg = (KB == 0) ? 0 : kWtTile * kRbK + 256;
     static constexpr int kColOff = kStgOff + 2 * kStg;          // fp32 n_k * scale * log2(e) [2][128]
-    static constexpr int kLseOff = kColOff + 1024;              // fp32 [256]
+    static constexpr int kLseOff = kColOff + 1024;              // fp32 -log2(sum) of a row [256]
+    static constexpr int kPosOff = kLseOff + 1024;              // query position of a row [256]
     // records copied [2], records read [2], K stored [kSlots], K read [kSlots], S done
     // [2], S read [2], Q' copied; the TMEM slot
-    static constexpr int kBarOff = kLseOff + 1024;
+    static constexpr int kBarOff = kPosOff + 1024;
     static constexpr int kSmem = kBarOff + (9 + 2 * kSlots) * 8 + 8;
     static constexpr int kSmemAlloc = kSmem + 768;              // to a 1024-byte boundary from a 256-byte one
     static_assert(kSmemAlloc <= 232448, "227 KB per CTA");
@@ -54,33 +54,35 @@ struct WtCfg {
 // A unit's part of a CTA's run: K tiles [k0, k1) of (sequence b, KV head h, pair).
 struct WtSeg {
     int b, h, pair, k0, k1, L;
+    int nt, base;   // the unit's tiles, and those of the units before it
 };
 
+// Smallest and largest query position of rows r0 .. r1.
+__device__ __forceinline__ int2 wt_span(const WeightsParams& p, int r0, int r1) {
+    const int g0 = r0 / p.tq, g1 = r1 / p.tq;
+    return g0 == g1 ? make_int2(r0 - g0 * p.tq, r1 - g1 * p.tq) : make_int2(0, p.tq - 1);
+}
 // K tiles that the rows of a pair see.
 __device__ __forceinline__ int wt_tiles(const WeightsParams& p, int L, int pair) {
-    const int r_hi = min(p.rows, 256 * (pair + 1)) - 1;
-    const int last = min(min(L, p.max_len) - 1, L - p.tq + r_hi / p.group);
+    const int j_hi = wt_span(p, 256 * pair, min(p.rows, 256 * (pair + 1)) - 1).y;
+    const int last = min(min(L, p.max_len) - 1, L - p.tq + j_hi);
     return last < 0 ? 0 : last / kWtTile + 1;
 }
 
-// Sums over the (sequence, pair) groups, by a warp: the tiles of all of them over the
-// KV heads, and (want >= 0) of those before group `want`.
-__device__ __forceinline__ void wt_total(const WeightsParams& p, int lane, int want, int& all, int& before) {
+// The tiles of all (sequence, pair) groups over the KV heads, by a warp.
+__device__ __forceinline__ void wt_total(const WeightsParams& p, int lane, int& all) {
     const int groups = p.batch * p.pairs;
-    all = before = 0;
+    all = 0;
     for (int g = lane; g < groups; g += 32) {
         const int b = g / p.pairs;
-        const int n = p.hkv * wt_tiles(p, p.lengths[b], p.pair0 + g - b * p.pairs);
-        all += n;
-        if (g < want) before += n;
+        all += p.hkv * wt_tiles(p, p.lengths[b], p.pair0 + g - b * p.pairs);
     }
     all = __reduce_add_sync(0xffffffffu, all);
-    before = __reduce_add_sync(0xffffffffu, before);
 }
 
 // A CTA's run [pos, hi) of the tiles, unit after unit; each warp keeps its own.
 struct WtRun {
-    int pos, hi;
+    int pos, hi, all;
     int b, pair, h, tile, L, nt;
 
     __device__ __forceinline__ void enter(const WeightsParams& p) {   // L and nt of (b, pair), past empty ones
@@ -91,8 +93,7 @@ struct WtRun {
         }
     }
     __device__ __forceinline__ void start(const WeightsParams& p, int lane) {
-        int all, none;
-        wt_total(p, lane, -1, all, none);
+        wt_total(p, lane, all);
         const long long c = blockIdx.x;
         pos = static_cast<int>(c * all / gridDim.x);
         hi = static_cast<int>((c + 1) * all / gridDim.x);
@@ -126,7 +127,7 @@ struct WtRun {
     }
     __device__ __forceinline__ bool next(const WeightsParams& p, WtSeg& s) {
         if (pos >= hi) return false;
-        s = WtSeg{b, h, pair, tile, min(nt, tile + hi - pos), L};
+        s = WtSeg{b, h, pair, tile, min(nt, tile + hi - pos), L, nt, pos - tile};
         pos += s.k1 - s.k0;
         tile = 0;
         if (++h == p.hkv) {
@@ -138,8 +139,7 @@ struct WtRun {
     }
 };
 
-// Rot(q) as q_hi and q_lo (quantized K), or q, in the MMA layout; a warp a row.
-template <bool QUANT>
+// Rot(q) as q_hi and q_lo in the MMA layout (quantized K); a warp a row.
 __global__ void __launch_bounds__(256) tq_weights_rows_kernel(const __grid_constant__ WeightsParams p) {
     const int lane = threadIdx.x & 31;
     const int per = p.pairs * 256;
@@ -150,35 +150,32 @@ __global__ void __launch_bounds__(256) tq_weights_rows_kernel(const __grid_const
     const int b = unit / p.hkv, h = unit - b * p.hkv, r = p.pair0 * 256 + rl;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (r < p.rows) {
-        const int j = r / p.group, g = r - j * p.group;
         const uint2 w = *reinterpret_cast<const uint2*>(
-            p.q + ((static_cast<size_t>(b) * p.hq + h * p.group + g) * p.tq + j) * kD + 4 * lane);
+            p.q + ((static_cast<size_t>(b) * p.hq + h * p.group) * p.tq + r) * kD + 4 * lane);
         const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
         const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
         v[0] = f0.x, v[1] = f0.y, v[2] = f1.x, v[3] = f1.y;
-        if constexpr (QUANT) {
-            const uint32_t sn = sign_nibble(p.signs, lane);
+        const uint32_t sn = sign_nibble(p.signs, lane);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = ((sn >> i) & 1u) ? -v[i] : v[i];
-            wht128_lane4(v, lane);
+        for (int i = 0; i < 4; ++i) v[i] = ((sn >> i) & 1u) ? -v[i] : v[i];
+        wht128_lane4(v, lane);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] *= 0.08838834764831845f;   // 1/sqrt(128)
-        }
+        for (int i = 0; i < 4; ++i) v[i] *= 0.08838834764831845f;   // 1/sqrt(128)
     }
-    uint8_t* tile = p.q_tiles + (static_cast<size_t>(unit) * (per / 128) + rl / 128) * (QUANT ? 65536 : 32768);
+    uint8_t* tile = p.q_tiles + (static_cast<size_t>(unit) * (per / 128) + rl / 128) * 65536;
     const uint2 hi = make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
     *reinterpret_cast<uint2*>(tile + sw128_offset(rl & 127, 4 * lane)) = hi;
-    if constexpr (QUANT) {   // q_lo = Rot(q) - q_hi (exact in fp32), rounded once more
-        const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&hi.x));
-        const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&hi.y));
-        *reinterpret_cast<uint2*>(tile + 32768 + sw128_offset(rl & 127, 4 * lane)) =
-            make_uint2(pack_half2(v[0] - h0.x, v[1] - h0.y), pack_half2(v[2] - h1.x, v[3] - h1.y));
-    }
+    // q_lo = Rot(q) - q_hi (exact in fp32), rounded once more
+    const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&hi.x));
+    const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&hi.y));
+    *reinterpret_cast<uint2*>(tile + 32768 + sw128_offset(rl & 127, 4 * lane)) =
+        make_uint2(pack_half2(v[0] - h0.x, v[1] - h0.y), pack_half2(v[2] - h1.x, v[3] - h1.y));
 }
 
 template <int KB, bool SUM>
 __global__ void __launch_bounds__(kWtThreads, 1)
-    tq_weights_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap kmap) {
+    tq_weights_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap qmap) {
     using C = WtCfg<KB>;
     constexpr int NS = C::kSlots;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -187,6 +184,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     float* s_col = reinterpret_cast<float*>(smem + C::kColOff);
     float* s_lse = reinterpret_cast<float*>(smem + C::kLseOff);
+    int* s_pos = reinterpret_cast<int*>(smem + C::kPosOff);
     const uint32_t bar_stg = smem_u32(smem + C::kBarOff), bar_stgf = bar_stg + 16, bar_s = bar_stg + 32,
                    bar_sf = bar_stg + 48, bar_q = bar_stg + 64, bar_k = bar_stg + 72, bar_kf = bar_k + 8 * NS;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (9 + 2 * NS) * 8);
@@ -204,9 +202,17 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         mbar_init(bar_q, 1);
         fence_barrier_init();
     }
-    if (KB == 0 && tid == 0) prefetch_tensormap(&kmap);
+    if (KB == 0 && tid == 0) {
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&qmap);
+    }
     griddep_wait();
     griddep_launch_dependents();
+    if (!SUM && p.pair0 == 0 && blockIdx.x == 0 && warp == 14) {   // rows that see no token
+        bool none = false;
+        for (int b = lane; b < p.batch; b += 32) none = none || p.lengths[b] < p.tq;
+        if (none) atomicOr(p.status, kStatusShortContext);
+    }
     WtRun run;
     run.start(p, lane);
     if (run.pos >= run.hi) return;   // (uniform over the CTA; nothing allocated yet)
@@ -230,53 +236,86 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const int row0 = (p.pair0 + s.pair) * 256;            // the pair's first row
             const int unit = (s.b * p.pairs + s.pair) * p.hkv + s.h;
             if constexpr (SUM) {
-                named_bar_sync(1, 256);   // (the unit before is done with its values)
-                s_lse[tid] = p.lse[static_cast<size_t>(unit) * 256 + tid];
-                named_bar_sync(1, 256);
                 const int nrows = min(256, p.rows - row0);
+                named_bar_sync(1, 256);   // (the unit before is done with its values)
+                // the row's partial sums joined (rows without any: hidden below)
+                {
+                    const long long all = run.all, P = gridDim.x;
+                    const int c0 = static_cast<int>(((s.base + 1ll) * P - 1) / all);
+                    const int c1 = static_cast<int>(((s.base + 0ll + s.nt) * P - 1) / all);
+                    const float2* ml = p.part_ml + static_cast<size_t>(unit) * 256 + tid;
+                    float M = -INFINITY, sum = 0.f;
+                    for (int c = c0; c <= c1; ++c) {
+                        if (c * all / P >= (c + 1) * all / P) continue;   // (an empty run wrote nothing)
+                        const float2 x = __ldcg(ml + static_cast<size_t>(c) * 256);
+                        const float mn = fmaxf(M, x.x);
+                        sum = (M == -INFINITY ? sum : sum * fast_exp2(M - mn)) +
+                              (x.x == -INFINITY ? x.y : x.y * fast_exp2(x.x - mn));
+                        M = mn;
+                    }
+                    s_lse[tid] = -(M + log2f(sum));
+                    s_pos[tid] = tid < nrows ? (row0 + tid) % p.tq : -0x40000000;
+                }
+                named_bar_sync(1, 256);
                 // tokens that every row of the pair sees
-                const int all_see = s.L - p.tq + row0 / p.group;
+                const int all_see = s.L - p.tq + wt_span(p, row0, row0 + nrows - 1).x;
                 const int seen = p.seen != nullptr ? p.seen[s.b] : s.L - p.tq;
+                const int chunks = (nrows + 31) / 32;
                 for (int k = s.k0; k < s.k1; ++k, ++n) {
                     if ((n & 1) != wg) continue;
                     wait(bar_s + 8 * wg, (n >> 1) & 1);
                     tc_fence_after();
                     const int t = k * kWtTile + r;
                     const float c = KB == 0 ? p.scale_log2e : s_col[128 * wg + r];
-                    // rows [lo, nrows) see this token
-                    const long long lo = static_cast<long long>(t - (s.L - p.tq)) * p.group - row0;
-                    const bool masked = k * kWtTile + kWtTile - 1 > all_see;
-                    float w = 0.f;
-                    for (int x = 0; x < nrows; x += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(tmem + 256 * wg + x + lane_off, v);
-                        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-                        const float4* ls = reinterpret_cast<const float4*>(s_lse + x);
-                        if (masked || x + 32 > nrows) {
+                    const uint32_t d = tmem + 256 * wg + lane_off;
+                    float w;
+                    if (k * kWtTile + kWtTile - 1 > all_see || (nrows & 31) != 0) {
+                        const int from = t - (s.L - p.tq);   // the first query position that sees the token
+                        w = 0.f;
+#pragma unroll 1
+                        for (int x = 0; x < nrows; x += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(d + x, v);
+                            float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 l = ls[e];
-                                const float y0 = fast_exp2(fmaf(__uint_as_float(v[4 * e]), c, -l.x));
-                                const float y1 = fast_exp2(fmaf(__uint_as_float(v[4 * e + 1]), c, -l.y));
-                                const float y2 = fast_exp2(fmaf(__uint_as_float(v[4 * e + 2]), c, -l.z));
-                                const float y3 = fast_exp2(fmaf(__uint_as_float(v[4 * e + 3]), c, -l.w));
-                                const int q = x + 4 * e;
-                                if (q >= lo && q < nrows) a0 += y0;
-                                if (q + 1 >= lo && q + 1 < nrows) a1 += y1;
-                                if (q + 2 >= lo && q + 2 < nrows) a2 += y2;
-                                if (q + 3 >= lo && q + 3 < nrows) a3 += y3;
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 l = *reinterpret_cast<const float4*>(s_lse + x + e);
+                                const int4 j = *reinterpret_cast<const int4*>(s_pos + x + e);
+                                const float y[4] = {l.x, l.y, l.z, l.w};
+                                const int jj[4] = {j.x, j.y, j.z, j.w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float z = fast_exp2(fmaf(__uint_as_float(v[e + i]), c, y[i]));
+                                    if (jj[i] >= from && jj[i] >= 0) a[i] += z;
+                                }
                             }
-                        } else {
+                            w += (a[0] + a[1]) + (a[2] + a[3]);
+                        }
+                    } else {
+                        const float2 cc = make_float2(c, c);
+                        float2 a[4] = {};
+                        uint32_t v[2][32];   // 32 rows at a time, the next ones in flight
+                        tmem_ld32_issue(d, v[0]);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 l = ls[e];
-                                a0 += fast_exp2(fmaf(__uint_as_float(v[4 * e]), c, -l.x));
-                                a1 += fast_exp2(fmaf(__uint_as_float(v[4 * e + 1]), c, -l.y));
-                                a2 += fast_exp2(fmaf(__uint_as_float(v[4 * e + 2]), c, -l.z));
-                                a3 += fast_exp2(fmaf(__uint_as_float(v[4 * e + 3]), c, -l.w));
+                        for (int x = 0; x < 8; ++x) {
+                            if (x >= chunks) break;
+                            tmem_ld_wait(v[x & 1]);
+                            if (x + 1 < chunks) tmem_ld32_issue(d + 32 * (x + 1), v[(x + 1) & 1]);
+                            const uint32_t* f = v[x & 1];
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 l = *reinterpret_cast<const float4*>(s_lse + 32 * x + e);
+                                const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(f[e]), __uint_as_float(f[e + 1])),
+                                                             cc, make_float2(l.x, l.y));
+                                const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(f[e + 2]), __uint_as_float(f[e + 3])),
+                                                             cc, make_float2(l.z, l.w));
+                                a[(e >> 1) & 3] = __fadd2_rn(a[(e >> 1) & 3], make_float2(fast_exp2(y0.x), fast_exp2(y0.y)));
+                                a[((e >> 1) & 3) + 1] =
+                                    __fadd2_rn(a[((e >> 1) & 3) + 1], make_float2(fast_exp2(y1.x), fast_exp2(y1.y)));
                             }
                         }
-                        w += (a0 + a1) + (a2 + a3);
+                        const float2 t2 = __fadd2_rn(__fadd2_rn(a[0], a[1]), __fadd2_rn(a[2], a[3]));
+                        w = t2.x + t2.y;
                     }
                     tc_fence_before();
                     mbar_arrive(bar_sf + 8 * wg);
@@ -292,38 +331,65 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             } else {
                 // rows of query tile wg: last visible token of this row, and of all of them
                 const int first = row0 + 128 * wg, row = first + r;
-                const int mine = row < p.rows ? min(s.L - p.tq + row / p.group, lim - 1) : -1;
-                const int all_see = first + 127 < p.rows ? min(s.L - p.tq + first / p.group, lim - 1) : -1;
+                const int mine = row < p.rows ? min(s.L - p.tq + row % p.tq, lim - 1) : -1;
+                const int all_see =
+                    first + 127 < p.rows ? min(s.L - p.tq + wt_span(p, first, first + 127).x, lim - 1) : -1;
                 const bool any = first < p.rows;
+                // A row's base m is the largest score of the tile that it first sees; later
+                // scores may pass it, as long as the sums stay in range.
                 float m = -INFINITY, l = 0.f;
                 for (int k = s.k0; k < s.k1; ++k, ++n) {
                     const int buf = n & 1;
                     wait(bar_s + 8 * buf, (n >> 1) & 1);
                     tc_fence_after();
-                    if (any) {
-                        const bool masked = k * kWtTile + kWtTile - 1 > all_see;
+                    const uint32_t d = tmem + 256 * buf + 128 * wg + lane_off;
+                    const float* col = s_col + 128 * buf;
+                    const bool masked = k * kWtTile + kWtTile - 1 > all_see;
+                    bool slow = any && (masked || __any_sync(0xffffffffu, m == -INFINITY));
+                    if (any && !slow) {
+                        const float2 nb = make_float2(-m, -m);
+                        float2 a[4] = {};
+                        uint32_t v[2][32];   // 32 tokens at a time, the next ones in flight
+                        tmem_ld32_issue(d, v[0]);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            tmem_ld_wait(v[x & 1]);
+                            if (x < 3) tmem_ld32_issue(d + 32 * (x + 1), v[(x + 1) & 1]);
+                            const uint32_t* f = v[x & 1];
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 c = KB == 0 ? make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e,
+                                                                       p.scale_log2e)
+                                                         : *reinterpret_cast<const float4*>(col + 32 * x + e);
+                                const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(f[e]), __uint_as_float(f[e + 1])),
+                                                             make_float2(c.x, c.y), nb);
+                                const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(f[e + 2]), __uint_as_float(f[e + 3])),
+                                                             make_float2(c.z, c.w), nb);
+                                a[(e >> 1) & 3] = __fadd2_rn(a[(e >> 1) & 3], make_float2(fast_exp2(y0.x), fast_exp2(y0.y)));
+                                a[((e >> 1) & 3) + 1] =
+                                    __fadd2_rn(a[((e >> 1) & 3) + 1], make_float2(fast_exp2(y1.x), fast_exp2(y1.y)));
+                            }
+                        }
+                        const float2 t2 = __fadd2_rn(__fadd2_rn(a[0], a[1]), __fadd2_rn(a[2], a[3]));
+                        const float sum = t2.x + t2.y;
+                        slow = __any_sync(0xffffffffu, !(sum < 1.2676506e30f));   // 2^100 (or NaN)
+                        if (!slow) l += sum;
+                    }
+                    if (slow) {
 #pragma unroll 1
                         for (int x = 0; x < 128; x += 32) {
                             uint32_t v[32];
-                            tmem_ld32(tmem + 256 * buf + 128 * wg + x + lane_off, v);
-                            const float4* col = reinterpret_cast<const float4*>(s_col + 128 * buf + x);
+                            tmem_ld32(d + x, v);
                             float mx = -INFINITY;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 c = KB == 0 ? make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e,
-                                                                       p.scale_log2e)
-                                                         : col[e];
-                                float y[4] = {__uint_as_float(v[4 * e]) * c.x, __uint_as_float(v[4 * e + 1]) * c.y,
-                                              __uint_as_float(v[4 * e + 2]) * c.z, __uint_as_float(v[4 * e + 3]) * c.w};
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    if (masked && k * kWtTile + x + 4 * e + i > mine) y[i] = -INFINITY;
-                                    mx = fmaxf(mx, y[i]);
-                                    v[4 * e + i] = __float_as_uint(y[i]);
-                                }
+                            for (int e = 0; e < 32; ++e) {
+                                float y = __uint_as_float(v[e]) * (KB == 0 ? p.scale_log2e : col[x + e]);
+                                if (masked && k * kWtTile + x + e > mine) y = -INFINITY;
+                                mx = fmaxf(mx, y);
+                                v[e] = __float_as_uint(y);
                             }
-                            if (mx > m) {   // (m = -inf: l is 0)
-                                l *= m == -INFINITY ? 0.f : fast_exp2(m - mx);
+                            if (mx > m) {
+                                l *= m == -INFINITY ? 1.f : fast_exp2(m - mx);   // (l is 0 there, or NaN)
                                 m = mx;
                             }
                             const float base = m == -INFINITY ? 0.f : m;
@@ -430,7 +496,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (n > 0) wait(bar_kf + 8 * ((n - 1) & (NS - 1)), ((n - 1) / NS) & 1);
             if (stalled) break;
             mbar_arrive_expect_tx(bar_q, tiles * C::kQBytes);
-            for (int t = 0; t < tiles; ++t)
+            if constexpr (KB == 0) {
+                // q itself (rows past the unit's are other heads', or zeros; masked later)
+                const int at = (s.b * p.hq + s.h * p.group) * p.tq + (p.pair0 + s.pair) * 256;
+                for (int t = 0; t < tiles; ++t)
+                    for (int half = 0; half < 2; ++half)
+                        tma_g2s_2d(smem_u32(smem + C::kQOff) + t * 32768 + half * 16384, &qmap, half * 64, at + 128 * t,
+                                   bar_q);
+            }
+            for (int t = 0; KB != 0 && t < tiles; ++t)
                 bulk_g2s(smem_u32(smem + C::kQOff) + t * C::kQBytes,
                          p.q_tiles + ((static_cast<size_t>(unit_q) * p.pairs + s.pair) * 2 + t) * C::kQBytes, C::kQBytes,
                          bar_q);
@@ -477,65 +551,29 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// A row's partial sums joined: lse = log2 of its sum of exp2(score); a CTA per (sequence,
-// pair, KV head), a thread a row.  Rows that see no token: +inf.
-__global__ void __launch_bounds__(256) tq_weights_lse_kernel(const __grid_constant__ WeightsParams p) {
-    __shared__ int s_all, s_before;
-    const int tid = threadIdx.x;
-    const int unit = static_cast<int>(blockIdx.x);
-    const int group = unit / p.hkv, h = unit - group * p.hkv;
-    const int b = group / p.pairs, pair = group - b * p.pairs;
-    griddep_wait();
-    griddep_launch_dependents();
-    if (tid < 32) {
-        int all, before;
-        wt_total(p, tid, group, all, before);
-        if (tid == 0) {
-            s_all = all;
-            s_before = before;
-        }
-    }
-    __syncthreads();
-    const int nt = wt_tiles(p, p.lengths[b], p.pair0 + pair);
-    float M = -INFINITY, sum = 0.f;
-    if (nt > 0) {
-        const long long all = s_all, P = p.ctas, k0 = s_before + static_cast<long long>(h) * nt;
-        // the CTAs whose runs meet tiles [k0, k0 + nt)
-        const int c0 = static_cast<int>(((k0 + 1) * P - 1) / all), c1 = static_cast<int>(((k0 + nt) * P - 1) / all);
-        const float2* ml = p.part_ml + static_cast<size_t>(unit) * 256 + tid;
-        for (int c = c0; c <= c1; ++c) {
-            if (c * all / P >= (c + 1) * all / P) continue;   // (an empty run wrote nothing)
-            const float2 x = __ldcg(ml + static_cast<size_t>(c) * 256);
-            const float mn = fmaxf(M, x.x);
-            if (x.x != -INFINITY || x.y != 0.f) {
-                sum = (M == -INFINITY ? sum : sum * fast_exp2(M - mn)) +
-                      (x.x == -INFINITY ? x.y : x.y * fast_exp2(x.x - mn));
-                M = mn;
-            }
-        }
-    }
-    const bool none = M == -INFINITY && sum == 0.f;   // (a NaN sum is a row of NaN scores)
-    p.lse[static_cast<size_t>(unit) * 256 + tid] = none ? INFINITY : M + log2f(sum);
-    if (none && (p.pair0 + pair) * 256 + tid < p.rows) atomicOr(p.status, kStatusShortContext);
-}
-
-// A token's sums over the pairs that see it, added to its weight.
+// A token's sums over the pairs that see it, added to its weight: 32 tokens a CTA, its
+// warps taking every eighth pair.
 __global__ void __launch_bounds__(256) tq_weights_add_kernel(const __grid_constant__ WeightsParams p) {
-    const int per = (p.max_len + 255) / 256;
-    const int unit = static_cast<int>(blockIdx.x) / per, t = (static_cast<int>(blockIdx.x) - unit * per) * 256 + threadIdx.x;
+    __shared__ float s_sum[8][32];
+    const int per = p.part_len / 32;
+    const int unit = static_cast<int>(blockIdx.x) / per, t0 = (static_cast<int>(blockIdx.x) - unit * per) * 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = t0 + lane;
     griddep_wait();
     griddep_launch_dependents();
-    const int b = unit / p.hkv, L = p.lengths[b];
-    if (t >= min(L, p.max_len)) return;
-    const int seen = p.seen != nullptr ? p.seen[b] : L - p.tq;
-    float* out = p.weights + static_cast<size_t>(unit) * p.cap + t;
+    const int b = unit / p.hkv, L = p.lengths[b], lim = min(L, p.max_len);
+    if (t0 >= lim) return;
     const float* part = p.part_w + static_cast<size_t>(unit) * p.pairs * p.part_len + t;
-    // the first row that sees the token, and its pair
-    const long long row = max(0ll, static_cast<long long>(t - (L - p.tq)) * p.group);
     float sum = 0.f;
 #pragma unroll 4
-    for (int q = max(0, static_cast<int>(row / 256) - p.pair0); q < p.pairs; ++q)
-        sum += __ldcg(part + static_cast<size_t>(q) * p.part_len);
+    for (int q = warp; q < p.pairs; q += 8)
+        if (t0 / kWtTile < wt_tiles(p, L, p.pair0 + q)) sum += __ldcg(part + static_cast<size_t>(q) * p.part_len);
+    s_sum[warp][lane] = sum;
+    __syncthreads();
+    if (warp != 0 || t >= lim) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) sum += s_sum[i][lane];
+    const int seen = p.seen != nullptr ? p.seen[b] : L - p.tq;
+    float* out = p.weights + static_cast<size_t>(unit) * p.cap + t;
     float old = 0.f;
     if (p.pair0 > 0) old = *out;   // (a call in several blocks of pairs)
     else if (t < seen && p.decay != 0.f) old = p.decay * *out;
@@ -543,28 +581,28 @@ __global__ void __launch_bounds__(256) tq_weights_add_kernel(const __grid_consta
 }
 
 template <int KB>
-static int launch_t(const WeightsParams& p, const CUtensorMap* kmap, cudaStream_t stream) {
+static int launch_t(const WeightsParams& p, const CUtensorMap* kmap, const CUtensorMap* qmap, cudaStream_t stream) {
     using C = WtCfg<KB>;
     static std::atomic<uint64_t> done0{0}, done1{0};
     cudaError_t e = set_smem_attr_once(tq_weights_kernel<KB, false>, C::kSmemAlloc, done0);
     if (e == cudaSuccess) e = set_smem_attr_once(tq_weights_kernel<KB, true>, C::kSmemAlloc, done1);
     if (e != cudaSuccess) return e;
     const unsigned units = static_cast<unsigned>(p.batch) * p.hkv;
-    e = launch_pdl(tq_weights_rows_kernel<KB != 0>, dim3(units * p.pairs * 32), dim3(256), 0, stream, p);
+    if (KB != 0) e = launch_pdl(tq_weights_rows_kernel, dim3(units * p.pairs * 32), dim3(256), 0, stream, p);
     if (e == cudaSuccess)
-        e = launch_pdl(tq_weights_kernel<KB, false>, dim3(p.ctas), dim3(kWtThreads), C::kSmemAlloc, stream, p, *kmap);
-    if (e == cudaSuccess) e = launch_pdl(tq_weights_lse_kernel, dim3(units * p.pairs), dim3(256), 0, stream, p);
+        e = launch_pdl(tq_weights_kernel<KB, false>, dim3(p.ctas), dim3(kWtThreads), C::kSmemAlloc, stream, p, *kmap, *qmap);
     if (e == cudaSuccess)
-        e = launch_pdl(tq_weights_kernel<KB, true>, dim3(p.ctas), dim3(kWtThreads), C::kSmemAlloc, stream, p, *kmap);
+        e = launch_pdl(tq_weights_kernel<KB, true>, dim3(p.ctas), dim3(kWtThreads), C::kSmemAlloc, stream, p, *kmap, *qmap);
     if (e == cudaSuccess && p.part_w != nullptr)
-        e = launch_pdl(tq_weights_add_kernel, dim3(units * ((p.max_len + 255) / 256)), dim3(256), 0, stream, p);
+        e = launch_pdl(tq_weights_add_kernel, dim3(units * (p.part_len / 32)), dim3(256), 0, stream, p);
     return e;
 }
 
-int launch_weights(int kbits, const WeightsParams& p, const CUtensorMap* kmap, cudaStream_t stream) {
-    if (kbits == 16) return launch_t<0>(p, kmap, stream);
-    if (kbits == 3) return launch_t<3>(p, kmap, stream);
-    if (kbits == 4) return launch_t<4>(p, kmap, stream);
+int launch_weights(int kbits, const WeightsParams& p, const CUtensorMap* kmap, const CUtensorMap* qmap,
+                   cudaStream_t stream) {
+    if (kbits == 16) return launch_t<0>(p, kmap, qmap, stream);
+    if (kbits == 3) return launch_t<3>(p, kmap, qmap, stream);
+    if (kbits == 4) return launch_t<4>(p, kmap, qmap, stream);
     return cudaErrorInvalidValue;
 }
 
