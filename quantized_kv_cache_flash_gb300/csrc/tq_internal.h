@@ -188,7 +188,7 @@ struct WeightsParams {
     const int32_t* seen;      // [B] tokens that have a weight already, or null: all but the last tq
     float* weights;           // [B, Hkv, cap]
     // workspace
-    uint8_t* q_tiles;         // [units][pairs][2] Q' tiles: q_hi, q_lo, 32 KB each (quantized K)
+    uint8_t* q_tiles;         // [units][pairs] Q': q_hi and q_lo of 256 rows, 64 KB each (quantized K)
     float2* part_ml;          // [ctas + units * pairs][256] a run's (maximum, sum) of each row
     float* part_w;            // [units][pairs][part_len] sums per pair; null: one pair, added at once
     uint32_t* status;

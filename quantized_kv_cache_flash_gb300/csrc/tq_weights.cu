@@ -18,7 +18,9 @@
 // Roles of a CTA's warps (hand-overs through mbarriers, every wait bounded):
 //   0-3, 4-7  stats: a query tile's rows each; sum: every second K tile's tokens each
 //   8-11      dequantise K (n) (quantized K)
-//   12        issues the MMAs     13  copies Q' and the records (fp16 K: the tiles)
+//   12, 14    issue the MMAs of every second K tile: the thread that issues stands still while
+//             the tensor core works, and the other one's waits are over when it is done
+//   13        copies Q' and the records (fp16 K: the tiles)
 // Tensor memory: two buffers of 256 columns, S(n) of both query tiles.
 #include <algorithm>
 
@@ -34,21 +36,22 @@ template <int KB>
 struct WtCfg {
     static constexpr int kRbK = (KB == 0) ? 256 : KB * 16;
     static constexpr int kSlots = (KB == 0) ? 4 : 2;            // K tiles
-    static constexpr int kQBytes = (KB == 0) ? 32768 : 65536;   // of a query tile: q_hi, q_lo
+    // Q' of the pair: q_hi, q_lo, each 256 rows in the layout of sw128_offset but with
+    // halves of 32 KB (dims 0-63, 64-127)
+    static constexpr int kParts = (KB == 0) ? 1 : 2;
     static constexpr int kQOff = 0;
-    static constexpr int kKOff = 2 * kQBytes;
+    static constexpr int kKOff = kParts * 65536;
     static constexpr int kStgOff = kKOff + kSlots * 32768;      // records and norms [2]
     static constexpr int kStg = (KB == 0) ? 0 : kWtTile * kRbK + 256;
     static constexpr int kColOff = kStgOff + 2 * kStg;          // fp32 n_k * scale * log2(e) [2][128]
     static constexpr int kLseOff = kColOff + 1024;              // fp32 -log2(sum) of a row [256]
     static constexpr int kPosOff = kLseOff + 1024;              // query position of a row [256]
     // records copied [2], records read [2], K stored [kSlots], K read [kSlots], S done
-    // [2], S read [2], Q' copied; the TMEM slot
+    // [2], S read [2], Q' copied, Q' read; the TMEM slot
     static constexpr int kBarOff = kPosOff + 1024;
-    static constexpr int kSmem = kBarOff + (9 + 2 * kSlots) * 8 + 8;
+    static constexpr int kSmem = kBarOff + (10 + 2 * kSlots) * 8 + 8;
     static constexpr int kSmemAlloc = kSmem + 768;              // to a 1024-byte boundary from a 256-byte one
     static_assert(kSmemAlloc <= 232448, "227 KB per CTA");
-    static constexpr uint32_t kIdesc = umma_idesc_f16_f32(128, 128);
 };
 
 // A unit's part of a CTA's run: K tiles [k0, k1) of (sequence b, KV head h, pair).
@@ -162,13 +165,14 @@ __global__ void __launch_bounds__(256) tq_weights_rows_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] *= 0.08838834764831845f;   // 1/sqrt(128)
     }
-    uint8_t* tile = p.q_tiles + (static_cast<size_t>(unit) * (per / 128) + rl / 128) * 65536;
+    uint8_t* at = p.q_tiles + (static_cast<size_t>(unit) * p.pairs + rl / 256) * 131072 + (lane >> 4) * 32768 +
+                  sw128_offset(rl & 255, (4 * lane) & 63);
     const uint2 hi = make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
-    *reinterpret_cast<uint2*>(tile + sw128_offset(rl & 127, 4 * lane)) = hi;
+    *reinterpret_cast<uint2*>(at) = hi;
     // q_lo = Rot(q) - q_hi (exact in fp32), rounded once more
     const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&hi.x));
     const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&hi.y));
-    *reinterpret_cast<uint2*>(tile + 32768 + sw128_offset(rl & 127, 4 * lane)) =
+    *reinterpret_cast<uint2*>(at + 65536) =
         make_uint2(pack_half2(v[0] - h0.x, v[1] - h0.y), pack_half2(v[2] - h1.x, v[3] - h1.y));
 }
 
@@ -186,8 +190,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     float* s_lse = reinterpret_cast<float*>(smem + C::kLseOff);
     int* s_pos = reinterpret_cast<int*>(smem + C::kPosOff);
     const uint32_t bar_stg = smem_u32(smem + C::kBarOff), bar_stgf = bar_stg + 16, bar_s = bar_stg + 32,
-                   bar_sf = bar_stg + 48, bar_q = bar_stg + 64, bar_k = bar_stg + 72, bar_kf = bar_k + 8 * NS;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (9 + 2 * NS) * 8);
+                   bar_sf = bar_stg + 48, bar_q = bar_stg + 64, bar_qf = bar_stg + 72, bar_k = bar_stg + 80,
+                   bar_kf = bar_k + 8 * NS;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (10 + 2 * NS) * 8);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_stg + 8 * i, 1);
@@ -200,6 +205,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             mbar_init(bar_kf + 8 * i, 1);
         }
         mbar_init(bar_q, 1);
+        mbar_init(bar_qf, 2);
         fence_barrier_init();
     }
     if (KB == 0 && tid == 0) {
@@ -208,7 +214,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     }
     griddep_wait();
     griddep_launch_dependents();
-    if (!SUM && p.pair0 == 0 && blockIdx.x == 0 && warp == 14) {   // rows that see no token
+    if (!SUM && p.pair0 == 0 && blockIdx.x == 0 && warp == 15) {   // rows that see no token
         bool none = false;
         for (int b = lane; b < p.batch; b += 32) none = none || p.lengths[b] < p.tq;
         if (none) atomicOr(p.status, kStatusShortContext);
@@ -439,46 +445,54 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 }
             }
         }
-    } else if (warp == 12) {
+    } else if (warp == 12 || warp == 14) {
         const bool one = lane == 0;
-        int seg = 0, done = 0;
+        const int odd = warp == 14;
+        int seg = 0, last = -1;   // units so far; the last tile issued
         while (run.next(p, s)) {
             if (!one) continue;
             const int tiles = (p.pair0 + s.pair) * 256 + 128 < p.rows ? 2 : 1;   // query tiles with rows
             wait(bar_q, seg++ & 1);
             for (int k = s.k0; k < s.k1; ++k, ++n) {
                 const int buf = n & 1, slot = n & (NS - 1);
+                if (buf != odd) continue;
                 wait(bar_k + 8 * slot, (n / NS) & 1);
                 if (n >= 2) wait(bar_sf + 8 * buf, ((n >> 1) - 1) & 1);
                 if (stalled) break;
                 tc_fence_after();
                 const uint32_t kbase = smem_u32(smem + C::kKOff) + slot * 32768;
+                const uint32_t qbase = smem_u32(smem + C::kQOff), d = tmem + 256 * buf;
+                // q_lo first: the sums are cut at every step, the less the smaller they are
+                if constexpr (SUM) {   // both query tiles at once
+                    const uint32_t idesc = umma_idesc_f16_f32(128, tiles == 2 ? 256 : 128);
+#pragma unroll
+                    for (int part = C::kParts - 1; part >= 0; --part)
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_f16(d, umma_desc_sw128(kbase + (kk >> 2) * 16384 + (kk & 3) * 32),
+                                     umma_desc_sw128(qbase + part * 65536 + (kk >> 2) * 32768 + (kk & 3) * 32), idesc,
+                                     kk > 0 || part + 1 < C::kParts ? 1u : 0u);
+                } else {
 #pragma unroll 1
-                for (int t = 0; t < tiles; ++t) {
-                    const uint32_t qbase = smem_u32(smem + C::kQOff) + t * C::kQBytes;
-                    const uint32_t d = tmem + 256 * buf + 128 * t;
-                    // q_lo first: the sums are cut at every step, the less the smaller they are
+                    for (int t = 0; t < tiles; ++t)
 #pragma unroll
-                    for (int part = KB == 0 ? 1 : 0; part < 2; ++part)
+                        for (int part = C::kParts - 1; part >= 0; --part)
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const uint32_t koff = (kk >> 2) * 16384 + (kk & 3) * 32;
-                            const uint64_t qd = umma_desc_sw128(qbase + (part == 0 ? 32768 : 0) + koff);
-                            const uint64_t kd = umma_desc_sw128(kbase + koff);
-                            const uint32_t acc = kk > 0 || (KB != 0 && part == 1) ? 1u : 0u;
-                            if constexpr (SUM) umma_f16(d, kd, qd, C::kIdesc, acc);
-                            else umma_f16(d, qd, kd, C::kIdesc, acc);
-                        }
+                            for (int kk = 0; kk < 8; ++kk)
+                                umma_f16(d + 128 * t,
+                                         umma_desc_sw128(qbase + part * 65536 + (kk >> 2) * 32768 + t * 16384 + (kk & 3) * 32),
+                                         umma_desc_sw128(kbase + (kk >> 2) * 16384 + (kk & 3) * 32),
+                                         umma_idesc_f16_f32(128, 128), kk > 0 || part + 1 < C::kParts ? 1u : 0u);
                 }
                 umma_commit(bar_s + 8 * buf);
                 umma_commit(bar_kf + 8 * slot);
-                ++done;
+                last = n;
             }
             if (stalled) break;
+            umma_commit(bar_qf);
         }
         // after a time-out: the MMAs in flight end before tensor memory is freed
-        if (one && stalled && done > 0)
-            (void)mbar_wait_bounded(bar_kf + 8 * ((done - 1) & (NS - 1)), ((done - 1) / NS) & 1);
+        if (one && stalled && last >= 0) (void)mbar_wait_bounded(bar_kf + 8 * (last & (NS - 1)), (last / NS) & 1);
         __syncwarp();
     } else if (warp == 13) {
         const bool one = lane == 0;
@@ -490,24 +504,23 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const size_t row0 = static_cast<size_t>(s.b * p.hkv + s.h) * p.cap;
             const int unit_q = s.b * p.hkv + s.h;
             const int tiles = (p.pair0 + s.pair) * 256 + 128 < p.rows ? 2 : 1;
-            // Q' once the last MMAs of the unit before have read theirs (phase after phase:
-            // with quantized K the copies may be two tiles of a slot ahead)
-            if (KB != 0 && n > 2) wait(bar_kf + 8 * ((n - 3) & (NS - 1)), ((n - 3) / NS) & 1);
-            if (n > 0) wait(bar_kf + 8 * ((n - 1) & (NS - 1)), ((n - 1) / NS) & 1);
+            // Q' once the MMAs of the unit before, of both issuing warps, have read theirs
+            if (seg > 0) wait(bar_qf, (seg - 1) & 1);
             if (stalled) break;
-            mbar_arrive_expect_tx(bar_q, tiles * C::kQBytes);
+            mbar_arrive_expect_tx(bar_q, tiles * C::kParts * 32768);
             if constexpr (KB == 0) {
                 // q itself (rows past the unit's are other heads', or zeros; masked later)
                 const int at = (s.b * p.hq + s.h * p.group) * p.tq + (p.pair0 + s.pair) * 256;
                 for (int t = 0; t < tiles; ++t)
                     for (int half = 0; half < 2; ++half)
-                        tma_g2s_2d(smem_u32(smem + C::kQOff) + t * 32768 + half * 16384, &qmap, half * 64, at + 128 * t,
+                        tma_g2s_2d(smem_u32(smem + C::kQOff) + half * 32768 + t * 16384, &qmap, half * 64, at + 128 * t,
                                    bar_q);
+            } else {
+                for (int x = 0; x < 4; ++x)   // parts and halves
+                    bulk_g2s(smem_u32(smem + C::kQOff) + x * 32768,
+                             p.q_tiles + (static_cast<size_t>(unit_q) * p.pairs + s.pair) * 131072 + x * 32768,
+                             tiles * 16384, bar_q);
             }
-            for (int t = 0; KB != 0 && t < tiles; ++t)
-                bulk_g2s(smem_u32(smem + C::kQOff) + t * C::kQBytes,
-                         p.q_tiles + ((static_cast<size_t>(unit_q) * p.pairs + s.pair) * 2 + t) * C::kQBytes, C::kQBytes,
-                         bar_q);
             ++seg;
             q_open = true;
             for (int k = s.k0; k < s.k1; ++k, ++n) {
