@@ -16,7 +16,7 @@
 // pairs' order.
 //
 // Roles of a CTA's warps (hand-overs through mbarriers, every wait bounded):
-//   0-3, 4-7  stats: a query tile's rows each; sum: every second K tile's tokens each
+//   0-3, 4-7  a query tile each: its rows' sums (stats), its part of the tokens' (sum)
 //   8-11      dequantise K (n) (quantized K)
 //   12, 14    issue the MMAs of every second K tile: the thread that issues stands still while
 //             the tensor core works, and the other one's waits are over when it is done
@@ -47,9 +47,11 @@ struct WtCfg {
     static constexpr int kLseOff = kColOff + 1024;              // fp32 -log2(sum) of a row [256]
     static constexpr int kPosOff = kLseOff + 1024;              // query position of a row [256]
     // records copied [2], records read [2], K stored [kSlots], K read [kSlots], S done
-    // [2], S read [2], Q' copied, Q' read; the TMEM slot
-    static constexpr int kBarOff = kPosOff + 1024;
-    static constexpr int kSmem = kBarOff + (10 + 2 * kSlots) * 8 + 8;
+    // [2], S read [2], Q' copied, Q' read, the issuing warps' turns [2]; the TMEM slot
+    static constexpr int kHalfOff = kPosOff + 1024;             // fp32 the second query tile's sums [4][128]
+    static constexpr int kGo = 10 + 2 * kSlots;                 // the other issuing warp's turn [2]
+    static constexpr int kBarOff = kHalfOff + 2048;
+    static constexpr int kSmem = kBarOff + (kGo + 2) * 8 + 8;
     static constexpr int kSmemAlloc = kSmem + 768;              // to a 1024-byte boundary from a 256-byte one
     static_assert(kSmemAlloc <= 232448, "227 KB per CTA");
 };
@@ -62,6 +64,7 @@ struct WtSeg {
 
 // Smallest and largest query position of rows r0 .. r1.
 __device__ __forceinline__ int2 wt_span(const WeightsParams& p, int r0, int r1) {
+    if (r1 - r0 >= p.tq - 1) return make_int2(0, p.tq - 1);   // (every position)
     const int g0 = r0 / p.tq, g1 = r1 / p.tq;
     return g0 == g1 ? make_int2(r0 - g0 * p.tq, r1 - g1 * p.tq) : make_int2(0, p.tq - 1);
 }
@@ -97,9 +100,11 @@ struct WtRun {
     }
     __device__ __forceinline__ void start(const WeightsParams& p, int lane) {
         wt_total(p, lane, all);
-        const long long c = blockIdx.x;
-        pos = static_cast<int>(c * all / gridDim.x);
-        hi = static_cast<int>((c + 1) * all / gridDim.x);
+        // floor(c * all / P) in 32 bits: c * (all mod P) < P^2
+        const int c = static_cast<int>(blockIdx.x), P = static_cast<int>(gridDim.x);
+        const int q = all / P, r = all - q * P;
+        pos = c * q + c * r / P;
+        hi = (c + 1) * q + (c + 1) * r / P;
         b = pair = h = tile = L = nt = 0;
         if (pos >= hi) return;
         // the group that holds pos
@@ -189,16 +194,18 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     float* s_col = reinterpret_cast<float*>(smem + C::kColOff);
     float* s_lse = reinterpret_cast<float*>(smem + C::kLseOff);
     int* s_pos = reinterpret_cast<int*>(smem + C::kPosOff);
+    float* s_half = reinterpret_cast<float*>(smem + C::kHalfOff);
     const uint32_t bar_stg = smem_u32(smem + C::kBarOff), bar_stgf = bar_stg + 16, bar_s = bar_stg + 32,
                    bar_sf = bar_stg + 48, bar_q = bar_stg + 64, bar_qf = bar_stg + 72, bar_k = bar_stg + 80,
-                   bar_kf = bar_k + 8 * NS;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (10 + 2 * NS) * 8);
+                   bar_kf = bar_k + 8 * NS, bar_go = bar_stg + 8 * C::kGo;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (C::kGo + 2) * 8);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_stg + 8 * i, 1);
             mbar_init(bar_stgf + 8 * i, 128);
             mbar_init(bar_s + 8 * i, 1);
-            mbar_init(bar_sf + 8 * i, SUM ? 128 : 256);
+            mbar_init(bar_sf + 8 * i, 256);
+            mbar_init(bar_go + 8 * i, 1);
         }
         for (int i = 0; i < NS; ++i) {
             mbar_init(bar_k + 8 * i, KB == 0 ? 1 : 128);
@@ -266,27 +273,30 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 // tokens that every row of the pair sees
                 const int all_see = s.L - p.tq + wt_span(p, row0, row0 + nrows - 1).x;
                 const int seen = p.seen != nullptr ? p.seen[s.b] : s.L - p.tq;
-                const int chunks = (nrows + 31) / 32;
+                const int here = min(128, nrows - 128 * wg);   // rows of this query tile (or below 1)
+                const int chunks = (here + 31) / 32;
+                const float* lse = s_lse + 128 * wg;
+                const int* pos = s_pos + 128 * wg;
                 for (int k = s.k0; k < s.k1; ++k, ++n) {
-                    if ((n & 1) != wg) continue;
-                    wait(bar_s + 8 * wg, (n >> 1) & 1);
+                    const int buf = n & 1;
+                    wait(bar_s + 8 * buf, (n >> 1) & 1);
                     tc_fence_after();
                     const int t = k * kWtTile + r;
-                    const float c = KB == 0 ? p.scale_log2e : s_col[128 * wg + r];
-                    const uint32_t d = tmem + 256 * wg + lane_off;
+                    const float c = KB == 0 ? p.scale_log2e : s_col[128 * buf + r];
+                    const uint32_t d = tmem + 256 * buf + 128 * wg + lane_off;
                     float w;
-                    if (k * kWtTile + kWtTile - 1 > all_see || (nrows & 31) != 0) {
+                    if (k * kWtTile + kWtTile - 1 > all_see || here <= 0 || (here & 31) != 0) {
                         const int from = t - (s.L - p.tq);   // the first query position that sees the token
                         w = 0.f;
 #pragma unroll 1
-                        for (int x = 0; x < nrows; x += 32) {
+                        for (int x = 0; x < here; x += 32) {
                             uint32_t v[32];
                             tmem_ld32(d + x, v);
                             float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                const float4 l = *reinterpret_cast<const float4*>(s_lse + x + e);
-                                const int4 j = *reinterpret_cast<const int4*>(s_pos + x + e);
+                                const float4 l = *reinterpret_cast<const float4*>(lse + x + e);
+                                const int4 j = *reinterpret_cast<const int4*>(pos + x + e);
                                 const float y[4] = {l.x, l.y, l.z, l.w};
                                 const int jj[4] = {j.x, j.y, j.z, j.w};
 #pragma unroll
@@ -303,14 +313,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         uint32_t v[2][32];   // 32 rows at a time, the next ones in flight
                         tmem_ld32_issue(d, v[0]);
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) {
+                        for (int x = 0; x < 4; ++x) {
                             if (x >= chunks) break;
                             tmem_ld_wait(v[x & 1]);
                             if (x + 1 < chunks) tmem_ld32_issue(d + 32 * (x + 1), v[(x + 1) & 1]);
                             const uint32_t* f = v[x & 1];
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                const float4 l = *reinterpret_cast<const float4*>(s_lse + 32 * x + e);
+                                const float4 l = *reinterpret_cast<const float4*>(lse + 32 * x + e);
                                 const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(f[e]), __uint_as_float(f[e + 1])),
                                                              cc, make_float2(l.x, l.y));
                                 const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(f[e + 2]), __uint_as_float(f[e + 3])),
@@ -324,7 +334,18 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         w = t2.x + t2.y;
                     }
                     tc_fence_before();
-                    mbar_arrive(bar_sf + 8 * wg);
+                    mbar_arrive(bar_sf + 8 * buf);
+                    // the second query tile's part goes to the first one's thread (four slots:
+                    // S(n + 4) waits for what the first group does after it has read this one)
+                    float* half = s_half + 128 * (n & 3);
+                    if (wg == 1) {
+                        half[r] = w;
+                        __threadfence_block();
+                        named_bar_arrive(2 + (n & 3), 256);
+                        continue;
+                    }
+                    named_bar_sync(2 + (n & 3), 256);
+                    w += half[r];
                     if (t < lim && !stalled) {
                         if (p.part_w != nullptr) {
                             p.part_w[(static_cast<size_t>(s.b * p.hkv + s.h) * p.pairs + s.pair) * p.part_len + t] = w;
@@ -458,6 +479,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 if (buf != odd) continue;
                 wait(bar_k + 8 * slot, (n / NS) & 1);
                 if (n >= 2) wait(bar_sf + 8 * buf, ((n >> 1) - 1) & 1);
+                // in turns, so that tile n is done while n + 1 is worked on; the other warp's
+                // begins a little before the end of this one's
+                if (n > 0) wait(bar_go + 8 * odd, ((n - 1) >> 1) & 1);
                 if (stalled) break;
                 tc_fence_after();
                 const uint32_t kbase = smem_u32(smem + C::kKOff) + slot * 32768;
@@ -468,21 +492,25 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 #pragma unroll
                     for (int part = C::kParts - 1; part >= 0; --part)
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
+                        for (int kk = 0; kk < 8; ++kk) {
+                            if (part == 0 && kk == 6) mbar_arrive(bar_go + 8 * (odd ^ 1));
                             umma_f16(d, umma_desc_sw128(kbase + (kk >> 2) * 16384 + (kk & 3) * 32),
                                      umma_desc_sw128(qbase + part * 65536 + (kk >> 2) * 32768 + (kk & 3) * 32), idesc,
                                      kk > 0 || part + 1 < C::kParts ? 1u : 0u);
+                        }
                 } else {
 #pragma unroll 1
                     for (int t = 0; t < tiles; ++t)
 #pragma unroll
                         for (int part = C::kParts - 1; part >= 0; --part)
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
+                            for (int kk = 0; kk < 8; ++kk) {
+                                if (part == 0 && kk == 4 && t == tiles - 1) mbar_arrive(bar_go + 8 * (odd ^ 1));
                                 umma_f16(d + 128 * t,
                                          umma_desc_sw128(qbase + part * 65536 + (kk >> 2) * 32768 + t * 16384 + (kk & 3) * 32),
                                          umma_desc_sw128(kbase + (kk >> 2) * 16384 + (kk & 3) * 32),
                                          umma_idesc_f16_f32(128, 128), kk > 0 || part + 1 < C::kParts ? 1u : 0u);
+                            }
                 }
                 umma_commit(bar_s + 8 * buf);
                 umma_commit(bar_kf + 8 * slot);
