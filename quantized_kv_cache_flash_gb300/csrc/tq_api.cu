@@ -1237,6 +1237,7 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
     p.cap = c->capacity;
     p.max_len = max_len_hint;
     p.ctas = ctas;
+    tq::div_magic(uint32_t(tq_rows), &p.div_tq_m, &p.div_tq_s);
     p.scale_log2e = sc * 1.4426950408889634f;
     p.decay = decay;
     if (kb != 16) std::memcpy(p.ktab, ctx->ktab.tab, sizeof(p.ktab));
@@ -1249,6 +1250,7 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
     for (long long q0 = 0; q0 < pairs; q0 += block) {
         p.pair0 = int32_t(q0);
         p.pairs = int32_t(std::min(block, pairs - q0));
+        tq::div_magic(uint32_t(p.pairs), &p.div_pairs_m, &p.div_pairs_s);
         const int e = tq::launch_weights(kb, p, kmap, kb == 16 ? &qmap : &dummy, s);
         if (e != 0) return TQ_ERR_CUDA;
     }

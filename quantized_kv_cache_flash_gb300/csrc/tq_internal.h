@@ -194,6 +194,8 @@ struct WeightsParams {
     uint32_t* status;
     int32_t batch, hkv, hq, group, tq, rows, cap, max_len;
     int32_t pairs, pair0, part_len, ctas;
+    uint32_t div_tq_m, div_pairs_m;   // n / tq and n / pairs as (n * m) >> s (see div_magic)
+    int32_t div_tq_s, div_pairs_s;
     float scale_log2e, decay;
     uint32_t ktab[4], signs[4];
 };

@@ -62,10 +62,17 @@ struct WtSeg {
     int nt, base;   // the unit's tiles, and those of the units before it
 };
 
+// x / p.tq and x / p.pairs for 0 <= x < 2^31 (see div_magic)
+__device__ __forceinline__ int over_tq(const WeightsParams& p, int x) {
+    return static_cast<int>((static_cast<uint64_t>(x) * p.div_tq_m) >> p.div_tq_s);
+}
+__device__ __forceinline__ int over_pairs(const WeightsParams& p, int x) {
+    return static_cast<int>((static_cast<uint64_t>(x) * p.div_pairs_m) >> p.div_pairs_s);
+}
 // Smallest and largest query position of rows r0 .. r1.
 __device__ __forceinline__ int2 wt_span(const WeightsParams& p, int r0, int r1) {
     if (r1 - r0 >= p.tq - 1) return make_int2(0, p.tq - 1);   // (every position)
-    const int g0 = r0 / p.tq, g1 = r1 / p.tq;
+    const int g0 = over_tq(p, r0), g1 = over_tq(p, r1);
     return g0 == g1 ? make_int2(r0 - g0 * p.tq, r1 - g1 * p.tq) : make_int2(0, p.tq - 1);
 }
 // K tiles that the rows of a pair see.
@@ -80,7 +87,7 @@ __device__ __forceinline__ void wt_total(const WeightsParams& p, int lane, int& 
     const int groups = p.batch * p.pairs;
     all = 0;
     for (int g = lane; g < groups; g += 32) {
-        const int b = g / p.pairs;
+        const int b = over_pairs(p, g);
         all += p.hkv * wt_tiles(p, p.lengths[b], p.pair0 + g - b * p.pairs);
     }
     all = __reduce_add_sync(0xffffffffu, all);
@@ -111,7 +118,7 @@ struct WtRun {
         const int groups = p.batch * p.pairs;
         int cum = 0;
         for (int g0 = 0; g0 < groups; g0 += 32) {
-            const int g = g0 + lane, bb = min(g / p.pairs, p.batch - 1);
+            const int g = g0 + lane, bb = min(over_pairs(p, g), p.batch - 1);
             const int n = g < groups ? p.hkv * wt_tiles(p, p.lengths[bb], p.pair0 + g - bb * p.pairs) : 0;
             int inc = n;
 #pragma unroll
@@ -123,7 +130,7 @@ struct WtRun {
             if (hit) {
                 const int l = __ffs(hit) - 1;
                 const int local = pos - cum - __shfl_sync(0xffffffffu, inc - n, l);
-                b = (g0 + l) / p.pairs;
+                b = over_pairs(p, g0 + l);
                 pair = g0 + l - b * p.pairs;
                 enter(p);
                 h = local / nt;
@@ -253,13 +260,16 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 named_bar_sync(1, 256);   // (the unit before is done with its values)
                 // the row's partial sums joined (rows without any: hidden below)
                 {
-                    const long long all = run.all, P = gridDim.x;
-                    const int c0 = static_cast<int>(((s.base + 1ll) * P - 1) / all);
-                    const int c1 = static_cast<int>(((s.base + 0ll + s.nt) * P - 1) / all);
+                    const int P = static_cast<int>(gridDim.x), q = run.all / P, rest = run.all - q * P;
+                    const uint64_t all = run.all;
+                    const int c0 = static_cast<int>(((s.base + 1ull) * P - 1) / all);
+                    const int c1 = static_cast<int>(((s.base + 0ull + s.nt) * P - 1) / all);
                     const float2* ml = p.part_ml + static_cast<size_t>(unit) * 256 + tid;
                     float M = -INFINITY, sum = 0.f;
+#pragma unroll 4
                     for (int c = c0; c <= c1; ++c) {
-                        if (c * all / P >= (c + 1) * all / P) continue;   // (an empty run wrote nothing)
+                        // (an empty run wrote nothing)
+                        if (q == 0 && c * rest / P == (c + 1) * rest / P) continue;
                         const float2 x = __ldcg(ml + static_cast<size_t>(c) * 256);
                         const float mn = fmaxf(M, x.x);
                         sum = (M == -INFINITY ? sum : sum * fast_exp2(M - mn)) +
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         M = mn;
                     }
                     s_lse[tid] = -(M + log2f(sum));
-                    s_pos[tid] = tid < nrows ? (row0 + tid) % p.tq : -0x40000000;
+                    s_pos[tid] = tid < nrows ? row0 + tid - over_tq(p, row0 + tid) * p.tq : -0x40000000;
                 }
                 named_bar_sync(1, 256);
                 // tokens that every row of the pair sees
@@ -275,6 +285,17 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const int seen = p.seen != nullptr ? p.seen[s.b] : s.L - p.tq;
                 const int here = min(128, nrows - 128 * wg);   // rows of this query tile (or below 1)
                 const int chunks = (here + 31) / 32;
+                float* const out = p.part_w != nullptr
+                                       ? p.part_w + (static_cast<size_t>(s.b * p.hkv + s.h) * p.pairs + s.pair) * p.part_len
+                                       : p.weights + static_cast<size_t>(s.b * p.hkv + s.h) * p.cap;
+                float before = 0.f;
+                auto put = [&](int m, int t, float w) {   // token t's sum, of tile number m
+                    named_bar_sync(2 + (m & 3), 256);
+                    w += s_half[128 * (m & 3) + r];
+                    if (t >= lim || stalled) return;
+                    if (p.part_w == nullptr && t < seen && p.decay != 0.f) w += p.decay * out[t];
+                    out[t] = w;
+                };
                 const float* lse = s_lse + 128 * wg;
                 const int* pos = s_pos + 128 * wg;
                 for (int k = s.k0; k < s.k1; ++k, ++n) {
@@ -335,30 +356,23 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     }
                     tc_fence_before();
                     mbar_arrive(bar_sf + 8 * buf);
-                    // the second query tile's part goes to the first one's thread (four slots:
-                    // S(n + 4) waits for what the first group does after it has read this one)
-                    float* half = s_half + 128 * (n & 3);
+                    // the second query tile's part goes to the first one's thread, which looks for
+                    // it a tile later (four slots: S(n + 4) waits for what the first group does
+                    // after it has read this one)
                     if (wg == 1) {
-                        half[r] = w;
+                        s_half[128 * (n & 3) + r] = w;
                         __threadfence_block();
                         named_bar_arrive(2 + (n & 3), 256);
-                        continue;
-                    }
-                    named_bar_sync(2 + (n & 3), 256);
-                    w += half[r];
-                    if (t < lim && !stalled) {
-                        if (p.part_w != nullptr) {
-                            p.part_w[(static_cast<size_t>(s.b * p.hkv + s.h) * p.pairs + s.pair) * p.part_len + t] = w;
-                        } else {
-                            float* out = p.weights + static_cast<size_t>(s.b * p.hkv + s.h) * p.cap + t;
-                            *out = (t < seen && p.decay != 0.f ? p.decay * *out : 0.f) + w;
-                        }
+                    } else {
+                        if (k > s.k0) put(n - 1, t - kWtTile, before);
+                        before = w;
                     }
                 }
+                if (wg == 0) put(n - 1, (s.k1 - 1) * kWtTile + r, before);
             } else {
                 // rows of query tile wg: last visible token of this row, and of all of them
                 const int first = row0 + 128 * wg, row = first + r;
-                const int mine = row < p.rows ? min(s.L - p.tq + row % p.tq, lim - 1) : -1;
+                const int mine = row < p.rows ? min(s.L - p.tq + row - over_tq(p, row) * p.tq, lim - 1) : -1;
                 const int all_see =
                     first + 127 < p.rows ? min(s.L - p.tq + wt_span(p, first, first + 127).x, lim - 1) : -1;
                 const bool any = first < p.rows;
