@@ -1175,7 +1175,7 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
         const size_t scores = size_t(chunks) * 32 * gr * sizeof(float);
         if (scores <= kWeightsWork) {
             tq::StepParams p{};
-            p.ctas = int(std::min<long long>(2ll * tq::host::kSMs * tq::weights_step_ctas_per_sm(kb, gr),
+            p.ctas = int(std::min<long long>(1ll * tq::host::kSMs * tq::weights_step_ctas_per_sm(kb, gr),
                                              std::max<long long>(1, (chunks + 7) / 8)));
             const size_t part = size_t(p.ctas + units) * gr * sizeof(float2);
             if ((r = ensure_work(ctx, scores + part, s)) != TQ_OK) return r;

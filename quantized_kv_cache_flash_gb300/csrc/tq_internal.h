@@ -213,6 +213,7 @@ struct StepParams {
     float2* part_ml;          // workspace: [ctas + units][group rows]
     uint32_t* status;
     int32_t batch, hkv, hq, group, tq, rows, cap, max_len, score_len, ctas;
+    int32_t span;             // tokens per CTA of the second kernel
     float scale_log2e, decay;
     uint32_t ktab[4], signs[4];
 };

@@ -22,11 +22,12 @@ struct StepCfg {
     static constexpr bool kPair = KB != 0 && ROWS == 4;     // column 2i: q_hi of row i, 2i + 1: q_lo
     static constexpr bool kQlo = KB != 0 && ROWS != 4;      // q_lo as a second B operand
     static constexpr int NE = kPair ? 1 : 2;                // query rows per thread per n-tile
-    static constexpr int kStages = KB == 0 ? 2 : 4;
-    static constexpr int kMinCtas = KB == 0 ? 3 : 4;        // resident CTAs per SM
+    static constexpr int kTok = KB == 0 ? 32 : 64;          // tokens per stage
+    static constexpr int kStages = 2;
+    static constexpr int kMinCtas = KB == 0 ? 3 : NT == 2 ? 4 : 6;   // resident CTAs per SM, at least
     static constexpr int kRbK = KB == 0 ? 256 : KB * 16;
-    static constexpr int kKnOff = kChunkTokens * kRbK;
-    static constexpr int kStageRaw = kKnOff + (KB == 0 ? 0 : kChunkTokens * 2);
+    static constexpr int kKnOff = kTok * kRbK;
+    static constexpr int kStageRaw = kKnOff + (KB == 0 ? 0 : kTok * 2);
     static constexpr int kStageAlign = KB == 0 ? 1024 : 128;
     static constexpr int kStage = (kStageRaw + kStageAlign - 1) / kStageAlign * kStageAlign;
     static constexpr int kPipe = kWarps * kStages * kStage;
@@ -98,12 +99,12 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
         const int k1 = min(nch, k0 + (hi - pos));
         const int unit = b * p.hkv + h;
         const int t_begin = k0 * kChunkTokens, t_end = min(k1 * kChunkTokens, min(L, p.max_len));
-        const int nchunks = k1 - k0;
+        const int nchunks = (t_end - t_begin + C::kTok - 1) / C::kTok;   // stages' worth of tokens
         const size_t row0 = static_cast<size_t>(unit) * p.cap;
 
         auto issue = [&](int c, int st) {   // lane 0 only
-            const int tok0 = t_begin + c * kChunkTokens;
-            const int nval = min(kChunkTokens, t_end - tok0);
+            const int tok0 = t_begin + c * C::kTok;
+            const int nval = min(C::kTok, t_end - tok0);
             const uint32_t dst = smem_u32(wpipe + st * C::kStage), bar = bar0 + st * 8;
             if constexpr (KB == 0) {
                 mbar_arrive_expect_tx(bar, 2 * 4096);
@@ -176,12 +177,17 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
                 l[n][e] = 0.f;
                 lim[n][e] = min(L - p.tq + C::slot_row(n, e, t) / p.group, t_end - 1);
             }
-        float* out = p.scores + static_cast<size_t>(unit) * p.score_len * ROWS;
+        // this thread's first score of the share
+        float* const out = p.scores + (static_cast<size_t>(unit) * p.score_len + t_begin + g) * ROWS + C::slot_row(0, 0, t);
         const int all_see = min(L - p.tq, t_end - 1);   // (padding rows see more; nobody reads them)
 
-        // a chunk: scores to the workspace, maxima and sums in registers
-        auto process = [&](const uint8_t* st, int tok0, auto full_tag) {
+        // 32 tokens of a stage from its token `at`: scores to the workspace, maxima and sums
+        // in registers.  A row's base m is the largest score that the thread first sees;
+        // later scores may pass it, as long as the sums stay in range.
+        auto process = [&](const uint8_t* st, int tok0, int at, auto full_tag) {
             constexpr bool FULL = decltype(full_tag)::value;
+            float* const o = out + static_cast<size_t>(tok0 - t_begin) * ROWS;
+            tok0 += at;
             float x[2][NT][4];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
                 for (int n = 0; n < NT; ++n) x[tt][n][0] = x[tt][n][1] = x[tt][n][2] = x[tt][n][3] = 0.f;
                 if constexpr (KB == 0) {
                     const int mi = lane >> 3;
-                    const int row = tt * 16 + (mi & 1) * 8 + (lane & 7);
+                    const int row = at + tt * 16 + (mi & 1) * 8 + (lane & 7);
 #pragma unroll
                     for (int kc2 = 0; kc2 < 4; ++kc2) {
                         uint32_t qb[NT][4];
@@ -207,8 +213,8 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
                         }
                     }
                 } else {
-                    const QuarterWords wa = load_quarter<KB>(st + (tt * 16 + g) * C::kRbK + t * (C::kRbK / 4));
-                    const QuarterWords wb = load_quarter<KB>(st + (tt * 16 + g + 8) * C::kRbK + t * (C::kRbK / 4));
+                    const QuarterWords wa = load_quarter<KB>(st + (at + tt * 16 + g) * C::kRbK + t * (C::kRbK / 4));
+                    const QuarterWords wb = load_quarter<KB>(st + (at + tt * 16 + g + 8) * C::kRbK + t * (C::kRbK / 4));
                     auto kgroup = [&](auto jtag) {
                         constexpr int J = decltype(jtag)::value;
                         uint32_t ha[4], hb[4], unused[2];
@@ -242,8 +248,8 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
                 const int ta = tt * 16 + g, tb = ta + 8;
                 float ka = p.scale_log2e, kb2 = p.scale_log2e;
                 if constexpr (KB != 0) {
-                    ka *= __half2float(*reinterpret_cast<const __half*>(st + C::kKnOff + 2 * ta));
-                    kb2 *= __half2float(*reinterpret_cast<const __half*>(st + C::kKnOff + 2 * tb));
+                    ka *= __half2float(*reinterpret_cast<const __half*>(st + C::kKnOff + 2 * (at + ta)));
+                    kb2 *= __half2float(*reinterpret_cast<const __half*>(st + C::kKnOff + 2 * (at + tb)));
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -256,9 +262,8 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
                             if (tok0 + tb > lim[n][e]) x[tt][n][e + 2] = -INFINITY;
                         }
                     }
-                    const int col = C::slot_row(n, 0, t);
-                    float* oa = out + static_cast<size_t>(tok0 + ta) * ROWS + col;
-                    float* ob = out + static_cast<size_t>(tok0 + tb) * ROWS + col;
+                    float* oa = o + (at + tt * 16) * ROWS + 8 * n;
+                    float* ob = oa + 8 * ROWS;
                     if constexpr (NE == 2) {
                         if (FULL || tok0 + ta < t_end) *reinterpret_cast<float2*>(oa) = make_float2(x[tt][n][0], x[tt][n][1]);
                         if (FULL || tok0 + tb < t_end) *reinterpret_cast<float2*>(ob) = make_float2(x[tt][n][2], x[tt][n][3]);
@@ -272,14 +277,20 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
-                    const float mx = fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2]));
-                    if (mx > m[n][e]) {
-                        l[n][e] *= m[n][e] == -INFINITY ? 1.f : fast_exp2(m[n][e] - mx);   // (l is 0 there, or NaN)
-                        m[n][e] = mx;
-                    }
-                    const float base = m[n][e] == -INFINITY ? 0.f : m[n][e];
-                    l[n][e] += (fast_exp2(x[0][n][e] - base) + fast_exp2(x[0][n][e + 2] - base)) +
+                    auto sum = [&](float base) {
+                        return (fast_exp2(x[0][n][e] - base) + fast_exp2(x[0][n][e + 2] - base)) +
                                (fast_exp2(x[1][n][e] - base) + fast_exp2(x[1][n][e + 2] - base));
+                    };
+                    float s = sum(m[n][e]);
+                    if (!(s < 1.2676506e30f)) {   // 2^100 (m = -inf makes it inf or NaN)
+                        const float mx = fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2]));
+                        if (mx > m[n][e]) {
+                            l[n][e] *= m[n][e] == -INFINITY ? 1.f : fast_exp2(m[n][e] - mx);   // (l is 0 there, or NaN)
+                            m[n][e] = mx;
+                        }
+                        s = sum(m[n][e] == -INFINITY ? 0.f : m[n][e]);
+                    }
+                    l[n][e] += s;
                 }
         };
 
@@ -289,9 +300,14 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
             const bool ok = mbar_wait_bounded(bar0 + 8 * stage, phase);
             if (__any_sync(0xffffffffu, !ok)) { stalled = true; break; }
             const uint8_t* st = wpipe + stage * C::kStage;
-            const int tok0 = t_begin + c * kChunkTokens;
-            if (tok0 + kChunkTokens - 1 <= all_see) process(st, tok0, std::true_type{});
-            else process(st, tok0, std::false_type{});
+            const int tok0 = t_begin + c * C::kTok;
+            if (tok0 + C::kTok - 1 <= all_see) {
+#pragma unroll 1
+                for (int at = 0; at < C::kTok; at += 32) process(st, tok0, at, std::true_type{});
+            } else {
+#pragma unroll 1
+                for (int at = 0; at < C::kTok && tok0 + at < t_end; at += 32) process(st, tok0, at, std::false_type{});
+            }
             __syncwarp();
             const int cn = c + C::kWarps * C::kStages;
             if (cn < nchunks && lane == 0) {
@@ -300,7 +316,7 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
             }
             if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
         }
-        if (pos + nchunks >= hi) griddep_launch_dependents();
+        if (pos + k1 - k0 >= hi) griddep_launch_dependents();
         if (stalled) {   // this warp's copies still in flight land (bounded)
             for (int k = 0; k < C::kStages; ++k) {
                 if (c + C::kWarps * k >= nchunks) break;
@@ -332,19 +348,19 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
             p.part_ml[(static_cast<size_t>(blockIdx.x) + unit) * ROWS + threadIdx.x] = a;
         }
         if (__syncthreads_or(stalled)) break;
-        pos += nchunks;
+        pos += k1 - k0;
     }
 }
 
-// The tokens' weights from the scores; a CTA 256 * TOK tokens of a unit.
+// The tokens' weights from the scores; a CTA p.span tokens of a unit, TOK a thread and turn.
 template <int ROWS, int TOK>
 __global__ void __launch_bounds__(256) tq_step_sums_kernel(const __grid_constant__ StepParams p) {
     __shared__ float2 s_part[16][ROWS];
     __shared__ float s_lse[ROWS];
     const int tid = threadIdx.x;
-    const int per = (p.max_len + 256 * TOK - 1) / (256 * TOK);
+    const int per = (p.max_len + p.span - 1) / p.span;
     const int unit = static_cast<int>(blockIdx.x) / per;
-    const int t0 = (static_cast<int>(blockIdx.x) - unit * per) * 256 * TOK + tid;
+    const int t0 = (static_cast<int>(blockIdx.x) - unit * per) * p.span;
     const int b = unit / p.hkv, h = unit - b * p.hkv;
     // (lengths may be read before the wait: the scores kernel's CTAs waited for what wrote
     // them before any of them let this grid launch)
@@ -359,44 +375,54 @@ __global__ void __launch_bounds__(256) tq_step_sums_kernel(const __grid_constant
     all = __reduce_add_sync(0xffffffffu, all);
     before = __reduce_add_sync(0xffffffffu, before);
     const int nch = unit_chunks(p.lengths, b, p.max_len);
-    griddep_wait();
-    griddep_launch_dependents();
-    const bool first = t0 - tid == 0;
-    if (t0 - tid >= lim && !first) return;   // (uniform over the CTA)
-
-    // the scores, in flight while the shares are joined
-    float x[TOK][ROWS];
-    float old[TOK];
-    float* out = p.weights + static_cast<size_t>(unit) * p.cap;
-    const int seen = p.seen != nullptr ? p.seen[b] : L - p.tq;
-    const float4* sc = reinterpret_cast<const float4*>(p.scores + static_cast<size_t>(unit) * p.score_len * ROWS);
-#pragma unroll
-    for (int k = 0; k < TOK; ++k) {
-        const int t = t0 + 256 * k;
-        old[k] = 0.f;
-        if (t < lim) {
-#pragma unroll
-            for (int i = 0; i < ROWS / 4; ++i) {
-                const float4 v = __ldcg(sc + static_cast<size_t>(t) * (ROWS / 4) + i);
-                x[k][4 * i] = v.x, x[k][4 * i + 1] = v.y, x[k][4 * i + 2] = v.z, x[k][4 * i + 3] = v.w;
-            }
-            if (t < seen && p.decay != 0.f) old[k] = p.decay * out[t];
+    // the shares c0 .. c1 that meet the unit's chunks
+    const int P = p.ctas, k_first = before + h * nch;
+    int c0 = 0, c1 = -1;
+    if (nch > 0) {
+        if (all < 0x7fffffff / P) {   // (32-bit divisions)
+            c0 = ((k_first + 1) * P - 1) / all;
+            c1 = ((k_first + nch) * P - 1) / all;
+        } else {
+            c0 = static_cast<int>((static_cast<long long>(k_first + 1) * P - 1) / all);
+            c1 = static_cast<int>((static_cast<long long>(k_first + nch) * P - 1) / all);
         }
     }
+    const int cq = all / P, cr = all - cq * P;
+    const int seen = p.seen != nullptr ? p.seen[b] : L - p.tq;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (t0 >= lim && t0 > 0) return;   // (uniform over the CTA)
+
+    float x[TOK][ROWS], old[TOK];
+    float* out = p.weights + static_cast<size_t>(unit) * p.cap;
+    const float4* sc = reinterpret_cast<const float4*>(p.scores + static_cast<size_t>(unit) * p.score_len * ROWS);
+    const int end = min(lim, t0 + p.span);
+    const bool fade = p.decay != 0.f;
+    auto load = [&](int t1) {
+#pragma unroll
+        for (int k = 0; k < TOK; ++k) {
+            const int t = t1 + tid + 256 * k;
+            old[k] = 0.f;
+            if (t < end) {
+#pragma unroll
+                for (int i = 0; i < ROWS / 4; ++i) {
+                    const float4 v = __ldcg(sc + static_cast<size_t>(t) * (ROWS / 4) + i);
+                    x[k][4 * i] = v.x, x[k][4 * i + 1] = v.y, x[k][4 * i + 2] = v.z, x[k][4 * i + 3] = v.w;
+                }
+                if (fade && t < seen) old[k] = out[t];
+            }
+        }
+    };
+    load(t0);   // (in flight while the shares are joined)
     {   // thread (i, r): every 16th share of row r
         const int i = tid / 16, r = tid % 16;
         float m = -INFINITY, l = 0.f;
-        if (nch > 0 && r < ROWS) {
-            const int P = p.ctas, cq = all / P, cr = all - cq * P;
-            const int k_first = before + h * nch;
-            const int c0 = static_cast<int>((static_cast<long long>(k_first + 1) * P - 1) / all);
-            const int c1 = static_cast<int>((static_cast<long long>(k_first + nch) * P - 1) / all);
+        if (r < ROWS)
             for (int c = c0 + i; c <= c1; c += 16) {
-                if (c * cq + (c * cr) / P >= (c + 1) * cq + ((c + 1) * cr) / P) continue;   // (an empty share)
+                if (cq == 0 && (c * cr) / P == ((c + 1) * cr) / P) continue;   // (an empty share)
                 const float2 v = __ldcg(p.part_ml + (static_cast<size_t>(c) + unit) * ROWS + r);
                 join(m, l, v.x, v.y);
             }
-        }
         if (r < ROWS) s_part[i][r] = make_float2(m, l);
     }
     __syncthreads();
@@ -406,38 +432,49 @@ __global__ void __launch_bounds__(256) tq_step_sums_kernel(const __grid_constant
         for (int i = 0; i < 16; ++i) join(m, l, s_part[i][tid].x, s_part[i][tid].y);
         const bool none = m == -INFINITY && l == 0.f;
         s_lse[tid] = none || tid >= p.rows ? INFINITY : m + log2f(l);
-        if (none && tid < p.rows && first) atomicOr(p.status, kStatusShortContext);
+        if (none && tid < p.rows && t0 == 0) atomicOr(p.status, kStatusShortContext);
     }
     __syncthreads();
     float lse[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) lse[r] = s_lse[r];
+    for (int t1 = t0; t1 < end; t1 += 256 * TOK) {
+        float w[TOK];
 #pragma unroll
-    for (int k = 0; k < TOK; ++k) {
-        const int t = t0 + 256 * k;
-        if (t >= lim) continue;
-        float w = 0.f;
+        for (int k = 0; k < TOK; ++k) {
+            w[k] = 0.f;
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r)   // (-inf: hidden, also from a row of NaN)
-            w += r < p.rows && x[k][r] != -INFINITY ? fast_exp2(x[k][r] - lse[r]) : 0.f;
-        out[t] = old[k] + w;
+            for (int r = 0; r < ROWS; ++r)   // (-inf: hidden, also from a row of NaN)
+                w[k] += r < p.rows && x[k][r] != -INFINITY ? fast_exp2(x[k][r] - lse[r]) : 0.f;
+            if (fade) w[k] = fmaf(p.decay, old[k], w[k]);
+        }
+        if (t1 + 256 * TOK < end) load(t1 + 256 * TOK);   // (in flight while these are stored)
+#pragma unroll
+        for (int k = 0; k < TOK; ++k)
+            if (t1 + tid + 256 * k < end) out[t1 + tid + 256 * k] = w[k];
     }
 }
 
 template <int KB, int ROWS>
-static int launch_t(const StepParams& p, const CUtensorMap* kmap, cudaStream_t stream) {
+static int launch_t(StepParams p, const CUtensorMap* kmap, cudaStream_t stream) {
     using C = StepCfg<KB, ROWS>;
     static std::atomic<uint64_t> attr_done{0};
     cudaError_t e = set_smem_attr_once(tq_step_scores_kernel<KB, ROWS>, C::kSmemAlloc, attr_done);
     if (e != cudaSuccess) return e;
     e = launch_pdl(tq_step_scores_kernel<KB, ROWS>, dim3(p.ctas), dim3(128), C::kSmemAlloc, stream, p, *kmap);
     if (e != cudaSuccess) return e;
-    const unsigned units = static_cast<unsigned>(p.batch) * p.hkv;
-    const unsigned small = (p.max_len + 255) / 256;
-    // few tokens: a token a thread (one trip of loads more SMs share); else four
-    if (ROWS == 16 || units * small <= 4 * 152)
-        return launch_pdl(tq_step_sums_kernel<ROWS, 1>, dim3(units * small), dim3(256), 0, stream, p);
-    return launch_pdl(tq_step_sums_kernel<ROWS, ROWS == 16 ? 1 : 4>, dim3(units * ((p.max_len + 1023) / 1024)),
+    // Few tokens: a token a thread, so that more SMs share them.  Many: up to 8 a thread,
+    // four loads in flight, for as many CTAs as are resident at once.
+    const long long units = 1ll * p.batch * p.hkv;
+    constexpr int kMany = ROWS == 16 ? 1 : 4;
+    if (units * ((p.max_len + 255) / 256) <= 4 * host::kSMs) {
+        p.span = 256;
+        return launch_pdl(tq_step_sums_kernel<ROWS, 1>, dim3(static_cast<unsigned>(units * ((p.max_len + 255) / 256))),
+                          dim3(256), 0, stream, p);
+    }
+    p.span = 256 * kMany;
+    while (p.span < 8192 && units * ((p.max_len + p.span - 1) / p.span) > 8 * host::kSMs) p.span *= 2;
+    return launch_pdl(tq_step_sums_kernel<ROWS, kMany>, dim3(static_cast<unsigned>(units * ((p.max_len + p.span - 1) / p.span))),
                       dim3(256), 0, stream, p);
 }
 
