@@ -416,7 +416,7 @@ int tq_cache_evict(tq_ctx **ctx, const tq_cache *dst, const tq_cache *src, const
  *   next_token: int32 [batch] device pointer.
  * Sums and differences carry 48 bits or more, in an order of their own: the same call
  * gives the same tokens.  What is not above 0 (NaN) counts as 0, what is above 1 as 1; a row
- * whose sum passes 2^7 gives an unspecified next token (of the vocabulary).  A tried
+ * whose sum passes 2^5 gives an unspecified next token (of the vocabulary).  A tried
  * node with a parent or a token out of range counts as a padding node and raises
  * TQ_STATUS_BAD_INDEX; a target's row without positive entries at the path's end gives
  * token 0 and raises TQ_STATUS_BAD_VALUE.  num_nodes <= TQ_MAX_TREE_NODES, vocab <=

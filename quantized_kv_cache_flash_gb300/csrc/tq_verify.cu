@@ -13,14 +13,14 @@
 //
 // Decisions at a border need more than fp32: what is left of a token is a pair of fp32
 // numbers (differences and products with their rounding errors, 2^-48 or less off), a
-// thread's sum is such a pair, and from there on sums are integers in units of 2^-56, the
+// thread's sum is such a pair, and from there on sums are integers in units of 2^-52, the
 // same however the row is split.  (Everything as 64-bit integers took 63 us for 8 trees
-// of 64 nodes over 131,072 tokens.)
+// of 64 nodes over 131,072 tokens; a test in 64-bit floating point alone 1 us.)
 //
 // A cluster of 4 to 16 CTAs takes a sequence.  All of them walk the tree alike, on the
 // first tests' numbers, which are fetched together at the start; where a sum over
-// the vocabulary is needed each reads its part of the rows and the sums meet in
-// distributed shared memory.
+// the vocabulary is needed each reads its part of the rows and sends its sum to all, with
+// the mbarrier that the first warp of each waits on.
 #include <cooperative_groups.h>
 
 #include "tq_device.cuh"
@@ -35,7 +35,10 @@ constexpr int kVerThreads = 1024;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerNodes = TQ_MAX_TREE_NODES;
 constexpr int kVerGroups = 2;            // groups of 4 elements that a thread holds
-constexpr float kUnits = 72057594037927936.f;   // 2^56
+constexpr float kUnits = 4503599627370496.f;    // 2^52
+// Sums are cut so that none wraps, whatever the rows hold: those of a lane and a warp at
+// 2^5, of a CTA at 2^7.
+constexpr uint64_t kMostWarp = 1ull << 57, kMostCta = 1ull << 59;
 
 // What is not above 0 (a NaN) counts as 0, what is above 1 as 1.
 __device__ __forceinline__ float unit(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
@@ -49,12 +52,12 @@ __device__ __forceinline__ uint64_t to_q64(float u) {
 struct Two {
     float h, l;
 };
-// In units of 2^-56 (of a number that is not below 0).
-__device__ __forceinline__ uint64_t to_q56(Two x) {
+// In units of 2^-52 (of a number that is not below 0).
+__device__ __forceinline__ uint64_t to_units(Two x) {
     const long long n = __float2ll_rz(x.h * kUnits) + __float2ll_rz(x.l * kUnits);
     return n > 0 ? static_cast<uint64_t>(n) : 0ull;
 }
-__device__ __forceinline__ Two from_q56(uint64_t n) {
+__device__ __forceinline__ Two from_units(uint64_t n) {
     const float h = __ull2float_rn(n) * (1.f / kUnits);
     return Two{h, __ll2float_rn(static_cast<long long>(n) - __float2ll_rz(h * kUnits)) * (1.f / kUnits)};
 }
@@ -75,12 +78,27 @@ __device__ __forceinline__ Two less(Two w, Two z, float q) {
     return h > 0.f ? Two{h, __fsub_rn(t, __fsub_rn(h, s))} : Two{0.f, 0.f};
 }
 
+// Bounded wait for a phase of a barrier that other CTAs complete.
+__device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 255u) == 0 && global_timer_ns() - t0 > 2000000000ull) return false;
+    }
+}
+
 struct VerifyShared {
     int parent[kVerNodes];     // -1: never tried
     int token[kVerNodes];
     float u[kVerNodes], p[kVerNodes], q[kVerNodes];   // p, q: of the node's token after its parent
-    double z[kVerNodes];       // Z_k at the path's end, k > 0
-    Two z2[kVerNodes];         // the same
+    Two z[kVerNodes];          // Z_k at the path's end, k > 0
     uint32_t first[kVerNodes / 32];   // bit i: accepted if it is its parent's first child to be tried
     int gone[kVerNodes];       // without draft rows: the tokens rejected there
     int path[kVerNodes];
@@ -88,25 +106,34 @@ struct VerifyShared {
     uint64_t cta_sum[2][kVerCtas];
     int cur, k, len, done;
     int tested;                // the child rejected last
+    uint64_t bar[2];           // the sums of every second sweep are here
 };
 
 // What is left of a token after rejection j, from what was before.
 template <bool DRAFT>
 __device__ __forceinline__ Two reject(const VerifyShared& s, int j, Two w, float q, int token) {
     if constexpr (!DRAFT) return s.gone[j] == token ? Two{0.f, 0.f} : w;
-    if (j > 0) return less(w, s.z2[j], q);
+    if (j > 0) return less(w, s.z[j], q);
     const float h = __fsub_rn(w.h, q);   // (Z_0 = 1; exact with its error where p > q)
     return h > 0.f ? Two{h, __fsub_rn(__fsub_rn(w.h, h), q)} : Two{0.f, 0.f};
 }
-// What is left of one token after k rejections, for a test.
-template <bool DRAFT>
-__device__ __forceinline__ double left_of_64(const VerifyShared& s, int k, float p, float q, int token) {
-    double w = unit(p);
-    for (int j = 0; j < k; ++j) {
-        if constexpr (DRAFT) w = fmax(w - (j == 0 ? 1.0 : s.z[j]) * double(unit(q)), 0.0);
-        else if (s.gone[j] == token) w = 0.0;
-    }
-    return w;
+// Whether u q z < w.
+__device__ __forceinline__ bool accepts(float u, float q, Two z, Two w) {
+    const float h = __fmul_rn(u, q), l = __fmaf_rn(u, q, -h);     // u q, exactly
+    const float ph = __fmul_rn(z.h, h);
+    const float pl = __fmaf_rn(z.h, l, __fmaf_rn(z.l, h, __fmaf_rn(z.h, h, -ph)));
+    // (the difference of the high parts is exact where they are near one another)
+    return __fadd_rn(__fsub_rn(ph, w.h), __fsub_rn(pl, w.l)) < 0.f;
+}
+
+// A number to the shared memory of CTA `rank` of the cluster (the place and barrier that
+// this CTA has at these addresses), whose barrier counts its 8 bytes.
+__device__ __forceinline__ void send_u64(uint32_t at, uint32_t bar, int rank, uint64_t x) {
+    asm volatile(
+        "{\n .reg .b32 a, b;\n mapa.shared::cluster.u32 a, %0, %2;\n mapa.shared::cluster.u32 b, %1, %2;\n"
+        " st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [a], %3, [b];\n}\n" ::"r"(at),
+        "r"(bar), "r"(rank), "l"(x)
+        : "memory");
 }
 
 // Elements 4 x .. 4 x + 3 of a row that starts `off` floats behind a 16-byte
@@ -131,13 +158,22 @@ __global__ void __launch_bounds__(kVerThreads, 1)
     const int ctas = static_cast<int>(cluster.num_blocks());
     const int b = static_cast<int>(blockIdx.x) / ctas;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t bar = smem_u32(s.bar);
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        mbar_init(bar + 8, 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
+    // (met before the first sum is sent: the other CTAs run and their barriers are there)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
     griddep_wait();
     griddep_launch_dependents();
     const size_t row0 = static_cast<size_t>(b) * p.nodes;
 
     // ---- the nodes, and the numbers of each one's first test ----
     bool bad = false;
-    static_assert(kVerNodes <= kVerThreads, "a node a thread");
+    static_assert(kVerNodes <= kVerThreads && kVerWarps == 32, "a node a thread, a warp's sum a lane");
     bool first = false;
     if (tid < p.nodes) {
         const int i = tid;
@@ -151,8 +187,7 @@ __global__ void __launch_bounds__(kVerThreads, 1)
         s.parent[i] = tried ? up : -1;
         s.p[i] = tried ? __ldg(p.target + (row0 + up) * p.ld_target + x) : 0.f;
         s.q[i] = !tried ? 0.f : DRAFT ? __ldg(p.draft + (row0 + up) * p.ld_draft + x) : 1.f;
-        // (a product of 48 bits: exact)
-        first = double(unit(s.u[i])) * double(unit(s.q[i])) < double(unit(s.p[i]));
+        first = accepts(unit(s.u[i]), unit(s.q[i]), Two{1.f, 0.f}, Two{unit(s.p[i]), 0.f});
     }
     const unsigned first_mask = __ballot_sync(0xffffffffu, first);
     if (lane == 0 && warp < kVerNodes / 32) s.first[warp] = first_mask;
@@ -162,15 +197,13 @@ __global__ void __launch_bounds__(kVerThreads, 1)
         s.k = 0;
         s.len = 1;
         s.path[0] = 0;
-        // (stands where no element is found: a row without positive entries, or whose sum
-        // passes 2^7; the warp that finds one writes after a cluster barrier)
-        if (rank == 0) p.next[b] = 0;
     }
     __syncthreads();
 
     // Sum of what is left of row `cur` after k rejections, over this CTA's part
     // (a contiguous run of elements a warp); then over the cluster.
     int sweeps = 0;
+    bool stalled = false;   // (warp 0) a sum did not come in time
     int run0 = 0, run1 = 0, off = 0;   // this warp's groups of 4 elements; the row's offset
     const float *pr = nullptr, *qr = nullptr;
     bool aligned = true;
@@ -250,20 +283,25 @@ __global__ void __launch_bounds__(kVerThreads, 1)
         }
         held_cur = cur;
         held_k = k;
-        uint64_t sum = to_q56(part);
+        uint64_t sum = min(to_units(part), kMostWarp);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum = min(sum, kMostWarp);
         if (lane == 0) s.warp_sum[warp] = sum;
         __syncthreads();
-        const int par = sweeps++ & 1;
+        // (two places and barriers in turn: a CTA may send its next sum before another has
+        // all of this one)
+        const int par = sweeps & 1;
         if (warp == 0) {
-            uint64_t all = lane < kVerWarps ? s.warp_sum[lane] : 0ull;
+            uint64_t all = s.warp_sum[lane];
 #pragma unroll
-            for (int o = kVerWarps / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-            // (two slots: a CTA may be at its next sweep before another has read this one)
-            if (lane < ctas) *cluster.map_shared_rank(&s.cta_sum[par][rank], lane) = all;
+            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+            if (lane == 0) mbar_arrive_expect_tx(bar + 8 * par, 8 * ctas);
+            __syncwarp();
+            if (lane < ctas) send_u64(smem_u32(&s.cta_sum[par][rank]), bar + 8 * par, lane, min(all, kMostCta));
+            stalled = stalled || !cluster_wait(bar + 8 * par, (sweeps >> 1) & 1);
         }
-        cluster.sync();
+        ++sweeps;
     };
     // The whole of the last sweep, for every lane of a warp.
     auto whole = [&]() {
@@ -273,6 +311,7 @@ __global__ void __launch_bounds__(kVerThreads, 1)
         return __shfl_sync(0xffffffffu, all, 0);
     };
 
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
     // ---- the walk ----
     const int up0 = lane < p.nodes ? s.parent[lane] : -1;   // (the first 32 nodes' at hand)
     for (;;) {
@@ -282,10 +321,13 @@ __global__ void __launch_bounds__(kVerThreads, 1)
             int done = 0;
             for (;;) {
                 int child = -1;
-                for (int x = (tested + 1) & ~31; x < p.nodes && child < 0; x += 32) {
+                if (tested < 31) {
+                    const unsigned hit = __ballot_sync(0xffffffffu, lane > tested && up0 == cur);
+                    if (hit) child = __ffs(hit) - 1;
+                }
+                for (int x = max(32, (tested + 1) & ~31); child < 0 && x < p.nodes; x += 32) {
                     const int i = x + lane;
-                    const int up = x == 0 ? up0 : i < p.nodes ? s.parent[i] : -1;
-                    const unsigned hit = __ballot_sync(0xffffffffu, i > tested && up == cur);
+                    const unsigned hit = __ballot_sync(0xffffffffu, i > tested && i < p.nodes && s.parent[i] == cur);
                     if (hit) child = x + __ffs(hit) - 1;
                 }
                 if (child < 0) {
@@ -297,8 +339,10 @@ __global__ void __launch_bounds__(kVerThreads, 1)
                 if (k == 0) {
                     yes = (s.first[child >> 5] >> (child & 31)) & 1u;
                 } else {
-                    const double left = left_of_64<DRAFT>(s, k, s.p[child], s.q[child], s.token[child]);
-                    yes = double(unit(s.u[child])) * double(unit(s.q[child])) * s.z[k] < left;
+                    Two left{unit(s.p[child]), 0.f};
+                    const float q = unit(s.q[child]);
+                    for (int j = 0; j < k; ++j) left = reject<DRAFT>(s, j, left, q, s.token[child]);
+                    yes = accepts(unit(s.u[child]), q, s.z[k], left);
                 }
                 if (!yes) break;   // (the sum of what is left comes next)
                 cur = child;
@@ -325,10 +369,7 @@ __global__ void __launch_bounds__(kVerThreads, 1)
         sweep(s.cur, s.k);
         if (warp == 0) {
             const uint64_t z = whole();
-            if (lane == 0) {
-                s.z[s.k] = double(z) / kUnits;
-                s.z2[s.k] = from_q56(z);
-            }
+            if (lane == 0) s.z[s.k] = from_units(z);
             __syncwarp();
         }
     }
@@ -337,14 +378,23 @@ __global__ void __launch_bounds__(kVerThreads, 1)
     int k = s.k;
     const int cur = s.cur;
     // (after a rejection the last sweep left its sums)
+    // (the other warps see the sums that warp 0 waited for behind a barrier: that of the
+    // walk, or the one here)
     uint64_t all = k > 0 ? whole() : 0ull;
     if (all == 0) {   // a leaf, or nothing left: the target's row itself
         k = 0;
         sweep(cur, 0);
+        __syncthreads();
         all = whole();
     }
+    if (__syncthreads_or(stalled) && tid == 0) atomicOr(p.status, kStatusPipelineStall);
+    // (met at the end: no CTA leaves while another may still send to it)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
     if (all == 0) {
-        if (rank == 0 && tid == 0) atomicOr(p.status, kStatusBadValue);
+        if (rank == 0 && tid == 0) {
+            p.next[b] = 0;
+            atomicOr(p.status, kStatusBadValue);
+        }
     } else {
         uint64_t t = __umul64hi(to_q64(s.u[0]), all);
         // the CTA, the warp and the element whose running sum passes t < all
@@ -367,7 +417,7 @@ __global__ void __launch_bounds__(kVerThreads, 1)
                     int mine = -1;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        own += n[e] = to_q56(w[i][e]);
+                        own += n[e] = to_units(w[i][e]);
                         if (w[i][e].h > 0.f) mine = at + e;
                     }
                     uint64_t inc = own;
@@ -401,7 +451,8 @@ __global__ void __launch_bounds__(kVerThreads, 1)
         for (int i = tid; i < p.nodes; i += kVerThreads) p.keep[row0 + i] = i < s.len ? s.path[i] : -1;
         if (tid == 0) p.num_keep[b] = s.len;
     }
-    cluster.sync();   // (no CTA leaves while another may still write to its shared memory)
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
 template <bool DRAFT>
