@@ -57,9 +57,12 @@ __device__ __forceinline__ uint64_t to_units(Two x) {
     const long long n = __float2ll_rz(x.h * kUnits) + __float2ll_rz(x.l * kUnits);
     return n > 0 ? static_cast<uint64_t>(n) : 0ull;
 }
-__device__ __forceinline__ Two from_units(uint64_t n) {
-    const float h = __ull2float_rn(n) * (1.f / kUnits);
-    return Two{h, __ll2float_rn(static_cast<long long>(n) - __float2ll_rz(h * kUnits)) * (1.f / kUnits)};
+__device__ __forceinline__ Two from_units(uint64_t n) {   // (n <= 2^63, in pieces of 27, 24 and 12 bits)
+    const float a = static_cast<float>(static_cast<uint32_t>(n >> 36)) * 1.52587890625e-5f;   // 2^-16
+    const float b = static_cast<float>(static_cast<uint32_t>(n >> 12) & 0xffffffu) * 9.094947017729282e-13f;   // 2^-40
+    const float c = static_cast<float>(static_cast<uint32_t>(n) & 0xfffu) * 2.220446049250313e-16f;   // 2^-52
+    const float h = __fadd_rn(a, b);
+    return Two{h, __fadd_rn(__fsub_rn(b, __fsub_rn(h, a)), c)};
 }
 __device__ __forceinline__ void add_to(Two& sum, Two x) {   // Knuth's two-sum, then the low parts
     const float s = __fadd_rn(sum.h, x.h), v = __fsub_rn(s, sum.h);
@@ -260,7 +263,8 @@ __global__ void __launch_bounds__(kVerThreads, 1)
             aligned = (reinterpret_cast<uintptr_t>(qr) & 15u) == 0;
         }
         const int groups = (off + p.vocab + 3) / 4;
-        const int per = (groups + ctas * kVerWarps - 1) / (ctas * kVerWarps);
+        const int log2 = 5 + (31 - __clz(ctas));   // warps of the cluster
+        const int per = (groups + (1 << log2) - 1) >> log2;
         run0 = min(groups, (rank * kVerWarps + warp) * per);
         run1 = min(groups, run0 + per);
         return per <= 32 * kVerGroups;
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kVerThreads, 1)
     bool held = false;            // the batch is the warp's whole run of the row,
     int held_cur = -1, held_k = 0;  // of this node after that many rejections
     auto sweep = [&](int cur, int k) {
-        held = rows_of(cur);
+        if (cur != held_cur) held = rows_of(cur);
         Two part{0.f, 0.f};
         for (int x0 = run0; x0 < run1; x0 += 32 * kVerGroups) {
             if (!held || held_cur != cur || held_k > k) {
@@ -412,6 +416,7 @@ __global__ void __launch_bounds__(kVerThreads, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < kVerGroups; ++i) {
+                    if (found) continue;   // (uniform)
                     const int at = 4 * (x0 + lane + 32 * i) - off;   // the first of the lane's four tokens
                     uint64_t n[4], own = 0;
                     int mine = -1;
@@ -427,7 +432,7 @@ __global__ void __launch_bounds__(kVerThreads, 1)
                         if (lane >= o) inc += y;
                     }
                     const unsigned hit = __ballot_sync(0xffffffffu, inc > t);
-                    if (hit && !found) {
+                    if (hit) {
                         if (lane == __ffs(hit) - 1) {
                             uint64_t run = inc - own;
                             int e = 0;

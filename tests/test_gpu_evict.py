@@ -92,6 +92,23 @@ def test_every_mode(dev, mode, other):
     assert run_evict(dev, mode, 608, lengths, counts, 3, 5, w, other) == 0
 
 
+@pytest.mark.parametrize("other", [False, True], ids=["in_place", "other"])
+@pytest.mark.parametrize("mode", MODES)
+def test_every_mode_with_many_units(dev, mode, other):
+    """More units than CTAs that are resident at once: the first ones are done while the
+    lengths of others are still read."""
+    rng = np.random.default_rng(16)
+    lengths = [int(x) for x in rng.integers(0, 1301, 100)]
+    counts = [int(x) for x in rng.integers(12, 1200, 100)]
+    bad = [int(b) for b in rng.choice(100, 9, replace=False)]
+    for b in bad:
+        counts[b], lengths[b] = -3, 900
+    w = heavy((100, 8, 1312), 17)
+    status = run_evict(dev, mode, 1312, lengths, counts, 3, 5, w, other, Hkv=8, bad=bad)
+    assert status == tqf.TQ_STATUS_BAD_INDEX
+    assert run_evict(dev, mode, 1312, [1300] * 100, [700] * 100, 0, 0, w, other, Hkv=8, weights_in_place=not other) == 0
+
+
 @pytest.mark.parametrize("L,n", [
     (1, 1), (2, 1), (33, 32), (4096, 1), (4095, 2000),       # 8 keys a thread
     (4097, 4096), (8192, 3001), (8191, 17),                  # 16, or 8 of twice the threads
