@@ -126,6 +126,14 @@ __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// The cluster's barrier, met in two steps by every thread of its CTAs (whole warps together).
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
 // Named barriers (ids 1..15; 0 is __syncthreads) over n threads, whole warps.
 // Every thread that takes part must reach each use: callers place them on
 // paths no thread leaves early.

@@ -82,7 +82,7 @@ __device__ __forceinline__ Two less(Two w, Two z, float q) {
 }
 
 // Bounded wait for a phase of a barrier that other CTAs complete.
-__device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_for_sums(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = global_timer_ns();
     for (uint32_t i = 1;; ++i) {
         uint32_t ok;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kVerThreads, 1)
     }
     __syncwarp();
     // (met before the first sum is sent: the other CTAs run and their barriers are there)
-    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+    cluster_arrive();
     griddep_wait();
     griddep_launch_dependents();
     const size_t row0 = static_cast<size_t>(b) * p.nodes;
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kVerThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(bar + 8 * par, 8 * ctas);
             __syncwarp();
             if (lane < ctas) send_u64(smem_u32(&s.cta_sum[par][rank]), bar + 8 * par, lane, min(all, kMostCta));
-            stalled = stalled || !cluster_wait(bar + 8 * par, (sweeps >> 1) & 1);
+            stalled = stalled || !wait_for_sums(bar + 8 * par, (sweeps >> 1) & 1);
         }
         ++sweeps;
     };
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kVerThreads, 1)
         return __shfl_sync(0xffffffffu, all, 0);
     };
 
-    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    cluster_wait();
     // ---- the walk ----
     const int up0 = lane < p.nodes ? s.parent[lane] : -1;   // (the first 32 nodes' at hand)
     for (;;) {
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kVerThreads, 1)
     }
     if (__syncthreads_or(stalled) && tid == 0) atomicOr(p.status, kStatusPipelineStall);
     // (met at the end: no CTA leaves while another may still send to it)
-    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+    cluster_arrive();
     if (all == 0) {
         if (rank == 0 && tid == 0) {
             p.next[b] = 0;
@@ -457,37 +457,19 @@ __global__ void __launch_bounds__(kVerThreads, 1)
         if (tid == 0) p.num_keep[b] = s.len;
     }
     __syncwarp();
-    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    cluster_wait();
 }
 
 template <bool DRAFT>
 static int launch_t(const VerifyParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> attr_done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = allow_large_clusters_once(tq_verify_kernel<DRAFT>, attr_done);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
-    if (bit == 0 || (attr_done.load(std::memory_order_acquire) & bit) == 0) {
-        e = cudaFuncSetAttribute(tq_verify_kernel<DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        attr_done.fetch_or(bit, std::memory_order_acq_rel);
-    }
     // as many CTAs as fit at once, one per SM
     int ctas = kVerCtas;
     while (ctas > 1 && 1ll * p.batch * ctas > host::kSMs) ctas /= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * ctas);
-    cfg.blockDim = dim3(kVerThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, tq_verify_kernel<DRAFT>, p);
+    return launch_pdl_cluster(tq_verify_kernel<DRAFT>, dim3(static_cast<unsigned>(p.batch) * ctas), dim3(kVerThreads),
+                              ctas, 0, stream, p);
 }
 
 int launch_verify(const VerifyParams& p, cudaStream_t stream) {

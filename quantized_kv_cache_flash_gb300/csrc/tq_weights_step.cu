@@ -9,11 +9,22 @@
 // log-sum-exp and turns the scores into the tokens' weights, a token a thread.  (Scores
 // of 4 to 8 rows are 16 to 32 bytes a token, mostly served by L2; reading K once more
 // would be 48 to 256 and another dequantisation.)
+//
+// Where a cluster of 16 CTAs per unit fits the GPU at once (few units), one kernel does
+// both: the scores stay in shared memory, and the CTAs of a cluster exchange their
+// (maximum, sum) pairs there.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "tq_decode_kernel.cuh"
 
 namespace tq {
+
+namespace cg = cooperative_groups;
+
+constexpr int kStepCluster = 16;   // CTAs per unit of the one-kernel form
+constexpr int kStepOneTokens = 512; // tokens of such a CTA, at most
 
 template <int KB, int ROWS>
 struct StepCfg {
@@ -39,6 +50,11 @@ struct StepCfg {
     static constexpr int kMlOff = kScanOff + kWarps * 512;  // (m, l) of the warps' rows
     static constexpr int kSmem = kMlOff + kWarps * ROWS * 8;
     static constexpr int kSmemAlloc = kSmem + 1024;
+    // one-kernel form: the cluster's (m, l) pairs, the rows' log-sum-exp, the scores
+    static constexpr int kPartOff = (kSmem + 15) / 16 * 16;
+    static constexpr int kLseOff = kPartOff + kStepCluster * ROWS * 8;
+    static constexpr int kScoreOff = kLseOff + ROWS * 4;
+    static constexpr int kOneAlloc(int tokens) { return kScoreOff + tokens * ROWS * 4 + 1024; }
 
     __device__ static __forceinline__ int slot_row(int n, int e, int t) { return kPair ? t : 8 * n + 2 * t + e; }
 };
@@ -50,8 +66,9 @@ __device__ __forceinline__ void join(float& m, float& l, float mb, float lb) {
     m = mn;
 }
 
-template <int KB, int ROWS>
-__global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
+// ONE: the one-kernel form.
+template <int KB, int ROWS, bool ONE>
+__global__ void __launch_bounds__(128, ONE ? 2 : StepCfg<KB, ROWS>::kMinCtas)
     tq_step_scores_kernel(const __grid_constant__ StepParams p, const __grid_constant__ CUtensorMap kmap) {
     using C = StepCfg<KB, ROWS>;
     constexpr int NT = C::NT, NE = C::NE;
@@ -68,16 +85,20 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
     }
     if (KB == 0 && threadIdx.x == 0) prefetch_tensormap(&kmap);
     __syncwarp();
+    if constexpr (ONE) cluster_arrive();   // (met before the pairs are exchanged: all CTAs run)
 
     griddep_wait();
     BatchScan scan;
-    scan.init(reinterpret_cast<int*>(smem + C::kScanOff) + warp * 128, p.lengths, p.batch, p.hkv, p.max_len, lane);
-    const int all = __shfl_sync(0xffffffffu, scan.total(p.lengths, p.batch, p.hkv, p.max_len, lane), 0);
-    const int P = static_cast<int>(gridDim.x), c_me = static_cast<int>(blockIdx.x);
-    const int cq = all / P, cr = all - cq * P;
-    const int lo = c_me * cq + (c_me * cr) / P;
-    const int hi = (c_me + 1) * cq + ((c_me + 1) * cr) / P;
-    if (lo >= hi) return;   // (uniform over the CTA)
+    int lo = 0, hi = 1;   // (ONE: a single share)
+    if constexpr (!ONE) {
+        scan.init(reinterpret_cast<int*>(smem + C::kScanOff) + warp * 128, p.lengths, p.batch, p.hkv, p.max_len, lane);
+        const int all = __shfl_sync(0xffffffffu, scan.total(p.lengths, p.batch, p.hkv, p.max_len, lane), 0);
+        const int P = static_cast<int>(gridDim.x), c_me = static_cast<int>(blockIdx.x);
+        const int cq = all / P, cr = all - cq * P;
+        lo = c_me * cq + (c_me * cr) / P;
+        hi = (c_me + 1) * cq + ((c_me + 1) * cr) / P;
+        if (lo >= hi) return;   // (uniform over the CTA)
+    }
     __half* sQ = reinterpret_cast<__half*>(smem + C::kQOff);
     __half* sQlo = reinterpret_cast<__half*>(smem + C::kQloOff);
     const uint32_t q_lds = smem_u32(sQ) + ((lane & 7) * C::kQStride + 8 * (lane >> 3)) * 2;
@@ -89,14 +110,26 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
     uint32_t phase = 0;
     int pos = lo;
     while (pos < hi) {
-        int b, before, L, nch;
-        scan.locate(p.lengths, p.batch, p.hkv, p.max_len, pos, lane, b, before, L, nch);
-        b = __shfl_sync(0xffffffffu, b, 0);
-        before = __shfl_sync(0xffffffffu, before, 0);
-        L = __shfl_sync(0xffffffffu, L, 0);
-        nch = __shfl_sync(0xffffffffu, nch, 0);
-        const int h = (pos - before) / nch, k0 = pos - before - h * nch;
-        const int k1 = min(nch, k0 + (hi - pos));
+        int b, h, L, k0, k1;   // tokens of chunks [k0, k1) of unit (b, h)
+        if constexpr (ONE) {
+            const int u = static_cast<int>(blockIdx.x) / kStepCluster, rank = static_cast<int>(blockIdx.x) % kStepCluster;
+            b = u / p.hkv;
+            h = u - b * p.hkv;
+            L = p.lengths[b];
+            const int nch = unit_chunks(p.lengths, b, p.max_len);
+            k0 = rank * nch / kStepCluster;
+            k1 = (rank + 1) * nch / kStepCluster;
+        } else {
+            int before, nch;
+            scan.locate(p.lengths, p.batch, p.hkv, p.max_len, pos, lane, b, before, L, nch);
+            b = __shfl_sync(0xffffffffu, b, 0);
+            before = __shfl_sync(0xffffffffu, before, 0);
+            L = __shfl_sync(0xffffffffu, L, 0);
+            nch = __shfl_sync(0xffffffffu, nch, 0);
+            h = (pos - before) / nch;
+            k0 = pos - before - h * nch;
+            k1 = min(nch, k0 + (hi - pos));
+        }
         const int unit = b * p.hkv + h;
         const int t_begin = k0 * kChunkTokens, t_end = min(k1 * kChunkTokens, min(L, p.max_len));
         const int nchunks = (t_end - t_begin + C::kTok - 1) / C::kTok;   // stages' worth of tokens
@@ -178,7 +211,9 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
                 lim[n][e] = min(L - p.tq + C::slot_row(n, e, t) / p.group, t_end - 1);
             }
         // this thread's first score of the share
-        float* const out = p.scores + (static_cast<size_t>(unit) * p.score_len + t_begin + g) * ROWS + C::slot_row(0, 0, t);
+        float* const out = (ONE ? reinterpret_cast<float*>(smem + C::kScoreOff)
+                                : p.scores + (static_cast<size_t>(unit) * p.score_len + t_begin) * ROWS) +
+                           g * ROWS + C::slot_row(0, 0, t);
         const int all_see = min(L - p.tq, t_end - 1);   // (padding rows see more; nobody reads them)
 
         // 32 tokens of a stage from its token `at`: scores to the workspace, maxima and sums
@@ -316,7 +351,7 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
             }
             if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
         }
-        if (pos + k1 - k0 >= hi) griddep_launch_dependents();
+        if (ONE || pos + k1 - k0 >= hi) griddep_launch_dependents();
         if (stalled) {   // this warp's copies still in flight land (bounded)
             for (int k = 0; k < C::kStages; ++k) {
                 if (c + C::kWarps * k >= nchunks) break;
@@ -345,7 +380,51 @@ __global__ void __launch_bounds__(128, StepCfg<KB, ROWS>::kMinCtas)
                 const float2 o = sML[w * ROWS + threadIdx.x];
                 join(a.x, a.y, o.x, o.y);
             }
-            p.part_ml[(static_cast<size_t>(blockIdx.x) + unit) * ROWS + threadIdx.x] = a;
+            if constexpr (ONE) sML[threadIdx.x] = a;
+            else p.part_ml[(static_cast<size_t>(blockIdx.x) + unit) * ROWS + threadIdx.x] = a;
+        }
+        if constexpr (ONE) {
+            // every CTA of the cluster gets all shares' pairs, joins them and weighs its tokens
+            cg::cluster_group cluster = cg::this_cluster();
+            float2* parts = reinterpret_cast<float2*>(smem + C::kPartOff);
+            float* lse = reinterpret_cast<float*>(smem + C::kLseOff);
+            cluster_wait();
+            __syncthreads();
+            for (int i = threadIdx.x; i < kStepCluster * ROWS; i += 128) {
+                const int r = i % ROWS;
+                *cluster.map_shared_rank(parts + cluster.block_rank() * ROWS + r, i / ROWS) = sML[r];
+            }
+            cluster.sync();
+            if (threadIdx.x < ROWS) {
+                float am = -INFINITY, al = 0.f;
+#pragma unroll
+                for (int c2 = 0; c2 < kStepCluster; ++c2) {
+                    const float2 v = parts[c2 * ROWS + threadIdx.x];
+                    join(am, al, v.x, v.y);
+                }
+                const bool none = am == -INFINITY && al == 0.f;
+                lse[threadIdx.x] = none || threadIdx.x >= p.rows ? INFINITY : am + log2f(al);
+                if (none && threadIdx.x < p.rows && cluster.block_rank() == 0) atomicOr(p.status, kStatusShortContext);
+            }
+            __syncthreads();
+            const int seen = p.seen != nullptr ? p.seen[b] : L - p.tq;
+            float* w_out = p.weights + static_cast<size_t>(unit) * p.cap;
+            for (int tok = t_begin + threadIdx.x; tok < t_end; tok += 128) {
+                const float* x = reinterpret_cast<const float*>(smem + C::kScoreOff) + (tok - t_begin) * ROWS;
+                float w = 0.f;
+#pragma unroll
+                for (int r = 0; r < ROWS; r += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(x + r), l4 = *reinterpret_cast<const float4*>(lse + r);
+                    // (-inf: hidden, also from a row of NaN; padding rows' lse is inf)
+                    w += r < p.rows && v.x != -INFINITY ? fast_exp2(v.x - l4.x) : 0.f;
+                    w += r + 1 < p.rows && v.y != -INFINITY ? fast_exp2(v.y - l4.y) : 0.f;
+                    w += r + 2 < p.rows && v.z != -INFINITY ? fast_exp2(v.z - l4.z) : 0.f;
+                    w += r + 3 < p.rows && v.w != -INFINITY ? fast_exp2(v.w - l4.w) : 0.f;
+                }
+                if (p.decay != 0.f && tok < seen) w = fmaf(p.decay, w_out[tok], w);
+                w_out[tok] = w;
+            }
+            return;
         }
         if (__syncthreads_or(stalled)) break;
         pos += k1 - k0;
@@ -456,12 +535,29 @@ __global__ void __launch_bounds__(256) tq_step_sums_kernel(const __grid_constant
 }
 
 template <int KB, int ROWS>
+static int launch_one(const StepParams& p, const CUtensorMap* kmap, int tokens, cudaStream_t stream) {
+    using C = StepCfg<KB, ROWS>;
+    auto* kernel = tq_step_scores_kernel<KB, ROWS, true>;
+    static std::atomic<uint64_t> attr_done{0}, size_done{0};
+    cudaError_t e = set_smem_attr_once(kernel, C::kOneAlloc(kStepOneTokens), size_done);
+    if (e == cudaSuccess) e = allow_large_clusters_once(kernel, attr_done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(p.batch) * p.hkv * kStepCluster), dim3(128), kStepCluster,
+                              C::kOneAlloc(tokens), stream, p, *kmap);
+}
+
+template <int KB, int ROWS>
 static int launch_t(StepParams p, const CUtensorMap* kmap, cudaStream_t stream) {
     using C = StepCfg<KB, ROWS>;
+    // tokens of a CTA of the one-kernel form, where all clusters are resident at once, two
+    // CTAs an SM
+    const int tokens = ((p.max_len + 31) / 32 + kStepCluster - 1) / kStepCluster * 32;
+    if (1ll * p.batch * p.hkv * kStepCluster <= 2 * host::kSMs && tokens <= kStepOneTokens)
+        return launch_one<KB, ROWS>(p, kmap, tokens, stream);
     static std::atomic<uint64_t> attr_done{0};
-    cudaError_t e = set_smem_attr_once(tq_step_scores_kernel<KB, ROWS>, C::kSmemAlloc, attr_done);
+    cudaError_t e = set_smem_attr_once(tq_step_scores_kernel<KB, ROWS, false>, C::kSmemAlloc, attr_done);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(tq_step_scores_kernel<KB, ROWS>, dim3(p.ctas), dim3(128), C::kSmemAlloc, stream, p, *kmap);
+    e = launch_pdl(tq_step_scores_kernel<KB, ROWS, false>, dim3(p.ctas), dim3(128), C::kSmemAlloc, stream, p, *kmap);
     if (e != cudaSuccess) return e;
     // Few tokens: a token a thread, so that more SMs share them.  Many: up to 8 a thread,
     // four loads in flight, for as many CTAs as are resident at once.
