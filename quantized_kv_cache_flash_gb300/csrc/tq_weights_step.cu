@@ -24,7 +24,7 @@ namespace tq {
 namespace cg = cooperative_groups;
 
 constexpr int kStepCluster = 16;   // CTAs per unit of the one-kernel form
-constexpr int kStepOneTokens = 512; // tokens of such a CTA, at most
+constexpr int kStepOneTokens = 1024;   // tokens of such a CTA, at most
 
 template <int KB, int ROWS>
 struct StepCfg {
@@ -549,10 +549,14 @@ static int launch_one(const StepParams& p, const CUtensorMap* kmap, int tokens, 
 template <int KB, int ROWS>
 static int launch_t(StepParams p, const CUtensorMap* kmap, cudaStream_t stream) {
     using C = StepCfg<KB, ROWS>;
-    // tokens of a CTA of the one-kernel form, where all clusters are resident at once, two
-    // CTAs an SM
+    // The one-kernel form: up to 1024 tokens a CTA where each has an SM of its own, for
+    // quantized K up to 512 where four share one.  (turbo3, 4 units of 8,000 tokens 7.2 us
+    // and 11.6 with two kernels, of 16,000 10.3 and 13.5, of 32,000 16.4 and 15.6; 32 units
+    // of 8,000 11.7 and 13.1; 16 of 16,000 14.4 and 13.0; fp16 K, 8 units of 16,000 11.3 and
+    // 13.0, 16 of 8,000 13.0 and 13.2, 32 of 4,000 15.8 and 13.6.)
     const int tokens = ((p.max_len + 31) / 32 + kStepCluster - 1) / kStepCluster * 32;
-    if (1ll * p.batch * p.hkv * kStepCluster <= 2 * host::kSMs && tokens <= kStepOneTokens)
+    const long long ctas = 1ll * p.batch * p.hkv * kStepCluster;
+    if (ctas <= host::kSMs ? tokens <= kStepOneTokens : KB != 0 && ctas <= 4 * host::kSMs && tokens <= kStepOneTokens / 2)
         return launch_one<KB, ROWS>(p, kmap, tokens, stream);
     static std::atomic<uint64_t> attr_done{0};
     cudaError_t e = set_smem_attr_once(tq_step_scores_kernel<KB, ROWS, false>, C::kSmemAlloc, attr_done);
