@@ -512,15 +512,23 @@ def tq_cache_evict(ctx: Context, dst: Cache, src: Cache, weights, num_keep, kept
 class _On:
     """The device of a call that has no cache, as the checks ask a cache for it."""
 
+    __slots__ = ("device_index", "_tensor")
+
     def __init__(self, t):
         if _F16 is None:
             _bind_torch()
-        self.device, self.device_index = t.device, t.get_device()
+        self.device_index, self._tensor = t.get_device(), t
+
+    @property
+    def device(self):
+        return self._tensor.device
 
 
 def _rows(name: str, t, shape, on) -> int:
     """Elements from one row to the next of probabilities fp32 [B, N, V] on this
     device, whose rows may have padding behind them."""
+    if t.dtype is _F32 and t.shape == shape and t.is_contiguous() and t.get_device() == on.device_index:
+        return shape[2]
     if t.dtype != _F32 or tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {_F32} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if t.get_device() != on.device_index:
@@ -542,7 +550,7 @@ def tq_verify_tree(ctx: Context, tokens, parents, target, draft, uniforms, keep,
     if target.dim() != 3 or parents.dim() != 2:
         raise ValueError("target must be [B, N, V] and parents [1 or B, N]")
     on = _On(target)
-    shape = b, n, v = tuple(target.shape)
+    b, n, v = shape = tuple(target.shape)
     ld_t = _rows("target", target, shape, on)
     ld_d = _rows("draft", draft, shape, on) if draft is not None else 0
     per_seq = parents.shape[0]

@@ -47,6 +47,14 @@ CASES = [
     ("turbo4", 8, 2, [5, 1], 4, 8.0),                       # 16 rows over fewer tokens than a stage
     ("turbo3", 28, 4, [2000], 1, 24.0),                     # peaked
     ("turbo3", 8, 2, [40 + i for i in range(40)], 1, 1.0),  # over 32 sequences
+    # (many units: two kernels; the ones above mostly take one)
+    ("turbo4", 28, 4, [11 * i for i in range(12)], 1, 1.0),
+    ("turbo3", 28, 4, [63 + i for i in range(12)], 1, 1.0),
+    ("turbo3_asym", 28, 4, [200, 0, 31, 777], 1, 1.0),
+    ("turbo4k_3v", 16, 2, [5 + 13 * i for i in range(20)], 2, 1.0),
+    ("turbo3", 16, 2, [300 - 9 * i for i in range(20)], 2, 1.0),
+    ("turbo4_asym", 16, 2, [90, 33, 0, 2, 500, 64], 2, 1.0),
+    ("turbo4", 8, 2, [2 * i for i in range(40)], 1, 16.0),
     ("turbo4", 8, 2, [300, 2], 5, 1.0),                     # 20 rows
     ("turbo3", 28, 4, [517, 33], 16, 1.0),                  # 112 rows
     ("turbo4_asym", 28, 4, [700, 0, 129], 33, 1.0),         # 231 rows
