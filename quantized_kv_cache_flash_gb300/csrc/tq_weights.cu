@@ -23,6 +23,7 @@
 //   13        copies Q' and the records (fp16 K: the tiles)
 // Tensor memory: two buffers of 256 columns, S(n) of both query tiles.
 #include <algorithm>
+#include <type_traits>
 
 #include "tq_device.cuh"
 #include "tq_internal.h"
@@ -49,8 +50,9 @@ struct WtCfg {
     // records copied [2], records read [2], K stored [kSlots], K read [kSlots], S done
     // [2], S read [2], Q' copied, Q' read, the issuing warps' turns [2]; the TMEM slot
     static constexpr int kHalfOff = kPosOff + 1024;             // fp32 the second query tile's sums [4][128]
+    static constexpr int kSpanOff = kHalfOff + 2048;            // int2 least and largest position of 32 rows [8]
     static constexpr int kGo = 10 + 2 * kSlots;                 // the other issuing warp's turn [2]
-    static constexpr int kBarOff = kHalfOff + 2048;
+    static constexpr int kBarOff = kSpanOff + 64;
     static constexpr int kSmem = kBarOff + (kGo + 2) * 8 + 8;
     static constexpr int kSmemAlloc = kSmem + 768;              // to a 1024-byte boundary from a 256-byte one
     static_assert(kSmemAlloc <= 232448, "227 KB per CTA");
@@ -202,6 +204,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     float* s_lse = reinterpret_cast<float*>(smem + C::kLseOff);
     int* s_pos = reinterpret_cast<int*>(smem + C::kPosOff);
     float* s_half = reinterpret_cast<float*>(smem + C::kHalfOff);
+    int2* s_span = reinterpret_cast<int2*>(smem + C::kSpanOff);
     const uint32_t bar_stg = smem_u32(smem + C::kBarOff), bar_stgf = bar_stg + 16, bar_s = bar_stg + 32,
                    bar_sf = bar_stg + 48, bar_q = bar_stg + 64, bar_qf = bar_stg + 72, bar_k = bar_stg + 80,
                    bar_kf = bar_k + 8 * NS, bar_go = bar_stg + 8 * C::kGo;
@@ -277,7 +280,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         M = mn;
                     }
                     s_lse[tid] = -(M + log2f(sum));
-                    s_pos[tid] = tid < nrows ? row0 + tid - over_tq(p, row0 + tid) * p.tq : -0x40000000;
+                    // (a row without any token is behind every token's first position)
+                    const int at = tid < nrows ? row0 + tid - over_tq(p, row0 + tid) * p.tq : -0x7fffffff - 1;
+                    s_pos[tid] = at;
+                    const int least = __reduce_min_sync(0xffffffffu, at), most = __reduce_max_sync(0xffffffffu, at);
+                    if (lane == 0) s_span[tid >> 5] = make_int2(least, most);
                 }
                 named_bar_sync(1, 256);
                 // tokens that every row of the pair sees
@@ -305,40 +312,21 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     const int t = k * kWtTile + r;
                     const float c = KB == 0 ? p.scale_log2e : s_col[128 * buf + r];
                     const uint32_t d = tmem + 256 * buf + 128 * wg + lane_off;
-                    float w;
-                    if (k * kWtTile + kWtTile - 1 > all_see || here <= 0 || (here & 31) != 0) {
-                        const int from = t - (s.L - p.tq);   // the first query position that sees the token
-                        w = 0.f;
-#pragma unroll 1
-                        for (int x = 0; x < here; x += 32) {
-                            uint32_t v[32];
-                            tmem_ld32(d + x, v);
-                            float a[4] = {0.f, 0.f, 0.f, 0.f};
+                    // 32 rows at a time, the next ones in flight: all of the warp's tokens are seen
+                    // by them, none is, or each row says which
+                    const int from = t - (s.L - p.tq);   // the first query position that sees the token
+                    const bool seen_by_all = k * kWtTile + kWtTile - 1 <= all_see;
+                    const float2 cc = make_float2(c, c);
+                    float2 a[4] = {};
+                    uint32_t v[2][32];
+                    if (chunks > 0) tmem_ld32_issue(d, v[0]);
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 l = *reinterpret_cast<const float4*>(lse + x + e);
-                                const int4 j = *reinterpret_cast<const int4*>(pos + x + e);
-                                const float y[4] = {l.x, l.y, l.z, l.w};
-                                const int jj[4] = {j.x, j.y, j.z, j.w};
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float z = fast_exp2(fmaf(__uint_as_float(v[e + i]), c, y[i]));
-                                    if (jj[i] >= from && jj[i] >= 0) a[i] += z;
-                                }
-                            }
-                            w += (a[0] + a[1]) + (a[2] + a[3]);
-                        }
-                    } else {
-                        const float2 cc = make_float2(c, c);
-                        float2 a[4] = {};
-                        uint32_t v[2][32];   // 32 rows at a time, the next ones in flight
-                        tmem_ld32_issue(d, v[0]);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            if (x >= chunks) break;
-                            tmem_ld_wait(v[x & 1]);
-                            if (x + 1 < chunks) tmem_ld32_issue(d + 32 * (x + 1), v[(x + 1) & 1]);
-                            const uint32_t* f = v[x & 1];
+                    for (int x = 0; x < 4; ++x) {
+                        if (x >= chunks) break;
+                        tmem_ld_wait(v[x & 1]);
+                        if (x + 1 < chunks) tmem_ld32_issue(d + 32 * (x + 1), v[(x + 1) & 1]);
+                        const uint32_t* f = v[x & 1];
+                        auto add = [&](auto masked) {
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
                                 const float4 l = *reinterpret_cast<const float4*>(lse + 32 * x + e);
@@ -346,14 +334,25 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                                                              cc, make_float2(l.x, l.y));
                                 const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(f[e + 2]), __uint_as_float(f[e + 3])),
                                                              cc, make_float2(l.z, l.w));
-                                a[(e >> 1) & 3] = __fadd2_rn(a[(e >> 1) & 3], make_float2(fast_exp2(y0.x), fast_exp2(y0.y)));
-                                a[((e >> 1) & 3) + 1] =
-                                    __fadd2_rn(a[((e >> 1) & 3) + 1], make_float2(fast_exp2(y1.x), fast_exp2(y1.y)));
+                                float2 z0 = make_float2(fast_exp2(y0.x), fast_exp2(y0.y));
+                                float2 z1 = make_float2(fast_exp2(y1.x), fast_exp2(y1.y));
+                                if constexpr (decltype(masked)::value) {
+                                    const int4 j = *reinterpret_cast<const int4*>(pos + 32 * x + e);
+                                    if (j.x < from) z0.x = 0.f;
+                                    if (j.y < from) z0.y = 0.f;
+                                    if (j.z < from) z1.x = 0.f;
+                                    if (j.w < from) z1.y = 0.f;
+                                }
+                                a[(e >> 1) & 3] = __fadd2_rn(a[(e >> 1) & 3], z0);
+                                a[((e >> 1) & 3) + 1] = __fadd2_rn(a[((e >> 1) & 3) + 1], z1);
                             }
-                        }
-                        const float2 t2 = __fadd2_rn(__fadd2_rn(a[0], a[1]), __fadd2_rn(a[2], a[3]));
-                        w = t2.x + t2.y;
+                        };
+                        const int2 span = s_span[4 * wg + x];   // (padding rows: -2^31)
+                        if (seen_by_all ? span.x >= 0 : span.x >= from - lane + 31) add(std::false_type{});
+                        else if (span.y >= from - lane) add(std::true_type{});
                     }
+                    const float2 t2 = __fadd2_rn(__fadd2_rn(a[0], a[1]), __fadd2_rn(a[2], a[3]));
+                    const float w = t2.x + t2.y;
                     tc_fence_before();
                     mbar_arrive(bar_sf + 8 * buf);
                     // the second query tile's part goes to the first one's thread, which looks for
@@ -373,9 +372,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 // rows of query tile wg: last visible token of this row, and of all of them
                 const int first = row0 + 128 * wg, row = first + r;
                 const int mine = row < p.rows ? min(s.L - p.tq + row - over_tq(p, row) * p.tq, lim - 1) : -1;
-                const int all_see =
-                    first + 127 < p.rows ? min(s.L - p.tq + wt_span(p, first, first + 127).x, lim - 1) : -1;
-                const bool any = first < p.rows;
+                const bool live = row < p.rows;
+                // over the warp's rows: the last token that all see, and that one sees
+                const int lo = __reduce_min_sync(0xffffffffu, live ? mine : 0x7fffffff);
+                const int hi = __reduce_max_sync(0xffffffffu, mine);
                 // A row's base m is the largest score of the tile that it first sees; later
                 // scores may pass it, as long as the sums stay in range.
                 float m = -INFINITY, l = 0.f;
@@ -385,35 +385,49 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     tc_fence_after();
                     const uint32_t d = tmem + 256 * buf + 128 * wg + lane_off;
                     const float* col = s_col + 128 * buf;
-                    const bool masked = k * kWtTile + kWtTile - 1 > all_see;
-                    bool slow = any && (masked || __any_sync(0xffffffffu, m == -INFINITY));
-                    if (any && !slow) {
-                        const float2 nb = make_float2(-m, -m);
+                    const int tok0 = k * kWtTile;
+                    const int visible = hi < tok0 ? 0 : min(4, (hi - tok0) / 32 + 1);   // pieces of 32 tokens
+                    bool slow = __any_sync(0xffffffffu, live && m == -INFINITY && mine >= tok0);
+                    if (visible > 0 && !slow) {
+                        const float base = m == -INFINITY ? 0.f : m;
+                        const float2 nb = make_float2(-base, -base);
                         float2 a[4] = {};
                         uint32_t v[2][32];   // 32 tokens at a time, the next ones in flight
                         tmem_ld32_issue(d, v[0]);
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
+                            if (x >= visible) break;
                             tmem_ld_wait(v[x & 1]);
-                            if (x < 3) tmem_ld32_issue(d + 32 * (x + 1), v[(x + 1) & 1]);
+                            if (x + 1 < visible) tmem_ld32_issue(d + 32 * (x + 1), v[(x + 1) & 1]);
                             const uint32_t* f = v[x & 1];
+                            auto add = [&](auto masked) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 c = KB == 0 ? make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e,
-                                                                       p.scale_log2e)
-                                                         : *reinterpret_cast<const float4*>(col + 32 * x + e);
-                                const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(f[e]), __uint_as_float(f[e + 1])),
-                                                             make_float2(c.x, c.y), nb);
-                                const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(f[e + 2]), __uint_as_float(f[e + 3])),
-                                                             make_float2(c.z, c.w), nb);
-                                a[(e >> 1) & 3] = __fadd2_rn(a[(e >> 1) & 3], make_float2(fast_exp2(y0.x), fast_exp2(y0.y)));
-                                a[((e >> 1) & 3) + 1] =
-                                    __fadd2_rn(a[((e >> 1) & 3) + 1], make_float2(fast_exp2(y1.x), fast_exp2(y1.y)));
-                            }
+                                for (int e = 0; e < 32; e += 4) {
+                                    const float4 c = KB == 0 ? make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e,
+                                                                           p.scale_log2e)
+                                                             : *reinterpret_cast<const float4*>(col + 32 * x + e);
+                                    float2 y0 = __ffma2_rn(make_float2(__uint_as_float(f[e]), __uint_as_float(f[e + 1])),
+                                                           make_float2(c.x, c.y), nb);
+                                    float2 y1 = __ffma2_rn(make_float2(__uint_as_float(f[e + 2]), __uint_as_float(f[e + 3])),
+                                                           make_float2(c.z, c.w), nb);
+                                    if constexpr (decltype(masked)::value) {
+                                        const int left = mine - (tok0 + 32 * x + e);
+                                        if (left < 0) y0.x = -INFINITY;
+                                        if (left < 1) y0.y = -INFINITY;
+                                        if (left < 2) y1.x = -INFINITY;
+                                        if (left < 3) y1.y = -INFINITY;
+                                    }
+                                    a[(e >> 1) & 3] = __fadd2_rn(a[(e >> 1) & 3], make_float2(fast_exp2(y0.x), fast_exp2(y0.y)));
+                                    a[((e >> 1) & 3) + 1] =
+                                        __fadd2_rn(a[((e >> 1) & 3) + 1], make_float2(fast_exp2(y1.x), fast_exp2(y1.y)));
+                                }
+                            };
+                            if (tok0 + 32 * x + 31 <= lo) add(std::false_type{});
+                            else add(std::true_type{});
                         }
                         const float2 t2 = __fadd2_rn(__fadd2_rn(a[0], a[1]), __fadd2_rn(a[2], a[3]));
                         const float sum = t2.x + t2.y;
-                        slow = __any_sync(0xffffffffu, !(sum < 1.2676506e30f));   // 2^100 (or NaN)
+                        slow = __any_sync(0xffffffffu, live && !(sum < 1.2676506e30f));   // 2^100 (or NaN)
                         if (!slow) l += sum;
                     }
                     if (slow) {
@@ -425,7 +439,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
                                 float y = __uint_as_float(v[e]) * (KB == 0 ? p.scale_log2e : col[x + e]);
-                                if (masked && k * kWtTile + x + e > mine) y = -INFINITY;
+                                if (tok0 + x + e > mine) y = -INFINITY;
                                 mx = fmaxf(mx, y);
                                 v[e] = __float_as_uint(y);
                             }
