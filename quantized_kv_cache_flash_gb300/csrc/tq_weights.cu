@@ -291,7 +291,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const int all_see = s.L - p.tq + wt_span(p, row0, row0 + nrows - 1).x;
                 const int seen = p.seen != nullptr ? p.seen[s.b] : s.L - p.tq;
                 const int here = min(128, nrows - 128 * wg);   // rows of this query tile (or below 1)
-                const int chunks = (here + 31) / 32;
                 float* const out = p.part_w != nullptr
                                        ? p.part_w + (static_cast<size_t>(s.b * p.hkv + s.h) * p.pairs + s.pair) * p.part_len
                                        : p.weights + static_cast<size_t>(s.b * p.hkv + s.h) * p.cap;
@@ -312,44 +311,49 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     const int t = k * kWtTile + r;
                     const float c = KB == 0 ? p.scale_log2e : s_col[128 * buf + r];
                     const uint32_t d = tmem + 256 * buf + 128 * wg + lane_off;
-                    // 32 rows at a time, the next ones in flight: all of the warp's tokens are seen
-                    // by them, none is, or each row says which
                     const int from = t - (s.L - p.tq);   // the first query position that sees the token
-                    const bool seen_by_all = k * kWtTile + kWtTile - 1 <= all_see;
                     const float2 cc = make_float2(c, c);
                     float2 a[4] = {};
-                    uint32_t v[2][32];
-                    if (chunks > 0) tmem_ld32_issue(d, v[0]);
+                    auto add = [&](const uint32_t* f, int x, auto masked) {   // rows x .. x + 31
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        if (x >= chunks) break;
-                        tmem_ld_wait(v[x & 1]);
-                        if (x + 1 < chunks) tmem_ld32_issue(d + 32 * (x + 1), v[(x + 1) & 1]);
-                        const uint32_t* f = v[x & 1];
-                        auto add = [&](auto masked) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 l = *reinterpret_cast<const float4*>(lse + 32 * x + e);
-                                const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(f[e]), __uint_as_float(f[e + 1])),
-                                                             cc, make_float2(l.x, l.y));
-                                const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(f[e + 2]), __uint_as_float(f[e + 3])),
-                                                             cc, make_float2(l.z, l.w));
-                                float2 z0 = make_float2(fast_exp2(y0.x), fast_exp2(y0.y));
-                                float2 z1 = make_float2(fast_exp2(y1.x), fast_exp2(y1.y));
-                                if constexpr (decltype(masked)::value) {
-                                    const int4 j = *reinterpret_cast<const int4*>(pos + 32 * x + e);
-                                    if (j.x < from) z0.x = 0.f;
-                                    if (j.y < from) z0.y = 0.f;
-                                    if (j.z < from) z1.x = 0.f;
-                                    if (j.w < from) z1.y = 0.f;
-                                }
-                                a[(e >> 1) & 3] = __fadd2_rn(a[(e >> 1) & 3], z0);
-                                a[((e >> 1) & 3) + 1] = __fadd2_rn(a[((e >> 1) & 3) + 1], z1);
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 l = *reinterpret_cast<const float4*>(lse + x + e);
+                            const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(f[e]), __uint_as_float(f[e + 1])), cc,
+                                                         make_float2(l.x, l.y));
+                            const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(f[e + 2]), __uint_as_float(f[e + 3])),
+                                                         cc, make_float2(l.z, l.w));
+                            float2 z0 = make_float2(fast_exp2(y0.x), fast_exp2(y0.y));
+                            float2 z1 = make_float2(fast_exp2(y1.x), fast_exp2(y1.y));
+                            if constexpr (decltype(masked)::value) {
+                                const int4 j = *reinterpret_cast<const int4*>(pos + x + e);
+                                if (j.x < from) z0.x = 0.f;
+                                if (j.y < from) z0.y = 0.f;
+                                if (j.z < from) z1.x = 0.f;
+                                if (j.w < from) z1.y = 0.f;
                             }
-                        };
-                        const int2 span = s_span[4 * wg + x];   // (padding rows: -2^31)
-                        if (seen_by_all ? span.x >= 0 : span.x >= from - lane + 31) add(std::false_type{});
-                        else if (span.y >= from - lane) add(std::true_type{});
+                            a[(e >> 1) & 3] = __fadd2_rn(a[(e >> 1) & 3], z0);
+                            a[((e >> 1) & 3) + 1] = __fadd2_rn(a[((e >> 1) & 3) + 1], z1);
+                        }
+                    };
+                    if (k * kWtTile + kWtTile - 1 <= all_see && here == 128) {
+                        uint32_t v[2][32];   // the next 32 rows in flight
+                        tmem_ld32_issue(d, v[0]);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            tmem_ld_wait(v[x & 1]);
+                            if (x < 3) tmem_ld32_issue(d + 32 * (x + 1), v[(x + 1) & 1]);
+                            add(v[x & 1], 32 * x, std::false_type{});
+                        }
+                    } else {   // all of the warp's tokens are seen by 32 rows, none is, or each row says which
+#pragma unroll 1
+                        for (int x = 0; x < here; x += 32) {
+                            const int2 span = s_span[4 * wg + x / 32];   // (padding rows: -2^31)
+                            if (span.y < from - lane) continue;
+                            uint32_t v[32];
+                            tmem_ld32(d + x, v);
+                            if (span.x >= 0 && span.x >= from - lane + 31) add(v, x, std::false_type{});
+                            else add(v, x, std::true_type{});
+                        }
                     }
                     const float2 t2 = __fadd2_rn(__fadd2_rn(a[0], a[1]), __fadd2_rn(a[2], a[3]));
                     const float w = t2.x + t2.y;
@@ -392,38 +396,45 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         const float base = m == -INFINITY ? 0.f : m;
                         const float2 nb = make_float2(-base, -base);
                         float2 a[4] = {};
-                        uint32_t v[2][32];   // 32 tokens at a time, the next ones in flight
-                        tmem_ld32_issue(d, v[0]);
+                        auto add = [&](const uint32_t* f, int x, auto masked) {   // tokens x .. x + 31 of the tile
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            if (x >= visible) break;
-                            tmem_ld_wait(v[x & 1]);
-                            if (x + 1 < visible) tmem_ld32_issue(d + 32 * (x + 1), v[(x + 1) & 1]);
-                            const uint32_t* f = v[x & 1];
-                            auto add = [&](auto masked) {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 4) {
-                                    const float4 c = KB == 0 ? make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e,
-                                                                           p.scale_log2e)
-                                                             : *reinterpret_cast<const float4*>(col + 32 * x + e);
-                                    float2 y0 = __ffma2_rn(make_float2(__uint_as_float(f[e]), __uint_as_float(f[e + 1])),
-                                                           make_float2(c.x, c.y), nb);
-                                    float2 y1 = __ffma2_rn(make_float2(__uint_as_float(f[e + 2]), __uint_as_float(f[e + 3])),
-                                                           make_float2(c.z, c.w), nb);
-                                    if constexpr (decltype(masked)::value) {
-                                        const int left = mine - (tok0 + 32 * x + e);
-                                        if (left < 0) y0.x = -INFINITY;
-                                        if (left < 1) y0.y = -INFINITY;
-                                        if (left < 2) y1.x = -INFINITY;
-                                        if (left < 3) y1.y = -INFINITY;
-                                    }
-                                    a[(e >> 1) & 3] = __fadd2_rn(a[(e >> 1) & 3], make_float2(fast_exp2(y0.x), fast_exp2(y0.y)));
-                                    a[((e >> 1) & 3) + 1] =
-                                        __fadd2_rn(a[((e >> 1) & 3) + 1], make_float2(fast_exp2(y1.x), fast_exp2(y1.y)));
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 c = KB == 0 ? make_float4(p.scale_log2e, p.scale_log2e, p.scale_log2e,
+                                                                       p.scale_log2e)
+                                                         : *reinterpret_cast<const float4*>(col + x + e);
+                                float2 y0 = __ffma2_rn(make_float2(__uint_as_float(f[e]), __uint_as_float(f[e + 1])),
+                                                       make_float2(c.x, c.y), nb);
+                                float2 y1 = __ffma2_rn(make_float2(__uint_as_float(f[e + 2]), __uint_as_float(f[e + 3])),
+                                                       make_float2(c.z, c.w), nb);
+                                if constexpr (decltype(masked)::value) {
+                                    const int left = mine - (tok0 + x + e);
+                                    if (left < 0) y0.x = -INFINITY;
+                                    if (left < 1) y0.y = -INFINITY;
+                                    if (left < 2) y1.x = -INFINITY;
+                                    if (left < 3) y1.y = -INFINITY;
                                 }
-                            };
-                            if (tok0 + 32 * x + 31 <= lo) add(std::false_type{});
-                            else add(std::true_type{});
+                                a[(e >> 1) & 3] = __fadd2_rn(a[(e >> 1) & 3], make_float2(fast_exp2(y0.x), fast_exp2(y0.y)));
+                                a[((e >> 1) & 3) + 1] =
+                                    __fadd2_rn(a[((e >> 1) & 3) + 1], make_float2(fast_exp2(y1.x), fast_exp2(y1.y)));
+                            }
+                        };
+                        if (tok0 + kWtTile - 1 <= lo) {
+                            uint32_t v[2][32];   // the next 32 tokens in flight
+                            tmem_ld32_issue(d, v[0]);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                tmem_ld_wait(v[x & 1]);
+                                if (x < 3) tmem_ld32_issue(d + 32 * (x + 1), v[(x + 1) & 1]);
+                                add(v[x & 1], 32 * x, std::false_type{});
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int x = 0; x < 32 * visible; x += 32) {
+                                uint32_t v[32];
+                                tmem_ld32(d + x, v);
+                                if (tok0 + x + 31 <= lo) add(v, x, std::false_type{});
+                                else add(v, x, std::true_type{});
+                            }
                         }
                         const float2 t2 = __fadd2_rn(__fadd2_rn(a[0], a[1]), __fadd2_rn(a[2], a[3]));
                         const float sum = t2.x + t2.y;
