@@ -17,7 +17,7 @@
 //
 // Roles of a CTA's warps (hand-overs through mbarriers, every wait bounded):
 //   0-3, 4-7  a query tile each: its rows' sums (stats), its part of the tokens' (sum)
-//   8-11      dequantise K (n) (quantized K)
+//   8-11      dequantise K (n) (quantized K); with a single query tile 4-7 take every second one
 //   12, 14    issue the MMAs of every second K tile: the thread that issues stands still while
 //             the tensor core works, and the other one's waits are over when it is done
 //   13        copies Q' and the records (fp16 K: the tiles)
@@ -42,16 +42,17 @@ struct WtCfg {
     static constexpr int kParts = (KB == 0) ? 1 : 2;
     static constexpr int kQOff = 0;
     static constexpr int kKOff = kParts * 65536;
-    static constexpr int kStgOff = kKOff + kSlots * 32768;      // records and norms [2]
+    static constexpr int kStages = (KB == 0) ? 0 : 3;           // records and norms
+    static constexpr int kStgOff = kKOff + kSlots * 32768;
     static constexpr int kStg = (KB == 0) ? 0 : kWtTile * kRbK + 256;
-    static constexpr int kColOff = kStgOff + 2 * kStg;          // fp32 n_k * scale * log2(e) [2][128]
+    static constexpr int kColOff = kStgOff + kStages * kStg;          // fp32 n_k * scale * log2(e) [2][128]
     static constexpr int kLseOff = kColOff + 1024;              // fp32 -log2(sum) of a row [256]
     static constexpr int kPosOff = kLseOff + 1024;              // query position of a row [256]
-    // records copied [2], records read [2], K stored [kSlots], K read [kSlots], S done
-    // [2], S read [2], Q' copied, Q' read, the issuing warps' turns [2]; the TMEM slot
     static constexpr int kHalfOff = kPosOff + 1024;             // fp32 the second query tile's sums [4][128]
     static constexpr int kSpanOff = kHalfOff + 2048;            // int2 least and largest position of 32 rows [8]
-    static constexpr int kGo = 10 + 2 * kSlots;                 // the other issuing warp's turn [2]
+    // S done [2], S read [2], Q' copied, Q' read, K stored [4], K read [4], records copied
+    // [kStages], records read [kStages], the other issuing warp's turn [2]; the TMEM slot
+    static constexpr int kGo = 14 + 2 * kStages;
     static constexpr int kBarOff = kSpanOff + 64;
     static constexpr int kSmem = kBarOff + (kGo + 2) * 8 + 8;
     static constexpr int kSmemAlloc = kSmem + 768;              // to a 1024-byte boundary from a 256-byte one
@@ -195,7 +196,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     tq_weights_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap qmap) {
     using C = WtCfg<KB>;
-    constexpr int NS = C::kSlots;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31;
@@ -205,19 +205,30 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     int* s_pos = reinterpret_cast<int*>(smem + C::kPosOff);
     float* s_half = reinterpret_cast<float*>(smem + C::kHalfOff);
     int2* s_span = reinterpret_cast<int2*>(smem + C::kSpanOff);
-    const uint32_t bar_stg = smem_u32(smem + C::kBarOff), bar_stgf = bar_stg + 16, bar_s = bar_stg + 32,
-                   bar_sf = bar_stg + 48, bar_q = bar_stg + 64, bar_qf = bar_stg + 72, bar_k = bar_stg + 80,
-                   bar_kf = bar_k + 8 * NS, bar_go = bar_stg + 8 * C::kGo;
+    const uint32_t bar_s = smem_u32(smem + C::kBarOff), bar_sf = bar_s + 16, bar_q = bar_s + 32, bar_qf = bar_s + 40,
+                   bar_k = bar_s + 48, bar_kf = bar_s + 80, bar_stg = bar_s + 112, bar_stgf = bar_stg + 8 * C::kStages,
+                   bar_go = bar_s + 8 * C::kGo;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (C::kGo + 2) * 8);
+    // one query tile (quantized K): warps 4-7 dequantise every second K tile instead
+    const bool single = KB != 0 && p.rows <= 128;
+    const uint32_t readers = single ? 128 : 256;   // threads that read S
+    // K tiles; with a single query tile two more in the second one's places of Q'
+    const int NS = KB == 0 || single ? 4 : 2, slot_bits = KB == 0 || single ? 2 : 1;
+    auto k_half = [&](int slot, int half) {   // dims 0-63 or 64-127 of a K tile
+        return KB != 0 && slot >= 2 ? C::kQOff + 16384 + (slot - 2) * 65536 + half * 32768
+                                    : C::kKOff + slot * 32768 + half * 16384;
+    };
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kStages; ++i) {
             mbar_init(bar_stg + 8 * i, 1);
             mbar_init(bar_stgf + 8 * i, 128);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar_s + 8 * i, 1);
-            mbar_init(bar_sf + 8 * i, 256);
+            mbar_init(bar_sf + 8 * i, readers);
             mbar_init(bar_go + 8 * i, 1);
         }
-        for (int i = 0; i < NS; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(bar_k + 8 * i, KB == 0 ? 1 : 128);
             mbar_init(bar_kf + 8 * i, 1);
         }
@@ -245,13 +256,19 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tslot;
 
+    int stage = 0;          // of the ring of records
+    uint32_t round = 0;
+    auto next_stage = [&] {
+        if (++stage == C::kStages) stage = 0, ++round;
+    };
+
     bool stalled = false;  // once set, waits return at once and no MMA or copy is issued
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (!stalled && !mbar_wait_bounded(bar, parity)) stalled = true;
     };
     int n = 0;             // K tiles so far, over the units
     WtSeg s;
-    if (warp < 8) {
+    if (warp < 4 || (warp < 8 && !single)) {
         const int wg = warp >> 2, r = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         while (run.next(p, s)) {
@@ -260,7 +277,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const int unit = (s.b * p.pairs + s.pair) * p.hkv + s.h;
             if constexpr (SUM) {
                 const int nrows = min(256, p.rows - row0);
-                named_bar_sync(1, 256);   // (the unit before is done with its values)
+                named_bar_sync(1, readers);   // (the unit before is done with its values)
                 // the row's partial sums joined (rows without any: hidden below)
                 {
                     const int P = static_cast<int>(gridDim.x), q = run.all / P, rest = run.all - q * P;
@@ -269,15 +286,22 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     const int c1 = static_cast<int>(((s.base + 0ull + s.nt) * P - 1) / all);
                     const float2* ml = p.part_ml + static_cast<size_t>(unit) * 256 + tid;
                     float M = -INFINITY, sum = 0.f;
-#pragma unroll 4
-                    for (int c = c0; c <= c1; ++c) {
-                        // (an empty run wrote nothing)
-                        if (q == 0 && c * rest / P == (c + 1) * rest / P) continue;
-                        const float2 x = __ldcg(ml + static_cast<size_t>(c) * 256);
-                        const float mn = fmaxf(M, x.x);
-                        sum = (M == -INFINITY ? sum : sum * fast_exp2(M - mn)) +
-                              (x.x == -INFINITY ? x.y : x.y * fast_exp2(x.x - mn));
-                        M = mn;
+                    for (int c = c0; c <= c1; c += 8) {   // (eight loads in flight)
+                        float2 x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            x[i] = make_float2(-INFINITY, 0.f);
+                            // (an empty run wrote nothing)
+                            if (c + i <= c1 && !(q == 0 && (c + i) * rest / P == (c + i + 1) * rest / P))
+                                x[i] = __ldcg(ml + static_cast<size_t>(c + i) * 256);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float mn = fmaxf(M, x[i].x);
+                            sum = (M == -INFINITY ? sum : sum * fast_exp2(M - mn)) +
+                                  (x[i].x == -INFINITY ? x[i].y : x[i].y * fast_exp2(x[i].x - mn));
+                            M = mn;
+                        }
                     }
                     s_lse[tid] = -(M + log2f(sum));
                     // (a row without any token is behind every token's first position)
@@ -286,7 +310,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     const int least = __reduce_min_sync(0xffffffffu, at), most = __reduce_max_sync(0xffffffffu, at);
                     if (lane == 0) s_span[tid >> 5] = make_int2(least, most);
                 }
-                named_bar_sync(1, 256);
+                named_bar_sync(1, readers);
                 // tokens that every row of the pair sees
                 const int all_see = s.L - p.tq + wt_span(p, row0, row0 + nrows - 1).x;
                 const int seen = p.seen != nullptr ? p.seen[s.b] : s.L - p.tq;
@@ -294,21 +318,24 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 float* const out = p.part_w != nullptr
                                        ? p.part_w + (static_cast<size_t>(s.b * p.hkv + s.h) * p.pairs + s.pair) * p.part_len
                                        : p.weights + static_cast<size_t>(s.b * p.hkv + s.h) * p.cap;
-                float before = 0.f;
+                float before = 0.f, old = 0.f;   // the tile before's sum and weight so far
                 auto put = [&](int m, int t, float w) {   // token t's sum, of tile number m
-                    named_bar_sync(2 + (m & 3), 256);
-                    w += s_half[128 * (m & 3) + r];
+                    if (!single) {
+                        named_bar_sync(2 + (m & 3), 256);
+                        w += s_half[128 * (m & 3) + r];
+                    }
                     if (t >= lim || stalled) return;
-                    if (p.part_w == nullptr && t < seen && p.decay != 0.f) w += p.decay * out[t];
-                    out[t] = w;
+                    out[t] = w + p.decay * old;
                 };
                 const float* lse = s_lse + 128 * wg;
                 const int* pos = s_pos + 128 * wg;
                 for (int k = s.k0; k < s.k1; ++k, ++n) {
-                    const int buf = n & 1;
+                    const int buf = n & 1, t = k * kWtTile + r;
+                    // (in flight while S is waited for)
+                    const bool more = wg == 0 && p.part_w == nullptr && t < min(seen, lim) && p.decay != 0.f;
+                    const float now = more ? out[t] : 0.f;
                     wait(bar_s + 8 * buf, (n >> 1) & 1);
                     tc_fence_after();
-                    const int t = k * kWtTile + r;
                     const float c = KB == 0 ? p.scale_log2e : s_col[128 * buf + r];
                     const uint32_t d = tmem + 256 * buf + 128 * wg + lane_off;
                     const int from = t - (s.L - p.tq);   // the first query position that sees the token
@@ -369,6 +396,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     } else {
                         if (k > s.k0) put(n - 1, t - kWtTile, before);
                         before = w;
+                        old = now;
                     }
                 }
                 if (wg == 0) put(n - 1, (s.k1 - 1) * kWtTile + r, before);
@@ -473,35 +501,37 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
     } else if (warp < 12) {
         if constexpr (KB != 0) {   // a token a thread
-            const int r = tid - 256;
+            const int r = tid & 127, other = warp < 8 ? 0 : 1;   // (single: the tiles of the other group)
             const Tables kt{p.ktab[0], p.ktab[1], p.ktab[2], p.ktab[3]};
             while (run.next(p, s)) {
                 const int lim = min(s.L, p.max_len);
-                for (int k = s.k0; k < s.k1; ++k, ++n) {
+                for (int k = s.k0; k < s.k1; ++k, ++n, next_stage()) {
                     const int buf = n & 1;
-                    const uint8_t* stg = smem + C::kStgOff + buf * C::kStg;
-                    uint8_t* sK = smem + C::kKOff + buf * 32768;
-                    wait(bar_stg + 8 * buf, (n >> 1) & 1);
-                    if (n >= 2) wait(bar_kf + 8 * buf, ((n >> 1) - 1) & 1);
+                    if (single && buf == other) continue;
+                    const uint8_t* stg = smem + C::kStgOff + stage * C::kStg;
+                    const int slot = n & (NS - 1);
+                    wait(bar_stg + 8 * stage, round & 1);
+                    if (n >= NS) wait(bar_kf + 8 * slot, ((n >> slot_bits) - 1) & 1);
                     // the quarters in an order that differs between lanes whose records
                     // start in the same banks
                     const int turn = KB == 4 ? r >> 1 : r >> 3;
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         const int side = (q + turn) & 3;
+                        uint8_t* sK = smem + k_half(slot, side >> 1);
                         uint32_t hh[16];
                         dequant_q32<KB>(stg + r * C::kRbK + side * (C::kRbK / 4), kt, hh);
 #pragma unroll
                         for (int m = 0; m < 4; ++m)
-                            *reinterpret_cast<uint4*>(sK + sw128_offset(r, 32 * side + 8 * m)) =
+                            *reinterpret_cast<uint4*>(sK + sw128_offset(r, 32 * (side & 1) + 8 * m)) =
                                 make_uint4(hh[4 * m], hh[4 * m + 1], hh[4 * m + 2], hh[4 * m + 3]);
                     }
                     const float nk = __half2float(reinterpret_cast<const __half*>(stg + kWtTile * C::kRbK)[r]);
-                    mbar_arrive(bar_stgf + 8 * buf);
+                    mbar_arrive(bar_stgf + 8 * stage);
                     if (n >= 2) wait(bar_sf + 8 * buf, ((n >> 1) - 1) & 1);   // the scales of n - 2 are read
                     s_col[128 * buf + r] = k * kWtTile + r < lim ? nk * p.scale_log2e : 0.f;
                     fence_proxy_async();
-                    mbar_arrive(bar_k + 8 * buf);
+                    mbar_arrive(bar_k + 8 * slot);
                 }
             }
         }
@@ -516,14 +546,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             for (int k = s.k0; k < s.k1; ++k, ++n) {
                 const int buf = n & 1, slot = n & (NS - 1);
                 if (buf != odd) continue;
-                wait(bar_k + 8 * slot, (n / NS) & 1);
+                wait(bar_k + 8 * slot, (n >> slot_bits) & 1);
                 if (n >= 2) wait(bar_sf + 8 * buf, ((n >> 1) - 1) & 1);
                 // in turns, so that tile n is done while n + 1 is worked on; the other warp's
                 // begins a little before the end of this one's
                 if (n > 0) wait(bar_go + 8 * odd, ((n - 1) >> 1) & 1);
                 if (stalled) break;
                 tc_fence_after();
-                const uint32_t kbase = smem_u32(smem + C::kKOff) + slot * 32768;
+                const uint32_t k0 = smem_u32(smem) + k_half(slot, 0), k1 = smem_u32(smem) + k_half(slot, 1);
                 const uint32_t qbase = smem_u32(smem + C::kQOff), d = tmem + 256 * buf;
                 // q_lo first: the sums are cut at every step, the less the smaller they are
                 if constexpr (SUM) {   // both query tiles at once
@@ -533,7 +563,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {
                             if (part == 0 && kk == 6) mbar_arrive(bar_go + 8 * (odd ^ 1));
-                            umma_f16(d, umma_desc_sw128(kbase + (kk >> 2) * 16384 + (kk & 3) * 32),
+                            umma_f16(d, umma_desc_sw128((kk < 4 ? k0 : k1) + (kk & 3) * 32),
                                      umma_desc_sw128(qbase + part * 65536 + (kk >> 2) * 32768 + (kk & 3) * 32), idesc,
                                      kk > 0 || part + 1 < C::kParts ? 1u : 0u);
                         }
@@ -547,7 +577,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                                 if (part == 0 && kk == 4 && t == tiles - 1) mbar_arrive(bar_go + 8 * (odd ^ 1));
                                 umma_f16(d + 128 * t,
                                          umma_desc_sw128(qbase + part * 65536 + (kk >> 2) * 32768 + t * 16384 + (kk & 3) * 32),
-                                         umma_desc_sw128(kbase + (kk >> 2) * 16384 + (kk & 3) * 32),
+                                         umma_desc_sw128((kk < 4 ? k0 : k1) + (kk & 3) * 32),
                                          umma_idesc_f16_f32(128, 128), kk > 0 || part + 1 < C::kParts ? 1u : 0u);
                             }
                 }
@@ -559,7 +589,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             umma_commit(bar_qf);
         }
         // after a time-out: the MMAs in flight end before tensor memory is freed
-        if (one && stalled && last >= 0) (void)mbar_wait_bounded(bar_kf + 8 * (last & (NS - 1)), (last / NS) & 1);
+        if (one && stalled && last >= 0) (void)mbar_wait_bounded(bar_kf + 8 * (last & (NS - 1)), (last >> slot_bits) & 1);
         __syncwarp();
     } else if (warp == 13) {
         const bool one = lane == 0;
@@ -594,24 +624,24 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const int tok0 = k * kWtTile;
                 if constexpr (KB == 0) {
                     const int slot = n & (NS - 1);
-                    if (n >= NS) wait(bar_kf + 8 * slot, (n / NS - 1) & 1);
+                    if (n >= NS) wait(bar_kf + 8 * slot, ((n >> slot_bits) - 1) & 1);
                     if (stalled) break;
                     mbar_arrive_expect_tx(bar_k + 8 * slot, 32768);
                     // (rows past the tensor's end are zero-filled; masked later)
                     for (int half = 0; half < 2; ++half)
                         for (int rb = 0; rb < 4; ++rb)
-                            tma_g2s_2d(smem_u32(smem + C::kKOff) + slot * 32768 + half * 16384 + rb * 4096, &kmap,
+                            tma_g2s_2d(smem_u32(smem) + k_half(slot, half) + rb * 4096, &kmap,
                                        half * 64, static_cast<int32_t>(row0 + tok0 + rb * 32), bar_k + 8 * slot);
                 } else {
-                    const int buf = n & 1;
-                    if (n >= 2) wait(bar_stgf + 8 * buf, ((n >> 1) - 1) & 1);
+                    if (round > 0) wait(bar_stgf + 8 * stage, (round - 1) & 1);
                     if (stalled) break;
                     const int nval = min(kWtTile, lim - tok0);
                     const uint32_t nb = static_cast<uint32_t>((nval + 7) & ~7) * 2;
-                    const uint32_t dst = smem_u32(smem + C::kStgOff) + buf * C::kStg;
-                    mbar_arrive_expect_tx(bar_stg + 8 * buf, nval * C::kRbK + nb);
-                    bulk_g2s(dst, p.k_codes + (row0 + tok0) * C::kRbK, nval * C::kRbK, bar_stg + 8 * buf);
-                    bulk_g2s(dst + kWtTile * C::kRbK, p.k_norm + row0 + tok0, nb, bar_stg + 8 * buf);
+                    const uint32_t dst = smem_u32(smem + C::kStgOff) + stage * C::kStg, bar = bar_stg + 8 * stage;
+                    mbar_arrive_expect_tx(bar, nval * C::kRbK + nb);
+                    bulk_g2s(dst, p.k_codes + (row0 + tok0) * C::kRbK, nval * C::kRbK, bar);
+                    bulk_g2s(dst + kWtTile * C::kRbK, p.k_norm + row0 + tok0, nb, bar);
+                    next_stage();
                 }
                 ++begun;
             }
@@ -620,7 +650,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         // (after a time-out: the copies in flight land before shared memory goes away)
         if (one && stalled) {
             if (q_open) (void)mbar_wait_bounded(bar_q, (seg - 1) & 1);
-            constexpr int ring = KB == 0 ? NS : 2;
+            constexpr int ring = KB == 0 ? 4 : C::kStages;
             for (int x = max(begun - ring, 0); x < begun; ++x)
                 (void)mbar_wait_bounded((KB == 0 ? bar_k : bar_stg) + 8 * (x % ring), (x / ring) & 1);
         }

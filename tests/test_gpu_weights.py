@@ -57,6 +57,9 @@ CASES = [
     ("turbo4", 8, 2, [2 * i for i in range(40)], 1, 16.0),
     ("turbo4", 8, 2, [300, 2], 5, 1.0),                     # 20 rows
     ("turbo3", 28, 4, [517, 33], 16, 1.0),                  # 112 rows
+    ("turbo4", 32, 4, [700, 0, 129, 1500], 16, 1.0),        # 128 rows
+    ("turbo3_asym", 28, 4, [400, 90], 18, 4.0),             # 126 rows
+    ("turbo3", 24, 8, [300, 1100], 43, 1.0),                # 129 rows
     ("turbo4_asym", 28, 4, [700, 0, 129], 33, 1.0),         # 231 rows
     ("turbo4", 32, 8, [900, 1, 260], 64, 1.0),              # 256 rows
     ("turbo3", 32, 8, [611], 65, 16.0),                     # just past them
