@@ -191,7 +191,9 @@ __global__ void __launch_bounds__(256) tq_weights_rows_kernel(const __grid_const
         make_uint2(pack_half2(v[0] - h0.x, v[1] - h0.y), pack_half2(v[2] - h1.x, v[3] - h1.y));
 }
 
-template <int KB, bool SUM>
+// SINGLE: one query tile in all (quantized K); its second group of warps dequantises every
+// second K tile instead, and two more K tiles lie in its part of Q'.
+template <int KB, bool SUM, bool SINGLE>
 __global__ void __launch_bounds__(kWtThreads, 1)
     tq_weights_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap qmap) {
@@ -209,11 +211,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                    bar_k = bar_s + 48, bar_kf = bar_s + 80, bar_stg = bar_s + 112, bar_stgf = bar_stg + 8 * C::kStages,
                    bar_go = bar_s + 8 * C::kGo;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (C::kGo + 2) * 8);
-    // one query tile (quantized K): warps 4-7 dequantise every second K tile instead
-    const bool single = KB != 0 && p.rows <= 128;
-    const uint32_t readers = single ? 128 : 256;   // threads that read S
-    // K tiles; with a single query tile two more in the second one's places of Q'
-    const int NS = KB == 0 || single ? 4 : 2, slot_bits = KB == 0 || single ? 2 : 1;
+    constexpr bool single = SINGLE;
+    constexpr int readers = single ? 128 : 256;   // threads that read S
+    constexpr int NS = KB == 0 || single ? 4 : 2, slot_bits = NS == 4 ? 2 : 1;   // K tiles
     auto k_half = [&](int slot, int half) {   // dims 0-63 or 64-127 of a K tile
         return KB != 0 && slot >= 2 ? C::kQOff + 16384 + (slot - 2) * 65536 + half * 32768
                                     : C::kKOff + slot * 32768 + half * 16384;
@@ -690,19 +690,19 @@ __global__ void __launch_bounds__(256) tq_weights_add_kernel(const __grid_consta
     *out = old + sum;
 }
 
-template <int KB>
+template <int KB, bool SINGLE>
 static int launch_t(const WeightsParams& p, const CUtensorMap* kmap, const CUtensorMap* qmap, cudaStream_t stream) {
     using C = WtCfg<KB>;
     static std::atomic<uint64_t> done0{0}, done1{0};
-    cudaError_t e = set_smem_attr_once(tq_weights_kernel<KB, false>, C::kSmemAlloc, done0);
-    if (e == cudaSuccess) e = set_smem_attr_once(tq_weights_kernel<KB, true>, C::kSmemAlloc, done1);
+    cudaError_t e = set_smem_attr_once(tq_weights_kernel<KB, false, SINGLE>, C::kSmemAlloc, done0);
+    if (e == cudaSuccess) e = set_smem_attr_once(tq_weights_kernel<KB, true, SINGLE>, C::kSmemAlloc, done1);
     if (e != cudaSuccess) return e;
     const unsigned units = static_cast<unsigned>(p.batch) * p.hkv;
     if (KB != 0) e = launch_pdl(tq_weights_rows_kernel, dim3(units * p.pairs * 32), dim3(256), 0, stream, p);
     if (e == cudaSuccess)
-        e = launch_pdl(tq_weights_kernel<KB, false>, dim3(p.ctas), dim3(kWtThreads), C::kSmemAlloc, stream, p, *kmap, *qmap);
+        e = launch_pdl(tq_weights_kernel<KB, false, SINGLE>, dim3(p.ctas), dim3(kWtThreads), C::kSmemAlloc, stream, p, *kmap, *qmap);
     if (e == cudaSuccess)
-        e = launch_pdl(tq_weights_kernel<KB, true>, dim3(p.ctas), dim3(kWtThreads), C::kSmemAlloc, stream, p, *kmap, *qmap);
+        e = launch_pdl(tq_weights_kernel<KB, true, SINGLE>, dim3(p.ctas), dim3(kWtThreads), C::kSmemAlloc, stream, p, *kmap, *qmap);
     if (e == cudaSuccess && p.part_w != nullptr)
         e = launch_pdl(tq_weights_add_kernel, dim3(units * (p.part_len / 32)), dim3(256), 0, stream, p);
     return e;
@@ -710,9 +710,10 @@ static int launch_t(const WeightsParams& p, const CUtensorMap* kmap, const CUten
 
 int launch_weights(int kbits, const WeightsParams& p, const CUtensorMap* kmap, const CUtensorMap* qmap,
                    cudaStream_t stream) {
-    if (kbits == 16) return launch_t<0>(p, kmap, qmap, stream);
-    if (kbits == 3) return launch_t<3>(p, kmap, qmap, stream);
-    if (kbits == 4) return launch_t<4>(p, kmap, qmap, stream);
+    const bool single = p.rows <= 128;
+    if (kbits == 16) return launch_t<0, false>(p, kmap, qmap, stream);
+    if (kbits == 3) return single ? launch_t<3, true>(p, kmap, qmap, stream) : launch_t<3, false>(p, kmap, qmap, stream);
+    if (kbits == 4) return single ? launch_t<4, true>(p, kmap, qmap, stream) : launch_t<4, false>(p, kmap, qmap, stream);
     return cudaErrorInvalidValue;
 }
 
