@@ -21,7 +21,7 @@
 //   12, 14    issue the MMAs of every second K tile: the thread that issues stands still while
 //             the tensor core works, and the other one's waits are over when it is done
 //   13        copies Q' and the records (fp16 K: the tiles)
-// Tensor memory: two buffers of 256 columns, S(n) of both query tiles.
+// Tensor memory: two buffers of 256 columns, S(n) of both query tiles; four of 128 with one.
 #include <algorithm>
 #include <type_traits>
 
@@ -45,14 +45,14 @@ struct WtCfg {
     static constexpr int kStages = (KB == 0) ? 0 : 3;           // records and norms
     static constexpr int kStgOff = kKOff + kSlots * 32768;
     static constexpr int kStg = (KB == 0) ? 0 : kWtTile * kRbK + 256;
-    static constexpr int kColOff = kStgOff + kStages * kStg;          // fp32 n_k * scale * log2(e) [2][128]
-    static constexpr int kLseOff = kColOff + 1024;              // fp32 -log2(sum) of a row [256]
+    static constexpr int kColOff = kStgOff + kStages * kStg;          // fp32 n_k * scale * log2(e) [4][128]
+    static constexpr int kLseOff = kColOff + 2048;              // fp32 -log2(sum) of a row [256]
     static constexpr int kPosOff = kLseOff + 1024;              // query position of a row [256]
     static constexpr int kHalfOff = kPosOff + 1024;             // fp32 the second query tile's sums [4][128]
     static constexpr int kSpanOff = kHalfOff + 2048;            // int2 least and largest position of 32 rows [8]
-    // S done [2], S read [2], Q' copied, Q' read, K stored [4], K read [4], records copied
+    // S done [4], S read [4], Q' copied, Q' read, K stored [4], K read [4], records copied
     // [kStages], records read [kStages], the other issuing warp's turn [2]; the TMEM slot
-    static constexpr int kGo = 14 + 2 * kStages;
+    static constexpr int kGo = 18 + 2 * kStages;
     static constexpr int kBarOff = kSpanOff + 64;
     static constexpr int kSmem = kBarOff + (kGo + 2) * 8 + 8;
     static constexpr int kSmemAlloc = kSmem + 768;              // to a 1024-byte boundary from a 256-byte one
@@ -207,13 +207,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     int* s_pos = reinterpret_cast<int*>(smem + C::kPosOff);
     float* s_half = reinterpret_cast<float*>(smem + C::kHalfOff);
     int2* s_span = reinterpret_cast<int2*>(smem + C::kSpanOff);
-    const uint32_t bar_s = smem_u32(smem + C::kBarOff), bar_sf = bar_s + 16, bar_q = bar_s + 32, bar_qf = bar_s + 40,
-                   bar_k = bar_s + 48, bar_kf = bar_s + 80, bar_stg = bar_s + 112, bar_stgf = bar_stg + 8 * C::kStages,
+    const uint32_t bar_s = smem_u32(smem + C::kBarOff), bar_sf = bar_s + 32, bar_q = bar_s + 64, bar_qf = bar_s + 72,
+                   bar_k = bar_s + 80, bar_kf = bar_s + 112, bar_stg = bar_s + 144, bar_stgf = bar_stg + 8 * C::kStages,
                    bar_go = bar_s + 8 * C::kGo;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (C::kGo + 2) * 8);
     constexpr bool single = SINGLE;
     constexpr int readers = single ? 128 : 256;   // threads that read S
     constexpr int NS = KB == 0 || single ? 4 : 2, slot_bits = NS == 4 ? 2 : 1;   // K tiles
+    constexpr int NB = single ? 4 : 2, buf_bits = single ? 2 : 1;   // buffers of S, 128 columns a query tile
     auto k_half = [&](int slot, int half) {   // dims 0-63 or 64-127 of a K tile
         return KB != 0 && slot >= 2 ? C::kQOff + 16384 + (slot - 2) * 65536 + half * 32768
                                     : C::kKOff + slot * 32768 + half * 16384;
@@ -223,11 +224,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             mbar_init(bar_stg + 8 * i, 1);
             mbar_init(bar_stgf + 8 * i, 128);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(bar_s + 8 * i, 1);
             mbar_init(bar_sf + 8 * i, readers);
-            mbar_init(bar_go + 8 * i, 1);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(bar_go + 8 * i, 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar_k + 8 * i, KB == 0 ? 1 : 128);
             mbar_init(bar_kf + 8 * i, 1);
@@ -330,14 +331,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const float* lse = s_lse + 128 * wg;
                 const int* pos = s_pos + 128 * wg;
                 for (int k = s.k0; k < s.k1; ++k, ++n) {
-                    const int buf = n & 1, t = k * kWtTile + r;
+                    const int buf = n & (NB - 1), t = k * kWtTile + r;
                     // (in flight while S is waited for)
                     const bool more = wg == 0 && p.part_w == nullptr && t < min(seen, lim) && p.decay != 0.f;
                     const float now = more ? out[t] : 0.f;
-                    wait(bar_s + 8 * buf, (n >> 1) & 1);
+                    wait(bar_s + 8 * buf, (n >> buf_bits) & 1);
                     tc_fence_after();
                     const float c = KB == 0 ? p.scale_log2e : s_col[128 * buf + r];
-                    const uint32_t d = tmem + 256 * buf + 128 * wg + lane_off;
+                    const uint32_t d = tmem + 512 / NB * buf + 128 * wg + lane_off;
                     const int from = t - (s.L - p.tq);   // the first query position that sees the token
                     const float2 cc = make_float2(c, c);
                     float2 a[4] = {};
@@ -412,10 +413,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 // scores may pass it, as long as the sums stay in range.
                 float m = -INFINITY, l = 0.f;
                 for (int k = s.k0; k < s.k1; ++k, ++n) {
-                    const int buf = n & 1;
-                    wait(bar_s + 8 * buf, (n >> 1) & 1);
+                    const int buf = n & (NB - 1);
+                    wait(bar_s + 8 * buf, (n >> buf_bits) & 1);
                     tc_fence_after();
-                    const uint32_t d = tmem + 256 * buf + 128 * wg + lane_off;
+                    const uint32_t d = tmem + 512 / NB * buf + 128 * wg + lane_off;
                     const float* col = s_col + 128 * buf;
                     const int tok0 = k * kWtTile;
                     const int visible = hi < tok0 ? 0 : min(4, (hi - tok0) / 32 + 1);   // pieces of 32 tokens
@@ -506,8 +507,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             while (run.next(p, s)) {
                 const int lim = min(s.L, p.max_len);
                 for (int k = s.k0; k < s.k1; ++k, ++n, next_stage()) {
-                    const int buf = n & 1;
-                    if (single && buf == other) continue;
+                    const int buf = n & (NB - 1);
+                    if (single && (n & 1) == other) continue;
                     const uint8_t* stg = smem + C::kStgOff + stage * C::kStg;
                     const int slot = n & (NS - 1);
                     wait(bar_stg + 8 * stage, round & 1);
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     }
                     const float nk = __half2float(reinterpret_cast<const __half*>(stg + kWtTile * C::kRbK)[r]);
                     mbar_arrive(bar_stgf + 8 * stage);
-                    if (n >= 2) wait(bar_sf + 8 * buf, ((n >> 1) - 1) & 1);   // the scales of n - 2 are read
+                    if (n >= NB) wait(bar_sf + 8 * buf, ((n >> buf_bits) - 1) & 1);   // the scales of n - NB are read
                     s_col[128 * buf + r] = k * kWtTile + r < lim ? nk * p.scale_log2e : 0.f;
                     fence_proxy_async();
                     mbar_arrive(bar_k + 8 * slot);
@@ -544,20 +545,20 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const int tiles = (p.pair0 + s.pair) * 256 + 128 < p.rows ? 2 : 1;   // query tiles with rows
             wait(bar_q, seg++ & 1);
             for (int k = s.k0; k < s.k1; ++k, ++n) {
-                const int buf = n & 1, slot = n & (NS - 1);
-                if (buf != odd) continue;
+                const int buf = n & (NB - 1), slot = n & (NS - 1);
+                if ((n & 1) != odd) continue;
                 wait(bar_k + 8 * slot, (n >> slot_bits) & 1);
-                if (n >= 2) wait(bar_sf + 8 * buf, ((n >> 1) - 1) & 1);
+                if (n >= NB) wait(bar_sf + 8 * buf, ((n >> buf_bits) - 1) & 1);
                 // in turns, so that tile n is done while n + 1 is worked on; the other warp's
                 // begins a little before the end of this one's
                 if (n > 0) wait(bar_go + 8 * odd, ((n - 1) >> 1) & 1);
                 if (stalled) break;
                 tc_fence_after();
                 const uint32_t k0 = smem_u32(smem) + k_half(slot, 0), k1 = smem_u32(smem) + k_half(slot, 1);
-                const uint32_t qbase = smem_u32(smem + C::kQOff), d = tmem + 256 * buf;
+                const uint32_t qbase = smem_u32(smem + C::kQOff), d = tmem + 512 / NB * buf;
                 // q_lo first: the sums are cut at every step, the less the smaller they are
                 if constexpr (SUM) {   // both query tiles at once
-                    const uint32_t idesc = umma_idesc_f16_f32(128, tiles == 2 ? 256 : 128);
+                    const uint32_t idesc = umma_idesc_f16_f32(128, single ? (p.rows + 15) / 16 * 16 : tiles == 2 ? 256 : 128);
 #pragma unroll
                     for (int part = C::kParts - 1; part >= 0; --part)
 #pragma unroll
