@@ -42,7 +42,10 @@ struct WtCfg {
     static constexpr int kParts = (KB == 0) ? 1 : 2;
     static constexpr int kQOff = 0;
     static constexpr int kKOff = kParts * 65536;
-    static constexpr int kStages = (KB == 0) ? 0 : 3;           // records and norms
+    // Records and norms.  With twice as many barriers as stages (an even number) each barrier
+    // belongs to one group of dequantising warps, which waits for all of its phases in order;
+    // a group that saw every second phase alone could take one for the one two later.
+    static constexpr int kStages = (KB == 0) ? 0 : 3, kStgBars = 2 * kStages;
     static constexpr int kStgOff = kKOff + kSlots * 32768;
     static constexpr int kStg = (KB == 0) ? 0 : kWtTile * kRbK + 256;
     static constexpr int kColOff = kStgOff + kStages * kStg;          // fp32 n_k * scale * log2(e) [4][128]
@@ -51,8 +54,8 @@ struct WtCfg {
     static constexpr int kHalfOff = kPosOff + 1024;             // fp32 the second query tile's sums [4][128]
     static constexpr int kSpanOff = kHalfOff + 2048;            // int2 least and largest position of 32 rows [8]
     // S done [4], S read [4], Q' copied, Q' read, K stored [4], K read [4], records copied
-    // [kStages], records read [kStages], the other issuing warp's turn [2]; the TMEM slot
-    static constexpr int kGo = 18 + 2 * kStages;
+    // [kStgBars], records read [kStgBars], the other issuing warp's turn [2]; the TMEM slot
+    static constexpr int kGo = 18 + 2 * kStgBars;
     static constexpr int kBarOff = kSpanOff + 64;
     static constexpr int kSmem = kBarOff + (kGo + 2) * 8 + 8;
     static constexpr int kSmemAlloc = kSmem + 768;              // to a 1024-byte boundary from a 256-byte one
@@ -208,7 +211,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     float* s_half = reinterpret_cast<float*>(smem + C::kHalfOff);
     int2* s_span = reinterpret_cast<int2*>(smem + C::kSpanOff);
     const uint32_t bar_s = smem_u32(smem + C::kBarOff), bar_sf = bar_s + 32, bar_q = bar_s + 64, bar_qf = bar_s + 72,
-                   bar_k = bar_s + 80, bar_kf = bar_s + 112, bar_stg = bar_s + 144, bar_stgf = bar_stg + 8 * C::kStages,
+                   bar_k = bar_s + 80, bar_kf = bar_s + 112, bar_stg = bar_s + 144, bar_stgf = bar_stg + 8 * C::kStgBars,
                    bar_go = bar_s + 8 * C::kGo;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (C::kGo + 2) * 8);
     constexpr bool single = SINGLE;
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                                     : C::kKOff + slot * 32768 + half * 16384;
     };
     if (tid == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
+        for (int i = 0; i < C::kStgBars; ++i) {
             mbar_init(bar_stg + 8 * i, 1);
             mbar_init(bar_stgf + 8 * i, 128);
         }
@@ -257,11 +260,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tslot;
 
-    int stage = 0;          // of the ring of records
+    int ring = 0;           // n % kStgBars, and n / kStgBars
     uint32_t round = 0;
     auto next_stage = [&] {
-        if (++stage == C::kStages) stage = 0, ++round;
+        if (++ring == C::kStgBars) ring = 0, ++round;
     };
+    auto stage_at = [&] { return C::kStgOff + (ring < C::kStages ? ring : ring - C::kStages) * C::kStg; };
 
     bool stalled = false;  // once set, waits return at once and no MMA or copy is issued
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -509,9 +513,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 for (int k = s.k0; k < s.k1; ++k, ++n, next_stage()) {
                     const int buf = n & (NB - 1);
                     if (single && (n & 1) == other) continue;
-                    const uint8_t* stg = smem + C::kStgOff + stage * C::kStg;
+                    const uint8_t* stg = smem + stage_at();
                     const int slot = n & (NS - 1);
-                    wait(bar_stg + 8 * stage, round & 1);
+                    wait(bar_stg + 8 * ring, round & 1);
                     if (n >= NS) wait(bar_kf + 8 * slot, ((n >> slot_bits) - 1) & 1);
                     // the quarters in an order that differs between lanes whose records
                     // start in the same banks
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                                 make_uint4(hh[4 * m], hh[4 * m + 1], hh[4 * m + 2], hh[4 * m + 3]);
                     }
                     const float nk = __half2float(reinterpret_cast<const __half*>(stg + kWtTile * C::kRbK)[r]);
-                    mbar_arrive(bar_stgf + 8 * stage);
+                    mbar_arrive(bar_stgf + 8 * ring);
                     if (n >= NB) wait(bar_sf + 8 * buf, ((n >> buf_bits) - 1) & 1);   // the scales of n - NB are read
                     s_col[128 * buf + r] = k * kWtTile + r < lim ? nk * p.scale_log2e : 0.f;
                     fence_proxy_async();
@@ -634,11 +638,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                             tma_g2s_2d(smem_u32(smem) + k_half(slot, half) + rb * 4096, &kmap,
                                        half * 64, static_cast<int32_t>(row0 + tok0 + rb * 32), bar_k + 8 * slot);
                 } else {
-                    if (round > 0) wait(bar_stgf + 8 * stage, (round - 1) & 1);
+                    // tile n - kStages, in the same stage, is read
+                    if (ring >= C::kStages) wait(bar_stgf + 8 * (ring - C::kStages), round & 1);
+                    else if (round > 0) wait(bar_stgf + 8 * (ring + C::kStages), (round - 1) & 1);
                     if (stalled) break;
                     const int nval = min(kWtTile, lim - tok0);
                     const uint32_t nb = static_cast<uint32_t>((nval + 7) & ~7) * 2;
-                    const uint32_t dst = smem_u32(smem + C::kStgOff) + stage * C::kStg, bar = bar_stg + 8 * stage;
+                    const uint32_t dst = smem_u32(smem) + stage_at(), bar = bar_stg + 8 * ring;
                     mbar_arrive_expect_tx(bar, nval * C::kRbK + nb);
                     bulk_g2s(dst, p.k_codes + (row0 + tok0) * C::kRbK, nval * C::kRbK, bar);
                     bulk_g2s(dst + kWtTile * C::kRbK, p.k_norm + row0 + tok0, nb, bar);
@@ -651,10 +657,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         // (after a time-out: the copies in flight land before shared memory goes away)
         if (one && stalled) {
             if (q_open) (void)mbar_wait_bounded(bar_q, (seg - 1) & 1);
-            constexpr int ring = KB == 0 ? 4 : C::kStages;
-            for (int x = max(begun - ring, 0); x < begun; ++x)
-                (void)mbar_wait_bounded((KB == 0 ? bar_k : bar_stg) + 8 * (x % ring), (x / ring) & 1);
+            constexpr int flight = KB == 0 ? NS : C::kStages, bars = KB == 0 ? NS : C::kStgBars;
+            for (int x = max(begun - flight, 0); x < begun; ++x)
+                (void)mbar_wait_bounded((KB == 0 ? bar_k : bar_stg) + 8 * (x % bars), (x / bars) & 1);
         }
+        // (the last commits have arrived before shared memory goes away)
+        if (one && !stalled) wait(bar_qf, (seg - 1) & 1);
         __syncwarp();
     }
     tc_fence_before();

@@ -285,3 +285,28 @@ def test_same_bits_again_on_other_streams_and_in_graphs(dev, T):
     w.zero_()
     g.replay()
     assert torch.equal(w, first) and tqf.tq_get_status(ctx) in (0, tqf.TQ_STATUS_SHORT_CONTEXT)
+
+
+@pytest.mark.parametrize("mode,Hq,T", [("turbo4", 32, 5), ("turbo4", 32, 32), ("turbo3", 32, 9), ("turbo4_asym", 32, 20),
+                                       ("turbo3", 32, 64)])
+def test_cold_caches(dev, mode, Hq, T):
+    """Copies that land late and out of order: the bits stay."""
+    B, Hkv, cap = 8, 8, 4000
+    cache = tqf.Cache(tqf.MODES[mode], B, Hkv, cap, dev)
+    if cache.k_norm is not None:
+        cache.k_data.random_(0, 256)
+        cache.k_norm.uniform_(0.5, 20.0)
+    else:
+        cache.k_data.normal_()
+    cache.lengths.fill_(cap)
+    q = H.upload(wl.random_fp16(81, (B, Hq, T, 128)), dev)
+    ctx, w = tqf.Context(), torch.zeros(B, Hkv, cap, device=dev)
+    tqf.tq_attention_weights(ctx, cache, q, w, cap, decay=0.0)
+    first = w.clone()
+    assert abs(first.double().sum().item() - B * Hq * T) < 1e-4 * B * Hq * T
+    other = torch.empty(300 << 20, dtype=torch.uint8, device=dev)
+    for i in range(40):
+        other.fill_(i)
+        tqf.tq_attention_weights(ctx, cache, q, w, cap, decay=0.0)
+        assert torch.equal(w, first)
+    assert tqf.tq_get_status(ctx) == 0
