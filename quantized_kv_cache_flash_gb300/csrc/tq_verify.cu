@@ -17,7 +17,7 @@
 // same however the row is split.  (Everything as 64-bit integers took 63 us for 8 trees
 // of 64 nodes over 131,072 tokens; a test in 64-bit floating point alone 1 us.)
 //
-// A cluster of 4 to 16 CTAs takes a sequence.  All of them walk the tree alike, on the
+// A cluster of 1 to 16 CTAs takes a sequence.  All of them walk the tree alike, on the
 // first tests' numbers, which are fetched together at the start; where a sum over
 // the vocabulary is needed each reads its part of the rows and sends its sum to all, with
 // the mbarrier that the first warp of each waits on.
@@ -465,9 +465,13 @@ static int launch_t(const VerifyParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> attr_done{0};
     const cudaError_t e = allow_large_clusters_once(tq_verify_kernel<DRAFT>, attr_done);
     if (e != cudaSuccess) return e;
-    // as many CTAs as fit at once, one per SM
+    // As many CTAs as fit at once, one per SM (a chain of 5 over 131,072 tokens: 16 CTAs 14.8
+    // us, 8 16.5, 4 20.8, 2 29.8, 1 47.5; over 32,000 13.4, 13.5, 14.4, 16.7, 21.0).  Of clusters
+    // of 16 seven run at once: more sequences take 8 where their registers hold the rows (8
+    // chains of 5 over 50,000: 15.2 us and 20.4; 8 stars of 16 over 131,072: 23.2 and 21.6).
     int ctas = kVerCtas;
     while (ctas > 1 && 1ll * p.batch * ctas > host::kSMs) ctas /= 2;
+    if (ctas == 16 && p.batch > 7 && p.vocab <= 8 * kVerThreads * 4 * kVerGroups) ctas = 8;
     return launch_pdl_cluster(tq_verify_kernel<DRAFT>, dim3(static_cast<unsigned>(p.batch) * ctas), dim3(kVerThreads),
                               ctas, 0, stream, p);
 }
