@@ -379,7 +379,8 @@ int tq_attention_weights(tq_ctx **ctx, const tq_cache *cache, const void *q, int
  * Records move bit for bit, in every mode.  A sequence with a count out of range (below 0,
  * above max_keep, or below sinks + recent where tokens are to go) is left untouched and
  * raises TQ_STATUS_BAD_INDEX; one longer than the hint, or whose kept tokens pass
- * dst's capacity, is left untouched and raises TQ_STATUS_CAPACITY.  num_keep must not
+ * dst's capacity, is left untouched and raises TQ_STATUS_CAPACITY.  The call uses the
+ * context's workspace like tq_decode_attention.  num_keep must not
  * lie in dst's lengths, which the call writes, nor kept or new_weights in a cache's
  * lengths: they are an invalid argument then.
  */
