@@ -13,6 +13,13 @@
 // Where a cluster of 16 CTAs per unit fits the GPU at once (few units), one kernel does
 // both: the scores stay in shared memory, and the CTAs of a cluster exchange their
 // (maximum, sum) pairs there.
+//
+// 32 sequences of 4,000 to 16,384 tokens, 32/8 heads, turbo4: 66 us, the scores 52 (K's 193 MB
+// would take 28; the issue of the dequantisation bounds it, as it does the decode kernel), the
+// sums 15 (scores and weights through L2).  One sequence of 8,177, 28/4 heads, turbo3: 6.7 us
+// (launch, one trip to memory, two cluster barriers); 5 with fp16 K: 17 (50 MB, 7.4).
+// Against the kernel for blocks of queries, which would read K twice: 64 units of 10,000
+// tokens with 4, 8, 16 rows 30, 36, 46 us and 93 there (turbo4; fp16 K 48, 50, 61 and 89).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -564,7 +571,9 @@ static int launch_t(StepParams p, const CUtensorMap* kmap, cudaStream_t stream) 
     e = launch_pdl(tq_step_scores_kernel<KB, ROWS, false>, dim3(p.ctas), dim3(128), C::kSmemAlloc, stream, p, *kmap);
     if (e != cudaSuccess) return e;
     // Few tokens: a token a thread, so that more SMs share them.  Many: up to 8 a thread,
-    // four loads in flight, for as many CTAs as are resident at once.
+    // four loads in flight, for as many CTAs as are resident at once.  (turbo3, 32 units of 4,000
+    // tokens 13.5 us and 14.4, 8 of 20,000 both 19.6, 16 of 10,000 19.6 and 18.6, 64 of 10,000 33.9
+    // and 29.8.)
     const long long units = 1ll * p.batch * p.hkv;
     constexpr int kMany = ROWS == 16 ? 1 : 4;
     if (units * ((p.max_len + 255) / 256) <= 4 * host::kSMs) {
