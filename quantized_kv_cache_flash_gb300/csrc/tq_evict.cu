@@ -228,13 +228,18 @@ __device__ __forceinline__ void evict_move(const EvictParams& p, int unit, int f
     uint4* vd = reinterpret_cast<uint4*>(p.v_dst) + rd * CV;
     // places ascend: where the last one is its own, all are, and records stay in place
     const bool moves = !INPLACE || (count > 0 && kept[count - 1] != count - 1);
-    // (in place every CTA of the cluster makes the same number of rounds)
+    // (in place every CTA of the cluster makes the same number of rounds; the places of the
+    // next one are fetched beside this one's records)
+    static_assert(R <= kMoveThreads, "a place a thread");
+    auto place = [&](int i) { return i < count && tid < R ? kept[i] : 0; };
+    int next = place(first * R + tid);
     for (int r0 = INPLACE ? 0 : first * R; r0 < count; r0 += step * R) {
         const int i0 = INPLACE ? r0 + first * R : r0;
         const int m = min(R, count - i0);   // (may be below 1)
         __syncthreads();
-        for (int i = tid; i < m; i += kMoveThreads) s_from[i] = kept[i0 + i];
+        if (tid < R) s_from[tid] = next;
         __syncthreads();
+        next = place(i0 + step * R + tid);
         uint4 k[NK], v[NV];
 #pragma unroll
         for (int e = 0; e < NK; ++e) {
