@@ -255,8 +255,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&qmap);
     }
-    griddep_wait();
-    griddep_launch_dependents();
+    // What each kernel reads of the ones before: stats Q' (quantized K), the sums part_ml; the warps
+    // that do so wait there, the others begin at once.  (The caller's data may be read before:
+    // the first kernel waited for what wrote them before any of its CTAs let the next grid
+    // launch, and so did stats for Q'.)
+    constexpr bool kWaitFirst = KB == 0 && !SUM;
+    if constexpr (kWaitFirst) {
+        griddep_wait();
+        griddep_launch_dependents();
+    }
     if (!SUM && p.pair0 == 0 && blockIdx.x == 0 && warp == 15) {   // rows that see no token
         bool none = false;
         for (int b = lane; b < p.batch; b += 32) none = none || p.lengths[b] < p.tq;
@@ -264,7 +271,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     }
     WtRun run;
     run.start(p, lane);
-    if (run.pos >= run.hi) return;   // (uniform over the CTA; nothing allocated yet)
+    if (run.pos >= run.hi) {   // (uniform over the CTA; nothing allocated yet)
+        if (!kWaitFirst) griddep_wait();
+        return;
+    }
     if (warp == 0) tmem_alloc(smem_u32(tslot), 512);
     tc_fence_before();
     __syncthreads();
@@ -287,6 +297,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     if (warp < 4 || (warp < 8 && !single)) {
         const int wg = warp >> 2, r = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        if constexpr (SUM) {
+            griddep_wait();
+            griddep_launch_dependents();
+        }
         while (run.next(p, s)) {
             const int lim = min(s.L, p.max_len);
             const int row0 = (p.pair0 + s.pair) * 256;            // the pair's first row
@@ -611,6 +625,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const bool one = lane == 0;
         int seg = 0, begun = 0;   // tiles whose copies were issued
         bool q_open = false;
+        if constexpr (!SUM && !kWaitFirst) {
+            griddep_wait();
+            griddep_launch_dependents();
+        }
         while (run.next(p, s)) {
             if (!one) continue;
             const int lim = min(s.L, p.max_len);
