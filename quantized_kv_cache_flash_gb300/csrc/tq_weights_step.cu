@@ -54,14 +54,15 @@ struct StepCfg {
     static constexpr int kQloOff = kQOff + 8 * NT * kQStride * 2;
     static constexpr int kBarOff = kQloOff + (kQlo ? 8 * NT * kQStride * 2 : 0);
     static constexpr int kScanOff = (kBarOff + kWarps * kStages * 8 + 15) / 16 * 16;
-    static constexpr int kMlOff = kScanOff + kWarps * 512;  // (m, l) of the warps' rows
+    static constexpr int kMlOff = kScanOff + 512;           // (m, l) of the warps' rows
     static constexpr int kSmem = kMlOff + kWarps * ROWS * 8;
-    static constexpr int kSmemAlloc = kSmem + 1024;
+    static constexpr int kPad = KB == 0 ? 1024 : 128;       // to a boundary of as much
+    static constexpr int kSmemAlloc = kSmem + kPad;
     // one-kernel form: the cluster's (m, l) pairs, the rows' log-sum-exp, the scores
     static constexpr int kPartOff = (kSmem + 15) / 16 * 16;
     static constexpr int kLseOff = kPartOff + kStepCluster * ROWS * 8;
     static constexpr int kScoreOff = kLseOff + ROWS * 4;
-    static constexpr int kOneAlloc(int tokens) { return kScoreOff + tokens * ROWS * 4 + 1024; }
+    static constexpr int kOneAlloc(int tokens) { return kScoreOff + tokens * ROWS * 4 + kPad; }
 
     __device__ static __forceinline__ int slot_row(int n, int e, int t) { return kPair ? t : 8 * n + 2 * t + e; }
 };
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(128, ONE ? 2 : StepCfg<KB, ROWS>::kMinCtas)
     using C = StepCfg<KB, ROWS>;
     constexpr int NT = C::NT, NE = C::NE;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & (C::kPad - 1u));
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -98,7 +99,9 @@ __global__ void __launch_bounds__(128, ONE ? 2 : StepCfg<KB, ROWS>::kMinCtas)
     BatchScan scan;
     int lo = 0, hi = 1;   // (ONE: a single share)
     if constexpr (!ONE) {
-        scan.init(reinterpret_cast<int*>(smem + C::kScanOff) + warp * 128, p.lengths, p.batch, p.hkv, p.max_len, lane);
+        scan.s = reinterpret_cast<int*>(smem + C::kScanOff);   // (the same for all warps)
+        if (warp == 0) scan.init(scan.s, p.lengths, p.batch, p.hkv, p.max_len, lane);
+        __syncthreads();
         const int all = __shfl_sync(0xffffffffu, scan.total(p.lengths, p.batch, p.hkv, p.max_len, lane), 0);
         const int P = static_cast<int>(gridDim.x), c_me = static_cast<int>(blockIdx.x);
         const int cq = all / P, cr = all - cq * P;
