@@ -15,9 +15,11 @@
 // before any stores.
 //
 // 32 sequences of 4,000 to 16,384 tokens brought to 2,048, 8 KV heads, turbo4, into another cache:
-// 50 us, the selection 16 (its three passes over keys in registers, two CTAs an SM) and the
-// move 29 (153 MB, 0.78 of the copy bandwidth in records of 64 bytes from places apart); 16
-// ragged sequences with fp16 K, in place: 37 us, 12 and 23.  A CTA per unit that does both:
+// 44 us, the selection 16 (its three passes over keys in registers, two CTAs an SM) and the
+// move 25 (90 MB read and 70 written, 0.94 of the copy bandwidth; with plain loads, for which
+// L2 fetches 128 bytes a record, 141 MB read and 30 us); 16
+// ragged sequences with fp16 K, in place: 36 us, 10.5 and 21.5 (23 before a round's places came
+// with the records before).  A CTA per unit that does both:
 // 49.1 us; digits of the distance from the least key, which are spread better: selection 18.8.
 #include <cooperative_groups.h>
 
@@ -211,6 +213,16 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 1) tq_evict_select_kernel(co
 constexpr int kMoveThreads = 256;
 constexpr int kMoveCtas = kEvictMoveCtas;
 
+// 16 bytes of a record; L2 fetches no more than the record's own 64 bytes for it.
+__device__ __forceinline__ uint4 load_piece(const uint4* at) {
+    uint4 v;
+    asm volatile("ld.global.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(at)
+                 : "memory");
+    return v;
+}
+
 // CK, CV: 16-byte pieces of a K and a V record.
 template <int CK, int CV, bool INPLACE>
 __device__ __forceinline__ void evict_move(const EvictParams& p, int unit, int first, int step) {
@@ -244,12 +256,12 @@ __device__ __forceinline__ void evict_move(const EvictParams& p, int unit, int f
 #pragma unroll
         for (int e = 0; e < NK; ++e) {
             const int x = tid + e * kMoveThreads, i = x / CK;
-            if (i < m && moves) k[e] = ks[static_cast<size_t>(s_from[i]) * CK + (x - i * CK)];
+            if (i < m && moves) k[e] = load_piece(ks + static_cast<size_t>(s_from[i]) * CK + (x - i * CK));
         }
 #pragma unroll
         for (int e = 0; e < NV; ++e) {
             const int x = tid + e * kMoveThreads, i = x / CV;
-            if (i < m && moves) v[e] = vs[static_cast<size_t>(s_from[i]) * CV + (x - i * CV)];
+            if (i < m && moves) v[e] = load_piece(vs + static_cast<size_t>(s_from[i]) * CV + (x - i * CV));
         }
         __half nk = __ushort_as_half(0), nv = __ushort_as_half(0);
         float w = 0.f;

@@ -22,7 +22,7 @@
 // the vocabulary is needed each reads its part of the rows and sends its sum to all, with
 // the mbarrier that the first warp of each waits on.
 //
-// 8 trees of 64 nodes over 131,072 tokens: 20 us, 64 looked-up chains of 11 over 50,001: 12,
+// 8 trees of 64 nodes over 131,072 tokens: 17 to 21 us, 64 looked-up chains of 11 over 50,001: 12,
 // one drafted chain of 6 over 32,000: 8.3.  What is read (8 MB, 13 MB, 0.3 MB) would take 1.2,
 // 1.9 and 0.04: the time is the chain of dependent steps, some 3 us a sum over a vocabulary (the
 // row from memory, 128 elements a warp in double fp32 numbers, the exchange).

@@ -23,15 +23,15 @@
 //   13        copies Q' and the records (fp16 K: the tiles)
 // Tensor memory: two buffers of 256 columns, S(n) of both query tiles; four of 128 with one.
 //
-// 8 sequences of 4,000 to 16,384 tokens, 64 queries, 32/8 heads, turbo4 (256 rows a unit): 141 us;
+// 8 sequences of 4,000 to 16,384 tokens, 64 queries, 32/8 heads, turbo4 (256 rows a unit): 139 us;
 // rows kernel 6.5, stats 68, sums 61.  The products with q_lo and both passes are 190 GFLOP,
 // 100 us at the measured rate; what bounds stats is shared memory (an MMA of 128 x 128 x 16
 // reads 8 KB, 87 cycles for 64 of the tensor core, beside 32 KB of K stored and its records read
 // a tile), what bounds the sums two exponentials a thread and column beside them.  Two prompts of
-// 2,047 tokens behind up to 511, 28/4 heads, fp16 K: 119 us; stats 59, sums 57, the pairs' sum 7: the
+// 2,047 tokens behind up to 511, 28/4 heads, fp16 K: 116 us; stats 59, sums 57, the pairs' sum 7: the
 // exponentials and the loads from tensor memory of two warps a scheduler.  The same 8 sequences of
-// 10,000 with 20 to 128 rows (one query tile): 76 to 81 us, 93 to 101 with both groups for S; 26
-// for one sequence of 8,000, of which 20 are launches and the first tile's way through the roles.
+// 10,000 with 20 to 128 rows (one query tile): 74 to 78 us, 91 to 100 with both groups for S; 24
+// for one sequence of 8,000, of which 18 are launches and the first tile's way through the roles.
 #include <algorithm>
 #include <type_traits>
 

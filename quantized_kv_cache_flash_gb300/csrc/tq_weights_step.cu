@@ -14,7 +14,7 @@
 // both: the scores stay in shared memory, and the CTAs of a cluster exchange their
 // (maximum, sum) pairs there.
 //
-// 32 sequences of 4,000 to 16,384 tokens, 32/8 heads, turbo4: 66 us, the scores 52 (K's 193 MB
+// 32 sequences of 4,000 to 16,384 tokens, 32/8 heads, turbo4: 65 us, the scores 52 (K's 193 MB
 // would take 28; the issue of the dequantisation bounds it, as it does the decode kernel), the
 // sums 15 (scores and weights through L2).  One sequence of 8,177, 28/4 heads, turbo3: 6.7 us
 // (launch, one trip to memory, two cluster barriers); 5 with fp16 K: 17 (50 MB, 7.4).
