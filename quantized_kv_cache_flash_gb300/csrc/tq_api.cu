@@ -1206,13 +1206,15 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
     }
     tq::WeightsParams p{};
     p.group = group;
-    // Pairs of query tiles in blocks whose workspace stays below kWeightsWork (64-bit
-    // rows * tokens otherwise); one pair needs no sums per pair.
+    // Pairs of query tiles in blocks whose workspace stays below kWeightsWork and whose passes
+    // take well below a second (2^26 tiles of some 1.5 us over all SMs: the second pass's
+    // bounded waits begin before the first one's last CTAs are done); one pair needs no sums
+    // per pair.
     const long long pairs = (rows + 255) / 256, tiles = (max_len_hint + 127) / 128;
     const size_t q_pair = kb == 16 ? 0 : 131072;   // (fp16 K: read from q)
     const size_t per_pair = size_t(units) * (q_pair + 256 * 8 + (pairs > 1 ? size_t(tiles) * 512 : 0));
     const long long block = std::max<long long>(
-        1, std::min<long long>(pairs, std::min<long long>(kWeightsWork / per_pair, (1ll << 30) / (units * tiles))));
+        1, std::min<long long>(pairs, std::min<long long>(kWeightsWork / per_pair, (1ll << 26) / (units * tiles))));
     const int ctas = int(std::min<long long>(tq::host::kSMs, units * block * tiles));
     if ((r = ensure_work(ctx, per_pair * block + size_t(ctas) * 2048, s)) != TQ_OK) return r;
     p.k_codes = static_cast<const uint8_t*>(c->k_data);
