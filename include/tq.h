@@ -347,8 +347,9 @@ int tq_cache_copy(tq_ctx **ctx, const tq_cache *dst, const tq_cache *src, const 
  *            NULL: all but the last tq (the block was appended for this call).
  *   num_q_heads, max_len_hint, scale: as in tq_prefill_attention, and so are the
  *            supported modes and codebooks and the group size.
- * Scores are those of the attention calls.  A row that sees no token adds nothing and
- * raises TQ_STATUS_SHORT_CONTEXT.  V is not read.  The sums run in fp32 in an order
+ * Scores are those of the attention calls.  A row that sees no token, or whose scores are
+ * all -inf, adds nothing and raises TQ_STATUS_SHORT_CONTEXT; one with a score of NaN or
+ * +inf is NaN on every token that it sees.  V is not read.  The sums run in fp32 in an order
  * that depends on the call's shape alone: the same call gives the same bits.  The
  * call uses the context's workspace like tq_decode_attention.
  */

@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if constexpr (SUM) {
                 const int nrows = min(256, p.rows - row0);
                 named_bar_sync(1, readers);   // (the unit before is done with its values)
-                // the row's partial sums joined (rows without any: hidden below)
+                // the row's partial sums joined
                 {
                     const int P = static_cast<int>(gridDim.x), q = run.all / P, rest = run.all - q * P;
                     const uint64_t all = run.all;
@@ -333,7 +333,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                             M = mn;
                         }
                     }
-                    s_lse[tid] = -(M + log2f(sum));
+                    float neg = -(M + log2f(sum));
+                    if (neg == INFINITY) {   // all its scores are -inf: it adds nothing, as one that sees no token
+                        neg = -INFINITY;
+                        if (tid < nrows) atomicOr(p.status, kStatusShortContext);
+                    }
+                    s_lse[tid] = neg;
                     // (a row without any token is behind every token's first position)
                     const int at = tid < nrows ? row0 + tid - over_tq(p, row0 + tid) * p.tq : -0x7fffffff - 1;
                     s_pos[tid] = at;

@@ -74,6 +74,17 @@ __device__ __forceinline__ void join(float& m, float& l, float mb, float lb) {
     m = mn;
 }
 
+// Rows whose normaliser is NaN are NaN on every token that they see (the first query's last
+// one: `last`), also where the score is -inf: NaN if there is one for this token, else 0.
+template <int ROWS>
+__device__ __noinline__ float nan_rows(const float* lse, int tok, int last, int group) {
+    float w = 0.f;
+#pragma unroll 1
+    for (int r = 0; r < ROWS; ++r)
+        if (lse[r] != lse[r] && tok <= last + r / group) w = lse[r];
+    return w;
+}
+
 // ONE: the one-kernel form.
 template <int KB, int ROWS, bool ONE>
 __global__ void __launch_bounds__(128, ONE ? 2 : StepCfg<KB, ROWS>::kMinCtas)
@@ -412,11 +423,15 @@ __global__ void __launch_bounds__(128, ONE ? 2 : StepCfg<KB, ROWS>::kMinCtas)
                     const float2 v = parts[c2 * ROWS + threadIdx.x];
                     join(am, al, v.x, v.y);
                 }
+                // (no token is seen, or all that are score -inf)
                 const bool none = am == -INFINITY && al == 0.f;
                 lse[threadIdx.x] = none || threadIdx.x >= p.rows ? INFINITY : am + log2f(al);
                 if (none && threadIdx.x < p.rows && cluster.block_rank() == 0) atomicOr(p.status, kStatusShortContext);
             }
             __syncthreads();
+            bool any_nan = false;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) any_nan = any_nan || lse[r] != lse[r];
             const int seen = p.seen != nullptr ? p.seen[b] : L - p.tq;
             float* w_out = p.weights + static_cast<size_t>(unit) * p.cap;
             for (int tok = t_begin + threadIdx.x; tok < t_end; tok += 128) {
@@ -425,12 +440,13 @@ __global__ void __launch_bounds__(128, ONE ? 2 : StepCfg<KB, ROWS>::kMinCtas)
 #pragma unroll
                 for (int r = 0; r < ROWS; r += 4) {
                     const float4 v = *reinterpret_cast<const float4*>(x + r), l4 = *reinterpret_cast<const float4*>(lse + r);
-                    // (-inf: hidden, also from a row of NaN; padding rows' lse is inf)
+                    // (-inf: hidden, or of no weight; padding rows' lse is inf)
                     w += r < p.rows && v.x != -INFINITY ? fast_exp2(v.x - l4.x) : 0.f;
                     w += r + 1 < p.rows && v.y != -INFINITY ? fast_exp2(v.y - l4.y) : 0.f;
                     w += r + 2 < p.rows && v.z != -INFINITY ? fast_exp2(v.z - l4.z) : 0.f;
                     w += r + 3 < p.rows && v.w != -INFINITY ? fast_exp2(v.w - l4.w) : 0.f;
                 }
+                if (any_nan) w += nan_rows<ROWS>(lse, tok, L - p.tq, p.group);
                 if (p.decay != 0.f && tok < seen) w = fmaf(p.decay, w_out[tok], w);
                 w_out[tok] = w;
             }
@@ -519,23 +535,35 @@ __global__ void __launch_bounds__(256) tq_step_sums_kernel(const __grid_constant
         float m = -INFINITY, l = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) join(m, l, s_part[i][tid].x, s_part[i][tid].y);
-        const bool none = m == -INFINITY && l == 0.f;
+        const bool none = m == -INFINITY && l == 0.f;   // (no token is seen, or all that are score -inf)
         s_lse[tid] = none || tid >= p.rows ? INFINITY : m + log2f(l);
         if (none && tid < p.rows && t0 == 0) atomicOr(p.status, kStatusShortContext);
     }
     __syncthreads();
     float lse[ROWS];
+    bool any_nan = false;
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) lse[r] = s_lse[r];
+    for (int r = 0; r < ROWS; ++r) {
+        lse[r] = s_lse[r];
+        any_nan = any_nan || lse[r] != lse[r];
+    }
     for (int t1 = t0; t1 < end; t1 += 256 * TOK) {
         float w[TOK];
 #pragma unroll
         for (int k = 0; k < TOK; ++k) {
             w[k] = 0.f;
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r)   // (-inf: hidden, also from a row of NaN)
+            for (int r = 0; r < ROWS; ++r)   // (-inf: hidden, or of no weight)
                 w[k] += r < p.rows && x[k][r] != -INFINITY ? fast_exp2(x[k][r] - lse[r]) : 0.f;
             if (fade) w[k] = fmaf(p.decay, old[k], w[k]);
+        }
+        if (any_nan) {
+#pragma unroll 1
+            for (int k = 0; k < TOK; ++k) {
+                const float x = nan_rows<ROWS>(s_lse, t1 + tid + 256 * k, L - p.tq, p.group);
+#pragma unroll
+                for (int i = 0; i < TOK; ++i) w[i] += i == k ? x : 0.f;
+            }
         }
         if (t1 + 256 * TOK < end) load(t1 + 256 * TOK);   // (in flight while these are stored)
 #pragma unroll
