@@ -351,7 +351,9 @@ int tq_cache_copy(tq_ctx **ctx, const tq_cache *dst, const tq_cache *src, const 
  * all -inf, adds nothing and raises TQ_STATUS_SHORT_CONTEXT; one with a score of NaN or
  * +inf is NaN on every token that it sees.  V is not read.  The sums run in fp32 in an order
  * that depends on the call's shape alone: the same call gives the same bits.  The
- * call uses the context's workspace like tq_decode_attention.
+ * call uses the context's workspace like tq_decode_attention: up to some 512 MiB, by its shape
+ * and max_len_hint (a call that would need more is taken in blocks; one KV head of one
+ * sequence takes what it needs).
  */
 int tq_attention_weights(tq_ctx **ctx, const tq_cache *cache, const void *q, int32_t num_q_heads,
                          int32_t tq, int32_t max_len_hint, float scale, float decay,

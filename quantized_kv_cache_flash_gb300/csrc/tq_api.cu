@@ -879,10 +879,124 @@ int tree_impl(tq_ctx** pctx, const tq_cache* c, const tq::host::DecodePlan& pl, 
         tq::launch_tree(pl.kb, pl.vb, p, pl.kb == 16 ? &ctx->kmap : &dummy, stream, e0, e1)));
 }
 
-// Workspace that a tq_attention_weights call keeps to: more queries are taken in blocks.
+// Workspace that a tq_attention_weights call keeps to: what needs more is taken in blocks, of
+// sequences or KV heads (whose sums are their own) and of queries (added up in their order).
+// One KV head of one sequence takes what it needs.
 constexpr size_t kWeightsWork = size_t(512) << 20;
 // Rows per KV head up to which its scores go through the workspace.
 constexpr int kWeightsStepRows = 16;
+
+struct WeightsCall {
+    int kb, group, tq, max_len;
+    float scale, decay;
+};
+
+int weights_step_group(const WeightsCall& w) {   // rows of a group of the decode step's
+    return std::max(tq::group_rows_for(w.group * w.tq, w.kb), w.kb == 16 ? 8 : 4);
+}
+// Workspace of a unit (and, for blocks of queries, a pair of query tiles): a decode step's scores
+// and the sums of a share; else Q' (fp16 K: read from q), the sums of a run, and with several
+// pairs the tokens' sums of each.
+size_t weights_work_per_unit(const WeightsCall& w) {
+    const long long rows = 1ll * w.group * w.tq;
+    if (rows <= kWeightsStepRows) {
+        const size_t gr = weights_step_group(w);
+        return size_t((w.max_len + 31) / 32) * 32 * gr * sizeof(float) + gr * sizeof(float2);
+    }
+    const size_t tiles = (w.max_len + 127) / 128;
+    return (w.kb == 16 ? 0 : 131072) + 256 * sizeof(float2) + (rows > 256 ? tiles * 512 : 0);
+}
+
+// The weights of a cache whose units fit the workspace (see weights_work_per_unit).
+int weights_block(tq_ctx* ctx, const WeightsCall& w, const tq_cache& c, const CUtensorMap* c_map, const __half* q,
+                  const int32_t* seen, float* weights, cudaStream_t s) {
+    const long long rows = 1ll * w.group * w.tq, units = 1ll * c.batch * c.num_kv_heads;
+    const size_t per_unit = weights_work_per_unit(w);
+    CUtensorMap dummy;
+    std::memset(&dummy, 0, sizeof(dummy));
+    const CUtensorMap* kmap = w.kb == 16 ? c_map : &dummy;
+    int r;
+    if (rows <= kWeightsStepRows) {
+        const int gr = weights_step_group(w);
+        const long long chunks = units * ((w.max_len + 31) / 32);
+        const size_t scores = size_t(chunks) * 32 * gr * sizeof(float);
+        tq::StepParams p{};
+        p.ctas = int(std::min<long long>(1ll * tq::host::kSMs * tq::weights_step_ctas_per_sm(w.kb, gr),
+                                         std::max<long long>(1, (chunks + 7) / 8)));
+        if ((r = ensure_work(ctx, per_unit * units + size_t(p.ctas) * gr * sizeof(float2), s)) != TQ_OK) return r;
+        p.k_codes = static_cast<const uint8_t*>(c.k_data);
+        p.k_norm = static_cast<const __half*>(c.k_norm);
+        p.lengths = c.lengths;
+        p.q = q;
+        p.seen = seen;
+        p.weights = weights;
+        p.scores = ctx->d_work;
+        p.part_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ctx->d_work) + scores);
+        p.status = ctx->d_words;
+        p.batch = c.batch;
+        p.hkv = c.num_kv_heads;
+        p.hq = w.group * c.num_kv_heads;
+        p.group = w.group;
+        p.tq = w.tq;
+        p.rows = int32_t(rows);
+        p.cap = c.capacity;
+        p.max_len = w.max_len;
+        p.score_len = (w.max_len + 31) / 32 * 32;
+        p.scale_log2e = w.scale * 1.4426950408889634f;
+        p.decay = w.decay;
+        if (w.kb != 16) std::memcpy(p.ktab, ctx->ktab.tab, sizeof(p.ktab));
+        std::memcpy(p.signs, ctx->signs, sizeof(p.signs));
+        return cuda_err(static_cast<cudaError_t>(tq::launch_weights_step(w.kb, gr, p, kmap, s)));
+    }
+    // Pairs of query tiles in blocks whose workspace stays below kWeightsWork and whose passes
+    // take well below a second (2^26 tiles of some 1.5 us over all SMs: the second pass's
+    // bounded waits begin before the first one's last CTAs are done); one pair needs no sums
+    // per pair.
+    tq::WeightsParams p{};
+    const long long pairs = (rows + 255) / 256, tiles = (w.max_len + 127) / 128;
+    const long long block = std::max<long long>(
+        1, std::min<long long>(pairs, std::min<long long>(kWeightsWork / (per_unit * units), (1ll << 26) / (units * tiles))));
+    const int ctas = int(std::min<long long>(tq::host::kSMs, units * block * tiles));
+    if ((r = ensure_work(ctx, per_unit * units * block + size_t(ctas) * 2048, s)) != TQ_OK) return r;
+    p.k_codes = static_cast<const uint8_t*>(c.k_data);
+    p.k_norm = static_cast<const __half*>(c.k_norm);
+    p.lengths = c.lengths;
+    p.q = q;
+    p.seen = seen;
+    p.weights = weights;
+    uint8_t* work = reinterpret_cast<uint8_t*>(ctx->d_work);
+    p.q_tiles = work;
+    work += w.kb == 16 ? 0 : size_t(units) * block * 131072;
+    p.part_ml = reinterpret_cast<float2*>(work);
+    work += (size_t(units) * block + ctas) * 2048;
+    p.part_w = pairs > 1 ? reinterpret_cast<float*>(work) : nullptr;
+    p.part_len = int32_t(tiles * 128);
+    p.status = ctx->d_words;
+    p.batch = c.batch;
+    p.hkv = c.num_kv_heads;
+    p.hq = w.group * c.num_kv_heads;
+    p.group = w.group;
+    p.tq = w.tq;
+    p.rows = int32_t(rows);
+    p.cap = c.capacity;
+    p.max_len = w.max_len;
+    p.ctas = ctas;
+    tq::div_magic(uint32_t(w.tq), &p.div_tq_m, &p.div_tq_s);
+    p.scale_log2e = w.scale * 1.4426950408889634f;
+    p.decay = w.decay;
+    if (w.kb != 16) std::memcpy(p.ktab, ctx->ktab.tab, sizeof(p.ktab));
+    std::memcpy(p.signs, ctx->signs, sizeof(p.signs));
+    CUtensorMap qmap;
+    if (w.kb == 16 && (r = tq::host::encode_rows_map(&qmap, q, uint64_t(units) * rows)) != TQ_OK) return r;
+    for (long long q0 = 0; q0 < pairs; q0 += block) {
+        p.pair0 = int32_t(q0);
+        p.pairs = int32_t(std::min(block, pairs - q0));
+        tq::div_magic(uint32_t(p.pairs), &p.div_pairs_m, &p.div_pairs_s);
+        const int e = tq::launch_weights(w.kb, p, kmap, w.kb == 16 ? &qmap : &dummy, s);
+        if (e != 0) return TQ_ERR_CUDA;
+    }
+    return TQ_OK;
+}
 
 // Arguments that both prefill calls take.
 int check_prefill(const tq_cache* c, const void* q, int32_t num_q_heads, int32_t max_len_hint, float scale,
@@ -1162,99 +1276,41 @@ int tq_attention_weights(tq_ctx** pctx, const tq_cache* c, const void* q, int32_
     tq_ctx* ctx;
     if ((r = get_ctx(pctx, &ctx)) != TQ_OK) return r;
     if ((r = prepare_tables(ctx, c, kb, vb)) != TQ_OK) return r;
-    if (kb == 16 && (r = prepare_kmap(ctx, c)) != TQ_OK) return r;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const float sc = (scale == 0.f) ? 1.0f / std::sqrt(float(kD)) : scale;
-    CUtensorMap dummy;
-    std::memset(&dummy, 0, sizeof(dummy));
-    const CUtensorMap* kmap = kb == 16 ? &ctx->kmap : &dummy;
     ctx->last_stream = s;
-    if (rows <= kWeightsStepRows) {
-        const int gr = std::max(tq::group_rows_for(int(rows), kb), kb == 16 ? 8 : 4);
-        const long long chunks = units * ((max_len_hint + 31) / 32);
-        const size_t scores = size_t(chunks) * 32 * gr * sizeof(float);
-        if (scores <= kWeightsWork) {
-            tq::StepParams p{};
-            p.ctas = int(std::min<long long>(1ll * tq::host::kSMs * tq::weights_step_ctas_per_sm(kb, gr),
-                                             std::max<long long>(1, (chunks + 7) / 8)));
-            const size_t part = size_t(p.ctas + units) * gr * sizeof(float2);
-            if ((r = ensure_work(ctx, scores + part, s)) != TQ_OK) return r;
-            p.k_codes = static_cast<const uint8_t*>(c->k_data);
-            p.k_norm = static_cast<const __half*>(c->k_norm);
-            p.lengths = c->lengths;
-            p.q = static_cast<const __half*>(q);
-            p.seen = seen;
-            p.weights = weights;
-            p.scores = ctx->d_work;
-            p.part_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ctx->d_work) + scores);
-            p.status = ctx->d_words;
-            p.batch = c->batch;
-            p.hkv = c->num_kv_heads;
-            p.hq = num_q_heads;
-            p.group = group;
-            p.tq = tq_rows;
-            p.rows = int32_t(rows);
-            p.cap = c->capacity;
-            p.max_len = max_len_hint;
-            p.score_len = (max_len_hint + 31) / 32 * 32;
-            p.scale_log2e = sc * 1.4426950408889634f;
-            p.decay = decay;
-            if (kb != 16) std::memcpy(p.ktab, ctx->ktab.tab, sizeof(p.ktab));
-            std::memcpy(p.signs, ctx->signs, sizeof(p.signs));
-            return cuda_err(static_cast<cudaError_t>(tq::launch_weights_step(kb, gr, p, kmap, s)));
+    WeightsCall w{};
+    w.kb = kb;
+    w.group = group;
+    w.tq = tq_rows;
+    w.max_len = max_len_hint;
+    w.scale = (scale == 0.f) ? 1.0f / std::sqrt(float(kD)) : scale;
+    w.decay = decay;
+    // Blocks of whole sequences, or of the KV heads of one, that keep to the workspace.
+    const long long fit = std::max<long long>(1, (long long)(kWeightsWork / weights_work_per_unit(w)));
+    if (units <= fit) {
+        if (kb == 16 && (r = prepare_kmap(ctx, c)) != TQ_OK) return r;
+        return weights_block(ctx, w, *c, &ctx->kmap, static_cast<const __half*>(q), seen, weights, s);
+    }
+    const bool whole = fit >= c->num_kv_heads;
+    const int of = whole ? c->batch : c->num_kv_heads, most = int(whole ? fit / c->num_kv_heads : fit);
+    const int blocks = (of + most - 1) / most, size = (of + blocks - 1) / blocks;   // of one size, but for the last
+    int32_t rbk, rbv;
+    record_bytes_of(c->mode, kb, vb, &rbk, &rbv);
+    for (int b = 0; b < c->batch; b += whole ? size : 1) {
+        for (int h = 0; h < c->num_kv_heads; h += whole ? c->num_kv_heads : size) {
+            const size_t unit = size_t(b) * c->num_kv_heads + h, row = unit * c->capacity;
+            tq_cache part = *c;
+            if (whole) part.batch = std::min(size, c->batch - b);
+            else part.batch = 1, part.num_kv_heads = std::min(size, c->num_kv_heads - h);
+            part.k_data = static_cast<uint8_t*>(c->k_data) + row * rbk;
+            if (kb != 16) part.k_norm = static_cast<__half*>(c->k_norm) + row;
+            part.lengths = c->lengths + b;
+            CUtensorMap kmap;
+            if (kb == 16 && (r = tq::host::encode_kmap(&kmap, &part)) != TQ_OK) return r;
+            r = weights_block(ctx, w, part, &kmap, static_cast<const __half*>(q) + unit * rows * kD,
+                              seen != nullptr ? seen + b : nullptr, weights + row, s);
+            if (r != TQ_OK) return r;
         }
-    }
-    tq::WeightsParams p{};
-    p.group = group;
-    // Pairs of query tiles in blocks whose workspace stays below kWeightsWork and whose passes
-    // take well below a second (2^26 tiles of some 1.5 us over all SMs: the second pass's
-    // bounded waits begin before the first one's last CTAs are done); one pair needs no sums
-    // per pair.
-    const long long pairs = (rows + 255) / 256, tiles = (max_len_hint + 127) / 128;
-    const size_t q_pair = kb == 16 ? 0 : 131072;   // (fp16 K: read from q)
-    const size_t per_pair = size_t(units) * (q_pair + 256 * 8 + (pairs > 1 ? size_t(tiles) * 512 : 0));
-    const long long block = std::max<long long>(
-        1, std::min<long long>(pairs, std::min<long long>(kWeightsWork / per_pair, (1ll << 26) / (units * tiles))));
-    const int ctas = int(std::min<long long>(tq::host::kSMs, units * block * tiles));
-    if ((r = ensure_work(ctx, per_pair * block + size_t(ctas) * 2048, s)) != TQ_OK) return r;
-    p.k_codes = static_cast<const uint8_t*>(c->k_data);
-    p.k_norm = static_cast<const __half*>(c->k_norm);
-    p.lengths = c->lengths;
-    p.q = static_cast<const __half*>(q);
-    p.seen = seen;
-    p.weights = weights;
-    uint8_t* work = reinterpret_cast<uint8_t*>(ctx->d_work);
-    p.q_tiles = work;
-    work += size_t(units) * block * q_pair;
-    p.part_ml = reinterpret_cast<float2*>(work);
-    work += (size_t(units) * block + ctas) * 2048;
-    p.part_w = pairs > 1 ? reinterpret_cast<float*>(work) : nullptr;
-    p.part_len = int32_t(tiles * 128);
-    p.status = ctx->d_words;
-    p.batch = c->batch;
-    p.hkv = c->num_kv_heads;
-    p.hq = num_q_heads;
-    p.tq = tq_rows;
-    p.rows = int32_t(rows);
-    p.cap = c->capacity;
-    p.max_len = max_len_hint;
-    p.ctas = ctas;
-    tq::div_magic(uint32_t(tq_rows), &p.div_tq_m, &p.div_tq_s);
-    p.scale_log2e = sc * 1.4426950408889634f;
-    p.decay = decay;
-    if (kb != 16) std::memcpy(p.ktab, ctx->ktab.tab, sizeof(p.ktab));
-    std::memcpy(p.signs, ctx->signs, sizeof(p.signs));
-    CUtensorMap qmap;
-    if (kb == 16) {
-        r = tq::host::encode_rows_map(&qmap, q, uint64_t(c->batch) * num_q_heads * tq_rows);
-        if (r != TQ_OK) return r;
-    }
-    for (long long q0 = 0; q0 < pairs; q0 += block) {
-        p.pair0 = int32_t(q0);
-        p.pairs = int32_t(std::min(block, pairs - q0));
-        tq::div_magic(uint32_t(p.pairs), &p.div_pairs_m, &p.div_pairs_s);
-        const int e = tq::launch_weights(kb, p, kmap, kb == 16 ? &qmap : &dummy, s);
-        if (e != 0) return TQ_ERR_CUDA;
     }
     return TQ_OK;
 }
