@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 1) tq_evict_select_kernel(co
         return;
     }
     const int lo = p.sinks, hi = L - p.recent;   // tokens [lo, hi) go by their weights
+    // (plain loads: a kernel before this one may have written the weights after this one began)
     const float* w = p.weights + static_cast<size_t>(blockIdx.x) * p.src_cap;
     auto key_of = [&](int t, float v) { return t >= L ? 0u : t < lo || t >= hi ? kKeyHeld : weight_key(v); };
     const int groups = (L + 31) / 32, per = KPT > 0 ? KPT : (groups + W - 1) / W;
@@ -95,14 +96,14 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 1) tq_evict_select_kernel(co
 #pragma unroll
         for (int i = 0; i < KPT; ++i) {
             const int t = 32 * (g0 + i) + lane;
-            v[i] = t >= lo && t < hi ? __ldg(w + t) : 0.f;
+            v[i] = t >= lo && t < hi ? w[t] : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < KPT; ++i) key[i] = key_of(32 * (g0 + i) + lane, v[i]);
     }
     auto key_at = [&](int g) {
         const int t = 32 * g + lane;
-        return key_of(t, t >= lo && t < hi ? __ldg(w + t) : 0.f);
+        return key_of(t, t >= lo && t < hi ? w[t] : 0.f);
     };
     // digits so far; how many of the keys with them are kept
     uint32_t prefix = 0, need = static_cast<uint32_t>(n);
