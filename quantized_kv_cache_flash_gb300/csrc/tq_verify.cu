@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(kVerThreads, 1)
         all = whole();
     }
     if (__syncthreads_or(stalled) && tid == 0) atomicOr(p.status, kStatusPipelineStall);
+    __syncwarp();   // (the barrier is met by whole warps)
     // (met at the end: no CTA leaves while another may still send to it)
     cluster_arrive();
     if (all == 0) {

@@ -409,8 +409,8 @@ __global__ void __launch_bounds__(128, ONE ? 2 : StepCfg<KB, ROWS>::kMinCtas)
             cg::cluster_group cluster = cg::this_cluster();
             float2* parts = reinterpret_cast<float2*>(smem + C::kPartOff);
             float* lse = reinterpret_cast<float*>(smem + C::kLseOff);
+            __syncthreads();   // (sML; and the warps are whole again)
             cluster_wait();
-            __syncthreads();
             for (int i = threadIdx.x; i < kStepCluster * ROWS; i += 128) {
                 const int r = i % ROWS;
                 *cluster.map_shared_rank(parts + cluster.block_rank() * ROWS + r, i / ROWS) = sML[r];
