@@ -418,14 +418,15 @@ int tq_cache_evict(tq_ctx **ctx, const tq_cache *dst, const tq_cache *src, const
  *             are tq_cache_compact's arguments (max_keep = num_nodes).
  *   num_keep: int32 [batch] device pointer: 1 .. num_nodes.
  *   next_token: int32 [batch] device pointer.
- * Sums and differences carry 48 bits or more, in an order of their own: the same call
- * gives the same tokens.  What is not above 0 (NaN) counts as 0, what is above 1 as 1; a row
- * whose sum passes 2^5 gives an unspecified next token (of the vocabulary).  A tried
- * node with a parent or a token out of range counts as a padding node and raises
- * TQ_STATUS_BAD_INDEX; a target's row without positive entries at the path's end gives
- * token 0 and raises TQ_STATUS_BAD_VALUE.  num_nodes <= TQ_MAX_TREE_NODES, vocab <=
- * 2^30, ld_target and ld_draft >= vocab; target and draft are 4-byte aligned (rows on
- * 16-byte boundaries are read fastest).  The outputs must not overlap the inputs.
+ * Differences carry 48 bits; a row's sum is within 2^-36 (to vocabularies of 2^20), in an
+ * order of its own: the same call gives the same tokens.  What is not above 0 (NaN) counts
+ * as 0, what is above 1 as 1; a row whose sum passes 2^5 gives an unspecified next token (of
+ * the vocabulary).  A node with a parent or a token out of range counts as a padding node
+ * and raises TQ_STATUS_BAD_INDEX; a target's row without positive entries at the path's end
+ * (or whose entries add up to less than 2^-36) gives token 0 and raises
+ * TQ_STATUS_BAD_VALUE.  num_nodes <= TQ_MAX_TREE_NODES, vocab <= 2^30, ld_target and
+ * ld_draft >= vocab; target and draft are 4-byte aligned (rows on 16-byte boundaries are
+ * read fastest).  The outputs must not overlap the inputs.
  */
 int tq_verify_tree(tq_ctx **ctx, const int32_t *tokens, const int32_t *parents, int32_t parents_batch,
                    const float *target, int64_t ld_target, const float *draft, int64_t ld_draft,
