@@ -101,9 +101,18 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 1) tq_evict_select_kernel(co
 #pragma unroll
         for (int i = 0; i < KPT; ++i) key[i] = key_of(32 * (g0 + i) + lane, v[i]);
     }
-    auto key_at = [&](int g) {
-        const int t = 32 * g + lane;
-        return key_of(t, t >= lo && t < hi ? w[t] : 0.f);
+    // KPT = 0: the run's groups in order, the next one's weights in flight
+    auto each = [&](auto f) {
+        auto at = [&](int g) {
+            const int t = 32 * g + lane;
+            return t >= lo && t < hi ? w[t] : 0.f;
+        };
+        float next = at(g0);
+        for (int g = g0; g < g1; ++g) {
+            const uint32_t k = key_of(32 * g + lane, next);
+            next = at(g + 1);
+            f(g, k);
+        }
     };
     // digits so far; how many of the keys with them are kept
     uint32_t prefix = 0, need = static_cast<uint32_t>(n);
@@ -121,7 +130,7 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 1) tq_evict_select_kernel(co
             for (int i = 0; i < KPT; ++i)
                 if (pass > 0 || g0 + i < g1) add(key[i]);
         } else {
-            for (int g = g0; g < g1; ++g) add(key_at(g));
+            each([&](int, uint32_t k) { add(k); });
         }
         __syncthreads();
         // the bin whose keys, with those of the bins above it, first make `need`:
@@ -167,11 +176,10 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 1) tq_evict_select_kernel(co
         n_above = __popc(above);
         n_same = __popc(same);
     } else {
-        for (int g = g0; g < g1; ++g) {
-            const uint32_t k = key_at(g);
+        each([&](int, uint32_t k) {
             n_above += k > prefix;
             n_same += k == prefix;
-        }
+        });
     }
     const uint32_t all_above = __reduce_add_sync(0xffffffffu, n_above), all_same = __reduce_add_sync(0xffffffffu, n_same);
     if (lane == 0) {
@@ -199,15 +207,14 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 1) tq_evict_select_kernel(co
             if ((mask >> lane) & 1u) kept[base + __popc(mask & below)] = 32 * (g0 + i) + lane;
         }
     } else {
-        for (int g = g0; g < g1; ++g) {
-            const uint32_t k = key_at(g);
+        each([&](int g, uint32_t k) {
             const uint32_t same_mask = __ballot_sync(0xffffffffu, k == prefix);
             const bool keep = k > prefix || (k == prefix && equal + __popc(same_mask & below) < need);
             const uint32_t mask = __ballot_sync(0xffffffffu, keep);
             if (keep) kept[at + __popc(mask & below)] = 32 * g + lane;
             at += __popc(mask);
             equal += __popc(same_mask);
-        }
+        });
     }
 }
 
