@@ -15,12 +15,12 @@
 // before any stores.
 //
 // 32 sequences of 4,000 to 16,384 tokens brought to 2,048, 8 KV heads, turbo4, into another cache:
-// 44 us, the selection 16 (its three passes over keys in registers, two CTAs an SM) and the
+// 45 us, the selection 16 (its three passes over keys in registers, two CTAs an SM) and the
 // move 25 (90 MB read and 70 written, 0.94 of the copy bandwidth; with plain loads, for which
-// L2 fetches 128 bytes a record, 141 MB read and 30 us); 16
-// ragged sequences with fp16 K, in place: 36 us, 10.5 and 21.5 (23 before a round's places came
-// with the records before).  A CTA per unit that does both:
-// 49.1 us; digits of the distance from the least key, which are spread better: selection 18.8.
+// L2 fetches 128 bytes a record, 141 MB read and 30 us, 50 in all: a CTA per unit that did
+// both took 49.1 then, and was not measured with the loads of today); 16 ragged sequences with
+// fp16 K, in place: 36 us, 10.5 and 21.5 (23 before a round's places came with the records
+// before).  Digits of the distance from the least key, which are spread better: selection 18.8.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -333,10 +333,9 @@ static int launch_move(EvictParams& p, cudaStream_t stream) {
 int launch_evict(EvictParams p, cudaStream_t stream) {
     // The smallest variant that holds the keys of the longest sequence in registers; 1024
     // threads where every unit has an SM of its own.  (The whole call in us, a quarter of the
-    // tokens kept, 3 bits: 4 units of 8,000 tokens, 8 keys a thread of 1024: 14.5, 16 of 512:
-    // 15.5, 32 of 1024: 22.7, read anew: 22.6; 256 units of 8,000: 48.2, 46.2, 62.6, 54.4; 256 of
-    // 16,000, 16 of 1024: 81.0, 32 of 512: 79.0, read anew: 95.4; 4 of 32,000, 32 of 1024: 25.7,
-    // read anew: 50.3.)
+    // tokens kept, 3 bits: 4 units of 8,000 tokens, 8 keys a thread of 1024 and 16 of 512: both
+    // 15.5, read anew: 19.6; 256 units of 8,000: 44.2, 41.2, 52.4; 256 of 16,000, 16 of 1024:
+    // 72.8, 32 of 512: 68.8, read anew: 87.2; 4 of 32,000, 32 of 1024: 24 to 26, read anew: 38.0.)
     const unsigned units = static_cast<unsigned>(p.batch) * p.hkv;
     const bool wide = units <= host::kSMs;
     auto select = [&](auto kernel, int threads) { return launch_pdl(kernel, dim3(units), dim3(threads), 0, stream, p); };

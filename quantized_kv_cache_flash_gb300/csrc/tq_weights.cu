@@ -27,11 +27,13 @@
 // rows kernel 6.5, stats 68, sums 61.  The products with q_lo and both passes are 190 GFLOP,
 // 100 us at the measured rate; what bounds stats is shared memory (an MMA of 128 x 128 x 16
 // reads 8 KB, 87 cycles for 64 of the tensor core, beside 32 KB of K stored and its records read
-// a tile), what bounds the sums two exponentials a thread and column beside them.  Two prompts of
-// 2,047 tokens behind up to 511, 28/4 heads, fp16 K: 116 us; stats 59, sums 57, the pairs' sum 7: the
-// exponentials and the loads from tensor memory of two warps a scheduler.  The same 8 sequences of
-// 10,000 with 20 to 128 rows (one query tile): 74 to 78 us, 91 to 100 with both groups for S; 24
-// for one sequence of 8,000, of which 18 are launches and the first tile's way through the roles.
+// a tile), what bounds the sums two exponentials a thread and column beside them.  With fp16 K the
+// window takes 95 us (K's 167 MB twice).  Two prompts of 2,047 tokens behind up to 511, 28/4 heads,
+// fp16 K: 116 us; stats 59, sums 57, the pairs' sum 7, with tensor core 0.41, exponentials 0.38 and
+// issue 0.44 active: none is full, each of the roles waits for another; turbo4: 184 us.  8
+// sequences of 10,000, 8 KV heads, with 20 to 128 rows (one query tile): 74 to 79 us, 91 to 100 with
+// both groups for S; 24 for one sequence of 8,000, of which 18 are launches and the first tile's way
+// through the roles.
 #include <algorithm>
 #include <type_traits>
 

@@ -14,12 +14,14 @@
 // both: the scores stay in shared memory, and the CTAs of a cluster exchange their
 // (maximum, sum) pairs there.
 //
-// 32 sequences of 4,000 to 16,384 tokens, 32/8 heads, turbo4: 65 us, the scores 52 (K's 193 MB
-// would take 28; the issue of the dequantisation bounds it, as it does the decode kernel), the
-// sums 15 (scores and weights through L2).  One sequence of 8,177, 28/4 heads, turbo3: 6.7 us
-// (launch, one trip to memory, two cluster barriers); 5 with fp16 K: 17 (50 MB, 7.4).
-// Against the kernel for blocks of queries, which would read K twice: 64 units of 10,000
-// tokens with 4, 8, 16 rows 30, 36, 46 us and 93 there (turbo4; fp16 K 48, 50, 61 and 89).
+// 32 sequences of 4,000 to 16,384 tokens, 32/8 heads, turbo4: 66 us, the scores 52 (K's 193 MB
+// would take 28), the sums 15 (scores and weights through L2).  Nothing is full in the scores
+// kernel: issue 0.57, the integer pipe 0.58, DRAM 0.47; its warps wait for the integer pipe
+// (1.5 cycles an instruction), for their turn (1.7) and for results (1.0) more than for memory
+// (0.7).  One sequence of 8,177, 28/4 heads, turbo3: 7.6 us in a graph (launch, one trip to
+// memory, two cluster barriers); 5 with fp16 K: 18 (50 MB, 7.4).
+// 64 units of 10,000 tokens with 4, 8, 16 rows: 30, 36, 45 us (turbo4; fp16 K 49, 50, 61); the kernel
+// for blocks of queries, which reads K twice, takes 75 with 20 rows (fp16 K 73).
 #include <cooperative_groups.h>
 
 #include <algorithm>

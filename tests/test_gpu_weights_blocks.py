@@ -145,7 +145,7 @@ def test_many_sequences(dev, mode, B, Hkv, G, T):
 @pytest.mark.parametrize("mode", ["turbo4", "turbo3_asym"])
 def test_queries_in_blocks(dev, mode):
     """Pairs of query tiles past the first block's: with a hint of 131,072, 64 pairs in blocks of
-    51 (quantized K) or 63 (fp16 K)."""
+    51 (quantized K) or 63 (fp16 K), of other queries each."""
     B, Hq, Hkv, T, cap = 4, 512, 4, 128, 131072
     lengths = [328, 129, 250, 123]
     cache, rec = poisoned(mode, B, Hkv, cap, lengths, 530, dev)
@@ -185,7 +185,8 @@ def test_records_past_32_bit_offsets(dev, mode, Hkv, cap, lengths, T):
     assert tqf.tq_get_status(ctx) == 0
 
 
-@pytest.mark.parametrize("mode,T", [("turbo4_asym", 1), ("turbo3", 2), ("turbo4_asym", 20), ("turbo4", 40)])
+@pytest.mark.parametrize("mode,T", [("turbo4_asym", 1), ("turbo3", 2), ("turbo4_asym", 20), ("turbo4", 40),
+                                    ("turbo3", 8)])   # (16 rows: 576 MB of scores for one KV head)
 def test_tokens_past_2_gb_within_a_sequence(dev, mode, T):
     """8,999,000 tokens that score 0 but for some, most of them behind the first 8 million: a
     row's softmax has e^0 from each of the others that it sees."""
